@@ -501,6 +501,164 @@ int qmoe_moe_forward(int scheme, const qmoe_dims* d, const uint16_t* x_bf16, con
                      const float* topk_w, const void* w1, const void* w1_s, const void* w2, const void* w2_s,
                      uint16_t* out_bf16, int32_t* dev_status, void* ws, size_t ws_bytes, qmoe_stream_t stream);
 
+/* ---------------------------------------------------------------- around the experts: norms
+ *
+ * The calls from here on take values of several types (qmoe_dtype) and rows
+ * with a stride: ld* is the distance in elements between rows, at least the
+ * columns; columns are contiguous.  Pointers need the alignment of their type
+ * only; 16-byte aligned rows of a multiple of 8 columns run faster.  A type
+ * code, mode or stride outside these rules returns QMOE_ERR_ARG, a shape
+ * beyond a stated limit QMOE_ERR_UNSUPPORTED.  An output may not overlap an
+ * input unless the call says so.  Zero rows are valid and write what sums over
+ * no rows give. */
+enum { QMOE_F32 = 0, QMOE_BF16 = 1, QMOE_F16 = 2 };
+
+/* What a block's gate is one value for: nothing (no gate), a row (fp32 [rows]),
+ * a column (fp32 [cols]) or an element (block type, [rows, cols] of row stride
+ * ldg). */
+enum { QMOE_GATE_NONE = 0, QMOE_GATE_ROW = 1, QMOE_GATE_COL = 2, QMOE_GATE_FULL = 3 };
+
+/* qmoe_norm_pre -- the norm that opens a block:
+ *   rstd[t] = 1 / sqrt(mean_c x[t][c]^2 + eps),  n[t][c] = x[t][c] * rstd[t] * w[c].
+ * x has the stream's type, n the block's type: the same as the stream's, or a
+ * 16-bit type beside an fp32 stream.  All arithmetic is fp32, rounded once.
+ * cols <= 16384.  eps >= 0.
+ * in x [rows, cols], w fp32 [cols];  out n [rows, cols], rstd fp32 [rows] (may
+ * be NULL; the gradient needs it). */
+int qmoe_norm_pre(int64_t rows, int64_t cols, int stream_dtype, int block_dtype, const void* x, int64_t ldx,
+                  const float* w, float eps, void* n, int64_t ldn, float* rstd, qmoe_stream_t stream);
+
+/* qmoe_norm_post -- the end of a block, and the norm that opens the next one:
+ *   z = y * rstd * w  (w NULL: z = y, no norm),
+ *   out = r + alpha * gate * z,
+ *   n = out * rstd_next * w_next  (w_next NULL: not computed),
+ * with rstd and rstd_next the reciprocal root mean squares of y and of out
+ * (taken of the fp32 sum, before out is rounded).  r and out have the stream's
+ * type, y, n and a full gate the block's.  out may be r.
+ * rstd and rstd_next fp32 [rows], may be NULL. */
+int qmoe_norm_post(int64_t rows, int64_t cols, int stream_dtype, int block_dtype, const void* r, int64_t ldr,
+                   const void* y, int64_t ldy, const float* w, int gate_mode, const void* gate, int64_t ldg,
+                   float alpha, const float* w_next, float eps, void* out, int64_t ldo, void* n, int64_t ldn,
+                   float* rstd, float* rstd_next, qmoe_stream_t stream);
+
+/* Gradients.  Column sums (dw, dw_next, a column gate's) are fp32, added in a
+ * fixed order through the workspace of qmoe_norm_bwd_workspace_bytes(rows,
+ * cols) bytes (256-byte aligned): the same inputs give the same bits.
+ *
+ * qmoe_norm_pre_backward -- dx = dres + d(n)/d(x) . dn (dres NULL: without it),
+ *   dw[c] = sum_t dn[t][c] x[t][c] rstd[t].  dres and dx have the stream's type;
+ *   dx may be dres.  rstd as qmoe_norm_pre gave it.
+ *
+ * qmoe_norm_post_backward -- with D = dout (NULL: 0) + d(n)/d(out) . dn (dn NULL:
+ *   without it, and out, w_next, rstd_next, dw_next are ignored):
+ *   dr = D;  dz = alpha * gate * D;  dy = d(z)/d(y) . dz;  dw = sum_t dz y rstd;
+ *   dgate = alpha * z * D summed over what the gate is shared by (fp32, a full
+ *   gate's in the block's type).  dout or dn must be given.  dw and dgate are
+ *   written where w and gate are given, and may then not be NULL.  dr may be dout. */
+size_t qmoe_norm_bwd_workspace_bytes(int64_t rows, int64_t cols);
+int qmoe_norm_pre_backward(int64_t rows, int64_t cols, int stream_dtype, int block_dtype, const void* dn,
+                           int64_t lddn, const void* x, int64_t ldx, const float* rstd, const float* w,
+                           const void* dres, int64_t lddres, void* dx, int64_t lddx, float* dw, void* ws,
+                           size_t ws_bytes, qmoe_stream_t stream);
+int qmoe_norm_post_backward(int64_t rows, int64_t cols, int stream_dtype, int block_dtype, const void* dout,
+                            int64_t lddout, const void* y, int64_t ldy, const float* w, const float* rstd,
+                            int gate_mode, const void* gate, int64_t ldg, float alpha, const void* dn, int64_t lddn,
+                            const void* out, int64_t ldo, const float* w_next, const float* rstd_next, void* dr,
+                            int64_t lddr, void* dy, int64_t lddy, float* dw, void* dgate, int64_t lddg,
+                            float* dw_next, void* ws, size_t ws_bytes, qmoe_stream_t stream);
+
+/* ---------------------------------------------------------------- around the experts: routing
+ *
+ * qmoe_route_topk -- the k experts of each token, their weights, and the load
+ *   statistics:
+ *   p[t] = softmax(logits[t]);  ids[t] = the k experts of largest logit + bias
+ *   (bias NULL: 0; an fp32 sum), largest first, the lower id first where equal;
+ *   w[t][j] = scale * p[t][ids[t][j]], or with renorm scale * softmax over the
+ *   k chosen logits.
+ * A logit of -inf is an expert that is not available: it has p = 0 and is never
+ * chosen; NaN counts as -inf, +inf as the largest finite value.  Places that no
+ * available expert fills hold id -1 and weight 0.  A token whose mask byte is 0
+ * (mask NULL: none) or whose logits are all -inf is routed nowhere: ids -1,
+ * weights 0, lse -inf, no part in the statistics.  (An id of -1 in topk_ids
+ * contributes nothing to qmoe_moe_forward and raises QMOE_DEV_BAD_EXPERT_ID.)
+ * Statistics (counts, probs, loss: all three or none), over the n routed tokens:
+ *   counts[e] = pairs of expert e, counts[E] = n;  probs[e] = mean_t p[t][e];
+ *   loss = coef * E * sum_e counts[e] / (k n) * probs[e]  (0 for n = 0).
+ * E <= 1024, k <= min(E, 32).  scale > 0.
+ * in logits [T, E] of row stride ld, bias fp32 [E], mask uint8 [T];  out ids
+ * int32 [T, k], w fp32 [T, k], lse fp32 [T] (logsumexp of the logits; may be
+ * NULL, the gradient needs it), counts int32 [E + 1], probs fp32 [E], loss fp32
+ * [1].  ws of qmoe_route_workspace_bytes(T, E) bytes, 256-byte aligned, for the
+ * statistics (else NULL). */
+size_t qmoe_route_workspace_bytes(int64_t T, int E);
+int qmoe_route_topk(int64_t T, int E, int k, int dtype, const void* logits, int64_t ld, const float* bias,
+                    const uint8_t* mask, int renorm, float scale, int32_t* ids, float* w, float* lse, float coef,
+                    int32_t* counts, float* probs, float* loss, void* ws, size_t ws_bytes, qmoe_stream_t stream);
+
+/* qmoe_route_topk_backward -- dlogits [T, E] (the logits' type, row stride ldd)
+ *   from dw fp32 [T, k] (gradient of the weights; NULL: none) and dloss fp32 [1]
+ *   (gradient of the loss; NULL: none), one at least.  The counts and the
+ *   choice of experts are constants.  logits, renorm, scale, coef as in the
+ *   forward call, ids, w, lse, counts as it gave them. */
+int qmoe_route_topk_backward(int64_t T, int E, int k, int dtype, const void* logits, int64_t ld, const int32_t* ids,
+                             const float* w, const float* lse, int renorm, float scale, const float* dw, float coef,
+                             const int32_t* counts, const float* dloss, void* dlogits, int64_t ldd,
+                             qmoe_stream_t stream);
+
+/* ---------------------------------------------------------------- around the experts: FP8 products
+ *
+ * E4M3 codes with one fp32 scale for each 128 values along the reduction axis
+ * (of one row, or of 128 rows together).  A block of values v gets
+ *   amax = max(max |v|, 2^-100),  code = E4M3(v * (448 / amax)),  scale = amax / 448
+ * with fp32 divisions and products rounded to nearest and codes rounded to
+ * nearest even, saturating; NaN keeps a NaN code, and a block with an infinity
+ * gives NaN products.  The last block of an axis may be shorter.
+ * Codes are uint8 [rows, cols], row stride ldq a multiple of 16, base 16-byte
+ * aligned; bytes from cols to the next multiple of 16 may be overwritten.
+ *
+ * qmoe_fp8_quant_rows -- a scale for each 128 of a row.  x [rows, cols] of type
+ *   dtype -> q, s fp32 [ceil(cols / 128), rows].
+ * qmoe_fp8_quant_cols -- a scale for each 128 of a column, transposed: qt [cols,
+ *   rows], st fp32 [ceil(rows / 128), cols]; where q is given also what
+ *   qmoe_fp8_quant_rows gives (q, s), from the same read of x.
+ * qmoe_fp8_quant_blocks -- a scale for each 128 x 128 block: q [rows, cols]
+ *   and / or qt [cols, rows] (the same codes transposed), s fp32 [ceil(rows / 128),
+ *   ceil(cols / 128)].  rows <= 8388480 for the last two. */
+int qmoe_fp8_quant_rows(int64_t rows, int64_t cols, int dtype, const void* x, int64_t ldx, uint8_t* q, int64_t ldq,
+                        float* s, qmoe_stream_t stream);
+int qmoe_fp8_quant_cols(int64_t rows, int64_t cols, int dtype, const void* x, int64_t ldx, uint8_t* qt, int64_t ldqt,
+                        float* st, uint8_t* q, int64_t ldq, float* s, qmoe_stream_t stream);
+int qmoe_fp8_quant_blocks(int64_t rows, int64_t cols, int dtype, const void* x, int64_t ldx, uint8_t* q, int64_t ldq,
+                          uint8_t* qt, int64_t ldqt, float* s, qmoe_stream_t stream);
+
+/* A matrix of E4M3 codes: q [rows, K] of row stride ld (as above); the scale of
+ * (row r, block b of 128 along K) is s[(r / s_rows) * s_row + b * s_blk], s_rows
+ * 1 or 128. */
+typedef struct {
+    const uint8_t* q;
+    int64_t ld;
+    const float* s;
+    int64_t s_row, s_blk;
+    int32_t s_rows;
+    int32_t reserved;
+} qmoe_fp8_mat;
+
+/* qmoe_fp8_matmul -- c[m][n] = sum over blocks of sa(m) sb(n) sum_k a[m][k] b[n][k]:
+ *   each block of 128 is summed by the tensor core from zero, the scaled sums
+ *   of the blocks in fp32 in a fixed order, and c (type c_dtype, row stride ldc)
+ *   rounded once.  a [M, K], b [N, K].  dev_status int32 [1]: bit
+ *   QMOE_DEV_WAIT_TIMEOUT is OR-ed in if a wait of the kernel runs out (c is
+ *   then undefined).  QMOE_ERR_UNSUPPORTED for sizes above 2^30.
+ * qmoe_fp8_linear -- y = x w^T: qmoe_fp8_quant_rows of x [M, K] (type x_dtype)
+ *   into the workspace (qmoe_fp8_linear_workspace_bytes(M, K) bytes, 256-byte
+ *   aligned), then qmoe_fp8_matmul. */
+int qmoe_fp8_matmul(int64_t M, int64_t N, int64_t K, const qmoe_fp8_mat* a, const qmoe_fp8_mat* b, void* c,
+                    int c_dtype, int64_t ldc, int32_t* dev_status, qmoe_stream_t stream);
+size_t qmoe_fp8_linear_workspace_bytes(int64_t M, int64_t K);
+int qmoe_fp8_linear(int64_t M, int64_t N, int64_t K, int x_dtype, const void* x, int64_t ldx, const qmoe_fp8_mat* w,
+                    void* y, int y_dtype, int64_t ldy, int32_t* dev_status, void* ws, size_t ws_bytes,
+                    qmoe_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -1,0 +1,480 @@
+// FP8 (E4M3) matrix product with one scale for each 128 values of the
+// reduction axis (qmoe_fp8_matmul, qmoe_fp8_linear):
+//
+//   C[m][n] = sum_kb sa(m, kb) sb(n, kb) sum_{k in block kb} a[m][k] b[n][k]
+//
+// The scales are fp32, not powers of two, so they cannot ride in the tensor
+// core's scale inputs; each block of 128 is its own tensor-core product from
+// zero, and the epilogue warps carry the scaled sum on in fp32 registers while
+// the tensor core works on the next block in another accumulator.
+//
+// The 128 lanes of a tile are rows n of b (a weight's output rows), its NT
+// columns rows m of a (tokens): few tokens then make narrow tiles, whose loads
+// are almost all weight; and a store of one token's 128 outputs is contiguous
+// across lanes.  Warps: 8 scale and sum (two for each quadrant of lanes, half
+// the columns each), one loads tiles by TMA, one issues the products, one
+// brings the scales with cp.async.
+//
+// Where the tiles are fewer than the SMs, the reduction axis is cut in S parts
+// for a cluster of S CTAs, which add their parts through distributed shared
+// memory in rank order: the same bits every time, one launch, no workspace.
+#include "row_ops.cuh"
+#include "tc_ptx.cuh"
+#include "tma_host.cuh"
+
+namespace qmoe {
+namespace fp8 {
+
+int quant_rows_launch(int64_t rows, int64_t cols, int dtype, const void* x, int64_t ldx, uint8_t* q, int64_t ldq,
+                      float* s, cudaStream_t st);
+
+constexpr int EPI_WARPS = 8, WARP_TMA = 8, WARP_MMA = 9, WARP_SCALE = 10, THREADS = 11 * 32;
+constexpr int SC_SLOTS = 8;  // scale ring
+
+struct Side {
+    const float* s;
+    int64_t s_row, s_blk;
+    int rows, shift;  // shift: log2 of the rows that share a scale (0 or 7)
+};
+
+struct GemmArgs {
+    int M, N, K;  // rows of a, rows of b, reduction
+    Side a, b;
+    void* c;
+    int64_t ldc;
+    int ctype;
+    int32_t* status;
+    int weights_early;  // b does not depend on the kernel before this one
+};
+
+template <int NT>
+struct GemmCfg {
+    static constexpr int BUFS = NT == 256 ? 2 : 4;  // accumulators in TMEM
+    static constexpr int TMEM_COLS = BUFS * NT < 32 ? 32 : BUFS * NT;
+    static constexpr int P_BYTES = 128 * 128, Q_BYTES = NT * 128, STAGE = P_BYTES + Q_BYTES;
+    static constexpr int SC_FLOATS = 128 + NT;
+    static constexpr int FIXED = SC_SLOTS * SC_FLOATS * 4 + 1024 + 512;
+    static constexpr int FIT = (232448 - FIXED) / STAGE;
+    static constexpr int STAGES = FIT > 10 ? 10 : FIT;
+    static constexpr int SC_OFF = STAGES * STAGE;
+    static constexpr int BAR_OFF = SC_OFF + SC_SLOTS * SC_FLOATS * 4;
+    static constexpr int BARS = 2 * STAGES + 2 * BUFS + 2 * SC_SLOTS;
+    static constexpr int MISC_OFF = BAR_OFF + BARS * 8;
+    static constexpr int SMEM = MISC_OFF + 16 + 1024;
+    static constexpr int COLS = NT / 2;  // columns of an epilogue warp
+    static_assert(SMEM <= 232448 && STAGES >= 4, "shared memory per CTA");
+    static_assert(STAGES * STAGE >= 128 * NT * 4, "the ring holds a tile of sums");
+};
+
+__device__ __forceinline__ void mma_f8(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                       uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+// Instruction descriptor: E4M3 operands (format 0), fp32 sums, both K-major.
+__host__ __device__ constexpr uint32_t idesc_f8(int M, int N) {
+    return (1u << 4) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+}
+
+__device__ __forceinline__ void cp_async_4_or_zero(void* dst, const void* src, bool real) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(tc::smem_u32(dst)), "l"(src), "r"(real ? 4 : 0)
+                 : "memory");
+}
+
+template <int N>
+__device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t (&r)[N]) {
+    static_assert(N == 8 || N == 16, "");
+    if constexpr (N == 16) {
+        tc::tmem_ld_32x32b_x16(taddr, r);
+    } else {
+        asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                     : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                     : "r"(taddr));
+    }
+}
+
+// Every lane waits, so that every lane sees what the barrier guards.
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag, int32_t* status) {
+    if (__all_sync(0xFFFFFFFFu, tc::mbar_wait(bar, parity))) return true;
+    if ((threadIdx.x & 31) == 0) {
+        *abort_flag = 1;
+        atomicOr(status, QMOE_DEV_WAIT_TIMEOUT);
+    }
+    return false;
+}
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ uint32_t cluster_size() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ float peer_load(const float* p, uint32_t rank) {
+    uint32_t at;
+    float v;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(tc::smem_u32(p)), "r"(rank));
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(at) : "memory");
+    return v;
+}
+
+__device__ __forceinline__ void put(void* c, int ctype, int64_t at, float v) {
+    if (ctype == QMOE_F32) static_cast<float*>(c)[at] = v;
+    else if (ctype == QMOE_BF16) static_cast<__nv_bfloat16*>(c)[at] = __float2bfloat16_rn(v);
+    else static_cast<__half*>(c)[at] = __float2half_rn(v);
+}
+
+template <int NT>
+__global__ void __launch_bounds__(THREADS, 1)
+fp8_gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
+                const GemmArgs g) {
+    using C = GemmCfg<NT>;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    float* sc = reinterpret_cast<float*>(smem + C::SC_OFF);
+    uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::BAR_OFF);
+    uint64_t* empty = full + C::STAGES;
+    uint64_t* acc_full = empty + C::STAGES;
+    uint64_t* acc_empty = acc_full + C::BUFS;
+    uint64_t* sc_full = acc_empty + C::BUFS;
+    uint64_t* sc_empty = sc_full + SC_SLOTS;
+    uint32_t* tmem_at = reinterpret_cast<uint32_t*>(smem + C::MISC_OFF);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::MISC_OFF + 8);
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int parts = (int)cluster_size(), part = (int)cluster_rank();
+    const int blocks = (g.K + 127) / 128;
+    const int kb0 = (int)((int64_t)blocks * part / parts), kb1 = (int)((int64_t)blocks * (part + 1) / parts);
+    const int p_tiles = (g.N + 127) / 128, q_tiles = (g.M + NT - 1) / NT;
+    const int tiles = p_tiles * q_tiles;
+    const int first = blockIdx.x / parts, stride = gridDim.x / parts;
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < C::STAGES; ++i) {
+            tc::mbar_init(&full[i], 1);
+            tc::mbar_init(&empty[i], 1);
+        }
+        for (int i = 0; i < C::BUFS; ++i) {
+            tc::mbar_init(&acc_full[i], 1);
+            tc::mbar_init(&acc_empty[i], EPI_WARPS);
+        }
+        for (int i = 0; i < SC_SLOTS; ++i) {
+            tc::mbar_init(&sc_full[i], 32);
+            tc::mbar_init(&sc_empty[i], EPI_WARPS);
+        }
+        *abort_flag = 0;
+        tc::fence_barrier_init();
+    }
+    if (warp == WARP_MMA) {
+        tc::tmem_alloc(tmem_at, C::TMEM_COLS);
+        tc::tmem_relinquish();
+    }
+    tc::tc_fence_before();
+    __syncthreads();
+    tc::tc_fence_after();
+    const uint32_t tm = *tmem_at;
+    pdl_wait();
+
+    if (warp == WARP_TMA) {
+        if (lane == 0) {
+            int slot = 0, in_flight = 0;
+            uint32_t phase = 0;
+            for (int u = first; u < tiles && !*abort_flag; u += stride) {
+                const int p0 = (u % p_tiles) * 128, q0 = (u / p_tiles) * NT;
+                for (int kb = kb0; kb < kb1; ++kb) {
+                    if (!tc::mbar_wait(&empty[slot], phase ^ 1)) {
+                        *abort_flag = 1;
+                        atomicOr(g.status, QMOE_DEV_WAIT_TIMEOUT);
+                        break;
+                    }
+                    uint8_t* st = smem + slot * C::STAGE;
+                    tc::mbar_arrive_expect_tx(&full[slot], C::STAGE);
+                    tc::tma_load_2d(st, &map_b, &full[slot], kb * 128, p0);
+                    tc::tma_load_2d(st + C::P_BYTES, &map_a, &full[slot], kb * 128, q0);
+                    if (in_flight < C::STAGES) ++in_flight;
+                    if (++slot == C::STAGES) { slot = 0; phase ^= 1; }
+                }
+            }
+            if (*abort_flag)  // nobody may have waited for these: no load outlives the CTA
+                for (; in_flight > 0; --in_flight) {
+                    if (slot == 0) { slot = C::STAGES; phase ^= 1; }
+                    --slot;
+                    tc::mbar_wait(&full[slot], phase);
+                }
+        }
+        __syncwarp();
+    } else if (warp == WARP_MMA) {
+        constexpr uint32_t idesc = idesc_f8(128, NT);
+        int slot = 0, buf = 0;
+        uint32_t phase = 0, acc_phase = 0;
+        bool issued = false;
+        for (int u = first; u < tiles && !*abort_flag; u += stride) {
+            for (int kb = kb0; kb < kb1; ++kb) {
+                if (!warp_wait(&acc_empty[buf], acc_phase ^ 1, abort_flag, g.status)) break;
+                if (!warp_wait(&full[slot], phase, abort_flag, g.status)) break;
+                tc::tc_fence_after();
+                if (lane == 0) {
+                    const uint32_t st = tc::smem_u32(smem + slot * C::STAGE);
+                    const uint64_t dp = tc::sdesc_kmajor_sw128(st), dq = tc::sdesc_kmajor_sw128(st + C::P_BYTES);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)  // 32 codes a step: 2 descriptor units of 16 bytes
+                        mma_f8(tm + buf * NT, dp + 2 * k, dq + 2 * k, idesc, k > 0);
+                    tc::mma_commit(&empty[slot]);
+                    tc::mma_commit(&acc_full[buf]);
+                }
+                __syncwarp();
+                if (++slot == C::STAGES) { slot = 0; phase ^= 1; }
+                if (++buf == C::BUFS) { buf = 0; acc_phase ^= 1; }
+                issued = true;
+            }
+        }
+        if (*abort_flag && issued) {  // no product outlives the accumulators
+            if (buf == 0) { buf = C::BUFS; acc_phase ^= 1; }
+            tc::mbar_wait(&acc_full[buf - 1], acc_phase);
+        }
+    } else if (warp == WARP_SCALE) {
+        int slot = 0;
+        uint32_t phase = 0;
+        for (int u = first; u < tiles && !*abort_flag; u += stride) {
+            const int p0 = (u % p_tiles) * 128, q0 = (u / p_tiles) * NT;
+            for (int kb = kb0; kb < kb1; ++kb) {
+                if (!warp_wait(&sc_empty[slot], phase ^ 1, abort_flag, g.status)) break;
+                float* to = sc + slot * C::SC_FLOATS;
+#pragma unroll
+                for (int i = lane; i < 128; i += 32) {
+                    const bool real = p0 + i < g.N;
+                    cp_async_4_or_zero(to + i, g.b.s + (real ? ((p0 + i) >> g.b.shift) * g.b.s_row + kb * g.b.s_blk : 0),
+                                       real);
+                }
+                for (int i = lane; i < NT; i += 32) {
+                    const bool real = q0 + i < g.M;
+                    cp_async_4_or_zero(to + 128 + i,
+                                       g.a.s + (real ? ((q0 + i) >> g.a.shift) * g.a.s_row + kb * g.a.s_blk : 0), real);
+                }
+                tc::cp_async_mbar_arrive_noinc(&sc_full[slot]);
+                if (++slot == SC_SLOTS) { slot = 0; phase ^= 1; }
+            }
+        }
+        tc::cp_async_wait<0>();
+    } else {
+        constexpr int STEP = C::COLS < 16 ? C::COLS : 16;
+        const int quad = warp & 3, half = warp >> 2;
+        const int p_lane = quad * 32 + lane;
+        const uint32_t t_lane = tm + ((uint32_t)(quad * 32) << 16) + half * C::COLS;
+        int slot = 0, buf = 0;
+        uint32_t phase = 0, acc_phase = 0;
+        float acc[C::COLS];
+        for (int u = first; u < tiles && !*abort_flag; u += stride) {
+            const int p0 = (u % p_tiles) * 128, q0 = (u / p_tiles) * NT;
+            bool ok = true;
+#pragma unroll
+            for (int i = 0; i < C::COLS; ++i) acc[i] = 0.f;
+            for (int kb = kb0; kb < kb1; ++kb) {
+                ok = warp_wait(&sc_full[slot], phase, abort_flag, g.status) &&
+                     warp_wait(&acc_full[buf], acc_phase, abort_flag, g.status);
+                if (!ok) break;
+                tc::tc_fence_after();
+                const float* s = sc + slot * C::SC_FLOATS;
+                const float sp = s[p_lane];
+                const float* sq = s + 128 + half * C::COLS;
+#pragma unroll
+                for (int i = 0; i < C::COLS; i += STEP) {
+                    uint32_t r[STEP];
+                    tmem_ld<STEP>(t_lane + buf * NT + i, r);
+                    tc::tmem_ld_wait();
+#pragma unroll
+                    for (int j = 0; j < STEP; ++j)
+                        acc[i + j] = fmaf(__uint_as_float(r[j]), sp * sq[i + j], acc[i + j]);
+                }
+                tc::tc_fence_before();
+                __syncwarp();
+                if (lane == 0) {
+                    tc::mbar_arrive(&acc_empty[buf]);
+                    tc::mbar_arrive(&sc_empty[slot]);
+                }
+                if (++slot == SC_SLOTS) { slot = 0; phase ^= 1; }
+                if (++buf == C::BUFS) { buf = 0; acc_phase ^= 1; }
+            }
+            if (!ok) break;
+            const int n = p0 + p_lane;
+            if (parts == 1) {
+                if (n < g.N) {
+#pragma unroll
+                    for (int i = 0; i < C::COLS; ++i) {
+                        const int m = q0 + half * C::COLS + i;
+                        if (m < g.M) put(g.c, g.ctype, (int64_t)m * g.ldc + n, acc[i]);
+                    }
+                }
+            } else {
+                // every load of this CTA's only tile has been consumed: the ring is free
+                float* sums = reinterpret_cast<float*>(smem);
+#pragma unroll
+                for (int i = 0; i < C::COLS; ++i) sums[(half * C::COLS + i) * 128 + p_lane] = acc[i];
+            }
+        }
+    }
+    __syncwarp();
+    if (parts > 1) {
+        cluster_sync();
+        const float* sums = reinterpret_cast<const float*>(smem);
+        const int p0 = (first % p_tiles) * 128, q0 = (first / p_tiles) * NT;
+        const int cols = min(NT, g.M - q0);
+        for (int i = part * THREADS + threadIdx.x; i < cols * 128; i += parts * THREADS) {
+            float v = 0.f;
+            for (int r = 0; r < parts; ++r) v += peer_load(sums + i, r);
+            const int n = p0 + (i & 127), m = q0 + (i >> 7);
+            if (n < g.N) put(g.c, g.ctype, (int64_t)m * g.ldc + n, v);
+        }
+        cluster_sync();
+    }
+    pdl_trigger();
+    tc::tc_fence_before();
+    __syncthreads();
+    tc::tc_fence_after();
+    if (warp == WARP_MMA) tc::tmem_dealloc(tm, C::TMEM_COLS);
+}
+
+// ------------------------------------------------------------------ host side
+
+static int code_map(CUtensorMap* map, const uint8_t* q, int64_t ld, int rows, int K, int box_rows) {
+    EncodeTiledFn enc = encode_tiled_fn();
+    if (!enc) return QMOE_ERR_CUDA;
+    const cuuint64_t dim[2] = {(cuuint64_t)K, (cuuint64_t)rows};
+    const cuuint64_t stride[1] = {(cuuint64_t)ld};
+    const cuuint32_t box[2] = {128, (cuuint32_t)box_rows};
+    const cuuint32_t one[2] = {1, 1};
+    return enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<uint8_t*>(q), dim, stride, box, one,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
+               ? QMOE_OK
+               : QMOE_ERR_UNSUPPORTED;
+}
+
+struct Plan {
+    int nt, parts;
+};
+
+// The narrowest tile that holds all tokens up to 128, else 256 columns; the
+// reduction in as many parts (a power of two up to 8, two blocks of 128 at
+// least in each) as keep one wave of CTAs.
+inline Plan plan_of(int M, int N, int K) {
+    Plan p;
+    p.nt = M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : M <= 128 ? 128 : 256;
+    const int64_t tiles = (int64_t)((N + 127) / 128) * ((M + p.nt - 1) / p.nt);
+    const int blocks = (K + 127) / 128;
+    p.parts = 1;
+    while (p.parts < 8 && tiles * p.parts * 2 <= row::kSMs && blocks >= p.parts * 4) p.parts *= 2;
+    return p;
+}
+
+template <int NT>
+static int gemm_launch(const CUtensorMap& ma, const CUtensorMap& mb, const GemmArgs& g, int parts, cudaStream_t st) {
+    using C = GemmCfg<NT>;
+    if (cudaFuncSetAttribute(fp8_gemm_kernel<NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM) != cudaSuccess)
+        return QMOE_ERR_CUDA;
+    const int64_t tiles = (int64_t)((g.N + 127) / 128) * ((g.M + NT - 1) / NT);
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = (unsigned)parts;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg = {};
+    // a split reduction gives each cluster exactly one tile
+    cfg.gridDim = dim3((unsigned)(parts > 1 ? tiles * parts : tiles < row::kSMs ? tiles : row::kSMs));
+    cfg.blockDim = dim3(THREADS);
+    cfg.dynamicSmemBytes = C::SMEM;
+    cfg.stream = st;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, fp8_gemm_kernel<NT>, ma, mb, g) == cudaSuccess ? QMOE_OK : QMOE_ERR_LAUNCH;
+}
+
+static int gemm_run(const qmoe_fp8_mat* a, const qmoe_fp8_mat* b, GemmArgs& g, cudaStream_t st) {
+    const Plan p = plan_of(g.M, g.N, g.K);
+    CUtensorMap ma, mb;
+    int rc = code_map(&ma, a->q, a->ld, g.M, g.K, p.nt);
+    if (rc != QMOE_OK) return rc;
+    rc = code_map(&mb, b->q, b->ld, g.N, g.K, 128);
+    if (rc != QMOE_OK) return rc;
+    switch (p.nt) {
+        case 16: return gemm_launch<16>(ma, mb, g, p.parts, st);
+        case 32: return gemm_launch<32>(ma, mb, g, p.parts, st);
+        case 64: return gemm_launch<64>(ma, mb, g, p.parts, st);
+        case 128: return gemm_launch<128>(ma, mb, g, p.parts, st);
+        default: return gemm_launch<256>(ma, mb, g, p.parts, st);
+    }
+}
+
+inline bool mat_ok(const qmoe_fp8_mat* m, int64_t K) {
+    return m && m->q && m->s && aligned16(m->q) && m->ld >= K && m->ld % 16 == 0 && row::type_aligned(m->s, 4) &&
+           (m->s_rows == 1 || m->s_rows == 128);
+}
+inline Side side_of(const qmoe_fp8_mat* m, int rows) {
+    Side s = {m->s, m->s_row, m->s_blk, rows, m->s_rows == 128 ? 7 : 0};
+    return s;
+}
+
+static int check_sizes(int64_t M, int64_t N, int64_t K, int ctype, int64_t ldc) {
+    if (M < 0 || N <= 0 || K <= 0 || !row::dtype_ok(ctype) || ldc < N) return QMOE_ERR_ARG;
+    const int64_t most = 1ll << 30;
+    if (M > most || N > most || K > most || ((M + 15) / 16) * ((N + 127) / 128) >= most) return QMOE_ERR_UNSUPPORTED;
+    return QMOE_OK;
+}
+
+}  // namespace fp8
+}  // namespace qmoe
+
+using namespace qmoe;
+
+extern "C" int qmoe_fp8_matmul(int64_t M, int64_t N, int64_t K, const qmoe_fp8_mat* a, const qmoe_fp8_mat* b, void* c,
+                               int c_dtype, int64_t ldc, int32_t* dev_status, qmoe_stream_t stream) {
+    const int rc = fp8::check_sizes(M, N, K, c_dtype, ldc);
+    if (rc != QMOE_OK) return rc;
+    if (M == 0) return QMOE_OK;
+    if (!fp8::mat_ok(a, K) || !fp8::mat_ok(b, K) || !c || !row::type_aligned(c, row::dtype_size(c_dtype)) ||
+        !dev_status || !row::type_aligned(dev_status, 4))
+        return QMOE_ERR_ARG;
+    fp8::GemmArgs g = {(int)M, (int)N, (int)K, fp8::side_of(a, (int)M), fp8::side_of(b, (int)N), c, ldc, c_dtype,
+                       dev_status, 0};
+    return fp8::gemm_run(a, b, g, (cudaStream_t)stream);
+}
+
+static int64_t linear_ld(int64_t K) { return (K + 15) / 16 * 16; }
+static size_t linear_codes(int64_t M, int64_t K) { return ((size_t)M * linear_ld(K) + 255) / 256 * 256; }
+
+extern "C" size_t qmoe_fp8_linear_workspace_bytes(int64_t M, int64_t K) {
+    if (M <= 0 || K <= 0) return 0;
+    return linear_codes(M, K) + ((size_t)M * ((K + 127) / 128) * 4 + 255) / 256 * 256;
+}
+
+extern "C" int qmoe_fp8_linear(int64_t M, int64_t N, int64_t K, int x_dtype, const void* x, int64_t ldx,
+                               const qmoe_fp8_mat* w, void* y, int y_dtype, int64_t ldy, int32_t* dev_status, void* ws,
+                               size_t ws_bytes, qmoe_stream_t stream) {
+    int rc = fp8::check_sizes(M, N, K, y_dtype, ldy);
+    if (rc != QMOE_OK) return rc;
+    if (!row::dtype_ok(x_dtype)) return QMOE_ERR_ARG;
+    if (M == 0) return QMOE_OK;
+    if (!x || ldx < K || !row::type_aligned(x, row::dtype_size(x_dtype)) || !fp8::mat_ok(w, K) || !y ||
+        !row::type_aligned(y, row::dtype_size(y_dtype)) || !dev_status || !row::type_aligned(dev_status, 4) || !ws ||
+        (reinterpret_cast<uintptr_t>(ws) & 255u) || ws_bytes < qmoe_fp8_linear_workspace_bytes(M, K))
+        return QMOE_ERR_ARG;
+    uint8_t* q = static_cast<uint8_t*>(ws);
+    float* s = reinterpret_cast<float*>(q + linear_codes(M, K));
+    rc = fp8::quant_rows_launch(M, K, x_dtype, x, ldx, q, linear_ld(K), s, (cudaStream_t)stream);
+    if (rc != QMOE_OK) return rc;
+    const qmoe_fp8_mat a = {q, linear_ld(K), s, 1, M, 1, 0};
+    fp8::GemmArgs g = {(int)M, (int)N, (int)K, fp8::side_of(&a, (int)M), fp8::side_of(w, (int)N), y, ldy, y_dtype,
+                       dev_status, 1};
+    return fp8::gemm_run(&a, w, g, (cudaStream_t)stream);
+}

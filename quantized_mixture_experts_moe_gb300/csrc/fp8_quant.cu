@@ -1,0 +1,265 @@
+// FP8 (E4M3) quantisation with one fp32 scale for each 128 values:
+// qmoe_fp8_quant_rows (128 along a row), qmoe_fp8_quant_cols (128 down a
+// column, codes transposed; the row form besides), qmoe_fp8_quant_blocks
+// (128 x 128; codes as they are and transposed).
+//
+//   amax = max(|block|, 2^-100),  q = E4M3(x * (448 / amax)) to nearest even,
+//   saturating,  scale = amax / 448
+//
+// Both divisions and the product are correctly rounded fp32 operations, so a
+// code does not depend on which of the kernels made it.  Each value is read
+// once; HBM is the bound (2 bytes in and 1 out for each code of a 16-bit
+// input).
+#include "row_ops.cuh"
+
+namespace qmoe {
+namespace fp8 {
+
+constexpr float AMAX_MIN = 7.888609052210118e-31f;  // 2^-100
+
+__device__ __forceinline__ float inverse_of(float amax) { return __fdiv_rn(448.f, amax); }
+__device__ __forceinline__ float scale_of(float amax) { return __fdiv_rn(amax, 448.f); }
+// fmaxf drops a NaN; its own code is still NaN.
+__device__ __forceinline__ float amax8(const float (&v)[8], float m) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) m = fmaxf(m, fabsf(v[i]));
+    return m;
+}
+__device__ __forceinline__ uint2 codes8(const float (&v)[8], float inv) {
+    uint2 q;
+    q.x = (uint32_t)e4m3x2_from_float(__fmul_rn(v[0], inv), __fmul_rn(v[1], inv)) |
+          ((uint32_t)e4m3x2_from_float(__fmul_rn(v[2], inv), __fmul_rn(v[3], inv)) << 16);
+    q.y = (uint32_t)e4m3x2_from_float(__fmul_rn(v[4], inv), __fmul_rn(v[5], inv)) |
+          ((uint32_t)e4m3x2_from_float(__fmul_rn(v[6], inv), __fmul_rn(v[7], inv)) << 16);
+    return q;
+}
+
+// 8 values of a row from column c on; zeros past the row's end.
+template <typename T, bool VEC>
+__device__ __forceinline__ void load8(const T* row, int64_t c, int64_t cols, float (&v)[8]) {
+    if (VEC) {
+        if (c < cols) {
+            row::load<8>(row + c, v);
+            return;
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = 0.f;
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = c + i < cols ? row::to_f32(row[c + i]) : 0.f;
+    }
+}
+
+// One row block of 128 for each half warp.
+template <typename T, bool VEC>
+__global__ void __launch_bounds__(256)
+quant_rows_kernel(const T* __restrict__ x, int64_t ldx, int64_t rows, int64_t cols, int64_t blocks,
+                  uint8_t* __restrict__ q, int64_t ldq, float* __restrict__ s) {
+    const int64_t n = rows * blocks;
+    const int lane = threadIdx.x & 15;
+    pdl_sync();
+    for (int64_t b = (int64_t)blockIdx.x * 16 + (threadIdx.x >> 4); b < n; b += (int64_t)gridDim.x * 16) {
+        const int64_t r = b / blocks, kb = b - r * blocks, c = kb * 128 + lane * 8;
+        float v[8];
+        load8<T, VEC>(x + r * ldx, c, cols, v);
+        float m = amax8(v, AMAX_MIN);
+#pragma unroll
+        for (int o = 8; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFu << (threadIdx.x & 16), m, o));
+        if (c < cols) *reinterpret_cast<uint2*>(q + r * ldq + c) = codes8(v, inverse_of(m));
+        if (lane == 0) s[kb * rows + r] = scale_of(m);
+    }
+}
+
+// A 128 x 128 tile a CTA; a thread holds 8 x 8 values (rows 8 (tid / 16) on,
+// columns 8 (tid % 16) on), so that its codes leave in 8-byte pieces both
+// ways; the transposed ones go through shared memory to leave in whole rows.
+//   MODE 0: column scales, codes transposed, and where q is given the row form
+//   MODE 1: one scale, codes where q is given, transposed where qt is given
+struct TileArgs {
+    const void* x;
+    int64_t ldx, rows, cols;
+    uint8_t* q;
+    int64_t ldq;
+    float* s;
+    uint8_t* qt;
+    int64_t ldqt;
+    float* st;
+};
+constexpr int TPITCH = 144;  // bytes between the columns of the transposed tile
+
+template <typename T, bool VEC, int MODE>
+__global__ void __launch_bounds__(256)
+quant_tile_kernel(const TileArgs a) {
+    __shared__ __align__(16) uint8_t tile[128 * TPITCH];
+    __shared__ float part[8][128];
+    __shared__ float col_max[128];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int rg = tid >> 4, cg = tid & 15;
+    const int64_t r0 = (int64_t)blockIdx.y * 128, c0 = (int64_t)blockIdx.x * 128;
+    const int64_t c = c0 + cg * 8;
+    pdl_sync();
+    float v[8][8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const int64_t r = r0 + rg * 8 + i;
+        if (r < a.rows) {
+            load8<T, VEC>(static_cast<const T*>(a.x) + r * a.ldx, c, a.cols, v[i]);
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[i][j] = 0.f;
+        }
+    }
+    float inv_c[8];
+    if (MODE == 0) {
+        float m[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            m[j] = AMAX_MIN;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) m[j] = fmaxf(m[j], fabsf(v[i][j]));
+            m[j] = fmaxf(m[j], __shfl_xor_sync(0xFFFFFFFFu, m[j], 16));
+            if (lane < 16) part[warp][cg * 8 + j] = m[j];
+        }
+        __syncthreads();
+        if (tid < 128) {
+            float t = part[0][tid];
+#pragma unroll
+            for (int i = 1; i < 8; ++i) t = fmaxf(t, part[i][tid]);
+            col_max[tid] = inverse_of(t);
+            if (c0 + tid < a.cols) a.st[(int64_t)blockIdx.y * a.cols + c0 + tid] = scale_of(t);
+        }
+        __syncthreads();
+#pragma unroll
+        for (int j = 0; j < 8; ++j) inv_c[j] = col_max[cg * 8 + j];
+        if (a.q) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const int64_t r = r0 + rg * 8 + i;
+                float t = amax8(v[i], AMAX_MIN);
+#pragma unroll
+                for (int o = 8; o > 0; o >>= 1) t = fmaxf(t, __shfl_xor_sync(0xFFFFFFFFu, t, o));
+                if (r < a.rows) {
+                    if (c < a.cols) *reinterpret_cast<uint2*>(a.q + r * a.ldq + c) = codes8(v[i], inverse_of(t));
+                    if (cg == 0) a.s[(int64_t)blockIdx.x * a.rows + r] = scale_of(t);
+                }
+            }
+        }
+    } else {
+        float m = AMAX_MIN;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) m = amax8(v[i], m);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+        if (lane == 0) part[0][warp] = m;
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < 8; ++i) m = fmaxf(m, part[0][i]);
+        if (tid == 0) a.s[(int64_t)blockIdx.y * gridDim.x + blockIdx.x] = scale_of(m);
+        const float inv = inverse_of(m);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) inv_c[j] = inv;
+        if (a.q && c < a.cols) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const int64_t r = r0 + rg * 8 + i;
+                if (r < a.rows) *reinterpret_cast<uint2*>(a.q + r * a.ldq + c) = codes8(v[i], inv);
+            }
+        }
+    }
+    if (!a.qt) return;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        float t[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) t[i] = v[i][j];
+        *reinterpret_cast<uint2*>(&tile[(cg * 8 + j) * TPITCH + rg * 8]) = codes8(t, inv_c[j]);
+    }
+    __syncthreads();
+    // a column of the tile is 128 codes of one transposed row: 8 lanes of 16 bytes
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int col = i * 32 + (tid >> 3), piece = (tid & 7) * 16;
+        const int64_t r = r0 + piece;
+        if (c0 + col < a.cols && r < a.rows)
+            *reinterpret_cast<uint4*>(a.qt + (c0 + col) * a.ldqt + r) =
+                *reinterpret_cast<const uint4*>(&tile[col * TPITCH + piece]);
+    }
+}
+
+template <typename T>
+int rows_launch(int64_t rows, int64_t cols, const T* x, int64_t ldx, uint8_t* q, int64_t ldq, float* s,
+                cudaStream_t st) {
+    const int64_t blocks = (cols + 127) / 128, ctas = (rows * blocks + 15) / 16, most = (int64_t)row::kSMs * 8;
+    const unsigned grid = (unsigned)(ctas < most ? ctas : most);
+    const bool vec = cols % 8 == 0 && aligned16(x) && (ldx * sizeof(T)) % 16 == 0;
+    if (vec) return launch_pdl(quant_rows_kernel<T, true>, grid, 256, 0, st, x, ldx, rows, cols, blocks, q, ldq, s);
+    return launch_pdl(quant_rows_kernel<T, false>, grid, 256, 0, st, x, ldx, rows, cols, blocks, q, ldq, s);
+}
+
+int quant_rows_launch(int64_t rows, int64_t cols, int dtype, const void* x, int64_t ldx, uint8_t* q, int64_t ldq,
+                      float* s, cudaStream_t st) {
+    if (dtype == QMOE_F32) return rows_launch(rows, cols, static_cast<const float*>(x), ldx, q, ldq, s, st);
+    if (dtype == QMOE_BF16) return rows_launch(rows, cols, static_cast<const __nv_bfloat16*>(x), ldx, q, ldq, s, st);
+    return rows_launch(rows, cols, static_cast<const __half*>(x), ldx, q, ldq, s, st);
+}
+
+template <int MODE, typename T>
+int tile_launch(const TileArgs& a, bool vec, cudaStream_t st) {
+    const dim3 grid((unsigned)((a.cols + 127) / 128), (unsigned)((a.rows + 127) / 128));
+    if (vec) return launch_pdl(quant_tile_kernel<T, true, MODE>, grid, 256, 0, st, a);
+    return launch_pdl(quant_tile_kernel<T, false, MODE>, grid, 256, 0, st, a);
+}
+template <int MODE>
+int tile_run(int dtype, const TileArgs& a, cudaStream_t st) {
+    const bool vec = a.cols % 8 == 0 && aligned16(a.x) && (a.ldx * row::dtype_size(dtype)) % 16 == 0;
+    if (dtype == QMOE_F32) return tile_launch<MODE, float>(a, vec, st);
+    if (dtype == QMOE_BF16) return tile_launch<MODE, __nv_bfloat16>(a, vec, st);
+    return tile_launch<MODE, __half>(a, vec, st);
+}
+
+// Codes [rows, cols]: rows on 16-byte boundaries.
+inline bool codes_ok(const uint8_t* q, int64_t ldq, int64_t cols) {
+    return q && aligned16(q) && ldq >= cols && ldq % 16 == 0;
+}
+inline bool source_ok(int64_t rows, int64_t cols, int dtype, const void* x, int64_t ldx) {
+    return rows == 0 || (x && ldx >= cols && row::type_aligned(x, row::dtype_size(dtype)));
+}
+inline bool fp32_ok(const float* s) { return s && row::type_aligned(s, 4); }
+
+}  // namespace fp8
+}  // namespace qmoe
+
+using namespace qmoe;
+
+extern "C" int qmoe_fp8_quant_rows(int64_t rows, int64_t cols, int dtype, const void* x, int64_t ldx, uint8_t* q,
+                                   int64_t ldq, float* s, qmoe_stream_t stream) {
+    if (rows < 0 || cols <= 0 || !row::dtype_ok(dtype) || !fp8::source_ok(rows, cols, dtype, x, ldx))
+        return QMOE_ERR_ARG;
+    if (rows == 0) return QMOE_OK;
+    if (!fp8::codes_ok(q, ldq, cols) || !fp8::fp32_ok(s)) return QMOE_ERR_ARG;
+    return fp8::quant_rows_launch(rows, cols, dtype, x, ldx, q, ldq, s, (cudaStream_t)stream);
+}
+
+extern "C" int qmoe_fp8_quant_cols(int64_t rows, int64_t cols, int dtype, const void* x, int64_t ldx, uint8_t* qt,
+                                   int64_t ldqt, float* st, uint8_t* q, int64_t ldq, float* s, qmoe_stream_t stream) {
+    if (rows < 0 || cols <= 0 || !row::dtype_ok(dtype) || !fp8::source_ok(rows, cols, dtype, x, ldx))
+        return QMOE_ERR_ARG;
+    if (rows == 0) return QMOE_OK;
+    if (!fp8::codes_ok(qt, ldqt, rows) || !fp8::fp32_ok(st)) return QMOE_ERR_ARG;
+    if (q && (!fp8::codes_ok(q, ldq, cols) || !fp8::fp32_ok(s))) return QMOE_ERR_ARG;
+    if ((rows + 127) / 128 > 65535) return QMOE_ERR_UNSUPPORTED;
+    const fp8::TileArgs a = {x, ldx, rows, cols, q, ldq, s, qt, ldqt, st};
+    return fp8::tile_run<0>(dtype, a, (cudaStream_t)stream);
+}
+
+extern "C" int qmoe_fp8_quant_blocks(int64_t rows, int64_t cols, int dtype, const void* x, int64_t ldx, uint8_t* q,
+                                     int64_t ldq, uint8_t* qt, int64_t ldqt, float* s, qmoe_stream_t stream) {
+    if (rows < 0 || cols <= 0 || !row::dtype_ok(dtype) || !fp8::source_ok(rows, cols, dtype, x, ldx))
+        return QMOE_ERR_ARG;
+    if (rows == 0) return QMOE_OK;
+    if ((!q && !qt) || !fp8::fp32_ok(s)) return QMOE_ERR_ARG;
+    if ((q && !fp8::codes_ok(q, ldq, cols)) || (qt && !fp8::codes_ok(qt, ldqt, rows))) return QMOE_ERR_ARG;
+    if ((rows + 127) / 128 > 65535) return QMOE_ERR_UNSUPPORTED;
+    const fp8::TileArgs a = {x, ldx, rows, cols, q, ldq, s, qt, ldqt, nullptr};
+    return fp8::tile_run<1>(dtype, a, (cudaStream_t)stream);
+}

@@ -1,0 +1,451 @@
+// Norms before and after a block, gradients (qmoe_norm_pre_backward,
+// qmoe_norm_post_backward).
+//
+//   D  = dout + rstd_n (dn w_n - x mean(dn w_n x)),  x = out rstd_n
+//   dz = alpha g D,  t = y rstd,  dy = rstd (dz w - t mean(dz w t))
+//   dw_n = sum_t dn x,  dw = sum_t dz t,  dg = alpha z D  (z = t w)
+//
+// norm_pre's gradient is the first line alone.  As in the forward, a row lives
+// in registers and is read and written once; HBM is the bound (6 values a
+// column for the whole sandwich).  The sums over rows stay in registers (rows
+// of up to 8 values a thread) or in shared memory words that one thread owns,
+// over all the rows of a CTA; each CTA then writes one partial row, and a
+// second launch adds the partial rows in a fixed order, so no atomic decides
+// an order.
+#include "norm_block.cuh"
+
+namespace qmoe {
+namespace norm {
+
+struct BwdArgs {
+    int64_t rows;
+    int cols;
+    const void* dout;  // stream type; may be null (norm_pre: dres)
+    int64_t lddout;
+    const void* dn;  // block type; null: no next norm
+    int64_t lddn;
+    const void* out;  // stream type: what the next norm read (norm_pre: x)
+    int64_t ldo;
+    const float* w_next;
+    const float* rstd_next;
+    const void* y;
+    int64_t ldy;
+    const float* w;
+    const float* rstd;
+    int gate_mode;
+    const void* gate;
+    int64_t ldg;
+    float alpha;
+    void* dr;
+    int64_t lddr;
+    void* dy;
+    int64_t lddy;
+    void* dgate;
+    int64_t lddg;
+    float* part;  // [3][partial rows][cols]: dw_next, dw, column gate
+    int64_t part_rows;
+};
+
+// Sums over rows that one thread owns: registers, or shared memory words laid
+// out so that a warp's accesses hit distinct banks.
+template <int E, int VEC, bool SMEM>
+struct ColSums {
+    float r[SMEM ? 1 : E];
+    float* s;
+    __device__ __forceinline__ void init(float* smem) {
+        if constexpr (SMEM) {
+            s = smem;
+#pragma unroll
+            for (int e = 0; e < E; ++e) s[at(e)] = 0.f;
+        } else {
+#pragma unroll
+            for (int e = 0; e < E; ++e) r[e] = 0.f;
+        }
+    }
+    __device__ __forceinline__ static int at(int e) { return e * blockDim.x + threadIdx.x; }
+    __device__ __forceinline__ void add(int e, float v) {
+        if constexpr (SMEM) s[at(e)] += v;
+        else r[e] += v;
+    }
+    __device__ __forceinline__ float get(int e) const {
+        if constexpr (SMEM) return s[at(e)];
+        else return r[e];
+    }
+};
+
+template <typename RT, typename YT, int NV, int VEC, bool POST>
+__global__ void __launch_bounds__(VEC == 1 && NV == 4 ? 1024 : 512)
+norm_bwd_kernel(const BwdArgs a) {
+    constexpr int E = NV * VEC;
+    constexpr bool SMEM = E > 8;
+    constexpr bool KEEP = E <= 8 && !(VEC == 1);
+    __shared__ float2 sums[2][32];
+    extern __shared__ float cols_smem[];
+    const int tx = threadIdx.x, step = blockDim.x * VEC, cols = a.cols;
+    const int64_t stride = (int64_t)gridDim.x * blockDim.y;
+    const float inv_cols = 1.f / (float)cols;
+    const bool next = POST ? a.dn != nullptr : true;
+    int flip = 0;
+
+    ColSums<E, VEC, SMEM> sum_wn, sum_w, sum_g;
+    sum_wn.init(cols_smem);
+    if (POST) {
+        sum_w.init(cols_smem + E * blockDim.x);
+        sum_g.init(cols_smem + 2 * E * blockDim.x);
+    }
+    float w[KEEP ? E : 1], wn[KEEP ? E : 1];
+    row::Raw<RT, VEC> r_do[NV], r_out[NV];
+    row::Raw<YT, VEC> r_dn[NV], r_y[NV];
+    auto fetch = [&](int64_t row) {
+#pragma unroll
+        for (int v = 0; v < NV; ++v) {
+            const int c = v * step + tx * VEC;
+            if (c >= cols) continue;
+            if (a.dout) row::load_raw<VEC>(r_do[v], static_cast<const RT*>(a.dout) + row * a.lddout + c);
+            if (next) {
+                row::load_raw<VEC>(r_dn[v], static_cast<const YT*>(a.dn) + row * a.lddn + c);
+                row::load_raw<VEC>(r_out[v], static_cast<const RT*>(a.out) + row * a.ldo + c);
+            }
+            if (POST) row::load_raw<VEC>(r_y[v], static_cast<const YT*>(a.y) + row * a.ldy + c);
+        }
+    };
+    int64_t row = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
+    pdl_sync();
+    if (row < a.rows) fetch(row);
+    if (KEEP) {
+#pragma unroll
+        for (int v = 0; v < NV; ++v) {
+            const int c = v * step + tx * VEC;
+            if (c >= cols) continue;
+            if (POST && a.w) row::load<VEC>(a.w + c, &w[v * VEC]);
+            if (next) row::load<VEC>(a.w_next + c, &wn[v * VEC]);
+        }
+    }
+    for (; row < a.rows; row += stride) {
+        float d[E], x[E], dn[E], y[POST ? E : 1];
+        const float rstd_n = next ? a.rstd_next[row] : 0.f;
+#pragma unroll
+        for (int v = 0; v < NV; ++v) {
+            const int c = v * step + tx * VEC;
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) {
+                d[v * VEC + i] = x[v * VEC + i] = dn[v * VEC + i] = 0.f;
+                if (POST) y[v * VEC + i] = 0.f;
+            }
+            if (c < cols) {
+                if (a.dout) row::widen<VEC>(r_do[v], &d[v * VEC]);
+                if (next) {
+                    row::widen<VEC>(r_dn[v], &dn[v * VEC]);
+                    row::widen<VEC>(r_out[v], &x[v * VEC]);
+                }
+                if (POST) row::widen<VEC>(r_y[v], &y[v * VEC]);
+            }
+        }
+        if (row + stride < a.rows) fetch(row + stride);
+        if (next) {
+            float s = 0.f;
+#pragma unroll
+            for (int v = 0; v < NV; ++v) {
+                const int c = v * step + tx * VEC;
+                if (c >= cols) continue;
+                float wv[VEC];
+                if (!KEEP) row::load<VEC>(a.w_next + c, wv);
+#pragma unroll
+                for (int i = 0; i < VEC; ++i) {
+                    const int e = v * VEC + i;
+                    x[e] *= rstd_n;
+                    sum_wn.add(e, dn[e] * x[e]);
+                    dn[e] *= KEEP ? wn[e] : wv[i];
+                    s = fmaf(dn[e], x[e], s);
+                }
+            }
+            const float mean = row::row_sum(s, 0.f, sums[flip]).x * inv_cols;
+            flip ^= 1;
+#pragma unroll
+            for (int e = 0; e < E; ++e) d[e] = fmaf(rstd_n, dn[e] - x[e] * mean, d[e]);
+        }
+#pragma unroll
+        for (int v = 0; v < NV; ++v) {
+            const int c = v * step + tx * VEC;
+            if (c < cols) row::store<VEC>(static_cast<RT*>(a.dr) + row * a.lddr + c, &d[v * VEC]);
+        }
+        if (POST) {
+            const float rstd = a.w ? a.rstd[row] : 1.f;
+            const float g_row = a.gate_mode == QMOE_GATE_ROW ? static_cast<const float*>(a.gate)[row] : 1.f;
+            float s = 0.f, s_gate = 0.f;
+            // from here on x holds t = y rstd and dn holds dz w
+#pragma unroll
+            for (int v = 0; v < NV; ++v) {
+                const int c = v * step + tx * VEC;
+                if (c >= cols) continue;
+                float wv[VEC], g[VEC], dg[VEC];
+                if (!KEEP && a.w) row::load<VEC>(a.w + c, wv);
+                if (a.gate_mode == QMOE_GATE_FULL)
+                    row::load<VEC>(static_cast<const YT*>(a.gate) + row * a.ldg + c, g);
+                else if (a.gate_mode == QMOE_GATE_COL)
+                    row::load<VEC>(static_cast<const float*>(a.gate) + c, g);
+#pragma unroll
+                for (int i = 0; i < VEC; ++i) {
+                    const int e = v * VEC + i;
+                    const float wt = a.w ? (KEEP ? w[e] : wv[i]) : 1.f;
+                    const float ad = a.alpha * d[e];
+                    const float gate = a.gate_mode >= QMOE_GATE_COL ? g[i] : g_row;
+                    const float t = y[e] * rstd, dz = ad * gate;
+                    dg[i] = ad * (t * wt);
+                    s_gate += dg[i];
+                    if (a.gate_mode == QMOE_GATE_COL) sum_g.add(e, dg[i]);
+                    if (a.w) sum_w.add(e, dz * t);
+                    x[e] = t;
+                    dn[e] = dz * wt;
+                    s = fmaf(dn[e], t, s);
+                }
+                if (a.gate_mode == QMOE_GATE_FULL)
+                    row::store<VEC>(static_cast<YT*>(a.dgate) + row * a.lddg + c, dg);
+            }
+            if (a.w || a.gate_mode == QMOE_GATE_ROW) {
+                const float2 both = row::row_sum(s, s_gate, sums[flip]);
+                flip ^= 1;
+                s = both.x * inv_cols;
+                if (a.gate_mode == QMOE_GATE_ROW && tx == 0) static_cast<float*>(a.dgate)[row] = both.y;
+            }
+#pragma unroll
+            for (int v = 0; v < NV; ++v) {
+                const int c = v * step + tx * VEC;
+                if (c >= cols) continue;
+                float dy[VEC];
+#pragma unroll
+                for (int i = 0; i < VEC; ++i) {
+                    const int e = v * VEC + i;
+                    dy[i] = a.w ? rstd * (dn[e] - x[e] * s) : dn[e];
+                }
+                row::store<VEC>(static_cast<YT*>(a.dy) + row * a.lddy + c, dy);
+            }
+        }
+    }
+    const int64_t part = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+        const int c = v * step + tx * VEC;
+        if (c >= cols) continue;
+        float t[VEC];
+        auto put = [&](ColSums<E, VEC, SMEM>& s, int which) {
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) t[i] = s.get(v * VEC + i);
+            float* to = a.part + (which * a.part_rows + part) * cols + c;
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) to[i] = t[i];
+        };
+        if (next) put(sum_wn, 0);
+        if (POST && a.w) put(sum_w, 1);
+        if (POST && a.gate_mode == QMOE_GATE_COL) put(sum_g, 2);
+    }
+}
+
+// out[j][c] = the sum of partial rows of output j, in row order within each of
+// 32 interleaved groups, then over the groups.
+struct SumArgs {
+    const float* part;
+    int64_t part_rows, used;
+    int cols;
+    float* out[3];
+};
+__global__ void __launch_bounds__(1024) norm_sum_kernel(const SumArgs a) {
+    __shared__ float group[32][33];
+    pdl_sync();
+    float* out = a.out[blockIdx.y];
+    if (!out) return;
+    const int c = blockIdx.x * 32 + threadIdx.x;
+    float s = 0.f;
+    if (c < a.cols) {
+        const float* p = a.part + (int64_t)blockIdx.y * a.part_rows * a.cols + c;
+#pragma unroll 4
+        for (int64_t i = threadIdx.y; i < a.used; i += 32) s += p[i * a.cols];
+    }
+    group[threadIdx.y][threadIdx.x] = s;
+    __syncthreads();
+    s = group[threadIdx.x][threadIdx.y];
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
+    const int oc = blockIdx.x * 32 + threadIdx.y;
+    if (threadIdx.x == 0 && oc < a.cols) out[oc] = s;
+}
+
+// CTAs of a launch: one wave of the kernels' occupancy.
+inline int64_t bwd_ctas(const Shape& s, int64_t rows) {
+    const int64_t ctas = (rows + s.rows_per_cta - 1) / s.rows_per_cta;
+    const int64_t per_sm = 512 / (s.threads * s.rows_per_cta);
+    const int64_t fit = (int64_t)row::kSMs * (per_sm > 1 ? per_sm : 1);
+    return ctas < fit ? ctas : fit;
+}
+inline int64_t part_rows(int64_t rows, int64_t cols) {
+    int64_t most = 1;
+    for (int vec = 0; vec < 2; ++vec) {
+        const Shape s = shape_of(cols, vec != 0, 512);
+        const int64_t n = bwd_ctas(s, rows) * s.rows_per_cta;
+        most = n > most ? n : most;
+    }
+    return most;
+}
+
+template <typename K>
+inline int start(K kernel, dim3 grid, dim3 block, size_t smem, cudaStream_t st, const BwdArgs& a) {
+    if (smem > 48 * 1024 &&
+        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
+        return QMOE_ERR_CUDA;
+    return launch_pdl(kernel, grid, block, smem, st, a);
+}
+
+template <bool POST>
+struct Bwd {
+    template <typename RT, typename YT>
+    struct Go {
+        static int go(const BwdArgs& a, const Shape& s, int64_t ctas, cudaStream_t st) {
+            const dim3 block(s.threads, s.rows_per_cta), grid((unsigned)ctas);
+            const int e = s.nv * s.vec;
+            const size_t smem = e > 8 ? (size_t)(POST ? 3 : 1) * e * s.threads * 4 : 0;
+            if (s.vec == 8) {
+                if (s.nv == 1) return start(norm_bwd_kernel<RT, YT, 1, 8, POST>, grid, block, smem, st, a);
+                if (s.nv == 2) return start(norm_bwd_kernel<RT, YT, 2, 8, POST>, grid, block, smem, st, a);
+                return start(norm_bwd_kernel<RT, YT, 4, 8, POST>, grid, block, smem, st, a);
+            }
+            if (s.nv == 4) return start(norm_bwd_kernel<RT, YT, 4, 1, POST>, grid, block, smem, st, a);
+            if (s.nv == 16) return start(norm_bwd_kernel<RT, YT, 16, 1, POST>, grid, block, smem, st, a);
+            return start(norm_bwd_kernel<RT, YT, 32, 1, POST>, grid, block, smem, st, a);
+        }
+    };
+};
+template <typename RT, typename YT> using PreGo = Bwd<false>::Go<RT, YT>;
+template <typename RT, typename YT> using PostGo = Bwd<true>::Go<RT, YT>;
+
+template <template <typename, typename> class F>
+inline int run(BwdArgs& a, int rt, int yt, bool vec, float* const (&out)[3], void* ws, cudaStream_t st) {
+    a.part = static_cast<float*>(ws);
+    a.part_rows = part_rows(a.rows, a.cols);
+    const Shape s = shape_of(a.cols, vec, 512);
+    const int64_t ctas = bwd_ctas(s, a.rows);
+    if (ctas > 0) {
+        const int rc = by_types<F>(rt, yt, a, s, ctas, st);
+        if (rc != QMOE_OK) return rc;
+    }
+    if (!out[0] && !out[1] && !out[2]) return QMOE_OK;
+    SumArgs b = {a.part, a.part_rows, ctas * s.rows_per_cta, a.cols, {out[0], out[1], out[2]}};
+    return launch_pdl(norm_sum_kernel, dim3((unsigned)((a.cols + 31) / 32), 3), dim3(32, 32), 0, st, b);
+}
+
+}  // namespace norm
+}  // namespace qmoe
+
+using namespace qmoe;
+
+extern "C" size_t qmoe_norm_bwd_workspace_bytes(int64_t rows, int64_t cols) {
+    if (rows < 0 || cols <= 0 || cols > norm::MAX_COLS) return 0;
+    return (size_t)(3 * norm::part_rows(rows, cols) * cols * 4 + 255) / 256 * 256;
+}
+
+static bool ws_ok(int64_t rows, int64_t cols, const void* ws, size_t bytes) {
+    return ws && (reinterpret_cast<uintptr_t>(ws) & 255u) == 0 && bytes >= qmoe_norm_bwd_workspace_bytes(rows, cols);
+}
+
+extern "C" int qmoe_norm_pre_backward(int64_t rows, int64_t cols, int stream_dtype, int block_dtype, const void* dn,
+                                      int64_t lddn, const void* x, int64_t ldx, const float* rstd, const float* w,
+                                      const void* dres, int64_t lddres, void* dx, int64_t lddx, float* dw, void* ws,
+                                      size_t ws_bytes, qmoe_stream_t stream) {
+    if (rows < 0 || cols <= 0 || !norm::types_ok(stream_dtype, block_dtype)) return QMOE_ERR_ARG;
+    if (!w || !dw || !row::type_aligned(w, 4) || !row::type_aligned(dw, 4)) return QMOE_ERR_ARG;
+    const int rs = row::dtype_size(stream_dtype), bs = row::dtype_size(block_dtype);
+    if (rows > 0) {
+        if (!dn || !x || !rstd || !dx || lddn < cols || ldx < cols || lddx < cols || (dres && lddres < cols))
+            return QMOE_ERR_ARG;
+        if (!row::type_aligned(dn, bs) || !row::type_aligned(x, rs) || !row::type_aligned(dx, rs) ||
+            !row::type_aligned(dres, rs) || !row::type_aligned(rstd, 4))
+            return QMOE_ERR_ARG;
+    }
+    if (cols > norm::MAX_COLS) return QMOE_ERR_UNSUPPORTED;
+    if (!ws_ok(rows, cols, ws, ws_bytes)) return QMOE_ERR_ARG;
+    norm::BwdArgs a = {};
+    a.rows = rows;
+    a.cols = (int)cols;
+    a.dout = dres;
+    a.lddout = lddres;
+    a.dn = dn;
+    a.lddn = lddn;
+    a.out = x;
+    a.ldo = ldx;
+    a.w_next = w;
+    a.rstd_next = rstd;
+    a.dr = dx;
+    a.lddr = lddx;
+    bool vec = cols % 8 == 0 && norm::row_aligned(dn, lddn, bs) && norm::row_aligned(x, ldx, rs) &&
+               norm::row_aligned(dx, lddx, rs) && aligned16(w);
+    if (dres) vec = vec && norm::row_aligned(dres, lddres, rs);
+    return norm::run<norm::PreGo>(a, stream_dtype, block_dtype, vec, {dw, nullptr, nullptr}, ws, (cudaStream_t)stream);
+}
+
+extern "C" int qmoe_norm_post_backward(int64_t rows, int64_t cols, int stream_dtype, int block_dtype, const void* dout,
+                                       int64_t lddout, const void* y, int64_t ldy, const float* w, const float* rstd,
+                                       int gate_mode, const void* gate, int64_t ldg, float alpha, const void* dn,
+                                       int64_t lddn, const void* out, int64_t ldo, const float* w_next,
+                                       const float* rstd_next, void* dr, int64_t lddr, void* dy, int64_t lddy,
+                                       float* dw, void* dgate, int64_t lddg, float* dw_next, void* ws, size_t ws_bytes,
+                                       qmoe_stream_t stream) {
+    if (rows < 0 || cols <= 0 || !norm::types_ok(stream_dtype, block_dtype) || !norm::gate_mode_ok(gate_mode))
+        return QMOE_ERR_ARG;
+    const int rs = row::dtype_size(stream_dtype), bs = row::dtype_size(block_dtype);
+    const bool full = gate_mode == QMOE_GATE_FULL, gated = gate_mode != QMOE_GATE_NONE;
+    if (w && (!dw || !row::type_aligned(w, 4) || !row::type_aligned(dw, 4))) return QMOE_ERR_ARG;
+    // a column gate's sum is written for zero rows too
+    if (gated && (!gate || !dgate) && (rows > 0 || gate_mode == QMOE_GATE_COL)) return QMOE_ERR_ARG;
+    if (gated && (!row::type_aligned(gate, full ? bs : 4) || !row::type_aligned(dgate, full ? bs : 4)))
+        return QMOE_ERR_ARG;
+    if (dn && (!w_next || !dw_next || !row::type_aligned(w_next, 4) || !row::type_aligned(dw_next, 4)))
+        return QMOE_ERR_ARG;
+    if (rows > 0) {
+        if ((!dout && !dn) || !y || !dr || !dy || (dout && lddout < cols) || ldy < cols || lddr < cols || lddy < cols)
+            return QMOE_ERR_ARG;
+        if (dn && (!out || !rstd_next || lddn < cols || ldo < cols)) return QMOE_ERR_ARG;
+        if (w && !rstd) return QMOE_ERR_ARG;
+        if (full && (ldg < cols || lddg < cols)) return QMOE_ERR_ARG;
+        if (!row::type_aligned(dout, rs) || !row::type_aligned(y, bs) || !row::type_aligned(dr, rs) ||
+            !row::type_aligned(dy, bs) || !row::type_aligned(rstd, 4) || !row::type_aligned(dn, bs) ||
+            (dn && (!row::type_aligned(out, rs) || !row::type_aligned(rstd_next, 4))))
+            return QMOE_ERR_ARG;
+    }
+    if (cols > norm::MAX_COLS) return QMOE_ERR_UNSUPPORTED;
+    if (!ws_ok(rows, cols, ws, ws_bytes)) return QMOE_ERR_ARG;
+    norm::BwdArgs a = {};
+    a.rows = rows;
+    a.cols = (int)cols;
+    a.dout = dout;
+    a.lddout = lddout;
+    a.y = y;
+    a.ldy = ldy;
+    a.w = w;
+    a.rstd = rstd;
+    a.gate_mode = gate_mode;
+    a.gate = gate;
+    a.ldg = ldg;
+    a.alpha = alpha;
+    a.dr = dr;
+    a.lddr = lddr;
+    a.dy = dy;
+    a.lddy = lddy;
+    a.dgate = dgate;
+    a.lddg = lddg;
+    bool vec = cols % 8 == 0 && norm::row_aligned(y, ldy, bs) && norm::row_aligned(dr, lddr, rs) &&
+               norm::row_aligned(dy, lddy, bs) && aligned16(w);
+    if (dout) vec = vec && norm::row_aligned(dout, lddout, rs);
+    if (full) vec = vec && norm::row_aligned(gate, ldg, bs) && norm::row_aligned(dgate, lddg, bs);
+    if (gate_mode == QMOE_GATE_COL) vec = vec && aligned16(gate);
+    if (dn) {
+        a.dn = dn;
+        a.lddn = lddn;
+        a.out = out;
+        a.ldo = ldo;
+        a.w_next = w_next;
+        a.rstd_next = rstd_next;
+        vec = vec && norm::row_aligned(dn, lddn, bs) && norm::row_aligned(out, ldo, rs) && aligned16(w_next);
+    }
+    float* const col_gate = gate_mode == QMOE_GATE_COL ? static_cast<float*>(dgate) : nullptr;
+    return norm::run<norm::PostGo>(a, stream_dtype, block_dtype, vec,
+                                   {dn ? dw_next : nullptr, w ? dw : nullptr, col_gate}, ws, (cudaStream_t)stream);
+}

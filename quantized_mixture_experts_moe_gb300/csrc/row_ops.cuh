@@ -1,0 +1,136 @@
+// Shared pieces of the row-wise operators (norms, FP8 quantisation): element
+// types, 8-element vector loads and stores, and the sum over the threads that
+// share a row.
+#pragma once
+
+#include "qmoe_common.cuh"
+
+namespace qmoe {
+namespace row {
+
+constexpr int kSMs = 152;  // GB300
+
+inline bool dtype_ok(int t) { return t == QMOE_F32 || t == QMOE_BF16 || t == QMOE_F16; }
+inline int dtype_size(int t) { return t == QMOE_F32 ? 4 : 2; }
+inline bool type_aligned(const void* p, int size) { return (reinterpret_cast<uintptr_t>(p) & (uintptr_t)(size - 1)) == 0; }
+
+__device__ __forceinline__ float to_f32(float v) { return v; }
+__device__ __forceinline__ float to_f32(__nv_bfloat16 v) { return __bfloat162float(v); }
+__device__ __forceinline__ float to_f32(__half v) { return __half2float(v); }
+
+template <typename T> __device__ __forceinline__ T from_f32(float v);
+template <> __device__ __forceinline__ float from_f32<float>(float v) { return v; }
+template <> __device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
+template <> __device__ __forceinline__ __half from_f32<__half>(float v) { return __float2half_rn(v); }
+
+// Two values in one 32-bit word, the first in the low half.
+__device__ __forceinline__ float2 unpack2(uint32_t u, __nv_bfloat16) {
+    return make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xFFFF0000u));
+}
+__device__ __forceinline__ float2 unpack2(uint32_t u, __half) {
+    return __half22float2(*reinterpret_cast<const __half2*>(&u));
+}
+__device__ __forceinline__ uint32_t pack2(float a, float b, __nv_bfloat16) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ uint32_t pack2(float a, float b, __half) {
+    const __half2 h = __floats2half2_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// VEC consecutive values as they lie in memory: loaded early, widened when
+// they are used.  VEC = 8 needs a 16-byte aligned address.
+template <typename T, int VEC> struct Raw { T v; };
+template <typename T> struct Raw<T, 8> { uint4 v; };
+template <> struct Raw<float, 8> { float4 a, b; };
+
+template <int VEC>
+__device__ __forceinline__ void load_raw(Raw<float, VEC>& r, const float* p) {
+    if constexpr (VEC == 8) {
+        r.a = reinterpret_cast<const float4*>(p)[0];
+        r.b = reinterpret_cast<const float4*>(p)[1];
+    } else {
+        r.v = p[0];
+    }
+}
+template <int VEC, typename T>
+__device__ __forceinline__ void load_raw(Raw<T, VEC>& r, const T* p) {
+    if constexpr (VEC == 8) r.v = *reinterpret_cast<const uint4*>(p);
+    else r.v = p[0];
+}
+template <int VEC>
+__device__ __forceinline__ void widen(const Raw<float, VEC>& r, float* v) {
+    if constexpr (VEC == 8) {
+        v[0] = r.a.x; v[1] = r.a.y; v[2] = r.a.z; v[3] = r.a.w;
+        v[4] = r.b.x; v[5] = r.b.y; v[6] = r.b.z; v[7] = r.b.w;
+    } else {
+        v[0] = r.v;
+    }
+}
+template <int VEC, typename T>
+__device__ __forceinline__ void widen(const Raw<T, VEC>& r, float* v) {
+    if constexpr (VEC == 8) {
+        const uint32_t u[4] = {r.v.x, r.v.y, r.v.z, r.v.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float2 f = unpack2(u[i], T{});
+            v[2 * i] = f.x;
+            v[2 * i + 1] = f.y;
+        }
+    } else {
+        v[0] = to_f32(r.v);
+    }
+}
+template <int VEC, typename T>
+__device__ __forceinline__ void load(const T* p, float* v) {
+    Raw<T, VEC> r;
+    load_raw<VEC>(r, p);
+    widen<VEC>(r, v);
+}
+template <int VEC>
+__device__ __forceinline__ void store(float* p, const float* v) {
+    if constexpr (VEC == 8) {
+        reinterpret_cast<float4*>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
+        reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
+    } else {
+        p[0] = v[0];
+    }
+}
+template <int VEC, typename T>
+__device__ __forceinline__ void store(T* p, const float* v) {
+    if constexpr (VEC == 8) {
+        *reinterpret_cast<uint4*>(p) = make_uint4(pack2(v[0], v[1], T{}), pack2(v[2], v[3], T{}),
+                                                  pack2(v[4], v[5], T{}), pack2(v[6], v[7], T{}));
+    } else {
+        p[0] = from_f32<T>(v[0]);
+    }
+}
+
+// Sum of (a, b) over the threads of a row: the lanes of a warp where the row
+// has 32 threads, else the whole CTA (blockDim.x threads; `buf` is one of the
+// two halves of a 2 x 32 float2 array, alternated by the caller so that one
+// barrier per sum is enough).  The order is fixed.
+__device__ __forceinline__ float2 row_sum(float a, float b, float2* buf) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        a += __shfl_xor_sync(0xFFFFFFFFu, a, o);
+        b += __shfl_xor_sync(0xFFFFFFFFu, b, o);
+    }
+    if (blockDim.x == 32) return make_float2(a, b);
+    const int warps = blockDim.x >> 5, lane = threadIdx.x & 31;
+    if (lane == 0) buf[threadIdx.x >> 5] = make_float2(a, b);
+    __syncthreads();
+    const float2 p = lane < warps ? buf[lane] : make_float2(0.f, 0.f);
+    a = p.x;
+    b = p.y;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        a += __shfl_xor_sync(0xFFFFFFFFu, a, o);
+        b += __shfl_xor_sync(0xFFFFFFFFu, b, o);
+    }
+    return make_float2(a, b);
+}
+
+}  // namespace row
+}  // namespace qmoe
