@@ -28,8 +28,11 @@ namespace fp8 {
 int quant_rows_launch(int64_t rows, int64_t cols, int dtype, const void* x, int64_t ldx, uint8_t* q, int64_t ldq,
                       float* s, cudaStream_t st);
 
-constexpr int EPI_WARPS = 8, WARP_TMA = 8, WARP_MMA = 9, WARP_SCALE = 10, THREADS = 11 * 32;
+constexpr int EPI_WARPS = 8, WARP_TMA = 8, WARP_MMA = 9, WARP_SCALE = 10, SCALE_WARPS = 2, THREADS = 12 * 32;
 constexpr int SC_SLOTS = 8;  // scale ring
+// Registers: launched with 168 a thread (64,512 in all); the two warpgroups of
+// epilogue warps take 208, the third keeps 80 (63,488 in all).
+constexpr int EPI_REGS = 208, OTHER_REGS = 80;
 
 struct Side {
     const float* s;
@@ -47,12 +50,14 @@ struct GemmArgs {
     int weights_early;  // b does not depend on the kernel before this one
 };
 
-template <int NT>
+// UNI: the 128 rows of a tile's lane side share their scale, and the scale
+// warps multiply it into the column scales; else each lane has its own.
+template <int NT, bool UNI>
 struct GemmCfg {
     static constexpr int BUFS = NT == 256 ? 2 : 4;  // accumulators in TMEM
     static constexpr int TMEM_COLS = BUFS * NT < 32 ? 32 : BUFS * NT;
     static constexpr int P_BYTES = 128 * 128, Q_BYTES = NT * 128, STAGE = P_BYTES + Q_BYTES;
-    static constexpr int SC_FLOATS = 128 + NT;
+    static constexpr int SC_FLOATS = NT + (UNI ? 0 : 128);
     static constexpr int FIXED = SC_SLOTS * SC_FLOATS * 4 + 1024 + 512;
     static constexpr int FIT = (232448 - FIXED) / STAGE;
     static constexpr int STAGES = FIT > 10 ? 10 : FIT;
@@ -79,9 +84,31 @@ __host__ __device__ constexpr uint32_t idesc_f8(int M, int N) {
     return (1u << 4) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
 }
 
-__device__ __forceinline__ void cp_async_4_or_zero(void* dst, const void* src, bool real) {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(tc::smem_u32(dst)), "l"(src), "r"(real ? 4 : 0)
-                 : "memory");
+// Two fp32 values in a 64-bit register pair.
+__device__ __forceinline__ uint64_t pair_of(float a, float b) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t pair_of(uint32_t a, uint32_t b) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(a), "r"(b));
+    return r;
+}
+__device__ __forceinline__ float2 halves_of(uint64_t p) {
+    float2 v;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(v.x), "=f"(v.y) : "l"(p));
+    return v;
+}
+__device__ __forceinline__ uint64_t fma_pair(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+__device__ __forceinline__ uint64_t mul_pair(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
 }
 
 template <int N>
@@ -133,11 +160,24 @@ __device__ __forceinline__ void put(void* c, int ctype, int64_t at, float v) {
     else static_cast<__half*>(c)[at] = __float2half_rn(v);
 }
 
-template <int NT>
+// One lane's outputs of a tile: COLS rows of c, as far as there are any.
+template <int COLS, typename T>
+__device__ __forceinline__ void put_cols(T* c, int64_t ldc, int rows, const uint64_t (&acc)[COLS / 2]) {
+#pragma unroll
+    for (int i = 0; i < COLS / 2; ++i) {
+        const float2 v = halves_of(acc[i]);
+        if (2 * i < rows) *c = row::from_f32<T>(v.x);
+        c += ldc;
+        if (2 * i + 1 < rows) *c = row::from_f32<T>(v.y);
+        c += ldc;
+    }
+}
+
+template <int NT, bool UNI>
 __global__ void __launch_bounds__(THREADS, 1)
 fp8_gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
                 const GemmArgs g) {
-    using C = GemmCfg<NT>;
+    using C = GemmCfg<NT, UNI>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     float* sc = reinterpret_cast<float*>(smem + C::SC_OFF);
@@ -168,7 +208,7 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant
             tc::mbar_init(&acc_empty[i], EPI_WARPS);
         }
         for (int i = 0; i < SC_SLOTS; ++i) {
-            tc::mbar_init(&sc_full[i], 32);
+            tc::mbar_init(&sc_full[i], 1);
             tc::mbar_init(&sc_empty[i], EPI_WARPS);
         }
         *abort_flag = 0;
@@ -184,6 +224,8 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant
     const uint32_t tm = *tmem_at;
     pdl_wait();
 
+    if (warp >= EPI_WARPS) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(OTHER_REGS));
     if (warp == WARP_TMA) {
         if (lane == 0) {
             int slot = 0, in_flight = 0;
@@ -241,84 +283,115 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant
             if (buf == 0) { buf = C::BUFS; acc_phase ^= 1; }
             tc::mbar_wait(&acc_full[buf - 1], acc_phase);
         }
-    } else if (warp == WARP_SCALE) {
-        int slot = 0;
-        uint32_t phase = 0;
+    } else {
+        // the scale warps take the blocks in turn; a block's loads go out before the slot is waited for
+        int it = 0;
         for (int u = first; u < tiles && !*abort_flag; u += stride) {
             const int p0 = (u % p_tiles) * 128, q0 = (u / p_tiles) * NT;
-            for (int kb = kb0; kb < kb1; ++kb) {
-                if (!warp_wait(&sc_empty[slot], phase ^ 1, abort_flag, g.status)) break;
+            for (int kb = kb0; kb < kb1; ++kb, ++it) {
+                if (it % SCALE_WARPS != warp - WARP_SCALE) continue;
+                const int slot = it % SC_SLOTS;
+                constexpr int QN = (NT + 31) / 32;
+                float sq[QN], sp[4];
+                const float uni = UNI ? g.b.s[(p0 >> 7) * g.b.s_row + kb * g.b.s_blk] : 1.f;
+#pragma unroll
+                for (int i = 0; i < QN; ++i) {
+                    const int m = q0 + i * 32 + lane;
+                    sq[i] = m < g.M && i * 32 + lane < NT ? g.a.s[(m >> g.a.shift) * g.a.s_row + kb * g.a.s_blk] : 0.f;
+                }
+                if (!UNI) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int n = p0 + i * 32 + lane;
+                        sp[i] = n < g.N ? g.b.s[(n >> g.b.shift) * g.b.s_row + kb * g.b.s_blk] : 0.f;
+                    }
+                }
+                if (!warp_wait(&sc_empty[slot], (it / SC_SLOTS & 1) ^ 1, abort_flag, g.status)) break;
                 float* to = sc + slot * C::SC_FLOATS;
 #pragma unroll
-                for (int i = lane; i < 128; i += 32) {
-                    const bool real = p0 + i < g.N;
-                    cp_async_4_or_zero(to + i, g.b.s + (real ? ((p0 + i) >> g.b.shift) * g.b.s_row + kb * g.b.s_blk : 0),
-                                       real);
+                for (int i = 0; i < QN; ++i)
+                    if (i * 32 + lane < NT) to[i * 32 + lane] = sq[i] * uni;
+                if (!UNI) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) to[NT + i * 32 + lane] = sp[i];
                 }
-                for (int i = lane; i < NT; i += 32) {
-                    const bool real = q0 + i < g.M;
-                    cp_async_4_or_zero(to + 128 + i,
-                                       g.a.s + (real ? ((q0 + i) >> g.a.shift) * g.a.s_row + kb * g.a.s_blk : 0), real);
-                }
-                tc::cp_async_mbar_arrive_noinc(&sc_full[slot]);
-                if (++slot == SC_SLOTS) { slot = 0; phase ^= 1; }
+                __syncwarp();
+                if (lane == 0) tc::mbar_arrive(&sc_full[slot]);
             }
         }
-        tc::cp_async_wait<0>();
+    }
     } else {
-        constexpr int STEP = C::COLS < 16 ? C::COLS : 16;
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(EPI_REGS));
+        constexpr int STEP = C::COLS < 16 ? C::COLS : 16, STEPS = C::COLS / STEP;
         const int quad = warp & 3, half = warp >> 2;
         const int p_lane = quad * 32 + lane;
         const uint32_t t_lane = tm + ((uint32_t)(quad * 32) << 16) + half * C::COLS;
         int slot = 0, buf = 0;
         uint32_t phase = 0, acc_phase = 0;
-        float acc[C::COLS];
+        uint64_t acc[C::COLS / 2];
         for (int u = first; u < tiles && !*abort_flag; u += stride) {
             const int p0 = (u % p_tiles) * 128, q0 = (u / p_tiles) * NT;
             bool ok = true;
 #pragma unroll
-            for (int i = 0; i < C::COLS; ++i) acc[i] = 0.f;
+            for (int i = 0; i < C::COLS / 2; ++i) acc[i] = 0ull;
             for (int kb = kb0; kb < kb1; ++kb) {
                 ok = warp_wait(&sc_full[slot], phase, abort_flag, g.status) &&
                      warp_wait(&acc_full[buf], acc_phase, abort_flag, g.status);
                 if (!ok) break;
                 tc::tc_fence_after();
-                const float* s = sc + slot * C::SC_FLOATS;
-                const float sp = s[p_lane];
-                const float* sq = s + 128 + half * C::COLS;
+                const float* s = sc + slot * C::SC_FLOATS + half * C::COLS;
+                const float own = UNI ? 1.f : sc[slot * C::SC_FLOATS + NT + p_lane];
+                const uint64_t sp = pair_of(own, own);
+                uint32_t r[2][STEP];
+                tmem_ld<STEP>(t_lane + buf * NT, r[0]);
 #pragma unroll
-                for (int i = 0; i < C::COLS; i += STEP) {
-                    uint32_t r[STEP];
-                    tmem_ld<STEP>(t_lane + buf * NT + i, r);
+                for (int i = 0; i < STEPS; ++i) {
                     tc::tmem_ld_wait();
+                    if (i + 1 < STEPS) {
+                        tmem_ld<STEP>(t_lane + buf * NT + (i + 1) * STEP, r[(i + 1) & 1]);
+                    } else {
+                        tc::tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) tc::mbar_arrive(&acc_empty[buf]);
+                    }
 #pragma unroll
-                    for (int j = 0; j < STEP; ++j)
-                        acc[i + j] = fmaf(__uint_as_float(r[j]), sp * sq[i + j], acc[i + j]);
+                    for (int j = 0; j < STEP; j += 4) {
+                        const float4 v = *reinterpret_cast<const float4*>(s + i * STEP + j);
+                        uint64_t s0 = pair_of(v.x, v.y), s1 = pair_of(v.z, v.w);
+                        if (!UNI) {
+                            s0 = mul_pair(s0, sp);
+                            s1 = mul_pair(s1, sp);
+                        }
+                        uint64_t* to = &acc[(i * STEP + j) / 2];
+                        const uint32_t* d = &r[i & 1][j];
+                        to[0] = fma_pair(pair_of(d[0], d[1]), s0, to[0]);
+                        to[1] = fma_pair(pair_of(d[2], d[3]), s1, to[1]);
+                    }
                 }
-                tc::tc_fence_before();
                 __syncwarp();
-                if (lane == 0) {
-                    tc::mbar_arrive(&acc_empty[buf]);
-                    tc::mbar_arrive(&sc_empty[slot]);
-                }
+                if (lane == 0) tc::mbar_arrive(&sc_empty[slot]);
                 if (++slot == SC_SLOTS) { slot = 0; phase ^= 1; }
                 if (++buf == C::BUFS) { buf = 0; acc_phase ^= 1; }
             }
             if (!ok) break;
-            const int n = p0 + p_lane;
             if (parts == 1) {
+                const int n = p0 + p_lane, m0 = q0 + half * C::COLS;
+                const int64_t at = (int64_t)m0 * g.ldc + n;
                 if (n < g.N) {
-#pragma unroll
-                    for (int i = 0; i < C::COLS; ++i) {
-                        const int m = q0 + half * C::COLS + i;
-                        if (m < g.M) put(g.c, g.ctype, (int64_t)m * g.ldc + n, acc[i]);
-                    }
+                    if (g.ctype == QMOE_F32) put_cols<C::COLS>(static_cast<float*>(g.c) + at, g.ldc, g.M - m0, acc);
+                    else if (g.ctype == QMOE_BF16)
+                        put_cols<C::COLS>(static_cast<__nv_bfloat16*>(g.c) + at, g.ldc, g.M - m0, acc);
+                    else put_cols<C::COLS>(static_cast<__half*>(g.c) + at, g.ldc, g.M - m0, acc);
                 }
             } else {
                 // every load of this CTA's only tile has been consumed: the ring is free
                 float* sums = reinterpret_cast<float*>(smem);
 #pragma unroll
-                for (int i = 0; i < C::COLS; ++i) sums[(half * C::COLS + i) * 128 + p_lane] = acc[i];
+                for (int i = 0; i < C::COLS / 2; ++i) {
+                    const float2 v = halves_of(acc[i]);
+                    sums[(half * C::COLS + 2 * i) * 128 + p_lane] = v.x;
+                    sums[(half * C::COLS + 2 * i + 1) * 128 + p_lane] = v.y;
+                }
             }
         }
     }
@@ -376,10 +449,11 @@ inline Plan plan_of(int M, int N, int K) {
     return p;
 }
 
-template <int NT>
+template <int NT, bool UNI>
 static int gemm_launch(const CUtensorMap& ma, const CUtensorMap& mb, const GemmArgs& g, int parts, cudaStream_t st) {
-    using C = GemmCfg<NT>;
-    if (cudaFuncSetAttribute(fp8_gemm_kernel<NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM) != cudaSuccess)
+    using C = GemmCfg<NT, UNI>;
+    auto kernel = fp8_gemm_kernel<NT, UNI>;
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM) != cudaSuccess)
         return QMOE_ERR_CUDA;
     const int64_t tiles = (int64_t)((g.N + 127) / 128) * ((g.M + NT - 1) / NT);
     cudaLaunchAttribute attr[2];
@@ -397,7 +471,12 @@ static int gemm_launch(const CUtensorMap& ma, const CUtensorMap& mb, const GemmA
     cfg.stream = st;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, fp8_gemm_kernel<NT>, ma, mb, g) == cudaSuccess ? QMOE_OK : QMOE_ERR_LAUNCH;
+    return cudaLaunchKernelEx(&cfg, kernel, ma, mb, g) == cudaSuccess ? QMOE_OK : QMOE_ERR_LAUNCH;
+}
+
+template <int NT>
+static int gemm_kind(const CUtensorMap& ma, const CUtensorMap& mb, const GemmArgs& g, int parts, cudaStream_t st) {
+    return g.b.shift ? gemm_launch<NT, true>(ma, mb, g, parts, st) : gemm_launch<NT, false>(ma, mb, g, parts, st);
 }
 
 static int gemm_run(const qmoe_fp8_mat* a, const qmoe_fp8_mat* b, GemmArgs& g, cudaStream_t st) {
@@ -408,11 +487,11 @@ static int gemm_run(const qmoe_fp8_mat* a, const qmoe_fp8_mat* b, GemmArgs& g, c
     rc = code_map(&mb, b->q, b->ld, g.N, g.K, 128);
     if (rc != QMOE_OK) return rc;
     switch (p.nt) {
-        case 16: return gemm_launch<16>(ma, mb, g, p.parts, st);
-        case 32: return gemm_launch<32>(ma, mb, g, p.parts, st);
-        case 64: return gemm_launch<64>(ma, mb, g, p.parts, st);
-        case 128: return gemm_launch<128>(ma, mb, g, p.parts, st);
-        default: return gemm_launch<256>(ma, mb, g, p.parts, st);
+        case 16: return gemm_kind<16>(ma, mb, g, p.parts, st);
+        case 32: return gemm_kind<32>(ma, mb, g, p.parts, st);
+        case 64: return gemm_kind<64>(ma, mb, g, p.parts, st);
+        case 128: return gemm_kind<128>(ma, mb, g, p.parts, st);
+        default: return gemm_kind<256>(ma, mb, g, p.parts, st);
     }
 }
 

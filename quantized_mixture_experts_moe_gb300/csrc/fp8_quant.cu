@@ -19,8 +19,14 @@ constexpr float AMAX_MIN = 7.888609052210118e-31f;  // 2^-100
 
 __device__ __forceinline__ float inverse_of(float amax) { return __fdiv_rn(448.f, amax); }
 __device__ __forceinline__ float scale_of(float amax) { return __fdiv_rn(amax, 448.f); }
+// 8 values of a row as they lie in memory.
+template <typename T> using Raw8 = row::Raw<T, 8>;
+
 // fmaxf drops a NaN; its own code is still NaN.
-__device__ __forceinline__ float amax8(const float (&v)[8], float m) {
+template <typename T>
+__device__ __forceinline__ float amax8(const Raw8<T>& r, float m) {
+    float v[8];
+    row::widen<8>(r, v);
 #pragma unroll
     for (int i = 0; i < 8; ++i) m = fmaxf(m, fabsf(v[i]));
     return m;
@@ -33,40 +39,62 @@ __device__ __forceinline__ uint2 codes8(const float (&v)[8], float inv) {
           ((uint32_t)e4m3x2_from_float(__fmul_rn(v[6], inv), __fmul_rn(v[7], inv)) << 16);
     return q;
 }
-
-// 8 values of a row from column c on; zeros past the row's end.
-template <typename T, bool VEC>
-__device__ __forceinline__ void load8(const T* row, int64_t c, int64_t cols, float (&v)[8]) {
-    if (VEC) {
-        if (c < cols) {
-            row::load<8>(row + c, v);
-            return;
-        }
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = 0.f;
-    } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = c + i < cols ? row::to_f32(row[c + i]) : 0.f;
-    }
+template <typename T>
+__device__ __forceinline__ uint2 codes8(const Raw8<T>& r, float inv) {
+    float v[8];
+    row::widen<8>(r, v);
+    return codes8(v, inv);
 }
 
-// One row block of 128 for each half warp.
+__device__ __forceinline__ void set8(Raw8<float>& r, const float (&v)[8]) {
+    r.a = make_float4(v[0], v[1], v[2], v[3]);
+    r.b = make_float4(v[4], v[5], v[6], v[7]);
+}
+template <typename T>
+__device__ __forceinline__ void set8(Raw8<T>& r, const float (&v)[8]) {
+    r.v = make_uint4(row::pack2(v[0], v[1], T{}), row::pack2(v[2], v[3], T{}), row::pack2(v[4], v[5], T{}),
+                     row::pack2(v[6], v[7], T{}));
+}
+
+// 8 values of a row from column c on; zeros past the row's end, and where the row is not `real`.
+template <typename T, bool VEC>
+__device__ __forceinline__ void load8(const T* row, bool real, int64_t c, int64_t cols, Raw8<T>& r) {
+    if (VEC && real && c < cols) {
+        row::load_raw<8>(r, row + c);
+        return;
+    }
+    float v[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = !VEC && real && c + i < cols ? row::to_f32(row[c + i]) : 0.f;
+    set8(r, v);
+}
+
+// A warp takes 8 row blocks of 128 at a time (1024 columns of a row), two to a
+// pass, a block for each half of the warp; the loads of all go out first.
+constexpr int ROW_PASSES = 4;
+
 template <typename T, bool VEC>
 __global__ void __launch_bounds__(256)
-quant_rows_kernel(const T* __restrict__ x, int64_t ldx, int64_t rows, int64_t cols, int64_t blocks,
+quant_rows_kernel(const T* __restrict__ x, int64_t ldx, int64_t rows, int64_t cols, int chunks,
                   uint8_t* __restrict__ q, int64_t ldq, float* __restrict__ s) {
-    const int64_t n = rows * blocks;
-    const int lane = threadIdx.x & 15;
+    const int lane = threadIdx.x & 31, half = lane >> 4;
+    const int64_t n = rows * chunks;
     pdl_sync();
-    for (int64_t b = (int64_t)blockIdx.x * 16 + (threadIdx.x >> 4); b < n; b += (int64_t)gridDim.x * 16) {
-        const int64_t r = b / blocks, kb = b - r * blocks, c = kb * 128 + lane * 8;
-        float v[8];
-        load8<T, VEC>(x + r * ldx, c, cols, v);
-        float m = amax8(v, AMAX_MIN);
+    for (int64_t u = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5); u < n; u += (int64_t)gridDim.x * 8) {
+        const int64_t r = n < (1ll << 31) ? (int64_t)((uint32_t)u / (uint32_t)chunks) : u / chunks;
+        const int64_t c0 = (u - r * chunks) * (ROW_PASSES * 256) + lane * 8;
+        Raw8<T> v[ROW_PASSES];
 #pragma unroll
-        for (int o = 8; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFu << (threadIdx.x & 16), m, o));
-        if (c < cols) *reinterpret_cast<uint2*>(q + r * ldq + c) = codes8(v, inverse_of(m));
-        if (lane == 0) s[kb * rows + r] = scale_of(m);
+        for (int i = 0; i < ROW_PASSES; ++i) load8<T, VEC>(x + r * ldx, true, c0 + i * 256, cols, v[i]);
+#pragma unroll
+        for (int i = 0; i < ROW_PASSES; ++i) {
+            const int64_t c = c0 + i * 256;
+            float m = amax8<T>(v[i], AMAX_MIN);
+#pragma unroll
+            for (int o = 8; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+            if (c < cols) *reinterpret_cast<uint2*>(q + r * ldq + c) = codes8<T>(v[i], inverse_of(m));
+            if ((lane & 15) == 0 && c < cols) s[(c >> 7) * rows + r] = scale_of(m);
+        }
     }
 }
 
@@ -88,7 +116,7 @@ struct TileArgs {
 constexpr int TPITCH = 144;  // bytes between the columns of the transposed tile
 
 template <typename T, bool VEC, int MODE>
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(256, sizeof(T) == 2 ? 4 : 2)
 quant_tile_kernel(const TileArgs a) {
     __shared__ __align__(16) uint8_t tile[128 * TPITCH];
     __shared__ float part[8][128];
@@ -98,25 +126,26 @@ quant_tile_kernel(const TileArgs a) {
     const int64_t r0 = (int64_t)blockIdx.y * 128, c0 = (int64_t)blockIdx.x * 128;
     const int64_t c = c0 + cg * 8;
     pdl_sync();
-    float v[8][8];
+    Raw8<T> v[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
         const int64_t r = r0 + rg * 8 + i;
-        if (r < a.rows) {
-            load8<T, VEC>(static_cast<const T*>(a.x) + r * a.ldx, c, a.cols, v[i]);
-        } else {
-#pragma unroll
-            for (int j = 0; j < 8; ++j) v[i][j] = 0.f;
-        }
+        load8<T, VEC>(static_cast<const T*>(a.x) + r * a.ldx, r < a.rows, c, a.cols, v[i]);
     }
     float inv_c[8];
     if (MODE == 0) {
         float m[8];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            m[j] = AMAX_MIN;
+        for (int j = 0; j < 8; ++j) m[j] = AMAX_MIN;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) m[j] = fmaxf(m[j], fabsf(v[i][j]));
+        for (int i = 0; i < 8; ++i) {
+            float t[8];
+            row::widen<8>(v[i], t);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) m[j] = fmaxf(m[j], fabsf(t[j]));
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
             m[j] = fmaxf(m[j], __shfl_xor_sync(0xFFFFFFFFu, m[j], 16));
             if (lane < 16) part[warp][cg * 8 + j] = m[j];
         }
@@ -135,11 +164,11 @@ quant_tile_kernel(const TileArgs a) {
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 const int64_t r = r0 + rg * 8 + i;
-                float t = amax8(v[i], AMAX_MIN);
+                float t = amax8<T>(v[i], AMAX_MIN);
 #pragma unroll
                 for (int o = 8; o > 0; o >>= 1) t = fmaxf(t, __shfl_xor_sync(0xFFFFFFFFu, t, o));
                 if (r < a.rows) {
-                    if (c < a.cols) *reinterpret_cast<uint2*>(a.q + r * a.ldq + c) = codes8(v[i], inverse_of(t));
+                    if (c < a.cols) *reinterpret_cast<uint2*>(a.q + r * a.ldq + c) = codes8<T>(v[i], inverse_of(t));
                     if (cg == 0) a.s[(int64_t)blockIdx.x * a.rows + r] = scale_of(t);
                 }
             }
@@ -147,7 +176,7 @@ quant_tile_kernel(const TileArgs a) {
     } else {
         float m = AMAX_MIN;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) m = amax8(v[i], m);
+        for (int i = 0; i < 8; ++i) m = amax8<T>(v[i], m);
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
         if (lane == 0) part[0][warp] = m;
@@ -162,7 +191,7 @@ quant_tile_kernel(const TileArgs a) {
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 const int64_t r = r0 + rg * 8 + i;
-                if (r < a.rows) *reinterpret_cast<uint2*>(a.q + r * a.ldq + c) = codes8(v[i], inv);
+                if (r < a.rows) *reinterpret_cast<uint2*>(a.q + r * a.ldq + c) = codes8<T>(v[i], inv);
             }
         }
     }
@@ -171,7 +200,11 @@ quant_tile_kernel(const TileArgs a) {
     for (int j = 0; j < 8; ++j) {
         float t[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) t[i] = v[i][j];
+        for (int i = 0; i < 8; ++i) {
+            float w[8];
+            row::widen<8>(v[i], w);
+            t[i] = w[j];
+        }
         *reinterpret_cast<uint2*>(&tile[(cg * 8 + j) * TPITCH + rg * 8]) = codes8(t, inv_c[j]);
     }
     __syncthreads();
@@ -189,11 +222,12 @@ quant_tile_kernel(const TileArgs a) {
 template <typename T>
 int rows_launch(int64_t rows, int64_t cols, const T* x, int64_t ldx, uint8_t* q, int64_t ldq, float* s,
                 cudaStream_t st) {
-    const int64_t blocks = (cols + 127) / 128, ctas = (rows * blocks + 15) / 16, most = (int64_t)row::kSMs * 8;
+    const int chunks = (int)((cols + ROW_PASSES * 256 - 1) / (ROW_PASSES * 256));
+    const int64_t ctas = (rows * chunks + 7) / 8, most = (int64_t)row::kSMs * 8;
     const unsigned grid = (unsigned)(ctas < most ? ctas : most);
     const bool vec = cols % 8 == 0 && aligned16(x) && (ldx * sizeof(T)) % 16 == 0;
-    if (vec) return launch_pdl(quant_rows_kernel<T, true>, grid, 256, 0, st, x, ldx, rows, cols, blocks, q, ldq, s);
-    return launch_pdl(quant_rows_kernel<T, false>, grid, 256, 0, st, x, ldx, rows, cols, blocks, q, ldq, s);
+    if (vec) return launch_pdl(quant_rows_kernel<T, true>, grid, 256, 0, st, x, ldx, rows, cols, chunks, q, ldq, s);
+    return launch_pdl(quant_rows_kernel<T, false>, grid, 256, 0, st, x, ldx, rows, cols, chunks, q, ldq, s);
 }
 
 int quant_rows_launch(int64_t rows, int64_t cols, int dtype, const void* x, int64_t ldx, uint8_t* q, int64_t ldq,

@@ -7,8 +7,7 @@
 // and y are read once and out and n written once (8 bytes a column in 16-bit
 // types), and the second sum runs on values already at hand.  The bound is
 // HBM; what there is besides are the two sums of a row, each a latency of two
-// shuffles' trees and a barrier.  A CTA therefore asks for its next row before
-// it sums the present one.
+// shuffles' trees and a barrier, which the rows on their way hide.
 #include "norm_block.cuh"
 
 namespace qmoe {
@@ -16,15 +15,11 @@ namespace norm {
 
 struct FwdArgs {
     int64_t rows;
-    int cols;
-    const void* r;  // the stream (norm_pre: x)
-    int64_t ldr;
-    const void* y;
-    int64_t ldy;
+    int cols, stages, stage_bytes;
+    Source r, y, full_gate;  // r: the stream (norm_pre: x)
     const float* w;
     int gate_mode;
-    const void* gate;
-    int64_t ldg;
+    const float* gate;
     float alpha, eps;
     const float* w_next;
     void* out;
@@ -36,89 +31,89 @@ struct FwdArgs {
 
 // POST: y, its norm and gate; without it the kernel is norm_pre (out = r, not written).
 template <typename RT, typename YT, int NV, int VEC, bool POST>
-__global__ void __launch_bounds__(NV * VEC > 8 ? 512 : 1024)
+__global__ void __launch_bounds__(512, NV * VEC > 8 ? 1 : 2)
 norm_fwd_kernel(const FwdArgs a) {
     constexpr int E = NV * VEC;
     constexpr bool KEEP = E <= 8;  // the weights stay in registers from row to row
-    __shared__ float2 sums[2][32];
-    const int tx = threadIdx.x, step = blockDim.x * VEC, cols = a.cols;
+    __shared__ __align__(16) float sums[2][16];
+    extern __shared__ __align__(16) uint8_t ring[];
+    const int tx = threadIdx.x, cols = a.cols, stages = a.stages;
     const int64_t stride = (int64_t)gridDim.x * blockDim.y;
+    uint8_t* const mine = ring + (int64_t)threadIdx.y * stages * a.stage_bytes;
     const float inv_cols = 1.f / (float)cols;
     int flip = 0;
 
-    float w[KEEP ? E : 1], wn[KEEP ? E : 1], gc[KEEP ? E : 1];
-    row::Raw<RT, VEC> rr[NV];
-    row::Raw<YT, VEC> ry[NV];
-    auto fetch = [&](int64_t row) {
-#pragma unroll
-        for (int v = 0; v < NV; ++v) {
-            const int c = v * step + tx * VEC;
-            if (c >= cols) continue;
-            if (POST) row::load_raw<VEC>(ry[v], static_cast<const YT*>(a.y) + row * a.ldy + c);
-            row::load_raw<VEC>(rr[v], static_cast<const RT*>(a.r) + row * a.ldr + c);
+    auto fetch = [&](int64_t row, int stage) {
+        if (row < a.rows) {
+            uint8_t* to = mine + stage * a.stage_bytes;
+            copy_row<VEC, NV, RT>(a.r, to, row, a.rows, cols);
+            if (POST) copy_row<VEC, NV, YT>(a.y, to, row, a.rows, cols);
+            if (POST) copy_row<VEC, NV, YT>(a.full_gate, to, row, a.rows, cols);
         }
+        tc::cp_async_commit();
     };
     int64_t row = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
     pdl_sync();
-    if (row < a.rows) fetch(row);
+    for (int i = 0; i + 1 < stages; ++i) fetch(row + i * stride, i);
+    // what a column of y and of out is multiplied by: w and a column gate in one
+    float wg[KEEP ? E : 1], wn[KEEP ? E : 1];
+    auto col_factor = [&](int c, float* f) {
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) f[i] = 1.f;
+        if (a.w) row::load<VEC>(a.w + c, f);
+        if (a.gate_mode == QMOE_GATE_COL) {
+            float g[VEC];
+            row::load<VEC>(a.gate + c, g);
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) f[i] *= g[i];
+        }
+    };
     if (KEEP) {
 #pragma unroll
         for (int v = 0; v < NV; ++v) {
-            const int c = v * step + tx * VEC;
+            const int c = (v * blockDim.x + tx) * VEC;
             if (c >= cols) continue;
-            if (POST && a.w) row::load<VEC>(a.w + c, &w[v * VEC]);
+            if (POST) col_factor(c, &wg[v * VEC]);
             if (a.w_next) row::load<VEC>(a.w_next + c, &wn[v * VEC]);
-            if (POST && a.gate_mode == QMOE_GATE_COL)
-                row::load<VEC>(static_cast<const float*>(a.gate) + c, &gc[v * VEC]);
         }
     }
+    int stage = 0;
     for (; row < a.rows; row += stride) {
-        float o[E], y[POST ? E : 1];
-#pragma unroll
-        for (int v = 0; v < NV; ++v) {
-            if (v * step + tx * VEC < cols) {
-                row::widen<VEC>(rr[v], &o[v * VEC]);
-                if (POST) row::widen<VEC>(ry[v], &y[v * VEC]);
-            } else {
-#pragma unroll
-                for (int i = 0; i < VEC; ++i) {
-                    o[v * VEC + i] = 0.f;
-                    if (POST) y[v * VEC + i] = 0.f;
-                }
-            }
-        }
-        if (row + stride < a.rows) fetch(row + stride);
+        const float g_row = POST && a.gate_mode == QMOE_GATE_ROW ? a.gate[row] : 1.f;
+        next_row<VEC>(stages, stage, [&](int ahead, int to) { fetch(row + ahead * stride, to); });
+        const uint8_t* const from = mine + stage * a.stage_bytes;
+        if (++stage == stages) stage = 0;
+        float o[E];
+        read_row<VEC, NV, true, RT>(a.r, from, row, cols, o);
         if (POST) {
-            float scale = a.alpha;
+            float y[E];
+            read_row<VEC, NV, true, YT>(a.y, from, row, cols, y);
+            float scale = a.alpha * g_row;
             if (a.w) {
                 float s = 0.f;
 #pragma unroll
                 for (int i = 0; i < E; ++i) s = fmaf(y[i], y[i], s);
-                const float rstd = rsqrtf(row::row_sum(s, 0.f, sums[flip]).x * inv_cols + a.eps);
+                const float rstd = rsqrtf(row::row_sum(s, sums[flip]) * inv_cols + a.eps);
                 flip ^= 1;
                 if (tx == 0 && a.rstd) a.rstd[row] = rstd;
                 scale *= rstd;
             }
-            if (a.gate_mode == QMOE_GATE_ROW) scale *= static_cast<const float*>(a.gate)[row];
+            if (a.gate_mode == QMOE_GATE_FULL) {
+                float g[E];
+                read_row<VEC, NV, true, YT>(a.full_gate, from, row, cols, g);
+#pragma unroll
+                for (int i = 0; i < E; ++i) y[i] *= g[i];
+            }
 #pragma unroll
             for (int v = 0; v < NV; ++v) {
-                const int c = v * step + tx * VEC;
+                const int c = (v * blockDim.x + tx) * VEC;
                 if (c >= cols) continue;
-                float g[VEC];
-                if (a.gate_mode == QMOE_GATE_FULL)
-                    row::load<VEC>(static_cast<const YT*>(a.gate) + row * a.ldg + c, g);
-                else if (!KEEP && a.gate_mode == QMOE_GATE_COL)
-                    row::load<VEC>(static_cast<const float*>(a.gate) + c, g);
-                float wv[VEC];
-                if (!KEEP && a.w) row::load<VEC>(a.w + c, wv);
+                float f[VEC];
+                if (!KEEP) col_factor(c, f);
 #pragma unroll
                 for (int i = 0; i < VEC; ++i) {
                     const int e = v * VEC + i;
-                    float z = y[e] * scale;
-                    if (a.w) z *= KEEP ? w[e] : wv[i];
-                    if (a.gate_mode == QMOE_GATE_FULL) z *= g[i];
-                    else if (a.gate_mode == QMOE_GATE_COL) z *= KEEP ? gc[e] : g[i];
-                    o[e] += z;
+                    o[e] = fmaf(y[e] * scale, KEEP ? wg[e] : f[i], o[e]);
                 }
                 row::store<VEC>(static_cast<RT*>(a.out) + row * a.ldo + c, &o[v * VEC]);
             }
@@ -127,12 +122,12 @@ norm_fwd_kernel(const FwdArgs a) {
             float s = 0.f;
 #pragma unroll
             for (int i = 0; i < E; ++i) s = fmaf(o[i], o[i], s);
-            const float rstd = rsqrtf(row::row_sum(s, 0.f, sums[flip]).x * inv_cols + a.eps);
+            const float rstd = rsqrtf(row::row_sum(s, sums[flip]) * inv_cols + a.eps);
             flip ^= 1;
             if (tx == 0 && a.rstd_next) a.rstd_next[row] = rstd;
 #pragma unroll
             for (int v = 0; v < NV; ++v) {
-                const int c = v * step + tx * VEC;
+                const int c = (v * blockDim.x + tx) * VEC;
                 if (c >= cols) continue;
                 float wv[VEC];
                 if (!KEEP) row::load<VEC>(a.w_next + c, wv);
@@ -145,24 +140,42 @@ norm_fwd_kernel(const FwdArgs a) {
     }
 }
 
+template <typename K>
+inline int start(K kernel, const Shape& s, FwdArgs& a, int row_bytes, cudaStream_t st) {
+    const int threads = s.threads * s.rows_per_cta;
+    const int64_t ctas = (a.rows + s.rows_per_cta - 1) / s.rows_per_cta;
+    // one wave: 1024 threads an SM where a thread holds 8 values, else 512; fewer CTAs where that leaves each two stages
+    int per_sm = (s.values() > 8 ? 512 : 1024) / threads;
+    a.stage_bytes = row_bytes;
+    while (per_sm > 1 && stages_of((int64_t)row_bytes * s.rows_per_cta, 0, per_sm) < 2) --per_sm;
+    a.stages = stages_of((int64_t)row_bytes * s.rows_per_cta, 0, per_sm);
+    if (!a.stages) return QMOE_ERR_UNSUPPORTED;
+    const int64_t fit = (int64_t)row::kSMs * per_sm;
+    const size_t smem = (size_t)a.stages * row_bytes * s.rows_per_cta;
+    if (smem > 48 * 1024 - 1024 &&
+        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 225 * 1024) != cudaSuccess)
+        return QMOE_ERR_CUDA;
+    return launch_pdl(kernel, dim3((unsigned)(ctas < fit ? ctas : fit)), dim3(s.threads, s.rows_per_cta), smem, st, a);
+}
+
 template <bool POST>
 struct Fwd {
     template <typename RT, typename YT>
     struct Go {
-        static int go(const FwdArgs& a, bool vec, cudaStream_t st) {
-            const Shape s = shape_of(a.cols, vec, 512);
-            const dim3 block(s.threads, s.rows_per_cta);
-            const int64_t ctas = (a.rows + s.rows_per_cta - 1) / s.rows_per_cta;
-            const int64_t fit = (int64_t)row::kSMs * (1024 / (s.threads * s.rows_per_cta));
-            const dim3 grid((unsigned)(ctas < fit ? ctas : fit));
-            if (s.vec == 8) {
-                if (s.nv == 1) return launch_pdl(norm_fwd_kernel<RT, YT, 1, 8, POST>, grid, block, 0, st, a);
-                if (s.nv == 2) return launch_pdl(norm_fwd_kernel<RT, YT, 2, 8, POST>, grid, block, 0, st, a);
-                return launch_pdl(norm_fwd_kernel<RT, YT, 4, 8, POST>, grid, block, 0, st, a);
+        static int go(FwdArgs& a, bool vec, cudaStream_t st) {
+            const Shape s = shape_of(a.cols, vec);
+            const int rb = stage_bytes(a.cols, sizeof(RT)), yb = stage_bytes(a.cols, sizeof(YT));
+            a.y.off = rb;
+            a.full_gate.off = rb + yb;
+            const int bytes = rb + (POST ? yb : 0) + (a.full_gate.p ? yb : 0);
+            if (vec) {
+                if (s.nv == 1) return start(norm_fwd_kernel<RT, YT, 1, 8, POST>, s, a, bytes, st);
+                if (s.nv == 2) return start(norm_fwd_kernel<RT, YT, 2, 8, POST>, s, a, bytes, st);
+                return start(norm_fwd_kernel<RT, YT, 4, 8, POST>, s, a, bytes, st);
             }
-            if (s.nv == 4) return launch_pdl(norm_fwd_kernel<RT, YT, 4, 1, POST>, grid, block, 0, st, a);
-            if (s.nv == 16) return launch_pdl(norm_fwd_kernel<RT, YT, 16, 1, POST>, grid, block, 0, st, a);
-            return launch_pdl(norm_fwd_kernel<RT, YT, 32, 1, POST>, grid, block, 0, st, a);
+            if (s.nv == 8) return start(norm_fwd_kernel<RT, YT, 8, 1, POST>, s, a, bytes, st);
+            if (s.nv == 16) return start(norm_fwd_kernel<RT, YT, 16, 1, POST>, s, a, bytes, st);
+            return start(norm_fwd_kernel<RT, YT, 32, 1, POST>, s, a, bytes, st);
         }
     };
 };
@@ -187,8 +200,7 @@ extern "C" int qmoe_norm_pre(int64_t rows, int64_t cols, int stream_dtype, int b
     norm::FwdArgs a = {};
     a.rows = rows;
     a.cols = (int)cols;
-    a.r = x;
-    a.ldr = ldx;
+    a.r = {x, ldx, 0};
     a.w_next = w;
     a.eps = eps;
     a.n = n;
@@ -220,14 +232,12 @@ extern "C" int qmoe_norm_post(int64_t rows, int64_t cols, int stream_dtype, int 
     norm::FwdArgs a = {};
     a.rows = rows;
     a.cols = (int)cols;
-    a.r = r;
-    a.ldr = ldr;
-    a.y = y;
-    a.ldy = ldy;
+    a.r = {r, ldr, 0};
+    a.y = {y, ldy, 0};
     a.w = w;
     a.gate_mode = gate_mode;
-    a.gate = gate;
-    a.ldg = ldg;
+    if (gate_mode == QMOE_GATE_FULL) a.full_gate = {gate, ldg, 0};
+    else a.gate = static_cast<const float*>(gate);
     a.alpha = alpha;
     a.eps = eps;
     a.w_next = w_next;

@@ -8,7 +8,7 @@
 // norm_pre's gradient is the first line alone.  As in the forward, a row lives
 // in registers and is read and written once; HBM is the bound (6 values a
 // column for the whole sandwich).  The sums over rows stay in registers (rows
-// of up to 8 values a thread) or in shared memory words that one thread owns,
+// of up to 16 values a thread) or in shared memory words that one thread owns,
 // over all the rows of a CTA; each CTA then writes one partial row, and a
 // second launch adds the partial rows in a fixed order, so no atomic decides
 // an order.
@@ -19,22 +19,16 @@ namespace norm {
 
 struct BwdArgs {
     int64_t rows;
-    int cols;
-    const void* dout;  // stream type; may be null (norm_pre: dres)
-    int64_t lddout;
-    const void* dn;  // block type; null: no next norm
-    int64_t lddn;
-    const void* out;  // stream type: what the next norm read (norm_pre: x)
-    int64_t ldo;
+    int cols, stages, stage_bytes;
+    // dout (norm_pre: dres) and out (what the next norm read; norm_pre: x) have the stream's type, dn, y and a full
+    // gate the block's; dn null: no next norm
+    Source dout, dn, out, y, full_gate;
     const float* w_next;
     const float* rstd_next;
-    const void* y;
-    int64_t ldy;
     const float* w;
     const float* rstd;
     int gate_mode;
-    const void* gate;
-    int64_t ldg;
+    const float* gate;
     float alpha;
     void* dr;
     int64_t lddr;
@@ -73,80 +67,82 @@ struct ColSums {
     }
 };
 
+// RING: the rows come through shared memory stages; else, where the widest
+// rows' column sums leave no room for them, straight from the matrices.
 template <typename RT, typename YT, int NV, int VEC, bool POST>
-__global__ void __launch_bounds__(VEC == 1 && NV == 4 ? 1024 : 512)
+__global__ void __launch_bounds__(512, 1)
 norm_bwd_kernel(const BwdArgs a) {
     constexpr int E = NV * VEC;
-    constexpr bool SMEM = E > 8;
-    constexpr bool KEEP = E <= 8 && !(VEC == 1);
-    __shared__ float2 sums[2][32];
-    extern __shared__ float cols_smem[];
-    const int tx = threadIdx.x, step = blockDim.x * VEC, cols = a.cols;
+    constexpr bool SMEM = E > 16, RING = !SMEM;
+    constexpr bool KEEP = E <= 8;
+    __shared__ __align__(16) float sums[2][16];
+    extern __shared__ __align__(16) uint8_t dynamic[];  // column sums, then the ring
+    const int tx = threadIdx.x, cols = a.cols, stages = a.stages;
     const int64_t stride = (int64_t)gridDim.x * blockDim.y;
     const float inv_cols = 1.f / (float)cols;
-    const bool next = POST ? a.dn != nullptr : true;
+    const bool next = POST ? a.dn.p != nullptr : true;
     int flip = 0;
 
     ColSums<E, VEC, SMEM> sum_wn, sum_w, sum_g;
+    float* const cols_smem = reinterpret_cast<float*>(dynamic);
     sum_wn.init(cols_smem);
     if (POST) {
         sum_w.init(cols_smem + E * blockDim.x);
         sum_g.init(cols_smem + 2 * E * blockDim.x);
     }
-    float w[KEEP ? E : 1], wn[KEEP ? E : 1];
-    row::Raw<RT, VEC> r_do[NV], r_out[NV];
-    row::Raw<YT, VEC> r_dn[NV], r_y[NV];
-    auto fetch = [&](int64_t row) {
-#pragma unroll
-        for (int v = 0; v < NV; ++v) {
-            const int c = v * step + tx * VEC;
-            if (c >= cols) continue;
-            if (a.dout) row::load_raw<VEC>(r_do[v], static_cast<const RT*>(a.dout) + row * a.lddout + c);
-            if (next) {
-                row::load_raw<VEC>(r_dn[v], static_cast<const YT*>(a.dn) + row * a.lddn + c);
-                row::load_raw<VEC>(r_out[v], static_cast<const RT*>(a.out) + row * a.ldo + c);
-            }
-            if (POST) row::load_raw<VEC>(r_y[v], static_cast<const YT*>(a.y) + row * a.ldy + c);
+    uint8_t* const mine = dynamic + (SMEM ? (POST ? 3 : 1) * E * blockDim.x * 4 : 0) +
+                          (int64_t)threadIdx.y * stages * a.stage_bytes;
+    auto fetch = [&](int64_t row, int stage) {
+        if (row < a.rows) {
+            uint8_t* to = mine + stage * a.stage_bytes;
+            copy_row<VEC, NV, RT>(a.dout, to, row, a.rows, cols);
+            copy_row<VEC, NV, YT>(a.dn, to, row, a.rows, cols);
+            copy_row<VEC, NV, RT>(a.out, to, row, a.rows, cols);
+            if (POST) copy_row<VEC, NV, YT>(a.y, to, row, a.rows, cols);
+            if (POST) copy_row<VEC, NV, YT>(a.full_gate, to, row, a.rows, cols);
         }
+        tc::cp_async_commit();
     };
     int64_t row = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
     pdl_sync();
-    if (row < a.rows) fetch(row);
+    if (RING)
+        for (int i = 0; i + 1 < stages; ++i) fetch(row + i * stride, i);
+    float w[KEEP ? E : 1], wn[KEEP ? E : 1], gc[KEEP ? E : 1];
     if (KEEP) {
 #pragma unroll
         for (int v = 0; v < NV; ++v) {
-            const int c = v * step + tx * VEC;
+            const int c = (v * blockDim.x + tx) * VEC;
             if (c >= cols) continue;
             if (POST && a.w) row::load<VEC>(a.w + c, &w[v * VEC]);
             if (next) row::load<VEC>(a.w_next + c, &wn[v * VEC]);
+            if (POST && a.gate_mode == QMOE_GATE_COL) row::load<VEC>(a.gate + c, &gc[v * VEC]);
         }
     }
+    int stage = 0;
     for (; row < a.rows; row += stride) {
-        float d[E], x[E], dn[E], y[POST ? E : 1];
         const float rstd_n = next ? a.rstd_next[row] : 0.f;
-#pragma unroll
-        for (int v = 0; v < NV; ++v) {
-            const int c = v * step + tx * VEC;
-#pragma unroll
-            for (int i = 0; i < VEC; ++i) {
-                d[v * VEC + i] = x[v * VEC + i] = dn[v * VEC + i] = 0.f;
-                if (POST) y[v * VEC + i] = 0.f;
-            }
-            if (c < cols) {
-                if (a.dout) row::widen<VEC>(r_do[v], &d[v * VEC]);
-                if (next) {
-                    row::widen<VEC>(r_dn[v], &dn[v * VEC]);
-                    row::widen<VEC>(r_out[v], &x[v * VEC]);
-                }
-                if (POST) row::widen<VEC>(r_y[v], &y[v * VEC]);
-            }
+        const float rstd = POST && a.w ? a.rstd[row] : 1.f;
+        const float g_row = POST && a.gate_mode == QMOE_GATE_ROW ? a.gate[row] : 1.f;
+        const uint8_t* from = nullptr;
+        if (RING) {
+            next_row<VEC>(stages, stage, [&](int ahead, int to) { fetch(row + ahead * stride, to); });
+            from = mine + stage * a.stage_bytes;
+            if (++stage == stages) stage = 0;
         }
-        if (row + stride < a.rows) fetch(row + stride);
+        float d[E];
+        if (a.dout.p) {
+            read_row<VEC, NV, RING, RT>(a.dout, from, row, cols, d);
+        } else {
+#pragma unroll
+            for (int e = 0; e < E; ++e) d[e] = 0.f;
+        }
         if (next) {
-            float s = 0.f;
+            float x[E], dn[E], s = 0.f;
+            read_row<VEC, NV, RING, YT>(a.dn, from, row, cols, dn);
+            read_row<VEC, NV, RING, RT>(a.out, from, row, cols, x);
 #pragma unroll
             for (int v = 0; v < NV; ++v) {
-                const int c = v * step + tx * VEC;
+                const int c = (v * blockDim.x + tx) * VEC;
                 if (c >= cols) continue;
                 float wv[VEC];
                 if (!KEEP) row::load<VEC>(a.w_next + c, wv);
@@ -159,73 +155,72 @@ norm_bwd_kernel(const BwdArgs a) {
                     s = fmaf(dn[e], x[e], s);
                 }
             }
-            const float mean = row::row_sum(s, 0.f, sums[flip]).x * inv_cols;
+            const float mean = row::row_sum(s, sums[flip]) * inv_cols;
             flip ^= 1;
 #pragma unroll
             for (int e = 0; e < E; ++e) d[e] = fmaf(rstd_n, dn[e] - x[e] * mean, d[e]);
         }
 #pragma unroll
         for (int v = 0; v < NV; ++v) {
-            const int c = v * step + tx * VEC;
+            const int c = (v * blockDim.x + tx) * VEC;
             if (c < cols) row::store<VEC>(static_cast<RT*>(a.dr) + row * a.lddr + c, &d[v * VEC]);
         }
         if (POST) {
-            const float rstd = a.w ? a.rstd[row] : 1.f;
-            const float g_row = a.gate_mode == QMOE_GATE_ROW ? static_cast<const float*>(a.gate)[row] : 1.f;
-            float s = 0.f, s_gate = 0.f;
-            // from here on x holds t = y rstd and dn holds dz w
+            float t[E], g[E], s = 0.f, s_gate = 0.f;
+            read_row<VEC, NV, RING, YT>(a.y, from, row, cols, t);
+            if (a.gate_mode == QMOE_GATE_FULL) read_row<VEC, NV, RING, YT>(a.full_gate, from, row, cols, g);
+            // t = y rstd; d becomes dz w
 #pragma unroll
             for (int v = 0; v < NV; ++v) {
-                const int c = v * step + tx * VEC;
+                const int c = (v * blockDim.x + tx) * VEC;
                 if (c >= cols) continue;
-                float wv[VEC], g[VEC], dg[VEC];
+                float wv[VEC], gv[VEC], dg[VEC];
                 if (!KEEP && a.w) row::load<VEC>(a.w + c, wv);
-                if (a.gate_mode == QMOE_GATE_FULL)
-                    row::load<VEC>(static_cast<const YT*>(a.gate) + row * a.ldg + c, g);
-                else if (a.gate_mode == QMOE_GATE_COL)
-                    row::load<VEC>(static_cast<const float*>(a.gate) + c, g);
+                if (!KEEP && a.gate_mode == QMOE_GATE_COL) row::load<VEC>(a.gate + c, gv);
 #pragma unroll
                 for (int i = 0; i < VEC; ++i) {
                     const int e = v * VEC + i;
                     const float wt = a.w ? (KEEP ? w[e] : wv[i]) : 1.f;
                     const float ad = a.alpha * d[e];
-                    const float gate = a.gate_mode >= QMOE_GATE_COL ? g[i] : g_row;
-                    const float t = y[e] * rstd, dz = ad * gate;
-                    dg[i] = ad * (t * wt);
+                    const float gate = a.gate_mode == QMOE_GATE_FULL  ? g[e]
+                                       : a.gate_mode == QMOE_GATE_COL ? (KEEP ? gc[e] : gv[i])
+                                                                      : g_row;
+                    t[e] *= rstd;
+                    const float dz = ad * gate;
+                    dg[i] = ad * (t[e] * wt);
                     s_gate += dg[i];
                     if (a.gate_mode == QMOE_GATE_COL) sum_g.add(e, dg[i]);
-                    if (a.w) sum_w.add(e, dz * t);
-                    x[e] = t;
-                    dn[e] = dz * wt;
-                    s = fmaf(dn[e], t, s);
+                    if (a.w) sum_w.add(e, dz * t[e]);
+                    d[e] = dz * wt;
+                    s = fmaf(d[e], t[e], s);
                 }
                 if (a.gate_mode == QMOE_GATE_FULL)
                     row::store<VEC>(static_cast<YT*>(a.dgate) + row * a.lddg + c, dg);
             }
-            if (a.w || a.gate_mode == QMOE_GATE_ROW) {
-                const float2 both = row::row_sum(s, s_gate, sums[flip]);
+            if (a.gate_mode == QMOE_GATE_ROW) {
+                s_gate = row::row_sum(s_gate, sums[flip]);
                 flip ^= 1;
-                s = both.x * inv_cols;
-                if (a.gate_mode == QMOE_GATE_ROW && tx == 0) static_cast<float*>(a.dgate)[row] = both.y;
+                if (tx == 0) static_cast<float*>(a.dgate)[row] = s_gate;
+            }
+            if (a.w) {
+                s = row::row_sum(s, sums[flip]) * inv_cols;
+                flip ^= 1;
+            }
+            if (a.w) {
+#pragma unroll
+                for (int e = 0; e < E; ++e) d[e] = rstd * (d[e] - t[e] * s);
             }
 #pragma unroll
             for (int v = 0; v < NV; ++v) {
-                const int c = v * step + tx * VEC;
-                if (c >= cols) continue;
-                float dy[VEC];
-#pragma unroll
-                for (int i = 0; i < VEC; ++i) {
-                    const int e = v * VEC + i;
-                    dy[i] = a.w ? rstd * (dn[e] - x[e] * s) : dn[e];
-                }
-                row::store<VEC>(static_cast<YT*>(a.dy) + row * a.lddy + c, dy);
+                const int c = (v * blockDim.x + tx) * VEC;
+                if (c < cols) row::store<VEC>(static_cast<YT*>(a.dy) + row * a.lddy + c, &d[v * VEC]);
             }
         }
     }
     const int64_t part = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
-        const int c = v * step + tx * VEC;
+        const int c = (v * blockDim.x + tx) * VEC;
         if (c >= cols) continue;
         float t[VEC];
         auto put = [&](ColSums<E, VEC, SMEM>& s, int which) {
@@ -264,23 +259,22 @@ __global__ void __launch_bounds__(1024) norm_sum_kernel(const SumArgs a) {
     group[threadIdx.y][threadIdx.x] = s;
     __syncthreads();
     s = group[threadIdx.x][threadIdx.y];
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
+    s = row::warp_sum(s);
     const int oc = blockIdx.x * 32 + threadIdx.y;
     if (threadIdx.x == 0 && oc < a.cols) out[oc] = s;
 }
 
-// CTAs of a launch: one wave of the kernels' occupancy.
+// CTAs of a launch: one wave of 512 threads an SM.
+inline int per_sm_of(const Shape& s) { return 512 / (s.threads * s.rows_per_cta); }
 inline int64_t bwd_ctas(const Shape& s, int64_t rows) {
     const int64_t ctas = (rows + s.rows_per_cta - 1) / s.rows_per_cta;
-    const int64_t per_sm = 512 / (s.threads * s.rows_per_cta);
-    const int64_t fit = (int64_t)row::kSMs * (per_sm > 1 ? per_sm : 1);
+    const int64_t fit = (int64_t)row::kSMs * per_sm_of(s);
     return ctas < fit ? ctas : fit;
 }
 inline int64_t part_rows(int64_t rows, int64_t cols) {
     int64_t most = 1;
     for (int vec = 0; vec < 2; ++vec) {
-        const Shape s = shape_of(cols, vec != 0, 512);
+        const Shape s = shape_of(cols, vec != 0);
         const int64_t n = bwd_ctas(s, rows) * s.rows_per_cta;
         most = n > most ? n : most;
     }
@@ -288,29 +282,43 @@ inline int64_t part_rows(int64_t rows, int64_t cols) {
 }
 
 template <typename K>
-inline int start(K kernel, dim3 grid, dim3 block, size_t smem, cudaStream_t st, const BwdArgs& a) {
-    if (smem > 48 * 1024 &&
-        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
+inline int start(K kernel, const Shape& s, BwdArgs& a, int sums, int row_bytes, int64_t ctas, cudaStream_t st) {
+    const int64_t sum_bytes = s.values() > 16 ? (int64_t)sums * s.values() * s.threads * 4 : 0;
+    a.stage_bytes = row_bytes;
+    a.stages = s.values() > 16 ? 0 : stages_of((int64_t)row_bytes * s.rows_per_cta, sum_bytes, per_sm_of(s));
+    if (s.values() <= 16 && !a.stages) return QMOE_ERR_UNSUPPORTED;
+    const size_t smem = (size_t)(sum_bytes + (int64_t)a.stages * row_bytes * s.rows_per_cta);
+    if (smem > 48 * 1024 - 1024 &&
+        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 225 * 1024) != cudaSuccess)
         return QMOE_ERR_CUDA;
-    return launch_pdl(kernel, grid, block, smem, st, a);
+    return launch_pdl(kernel, dim3((unsigned)ctas), dim3(s.threads, s.rows_per_cta), smem, st, a);
 }
 
 template <bool POST>
 struct Bwd {
     template <typename RT, typename YT>
     struct Go {
-        static int go(const BwdArgs& a, const Shape& s, int64_t ctas, cudaStream_t st) {
-            const dim3 block(s.threads, s.rows_per_cta), grid((unsigned)ctas);
-            const int e = s.nv * s.vec;
-            const size_t smem = e > 8 ? (size_t)(POST ? 3 : 1) * e * s.threads * 4 : 0;
+        static int go(BwdArgs& a, const Shape& s, int64_t ctas, cudaStream_t st) {
+            const int rb = stage_bytes(a.cols, sizeof(RT)), yb = stage_bytes(a.cols, sizeof(YT));
+            int at = 0;
+            auto place = [&](Source& src, int bytes) {
+                src.off = at;
+                if (src.p) at += bytes;
+            };
+            place(a.dout, rb);
+            place(a.dn, yb);
+            place(a.out, rb);
+            place(a.y, yb);
+            place(a.full_gate, yb);
+            constexpr int sums = POST ? 3 : 1;
             if (s.vec == 8) {
-                if (s.nv == 1) return start(norm_bwd_kernel<RT, YT, 1, 8, POST>, grid, block, smem, st, a);
-                if (s.nv == 2) return start(norm_bwd_kernel<RT, YT, 2, 8, POST>, grid, block, smem, st, a);
-                return start(norm_bwd_kernel<RT, YT, 4, 8, POST>, grid, block, smem, st, a);
+                if (s.nv == 1) return start(norm_bwd_kernel<RT, YT, 1, 8, POST>, s, a, sums, at, ctas, st);
+                if (s.nv == 2) return start(norm_bwd_kernel<RT, YT, 2, 8, POST>, s, a, sums, at, ctas, st);
+                return start(norm_bwd_kernel<RT, YT, 4, 8, POST>, s, a, sums, at, ctas, st);
             }
-            if (s.nv == 4) return start(norm_bwd_kernel<RT, YT, 4, 1, POST>, grid, block, smem, st, a);
-            if (s.nv == 16) return start(norm_bwd_kernel<RT, YT, 16, 1, POST>, grid, block, smem, st, a);
-            return start(norm_bwd_kernel<RT, YT, 32, 1, POST>, grid, block, smem, st, a);
+            if (s.nv == 8) return start(norm_bwd_kernel<RT, YT, 8, 1, POST>, s, a, sums, at, ctas, st);
+            if (s.nv == 16) return start(norm_bwd_kernel<RT, YT, 16, 1, POST>, s, a, sums, at, ctas, st);
+            return start(norm_bwd_kernel<RT, YT, 32, 1, POST>, s, a, sums, at, ctas, st);
         }
     };
 };
@@ -321,7 +329,7 @@ template <template <typename, typename> class F>
 inline int run(BwdArgs& a, int rt, int yt, bool vec, float* const (&out)[3], void* ws, cudaStream_t st) {
     a.part = static_cast<float*>(ws);
     a.part_rows = part_rows(a.rows, a.cols);
-    const Shape s = shape_of(a.cols, vec, 512);
+    const Shape s = shape_of(a.cols, vec);
     const int64_t ctas = bwd_ctas(s, a.rows);
     if (ctas > 0) {
         const int rc = by_types<F>(rt, yt, a, s, ctas, st);
@@ -365,12 +373,9 @@ extern "C" int qmoe_norm_pre_backward(int64_t rows, int64_t cols, int stream_dty
     norm::BwdArgs a = {};
     a.rows = rows;
     a.cols = (int)cols;
-    a.dout = dres;
-    a.lddout = lddres;
-    a.dn = dn;
-    a.lddn = lddn;
-    a.out = x;
-    a.ldo = ldx;
+    a.dout = {dres, lddres, 0};
+    a.dn = {dn, lddn, 0};
+    a.out = {x, ldx, 0};
     a.w_next = w;
     a.rstd_next = rstd;
     a.dr = dx;
@@ -415,15 +420,13 @@ extern "C" int qmoe_norm_post_backward(int64_t rows, int64_t cols, int stream_dt
     norm::BwdArgs a = {};
     a.rows = rows;
     a.cols = (int)cols;
-    a.dout = dout;
-    a.lddout = lddout;
-    a.y = y;
-    a.ldy = ldy;
+    a.dout = {dout, lddout, 0};
+    a.y = {y, ldy, 0};
     a.w = w;
     a.rstd = rstd;
     a.gate_mode = gate_mode;
-    a.gate = gate;
-    a.ldg = ldg;
+    if (full) a.full_gate = {gate, ldg, 0};
+    else a.gate = static_cast<const float*>(gate);
     a.alpha = alpha;
     a.dr = dr;
     a.lddr = lddr;
@@ -437,10 +440,8 @@ extern "C" int qmoe_norm_post_backward(int64_t rows, int64_t cols, int stream_dt
     if (full) vec = vec && norm::row_aligned(gate, ldg, bs) && norm::row_aligned(dgate, lddg, bs);
     if (gate_mode == QMOE_GATE_COL) vec = vec && aligned16(gate);
     if (dn) {
-        a.dn = dn;
-        a.lddn = lddn;
-        a.out = out;
-        a.ldo = ldo;
+        a.dn = {dn, lddn, 0};
+        a.out = {out, ldo, 0};
         a.w_next = w_next;
         a.rstd_next = rstd_next;
         vec = vec && norm::row_aligned(dn, lddn, bs) && norm::row_aligned(out, ldo, rs) && aligned16(w_next);

@@ -7,20 +7,21 @@
 //   dlogit = p (a - sum p a - s) + [selected] w_j (dw_j - r),
 //   a_e = dloss coef E counts_e / (k n^2)
 //
-// A warp takes a token at a time, its logits spread over the lanes' registers,
-// so a row is read once for the softmax, the selection and the statistics.
-// Selection is k rounds of a warp-wide maximum over order-preserving integer
-// keys, the lowest expert first among equal keys.  That, not the 2 E bytes of a
-// row, is the bound: the rounds are instruction issue and the latency of
-// redux.  Probabilities are summed per lane over a warp's tokens, then over a
-// CTA's warps, then over CTAs, in a fixed order.
+// A warp takes a token at a time, its logits spread over the lanes' registers
+// (by 16-byte loads where rows allow it), so a row is read once for the
+// softmax, the selection and the statistics.  Selection is k rounds of a
+// warp-wide maximum over order-preserving integer keys, the lowest expert first
+// among equal keys; a 16-bit logit's key leaves room for the expert's number,
+// so one redux gives both.  These rounds, not the 2 E bytes of a row, are the
+// bound: instruction issue and the latency of redux.  Probabilities are summed
+// per lane over a warp's tokens, then over a CTA's warps, then over CTAs, in a
+// fixed order.
 #include "row_ops.cuh"
 
 namespace qmoe {
 namespace route {
 
-constexpr int MAX_E = 1024, MAX_K = 32, WARPS = 8;
-constexpr uint32_t KEY_NONE = 0x007FFFFFu;  // key of -inf: that expert is not available
+constexpr int MAX_E = 1024, MAX_K = 32, WARPS = 16;
 
 struct Args {
     int64_t T;
@@ -37,6 +38,7 @@ struct Args {
     // statistics (part_p null: none): per CTA, probabilities and counts by expert, then the routed tokens
     float* part_p;
     int32_t* part_c;
+    int32_t* arrived;
     // gradient
     const float* dw;
     float coef;
@@ -50,25 +52,80 @@ struct Args {
 // finite value.
 __device__ __forceinline__ float clean(float v) { return v > -INFINITY ? fminf(v, 3.402823466e38f) : -INFINITY; }
 
-// Larger floats have larger keys; -0 and +0 have the same.
+// Larger floats have larger keys; -0 and +0 have the same.  16-bit types: the
+// bits' order alone, in the upper half.
 __device__ __forceinline__ uint32_t key_of(float v) {
     const uint32_t u = __float_as_uint(v == 0.f ? 0.f : v);
     return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
-
-__device__ __forceinline__ float warp_sum(float v) {
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
-    return v;
+__device__ __forceinline__ float value_of(uint32_t key) {
+    return __uint_as_float((key & 0x80000000u) ? (key & 0x7FFFFFFFu) : ~key);
 }
+template <typename T> __device__ __forceinline__ uint32_t bits16(float v);
+template <> __device__ __forceinline__ uint32_t bits16<__nv_bfloat16>(float v) {
+    return __bfloat16_as_ushort(__float2bfloat16_rn(v));
+}
+template <> __device__ __forceinline__ uint32_t bits16<__half>(float v) { return __half_as_ushort(__float2half_rn(v)); }
+template <typename T> __device__ __forceinline__ float from16(uint32_t u);
+template <> __device__ __forceinline__ float from16<__nv_bfloat16>(uint32_t u) { return __uint_as_float(u << 16); }
+template <> __device__ __forceinline__ float from16<__half>(uint32_t u) {
+    return __half2float(__ushort_as_half((unsigned short)u));
+}
+
+// The keys of a lane's experts and the k rounds.  PACK: 16-bit logits without
+// a bias, key = order of the 16 bits << 16 | (0xFFFF - expert), 0 for a gone or
+// unavailable expert; else key = 32-bit order of the score, NONE or less for one
+// that is not available.
+constexpr uint32_t NONE = 0x007FFFFFu;  // key of -inf
+
+template <typename T>
+__device__ __forceinline__ uint32_t packed_key(float v, int e) {
+    if (!(v > -INFINITY)) return 0u;
+    uint32_t u = bits16<T>(v == 0.f ? 0.f : v);
+    u = (u & 0x8000u) ? (u ^ 0xFFFFu) : (u | 0x8000u);
+    return (u << 16) | (0xFFFFu - (uint32_t)e);
+}
+template <typename T>
+__device__ __forceinline__ float packed_value(uint32_t key) {
+    const uint32_t u = key >> 16;
+    return from16<T>((u & 0x8000u) ? (u & 0x7FFFu) : (u ^ 0xFFFFu));
+}
+
+// Which experts a lane holds: value i is expert (i / V) 32 V + lane V + i % V.
+template <int V>
+__device__ __forceinline__ int expert_of(int i, int lane) {
+    return (i / V) * (32 * V) + lane * V + i % V;
+}
+
+// A row's logits, cleaned; -inf past the last expert.
+template <typename T, int NE, int V>
+__device__ __forceinline__ void load_logits(const T* row, int E, int lane, float (&v)[NE]) {
+#pragma unroll
+    for (int i = 0; i < NE; i += V) {
+        const int e = expert_of<V>(i, lane);
+        if (V == 1) {
+            v[i] = e < E ? clean(row::to_f32(row[e])) : -INFINITY;
+        } else if (e < E) {
+            struct alignas(sizeof(T) * V) Pack { T x[V]; };
+            const Pack p = *reinterpret_cast<const Pack*>(row + e);
+#pragma unroll
+            for (int j = 0; j < V; ++j) v[i + j] = clean(row::to_f32(p.x[j]));
+        } else {
+#pragma unroll
+            for (int j = 0; j < V; ++j) v[i + j] = -INFINITY;
+        }
+    }
+}
+
+using row::warp_sum;
 __device__ __forceinline__ float warp_max(float v) {
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, o));
     return v;
 }
 
-template <typename T, int NE>
-__global__ void __launch_bounds__(WARPS * 32)
+template <typename T, int NE, int V, bool PACK>
+__global__ void __launch_bounds__(WARPS * 32, NE > 16 ? 1 : 2)
 route_kernel(const Args a) {
     extern __shared__ float smem[];  // statistics: [WARPS][E] sums of p, then [E + 1] counts
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, E = a.E;
@@ -77,6 +134,7 @@ route_kernel(const Args a) {
     pdl_sync();
     if (stats) {
         for (int i = threadIdx.x; i <= E; i += blockDim.x) count[i] = 0;
+        if (blockIdx.x == 0 && threadIdx.x == 0) *a.arrived = 0;  // for route_stats_kernel
         __syncthreads();
     }
     float psum[NE];
@@ -85,12 +143,9 @@ route_kernel(const Args a) {
     for (int64_t t = (int64_t)blockIdx.x * WARPS + warp; t < a.T; t += (int64_t)gridDim.x * WARPS) {
         const T* row = static_cast<const T*>(a.logits) + t * a.ld;
         float v[NE], m = -INFINITY;
+        load_logits<T, NE, V>(row, E, lane, v);
 #pragma unroll
-        for (int i = 0; i < NE; ++i) {
-            const int e = i * 32 + lane;
-            v[i] = e < E ? clean(row::to_f32(row[e])) : -INFINITY;
-            m = fmaxf(m, v[i]);
-        }
+        for (int i = 0; i < NE; ++i) m = fmaxf(m, v[i]);
         m = warp_max(m);
         const bool routed = m > -INFINITY && (!a.mask || a.mask[t]);
         if (!routed) {
@@ -104,8 +159,9 @@ route_kernel(const Args a) {
         uint32_t key[NE];
 #pragma unroll
         for (int i = 0; i < NE; ++i) {
-            const int e = i * 32 + lane;
-            key[i] = e < E ? key_of(a.bias ? clean(v[i] + a.bias[e]) : v[i]) : 0u;
+            const int e = expert_of<V>(i, lane);
+            if constexpr (PACK) key[i] = packed_key<T>(v[i], e);
+            else key[i] = e < E ? key_of(a.bias ? clean(v[i] + a.bias[e]) : v[i]) : 0u;
         }
         float sum = 0.f;
 #pragma unroll
@@ -119,29 +175,41 @@ route_kernel(const Args a) {
 #pragma unroll
             for (int i = 0; i < NE; ++i) psum[i] = fmaf(v[i], inv, psum[i]);
         }
-        int mine = -1;  // lane j: the expert of rank j
+        int mine = -1;  // lane j: the expert of rank j, and its key
+        uint32_t my_key = 0;
         for (int j = 0; j < a.k; ++j) {
             uint32_t best = key[0];
-            int at = 0;
 #pragma unroll
-            for (int i = 1; i < NE; ++i)
-                if (key[i] > best) {
-                    best = key[i];
-                    at = i;
-                }
+            for (int i = 1; i < NE; ++i) best = max(best, key[i]);
             const uint32_t top = __reduce_max_sync(0xFFFFFFFFu, best);
-            if (top <= KEY_NONE) break;
-            const int e = at * 32 + lane;
-            const int win = (int)__reduce_min_sync(0xFFFFFFFFu, best == top ? (unsigned)e : 0x7FFFFFFFu);
-            if (lane == j) mine = win;
-            if (win == e) {
+            int win;
+            if constexpr (PACK) {
+                if (top == 0u) break;
+                win = 0xFFFF - (int)(top & 0xFFFFu);
+            } else {
+                if (top <= NONE) break;
+                unsigned at = 0x7FFFFFFFu;
 #pragma unroll
-                for (int i = 0; i < NE; ++i)
-                    if (i == at) key[i] = 0u;
+                for (int i = NE - 1; i >= 0; --i)
+                    if (key[i] == top) at = expert_of<V>(i, lane);
+                win = (int)__reduce_min_sync(0xFFFFFFFFu, at);
             }
+            if (lane == j) {
+                mine = win;
+                my_key = top;
+            }
+            // the winner leaves: its register is the same in every lane, its lane is not
+            const int reg = (win / (32 * V)) * V + win % V;
+            const bool owner = (win / V) % 32 == lane;
+#pragma unroll
+            for (int i = 0; i < NE; ++i)
+                if (i == reg && owner) key[i] = 0u;
         }
-        // the chosen logits again (they are in L1), so that no register is indexed by a variable
-        const float l = mine >= 0 ? clean(row::to_f32(row[mine])) : -INFINITY;
+        float l = -INFINITY;
+        if (mine >= 0) {
+            if constexpr (PACK) l = clean(packed_value<T>(my_key));
+            else l = a.bias ? clean(row::to_f32(row[mine])) : value_of(my_key);
+        }
         float w;
         if (a.renorm) {
             const float best = warp_max(l);
@@ -162,8 +230,10 @@ route_kernel(const Args a) {
     }
     if (!stats) return;
 #pragma unroll
-    for (int i = 0; i < NE; ++i)
-        if (i * 32 + lane < E) smem[warp * E + i * 32 + lane] = psum[i];
+    for (int i = 0; i < NE; ++i) {
+        const int e = expert_of<V>(i, lane);
+        if (e < E) smem[warp * E + e] = psum[i];
+    }
     __syncthreads();
     for (int e = threadIdx.x; e <= E; e += blockDim.x) {
         a.part_c[(int64_t)blockIdx.x * (E + 1) + e] = count[e];
@@ -175,63 +245,81 @@ route_kernel(const Args a) {
     }
 }
 
-// Sums the CTAs' statistics: counts[E + 1], probs[E] and the loss.  One CTA.
+// Sums the CTAs' statistics: counts[E + 1], probs[E] and the loss.  A CTA takes
+// 32 experts, 32 threads each; the CTA that is last to arrive adds the CTAs'
+// parts of the loss, in their order.
 struct StatArgs {
     int parts, E, k;
     const float* part_p;
     const int32_t* part_c;
+    float* part_loss;
+    int32_t* arrived;
     float coef;
     int32_t* counts;
     float* probs;
     float* loss;
 };
 __global__ void __launch_bounds__(1024) route_stats_kernel(const StatArgs a) {
-    __shared__ float warp_part[32];
-    __shared__ int routed;
+    __shared__ float sp[32][33];
+    __shared__ int sc[32][33];
+    __shared__ int last, routed;
     pdl_sync();
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, E = a.E;
-    if (warp == 0) {
-        int n = 0;
-        for (int i = lane; i < a.parts; i += 32) n += a.part_c[(int64_t)i * (E + 1) + E];
-        n = __reduce_add_sync(0xFFFFFFFFu, n);
-        if (lane == 0) {
-            routed = n;
-            a.counts[E] = n;
-        }
-    }
-    __syncthreads();
-    const float n = (float)(routed > 0 ? routed : 1);
-    float loss = 0.f;
-    for (int e = threadIdx.x; e < E; e += blockDim.x) {
-        int c = 0;
-        float p = 0.f;
-#pragma unroll 8
-        for (int i = 0; i < a.parts; ++i) {
+    const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5, E = a.E, e = blockIdx.x * 32 + tx;
+    int n = 0;
+    for (int i = threadIdx.x; i < a.parts; i += 1024) n += a.part_c[(int64_t)i * (E + 1) + E];
+    int c = 0;
+    float p = 0.f;
+    if (e < E) {
+#pragma unroll 4
+        for (int i = ty; i < a.parts; i += 32) {
             c += a.part_c[(int64_t)i * (E + 1) + e];
             p += a.part_p[(int64_t)i * E + e];
         }
-        p /= n;
-        a.counts[e] = c;
-        a.probs[e] = p;
-        loss = fmaf((float)c / (n * (float)a.k), p, loss);
     }
-    loss = warp_sum(loss);
-    if (lane == 0) warp_part[warp] = loss;
+    if (threadIdx.x == 0) routed = 0;
+    sp[ty][tx] = p;
+    sc[ty][tx] = c;
     __syncthreads();
-    if (warp == 0) {
-        loss = warp_sum(warp_part[lane]);
-        if (lane == 0) a.loss[0] = a.coef * (float)E * loss;
+    n = __reduce_add_sync(0xFFFFFFFFu, n);
+    if (tx == 0 && n) atomicAdd(&routed, n);
+    // warp ty sums expert ty
+    p = warp_sum(sp[tx][ty]);
+    c = __reduce_add_sync(0xFFFFFFFFu, sc[tx][ty]);
+    __syncthreads();
+    const float total = (float)(routed > 0 ? routed : 1);
+    const int mine = blockIdx.x * 32 + ty;
+    p /= total;
+    if (tx == 0) {
+        if (mine < E) {
+            a.counts[mine] = c;
+            a.probs[mine] = p;
+        }
+        sp[0][ty] = mine < E ? (float)c / (total * (float)a.k) * p : 0.f;
     }
+    __syncthreads();
+    if (ty != 0) return;
+    const float part = warp_sum(sp[0][tx]);
+    if (tx == 0) {
+        if (blockIdx.x == 0) a.counts[E] = routed;
+        a.part_loss[blockIdx.x] = part;
+        __threadfence();
+        last = atomicAdd(a.arrived, 1) == (int)gridDim.x - 1;
+    }
+    __syncwarp();
+    if (!last) return;
+    __threadfence();
+    const float loss = warp_sum(tx < (int)gridDim.x ? __ldcg(a.part_loss + tx) : 0.f);  // E <= 1024: 32 CTAs at most
+    if (tx == 0) a.loss[0] = a.coef * (float)E * loss;
 }
 
-template <typename T, int NE>
-__global__ void __launch_bounds__(WARPS * 32)
+template <typename T, int NE, int V>
+__global__ void __launch_bounds__(WARPS * 32, NE > 16 ? 1 : 2)
 route_bwd_kernel(const Args a) {
-    extern __shared__ float smem[];  // [WARPS][E]: what the selected experts get besides
+    extern __shared__ float smem[];  // [WARPS][NE * 32]: what the selected experts get besides
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, E = a.E;
-    float* const extra = smem + warp * E;
+    float* const extra = smem + warp * NE * 32;
     pdl_sync();
-    for (int e = lane; e < E; e += 32) extra[e] = 0.f;
+    for (int e = lane; e < NE * 32; e += 32) extra[e] = 0.f;
     __syncwarp();
     float ga[NE];
     float c = 0.f;
@@ -241,45 +329,41 @@ route_bwd_kernel(const Args a) {
     }
 #pragma unroll
     for (int i = 0; i < NE; ++i) {
-        const int e = i * 32 + lane;
+        const int e = expert_of<V>(i, lane);
         ga[i] = a.dloss && e < E ? c * (float)a.counts[e] : 0.f;
     }
     for (int64_t t = (int64_t)blockIdx.x * WARPS + warp; t < a.T; t += (int64_t)gridDim.x * WARPS) {
         const T* row = static_cast<const T*>(a.logits) + t * a.ld;
         T* out = static_cast<T*>(a.dlogits) + t * a.ldd;
-        if (!(a.lse[t] > -INFINITY)) {  // routed nowhere
-            for (int e = lane; e < E; e += 32) out[e] = row::from_f32<T>(0.f);
-            continue;
-        }
         // the softmax again from the row's maximum: exp(logit - lse) would lose what lse has lost beside a large logit
         float p[NE], m = -INFINITY, sum = 0.f, u = 0.f;
-#pragma unroll
-        for (int i = 0; i < NE; ++i) {
-            const int e = i * 32 + lane;
-            p[i] = e < E ? clean(row::to_f32(row[e])) : -INFINITY;
-            m = fmaxf(m, p[i]);
+        load_logits<T, NE, V>(row, E, lane, p);
+        const bool routed = a.lse[t] > -INFINITY;
+        int id = -1;
+        float w = 0.f, wdw = 0.f;
+        if (a.dw && lane < a.k) {
+            id = a.ids[t * a.k + lane];
+            w = a.w[t * a.k + lane];
+            wdw = w * a.dw[t * a.k + lane];
+            if (id < 0 || id >= E || !routed) {
+                id = -1;
+                w = wdw = 0.f;
+            }
         }
+#pragma unroll
+        for (int i = 0; i < NE; ++i) m = fmaxf(m, p[i]);
         m = warp_max(m);
+        if (!routed) m = 0.f;
 #pragma unroll
         for (int i = 0; i < NE; ++i) {
             p[i] = __expf(p[i] - m);
             sum += p[i];
         }
-        const float inv = 1.f / warp_sum(sum);
+        const float inv = routed ? 1.f / warp_sum(sum) : 0.f;
 #pragma unroll
         for (int i = 0; i < NE; ++i) {
-            p[i] *= inv;
+            p[i] = routed ? p[i] * inv : 0.f;
             u = fmaf(p[i], ga[i], u);
-        }
-        int id = -1;
-        float w = 0.f, wdw = 0.f;
-        if (a.dw && lane < a.k) {
-            id = a.ids[t * a.k + lane];
-            if (id >= E) id = -1;
-            if (id >= 0) {
-                w = a.w[t * a.k + lane];
-                wdw = w * a.dw[t * a.k + lane];
-            }
         }
         const float s = a.dw ? warp_sum(wdw) : 0.f;
         u = warp_sum(u);
@@ -288,9 +372,12 @@ route_bwd_kernel(const Args a) {
         if (id >= 0) extra[id] = wdw;
         __syncwarp();
 #pragma unroll
-        for (int i = 0; i < NE; ++i) {
-            const int e = i * 32 + lane;
-            if (e < E) out[e] = row::from_f32<T>(fmaf(p[i], ga[i] - u, extra[e]));
+        for (int i = 0; i < NE; i += V) {
+            const int e = expert_of<V>(i, lane);
+            struct alignas(sizeof(T) * V) Pack { T x[V]; } o;
+#pragma unroll
+            for (int j = 0; j < V; ++j) o.x[j] = row::from_f32<T>(fmaf(p[i + j], ga[i + j] - u, extra[e + j]));
+            if (e < E) *reinterpret_cast<Pack*>(out + e) = o;
         }
         __syncwarp();
         if (id >= 0) extra[id] = 0.f;
@@ -300,24 +387,45 @@ route_bwd_kernel(const Args a) {
 
 // At most this many CTAs: 32 warps an SM.
 inline int ctas(int64_t T) {
-    const int64_t n = (T + WARPS - 1) / WARPS, most = row::kSMs * 4;
+    const int64_t n = (T + WARPS - 1) / WARPS, most = row::kSMs * 2;
     return (int)(n < most ? n : most);
 }
 
-template <bool BWD, typename T, int NE>
+template <typename K>
+inline int launch(K kernel, const Args& a, size_t smem, cudaStream_t st) {
+    if (smem > 48 * 1024 &&
+        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
+        return QMOE_ERR_CUDA;
+    return launch_pdl(kernel, ctas(a.T), WARPS * 32, smem, st, a);
+}
+template <bool BWD, typename T, int NE, int V>
 inline int start(const Args& a, cudaStream_t st) {
-    const size_t smem = BWD ? (size_t)WARPS * a.E * 4 : a.part_p ? ((size_t)WARPS * a.E + a.E + 1) * 4 : 0;
-    if constexpr (BWD) return launch_pdl(route_bwd_kernel<T, NE>, ctas(a.T), WARPS * 32, smem, st, a);
-    else return launch_pdl(route_kernel<T, NE>, ctas(a.T), WARPS * 32, smem, st, a);
+    if constexpr (BWD) {
+        return launch(route_bwd_kernel<T, NE, V>, a, (size_t)WARPS * NE * 32 * 4, st);
+    } else {
+        const size_t smem = a.part_p ? ((size_t)WARPS * a.E + a.E + 1) * 4 : 0;
+        if constexpr (sizeof(T) == 2)
+            if (!a.bias) return launch(route_kernel<T, NE, V, true>, a, smem, st);
+        return launch(route_kernel<T, NE, V, false>, a, smem, st);
+    }
+}
+// The widest loads, up to 16 bytes, that the rows allow: else one value at a time.
+template <bool BWD, typename T, int NE>
+inline int by_rows(const Args& a, cudaStream_t st) {
+    constexpr int most = 16 / sizeof(T), V = NE < most ? NE : most;
+    const uintptr_t bytes = V * sizeof(T);
+    const bool fits = a.E % V == 0 && reinterpret_cast<uintptr_t>(a.logits) % bytes == 0 && a.ld % V == 0 &&
+                      (!BWD || (reinterpret_cast<uintptr_t>(a.dlogits) % bytes == 0 && a.ldd % V == 0));
+    return fits ? start<BWD, T, NE, V>(a, st) : start<BWD, T, NE, 1>(a, st);
 }
 template <bool BWD, typename T>
 inline int by_experts(const Args& a, cudaStream_t st) {
-    if (a.E <= 32) return start<BWD, T, 1>(a, st);
-    if (a.E <= 64) return start<BWD, T, 2>(a, st);
-    if (a.E <= 128) return start<BWD, T, 4>(a, st);
-    if (a.E <= 256) return start<BWD, T, 8>(a, st);
-    if (a.E <= 512) return start<BWD, T, 16>(a, st);
-    return start<BWD, T, 32>(a, st);
+    if (a.E <= 32) return by_rows<BWD, T, 1>(a, st);
+    if (a.E <= 64) return by_rows<BWD, T, 2>(a, st);
+    if (a.E <= 128) return by_rows<BWD, T, 4>(a, st);
+    if (a.E <= 256) return by_rows<BWD, T, 8>(a, st);
+    if (a.E <= 512) return by_rows<BWD, T, 16>(a, st);
+    return by_rows<BWD, T, 32>(a, st);
 }
 template <bool BWD>
 inline int run(int dtype, const Args& a, cudaStream_t st) {
@@ -325,6 +433,9 @@ inline int run(int dtype, const Args& a, cudaStream_t st) {
     if (dtype == QMOE_BF16) return by_experts<BWD, __nv_bfloat16>(a, st);
     return by_experts<BWD, __half>(a, st);
 }
+
+// The workspace: the CTAs' sums of p, their counts, the parts of the loss, and the arrivals.
+inline size_t ws_words(int64_t T, int E) { return (size_t)ctas(T) * (2 * (size_t)E + 1) + 32 + 1; }
 
 inline int check(int64_t T, int E, int k, int dtype, int64_t ld, float scale) {
     if (T < 0 || E <= 0 || k <= 0 || k > E || !row::dtype_ok(dtype) || ld < E || !(scale > 0.f && scale < INFINITY))
@@ -340,8 +451,7 @@ using namespace qmoe;
 
 extern "C" size_t qmoe_route_workspace_bytes(int64_t T, int E) {
     if (T < 0 || E <= 0 || E > route::MAX_E) return 0;
-    const size_t n = (size_t)route::ctas(T > 0 ? T : 1);
-    return (n * (2 * (size_t)E + 1) * 4 + 255) / 256 * 256;
+    return (route::ws_words(T, E) * 4 + 255) / 256 * 256;
 }
 
 extern "C" int qmoe_route_topk(int64_t T, int E, int k, int dtype, const void* logits, int64_t ld, const float* bias,
@@ -373,17 +483,21 @@ extern "C" int qmoe_route_topk(int64_t T, int E, int k, int dtype, const void* l
     a.w = w;
     a.lse = lse;
     const int parts = route::ctas(T);
+    route::StatArgs s = {};
     if (stats) {
         a.part_p = static_cast<float*>(ws);
         a.part_c = reinterpret_cast<int32_t*>(a.part_p + (size_t)parts * E);
+        float* const part_loss = reinterpret_cast<float*>(a.part_c + (size_t)parts * (E + 1));
+        a.arrived = reinterpret_cast<int32_t*>(part_loss + 32);
+        s = {parts, E, k, a.part_p, a.part_c, part_loss, a.arrived, coef, counts, probs, loss};
+        if (T == 0 && cudaMemsetAsync(a.arrived, 0, 4, (cudaStream_t)stream) != cudaSuccess) return QMOE_ERR_CUDA;
     }
     if (T > 0) {
         const int started = route::run<false>(dtype, a, (cudaStream_t)stream);
         if (started != QMOE_OK) return started;
     }
     if (!stats) return QMOE_OK;
-    const route::StatArgs s = {parts, E, k, a.part_p, a.part_c, coef, counts, probs, loss};
-    return launch_pdl(route::route_stats_kernel, 1, 1024, 0, (cudaStream_t)stream, s);
+    return launch_pdl(route::route_stats_kernel, ceil_div(E, 32), 1024, 0, (cudaStream_t)stream, s);
 }
 
 extern "C" int qmoe_route_topk_backward(int64_t T, int E, int k, int dtype, const void* logits, int64_t ld,

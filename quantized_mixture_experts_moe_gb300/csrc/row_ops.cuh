@@ -107,29 +107,30 @@ __device__ __forceinline__ void store(T* p, const float* v) {
     }
 }
 
-// Sum of (a, b) over the threads of a row: the lanes of a warp where the row
-// has 32 threads, else the whole CTA (blockDim.x threads; `buf` is one of the
-// two halves of a 2 x 32 float2 array, alternated by the caller so that one
+// Sum of v over the threads of a row: the lanes of a warp where the row has 32
+// threads, else the whole CTA (blockDim.x <= 512 threads; `buf` is one of the
+// two halves of a 2 x 16 float array, alternated by the caller so that one
 // barrier per sum is enough).  The order is fixed.
-__device__ __forceinline__ float2 row_sum(float a, float b, float2* buf) {
+__device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-        a += __shfl_xor_sync(0xFFFFFFFFu, a, o);
-        b += __shfl_xor_sync(0xFFFFFFFFu, b, o);
-    }
-    if (blockDim.x == 32) return make_float2(a, b);
-    const int warps = blockDim.x >> 5, lane = threadIdx.x & 31;
-    if (lane == 0) buf[threadIdx.x >> 5] = make_float2(a, b);
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+    return v;
+}
+__device__ __forceinline__ float row_sum(float v, float (&buf)[16]) {
+    v = warp_sum(v);
+    if (blockDim.x == 32) return v;
+    if ((threadIdx.x & 31) == 0) buf[threadIdx.x >> 5] = v;
     __syncthreads();
-    const float2 p = lane < warps ? buf[lane] : make_float2(0.f, 0.f);
-    a = p.x;
-    b = p.y;
+    const int warps = blockDim.x >> 5;
+    const float4* part = reinterpret_cast<const float4*>(buf);
+    v = 0.f;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-        a += __shfl_xor_sync(0xFFFFFFFFu, a, o);
-        b += __shfl_xor_sync(0xFFFFFFFFu, b, o);
+    for (int i = 0; i < 4; ++i) {
+        if (4 * i >= warps) break;
+        const float4 p = part[i];
+        v += (p.x + (4 * i + 1 < warps ? p.y : 0.f)) + ((4 * i + 2 < warps ? p.z : 0.f) + (4 * i + 3 < warps ? p.w : 0.f));
     }
-    return make_float2(a, b);
+    return v;
 }
 
 }  // namespace row

@@ -142,4 +142,4 @@ def test_reference_notices_a_planted_mistake():
     lg = torch.randn(6, 10, generator=g).double().requires_grad_()
     one = ref.route(lg, 2, None, None, True, 1.0, 1.0)
     other = ref.route(lg, 2, None, torch.tensor([1, 1, 1, 1, 1, 0]).bool(), True, 1.0, 1.0)
-    assert not torch.equal(one["counts"], other["counts"]) and abs(float(one["loss"] - other["loss"])) > 1e-4
+    assert not torch.equal(one["counts"], other["counts"]) and abs(float((one["loss"] - other["loss"]).detach())) > 1e-4
