@@ -31,63 +31,73 @@ struct FwdArgs {
 
 // POST: y, its norm and gate; without it the kernel is norm_pre (out = r, not written).
 template <typename RT, typename YT, int NV, int VEC, bool POST>
-__global__ void __launch_bounds__(512, NV * VEC > 8 ? 1 : 2)
+__global__ void __launch_bounds__(512, 1)
 norm_fwd_kernel(const FwdArgs a) {
     constexpr int E = NV * VEC;
-    constexpr bool KEEP = E <= 8;  // the weights stay in registers from row to row
+    constexpr bool KEEP = E <= 16;  // the weights stay in registers from row to row
     __shared__ __align__(16) float sums[2][16];
-    extern __shared__ __align__(16) uint8_t ring[];
-    const int tx = threadIdx.x, cols = a.cols, stages = a.stages;
+    __shared__ uint64_t full[MAX_ROWS][MAX_STAGES];
+    extern __shared__ __align__(128) uint8_t dynamic[];
+    const int tx = threadIdx.x, cols = a.cols;
     const int64_t stride = (int64_t)gridDim.x * blockDim.y;
-    uint8_t* const mine = ring + (int64_t)threadIdx.y * stages * a.stage_bytes;
     const float inv_cols = 1.f / (float)cols;
     int flip = 0;
 
-    auto fetch = [&](int64_t row, int stage) {
-        if (row < a.rows) {
-            uint8_t* to = mine + stage * a.stage_bytes;
-            copy_row<VEC, NV, RT>(a.r, to, row, a.rows, cols);
-            if (POST) copy_row<VEC, NV, YT>(a.y, to, row, a.rows, cols);
-            if (POST) copy_row<VEC, NV, YT>(a.full_gate, to, row, a.rows, cols);
-        }
-        tc::cp_async_commit();
-    };
+    auto ring = make_ring(full[threadIdx.y], dynamic + (int64_t)threadIdx.y * a.stages * a.stage_bytes, a.stages,
+                          a.stage_bytes, a.rows, stride, tx == 0, [&](int64_t row, uint8_t* to, uint64_t* bar) {
+                              uint32_t n = send_row<VEC, RT>(a.r, to, row, a.rows, cols, bar);
+                              if (POST) n += send_row<VEC, YT>(a.y, to, row, a.rows, cols, bar);
+                              if (POST) n += send_row<VEC, YT>(a.full_gate, to, row, a.rows, cols, bar);
+                              return n;
+                          });
+    if (tx == 0)
+        for (int i = 0; i < MAX_STAGES; ++i) tc::mbar_init(&full[threadIdx.y][i], 1);
+    if (tx < 32) sums[tx >> 4][tx & 15] = 0.f;
+    tc::fence_barrier_init();
+    __syncthreads();
     int64_t row = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
     pdl_sync();
-    for (int i = 0; i + 1 < stages; ++i) fetch(row + i * stride, i);
+    ring.begin(row);
     // what a column of y and of out is multiplied by: w and a column gate in one
-    float wg[KEEP ? E : 1], wn[KEEP ? E : 1];
-    auto col_factor = [&](int c, float* f) {
-#pragma unroll
-        for (int i = 0; i < VEC; ++i) f[i] = 1.f;
-        if (a.w) row::load<VEC>(a.w + c, f);
-        if (a.gate_mode == QMOE_GATE_COL) {
-            float g[VEC];
-            row::load<VEC>(a.gate + c, g);
-#pragma unroll
-            for (int i = 0; i < VEC; ++i) f[i] *= g[i];
-        }
-    };
-    if (KEEP) {
+    float wg[E], wn[E];
+    auto col_factors = [&] {
 #pragma unroll
         for (int v = 0; v < NV; ++v) {
             const int c = (v * blockDim.x + tx) * VEC;
             if (c >= cols) continue;
-            if (POST) col_factor(c, &wg[v * VEC]);
-            if (a.w_next) row::load<VEC>(a.w_next + c, &wn[v * VEC]);
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) wg[v * VEC + i] = 1.f;
+            if (a.w) row::load<VEC>(a.w + c, &wg[v * VEC]);
+            if (a.gate_mode == QMOE_GATE_COL) {
+                float g[VEC];
+                row::load<VEC>(a.gate + c, g);
+#pragma unroll
+                for (int i = 0; i < VEC; ++i) wg[v * VEC + i] *= g[i];
+            }
         }
+    };
+    auto next_weights = [&] {
+#pragma unroll
+        for (int v = 0; v < NV; ++v) {
+            const int c = (v * blockDim.x + tx) * VEC;
+            if (c < cols && a.w_next) row::load<VEC>(a.w_next + c, &wn[v * VEC]);
+        }
+    };
+    if (KEEP) {
+        if (POST) col_factors();
+        next_weights();
     }
-    int stage = 0;
     for (; row < a.rows; row += stride) {
         const float g_row = POST && a.gate_mode == QMOE_GATE_ROW ? a.gate[row] : 1.f;
-        next_row<VEC>(stages, stage, [&](int ahead, int to) { fetch(row + ahead * stride, to); });
-        const uint8_t* const from = mine + stage * a.stage_bytes;
-        if (++stage == stages) stage = 0;
+        const uint8_t* const from = ring.wait();
+        bool met = false;
         float o[E];
         read_row<VEC, NV, true, RT>(a.r, from, row, cols, o);
+        if (ring.lost) o[0] = NAN;
         if (POST) {
             float y[E];
             read_row<VEC, NV, true, YT>(a.y, from, row, cols, y);
+            if (!KEEP) col_factors();
             float scale = a.alpha * g_row;
             if (a.w) {
                 float s = 0.f;
@@ -95,6 +105,8 @@ norm_fwd_kernel(const FwdArgs a) {
                 for (int i = 0; i < E; ++i) s = fmaf(y[i], y[i], s);
                 const float rstd = rsqrtf(row::row_sum(s, sums[flip]) * inv_cols + a.eps);
                 flip ^= 1;
+                met = true;
+                ring.refill(row);
                 if (tx == 0 && a.rstd) a.rstd[row] = rstd;
                 scale *= rstd;
             }
@@ -108,35 +120,43 @@ norm_fwd_kernel(const FwdArgs a) {
             for (int v = 0; v < NV; ++v) {
                 const int c = (v * blockDim.x + tx) * VEC;
                 if (c >= cols) continue;
-                float f[VEC];
-                if (!KEEP) col_factor(c, f);
 #pragma unroll
                 for (int i = 0; i < VEC; ++i) {
                     const int e = v * VEC + i;
-                    o[e] = fmaf(y[e] * scale, KEEP ? wg[e] : f[i], o[e]);
+                    o[e] = fmaf(y[e] * scale, wg[e], o[e]);
                 }
                 row::store<VEC>(static_cast<RT*>(a.out) + row * a.ldo + c, &o[v * VEC]);
             }
         }
         if (a.w_next) {
+            if (!KEEP) next_weights();
             float s = 0.f;
 #pragma unroll
             for (int i = 0; i < E; ++i) s = fmaf(o[i], o[i], s);
             const float rstd = rsqrtf(row::row_sum(s, sums[flip]) * inv_cols + a.eps);
             flip ^= 1;
+            if (!met) ring.refill(row);
+            met = true;
             if (tx == 0 && a.rstd_next) a.rstd_next[row] = rstd;
 #pragma unroll
             for (int v = 0; v < NV; ++v) {
                 const int c = (v * blockDim.x + tx) * VEC;
                 if (c >= cols) continue;
-                float wv[VEC];
-                if (!KEEP) row::load<VEC>(a.w_next + c, wv);
                 float n[VEC];
 #pragma unroll
-                for (int i = 0; i < VEC; ++i) n[i] = o[v * VEC + i] * rstd * (KEEP ? wn[v * VEC + i] : wv[i]);
+                for (int i = 0; i < VEC; ++i) n[i] = o[v * VEC + i] * rstd * wn[v * VEC + i];
                 row::store<VEC>(static_cast<YT*>(a.n) + row * a.ldn + c, n);
             }
         }
+        if (!met || blockDim.x == 32) {
+            row_barrier();
+            if (!met) ring.refill(row);
+        }
+        if (a.stages == 1) {
+            row_barrier();
+            ring.post(row + stride, 0);
+        }
+        ring.next();
     }
 }
 
@@ -144,8 +164,8 @@ template <typename K>
 inline int start(K kernel, const Shape& s, FwdArgs& a, int row_bytes, cudaStream_t st) {
     const int threads = s.threads * s.rows_per_cta;
     const int64_t ctas = (a.rows + s.rows_per_cta - 1) / s.rows_per_cta;
-    // one wave: 1024 threads an SM where a thread holds 8 values, else 512; fewer CTAs where that leaves each two stages
-    int per_sm = (s.values() > 8 ? 512 : 1024) / threads;
+    // one wave of 512 threads an SM; fewer CTAs where that leaves each two stages
+    int per_sm = 512 / threads;
     a.stage_bytes = row_bytes;
     while (per_sm > 1 && stages_of((int64_t)row_bytes * s.rows_per_cta, 0, per_sm) < 2) --per_sm;
     a.stages = stages_of((int64_t)row_bytes * s.rows_per_cta, 0, per_sm);
@@ -163,17 +183,15 @@ struct Fwd {
     template <typename RT, typename YT>
     struct Go {
         static int go(FwdArgs& a, bool vec, cudaStream_t st) {
-            const Shape s = shape_of(a.cols, vec);
+            const Shape s = shape_of(a.cols, vec, 16);
             const int rb = stage_bytes(a.cols, sizeof(RT)), yb = stage_bytes(a.cols, sizeof(YT));
             a.y.off = rb;
             a.full_gate.off = rb + yb;
             const int bytes = rb + (POST ? yb : 0) + (a.full_gate.p ? yb : 0);
             if (vec) {
-                if (s.nv == 1) return start(norm_fwd_kernel<RT, YT, 1, 8, POST>, s, a, bytes, st);
                 if (s.nv == 2) return start(norm_fwd_kernel<RT, YT, 2, 8, POST>, s, a, bytes, st);
                 return start(norm_fwd_kernel<RT, YT, 4, 8, POST>, s, a, bytes, st);
             }
-            if (s.nv == 8) return start(norm_fwd_kernel<RT, YT, 8, 1, POST>, s, a, bytes, st);
             if (s.nv == 16) return start(norm_fwd_kernel<RT, YT, 16, 1, POST>, s, a, bytes, st);
             return start(norm_fwd_kernel<RT, YT, 32, 1, POST>, s, a, bytes, st);
         }

@@ -15,19 +15,18 @@ inline bool gate_mode_ok(int m) { return m >= QMOE_GATE_NONE && m <= QMOE_GATE_F
 // Rows of 16-byte accesses: an aligned base and row stride.
 inline bool row_aligned(const void* p, int64_t ld, int size) { return aligned16(p) && (ld * size) % 16 == 0; }
 
-// How a row is cut: nv vectors of vec columns in each of `threads` threads, 8,
-// 16 or 32 values each (the fewer a thread holds, the more threads share a
-// row's loads and a single row is spread widest), at most 512 threads; rows of
-// 32 threads go four to a CTA.
+// How a row is cut: nv vectors of vec columns in each of `threads` threads, at
+// least `values` each, then 16 and 32 where that takes more than 512 threads;
+// rows of 32 threads go four to a CTA.
 struct Shape {
     int vec, nv, threads, rows_per_cta;
     int values() const { return vec * nv; }
 };
 
-inline Shape shape_of(int64_t cols, bool vec) {
+inline Shape shape_of(int64_t cols, bool vec, int values) {
     Shape s;
     s.vec = vec ? 8 : 1;
-    for (int values = 8;; values *= 2) {
+    for (;; values *= 2) {
         s.nv = values / s.vec;
         const int64_t per = (cols + values - 1) / values;
         s.threads = (int)((per + 31) / 32 * 32);
@@ -39,15 +38,15 @@ inline Shape shape_of(int64_t cols, bool vec) {
 
 // ------------------------------------------------------------------ rows on their way
 //
-// A CTA's next rows are copied into a ring of shared memory stages with
-// cp.async while it works on the present one: HBM wants some 40 KB in flight
-// for each SM, more than the registers of the threads that share a row can
-// hold beside their work.  Rows of 16-byte accesses (VEC = 8): a thread copies
-// what it reads itself, so no barrier is needed.  Other rows: the threads copy
-// the 16-byte granules that the row lies in, in step with their addresses,
-// and meet at a barrier; a granule reaches past the row, but never past the
-// first and the last value of the matrix (there its values are copied one by
-// one).
+// The next rows come by bulk copies into a ring of shared memory stages while
+// the present one is worked on: HBM wants some 40 KB in flight for each SM,
+// more than the registers of the threads that share a row can hold beside
+// their work, and one thread's bulk copies cost the others no instructions
+// (with a cp.async by each thread for its own values the kernels were bound by
+// instruction issue).  Rows that do not start on 16-byte boundaries are copied
+// by the 16-byte granules that they lie in; a granule reaches past its row but
+// never past the first and the last value of the matrix, where the values are
+// copied one by one.
 
 // One matrix that a kernel reads: rows of `cols` values, at `off` in a stage.
 struct Source {
@@ -56,7 +55,7 @@ struct Source {
     int off;
 };
 
-constexpr int MAX_STAGES = 6;
+constexpr int MAX_STAGES = 6, MAX_ROWS = 4;  // stages of a ring, rings of a CTA
 
 inline int stage_bytes(int64_t cols, int size) { return (int)((cols * size + 15) / 16 * 16 + 16); }
 
@@ -66,33 +65,29 @@ inline int stages_of(int64_t bytes_per_stage, int64_t other_bytes, int ctas_per_
     return n > MAX_STAGES ? MAX_STAGES : n > 0 ? (int)n : 0;
 }
 
-template <int VEC, int NV, typename T>
-__device__ __forceinline__ void copy_row(const Source& s, uint8_t* stage, int64_t row, int64_t rows, int cols) {
-    if (!s.p) return;
+// Sends for one row of a matrix; returns the bytes that the barrier will count.
+template <int VEC, typename T>
+__device__ __forceinline__ uint32_t send_row(const Source& s, uint8_t* stage, int64_t row, int64_t rows, int cols,
+                                             uint64_t* bar) {
+    if (!s.p) return 0;
     const T* src = static_cast<const T*>(s.p) + row * s.ld;
     uint8_t* dst = stage + s.off;
     if constexpr (VEC == 8) {
-#pragma unroll
-        for (int v = 0; v < NV; ++v) {
-            const int c = (v * blockDim.x + threadIdx.x) * 8;
-            if (c >= cols) continue;
-#pragma unroll
-            for (int i = 0; i < (int)sizeof(T) / 2; ++i)
-                tc::cp_async_16(dst + c * sizeof(T) + i * 16, reinterpret_cast<const uint8_t*>(src + c) + i * 16);
-        }
+        tc::bulk_load(dst, src, cols * sizeof(T), bar);
+        return cols * sizeof(T);
     } else {
         const uintptr_t g0 = reinterpret_cast<uintptr_t>(src), g1 = g0 + (uintptr_t)cols * sizeof(T);
-        const uintptr_t lo = reinterpret_cast<uintptr_t>(s.p);
-        const uintptr_t hi = lo + ((uintptr_t)(rows - 1) * s.ld + cols) * sizeof(T);
         const uintptr_t base = g0 & ~uintptr_t(15);
-        for (uintptr_t a = base + threadIdx.x * 16; a < g1; a += blockDim.x * 16) {
-            if (a >= lo && a + 16 <= hi) {
-                tc::cp_async_16(dst + (a - base), reinterpret_cast<const void*>(a));
-            } else {
-                for (uintptr_t b = a > g0 ? a : g0; b < a + 16 && b < g1; b += sizeof(T))
-                    *reinterpret_cast<T*>(dst + (b - base)) = *reinterpret_cast<const T*>(b);
-            }
-        }
+        uintptr_t a0 = base, a1 = (g1 + 15) & ~uintptr_t(15);
+        if (row == 0 && a0 < g0) a0 += 16;
+        if (row == rows - 1 && a1 > g1) a1 -= 16;
+        if (a1 < a0) a1 = a0;  // a row within one granule
+        for (uintptr_t b = g0; b < a0 && b < g1; b += sizeof(T))
+            *reinterpret_cast<T*>(dst + (b - base)) = *reinterpret_cast<const T*>(b);
+        for (uintptr_t b = a1 > g0 ? a1 : g0; b < g1; b += sizeof(T))
+            *reinterpret_cast<T*>(dst + (b - base)) = *reinterpret_cast<const T*>(b);
+        if (a1 > a0) tc::bulk_load(dst + (a0 - base), reinterpret_cast<const void*>(a0), (uint32_t)(a1 - a0), bar);
+        return (uint32_t)(a1 - a0);
     }
 }
 
@@ -114,27 +109,53 @@ __device__ __forceinline__ void read_row(const Source& s, const uint8_t* stage, 
     }
 }
 
+// The ring of one row's threads.  send(row, stage, barrier) issues a row's
+// copies and returns their bytes; one thread calls it.  A stage is refilled
+// when its row's threads have met once more after reading it (refill).
+template <typename Send>
+struct Ring {
+    uint64_t* full;
+    uint8_t* base;
+    int stages, bytes;
+    int64_t rows, stride;
+    bool lead;
+    Send send;
+    int stage = 0;
+    uint32_t phase = 0;
+    bool lost = false;  // a copy did not arrive in time: what follows is NaN
+
+    __device__ __forceinline__ void post(int64_t row, int at) {
+        if (lead && row < rows) tc::mbar_arrive_expect_tx(&full[at], send(row, base + at * bytes, &full[at]));
+    }
+    __device__ __forceinline__ void begin(int64_t row) {
+        for (int i = 0; i + 1 < stages || i == 0; ++i) post(row + i * stride, i);
+    }
+    // The stage of the present row.
+    __device__ __forceinline__ const uint8_t* wait() {
+        if (!lost && !tc::mbar_wait(&full[stage], phase)) lost = true;
+        return base + stage * bytes;
+    }
+    // The row's threads have met since `row` was waited for: the stage read before it is free.
+    __device__ __forceinline__ void refill(int64_t row) {
+        if (stages > 1 && !lost) post(row + (stages - 1) * stride, stage == 0 ? stages - 1 : stage - 1);
+    }
+    __device__ __forceinline__ void next() {
+        if (++stage == stages) {
+            stage = 0;
+            phase ^= 1;
+        }
+    }
+};
+template <typename Send>
+__device__ __forceinline__ Ring<Send> make_ring(uint64_t* full, uint8_t* base, int stages, int bytes, int64_t rows,
+                                                int64_t stride, bool lead, Send send) {
+    return Ring<Send>{full, base, stages, bytes, rows, stride, lead, send};
+}
+
 // The threads of a row meet.
 __device__ __forceinline__ void row_barrier() {
     if (blockDim.x == 32) __syncwarp();
     else __syncthreads();
-}
-
-// Waits for the present row, in stage `stage`, and sends for the row that is
-// stages - 1 further on, into the stage that was read last time.  fetch(ahead,
-// stage) commits one group.  With a single stage the row is fetched here.
-template <int VEC, typename Fetch>
-__device__ __forceinline__ void next_row(int stages, int stage, Fetch&& fetch) {
-    if (stages > 1) {
-        tc::cp_async_wait_dyn(stages - 2);
-        if (VEC == 1) row_barrier();
-        fetch(stages - 1, stage == 0 ? stages - 1 : stage - 1);
-    } else {
-        if (VEC == 1) row_barrier();
-        fetch(0, 0);
-        tc::cp_async_wait<0>();
-        if (VEC == 1) row_barrier();
-    }
 }
 
 // (stream type, block type): the same type twice, or a 16-bit block beside an

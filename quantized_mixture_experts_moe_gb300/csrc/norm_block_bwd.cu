@@ -42,7 +42,7 @@ struct BwdArgs {
 
 // Sums over rows that one thread owns: registers, or shared memory words laid
 // out so that a warp's accesses hit distinct banks.
-template <int E, int VEC, bool SMEM>
+template <int E, bool SMEM>
 struct ColSums {
     float r[SMEM ? 1 : E];
     float* s;
@@ -67,68 +67,88 @@ struct ColSums {
     }
 };
 
-// RING: the rows come through shared memory stages; else, where the widest
-// rows' column sums leave no room for them, straight from the matrices.
+// Where a kernel of E values a thread keeps things: 8: sums and weights in
+// registers; 16: the weights in shared memory; 32: the sums there, and then no
+// room for a ring, so rows and weights come straight from global memory.
+// POST: the whole sandwich; without it the kernel is norm_pre's gradient.
 template <typename RT, typename YT, int NV, int VEC, bool POST>
 __global__ void __launch_bounds__(512, 1)
 norm_bwd_kernel(const BwdArgs a) {
     constexpr int E = NV * VEC;
-    constexpr bool SMEM = E > 16, RING = !SMEM;
-    constexpr bool KEEP = E <= 8;
+    constexpr bool SMEM = E > 16, RING = !SMEM, KEEP = E <= 8, W_SMEM = E == 16;
     __shared__ __align__(16) float sums[2][16];
-    extern __shared__ __align__(16) uint8_t dynamic[];  // column sums, then the ring
-    const int tx = threadIdx.x, cols = a.cols, stages = a.stages;
+    __shared__ uint64_t full[MAX_ROWS][MAX_STAGES];
+    extern __shared__ __align__(128) uint8_t dynamic[];  // the ring; column sums or weights [w_next, w]
+    const int tx = threadIdx.x, cols = a.cols;
     const int64_t stride = (int64_t)gridDim.x * blockDim.y;
     const float inv_cols = 1.f / (float)cols;
     const bool next = POST ? a.dn.p != nullptr : true;
     int flip = 0;
 
-    ColSums<E, VEC, SMEM> sum_wn, sum_w, sum_g;
-    float* const cols_smem = reinterpret_cast<float*>(dynamic);
+    float* const cols_smem = reinterpret_cast<float*>(dynamic + (int64_t)blockDim.y * a.stages * a.stage_bytes);
+    ColSums<E, SMEM> sum_wn, sum_w, sum_g;
     sum_wn.init(cols_smem);
     if (POST) {
         sum_w.init(cols_smem + E * blockDim.x);
         sum_g.init(cols_smem + 2 * E * blockDim.x);
     }
-    uint8_t* const mine = dynamic + (SMEM ? (POST ? 3 : 1) * E * blockDim.x * 4 : 0) +
-                          (int64_t)threadIdx.y * stages * a.stage_bytes;
-    auto fetch = [&](int64_t row, int stage) {
-        if (row < a.rows) {
-            uint8_t* to = mine + stage * a.stage_bytes;
-            copy_row<VEC, NV, RT>(a.dout, to, row, a.rows, cols);
-            copy_row<VEC, NV, YT>(a.dn, to, row, a.rows, cols);
-            copy_row<VEC, NV, RT>(a.out, to, row, a.rows, cols);
-            if (POST) copy_row<VEC, NV, YT>(a.y, to, row, a.rows, cols);
-            if (POST) copy_row<VEC, NV, YT>(a.full_gate, to, row, a.rows, cols);
-        }
-        tc::cp_async_commit();
-    };
+    auto ring = make_ring(full[threadIdx.y], dynamic + (int64_t)threadIdx.y * a.stages * a.stage_bytes, a.stages,
+                          a.stage_bytes, a.rows, stride, tx == 0, [&](int64_t row, uint8_t* to, uint64_t* bar) {
+                              uint32_t n = send_row<VEC, RT>(a.dout, to, row, a.rows, cols, bar);
+                              n += send_row<VEC, YT>(a.dn, to, row, a.rows, cols, bar);
+                              n += send_row<VEC, RT>(a.out, to, row, a.rows, cols, bar);
+                              if (POST) n += send_row<VEC, YT>(a.y, to, row, a.rows, cols, bar);
+                              if (POST) n += send_row<VEC, YT>(a.full_gate, to, row, a.rows, cols, bar);
+                              return n;
+                          });
+    if (RING && tx == 0)
+        for (int i = 0; i < MAX_STAGES; ++i) tc::mbar_init(&full[threadIdx.y][i], 1);
+    if (tx < 32) sums[tx >> 4][tx & 15] = 0.f;
+    tc::fence_barrier_init();
+    __syncthreads();
     int64_t row = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
     pdl_sync();
-    if (RING)
-        for (int i = 0; i + 1 < stages; ++i) fetch(row + i * stride, i);
-    float w[KEEP ? E : 1], wn[KEEP ? E : 1], gc[KEEP ? E : 1];
-    if (KEEP) {
+    if (RING) ring.begin(row);
+    float w[KEEP ? E : VEC], wn[KEEP ? E : VEC], gc[KEEP ? E : VEC];
+    auto column = [&](int v) { return (int)(v * blockDim.x + tx) * VEC; };
 #pragma unroll
-        for (int v = 0; v < NV; ++v) {
-            const int c = (v * blockDim.x + tx) * VEC;
-            if (c >= cols) continue;
+    for (int v = 0; v < NV; ++v) {
+        const int c = column(v);
+        if (c >= cols) continue;
+        if (KEEP) {
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) w[v * VEC + i] = gc[v * VEC + i] = 1.f;
             if (POST && a.w) row::load<VEC>(a.w + c, &w[v * VEC]);
             if (next) row::load<VEC>(a.w_next + c, &wn[v * VEC]);
             if (POST && a.gate_mode == QMOE_GATE_COL) row::load<VEC>(a.gate + c, &gc[v * VEC]);
+        } else if (W_SMEM) {  // a thread reads back what it wrote itself
+            float t[VEC];
+            if (next) {
+                row::load<VEC>(a.w_next + c, t);
+                row::store<VEC>(cols_smem + c, t);
+            }
+            if (POST && a.w) {
+                row::load<VEC>(a.w + c, t);
+                row::store<VEC>(cols_smem + (cols + 7) / 8 * 8 + c, t);
+            }
         }
     }
-    int stage = 0;
+    // a vector's weights, where they are not in registers from row to row
+    auto weights_next = [&](int c, int v) -> const float* {
+        if (KEEP) return &wn[v * VEC];
+        row::load<VEC>(W_SMEM ? cols_smem + c : a.w_next + c, wn);
+        return wn;
+    };
     for (; row < a.rows; row += stride) {
         const float rstd_n = next ? a.rstd_next[row] : 0.f;
         const float rstd = POST && a.w ? a.rstd[row] : 1.f;
         const float g_row = POST && a.gate_mode == QMOE_GATE_ROW ? a.gate[row] : 1.f;
-        const uint8_t* from = nullptr;
-        if (RING) {
-            next_row<VEC>(stages, stage, [&](int ahead, int to) { fetch(row + ahead * stride, to); });
-            from = mine + stage * a.stage_bytes;
-            if (++stage == stages) stage = 0;
-        }
+        const uint8_t* const from = RING ? ring.wait() : nullptr;
+        bool met = false;
+        auto meet = [&] {  // the row's threads have met: what the last row's stage held is free
+            if (RING && !met) ring.refill(row);
+            met = true;
+        };
         float d[E];
         if (a.dout.p) {
             read_row<VEC, NV, RING, RT>(a.dout, from, row, cols, d);
@@ -136,63 +156,72 @@ norm_bwd_kernel(const BwdArgs a) {
 #pragma unroll
             for (int e = 0; e < E; ++e) d[e] = 0.f;
         }
+        if (RING && ring.lost) d[0] = NAN;
         if (next) {
             float x[E], dn[E], s = 0.f;
             read_row<VEC, NV, RING, YT>(a.dn, from, row, cols, dn);
             read_row<VEC, NV, RING, RT>(a.out, from, row, cols, x);
 #pragma unroll
             for (int v = 0; v < NV; ++v) {
-                const int c = (v * blockDim.x + tx) * VEC;
-                if (c >= cols) continue;
-                float wv[VEC];
-                if (!KEEP) row::load<VEC>(a.w_next + c, wv);
+                if (column(v) >= cols) continue;
+                const float* const wv = weights_next(column(v), v);
 #pragma unroll
                 for (int i = 0; i < VEC; ++i) {
                     const int e = v * VEC + i;
                     x[e] *= rstd_n;
                     sum_wn.add(e, dn[e] * x[e]);
-                    dn[e] *= KEEP ? wn[e] : wv[i];
+                    dn[e] *= wv[i];
                     s = fmaf(dn[e], x[e], s);
                 }
             }
             const float mean = row::row_sum(s, sums[flip]) * inv_cols;
             flip ^= 1;
+            meet();
 #pragma unroll
             for (int e = 0; e < E; ++e) d[e] = fmaf(rstd_n, dn[e] - x[e] * mean, d[e]);
         }
 #pragma unroll
-        for (int v = 0; v < NV; ++v) {
-            const int c = (v * blockDim.x + tx) * VEC;
-            if (c < cols) row::store<VEC>(static_cast<RT*>(a.dr) + row * a.lddr + c, &d[v * VEC]);
-        }
+        for (int v = 0; v < NV; ++v)
+            if (column(v) < cols) row::store<VEC>(static_cast<RT*>(a.dr) + row * a.lddr + column(v), &d[v * VEC]);
         if (POST) {
-            float t[E], g[E], s = 0.f, s_gate = 0.f;
+            float t[E], s = 0.f, s_gate = 0.f;
             read_row<VEC, NV, RING, YT>(a.y, from, row, cols, t);
-            if (a.gate_mode == QMOE_GATE_FULL) read_row<VEC, NV, RING, YT>(a.full_gate, from, row, cols, g);
             // t = y rstd; d becomes dz w
 #pragma unroll
             for (int v = 0; v < NV; ++v) {
-                const int c = (v * blockDim.x + tx) * VEC;
+                const int c = column(v);
                 if (c >= cols) continue;
-                float wv[VEC], gv[VEC], dg[VEC];
-                if (!KEEP && a.w) row::load<VEC>(a.w + c, wv);
-                if (!KEEP && a.gate_mode == QMOE_GATE_COL) row::load<VEC>(a.gate + c, gv);
+                float wt[VEC], g[VEC], dg[VEC];
+#pragma unroll
+                for (int i = 0; i < VEC; ++i) {
+                    wt[i] = KEEP ? w[v * VEC + i] : 1.f;
+                    g[i] = g_row;
+                    if (KEEP) g[i] *= gc[v * VEC + i];
+                }
+                if (!KEEP && a.w) row::load<VEC>(W_SMEM ? cols_smem + (cols + 7) / 8 * 8 + c : a.w + c, wt);
+                if (!KEEP && a.gate_mode == QMOE_GATE_COL) row::load<VEC>(a.gate + c, g);
+                if (a.gate_mode == QMOE_GATE_FULL) {
+                    const YT* at = static_cast<const YT*>(a.full_gate.p) + row * a.full_gate.ld;
+                    if (RING)
+                        at = reinterpret_cast<const YT*>(
+                            from + a.full_gate.off + (VEC == 1 ? reinterpret_cast<uintptr_t>(at) & 15 : 0));
+                    row::load<VEC>(at + c, g);
+                }
 #pragma unroll
                 for (int i = 0; i < VEC; ++i) {
                     const int e = v * VEC + i;
-                    const float wt = a.w ? (KEEP ? w[e] : wv[i]) : 1.f;
                     const float ad = a.alpha * d[e];
-                    const float gate = a.gate_mode == QMOE_GATE_FULL  ? g[e]
-                                       : a.gate_mode == QMOE_GATE_COL ? (KEEP ? gc[e] : gv[i])
-                                                                      : g_row;
                     t[e] *= rstd;
-                    const float dz = ad * gate;
-                    dg[i] = ad * (t[e] * wt);
+                    const float dz = ad * g[i];
+                    dg[i] = ad * (t[e] * wt[i]);
                     s_gate += dg[i];
-                    if (a.gate_mode == QMOE_GATE_COL) sum_g.add(e, dg[i]);
-                    if (a.w) sum_w.add(e, dz * t[e]);
-                    d[e] = dz * wt;
+                    sum_w.add(e, dz * t[e]);
+                    d[e] = dz * wt[i];
                     s = fmaf(d[e], t[e], s);
+                }
+                if (a.gate_mode == QMOE_GATE_COL) {
+#pragma unroll
+                    for (int i = 0; i < VEC; ++i) sum_g.add(v * VEC + i, dg[i]);
                 }
                 if (a.gate_mode == QMOE_GATE_FULL)
                     row::store<VEC>(static_cast<YT*>(a.dgate) + row * a.lddg + c, dg);
@@ -200,30 +229,39 @@ norm_bwd_kernel(const BwdArgs a) {
             if (a.gate_mode == QMOE_GATE_ROW) {
                 s_gate = row::row_sum(s_gate, sums[flip]);
                 flip ^= 1;
+                meet();
                 if (tx == 0) static_cast<float*>(a.dgate)[row] = s_gate;
             }
             if (a.w) {
                 s = row::row_sum(s, sums[flip]) * inv_cols;
                 flip ^= 1;
-            }
-            if (a.w) {
+                meet();
 #pragma unroll
                 for (int e = 0; e < E; ++e) d[e] = rstd * (d[e] - t[e] * s);
             }
 #pragma unroll
-            for (int v = 0; v < NV; ++v) {
-                const int c = (v * blockDim.x + tx) * VEC;
-                if (c < cols) row::store<VEC>(static_cast<YT*>(a.dy) + row * a.lddy + c, &d[v * VEC]);
+            for (int v = 0; v < NV; ++v)
+                if (column(v) < cols) row::store<VEC>(static_cast<YT*>(a.dy) + row * a.lddy + column(v), &d[v * VEC]);
+        }
+        if (RING) {
+            if (!met || blockDim.x == 32) {
+                row_barrier();
+                meet();
             }
+            if (a.stages == 1) {
+                row_barrier();
+                ring.post(row + stride, 0);
+            }
+            ring.next();
         }
     }
     const int64_t part = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
-        const int c = (v * blockDim.x + tx) * VEC;
+        const int c = column(v);
         if (c >= cols) continue;
         float t[VEC];
-        auto put = [&](ColSums<E, VEC, SMEM>& s, int which) {
+        auto put = [&](ColSums<E, SMEM>& s, int which) {
 #pragma unroll
             for (int i = 0; i < VEC; ++i) t[i] = s.get(v * VEC + i);
             float* to = a.part + (which * a.part_rows + part) * cols + c;
@@ -274,7 +312,7 @@ inline int64_t bwd_ctas(const Shape& s, int64_t rows) {
 inline int64_t part_rows(int64_t rows, int64_t cols) {
     int64_t most = 1;
     for (int vec = 0; vec < 2; ++vec) {
-        const Shape s = shape_of(cols, vec != 0);
+        const Shape s = shape_of(cols, vec != 0, 8);
         const int64_t n = bwd_ctas(s, rows) * s.rows_per_cta;
         most = n > most ? n : most;
     }
@@ -283,11 +321,14 @@ inline int64_t part_rows(int64_t rows, int64_t cols) {
 
 template <typename K>
 inline int start(K kernel, const Shape& s, BwdArgs& a, int sums, int row_bytes, int64_t ctas, cudaStream_t st) {
-    const int64_t sum_bytes = s.values() > 16 ? (int64_t)sums * s.values() * s.threads * 4 : 0;
+    const int64_t padded = (a.cols + 7) / 8 * 8;
+    const int64_t besides = s.values() == 32   ? (int64_t)sums * 32 * s.threads * 4
+                            : s.values() == 16 ? (sums == 3 ? 2 : 1) * padded * 4
+                                               : 0;
     a.stage_bytes = row_bytes;
-    a.stages = s.values() > 16 ? 0 : stages_of((int64_t)row_bytes * s.rows_per_cta, sum_bytes, per_sm_of(s));
-    if (s.values() <= 16 && !a.stages) return QMOE_ERR_UNSUPPORTED;
-    const size_t smem = (size_t)(sum_bytes + (int64_t)a.stages * row_bytes * s.rows_per_cta);
+    a.stages = s.values() == 32 ? 0 : stages_of((int64_t)row_bytes * s.rows_per_cta, besides, per_sm_of(s));
+    if (s.values() < 32 && !a.stages) return QMOE_ERR_UNSUPPORTED;
+    const size_t smem = (size_t)(besides + (int64_t)a.stages * row_bytes * s.rows_per_cta);
     if (smem > 48 * 1024 - 1024 &&
         cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 225 * 1024) != cudaSuccess)
         return QMOE_ERR_CUDA;
@@ -329,7 +370,7 @@ template <template <typename, typename> class F>
 inline int run(BwdArgs& a, int rt, int yt, bool vec, float* const (&out)[3], void* ws, cudaStream_t st) {
     a.part = static_cast<float*>(ws);
     a.part_rows = part_rows(a.rows, a.cols);
-    const Shape s = shape_of(a.cols, vec);
+    const Shape s = shape_of(a.cols, vec, 8);
     const int64_t ctas = bwd_ctas(s, a.rows);
     if (ctas > 0) {
         const int rc = by_types<F>(rt, yt, a, s, ctas, st);

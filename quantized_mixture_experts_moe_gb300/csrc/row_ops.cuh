@@ -107,28 +107,27 @@ __device__ __forceinline__ void store(T* p, const float* v) {
     }
 }
 
-// Sum of v over the threads of a row: the lanes of a warp where the row has 32
-// threads, else the whole CTA (blockDim.x <= 512 threads; `buf` is one of the
-// two halves of a 2 x 16 float array, alternated by the caller so that one
-// barrier per sum is enough).  The order is fixed.
 __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
     return v;
 }
+// Sum of v over the threads of a row: the lanes of a warp where the row has 32
+// threads, else the whole CTA (blockDim.x <= 512 threads).  `buf` is one of the
+// two halves of a 2 x 16 float array, zeroed before the first sum and
+// alternated by the caller, so that one barrier per sum is enough.  The order
+// is fixed.
 __device__ __forceinline__ float row_sum(float v, float (&buf)[16]) {
     v = warp_sum(v);
     if (blockDim.x == 32) return v;
     if ((threadIdx.x & 31) == 0) buf[threadIdx.x >> 5] = v;
     __syncthreads();
-    const int warps = blockDim.x >> 5;
     const float4* part = reinterpret_cast<const float4*>(buf);
-    v = 0.f;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        if (4 * i >= warps) break;
-        const float4 p = part[i];
-        v += (p.x + (4 * i + 1 < warps ? p.y : 0.f)) + ((4 * i + 2 < warps ? p.z : 0.f) + (4 * i + 3 < warps ? p.w : 0.f));
+    const float4 p = part[0], q = part[1];
+    v = ((p.x + p.y) + (p.z + p.w)) + ((q.x + q.y) + (q.z + q.w));
+    if (blockDim.x > 256) {
+        const float4 r = part[2], s = part[3];
+        v += ((r.x + r.y) + (r.z + r.w)) + ((s.x + s.y) + (s.z + s.w));
     }
     return v;
 }
