@@ -9,7 +9,6 @@ when the CUDA library is missing or fails to load, every call raises.
 from __future__ import annotations
 
 import ctypes
-import dataclasses
 import functools
 import os
 
@@ -473,42 +472,62 @@ def moe_forward(scheme, x, topk_ids, topk_w, w1, w1_s, w2, w2_s, H=None, I=None,
 GATE_NONE, GATE_ROW, GATE_COL, GATE_FULL = 0, 1, 2, 3
 FP8_BLOCK = 128
 
+_F32, _U8, _I32 = torch.float32, torch.uint8, torch.int32
 _DTYPE = {torch.float32: 0, torch.bfloat16: 1, torch.int16: 1, torch.float16: 2}
 
+# These calls are made for single tokens too, where the kernels take a few
+# microseconds: the checks below cost one comparison each, messages are built
+# only to be raised, and the stream is asked for by device index.
+_empty = torch.empty
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # absent from builds without CUDA
 
-def _dtype(t) -> int:
+
+def _dtype(dtype) -> int:
     try:
-        return _DTYPE[t if isinstance(t, torch.dtype) else t.dtype]
+        return _DTYPE[dtype]
     except KeyError:
-        raise ValueError(f"expected float32, bfloat16 or float16, got {t if isinstance(t, torch.dtype) else t.dtype}") from None
+        raise ValueError(f"expected float32, bfloat16 or float16, got {dtype}") from None
 
 
-def _need(ok, what):
-    if not ok:
-        raise ValueError(what)
+def _here(t):
+    """The current stream of the device of tensor t."""
+    i = t.get_device()
+    if i < 0:
+        raise QmoeError("qmoe kernels take device tensors")
+    return _raw_stream(i)
 
 
-def _rows(t, shape=None):
-    """(pointer, row stride) of a 2-D device tensor with contiguous rows."""
-    _need(t.dim() == 2 and (shape is None or tuple(t.shape) == tuple(shape)),
-          f"expected a tensor of shape {'[rows, cols]' if shape is None else list(shape)}, got {list(t.shape)}")
+def _rows(t, T, H):
+    """(pointer, row stride) of a [T, H] device tensor with contiguous rows."""
+    if t.shape != (T, H):
+        raise ValueError(f"expected a tensor of shape {[T, H]}, got {list(t.shape)}")
     if not t.is_cuda:
         raise QmoeError("qmoe kernels take device tensors")
-    rows, cols = t.shape
-    if cols > 1 and t.stride(1) != 1:
+    ld, step = t.stride()
+    if step != 1 and H > 1:
         raise QmoeError("qmoe kernels take rows of contiguous columns")
-    ld = t.stride(0) if rows > 1 else max(cols, t.stride(0))
-    if ld < cols:
-        raise QmoeError("qmoe kernels take rows that do not overlap")
+    if ld < H:
+        if T > 1:
+            raise QmoeError("qmoe kernels take rows that do not overlap")
+        ld = H
     return t.data_ptr(), ld
 
 
-def _vec(t, n, dtype=torch.float32):
-    """Pointer of a contiguous 1-D device tensor of n values (None: NULL)."""
+def _vec(t, n, dtype=_F32):
+    """Pointer of a contiguous device tensor of n values (None: NULL)."""
     if t is None:
         return None
-    _need(t.dtype == dtype and t.numel() == n, f"expected {n} values of {dtype}, got {list(t.shape)} of {t.dtype}")
-    return _ptr(t)
+    if t.dtype != dtype or t.numel() != n:
+        raise ValueError(f"expected {n} values of {dtype}, got {list(t.shape)} of {t.dtype}")
+    if not t.is_cuda:
+        raise QmoeError("qmoe kernels take device tensors")
+    if not t.is_contiguous():
+        raise QmoeError("qmoe kernels take contiguous tensors")
+    return t.data_ptr()
+
+
+def _at(t):
+    return None if t is None else t.data_ptr()
 
 
 def _on_stream(fn):
@@ -523,8 +542,12 @@ def _on_stream(fn):
     return call
 
 
-def _ws_for(nbytes, ws, like):
-    return alloc_workspace(nbytes, like.device) if ws is None else ws
+def _ws_for(nbytes, ws, device):
+    """(pointer, bytes, tensor) of a workspace: the caller's, or a new one."""
+    if ws is None:
+        ws = _empty(max(nbytes, 256), dtype=_U8, device=device)
+        return ws.data_ptr(), max(nbytes, 256), ws
+    return _ptr(ws), ws.numel() * ws.element_size(), ws
 
 
 @_on_stream
@@ -532,11 +555,16 @@ def norm_pre(x, w, eps=1e-6, out_dtype=None):
     """n = x / rms(x) * w for rows x [T, H], w fp32 [H]; returns (n, rstd fp32 [T]).  n has x's type, or a 16-bit
     out_dtype beside fp32 x."""
     T, H = x.shape
-    n = torch.empty((T, H), dtype=x.dtype if out_dtype is None else out_dtype, device=x.device)
-    rstd = torch.empty(T, dtype=torch.float32, device=x.device)
-    xp, ldx = _rows(x)
-    _check(lib().qmoe_norm_pre(T, H, _dtype(x), _dtype(n), xp, ldx, _vec(w, H), eps, n.data_ptr(), H, rstd.data_ptr(),
-                               _stream()), "qmoe_norm_pre")
+    dev, dtype = x.device, x.dtype
+    if out_dtype is None:
+        out_dtype = dtype
+    xp, ldx = _rows(x, T, H)
+    n = _empty((T, H), dtype=out_dtype, device=dev)
+    rstd = _empty((T,), dtype=_F32, device=dev)
+    rc = lib().qmoe_norm_pre(T, H, _dtype(dtype), _dtype(out_dtype), xp, ldx, _vec(w, H), eps, n.data_ptr(), H,
+                             rstd.data_ptr(), _here(x))
+    if rc:
+        _check(rc, "qmoe_norm_pre")
     return n, rstd
 
 
@@ -544,16 +572,22 @@ def norm_pre(x, w, eps=1e-6, out_dtype=None):
 def norm_pre_backward(dn, x, rstd, w, dres=None, ws=None):
     """Gradients of norm_pre: (dx [T, H] in x's type, dw fp32 [H]); dres (x's type) is added to dx."""
     T, H = x.shape
-    _need(dres is None or dres.dtype == x.dtype, "dres has x's type")
-    dx = torch.empty((T, H), dtype=x.dtype, device=x.device)
-    dw = torch.empty(H, dtype=torch.float32, device=x.device)
-    ws = _ws_for(int(lib().qmoe_norm_bwd_workspace_bytes(T, H)), ws, x)
-    xp, ldx = _rows(x)
-    dnp, lddn = _rows(dn, (T, H))
-    drp, lddr = (None, 0) if dres is None else _rows(dres, (T, H))
-    _check(lib().qmoe_norm_pre_backward(T, H, _dtype(x), _dtype(dn), dnp, lddn, xp, ldx, _vec(rstd, T), _vec(w, H), drp,
-                                        lddr, dx.data_ptr(), H, dw.data_ptr(), *_ws(ws), _stream()),
-           "qmoe_norm_pre_backward")
+    dev, dtype = x.device, x.dtype
+    xp, ldx = _rows(x, T, H)
+    dnp, lddn = _rows(dn, T, H)
+    drp, lddr = None, 0
+    if dres is not None:
+        if dres.dtype != dtype:
+            raise ValueError("dres has x's type")
+        drp, lddr = _rows(dres, T, H)
+    dx = _empty((T, H), dtype=dtype, device=dev)
+    dw = _empty((H,), dtype=_F32, device=dev)
+    L = lib()
+    wp, wn, ws = _ws_for(L.qmoe_norm_bwd_workspace_bytes(T, H), ws, dev)
+    rc = L.qmoe_norm_pre_backward(T, H, _dtype(dtype), _dtype(dn.dtype), dnp, lddn, xp, ldx, _vec(rstd, T), _vec(w, H), drp,
+                                  lddr, dx.data_ptr(), H, dw.data_ptr(), wp, wn, _here(x))
+    if rc:
+        _check(rc, "qmoe_norm_pre_backward")
     return dx, dw
 
 
@@ -564,11 +598,11 @@ def _gate(gate, T, H, block_dtype):
     if gate is None:
         return GATE_NONE, None, 0
     shape = tuple(gate.shape)
-    if shape == (T, H) and gate.dtype == block_dtype:
-        return (GATE_FULL, *_rows(gate))
-    if shape in ((T,), (T, 1)):
+    if shape == (T,) or shape == (T, 1) and gate.dtype == _F32:
         return GATE_ROW, _vec(gate, T), 0
-    if shape in ((H,), (1, H)):
+    if shape == (T, H) and gate.dtype == block_dtype:
+        return (GATE_FULL, *_rows(gate, T, H))
+    if shape == (H,) or shape == (1, H):
         return GATE_COL, _vec(gate, H), 0
     raise ValueError(f"a gate is fp32 [T, 1], [T], [1, H] or [H], or [T, H] of the block's type; got {list(shape)} of {gate.dtype}")
 
@@ -577,24 +611,24 @@ def _gate(gate, T, H, block_dtype):
 def norm_post(r, y, w=None, gate=None, alpha=1.0, w_next=None, eps=1e-6):
     """out = r + alpha * gate * (y / rms(y) * w) for rows r, y [T, H] (w None: y itself), and n = out / rms(out) * w_next
     where w_next is given.  Returns (out, n, rstd, rstd_next), None for what is not computed.  out has r's type, n y's.
-    gate: None, fp32 [T, 1] or [T] (one for each row),
-    fp32 [1, H] or [H] (one for each column; [H] is taken as [T] where T == H), or [T, H] of y's type."""
+    gate: None, fp32 [T, 1] or [T] (one for each row), fp32 [1, H] or [H] (one for each column; [H] is taken as [T]
+    where T == H), or [T, H] of y's type."""
     T, H = y.shape
-    dev = y.device
-    rp, ldr = _rows(r, (T, H))
-    yp, ldy = _rows(y)
-    mode, gp, ldg = _gate(gate, T, H, y.dtype)
-    out = torch.empty((T, H), dtype=r.dtype, device=dev)
+    dev, st, bt = y.device, r.dtype, y.dtype
+    rp, ldr = _rows(r, T, H)
+    yp, ldy = _rows(y, T, H)
+    mode, gp, ldg = _gate(gate, T, H, bt)
+    out = _empty((T, H), dtype=st, device=dev)
     n = rstd = rstd_next = None
     if w is not None:
-        rstd = torch.empty(T, dtype=torch.float32, device=dev)
+        rstd = _empty((T,), dtype=_F32, device=dev)
     if w_next is not None:
-        n = torch.empty((T, H), dtype=y.dtype, device=dev)
-        rstd_next = torch.empty(T, dtype=torch.float32, device=dev)
-    _check(lib().qmoe_norm_post(T, H, _dtype(r), _dtype(y), rp, ldr, yp, ldy, _vec(w, H), mode, gp, ldg, alpha,
-                                _vec(w_next, H), eps, out.data_ptr(), H, None if n is None else n.data_ptr(), H,
-                                None if rstd is None else rstd.data_ptr(),
-                                None if rstd_next is None else rstd_next.data_ptr(), _stream()), "qmoe_norm_post")
+        n = _empty((T, H), dtype=bt, device=dev)
+        rstd_next = _empty((T,), dtype=_F32, device=dev)
+    rc = lib().qmoe_norm_post(T, H, _dtype(st), _dtype(bt), rp, ldr, yp, ldy, _vec(w, H), mode, gp, ldg, alpha,
+                              _vec(w_next, H), eps, out.data_ptr(), H, _at(n), H, _at(rstd), _at(rstd_next), _here(y))
+    if rc:
+        _check(rc, "qmoe_norm_post")
     return out, n, rstd, rstd_next
 
 
@@ -604,48 +638,54 @@ def norm_post_backward(dout, y, w=None, rstd=None, gate=None, alpha=1.0, dn=None
     """Gradients of norm_post from dout (the stream's; None: 0) and dn (of n; None: 0): (dr, dy, dw, dgate, dw_next), None
     for what has no input.  y, w, gate, alpha, w_next as in the forward call, out, rstd, rstd_next as it returned them."""
     T, H = y.shape
-    dev = y.device
-    _need(dout is not None or dn is not None, "norm_post_backward needs dout or dn")
-    _need(dn is None or (out is not None and w_next is not None and rstd_next is not None), "dn needs out, w_next and rstd_next")
-    _need(w is None or rstd is not None, "w needs rstd")
-    _need(dn is None or dn.dtype == y.dtype, "dn has y's type")
-    stream_t = dout if dout is not None else out
-    _need(dn is None or out.dtype == stream_t.dtype, "out has dout's type")
-    mode, gp, ldg = _gate(gate, T, H, y.dtype)
-    dr = torch.empty((T, H), dtype=stream_t.dtype, device=dev)
-    dy = torch.empty((T, H), dtype=y.dtype, device=dev)
-    dw = None if w is None else torch.empty(H, dtype=torch.float32, device=dev)
-    dw_next = None if dn is None else torch.empty(H, dtype=torch.float32, device=dev)
-    dgate = None if gate is None else torch.empty(gate.shape, dtype=gate.dtype, device=dev)
+    dev, bt = y.device, y.dtype
+    if dout is None and dn is None:
+        raise ValueError("norm_post_backward needs dout or dn")
+    if w is not None and rstd is None:
+        raise ValueError("w needs rstd")
+    dop, lddo, dnp, lddn, op, ldo, wnp, rnp = None, 0, None, 0, None, 0, None, None
+    dw = dw_next = dgate = None
+    if dn is not None:
+        if out is None or w_next is None or rstd_next is None:
+            raise ValueError("dn needs out, w_next and rstd_next")
+        if dn.dtype != bt or dout is not None and out.dtype != dout.dtype:
+            raise ValueError("dn has y's type, and out dout's")
+        dnp, lddn = _rows(dn, T, H)
+        op, ldo = _rows(out, T, H)
+        wnp, rnp = _vec(w_next, H), _vec(rstd_next, T)
+        dw_next = _empty((H,), dtype=_F32, device=dev)
+    if dout is not None:
+        dop, lddo = _rows(dout, T, H)
+    st = out.dtype if dout is None else dout.dtype
+    yp, ldy = _rows(y, T, H)
+    mode, gp, ldg = _gate(gate, T, H, bt)
+    dr = _empty((T, H), dtype=st, device=dev)
+    dy = _empty((T, H), dtype=bt, device=dev)
+    if w is not None:
+        dw = _empty((H,), dtype=_F32, device=dev)
+    if gate is not None:
+        dgate = _empty(gate.shape, dtype=gate.dtype, device=dev)
     if T == 0:  # no rows (and no pointers to tell what was given): the sums are zero
         return dr, dy, *(t if t is None else t.zero_() for t in (dw, dgate, dw_next))
-    ws = _ws_for(int(lib().qmoe_norm_bwd_workspace_bytes(T, H)), ws, y)
-    yp, ldy = _rows(y)
-    dop, lddo = (None, 0) if dout is None else _rows(dout, (T, H))
-    dnp, lddn = (None, 0) if dn is None else _rows(dn, (T, H))
-    op, ldo = (None, 0) if dn is None else _rows(out, (T, H))
-    _check(lib().qmoe_norm_post_backward(
-        T, H, _dtype(stream_t), _dtype(y), dop, lddo, yp, ldy, _vec(w, H), _vec(rstd, T) if w is not None else None, mode,
-        gp, ldg, alpha, dnp, lddn, op, ldo, _vec(w_next, H) if dn is not None else None,
-        _vec(rstd_next, T) if dn is not None else None, dr.data_ptr(), H, dy.data_ptr(), H,
-        None if dw is None else dw.data_ptr(), None if dgate is None else dgate.data_ptr(), H,
-        None if dw_next is None else dw_next.data_ptr(), *_ws(ws), _stream()), "qmoe_norm_post_backward")
+    L = lib()
+    wp, wn, ws = _ws_for(L.qmoe_norm_bwd_workspace_bytes(T, H), ws, dev)
+    rc = L.qmoe_norm_post_backward(T, H, _dtype(st), _dtype(bt), dop, lddo, yp, ldy, _vec(w, H),
+                                   None if w is None else _vec(rstd, T), mode, gp, ldg, alpha, dnp, lddn, op, ldo, wnp, rnp,
+                                   dr.data_ptr(), H, dy.data_ptr(), H, _at(dw), _at(dgate), H, _at(dw_next), wp, wn, _here(y))
+    if rc:
+        _check(rc, "qmoe_norm_post_backward")
     return dr, dy, dw, dgate, dw_next
 
 
-@dataclasses.dataclass
 class Routing:
     """What route_topk returns, and what its gradient takes: ids int32 [T, k], w fp32 [T, k], lse fp32 [T]; with coef also
-    counts int32 [E + 1] (the last is the number of routed tokens), probs fp32 [E], loss fp32 [1]."""
-    ids: torch.Tensor
-    w: torch.Tensor
-    lse: torch.Tensor
-    counts: torch.Tensor | None
-    probs: torch.Tensor | None
-    loss: torch.Tensor | None
-    renorm: bool
-    scale: float
-    coef: float | None
+    counts int32 [E + 1] (the last is the number of routed tokens), probs fp32 [E], loss fp32 [1] (else None); and the
+    call's renorm, scale and coef."""
+    __slots__ = ("ids", "w", "lse", "counts", "probs", "loss", "renorm", "scale", "coef")
+
+    def __init__(self, ids, w, lse, counts, probs, loss, renorm, scale, coef):
+        self.ids, self.w, self.lse, self.counts, self.probs, self.loss = ids, w, lse, counts, probs, loss
+        self.renorm, self.scale, self.coef = renorm, scale, coef
 
 
 @_on_stream
@@ -654,25 +694,28 @@ def route_topk(logits, k, bias=None, mask=None, renorm=True, scale=1.0, coef=Non
     loss and the per-expert counts.  mask (bool or uint8 [T]): rows where it is 0 are routed nowhere (ids -1)."""
     T, E = logits.shape
     dev = logits.device
-    lp, ld = _rows(logits)
+    lp, ld = _rows(logits, T, E)
     if mask is not None and mask.dtype == torch.bool:
-        mask = mask.view(torch.uint8)
-    ids = torch.empty((T, k), dtype=torch.int32, device=dev)
-    w = torch.empty((T, k), dtype=torch.float32, device=dev)
-    lse = torch.empty(T, dtype=torch.float32, device=dev)
-    counts = probs = loss = None
-    wp, wn = None, 0
-    if coef is not None:
-        counts = torch.empty(E + 1, dtype=torch.int32, device=dev)
-        probs = torch.empty(E, dtype=torch.float32, device=dev)
-        loss = torch.empty(1, dtype=torch.float32, device=dev)
-        ws = _ws_for(int(lib().qmoe_route_workspace_bytes(T, E)), ws, logits)
-        wp, wn = _ws(ws)
-    _check(lib().qmoe_route_topk(T, E, k, _dtype(logits), lp, ld, _vec(bias, E), _vec(mask, T, torch.uint8), int(renorm),
-                                 scale, ids.data_ptr(), w.data_ptr(), lse.data_ptr(), 0.0 if coef is None else coef,
-                                 None if counts is None else counts.data_ptr(), None if probs is None else probs.data_ptr(),
-                                 None if loss is None else loss.data_ptr(), wp, wn, _stream()), "qmoe_route_topk")
-    return Routing(ids, w, lse, counts, probs, loss, bool(renorm), scale, coef)
+        mask = mask.view(_U8)
+    ids = _empty((T, k), dtype=_I32, device=dev)
+    w = _empty((T, k), dtype=_F32, device=dev)
+    lse = _empty((T,), dtype=_F32, device=dev)
+    L = lib()
+    if coef is None:
+        counts = probs = loss = None
+        rc = L.qmoe_route_topk(T, E, k, _dtype(logits.dtype), lp, ld, _vec(bias, E), _vec(mask, T, _U8), renorm, scale,
+                               ids.data_ptr(), w.data_ptr(), lse.data_ptr(), 0.0, None, None, None, None, 0, _here(logits))
+    else:
+        counts = _empty((E + 1,), dtype=_I32, device=dev)
+        probs = _empty((E,), dtype=_F32, device=dev)
+        loss = _empty((1,), dtype=_F32, device=dev)
+        wp, wn, ws = _ws_for(L.qmoe_route_workspace_bytes(T, E), ws, dev)
+        rc = L.qmoe_route_topk(T, E, k, _dtype(logits.dtype), lp, ld, _vec(bias, E), _vec(mask, T, _U8), renorm, scale,
+                               ids.data_ptr(), w.data_ptr(), lse.data_ptr(), coef, counts.data_ptr(), probs.data_ptr(),
+                               loss.data_ptr(), wp, wn, _here(logits))
+    if rc:
+        _check(rc, "qmoe_route_topk")
+    return Routing(ids, w, lse, counts, probs, loss, renorm, scale, coef)
 
 
 @_on_stream
@@ -680,38 +723,46 @@ def route_topk_backward(logits, routing: Routing, dw=None, dloss=None):
     """dlogits (the logits' type) from dw fp32 [T, k] and / or dloss fp32 [1]."""
     T, E = logits.shape
     k = routing.ids.shape[1]
-    lp, ld = _rows(logits)
-    _need(dw is not None or dloss is not None, "route_topk_backward needs dw or dloss")
-    _need(dloss is None or routing.coef is not None, "dloss needs a routing made with coef")
-    dlogits = torch.empty((T, E), dtype=logits.dtype, device=logits.device)
+    if dw is None and dloss is None:
+        raise ValueError("route_topk_backward needs dw or dloss")
+    if dloss is not None and routing.coef is None:
+        raise ValueError("dloss needs a routing made with coef")
+    lp, ld = _rows(logits, T, E)
+    dlogits = _empty((T, E), dtype=logits.dtype, device=logits.device)
     if T == 0:
         return dlogits
-    _check(lib().qmoe_route_topk_backward(T, E, k, _dtype(logits), lp, ld, _vec(routing.ids, T * k, torch.int32),
-                                          _vec(routing.w, T * k), _vec(routing.lse, T), int(routing.renorm), routing.scale,
-                                          _vec(dw, T * k), routing.coef or 0.0, _vec(routing.counts, E + 1, torch.int32),
-                                          _vec(dloss, 1), dlogits.data_ptr(), E, _stream()),
-           "qmoe_route_topk_backward")
+    rc = lib().qmoe_route_topk_backward(T, E, k, _dtype(logits.dtype), lp, ld, _vec(routing.ids, T * k, _I32),
+                                        _vec(routing.w, T * k), _vec(routing.lse, T), routing.renorm, routing.scale,
+                                        _vec(dw, T * k), routing.coef or 0.0, _vec(routing.counts, E + 1, _I32),
+                                        _vec(dloss, 1), dlogits.data_ptr(), E, _here(logits))
+    if rc:
+        _check(rc, "qmoe_route_topk_backward")
     return dlogits
+
+
+def _blocks(n):
+    return (n + 127) // 128
+
+
+def _up16(n):
+    return (n + 15) // 16 * 16
 
 
 def _codes(rows, cols, device):
     """Uninitialised E4M3 codes [rows, cols] whose rows start on 16-byte boundaries."""
-    return torch.empty((rows, (cols + 15) // 16 * 16), dtype=torch.uint8, device=device).view(torch.float8_e4m3fn)[:, :cols]
-
-
-def _blocks(n):
-    return (n + FP8_BLOCK - 1) // FP8_BLOCK
+    return _empty((rows, _up16(cols)), dtype=torch.float8_e4m3fn, device=device)[:, :cols]
 
 
 @_on_stream
 def fp8_quant_rows(x):
     """E4M3 codes of x [T, K] (float8_e4m3fn) and their scales [T, ceil(K / 128)], one for each 128 of a row."""
     T, K = x.shape
-    xp, ldx = _rows(x)
+    xp, ldx = _rows(x, T, K)
     q = _codes(T, K, x.device)
-    s = torch.empty((_blocks(K), T), dtype=torch.float32, device=x.device)
-    _check(lib().qmoe_fp8_quant_rows(T, K, _dtype(x), xp, ldx, q.data_ptr(), (K + 15) // 16 * 16, s.data_ptr(),
-                                     _stream()), "qmoe_fp8_quant_rows")
+    s = _empty((_blocks(K), T), dtype=_F32, device=x.device)
+    rc = lib().qmoe_fp8_quant_rows(T, K, _dtype(x.dtype), xp, ldx, q.data_ptr(), _up16(K), s.data_ptr(), _here(x))
+    if rc:
+        _check(rc, "qmoe_fp8_quant_rows")
     return q, s.t()
 
 
@@ -720,16 +771,17 @@ def fp8_quant_cols(x, rows_too=False):
     """E4M3 codes of x [T, K] transposed, [K, T], and their scales [K, ceil(T / 128)], one for each 128 of a column of x;
     with rows_too (qt, st, q, s), what fp8_quant_rows gives from the same read of x."""
     T, K = x.shape
-    xp, ldx = _rows(x)
+    xp, ldx = _rows(x, T, K)
     qt = _codes(K, T, x.device)
-    st = torch.empty((_blocks(T), K), dtype=torch.float32, device=x.device)
+    st = _empty((_blocks(T), K), dtype=_F32, device=x.device)
     q = s = None
     if rows_too:
         q = _codes(T, K, x.device)
-        s = torch.empty((_blocks(K), T), dtype=torch.float32, device=x.device)
-    _check(lib().qmoe_fp8_quant_cols(T, K, _dtype(x), xp, ldx, qt.data_ptr(), (T + 15) // 16 * 16, st.data_ptr(),
-                                     None if q is None else q.data_ptr(), (K + 15) // 16 * 16,
-                                     None if s is None else s.data_ptr(), _stream()), "qmoe_fp8_quant_cols")
+        s = _empty((_blocks(K), T), dtype=_F32, device=x.device)
+    rc = lib().qmoe_fp8_quant_cols(T, K, _dtype(x.dtype), xp, ldx, qt.data_ptr(), _up16(T), st.data_ptr(), _at(q), _up16(K),
+                                   _at(s), _here(x))
+    if rc:
+        _check(rc, "qmoe_fp8_quant_cols")
     return (qt, st.t(), q, s.t()) if rows_too else (qt, st.t())
 
 
@@ -738,27 +790,36 @@ def fp8_quant_blocks(w, transposed=False):
     """E4M3 codes of w [N, K] and their scales [ceil(N / 128), ceil(K / 128)], one for each 128 x 128 block; with
     transposed also the codes as [K, N] (their scales are the transposed scales)."""
     N, K = w.shape
-    wp, ldw = _rows(w)
+    wp, ldw = _rows(w, N, K)
     q = _codes(N, K, w.device)
     qt = _codes(K, N, w.device) if transposed else None
-    s = torch.empty((_blocks(N), _blocks(K)), dtype=torch.float32, device=w.device)
-    _check(lib().qmoe_fp8_quant_blocks(N, K, _dtype(w), wp, ldw, q.data_ptr(), (K + 15) // 16 * 16,
-                                       None if qt is None else qt.data_ptr(), (N + 15) // 16 * 16, s.data_ptr(),
-                                       _stream()), "qmoe_fp8_quant_blocks")
+    s = _empty((_blocks(N), _blocks(K)), dtype=_F32, device=w.device)
+    rc = lib().qmoe_fp8_quant_blocks(N, K, _dtype(w.dtype), wp, ldw, q.data_ptr(), _up16(K), _at(qt), _up16(N), s.data_ptr(),
+                                     _here(w))
+    if rc:
+        _check(rc, "qmoe_fp8_quant_blocks")
     return (q, s, qt) if transposed else (q, s)
 
 
 def _fp8_mat(q, s):
     rows, K = q.shape
-    _need(q.dtype in (torch.float8_e4m3fn, torch.uint8), f"expected float8_e4m3fn or uint8 codes, got {q.dtype}")
-    _need(s.dtype == torch.float32 and s.dim() == 2 and s.shape[1] == _blocks(K) and s.shape[0] in (rows, _blocks(rows)),
-          f"expected fp32 scales [{rows} or {_blocks(rows)}, {_blocks(K)}], got {list(s.shape)} of {s.dtype}")
-    qp, ld = _rows(q)
+    if q.dtype != torch.float8_e4m3fn and q.dtype != _U8:
+        raise ValueError(f"expected float8_e4m3fn or uint8 codes, got {q.dtype}")
+    blocks = (K + 127) // 128
+    tall = 1
+    if s.shape != (rows, blocks):
+        tall = FP8_BLOCK
+        if s.shape != (_blocks(rows), blocks):
+            raise ValueError(f"expected scales [{rows} or {_blocks(rows)}, {blocks}], got {list(s.shape)}")
+    if s.dtype != _F32:
+        raise ValueError(f"expected fp32 scales, got {s.dtype}")
     if not s.is_cuda:
         raise QmoeError("qmoe kernels take device tensors")
+    qp, ld = _rows(q, rows, K)
     if rows == 1:
-        ld = (ld + 15) // 16 * 16  # the stride of a single row is not used
-    return Fp8Mat(qp, ld, s.data_ptr(), s.stride(0), s.stride(1), 1 if s.shape[0] == rows else FP8_BLOCK, 0)
+        ld = _up16(ld)  # the stride of a single row is not used
+    s_row, s_blk = s.stride()
+    return Fp8Mat(qp, ld, s.data_ptr(), s_row, s_blk, tall, 0)
 
 
 _status_words = {}
@@ -770,9 +831,17 @@ def status_word(device):
     device = torch.device(device)
     index = torch.cuda.current_device() if device.index is None else device.index
     if index not in _status_words:
-        _status_words[index] = torch.zeros(1, dtype=torch.int32, device=f"cuda:{index}")
+        _status_words[index] = torch.zeros(1, dtype=_I32, device=f"cuda:{index}")
         torch.cuda.synchronize(index)  # seen by every stream
     return _status_words[index]
+
+
+def _status(dev_status, t):
+    if dev_status is None:
+        dev_status = _status_words.get(t.get_device())
+        if dev_status is None:
+            dev_status = status_word(t.device)
+    return _vec(dev_status, 1, _I32)
 
 
 @_on_stream
@@ -781,11 +850,14 @@ def fp8_matmul(a_q, a_s, b_q, b_s, out_dtype=torch.bfloat16, dev_status=None):
     any strides."""
     M, K = a_q.shape
     N = b_q.shape[0]
-    _need(b_q.shape[1] == K, f"reduction lengths {K} and {b_q.shape[1]} differ")
-    c = torch.empty((M, N), dtype=out_dtype, device=a_q.device)
-    st = status_word(a_q.device) if dev_status is None else dev_status
-    _check(lib().qmoe_fp8_matmul(M, N, K, ctypes.byref(_fp8_mat(a_q, a_s)), ctypes.byref(_fp8_mat(b_q, b_s)), c.data_ptr(),
-                                 _dtype(out_dtype), N, _vec(st, 1, torch.int32), _stream()), "qmoe_fp8_matmul")
+    if b_q.shape[1] != K:
+        raise ValueError(f"reduction lengths {K} and {b_q.shape[1]} differ")
+    a, b = _fp8_mat(a_q, a_s), _fp8_mat(b_q, b_s)
+    c = _empty((M, N), dtype=out_dtype, device=a_q.device)
+    rc = lib().qmoe_fp8_matmul(M, N, K, ctypes.byref(a), ctypes.byref(b), c.data_ptr(), _dtype(out_dtype), N,
+                               _status(dev_status, a_q), _here(a_q))
+    if rc:
+        _check(rc, "qmoe_fp8_matmul")
     return c
 
 
@@ -794,13 +866,20 @@ def fp8_linear(x, w_q, w_s, out_dtype=None, dev_status=None, ws=None):
     """y = x w^T for x [T, K], quantised on the way (fp8_quant_rows), and a quantised weight w_q [N, K], w_s."""
     T, K = x.shape
     N = w_q.shape[0]
-    _need(w_q.shape[1] == K, f"reduction lengths {K} and {w_q.shape[1]} differ")
-    xp, ldx = _rows(x)
-    y = torch.empty((T, N), dtype=x.dtype if out_dtype is None else out_dtype, device=x.device)
-    st = status_word(x.device) if dev_status is None else dev_status
-    ws = _ws_for(int(lib().qmoe_fp8_linear_workspace_bytes(T, K)), ws, x)
-    _check(lib().qmoe_fp8_linear(T, N, K, _dtype(x), xp, ldx, ctypes.byref(_fp8_mat(w_q, w_s)), y.data_ptr(), _dtype(y), N,
-                                 _vec(st, 1, torch.int32), *_ws(ws), _stream()), "qmoe_fp8_linear")
+    if w_q.shape[1] != K:
+        raise ValueError(f"reduction lengths {K} and {w_q.shape[1]} differ")
+    dev, dtype = x.device, x.dtype
+    if out_dtype is None:
+        out_dtype = dtype
+    xp, ldx = _rows(x, T, K)
+    w = _fp8_mat(w_q, w_s)
+    y = _empty((T, N), dtype=out_dtype, device=dev)
+    L = lib()
+    wp, wn, ws = _ws_for(L.qmoe_fp8_linear_workspace_bytes(T, K), ws, dev)
+    rc = L.qmoe_fp8_linear(T, N, K, _dtype(dtype), xp, ldx, ctypes.byref(w), y.data_ptr(), _dtype(out_dtype), N,
+                           _status(dev_status, x), wp, wn, _here(x))
+    if rc:
+        _check(rc, "qmoe_fp8_linear")
     return y
 
 
@@ -810,11 +889,12 @@ def fp8_linear_backward(dy, x, wt_q, w_s, dev_status=None):
     each product sums; wt_q [K, N] are the weight's transposed codes and w_s its scales (fp8_quant_blocks)."""
     T, N = dy.shape
     K = x.shape[1]
-    _need(x.shape[0] == T and tuple(wt_q.shape) == (K, N), "dy [T, N], x [T, K] and wt_q [K, N] do not go together")
+    if x.shape[0] != T or wt_q.shape != (K, N):
+        raise ValueError("dy [T, N], x [T, K] and wt_q [K, N] do not go together")
     if T == 0:
-        return torch.empty((0, K), dtype=dy.dtype, device=dy.device), torch.zeros((N, K), dtype=torch.float32, device=dy.device)
+        return _empty((0, K), dtype=dy.dtype, device=dy.device), torch.zeros((N, K), dtype=_F32, device=dy.device)
     dyt_q, dyt_s, dy_q, dy_s = fp8_quant_cols(dy, rows_too=True)
     xt_q, xt_s = fp8_quant_cols(x)
     dx = fp8_matmul(dy_q, dy_s, wt_q, w_s.t(), out_dtype=dy.dtype, dev_status=dev_status)
-    dw = fp8_matmul(dyt_q, dyt_s, xt_q, xt_s, out_dtype=torch.float32, dev_status=dev_status)
+    dw = fp8_matmul(dyt_q, dyt_s, xt_q, xt_s, out_dtype=_F32, dev_status=dev_status)
     return dx, dw

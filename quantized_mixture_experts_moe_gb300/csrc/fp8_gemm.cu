@@ -18,37 +18,13 @@
 // Where the tiles are fewer than the SMs, the reduction axis is cut in S parts
 // for a cluster of S CTAs, which add their parts through distributed shared
 // memory in rank order: the same bits every time, one launch, no workspace.
-#include "row_ops.cuh"
-#include "tc_ptx.cuh"
-#include "tma_host.cuh"
+#include "fp8_gemm.cuh"
 
 namespace qmoe {
 namespace fp8 {
 
 int quant_rows_launch(int64_t rows, int64_t cols, int dtype, const void* x, int64_t ldx, uint8_t* q, int64_t ldq,
                       float* s, cudaStream_t st);
-
-constexpr int EPI_WARPS = 8, WARP_TMA = 8, WARP_MMA = 9, WARP_SCALE = 10, SCALE_WARPS = 2, THREADS = 12 * 32;
-constexpr int SC_SLOTS = 8;  // scale ring
-// Registers: launched with 168 a thread (64,512 in all); the two warpgroups of
-// epilogue warps take 208, the third keeps 80 (63,488 in all).
-constexpr int EPI_REGS = 208, OTHER_REGS = 80;
-
-struct Side {
-    const float* s;
-    int64_t s_row, s_blk;
-    int rows, shift;  // shift: log2 of the rows that share a scale (0 or 7)
-};
-
-struct GemmArgs {
-    int M, N, K;  // rows of a, rows of b, reduction
-    Side a, b;
-    void* c;
-    int64_t ldc;
-    int ctype;
-    int32_t* status;
-    int weights_early;  // b does not depend on the kernel before this one
-};
 
 // UNI: the 128 rows of a tile's lane side share their scale, and the scale
 // warps multiply it into the column scales; else each lane has its own.
@@ -70,89 +46,6 @@ struct GemmCfg {
     static_assert(SMEM <= 232448 && STAGES >= 4, "shared memory per CTA");
     static_assert(STAGES * STAGE >= 128 * NT * 4, "the ring holds a tile of sums");
 };
-
-__device__ __forceinline__ void mma_f8(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
-                                       uint32_t accumulate) {
-    asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
-        : "memory");
-}
-// Instruction descriptor: E4M3 operands (format 0), fp32 sums, both K-major.
-__host__ __device__ constexpr uint32_t idesc_f8(int M, int N) {
-    return (1u << 4) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
-}
-
-// Two fp32 values in a 64-bit register pair.
-__device__ __forceinline__ uint64_t pair_of(float a, float b) {
-    uint64_t r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
-    return r;
-}
-__device__ __forceinline__ uint64_t pair_of(uint32_t a, uint32_t b) {
-    uint64_t r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(a), "r"(b));
-    return r;
-}
-__device__ __forceinline__ float2 halves_of(uint64_t p) {
-    float2 v;
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(v.x), "=f"(v.y) : "l"(p));
-    return v;
-}
-__device__ __forceinline__ uint64_t fma_pair(uint64_t a, uint64_t b, uint64_t c) {
-    uint64_t d;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
-    return d;
-}
-__device__ __forceinline__ uint64_t mul_pair(uint64_t a, uint64_t b) {
-    uint64_t d;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-    return d;
-}
-
-template <int N>
-__device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t (&r)[N]) {
-    static_assert(N == 8 || N == 16, "");
-    if constexpr (N == 16) {
-        tc::tmem_ld_32x32b_x16(taddr, r);
-    } else {
-        asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
-                     : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
-                     : "r"(taddr));
-    }
-}
-
-// Every lane waits, so that every lane sees what the barrier guards.
-__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag, int32_t* status) {
-    if (__all_sync(0xFFFFFFFFu, tc::mbar_wait(bar, parity))) return true;
-    if ((threadIdx.x & 31) == 0) {
-        *abort_flag = 1;
-        atomicOr(status, QMOE_DEV_WAIT_TIMEOUT);
-    }
-    return false;
-}
-
-__device__ __forceinline__ uint32_t cluster_rank() {
-    uint32_t r;
-    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-    return r;
-}
-__device__ __forceinline__ uint32_t cluster_size() {
-    uint32_t r;
-    asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
-    return r;
-}
-__device__ __forceinline__ void cluster_sync() {
-    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-__device__ __forceinline__ float peer_load(const float* p, uint32_t rank) {
-    uint32_t at;
-    float v;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(tc::smem_u32(p)), "r"(rank));
-    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(at) : "memory");
-    return v;
-}
 
 __device__ __forceinline__ void put(void* c, int ctype, int64_t at, float v) {
     if (ctype == QMOE_F32) static_cast<float*>(c)[at] = v;
@@ -433,7 +326,7 @@ static int code_map(CUtensorMap* map, const uint8_t* q, int64_t ld, int rows, in
 }
 
 struct Plan {
-    int nt, parts;
+    int nt, parts;  // parts 0: pairs of CTAs
 };
 
 // The narrowest tile that holds all tokens up to 128, else 256 columns; the
@@ -444,6 +337,8 @@ inline Plan plan_of(int M, int N, int K) {
     p.nt = M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : M <= 128 ? 128 : 256;
     const int64_t tiles = (int64_t)((N + 127) / 128) * ((M + p.nt - 1) / p.nt);
     const int blocks = (K + 127) / 128;
+    p.parts = 0;
+    if ((int64_t)((M + 255) / 256) * ((N + 255) / 256) >= row::kSMs / 4) return p;
     p.parts = 1;
     while (p.parts < 8 && tiles * p.parts * 2 <= row::kSMs && blocks >= p.parts * 4) p.parts *= 2;
     return p;
@@ -482,10 +377,11 @@ static int gemm_kind(const CUtensorMap& ma, const CUtensorMap& mb, const GemmArg
 static int gemm_run(const qmoe_fp8_mat* a, const qmoe_fp8_mat* b, GemmArgs& g, cudaStream_t st) {
     const Plan p = plan_of(g.M, g.N, g.K);
     CUtensorMap ma, mb;
-    int rc = code_map(&ma, a->q, a->ld, g.M, g.K, p.nt);
+    int rc = code_map(&ma, a->q, a->ld, g.M, g.K, p.parts ? p.nt : 128);
     if (rc != QMOE_OK) return rc;
     rc = code_map(&mb, b->q, b->ld, g.N, g.K, 128);
     if (rc != QMOE_OK) return rc;
+    if (!p.parts) return gemm_pair(ma, mb, g, st);
     switch (p.nt) {
         case 16: return gemm_kind<16>(ma, mb, g, p.parts, st);
         case 32: return gemm_kind<32>(ma, mb, g, p.parts, st);

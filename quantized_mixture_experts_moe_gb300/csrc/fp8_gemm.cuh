@@ -1,0 +1,121 @@
+// Pieces shared by the FP8 product kernels (fp8_gemm.cu, fp8_gemm_pair.cu):
+// arguments, fp32 pairs, waits, cluster addressing.
+#pragma once
+
+#include "row_ops.cuh"
+#include "tc_ptx.cuh"
+#include "tma_host.cuh"
+
+namespace qmoe {
+namespace fp8 {
+
+constexpr int EPI_WARPS = 8, WARP_TMA = 8, WARP_MMA = 9, WARP_SCALE = 10, SCALE_WARPS = 2, THREADS = 12 * 32;
+constexpr int SC_SLOTS = 8;  // scale ring
+// Registers: launched with 168 a thread (64,512 in all); the two warpgroups of
+// epilogue warps take 208, the third keeps 80 (63,488 in all).
+constexpr int EPI_REGS = 208, OTHER_REGS = 80;
+
+struct Side {
+    const float* s;
+    int64_t s_row, s_blk;
+    int rows, shift;  // shift: log2 of the rows that share a scale (0 or 7)
+};
+
+struct GemmArgs {
+    int M, N, K;  // rows of a, rows of b, reduction
+    Side a, b;
+    void* c;
+    int64_t ldc;
+    int ctype;
+    int32_t* status;
+    int weights_early;  // b does not depend on the kernel before this one
+};
+
+__device__ __forceinline__ void mma_f8(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                       uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+// Instruction descriptor: E4M3 operands (format 0), fp32 sums, both K-major.
+__host__ __device__ constexpr uint32_t idesc_f8(int M, int N) {
+    return (1u << 4) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+}
+
+// Two fp32 values in a 64-bit register pair.
+__device__ __forceinline__ uint64_t pair_of(float a, float b) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t pair_of(uint32_t a, uint32_t b) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(a), "r"(b));
+    return r;
+}
+__device__ __forceinline__ float2 halves_of(uint64_t p) {
+    float2 v;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(v.x), "=f"(v.y) : "l"(p));
+    return v;
+}
+__device__ __forceinline__ uint64_t fma_pair(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+__device__ __forceinline__ uint64_t mul_pair(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+
+template <int N>
+__device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t (&r)[N]) {
+    static_assert(N == 8 || N == 16, "");
+    if constexpr (N == 16) {
+        tc::tmem_ld_32x32b_x16(taddr, r);
+    } else {
+        asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                     : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                     : "r"(taddr));
+    }
+}
+
+// Every lane waits, so that every lane sees what the barrier guards.
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag, int32_t* status) {
+    if (__all_sync(0xFFFFFFFFu, tc::mbar_wait(bar, parity))) return true;
+    if ((threadIdx.x & 31) == 0) {
+        *abort_flag = 1;
+        atomicOr(status, QMOE_DEV_WAIT_TIMEOUT);
+    }
+    return false;
+}
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ uint32_t cluster_size() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ float peer_load(const float* p, uint32_t rank) {
+    uint32_t at;
+    float v;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(tc::smem_u32(p)), "r"(rank));
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(at) : "memory");
+    return v;
+}
+
+// The product of both maps (boxes of 128 rows), by pairs of CTAs.
+int gemm_pair(const CUtensorMap& ma, const CUtensorMap& mb, const GemmArgs& g, cudaStream_t st);
+
+}  // namespace fp8
+}  // namespace qmoe

@@ -484,7 +484,7 @@ def test_fp8_quant_strides_and_specials():
 
 MATMUL_SIZES = [(1, 1, 1), (1, 128, 128), (1, 512, 2048), (2, 200, 300), (15, 129, 100), (16, 384, 1024), (17, 127, 257), (33, 1000, 512),
                 (60, 8, 2040), (64, 640, 640), (65, 130, 129), (128, 256, 1536), (129, 384, 16), (200, 1, 4096), (256, 129, 384),
-                (257, 300, 200), (513, 260, 256), (2000, 2816, 320), (700, 4096, 130)]
+                (257, 300, 200), (513, 260, 256), (2000, 2816, 320), (700, 4096, 130), (2050, 2501, 200), (10001, 300, 1290), (256, 9800, 128)]
 
 
 def _mats(g, M, N, K, b_tall):
