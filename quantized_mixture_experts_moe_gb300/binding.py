@@ -466,215 +466,69 @@ def moe_forward(scheme, x, topk_ids, topk_w, w1, w1_s, w2, w2_s, H=None, I=None,
 # These take tensors of torch's float32, bfloat16 and float16 (int16 tensors
 # are bf16 bits, as above) whose last axis is contiguous; rows may be strided.
 # They allocate their outputs, run on the current stream (or on the one that
-# the keyword `stream` names, on which their outputs then belong) and raise QmoeError for what the library refuses and ValueError for tensors whose
-# shapes or types do not go together.
+# the keyword `stream` names, on which their outputs then belong) and raise
+# QmoeError for what the library refuses and ValueError for tensors whose
+# shapes or types do not go together.  The marshalling itself is compiled
+# (csrc/bind.cpp): for a single token a kernel takes a few microseconds.
 
 GATE_NONE, GATE_ROW, GATE_COL, GATE_FULL = 0, 1, 2, 3
 FP8_BLOCK = 128
 
-_F32, _U8, _I32 = torch.float32, torch.uint8, torch.int32
-_DTYPE = {torch.float32: 0, torch.bfloat16: 1, torch.int16: 1, torch.float16: 2}
-
-# These calls are made for single tokens too, where the kernels take a few
-# microseconds: the checks below cost one comparison each, messages are built
-# only to be raised, and the stream is asked for by device index.
-_empty = torch.empty
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # absent from builds without CUDA
+_bind = None
 
 
-def _dtype(dtype) -> int:
-    try:
-        return _DTYPE[dtype]
-    except KeyError:
-        raise ValueError(f"expected float32, bfloat16 or float16, got {dtype}") from None
+def _load_bind():
+    """The compiled marshalling module (raises when it is missing: there is no other path)."""
+    global _bind
+    if _bind is None:
+        lib()
+        try:
+            from . import _bind as module
+        except ImportError as e:
+            raise QmoeError(f"the marshalling module is not built ({e}); run quantized_mixture_experts_moe_gb300.build.build()") from e
+        module.init(QmoeError)
+        _bind = module
+    return _bind
 
 
-def _here(t):
-    """The current stream of the device of tensor t."""
-    i = t.get_device()
-    if i < 0:
-        raise QmoeError("qmoe kernels take device tensors")
-    return _raw_stream(i)
-
-
-def _rows(t, T, H):
-    """(pointer, row stride) of a [T, H] device tensor with contiguous rows."""
-    if t.shape != (T, H):
-        raise ValueError(f"expected a tensor of shape {[T, H]}, got {list(t.shape)}")
-    if not t.is_cuda:
-        raise QmoeError("qmoe kernels take device tensors")
-    ld, step = t.stride()
-    if step != 1 and H > 1:
-        raise QmoeError("qmoe kernels take rows of contiguous columns")
-    if ld < H:
-        if T > 1:
-            raise QmoeError("qmoe kernels take rows that do not overlap")
-        ld = H
-    return t.data_ptr(), ld
-
-
-def _vec(t, n, dtype=_F32):
-    """Pointer of a contiguous device tensor of n values (None: NULL)."""
-    if t is None:
-        return None
-    if t.dtype != dtype or t.numel() != n:
-        raise ValueError(f"expected {n} values of {dtype}, got {list(t.shape)} of {t.dtype}")
-    if not t.is_cuda:
-        raise QmoeError("qmoe kernels take device tensors")
-    if not t.is_contiguous():
-        raise QmoeError("qmoe kernels take contiguous tensors")
-    return t.data_ptr()
-
-
-def _at(t):
-    return None if t is None else t.data_ptr()
-
-
-def _on_stream(fn):
-    """Runs a call that was given a stream as the current stream's, so that what it allocates (outputs, workspaces, codes)
-    belongs to the stream that uses it."""
-    @functools.wraps(fn)
-    def call(*args, stream=None, **kw):
-        if stream is None:
-            return fn(*args, **kw)
-        with torch.cuda.stream(stream):
-            return fn(*args, **kw)
-    return call
-
-
-def _ws_for(nbytes, ws, device):
-    """(pointer, bytes, tensor) of a workspace: the caller's, or a new one."""
-    if ws is None:
-        ws = _empty(max(nbytes, 256), dtype=_U8, device=device)
-        return ws.data_ptr(), max(nbytes, 256), ws
-    return _ptr(ws), ws.numel() * ws.element_size(), ws
-
-
-@_on_stream
-def norm_pre(x, w, eps=1e-6, out_dtype=None):
+def norm_pre(x, w, eps=1e-6, out_dtype=None, stream=None):
     """n = x / rms(x) * w for rows x [T, H], w fp32 [H]; returns (n, rstd fp32 [T]).  n has x's type, or a 16-bit
     out_dtype beside fp32 x."""
-    T, H = x.shape
-    dev, dtype = x.device, x.dtype
-    if out_dtype is None:
-        out_dtype = dtype
-    xp, ldx = _rows(x, T, H)
-    n = _empty((T, H), dtype=out_dtype, device=dev)
-    rstd = _empty((T,), dtype=_F32, device=dev)
-    rc = lib().qmoe_norm_pre(T, H, _dtype(dtype), _dtype(out_dtype), xp, ldx, _vec(w, H), eps, n.data_ptr(), H,
-                             rstd.data_ptr(), _here(x))
-    if rc:
-        _check(rc, "qmoe_norm_pre")
-    return n, rstd
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return norm_pre(x, w, eps, out_dtype)
+    return (_bind or _load_bind()).norm_pre(x, w, eps, out_dtype)
 
 
-@_on_stream
-def norm_pre_backward(dn, x, rstd, w, dres=None, ws=None):
+def norm_pre_backward(dn, x, rstd, w, dres=None, ws=None, stream=None):
     """Gradients of norm_pre: (dx [T, H] in x's type, dw fp32 [H]); dres (x's type) is added to dx."""
-    T, H = x.shape
-    dev, dtype = x.device, x.dtype
-    xp, ldx = _rows(x, T, H)
-    dnp, lddn = _rows(dn, T, H)
-    drp, lddr = None, 0
-    if dres is not None:
-        if dres.dtype != dtype:
-            raise ValueError("dres has x's type")
-        drp, lddr = _rows(dres, T, H)
-    dx = _empty((T, H), dtype=dtype, device=dev)
-    dw = _empty((H,), dtype=_F32, device=dev)
-    L = lib()
-    wp, wn, ws = _ws_for(L.qmoe_norm_bwd_workspace_bytes(T, H), ws, dev)
-    rc = L.qmoe_norm_pre_backward(T, H, _dtype(dtype), _dtype(dn.dtype), dnp, lddn, xp, ldx, _vec(rstd, T), _vec(w, H), drp,
-                                  lddr, dx.data_ptr(), H, dw.data_ptr(), wp, wn, _here(x))
-    if rc:
-        _check(rc, "qmoe_norm_pre_backward")
-    return dx, dw
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return norm_pre_backward(dn, x, rstd, w, dres, ws)
+    return (_bind or _load_bind()).norm_pre_backward(dn, x, rstd, w, dres, ws)
 
 
-def _gate(gate, T, H, block_dtype):
-    """(mode, pointer, row stride) of a gate: None; one fp32 value for each row, [T, 1] or [T]; one fp32 value for each
-    column, [1, H] or [H]; or [T, H] of the block's type.  A 1-D gate of T == H values is one for each row: give a column
-    gate as [1, H] where the number of rows may be anything."""
-    if gate is None:
-        return GATE_NONE, None, 0
-    shape = tuple(gate.shape)
-    if shape == (T,) or shape == (T, 1) and gate.dtype == _F32:
-        return GATE_ROW, _vec(gate, T), 0
-    if shape == (T, H) and gate.dtype == block_dtype:
-        return (GATE_FULL, *_rows(gate, T, H))
-    if shape == (H,) or shape == (1, H):
-        return GATE_COL, _vec(gate, H), 0
-    raise ValueError(f"a gate is fp32 [T, 1], [T], [1, H] or [H], or [T, H] of the block's type; got {list(shape)} of {gate.dtype}")
-
-
-@_on_stream
-def norm_post(r, y, w=None, gate=None, alpha=1.0, w_next=None, eps=1e-6):
+def norm_post(r, y, w=None, gate=None, alpha=1.0, w_next=None, eps=1e-6, stream=None):
     """out = r + alpha * gate * (y / rms(y) * w) for rows r, y [T, H] (w None: y itself), and n = out / rms(out) * w_next
     where w_next is given.  Returns (out, n, rstd, rstd_next), None for what is not computed.  out has r's type, n y's.
-    gate: None, fp32 [T, 1] or [T] (one for each row), fp32 [1, H] or [H] (one for each column; [H] is taken as [T]
-    where T == H), or [T, H] of y's type."""
-    T, H = y.shape
-    dev, st, bt = y.device, r.dtype, y.dtype
-    rp, ldr = _rows(r, T, H)
-    yp, ldy = _rows(y, T, H)
-    mode, gp, ldg = _gate(gate, T, H, bt)
-    out = _empty((T, H), dtype=st, device=dev)
-    n = rstd = rstd_next = None
-    if w is not None:
-        rstd = _empty((T,), dtype=_F32, device=dev)
-    if w_next is not None:
-        n = _empty((T, H), dtype=bt, device=dev)
-        rstd_next = _empty((T,), dtype=_F32, device=dev)
-    rc = lib().qmoe_norm_post(T, H, _dtype(st), _dtype(bt), rp, ldr, yp, ldy, _vec(w, H), mode, gp, ldg, alpha,
-                              _vec(w_next, H), eps, out.data_ptr(), H, _at(n), H, _at(rstd), _at(rstd_next), _here(y))
-    if rc:
-        _check(rc, "qmoe_norm_post")
-    return out, n, rstd, rstd_next
+
+    gate: None; fp32 [T, 1] or [T], one value for each row; fp32 [1, H] or [H], one for each column; or [T, H] of y's
+    type.  A 1-D gate of T == H values is one for each row: give a column gate as [1, H] where the number of rows may be
+    anything."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return norm_post(r, y, w, gate, alpha, w_next, eps)
+    return (_bind or _load_bind()).norm_post(r, y, w, gate, alpha, w_next, eps)
 
 
-@_on_stream
 def norm_post_backward(dout, y, w=None, rstd=None, gate=None, alpha=1.0, dn=None, out=None, w_next=None, rstd_next=None,
-                       ws=None):
+                       ws=None, stream=None):
     """Gradients of norm_post from dout (the stream's; None: 0) and dn (of n; None: 0): (dr, dy, dw, dgate, dw_next), None
     for what has no input.  y, w, gate, alpha, w_next as in the forward call, out, rstd, rstd_next as it returned them."""
-    T, H = y.shape
-    dev, bt = y.device, y.dtype
-    if dout is None and dn is None:
-        raise ValueError("norm_post_backward needs dout or dn")
-    if w is not None and rstd is None:
-        raise ValueError("w needs rstd")
-    dop, lddo, dnp, lddn, op, ldo, wnp, rnp = None, 0, None, 0, None, 0, None, None
-    dw = dw_next = dgate = None
-    if dn is not None:
-        if out is None or w_next is None or rstd_next is None:
-            raise ValueError("dn needs out, w_next and rstd_next")
-        if dn.dtype != bt or dout is not None and out.dtype != dout.dtype:
-            raise ValueError("dn has y's type, and out dout's")
-        dnp, lddn = _rows(dn, T, H)
-        op, ldo = _rows(out, T, H)
-        wnp, rnp = _vec(w_next, H), _vec(rstd_next, T)
-        dw_next = _empty((H,), dtype=_F32, device=dev)
-    if dout is not None:
-        dop, lddo = _rows(dout, T, H)
-    st = out.dtype if dout is None else dout.dtype
-    yp, ldy = _rows(y, T, H)
-    mode, gp, ldg = _gate(gate, T, H, bt)
-    dr = _empty((T, H), dtype=st, device=dev)
-    dy = _empty((T, H), dtype=bt, device=dev)
-    if w is not None:
-        dw = _empty((H,), dtype=_F32, device=dev)
-    if gate is not None:
-        dgate = _empty(gate.shape, dtype=gate.dtype, device=dev)
-    if T == 0:  # no rows (and no pointers to tell what was given): the sums are zero
-        return dr, dy, *(t if t is None else t.zero_() for t in (dw, dgate, dw_next))
-    L = lib()
-    wp, wn, ws = _ws_for(L.qmoe_norm_bwd_workspace_bytes(T, H), ws, dev)
-    rc = L.qmoe_norm_post_backward(T, H, _dtype(st), _dtype(bt), dop, lddo, yp, ldy, _vec(w, H),
-                                   None if w is None else _vec(rstd, T), mode, gp, ldg, alpha, dnp, lddn, op, ldo, wnp, rnp,
-                                   dr.data_ptr(), H, dy.data_ptr(), H, _at(dw), _at(dgate), H, _at(dw_next), wp, wn, _here(y))
-    if rc:
-        _check(rc, "qmoe_norm_post_backward")
-    return dr, dy, dw, dgate, dw_next
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return norm_post_backward(dout, y, w, rstd, gate, alpha, dn, out, w_next, rstd_next, ws)
+    return (_bind or _load_bind()).norm_post_backward(dout, y, w, rstd, gate, alpha, dn, out, w_next, rstd_next, ws)
 
 
 class Routing:
@@ -683,143 +537,52 @@ class Routing:
     call's renorm, scale and coef."""
     __slots__ = ("ids", "w", "lse", "counts", "probs", "loss", "renorm", "scale", "coef")
 
-    def __init__(self, ids, w, lse, counts, probs, loss, renorm, scale, coef):
-        self.ids, self.w, self.lse, self.counts, self.probs, self.loss = ids, w, lse, counts, probs, loss
-        self.renorm, self.scale, self.coef = renorm, scale, coef
 
-
-@_on_stream
-def route_topk(logits, k, bias=None, mask=None, renorm=True, scale=1.0, coef=None, ws=None) -> Routing:
+def route_topk(logits, k, bias=None, mask=None, renorm=True, scale=1.0, coef=None, ws=None, stream=None) -> Routing:
     """The k experts of largest logit + bias of each row of logits [T, E] and their weights; with coef also the balance
     loss and the per-expert counts.  mask (bool or uint8 [T]): rows where it is 0 are routed nowhere (ids -1)."""
-    T, E = logits.shape
-    dev = logits.device
-    lp, ld = _rows(logits, T, E)
-    if mask is not None and mask.dtype == torch.bool:
-        mask = mask.view(_U8)
-    ids = _empty((T, k), dtype=_I32, device=dev)
-    w = _empty((T, k), dtype=_F32, device=dev)
-    lse = _empty((T,), dtype=_F32, device=dev)
-    L = lib()
-    if coef is None:
-        counts = probs = loss = None
-        rc = L.qmoe_route_topk(T, E, k, _dtype(logits.dtype), lp, ld, _vec(bias, E), _vec(mask, T, _U8), renorm, scale,
-                               ids.data_ptr(), w.data_ptr(), lse.data_ptr(), 0.0, None, None, None, None, 0, _here(logits))
-    else:
-        counts = _empty((E + 1,), dtype=_I32, device=dev)
-        probs = _empty((E,), dtype=_F32, device=dev)
-        loss = _empty((1,), dtype=_F32, device=dev)
-        wp, wn, ws = _ws_for(L.qmoe_route_workspace_bytes(T, E), ws, dev)
-        rc = L.qmoe_route_topk(T, E, k, _dtype(logits.dtype), lp, ld, _vec(bias, E), _vec(mask, T, _U8), renorm, scale,
-                               ids.data_ptr(), w.data_ptr(), lse.data_ptr(), coef, counts.data_ptr(), probs.data_ptr(),
-                               loss.data_ptr(), wp, wn, _here(logits))
-    if rc:
-        _check(rc, "qmoe_route_topk")
-    return Routing(ids, w, lse, counts, probs, loss, renorm, scale, coef)
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return route_topk(logits, k, bias, mask, renorm, scale, coef, ws)
+    r = Routing()
+    r.ids, r.w, r.lse, r.counts, r.probs, r.loss = (_bind or _load_bind()).route_topk(logits, k, bias, mask, renorm, scale, coef, ws)
+    r.renorm, r.scale, r.coef = renorm, scale, coef
+    return r
 
 
-@_on_stream
-def route_topk_backward(logits, routing: Routing, dw=None, dloss=None):
+def route_topk_backward(logits, routing: Routing, dw=None, dloss=None, stream=None):
     """dlogits (the logits' type) from dw fp32 [T, k] and / or dloss fp32 [1]."""
-    T, E = logits.shape
-    k = routing.ids.shape[1]
-    if dw is None and dloss is None:
-        raise ValueError("route_topk_backward needs dw or dloss")
-    if dloss is not None and routing.coef is None:
-        raise ValueError("dloss needs a routing made with coef")
-    lp, ld = _rows(logits, T, E)
-    dlogits = _empty((T, E), dtype=logits.dtype, device=logits.device)
-    if T == 0:
-        return dlogits
-    rc = lib().qmoe_route_topk_backward(T, E, k, _dtype(logits.dtype), lp, ld, _vec(routing.ids, T * k, _I32),
-                                        _vec(routing.w, T * k), _vec(routing.lse, T), routing.renorm, routing.scale,
-                                        _vec(dw, T * k), routing.coef or 0.0, _vec(routing.counts, E + 1, _I32),
-                                        _vec(dloss, 1), dlogits.data_ptr(), E, _here(logits))
-    if rc:
-        _check(rc, "qmoe_route_topk_backward")
-    return dlogits
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return route_topk_backward(logits, routing, dw, dloss)
+    r = routing
+    return (_bind or _load_bind()).route_topk_backward(logits, r.ids, r.w, r.lse, r.counts, r.renorm, r.scale, r.coef, dw, dloss)
 
 
-def _blocks(n):
-    return (n + 127) // 128
-
-
-def _up16(n):
-    return (n + 15) // 16 * 16
-
-
-def _codes(rows, cols, device):
-    """Uninitialised E4M3 codes [rows, cols] whose rows start on 16-byte boundaries."""
-    return _empty((rows, _up16(cols)), dtype=torch.float8_e4m3fn, device=device)[:, :cols]
-
-
-@_on_stream
-def fp8_quant_rows(x):
+def fp8_quant_rows(x, stream=None):
     """E4M3 codes of x [T, K] (float8_e4m3fn) and their scales [T, ceil(K / 128)], one for each 128 of a row."""
-    T, K = x.shape
-    xp, ldx = _rows(x, T, K)
-    q = _codes(T, K, x.device)
-    s = _empty((_blocks(K), T), dtype=_F32, device=x.device)
-    rc = lib().qmoe_fp8_quant_rows(T, K, _dtype(x.dtype), xp, ldx, q.data_ptr(), _up16(K), s.data_ptr(), _here(x))
-    if rc:
-        _check(rc, "qmoe_fp8_quant_rows")
-    return q, s.t()
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return fp8_quant_rows(x)
+    return (_bind or _load_bind()).fp8_quant_rows(x)
 
 
-@_on_stream
-def fp8_quant_cols(x, rows_too=False):
+def fp8_quant_cols(x, rows_too=False, stream=None):
     """E4M3 codes of x [T, K] transposed, [K, T], and their scales [K, ceil(T / 128)], one for each 128 of a column of x;
     with rows_too (qt, st, q, s), what fp8_quant_rows gives from the same read of x."""
-    T, K = x.shape
-    xp, ldx = _rows(x, T, K)
-    qt = _codes(K, T, x.device)
-    st = _empty((_blocks(T), K), dtype=_F32, device=x.device)
-    q = s = None
-    if rows_too:
-        q = _codes(T, K, x.device)
-        s = _empty((_blocks(K), T), dtype=_F32, device=x.device)
-    rc = lib().qmoe_fp8_quant_cols(T, K, _dtype(x.dtype), xp, ldx, qt.data_ptr(), _up16(T), st.data_ptr(), _at(q), _up16(K),
-                                   _at(s), _here(x))
-    if rc:
-        _check(rc, "qmoe_fp8_quant_cols")
-    return (qt, st.t(), q, s.t()) if rows_too else (qt, st.t())
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return fp8_quant_cols(x, rows_too)
+    return (_bind or _load_bind()).fp8_quant_cols(x, rows_too)
 
 
-@_on_stream
-def fp8_quant_blocks(w, transposed=False):
+def fp8_quant_blocks(w, transposed=False, stream=None):
     """E4M3 codes of w [N, K] and their scales [ceil(N / 128), ceil(K / 128)], one for each 128 x 128 block; with
     transposed also the codes as [K, N] (their scales are the transposed scales)."""
-    N, K = w.shape
-    wp, ldw = _rows(w, N, K)
-    q = _codes(N, K, w.device)
-    qt = _codes(K, N, w.device) if transposed else None
-    s = _empty((_blocks(N), _blocks(K)), dtype=_F32, device=w.device)
-    rc = lib().qmoe_fp8_quant_blocks(N, K, _dtype(w.dtype), wp, ldw, q.data_ptr(), _up16(K), _at(qt), _up16(N), s.data_ptr(),
-                                     _here(w))
-    if rc:
-        _check(rc, "qmoe_fp8_quant_blocks")
-    return (q, s, qt) if transposed else (q, s)
-
-
-def _fp8_mat(q, s):
-    rows, K = q.shape
-    if q.dtype != torch.float8_e4m3fn and q.dtype != _U8:
-        raise ValueError(f"expected float8_e4m3fn or uint8 codes, got {q.dtype}")
-    blocks = (K + 127) // 128
-    tall = 1
-    if s.shape != (rows, blocks):
-        tall = FP8_BLOCK
-        if s.shape != (_blocks(rows), blocks):
-            raise ValueError(f"expected scales [{rows} or {_blocks(rows)}, {blocks}], got {list(s.shape)}")
-    if s.dtype != _F32:
-        raise ValueError(f"expected fp32 scales, got {s.dtype}")
-    if not s.is_cuda:
-        raise QmoeError("qmoe kernels take device tensors")
-    qp, ld = _rows(q, rows, K)
-    if rows == 1:
-        ld = _up16(ld)  # the stride of a single row is not used
-    s_row, s_blk = s.stride()
-    return Fp8Mat(qp, ld, s.data_ptr(), s_row, s_blk, tall, 0)
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return fp8_quant_blocks(w, transposed)
+    return (_bind or _load_bind()).fp8_quant_blocks(w, transposed)
 
 
 _status_words = {}
@@ -831,70 +594,50 @@ def status_word(device):
     device = torch.device(device)
     index = torch.cuda.current_device() if device.index is None else device.index
     if index not in _status_words:
-        _status_words[index] = torch.zeros(1, dtype=_I32, device=f"cuda:{index}")
+        _status_words[index] = torch.zeros(1, dtype=torch.int32, device=f"cuda:{index}")
         torch.cuda.synchronize(index)  # seen by every stream
     return _status_words[index]
 
 
-def _status(dev_status, t):
-    if dev_status is None:
-        dev_status = _status_words.get(t.get_device())
-        if dev_status is None:
-            dev_status = status_word(t.device)
-    return _vec(dev_status, 1, _I32)
+def _status(t):
+    i = t.get_device()
+    if i < 0:
+        raise QmoeError("qmoe kernels take device tensors")
+    return _status_words.get(i) if i in _status_words else status_word(t.device)
 
 
-@_on_stream
-def fp8_matmul(a_q, a_s, b_q, b_s, out_dtype=torch.bfloat16, dev_status=None):
+def fp8_matmul(a_q, a_s, b_q, b_s, out_dtype=torch.bfloat16, dev_status=None, stream=None):
     """c [M, N] = a b^T of E4M3 codes a_q [M, K], b_q [N, K] with fp32 scales [rows or ceil(rows / 128), ceil(K / 128)] of
     any strides."""
-    M, K = a_q.shape
-    N = b_q.shape[0]
-    if b_q.shape[1] != K:
-        raise ValueError(f"reduction lengths {K} and {b_q.shape[1]} differ")
-    a, b = _fp8_mat(a_q, a_s), _fp8_mat(b_q, b_s)
-    c = _empty((M, N), dtype=out_dtype, device=a_q.device)
-    rc = lib().qmoe_fp8_matmul(M, N, K, ctypes.byref(a), ctypes.byref(b), c.data_ptr(), _dtype(out_dtype), N,
-                               _status(dev_status, a_q), _here(a_q))
-    if rc:
-        _check(rc, "qmoe_fp8_matmul")
-    return c
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return fp8_matmul(a_q, a_s, b_q, b_s, out_dtype, dev_status)
+    return (_bind or _load_bind()).fp8_matmul(a_q, a_s, b_q, b_s, out_dtype, _status(a_q) if dev_status is None else dev_status)
 
 
-@_on_stream
-def fp8_linear(x, w_q, w_s, out_dtype=None, dev_status=None, ws=None):
+def fp8_linear(x, w_q, w_s, out_dtype=None, dev_status=None, ws=None, stream=None):
     """y = x w^T for x [T, K], quantised on the way (fp8_quant_rows), and a quantised weight w_q [N, K], w_s."""
-    T, K = x.shape
-    N = w_q.shape[0]
-    if w_q.shape[1] != K:
-        raise ValueError(f"reduction lengths {K} and {w_q.shape[1]} differ")
-    dev, dtype = x.device, x.dtype
-    if out_dtype is None:
-        out_dtype = dtype
-    xp, ldx = _rows(x, T, K)
-    w = _fp8_mat(w_q, w_s)
-    y = _empty((T, N), dtype=out_dtype, device=dev)
-    L = lib()
-    wp, wn, ws = _ws_for(L.qmoe_fp8_linear_workspace_bytes(T, K), ws, dev)
-    rc = L.qmoe_fp8_linear(T, N, K, _dtype(dtype), xp, ldx, ctypes.byref(w), y.data_ptr(), _dtype(out_dtype), N,
-                           _status(dev_status, x), wp, wn, _here(x))
-    if rc:
-        _check(rc, "qmoe_fp8_linear")
-    return y
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return fp8_linear(x, w_q, w_s, out_dtype, dev_status, ws)
+    return (_bind or _load_bind()).fp8_linear(x, w_q, w_s, out_dtype, _status(x) if dev_status is None else dev_status, ws)
 
 
-@_on_stream
-def fp8_linear_backward(dy, x, wt_q, w_s, dev_status=None):
+def fp8_linear_backward(dy, x, wt_q, w_s, dev_status=None, stream=None):
     """Gradients of y = x w^T: (dx = dy w in dy's type, dw = dy^T x in fp32).  dy and x are quantised along the axis that
     each product sums; wt_q [K, N] are the weight's transposed codes and w_s its scales (fp8_quant_blocks)."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return fp8_linear_backward(dy, x, wt_q, w_s, dev_status)
     T, N = dy.shape
     K = x.shape[1]
     if x.shape[0] != T or wt_q.shape != (K, N):
         raise ValueError("dy [T, N], x [T, K] and wt_q [K, N] do not go together")
     if T == 0:
-        return _empty((0, K), dtype=dy.dtype, device=dy.device), torch.zeros((N, K), dtype=_F32, device=dy.device)
-    dyt_q, dyt_s, dy_q, dy_s = fp8_quant_cols(dy, rows_too=True)
+        return (torch.empty((0, K), dtype=dy.dtype, device=dy.device),
+                torch.zeros((N, K), dtype=torch.float32, device=dy.device))
+    dyt_q, dyt_s, dy_q, dy_s = fp8_quant_cols(dy, True)
     xt_q, xt_s = fp8_quant_cols(x)
-    dx = fp8_matmul(dy_q, dy_s, wt_q, w_s.t(), out_dtype=dy.dtype, dev_status=dev_status)
-    dw = fp8_matmul(dyt_q, dyt_s, xt_q, xt_s, out_dtype=_F32, dev_status=dev_status)
+    dx = fp8_matmul(dy_q, dy_s, wt_q, w_s.t(), dy.dtype, dev_status)
+    dw = fp8_matmul(dyt_q, dyt_s, xt_q, xt_s, torch.float32, dev_status)
     return dx, dw

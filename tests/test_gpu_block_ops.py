@@ -494,9 +494,14 @@ def _mats(g, M, N, K, b_tall):
 
 
 def _padded(q):
-    out = qb._codes(*q.shape, "cuda")
+    """The same codes on the GPU with rows on 16-byte boundaries."""
+    out = torch.zeros(q.shape[0], -(-q.shape[1] // 16) * 16, dtype=torch.float8_e4m3fn, device="cuda")[:, :q.shape[1]]
     out.copy_(q.cuda())
     return out
+
+
+def _mat(q, s):
+    return qb.Fp8Mat(q.data_ptr(), q.stride(0), s.data_ptr(), s.stride(0), s.stride(1), 1 if s.shape[0] == q.shape[0] else 128, 0)
 
 
 @pytest.mark.parametrize("b_tall", [1, 128])
@@ -535,7 +540,7 @@ def test_fp8_matmul_strided_output_and_codes():
     ref.close(qb.fp8_matmul(wide[:, 128:384], a_s.cuda(), _padded(b), b_s.cuda(), out_dtype=F32), want, slack, "c")
     c = torch.full((70, 211), 9.0, device="cuda")
     bq, bs, as_ = _padded(b), b_s.cuda(), a_s.cuda()
-    ma, mb = qb._fp8_mat(wide[:, 128:384], as_), qb._fp8_mat(bq, bs)
+    ma, mb = _mat(wide[:, 128:384], as_), _mat(bq, bs)
     st = torch.zeros(1, dtype=torch.int32, device="cuda")
     assert qb.lib().qmoe_fp8_matmul(70, 200, 256, ctypes.byref(ma), ctypes.byref(mb), c.data_ptr(), 0, 211, st.data_ptr(), None) == 0
     torch.cuda.synchronize()
