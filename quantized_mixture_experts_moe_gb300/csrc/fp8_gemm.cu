@@ -119,70 +119,69 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant
 
     if (warp >= EPI_WARPS) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(OTHER_REGS));
-    if (warp == WARP_TMA) {
-        if (lane == 0) {
-            int slot = 0, in_flight = 0;
-            uint32_t phase = 0;
-            for (int u = first; u < tiles && !*abort_flag; u += stride) {
-                const int p0 = (u % p_tiles) * 128, q0 = (u / p_tiles) * NT;
-                for (int kb = kb0; kb < kb1; ++kb) {
-                    if (!tc::mbar_wait(&empty[slot], phase ^ 1)) {
-                        *abort_flag = 1;
-                        atomicOr(g.status, QMOE_DEV_WAIT_TIMEOUT);
-                        break;
+        if (warp < WARP_MMA) {
+            if (lane == 0) {
+                const int turn = warp - WARP_TMA;
+                int it = 0, sent = 0;
+                for (int u = first; u < tiles && !*abort_flag; u += stride) {
+                    const int p0 = (u % p_tiles) * 128, q0 = (u / p_tiles) * NT;
+                    for (int kb = kb0; kb < kb1; ++kb, ++it) {
+                        if ((it & 1) != turn) continue;
+                        const int slot = it % C::STAGES;
+                        if (!tc::mbar_wait(&empty[slot], (it / C::STAGES & 1) ^ 1)) {
+                            *abort_flag = 1;
+                            atomicOr(g.status, QMOE_DEV_WAIT_TIMEOUT);
+                            break;
+                        }
+                        uint8_t* st = smem + slot * C::STAGE;
+                        tc::mbar_arrive_expect_tx(&full[slot], C::STAGE);
+                        tc::tma_load_2d(st, &map_b, &full[slot], kb * 128, p0);
+                        tc::tma_load_2d(st + C::P_BYTES, &map_a, &full[slot], kb * 128, q0);
+                        sent = it + 1;
                     }
-                    uint8_t* st = smem + slot * C::STAGE;
-                    tc::mbar_arrive_expect_tx(&full[slot], C::STAGE);
-                    tc::tma_load_2d(st, &map_b, &full[slot], kb * 128, p0);
-                    tc::tma_load_2d(st + C::P_BYTES, &map_a, &full[slot], kb * 128, q0);
-                    if (in_flight < C::STAGES) ++in_flight;
-                    if (++slot == C::STAGES) { slot = 0; phase ^= 1; }
                 }
+                if (*abort_flag)  // nobody may have waited for these: no load outlives the CTA
+                    for (int i = sent - 1; i >= 0 && i > sent - 1 - C::STAGES; i -= TURNS)
+                        tc::mbar_wait(&full[i % C::STAGES], i / C::STAGES & 1);
             }
-            if (*abort_flag)  // nobody may have waited for these: no load outlives the CTA
-                for (; in_flight > 0; --in_flight) {
-                    if (slot == 0) { slot = C::STAGES; phase ^= 1; }
-                    --slot;
-                    tc::mbar_wait(&full[slot], phase);
-                }
-        }
-        __syncwarp();
-    } else if (warp == WARP_MMA) {
-        constexpr uint32_t idesc = idesc_f8(128, NT);
-        int slot = 0, buf = 0;
-        uint32_t phase = 0, acc_phase = 0;
-        bool issued = false;
-        for (int u = first; u < tiles && !*abort_flag; u += stride) {
-            for (int kb = kb0; kb < kb1; ++kb) {
-                if (!warp_wait(&acc_empty[buf], acc_phase ^ 1, abort_flag, g.status)) break;
-                if (!warp_wait(&full[slot], phase, abort_flag, g.status)) break;
-                tc::tc_fence_after();
-                if (lane == 0) {
-                    const uint32_t st = tc::smem_u32(smem + slot * C::STAGE);
-                    const uint64_t dp = tc::sdesc_kmajor_sw128(st), dq = tc::sdesc_kmajor_sw128(st + C::P_BYTES);
+            __syncwarp();
+        } else if (warp < WARP_SCALE) {
+            if (lane == 0) {
+                constexpr uint32_t idesc = idesc_f8(128, NT);
+                const int turn = warp - WARP_MMA;
+                int it = 0, sent = 0;
+                for (int u = first; u < tiles && !*abort_flag; u += stride) {
+                    for (int kb = kb0; kb < kb1; ++kb, ++it) {
+                        if ((it & 1) != turn) continue;
+                        const int slot = it % C::STAGES, buf = it % C::BUFS;
+                        if (!tc::mbar_wait(&acc_empty[buf], (it / C::BUFS & 1) ^ 1) ||
+                            !tc::mbar_wait(&full[slot], it / C::STAGES & 1)) {
+                            *abort_flag = 1;
+                            atomicOr(g.status, QMOE_DEV_WAIT_TIMEOUT);
+                            break;
+                        }
+                        tc::tc_fence_after();
+                        const uint32_t st = tc::smem_u32(smem + slot * C::STAGE);
+                        const uint64_t dp = tc::sdesc_kmajor_sw128(st), dq = tc::sdesc_kmajor_sw128(st + C::P_BYTES);
 #pragma unroll
-                    for (int k = 0; k < 4; ++k)  // 32 codes a step: 2 descriptor units of 16 bytes
-                        mma_f8(tm + buf * NT, dp + 2 * k, dq + 2 * k, idesc, k > 0);
-                    tc::mma_commit(&empty[slot]);
-                    tc::mma_commit(&acc_full[buf]);
+                        for (int k = 0; k < 4; ++k)  // 32 codes a step: 2 descriptor units of 16 bytes
+                            mma_f8(tm + buf * NT, dp + 2 * k, dq + 2 * k, idesc, k > 0);
+                        tc::mma_commit(&empty[slot]);
+                        tc::mma_commit(&acc_full[buf]);
+                        sent = it + 1;
+                    }
                 }
-                __syncwarp();
-                if (++slot == C::STAGES) { slot = 0; phase ^= 1; }
-                if (++buf == C::BUFS) { buf = 0; acc_phase ^= 1; }
-                issued = true;
+                if (*abort_flag && sent)  // no product outlives the accumulators
+                    tc::mbar_wait(&acc_full[(sent - 1) % C::BUFS], (sent - 1) / C::BUFS & 1);
             }
-        }
-        if (*abort_flag && issued) {  // no product outlives the accumulators
-            if (buf == 0) { buf = C::BUFS; acc_phase ^= 1; }
-            tc::mbar_wait(&acc_full[buf - 1], acc_phase);
-        }
-    } else {
+            __syncwarp();
+        } else if (warp < WARP_SCALE + TURNS) {
         // the scale warps take the blocks in turn; a block's loads go out before the slot is waited for
         int it = 0;
         for (int u = first; u < tiles && !*abort_flag; u += stride) {
             const int p0 = (u % p_tiles) * 128, q0 = (u / p_tiles) * NT;
             for (int kb = kb0; kb < kb1; ++kb, ++it) {
-                if (it % SCALE_WARPS != warp - WARP_SCALE) continue;
+                if ((it & 1) != warp - WARP_SCALE) continue;
                 const int slot = it % SC_SLOTS;
                 constexpr int QN = (NT + 31) / 32;
                 float sq[QN], sp[4];
@@ -212,7 +211,7 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant
                 if (lane == 0) tc::mbar_arrive(&sc_full[slot]);
             }
         }
-    }
+        }
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(EPI_REGS));
         constexpr int STEP = C::COLS < 16 ? C::COLS : 16, STEPS = C::COLS / STEP;
@@ -326,7 +325,7 @@ static int code_map(CUtensorMap* map, const uint8_t* q, int64_t ld, int rows, in
 }
 
 struct Plan {
-    int nt, parts;  // parts 0: pairs of CTAs
+    int nt, parts;  // parts 0: the wide kernel
 };
 
 // The narrowest tile that holds all tokens up to 128, else 256 columns; the
@@ -338,7 +337,7 @@ inline Plan plan_of(int M, int N, int K) {
     const int64_t tiles = (int64_t)((N + 127) / 128) * ((M + p.nt - 1) / p.nt);
     const int blocks = (K + 127) / 128;
     p.parts = 0;
-    if ((int64_t)((M + 255) / 256) * ((N + 255) / 256) >= row::kSMs / 4) return p;
+    if ((int64_t)((M + 127) / 128) * ((N + 255) / 256) >= row::kSMs / 2) return p;
     p.parts = 1;
     while (p.parts < 8 && tiles * p.parts * 2 <= row::kSMs && blocks >= p.parts * 4) p.parts *= 2;
     return p;
@@ -379,9 +378,9 @@ static int gemm_run(const qmoe_fp8_mat* a, const qmoe_fp8_mat* b, GemmArgs& g, c
     CUtensorMap ma, mb;
     int rc = code_map(&ma, a->q, a->ld, g.M, g.K, p.parts ? p.nt : 128);
     if (rc != QMOE_OK) return rc;
-    rc = code_map(&mb, b->q, b->ld, g.N, g.K, 128);
+    rc = code_map(&mb, b->q, b->ld, g.N, g.K, p.parts ? 128 : 256);
     if (rc != QMOE_OK) return rc;
-    if (!p.parts) return gemm_pair(ma, mb, g, st);
+    if (!p.parts) return gemm_wide(ma, mb, g, st);
     switch (p.nt) {
         case 16: return gemm_kind<16>(ma, mb, g, p.parts, st);
         case 32: return gemm_kind<32>(ma, mb, g, p.parts, st);

@@ -1,4 +1,4 @@
-// Pieces shared by the FP8 product kernels (fp8_gemm.cu, fp8_gemm_pair.cu):
+// Pieces shared by the FP8 product kernels (fp8_gemm.cu, fp8_gemm_wide.cu):
 // arguments, fp32 pairs, waits, cluster addressing.
 #pragma once
 
@@ -9,11 +9,17 @@
 namespace qmoe {
 namespace fp8 {
 
-constexpr int EPI_WARPS = 8, WARP_TMA = 8, WARP_MMA = 9, WARP_SCALE = 10, SCALE_WARPS = 2, THREADS = 12 * 32;
+// Warps: 8 scale and sum; then two each that load tiles, issue products and
+// bring scales, and two without work (registers are split by warpgroups).  The
+// two of a kind take the reduction's blocks in turn: a thread needs about 400
+// cycles to wait for a stage and issue its loads, and about 700 to issue a
+// block's products, against 512 cycles that the products of a block take.
+constexpr int EPI_WARPS = 8, WARP_TMA = 8, WARP_MMA = 10, WARP_SCALE = 12, THREADS = 16 * 32;
+constexpr int TURNS = 2;
 constexpr int SC_SLOTS = 8;  // scale ring
-// Registers: launched with 168 a thread (64,512 in all); the two warpgroups of
-// epilogue warps take 208, the third keeps 80 (63,488 in all).
-constexpr int EPI_REGS = 208, OTHER_REGS = 80;
+// Registers: launched with 128 a thread (65,536 in all); the epilogue's two
+// warpgroups take 200, the others keep 56 (65,536 in all).
+constexpr int EPI_REGS = 200, OTHER_REGS = 56;
 
 struct Side {
     const float* s;
@@ -114,8 +120,8 @@ __device__ __forceinline__ float peer_load(const float* p, uint32_t rank) {
     return v;
 }
 
-// The product of both maps (boxes of 128 rows), by pairs of CTAs.
-int gemm_pair(const CUtensorMap& ma, const CUtensorMap& mb, const GemmArgs& g, cudaStream_t st);
+// The product of both maps (boxes of 128 rows of a, 256 of b) in 128 x 256 tiles.
+int gemm_wide(const CUtensorMap& ma, const CUtensorMap& mb, const GemmArgs& g, cudaStream_t st);
 
 }  // namespace fp8
 }  // namespace qmoe
