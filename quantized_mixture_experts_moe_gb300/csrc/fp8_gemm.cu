@@ -227,8 +227,7 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant
 #pragma unroll
             for (int i = 0; i < C::COLS / 2; ++i) acc[i] = 0ull;
             for (int kb = kb0; kb < kb1; ++kb) {
-                ok = warp_wait(&sc_full[slot], phase, abort_flag, g.status) &&
-                     warp_wait(&acc_full[buf], acc_phase, abort_flag, g.status);
+                ok = warp_wait(&sc_full[slot], phase, &acc_full[buf], acc_phase, abort_flag, g.status);
                 if (!ok) break;
                 tc::tc_fence_after();
                 const float* s = sc + slot * C::SC_FLOATS + half * C::COLS;

@@ -89,14 +89,23 @@ __device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t (&r)[N]) {
     }
 }
 
-// Every lane waits, so that every lane sees what the barrier guards.
-__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag, int32_t* status) {
-    if (__all_sync(0xFFFFFFFFu, tc::mbar_wait(bar, parity))) return true;
-    if ((threadIdx.x & 31) == 0) {
+// One lane waits for both barriers (a wait by all 32 lanes takes some 200
+// cycles even where the phase is over, by one lane 50); __syncwarp passes on
+// to the others what the barriers guard.
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, uint64_t* bar2, uint32_t parity2,
+                                          volatile int* abort_flag, int32_t* status) {
+    int ok = 1;
+    if ((threadIdx.x & 31) == 0 && !(tc::mbar_wait(bar, parity) && (!bar2 || tc::mbar_wait(bar2, parity2)))) {
         *abort_flag = 1;
         atomicOr(status, QMOE_DEV_WAIT_TIMEOUT);
+        ok = 0;
     }
-    return false;
+    ok = __shfl_sync(0xFFFFFFFFu, ok, 0);
+    __syncwarp();
+    return ok != 0;
+}
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag, int32_t* status) {
+    return warp_wait(bar, parity, nullptr, 0, abort_flag, status);
 }
 
 __device__ __forceinline__ uint32_t cluster_rank() {

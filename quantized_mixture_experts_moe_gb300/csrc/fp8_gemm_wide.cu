@@ -20,10 +20,10 @@ namespace fp8 {
 
 // Warps: 8 scale and sum, then one that loads, two that issue products (one for
 // each accumulator) and one that brings scales.  Registers: launched with 168 a
-// thread (64,512 in all); the epilogue's warpgroups take 232, the third keeps 40
+// thread (64,512 in all); the epilogue's warpgroups take 216, the third keeps 72
 // (64,512 in all).
 constexpr int WIDE_TMA = 8, WIDE_MMA = 9, WIDE_SCALE = 11, WIDE_THREADS = 12 * 32;
-constexpr int WIDE_EPI_REGS = 232, WIDE_OTHER_REGS = 40;
+constexpr int WIDE_EPI_REGS = 216, WIDE_OTHER_REGS = 72;
 constexpr int WIDE_STAGE = (128 + 256) * 128, WIDE_STAGES = 4;
 constexpr int OUT_PITCH = 80;  // bytes of a row (64 used) in a warp's output stage
 template <bool UNI>
@@ -33,7 +33,7 @@ struct WideCfg {
     static constexpr int SC_OFF = WIDE_STAGES * WIDE_STAGE;
     static constexpr int OUT_OFF = SC_OFF + SC_SLOTS * SC_FLOATS * 4;
     static constexpr int BAR_OFF = OUT_OFF + EPI_WARPS * 32 * OUT_PITCH;
-    static constexpr int MISC_OFF = BAR_OFF + (2 * WIDE_STAGES + 4 + 2 * SC_SLOTS) * 8;
+    static constexpr int MISC_OFF = BAR_OFF + (2 * WIDE_STAGES + 8 + 2 * SC_SLOTS) * 8;
     static constexpr int SMEM = MISC_OFF + 16 + 1024;
     static_assert(SMEM <= 232448, "shared memory per CTA");
 };
@@ -44,7 +44,17 @@ __device__ __forceinline__ void cp_async_4_or_zero(void* dst, const void* src, b
                  : "memory");
 }
 
-__device__ __forceinline__ void tmem_ld64(uint32_t taddr, uint32_t (&r)[64]) {
+__device__ __forceinline__ void tmem_load(uint32_t taddr, uint32_t (&r)[32]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,"
+        "%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+          "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+          "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_load(uint32_t taddr, uint32_t (&r)[64]) {
     asm volatile(
         "tcgen05.ld.sync.aligned.32x32b.x64.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,"
         "%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32,%33,%34,%35,%36,%37,%38,%39,%40,%41,%42,%43,%44,%45,%46,"
@@ -118,8 +128,8 @@ fp8_gemm_wide_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_con
     uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::BAR_OFF);
     uint64_t* empty = full + WIDE_STAGES;
     uint64_t* acc_full = empty + WIDE_STAGES;
-    uint64_t* acc_empty = acc_full + 2;
-    uint64_t* sc_full = acc_empty + 2;
+    uint64_t* acc_empty = acc_full + 4;  // [accumulator][half of the columns]
+    uint64_t* sc_full = acc_empty + 4;
     uint64_t* sc_empty = sc_full + SC_SLOTS;
     uint32_t* tmem_at = reinterpret_cast<uint32_t*>(smem + C::MISC_OFF);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::MISC_OFF + 8);
@@ -133,9 +143,9 @@ fp8_gemm_wide_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_con
             tc::mbar_init(&full[i], 1);
             tc::mbar_init(&empty[i], 1);
         }
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < 4; ++i) {
             tc::mbar_init(&acc_full[i], 1);
-            tc::mbar_init(&acc_empty[i], EPI_WARPS);
+            tc::mbar_init(&acc_empty[i], EPI_WARPS / 2);
         }
         for (int i = 0; i < SC_SLOTS; ++i) {
             tc::mbar_init(&sc_full[i], 32);
@@ -186,32 +196,38 @@ fp8_gemm_wide_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_con
             __syncwarp();
         } else if (warp < WIDE_SCALE) {
             if (lane == 0) {
-                constexpr uint32_t idesc = idesc_f8(128, 256);
+                constexpr uint32_t idesc = idesc_f8(128, 128);
                 const int turn = warp - WIDE_MMA;  // this warp's accumulator
                 int it = 0, sent = 0;
                 for (int u = blockIdx.x; u < tiles && !*abort_flag; u += gridDim.x) {
                     for (int kb = 0; kb < blocks; ++kb, ++it) {
                         if ((it & 1) != turn) continue;
                         const int slot = it % WIDE_STAGES;
-                        if (!tc::mbar_wait(&acc_empty[turn], (it >> 1 & 1) ^ 1) ||
-                            !tc::mbar_wait(&full[slot], it / WIDE_STAGES & 1)) {
+                        bool ok = tc::mbar_wait(&full[slot], it / WIDE_STAGES & 1);
+                        const uint32_t st = tc::smem_u32(smem + slot * WIDE_STAGE);
+                        const uint64_t da = tc::sdesc_kmajor_sw128(st);
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            ok = ok && tc::mbar_wait(&acc_empty[2 * turn + h], (it >> 1 & 1) ^ 1);
+                            if (!ok) break;
+                            tc::tc_fence_after();
+                            const uint64_t db = tc::sdesc_kmajor_sw128(st + (1 + h) * 128 * 128);
+#pragma unroll
+                            for (int k = 0; k < 4; ++k)  // 32 codes a step: 2 descriptor units of 16 bytes
+                                mma_f8(tm + turn * 256 + h * 128, da + 2 * k, db + 2 * k, idesc, k > 0);
+                            tc::mma_commit(&acc_full[2 * turn + h]);
+                        }
+                        tc::mma_commit(&empty[slot]);
+                        sent = it + 1;
+                        if (!ok) {
                             *abort_flag = 1;
                             atomicOr(g.status, QMOE_DEV_WAIT_TIMEOUT);
                             break;
                         }
-                        tc::tc_fence_after();
-                        const uint32_t st = tc::smem_u32(smem + slot * WIDE_STAGE);
-                        const uint64_t da = tc::sdesc_kmajor_sw128(st), db = tc::sdesc_kmajor_sw128(st + 128 * 128);
-#pragma unroll
-                        for (int k = 0; k < 4; ++k)  // 32 codes a step: 2 descriptor units of 16 bytes
-                            mma_f8(tm + turn * 256, da + 2 * k, db + 2 * k, idesc, k > 0);
-                        tc::mma_commit(&empty[slot]);
-                        tc::mma_commit(&acc_full[turn]);
-                        sent = it + 1;
                     }
                 }
                 if (*abort_flag && sent)  // no product outlives the accumulators
-                    tc::mbar_wait(&acc_full[turn], (sent - 1) >> 1 & 1);
+                    tc::mbar_wait(&empty[(sent - 1) % WIDE_STAGES], (sent - 1) / WIDE_STAGES & 1);
             }
             __syncwarp();
         } else {
@@ -219,21 +235,32 @@ fp8_gemm_wide_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_con
             uint32_t phase = 0;
             for (int u = blockIdx.x; u < tiles && !*abort_flag; u += gridDim.x) {
                 const int m0 = (u / q_tiles) * 128, n0 = (u % q_tiles) * 256;
+                // where the scales of this lane's first rows in the block to come lie (its others are 32, 64, ... rows
+                // further on), and which of its rows there are
+                constexpr int NA = 4, NB = UNI ? 1 : 8;
+                const float* pa = g.a.s + (int64_t)(g.a.shift ? m0 >> 7 : m0 + lane) * g.a.s_row;
+                const float* pb = g.b.s + (int64_t)(UNI ? (n0 >> 7) + (lane & 1) : n0 + lane) * g.b.s_row;
+                const int64_t step_a = g.a.shift ? 0 : 32 * g.a.s_row, step_b = 32 * g.b.s_row;
+                uint32_t real = 0;
+#pragma unroll
+                for (int i = 0; i < NA; ++i) real |= (uint32_t)(m0 + i * 32 + lane < g.M) << i;
+#pragma unroll
+                for (int i = 0; i < NB; ++i)
+                    real |= (uint32_t)((UNI ? n0 + (lane & 1) * 128 : n0 + i * 32 + lane) < g.N) << (NA + i);
                 for (int kb = 0; kb < blocks; ++kb) {
                     if (!warp_wait(&sc_empty[slot], phase ^ 1, abort_flag, g.status)) break;
-                    float* to = sc + slot * C::SC_FLOATS;
-                    auto bring = [&](const Side& s, int r, int rows, float* at) {
-                        const bool real = r < rows;
-                        cp_async_4_or_zero(at, s.s + (real ? (r >> s.shift) * s.s_row + kb * s.s_blk : 0), real);
-                    };
+                    float* const to = sc + slot * C::SC_FLOATS + lane;
 #pragma unroll
-                    for (int i = 0; i < 128; i += 32) bring(g.a, m0 + i + lane, g.M, to + i + lane);
-                    if (UNI) {
-                        if (lane < 2) bring(g.b, n0 + lane * 128, g.N, to + 128 + lane);
-                    } else {
+                    for (int i = 0; i < NA; ++i)
+                        cp_async_4_or_zero(to + i * 32, real >> i & 1 ? pa + i * step_a : g.a.s, real >> i & 1);
+                    if (!UNI || lane < 2) {
 #pragma unroll
-                        for (int i = 0; i < 256; i += 32) bring(g.b, n0 + i + lane, g.N, to + 128 + i + lane);
+                        for (int i = 0; i < NB; ++i)
+                            cp_async_4_or_zero(to + 128 + i * 32, real >> (NA + i) & 1 ? pb + i * step_b : g.b.s,
+                                               real >> (NA + i) & 1);
                     }
+                    pa += g.a.s_blk;
+                    pb += g.b.s_blk;
                     tc::cp_async_mbar_arrive_noinc(&sc_full[slot]);
                     if (++slot == SC_SLOTS) { slot = 0; phase ^= 1; }
                 }
@@ -254,33 +281,32 @@ fp8_gemm_wide_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_con
 #pragma unroll
             for (int i = 0; i < 64; ++i) acc[i] = 0ull;
             for (int kb = 0; kb < blocks; ++kb) {
-                ok = warp_wait(&sc_full[slot], phase, abort_flag, g.status);
+                ok = warp_wait(&sc_full[slot], phase, &acc_full[2 * buf + half], acc_phase, abort_flag, g.status);
                 if (!ok) break;
+                tc::tc_fence_after();
                 const float* s = sc + slot * C::SC_FLOATS;
                 const float own = UNI ? s[p_lane] * s[128 + half] : s[p_lane];
                 const uint64_t sp = pair_of(own, own);
-                ok = warp_wait(&acc_full[buf], acc_phase, abort_flag, g.status);
-                if (!ok) break;
-                tc::tc_fence_after();
+                constexpr int STEP = UNI ? 64 : 32;  // columns in registers at a time (no room for 64 beside column scales)
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    uint32_t d[64];
-                    tmem_ld64(t_lane + buf * 256 + i * 64, d);
+                for (int i = 0; i < 128; i += STEP) {
+                    uint32_t d[STEP];
+                    tmem_load(t_lane + buf * 256 + i, d);
                     tc::tmem_ld_wait();
-                    if (i == 1) {
+                    if (i + STEP == 128) {
                         tc::tc_fence_before();
                         __syncwarp();
-                        if (lane == 0) tc::mbar_arrive(&acc_empty[buf]);
+                        if (lane == 0) tc::mbar_arrive(&acc_empty[2 * buf + half]);
                     }
 #pragma unroll
-                    for (int j = 0; j < 64; j += 4) {
+                    for (int j = 0; j < STEP; j += 4) {
                         uint64_t s0 = sp, s1 = sp;
                         if (!UNI) {
-                            const float4 v = *reinterpret_cast<const float4*>(s + 128 + half * 128 + i * 64 + j);
+                            const float4 v = *reinterpret_cast<const float4*>(s + 128 + half * 128 + i + j);
                             s0 = mul_pair(pair_of(v.x, v.y), sp);
                             s1 = mul_pair(pair_of(v.z, v.w), sp);
                         }
-                        uint64_t* to = &acc[(i * 64 + j) / 2];
+                        uint64_t* to = &acc[(i + j) / 2];
                         to[0] = fma_pair(pair_of(d[j], d[j + 1]), s0, to[0]);
                         to[1] = fma_pair(pair_of(d[j + 2], d[j + 3]), s1, to[1]);
                     }
