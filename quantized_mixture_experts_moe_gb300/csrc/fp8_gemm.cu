@@ -30,7 +30,7 @@ int quant_rows_launch(int64_t rows, int64_t cols, int dtype, const void* x, int6
 // warps multiply it into the column scales; else each lane has its own.
 template <int NT, bool UNI>
 struct GemmCfg {
-    static constexpr int BUFS = NT == 256 ? 2 : 4;  // accumulators in TMEM
+    static constexpr int BUFS = 4;  // accumulators in TMEM
     static constexpr int TMEM_COLS = BUFS * NT < 32 ? 32 : BUFS * NT;
     static constexpr int P_BYTES = 128 * 128, Q_BYTES = NT * 128, STAGE = P_BYTES + Q_BYTES;
     static constexpr int SC_FLOATS = NT + (UNI ? 0 : 128);
@@ -115,27 +115,40 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant
     __syncthreads();
     tc::tc_fence_after();
     const uint32_t tm = *tmem_at;
-    pdl_wait();
+    // what comes of a and its scales waits for the kernel before this one; b may not depend on it (weights_early)
+    if (!g.weights_early) pdl_wait();
 
     if (warp >= EPI_WARPS) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(OTHER_REGS));
         if (warp < WARP_MMA) {
             if (lane == 0) {
                 const int turn = warp - WARP_TMA;
-                int it = 0, sent = 0;
+                int it = 0, sent = 0, early = 0;
+                if (g.weights_early) {
+                    if (first < tiles) {
+                        early = min(kb1 - kb0, C::STAGES);
+                        for (int i = turn; i < early; i += TURNS) {
+                            tc::mbar_arrive_expect_tx(&full[i], C::STAGE);
+                            tc::tma_load_2d(smem + i * C::STAGE, &map_b, &full[i], (kb0 + i) * 128, (first % p_tiles) * 128);
+                        }
+                    }
+                    pdl_wait();
+                }
                 for (int u = first; u < tiles && !*abort_flag; u += stride) {
                     const int p0 = (u % p_tiles) * 128, q0 = (u / p_tiles) * NT;
                     for (int kb = kb0; kb < kb1; ++kb, ++it) {
                         if ((it & 1) != turn) continue;
                         const int slot = it % C::STAGES;
-                        if (!tc::mbar_wait(&empty[slot], (it / C::STAGES & 1) ^ 1)) {
-                            *abort_flag = 1;
-                            atomicOr(g.status, QMOE_DEV_WAIT_TIMEOUT);
-                            break;
-                        }
                         uint8_t* st = smem + slot * C::STAGE;
-                        tc::mbar_arrive_expect_tx(&full[slot], C::STAGE);
-                        tc::tma_load_2d(st, &map_b, &full[slot], kb * 128, p0);
+                        if (it >= early) {
+                            if (!tc::mbar_wait(&empty[slot], (it / C::STAGES & 1) ^ 1)) {
+                                *abort_flag = 1;
+                                atomicOr(g.status, QMOE_DEV_WAIT_TIMEOUT);
+                                break;
+                            }
+                            tc::mbar_arrive_expect_tx(&full[slot], C::STAGE);
+                            tc::tma_load_2d(st, &map_b, &full[slot], kb * 128, p0);
+                        }
                         tc::tma_load_2d(st + C::P_BYTES, &map_a, &full[slot], kb * 128, q0);
                         sent = it + 1;
                     }
@@ -177,6 +190,7 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant
             __syncwarp();
         } else if (warp < WARP_SCALE + TURNS) {
         // the scale warps take the blocks in turn; a block's loads go out before the slot is waited for
+        if (g.weights_early) pdl_wait();
         int it = 0;
         for (int u = first; u < tiles && !*abort_flag; u += stride) {
             const int p0 = (u % p_tiles) * 128, q0 = (u / p_tiles) * NT;
@@ -327,27 +341,54 @@ struct Plan {
     int nt, parts;  // parts 0: the wide kernel
 };
 
-// The narrowest tile that holds all tokens up to 128, else 256 columns; the
-// reduction in as many parts (a power of two up to 8, two blocks of 128 at
-// least in each) as keep one wave of CTAs.
-inline Plan plan_of(int M, int N, int K) {
-    Plan p;
-    p.nt = M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : M <= 128 ? 128 : 256;
-    const int64_t tiles = (int64_t)((N + 127) / 128) * ((M + p.nt - 1) / p.nt);
+// Tile and split by a model of the time in us, fitted to sweeps of both on
+// GB300 (K 64 to 8192, M 1 to 2048, N 1024 to 4096; within 15% of every
+// measured time):
+//   start + rounds * blocks * per_block + (split: 1.3 + nt / 30)
+// rounds: tiles an SM takes in turn; blocks: of 128 along the reduction, in one
+// part.  A split gives every cluster one tile; clusters of 8 fill no more than
+// some 96 SMs, smaller ones 132.  A block costs a narrow tile little more than
+// its handshakes (0.24 us at 16 columns, 0.31 at 64), so few tokens take the
+// narrowest tile and split far: 5.7 us at M 1, N 2048, K 4096, 10.8 unsplit.
+// The wide kernel does twice the columns of nt = 128 in 0.55 us against 0.48,
+// and only where a row block of b shares its scales: with column scales it took
+// 1.03.
+inline Plan plan_of(int M, int N, int K, bool uniform) {
+    struct Tile {
+        int nt;
+        float start, per_block;
+    };
+    const Tile tile[4] = {{16, 2.6f, 0.24f}, {32, 2.6f, 0.25f}, {64, 2.9f, 0.31f}, {128, 3.1f, uniform ? 0.48f : 0.52f}};
+    const int splits[6] = {1, 2, 3, 4, 6, 8};
     const int blocks = (K + 127) / 128;
-    p.parts = 0;
-    if ((int64_t)((M + 127) / 128) * ((N + 255) / 256) >= row::kSMs / 2) return p;
-    p.parts = 1;
-    while (p.parts < 8 && tiles * p.parts * 2 <= row::kSMs && blocks >= p.parts * 4) p.parts *= 2;
-    return p;
+    Plan best = {128, 1};
+    float least = 1e30f;
+    for (const Tile& c : tile) {
+        const int64_t tiles = (int64_t)((N + 127) / 128) * ((M + c.nt - 1) / c.nt);
+        for (const int parts : splits) {
+            if (parts > 1 && (parts > blocks || tiles * parts > (parts == 8 ? 96 : 132))) continue;
+            const int64_t rounds = parts > 1 ? 1 : (tiles + row::kSMs - 1) / row::kSMs;
+            const float us = c.start + (float)rounds * (float)((blocks + parts - 1) / parts) * c.per_block +
+                             (parts > 1 ? 1.3f + (float)c.nt / 30.f : 0.f);
+            if (us < least) {
+                least = us;
+                best = {c.nt, parts};
+            }
+        }
+    }
+    if (uniform) {
+        const int64_t tiles = (int64_t)((M + 127) / 128) * ((N + WIDE_N - 1) / WIDE_N);
+        const float us = 4.2f + (float)((tiles + row::kSMs - 1) / row::kSMs) * (float)blocks * 0.55f;
+        if (us < least) best = {WIDE_N, 0};
+    }
+    return best;
 }
 
 template <int NT, bool UNI>
 static int gemm_launch(const CUtensorMap& ma, const CUtensorMap& mb, const GemmArgs& g, int parts, cudaStream_t st) {
     using C = GemmCfg<NT, UNI>;
-    auto kernel = fp8_gemm_kernel<NT, UNI>;
-    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM) != cudaSuccess)
-        return QMOE_ERR_CUDA;
+    const int rc = row::allow_smem<fp8_gemm_kernel<NT, UNI>>(C::SMEM);
+    if (rc != QMOE_OK) return rc;
     const int64_t tiles = (int64_t)((g.N + 127) / 128) * ((g.M + NT - 1) / NT);
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -364,7 +405,7 @@ static int gemm_launch(const CUtensorMap& ma, const CUtensorMap& mb, const GemmA
     cfg.stream = st;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, kernel, ma, mb, g) == cudaSuccess ? QMOE_OK : QMOE_ERR_LAUNCH;
+    return cudaLaunchKernelEx(&cfg, fp8_gemm_kernel<NT, UNI>, ma, mb, g) == cudaSuccess ? QMOE_OK : QMOE_ERR_LAUNCH;
 }
 
 template <int NT>
@@ -373,7 +414,7 @@ static int gemm_kind(const CUtensorMap& ma, const CUtensorMap& mb, const GemmArg
 }
 
 static int gemm_run(const qmoe_fp8_mat* a, const qmoe_fp8_mat* b, GemmArgs& g, cudaStream_t st) {
-    const Plan p = plan_of(g.M, g.N, g.K);
+    const Plan p = plan_of(g.M, g.N, g.K, g.b.shift != 0);
     CUtensorMap ma, mb;
     int rc = code_map(&ma, a->q, a->ld, g.M, g.K, p.parts ? p.nt : 128);
     if (rc != QMOE_OK) return rc;
@@ -384,8 +425,7 @@ static int gemm_run(const qmoe_fp8_mat* a, const qmoe_fp8_mat* b, GemmArgs& g, c
         case 16: return gemm_kind<16>(ma, mb, g, p.parts, st);
         case 32: return gemm_kind<32>(ma, mb, g, p.parts, st);
         case 64: return gemm_kind<64>(ma, mb, g, p.parts, st);
-        case 128: return gemm_kind<128>(ma, mb, g, p.parts, st);
-        default: return gemm_kind<256>(ma, mb, g, p.parts, st);
+        default: return gemm_kind<128>(ma, mb, g, p.parts, st);
     }
 }
 

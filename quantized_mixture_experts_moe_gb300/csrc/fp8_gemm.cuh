@@ -129,7 +129,9 @@ __device__ __forceinline__ float peer_load(const float* p, uint32_t rank) {
     return v;
 }
 
-// The product of both maps (boxes of 128 rows of a, 256 of b) in 128 x 256 tiles.
+// The product of both maps (boxes of 128 rows of a, 256 of b) in 128 x 256
+// tiles, for b whose rows share their scales by 128.
+constexpr int WIDE_N = 256;
 int gemm_wide(const CUtensorMap& ma, const CUtensorMap& mb, const GemmArgs& g, cudaStream_t st);
 
 }  // namespace fp8

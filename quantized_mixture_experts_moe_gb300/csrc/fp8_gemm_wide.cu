@@ -1,18 +1,20 @@
-// The FP8 product for many rows (see fp8_gemm.cu for the arithmetic): 128 x 256
-// tiles of c, rows of a on the lanes.
+// The FP8 product for many rows of a and a b whose rows share their scales by
+// 128, as a weight's do (see fp8_gemm.cu for the arithmetic): 128 x 256 tiles of
+// c, rows of a on the lanes.
 //
-// Where 128 rows of b share a scale (weights), a thread's 128 columns have one
-// scale in a block, and adding a block is 64 paired fused multiply-adds a
-// thread.  Otherwise (two activations, as in a weight's gradient) each column
-// has its own, read from shared memory: one wavefront a column and warp, 1024
-// cycles a block against 512 of products, which is then the bound.  Reading an
-// accumulator is latency (about 200 cycles a tcgen05.ld, whatever its width),
-// so it is read 64 columns at a time.
+// A thread's 128 columns then have one scale in a block, and adding a block is
+// 64 paired fused multiply-adds a thread, with no scale read for each column
+// (those reads are one wavefront a column and warp: 1024 cycles a block).  The
+// two accumulators take the blocks in turn, and their halves are handed over
+// separately: a block's products are 512 cycles, but issuing four of them and
+// the way to the epilogue and back cost as much again, which the halves hide
+// in part.  8192 x 2816 x 4096: 93 us, 2.02 PFLOP/s.
 //
-// With two-CTA products (256 x 256 a pair, half the rows of b loaded by each)
-// it was slower, 189 us against 135 at 8192 x 2816 x 4096: loads that report
-// to the other CTA's barrier took 0.8 us a block, and handing accumulators
-// between the CTAs another 0.35 us.
+// Two-CTA products (256 x 256 a pair, half the rows of b loaded by each) were
+// slower, 189 us at that size against 135 of the narrow kernel: loads that
+// report to the other CTA's barrier took 0.8 us a block, and handing
+// accumulators between the CTAs another 0.35 us.  So were 128 x 192 tiles with
+// 12 epilogue warps (125 us) and 16 epilogue warps (120 us).
 #include "fp8_gemm.cuh"
 
 namespace qmoe {
@@ -20,16 +22,14 @@ namespace fp8 {
 
 // Warps: 8 scale and sum, then one that loads, two that issue products (one for
 // each accumulator) and one that brings scales.  Registers: launched with 168 a
-// thread (64,512 in all); the epilogue's warpgroups take 216, the third keeps 72
+// thread (64,512 in all); the epilogue's warpgroups take 232, the third keeps 40
 // (64,512 in all).
 constexpr int WIDE_TMA = 8, WIDE_MMA = 9, WIDE_SCALE = 11, WIDE_THREADS = 12 * 32;
-constexpr int WIDE_EPI_REGS = 216, WIDE_OTHER_REGS = 72;
+constexpr int WIDE_EPI_REGS = 232, WIDE_OTHER_REGS = 40;
 constexpr int WIDE_STAGE = (128 + 256) * 128, WIDE_STAGES = 4;
 constexpr int OUT_PITCH = 80;  // bytes of a row (64 used) in a warp's output stage
-template <bool UNI>
 struct WideCfg {
-    // 128 lane scales, then 2 (UNI) or 256 column scales
-    static constexpr int SC_FLOATS = 128 + (UNI ? 4 : 256);
+    static constexpr int SC_FLOATS = 128 + 4;  // 128 lane scales, then one for each half of the columns
     static constexpr int SC_OFF = WIDE_STAGES * WIDE_STAGE;
     static constexpr int OUT_OFF = SC_OFF + SC_SLOTS * SC_FLOATS * 4;
     static constexpr int BAR_OFF = OUT_OFF + EPI_WARPS * 32 * OUT_PITCH;
@@ -44,16 +44,6 @@ __device__ __forceinline__ void cp_async_4_or_zero(void* dst, const void* src, b
                  : "memory");
 }
 
-__device__ __forceinline__ void tmem_load(uint32_t taddr, uint32_t (&r)[32]) {
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,"
-        "%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
-          "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
-          "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-        : "r"(taddr));
-}
 __device__ __forceinline__ void tmem_load(uint32_t taddr, uint32_t (&r)[64]) {
     asm volatile(
         "tcgen05.ld.sync.aligned.32x32b.x64.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,"
@@ -117,11 +107,10 @@ __device__ __forceinline__ void put_rows(const GemmArgs& g, uint8_t* stage, int 
     }
 }
 
-template <bool UNI>
 __global__ void __launch_bounds__(WIDE_THREADS, 1)
 fp8_gemm_wide_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
                      const GemmArgs g) {
-    using C = WideCfg<UNI>;
+    using C = WideCfg;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     float* sc = reinterpret_cast<float*>(smem + C::SC_OFF);
@@ -235,32 +224,26 @@ fp8_gemm_wide_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_con
             uint32_t phase = 0;
             for (int u = blockIdx.x; u < tiles && !*abort_flag; u += gridDim.x) {
                 const int m0 = (u / q_tiles) * 128, n0 = (u % q_tiles) * 256;
-                // where the scales of this lane's first rows in the block to come lie (its others are 32, 64, ... rows
-                // further on), and which of its rows there are
-                constexpr int NA = 4, NB = UNI ? 1 : 8;
-                const float* pa = g.a.s + (int64_t)(g.a.shift ? m0 >> 7 : m0 + lane) * g.a.s_row;
-                const float* pb = g.b.s + (int64_t)(UNI ? (n0 >> 7) + (lane & 1) : n0 + lane) * g.b.s_row;
-                const int64_t step_a = g.a.shift ? 0 : 32 * g.a.s_row, step_b = 32 * g.b.s_row;
+                // this lane's rows of a (and lanes 0 and 1: a half's rows of b): where their scales in the block to
+                // come lie, and whether there are such rows
+                const float* at[5];
                 uint32_t real = 0;
 #pragma unroll
-                for (int i = 0; i < NA; ++i) real |= (uint32_t)(m0 + i * 32 + lane < g.M) << i;
-#pragma unroll
-                for (int i = 0; i < NB; ++i)
-                    real |= (uint32_t)((UNI ? n0 + (lane & 1) * 128 : n0 + i * 32 + lane) < g.N) << (NA + i);
+                for (int i = 0; i < 5; ++i) {
+                    const Side& s = i < 4 ? g.a : g.b;
+                    const int r = i < 4 ? m0 + i * 32 + lane : n0 + (lane & 1) * 128;
+                    const bool there = r < (i < 4 ? g.M : g.N);
+                    at[i] = s.s + (there ? (int64_t)(r >> s.shift) * s.s_row : 0);
+                    real |= (uint32_t)there << i;
+                }
                 for (int kb = 0; kb < blocks; ++kb) {
                     if (!warp_wait(&sc_empty[slot], phase ^ 1, abort_flag, g.status)) break;
                     float* const to = sc + slot * C::SC_FLOATS + lane;
 #pragma unroll
-                    for (int i = 0; i < NA; ++i)
-                        cp_async_4_or_zero(to + i * 32, real >> i & 1 ? pa + i * step_a : g.a.s, real >> i & 1);
-                    if (!UNI || lane < 2) {
-#pragma unroll
-                        for (int i = 0; i < NB; ++i)
-                            cp_async_4_or_zero(to + 128 + i * 32, real >> (NA + i) & 1 ? pb + i * step_b : g.b.s,
-                                               real >> (NA + i) & 1);
+                    for (int i = 0; i < 5; ++i) {
+                        if (i < 4 || lane < 2) cp_async_4_or_zero(to + i * 32, at[i], real >> i & 1);
+                        at[i] += i < 4 ? g.a.s_blk : g.b.s_blk;
                     }
-                    pa += g.a.s_blk;
-                    pb += g.b.s_blk;
                     tc::cp_async_mbar_arrive_noinc(&sc_full[slot]);
                     if (++slot == SC_SLOTS) { slot = 0; phase ^= 1; }
                 }
@@ -285,31 +268,21 @@ fp8_gemm_wide_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_con
                 if (!ok) break;
                 tc::tc_fence_after();
                 const float* s = sc + slot * C::SC_FLOATS;
-                const float own = UNI ? s[p_lane] * s[128 + half] : s[p_lane];
+                const float own = s[p_lane] * s[128 + half];
                 const uint64_t sp = pair_of(own, own);
-                constexpr int STEP = UNI ? 64 : 32;  // columns in registers at a time (no room for 64 beside column scales)
 #pragma unroll
-                for (int i = 0; i < 128; i += STEP) {
-                    uint32_t d[STEP];
+                for (int i = 0; i < 128; i += 64) {
+                    uint32_t d[64];
                     tmem_load(t_lane + buf * 256 + i, d);
                     tc::tmem_ld_wait();
-                    if (i + STEP == 128) {
+                    if (i > 0) {
                         tc::tc_fence_before();
                         __syncwarp();
                         if (lane == 0) tc::mbar_arrive(&acc_empty[2 * buf + half]);
                     }
 #pragma unroll
-                    for (int j = 0; j < STEP; j += 4) {
-                        uint64_t s0 = sp, s1 = sp;
-                        if (!UNI) {
-                            const float4 v = *reinterpret_cast<const float4*>(s + 128 + half * 128 + i + j);
-                            s0 = mul_pair(pair_of(v.x, v.y), sp);
-                            s1 = mul_pair(pair_of(v.z, v.w), sp);
-                        }
-                        uint64_t* to = &acc[(i + j) / 2];
-                        to[0] = fma_pair(pair_of(d[j], d[j + 1]), s0, to[0]);
-                        to[1] = fma_pair(pair_of(d[j + 2], d[j + 3]), s1, to[1]);
-                    }
+                    for (int j = 0; j < 64; j += 2)
+                        acc[(i + j) / 2] = fma_pair(pair_of(d[j], d[j + 1]), sp, acc[(i + j) / 2]);
                 }
                 __syncwarp();
                 if (lane == 0) tc::mbar_arrive(&sc_empty[slot]);
@@ -331,19 +304,12 @@ fp8_gemm_wide_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_con
     if (warp == WIDE_MMA) tc::tmem_dealloc(tm, 512);
 }
 
-template <bool UNI>
-static int wide_launch(const CUtensorMap& ma, const CUtensorMap& mb, const GemmArgs& g, cudaStream_t st) {
-    auto kernel = fp8_gemm_wide_kernel<UNI>;
-    const int smem = WideCfg<UNI>::SMEM;
-    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
-        return QMOE_ERR_CUDA;
-    const int64_t tiles = (int64_t)((g.M + 127) / 128) * ((g.N + 255) / 256);
-    return launch_pdl(kernel, dim3((unsigned)(tiles < row::kSMs ? tiles : row::kSMs)), dim3(WIDE_THREADS), (size_t)smem,
-                      st, ma, mb, g);
-}
-
 int gemm_wide(const CUtensorMap& ma, const CUtensorMap& mb, const GemmArgs& g, cudaStream_t st) {
-    return g.b.shift ? wide_launch<true>(ma, mb, g, st) : wide_launch<false>(ma, mb, g, st);
+    const int rc = row::allow_smem<fp8_gemm_wide_kernel>(WideCfg::SMEM);
+    if (rc != QMOE_OK) return rc;
+    const int64_t tiles = (int64_t)((g.M + 127) / 128) * ((g.N + WIDE_N - 1) / WIDE_N);
+    return launch_pdl(fp8_gemm_wide_kernel, dim3((unsigned)(tiles < row::kSMs ? tiles : row::kSMs)), dim3(WIDE_THREADS),
+                      (size_t)WideCfg::SMEM, st, ma, mb, g);
 }
 
 }  // namespace fp8

@@ -160,8 +160,8 @@ norm_fwd_kernel(const FwdArgs a) {
     }
 }
 
-template <typename K>
-inline int start(K kernel, const Shape& s, FwdArgs& a, int row_bytes, cudaStream_t st) {
+template <auto Kernel>
+inline int start(const Shape& s, FwdArgs& a, int row_bytes, cudaStream_t st) {
     const int threads = s.threads * s.rows_per_cta;
     const int64_t ctas = (a.rows + s.rows_per_cta - 1) / s.rows_per_cta;
     // one wave of 512 threads an SM; fewer CTAs where that leaves each two stages
@@ -172,10 +172,11 @@ inline int start(K kernel, const Shape& s, FwdArgs& a, int row_bytes, cudaStream
     if (!a.stages) return QMOE_ERR_UNSUPPORTED;
     const int64_t fit = (int64_t)row::kSMs * per_sm;
     const size_t smem = (size_t)a.stages * row_bytes * s.rows_per_cta;
-    if (smem > 48 * 1024 - 1024 &&
-        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 225 * 1024) != cudaSuccess)
-        return QMOE_ERR_CUDA;
-    return launch_pdl(kernel, dim3((unsigned)(ctas < fit ? ctas : fit)), dim3(s.threads, s.rows_per_cta), smem, st, a);
+    if (smem > 47 * 1024) {
+        const int rc = row::allow_smem<Kernel>(225 * 1024);
+        if (rc != QMOE_OK) return rc;
+    }
+    return launch_pdl(Kernel, dim3((unsigned)(ctas < fit ? ctas : fit)), dim3(s.threads, s.rows_per_cta), smem, st, a);
 }
 
 template <bool POST>
@@ -189,11 +190,11 @@ struct Fwd {
             a.full_gate.off = rb + yb;
             const int bytes = rb + (POST ? yb : 0) + (a.full_gate.p ? yb : 0);
             if (vec) {
-                if (s.nv == 2) return start(norm_fwd_kernel<RT, YT, 2, 8, POST>, s, a, bytes, st);
-                return start(norm_fwd_kernel<RT, YT, 4, 8, POST>, s, a, bytes, st);
+                if (s.nv == 2) return start<norm_fwd_kernel<RT, YT, 2, 8, POST>>(s, a, bytes, st);
+                return start<norm_fwd_kernel<RT, YT, 4, 8, POST>>(s, a, bytes, st);
             }
-            if (s.nv == 16) return start(norm_fwd_kernel<RT, YT, 16, 1, POST>, s, a, bytes, st);
-            return start(norm_fwd_kernel<RT, YT, 32, 1, POST>, s, a, bytes, st);
+            if (s.nv == 16) return start<norm_fwd_kernel<RT, YT, 16, 1, POST>>(s, a, bytes, st);
+            return start<norm_fwd_kernel<RT, YT, 32, 1, POST>>(s, a, bytes, st);
         }
     };
 };

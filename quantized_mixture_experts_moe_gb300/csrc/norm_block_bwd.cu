@@ -319,8 +319,8 @@ inline int64_t part_rows(int64_t rows, int64_t cols) {
     return most;
 }
 
-template <typename K>
-inline int start(K kernel, const Shape& s, BwdArgs& a, int sums, int row_bytes, int64_t ctas, cudaStream_t st) {
+template <auto Kernel>
+inline int start(const Shape& s, BwdArgs& a, int sums, int row_bytes, int64_t ctas, cudaStream_t st) {
     const int64_t padded = (a.cols + 7) / 8 * 8;
     const int64_t besides = s.values() == 32   ? (int64_t)sums * 32 * s.threads * 4
                             : s.values() == 16 ? (sums == 3 ? 2 : 1) * padded * 4
@@ -329,10 +329,11 @@ inline int start(K kernel, const Shape& s, BwdArgs& a, int sums, int row_bytes, 
     a.stages = s.values() == 32 ? 0 : stages_of((int64_t)row_bytes * s.rows_per_cta, besides, per_sm_of(s));
     if (s.values() < 32 && !a.stages) return QMOE_ERR_UNSUPPORTED;
     const size_t smem = (size_t)(besides + (int64_t)a.stages * row_bytes * s.rows_per_cta);
-    if (smem > 48 * 1024 - 1024 &&
-        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 225 * 1024) != cudaSuccess)
-        return QMOE_ERR_CUDA;
-    return launch_pdl(kernel, dim3((unsigned)ctas), dim3(s.threads, s.rows_per_cta), smem, st, a);
+    if (smem > 47 * 1024) {
+        const int rc = row::allow_smem<Kernel>(225 * 1024);
+        if (rc != QMOE_OK) return rc;
+    }
+    return launch_pdl(Kernel, dim3((unsigned)ctas), dim3(s.threads, s.rows_per_cta), smem, st, a);
 }
 
 template <bool POST>
@@ -353,13 +354,13 @@ struct Bwd {
             place(a.full_gate, yb);
             constexpr int sums = POST ? 3 : 1;
             if (s.vec == 8) {
-                if (s.nv == 1) return start(norm_bwd_kernel<RT, YT, 1, 8, POST>, s, a, sums, at, ctas, st);
-                if (s.nv == 2) return start(norm_bwd_kernel<RT, YT, 2, 8, POST>, s, a, sums, at, ctas, st);
-                return start(norm_bwd_kernel<RT, YT, 4, 8, POST>, s, a, sums, at, ctas, st);
+                if (s.nv == 1) return start<norm_bwd_kernel<RT, YT, 1, 8, POST>>(s, a, sums, at, ctas, st);
+                if (s.nv == 2) return start<norm_bwd_kernel<RT, YT, 2, 8, POST>>(s, a, sums, at, ctas, st);
+                return start<norm_bwd_kernel<RT, YT, 4, 8, POST>>(s, a, sums, at, ctas, st);
             }
-            if (s.nv == 8) return start(norm_bwd_kernel<RT, YT, 8, 1, POST>, s, a, sums, at, ctas, st);
-            if (s.nv == 16) return start(norm_bwd_kernel<RT, YT, 16, 1, POST>, s, a, sums, at, ctas, st);
-            return start(norm_bwd_kernel<RT, YT, 32, 1, POST>, s, a, sums, at, ctas, st);
+            if (s.nv == 8) return start<norm_bwd_kernel<RT, YT, 8, 1, POST>>(s, a, sums, at, ctas, st);
+            if (s.nv == 16) return start<norm_bwd_kernel<RT, YT, 16, 1, POST>>(s, a, sums, at, ctas, st);
+            return start<norm_bwd_kernel<RT, YT, 32, 1, POST>>(s, a, sums, at, ctas, st);
         }
     };
 };

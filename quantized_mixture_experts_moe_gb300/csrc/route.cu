@@ -74,9 +74,8 @@ template <> __device__ __forceinline__ float from16<__half>(uint32_t u) {
 
 // The keys of a lane's experts and the k rounds.  PACK: 16-bit logits without
 // a bias, key = order of the 16 bits << 16 | (0xFFFF - expert), 0 for a gone or
-// unavailable expert; else key = 32-bit order of the score, NONE or less for one
-// that is not available.
-constexpr uint32_t NONE = 0x007FFFFFu;  // key of -inf
+// unavailable expert; else key = 32-bit order of the score, where -inf has
+// 0x007FFFFF.
 
 template <typename T>
 __device__ __forceinline__ uint32_t packed_key(float v, int e) {
@@ -187,7 +186,7 @@ route_kernel(const Args a) {
                 if (top == 0u) break;
                 win = 0xFFFF - (int)(top & 0xFFFFu);
             } else {
-                if (top <= NONE) break;
+                if (top <= 0x007FFFFFu) break;
                 unsigned at = 0x7FFFFFFFu;
 #pragma unroll
                 for (int i = NE - 1; i >= 0; --i)
@@ -391,22 +390,23 @@ inline int ctas(int64_t T) {
     return (int)(n < most ? n : most);
 }
 
-template <typename K>
-inline int launch(K kernel, const Args& a, size_t smem, cudaStream_t st) {
-    if (smem > 48 * 1024 &&
-        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
-        return QMOE_ERR_CUDA;
-    return launch_pdl(kernel, ctas(a.T), WARPS * 32, smem, st, a);
+template <auto Kernel>
+inline int launch(const Args& a, size_t smem, cudaStream_t st) {
+    if (smem > 48 * 1024) {
+        const int rc = row::allow_smem<Kernel>(((WARPS + 1) * MAX_E + 1) * 4);
+        if (rc != QMOE_OK) return rc;
+    }
+    return launch_pdl(Kernel, ctas(a.T), WARPS * 32, smem, st, a);
 }
 template <bool BWD, typename T, int NE, int V>
 inline int start(const Args& a, cudaStream_t st) {
     if constexpr (BWD) {
-        return launch(route_bwd_kernel<T, NE, V>, a, (size_t)WARPS * NE * 32 * 4, st);
+        return launch<route_bwd_kernel<T, NE, V>>(a, (size_t)WARPS * NE * 32 * 4, st);
     } else {
         const size_t smem = a.part_p ? ((size_t)WARPS * a.E + a.E + 1) * 4 : 0;
         if constexpr (sizeof(T) == 2)
-            if (!a.bias) return launch(route_kernel<T, NE, V, true>, a, smem, st);
-        return launch(route_kernel<T, NE, V, false>, a, smem, st);
+            if (!a.bias) return launch<route_kernel<T, NE, V, true>>(a, smem, st);
+        return launch<route_kernel<T, NE, V, false>>(a, smem, st);
     }
 }
 // The widest loads, up to 16 bytes, that the rows allow: else one value at a time.

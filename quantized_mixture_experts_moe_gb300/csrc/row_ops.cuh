@@ -3,12 +3,29 @@
 // share a row.
 #pragma once
 
+#include <atomic>
+
 #include "qmoe_common.cuh"
 
 namespace qmoe {
 namespace row {
 
 constexpr int kSMs = 152;  // GB300
+
+// Lets a kernel use `bytes` of dynamic shared memory; asked of the runtime once
+// for each kernel and device.
+template <auto Kernel>
+inline int allow_smem(int bytes) {
+    static std::atomic<uint64_t> done{0};
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return QMOE_ERR_CUDA;
+    const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+    if (done.load(std::memory_order_acquire) & bit) return QMOE_OK;
+    if (cudaFuncSetAttribute(Kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess)
+        return QMOE_ERR_CUDA;
+    done.fetch_or(bit, std::memory_order_release);
+    return QMOE_OK;
+}
 
 inline bool dtype_ok(int t) { return t == QMOE_F32 || t == QMOE_BF16 || t == QMOE_F16; }
 inline int dtype_size(int t) { return t == QMOE_F32 ? 4 : 2; }
