@@ -98,9 +98,12 @@ quant_rows_kernel(const T* __restrict__ x, int64_t ldx, int64_t rows, int64_t co
     }
 }
 
-// A 128 x 128 tile a CTA; a thread holds 8 x 8 values (rows 8 (tid / 16) on,
-// columns 8 (tid % 16) on), so that its codes leave in 8-byte pieces both
-// ways; the transposed ones go through shared memory to leave in whole rows.
+// A 128 x 128 tile a CTA of 512 threads; a thread holds 4 x 8 values (rows
+// 4 (tid / 16) on, columns 8 (tid % 16) on), 16 registers of a 16-bit type, so
+// that two CTAs' loads are in flight on an SM.  Row codes leave in 8-byte
+// pieces; the transposed ones go through shared memory, 4 bytes a column and
+// thread, exclusive-ored so that neither side's accesses share a bank, to leave
+// in 16-byte pieces of whole rows.
 //   MODE 0: column scales, codes transposed, and where q is given the row form
 //   MODE 1: one scale, codes where q is given, transposed where qt is given
 struct TileArgs {
@@ -113,23 +116,23 @@ struct TileArgs {
     int64_t ldqt;
     float* st;
 };
-constexpr int TPITCH = 144;  // bytes between the columns of the transposed tile
+constexpr int TILE_THREADS = 512, TILE_WARPS = 16, TILE_ROWS = 4;
 
 template <typename T, bool VEC, int MODE>
-__global__ void __launch_bounds__(256, sizeof(T) == 2 ? 4 : 2)
+__global__ void __launch_bounds__(TILE_THREADS, 2)
 quant_tile_kernel(const TileArgs a) {
-    __shared__ __align__(16) uint8_t tile[128 * TPITCH];
-    __shared__ float part[8][128];
-    __shared__ float col_max[128];
+    __shared__ __align__(16) uint32_t tile[128 * 32];  // [column][4-row piece ^ 2 (column / 8)]
+    __shared__ float part[TILE_WARPS][128];
+    __shared__ float col_inv[128];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int rg = tid >> 4, cg = tid & 15;
     const int64_t r0 = (int64_t)blockIdx.y * 128, c0 = (int64_t)blockIdx.x * 128;
     const int64_t c = c0 + cg * 8;
     pdl_sync();
-    Raw8<T> v[8];
+    Raw8<T> v[TILE_ROWS];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const int64_t r = r0 + rg * 8 + i;
+    for (int i = 0; i < TILE_ROWS; ++i) {
+        const int64_t r = r0 + rg * TILE_ROWS + i;
         load8<T, VEC>(static_cast<const T*>(a.x) + r * a.ldx, r < a.rows, c, a.cols, v[i]);
     }
     float inv_c[8];
@@ -138,32 +141,31 @@ quant_tile_kernel(const TileArgs a) {
 #pragma unroll
         for (int j = 0; j < 8; ++j) m[j] = AMAX_MIN;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
+        for (int i = 0; i < TILE_ROWS; ++i) {
             float t[8];
             row::widen<8>(v[i], t);
 #pragma unroll
             for (int j = 0; j < 8; ++j) m[j] = fmaxf(m[j], fabsf(t[j]));
         }
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            m[j] = fmaxf(m[j], __shfl_xor_sync(0xFFFFFFFFu, m[j], 16));
-            if (lane < 16) part[warp][cg * 8 + j] = m[j];
+        for (int j = 0; j < 8; ++j) m[j] = fmaxf(m[j], __shfl_xor_sync(0xFFFFFFFFu, m[j], 16));
+        if (lane < 16) {
+            float4* to = reinterpret_cast<float4*>(&part[warp][cg * 8]);
+            to[0] = make_float4(m[0], m[1], m[2], m[3]);
+            to[1] = make_float4(m[4], m[5], m[6], m[7]);
         }
         __syncthreads();
         if (tid < 128) {
             float t = part[0][tid];
 #pragma unroll
-            for (int i = 1; i < 8; ++i) t = fmaxf(t, part[i][tid]);
-            col_max[tid] = inverse_of(t);
+            for (int i = 1; i < TILE_WARPS; ++i) t = fmaxf(t, part[i][tid]);
+            col_inv[tid] = inverse_of(t);
             if (c0 + tid < a.cols) a.st[(int64_t)blockIdx.y * a.cols + c0 + tid] = scale_of(t);
         }
-        __syncthreads();
-#pragma unroll
-        for (int j = 0; j < 8; ++j) inv_c[j] = col_max[cg * 8 + j];
         if (a.q) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const int64_t r = r0 + rg * 8 + i;
+            for (int i = 0; i < TILE_ROWS; ++i) {
+                const int64_t r = r0 + rg * TILE_ROWS + i;
                 float t = amax8<T>(v[i], AMAX_MIN);
 #pragma unroll
                 for (int o = 8; o > 0; o >>= 1) t = fmaxf(t, __shfl_xor_sync(0xFFFFFFFFu, t, o));
@@ -173,49 +175,51 @@ quant_tile_kernel(const TileArgs a) {
                 }
             }
         }
+        __syncthreads();
+        const float4* from = reinterpret_cast<const float4*>(&col_inv[cg * 8]);
+        const float4 lo = from[0], hi = from[1];
+        inv_c[0] = lo.x; inv_c[1] = lo.y; inv_c[2] = lo.z; inv_c[3] = lo.w;
+        inv_c[4] = hi.x; inv_c[5] = hi.y; inv_c[6] = hi.z; inv_c[7] = hi.w;
     } else {
         float m = AMAX_MIN;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) m = amax8<T>(v[i], m);
+        for (int i = 0; i < TILE_ROWS; ++i) m = amax8<T>(v[i], m);
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
         if (lane == 0) part[0][warp] = m;
         __syncthreads();
 #pragma unroll
-        for (int i = 0; i < 8; ++i) m = fmaxf(m, part[0][i]);
+        for (int i = 0; i < TILE_WARPS; ++i) m = fmaxf(m, part[0][i]);
         if (tid == 0) a.s[(int64_t)blockIdx.y * gridDim.x + blockIdx.x] = scale_of(m);
         const float inv = inverse_of(m);
 #pragma unroll
         for (int j = 0; j < 8; ++j) inv_c[j] = inv;
         if (a.q && c < a.cols) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const int64_t r = r0 + rg * 8 + i;
+            for (int i = 0; i < TILE_ROWS; ++i) {
+                const int64_t r = r0 + rg * TILE_ROWS + i;
                 if (r < a.rows) *reinterpret_cast<uint2*>(a.q + r * a.ldq + c) = codes8<T>(v[i], inv);
             }
         }
     }
     if (!a.qt) return;
+    float w[TILE_ROWS][8];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        float t[8];
+    for (int i = 0; i < TILE_ROWS; ++i) row::widen<8>(v[i], w[i]);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            float w[8];
-            row::widen<8>(v[i], w);
-            t[i] = w[j];
-        }
-        *reinterpret_cast<uint2*>(&tile[(cg * 8 + j) * TPITCH + rg * 8]) = codes8(t, inv_c[j]);
-    }
+    for (int j = 0; j < 8; ++j)
+        tile[(cg * 8 + j) * 32 + (rg ^ (2 * cg))] =
+            (uint32_t)e4m3x2_from_float(__fmul_rn(w[0][j], inv_c[j]), __fmul_rn(w[1][j], inv_c[j])) |
+            ((uint32_t)e4m3x2_from_float(__fmul_rn(w[2][j], inv_c[j]), __fmul_rn(w[3][j], inv_c[j])) << 16);
     __syncthreads();
     // a column of the tile is 128 codes of one transposed row: 8 lanes of 16 bytes
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int col = i * 32 + (tid >> 3), piece = (tid & 7) * 16;
-        const int64_t r = r0 + piece;
-        if (c0 + col < a.cols && r < a.rows)
-            *reinterpret_cast<uint4*>(a.qt + (c0 + col) * a.ldqt + r) =
-                *reinterpret_cast<const uint4*>(&tile[col * TPITCH + piece]);
+    for (int i = 0; i < 2; ++i) {
+        const int col = i * 64 + (tid >> 3), g = tid & 7, x = col >> 3;
+        const int64_t r = r0 + g * 16;
+        uint4 q = *reinterpret_cast<const uint4*>(&tile[col * 32 + ((g ^ (x >> 1)) << 2)]);
+        if (x & 1) q = make_uint4(q.z, q.w, q.x, q.y);
+        if (c0 + col < a.cols && r < a.rows) *reinterpret_cast<uint4*>(a.qt + (c0 + col) * a.ldqt + r) = q;
     }
 }
 
@@ -240,8 +244,8 @@ int quant_rows_launch(int64_t rows, int64_t cols, int dtype, const void* x, int6
 template <int MODE, typename T>
 int tile_launch(const TileArgs& a, bool vec, cudaStream_t st) {
     const dim3 grid((unsigned)((a.cols + 127) / 128), (unsigned)((a.rows + 127) / 128));
-    if (vec) return launch_pdl(quant_tile_kernel<T, true, MODE>, grid, 256, 0, st, a);
-    return launch_pdl(quant_tile_kernel<T, false, MODE>, grid, 256, 0, st, a);
+    if (vec) return launch_pdl(quant_tile_kernel<T, true, MODE>, grid, TILE_THREADS, 0, st, a);
+    return launch_pdl(quant_tile_kernel<T, false, MODE>, grid, TILE_THREADS, 0, st, a);
 }
 template <int MODE>
 int tile_run(int dtype, const TileArgs& a, cudaStream_t st) {
