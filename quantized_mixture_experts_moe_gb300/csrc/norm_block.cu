@@ -87,8 +87,12 @@ norm_fwd_kernel(const FwdArgs a) {
         if (POST) col_factors();
         next_weights();
     }
+    // a row's own scalars are asked for one row early
+    const bool row_gate = POST && a.gate_mode == QMOE_GATE_ROW;
+    float g_next = row_gate && row < a.rows ? a.gate[row] : 1.f;
     for (; row < a.rows; row += stride) {
-        const float g_row = POST && a.gate_mode == QMOE_GATE_ROW ? a.gate[row] : 1.f;
+        const float g_row = g_next;
+        if (row_gate && row + stride < a.rows) g_next = a.gate[row + stride];
         const uint8_t* const from = ring.wait();
         bool met = false;
         float o[E];
@@ -184,16 +188,17 @@ struct Fwd {
     template <typename RT, typename YT>
     struct Go {
         static int go(FwdArgs& a, bool vec, cudaStream_t st) {
-            const Shape s = shape_of(a.cols, vec, 16);
+            constexpr int W = wide_vec<RT, YT>();
+            const Shape s = shape_of(a.cols, vec ? W : 1, 16);
             const int rb = stage_bytes(a.cols, sizeof(RT)), yb = stage_bytes(a.cols, sizeof(YT));
             a.y.off = rb;
             a.full_gate.off = rb + yb;
             const int bytes = rb + (POST ? yb : 0) + (a.full_gate.p ? yb : 0);
             if (vec) {
-                if (s.nv == 2) return start<norm_fwd_kernel<RT, YT, 2, 8, POST>>(s, a, bytes, st);
-                return start<norm_fwd_kernel<RT, YT, 4, 8, POST>>(s, a, bytes, st);
+                if (s.values() == 16) return start<norm_fwd_kernel<RT, YT, 16 / W, W, POST>>(s, a, bytes, st);
+                return start<norm_fwd_kernel<RT, YT, 32 / W, W, POST>>(s, a, bytes, st);
             }
-            if (s.nv == 16) return start<norm_fwd_kernel<RT, YT, 16, 1, POST>>(s, a, bytes, st);
+            if (s.values() == 16) return start<norm_fwd_kernel<RT, YT, 16, 1, POST>>(s, a, bytes, st);
             return start<norm_fwd_kernel<RT, YT, 32, 1, POST>>(s, a, bytes, st);
         }
     };

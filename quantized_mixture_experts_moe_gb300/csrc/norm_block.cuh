@@ -23,9 +23,15 @@ struct Shape {
     int values() const { return vec * nv; }
 };
 
-inline Shape shape_of(int64_t cols, bool vec, int values) {
+// vec: the columns of one access (8 where all matrices are 16-bit; 4 beside an
+// fp32 one, so that its lanes' 16 bytes touch; 1 for rows off the 16-byte
+// boundaries).
+template <typename RT, typename YT>
+constexpr int wide_vec() { return sizeof(RT) == 4 || sizeof(YT) == 4 ? 4 : 8; }
+
+inline Shape shape_of(int64_t cols, int vec, int values) {
     Shape s;
-    s.vec = vec ? 8 : 1;
+    s.vec = vec;
     for (;; values *= 2) {
         s.nv = values / s.vec;
         const int64_t per = (cols + values - 1) / values;
@@ -72,7 +78,7 @@ __device__ __forceinline__ uint32_t send_row(const Source& s, uint8_t* stage, in
     if (!s.p) return 0;
     const T* src = static_cast<const T*>(s.p) + row * s.ld;
     uint8_t* dst = stage + s.off;
-    if constexpr (VEC == 8) {
+    if constexpr (VEC > 1) {
         tc::bulk_load(dst, src, cols * sizeof(T), bar);
         return cols * sizeof(T);
     } else {

@@ -139,10 +139,18 @@ norm_bwd_kernel(const BwdArgs a) {
         row::load<VEC>(W_SMEM ? cols_smem + c : a.w_next + c, wn);
         return wn;
     };
+    // a row's own scalars are asked for one row early
+    float rstd_n_ahead = 0.f, rstd_ahead = 1.f, g_ahead = 1.f;
+    auto ahead = [&](int64_t r) {
+        if (r >= a.rows) return;
+        if (next) rstd_n_ahead = a.rstd_next[r];
+        if (POST && a.w) rstd_ahead = a.rstd[r];
+        if (POST && a.gate_mode == QMOE_GATE_ROW) g_ahead = a.gate[r];
+    };
+    ahead(row);
     for (; row < a.rows; row += stride) {
-        const float rstd_n = next ? a.rstd_next[row] : 0.f;
-        const float rstd = POST && a.w ? a.rstd[row] : 1.f;
-        const float g_row = POST && a.gate_mode == QMOE_GATE_ROW ? a.gate[row] : 1.f;
+        const float rstd_n = rstd_n_ahead, rstd = rstd_ahead, g_row = g_ahead;
+        ahead(row + stride);
         const uint8_t* const from = RING ? ring.wait() : nullptr;
         bool met = false;
         auto meet = [&] {  // the row's threads have met: what the last row's stage held is free
@@ -310,13 +318,9 @@ inline int64_t bwd_ctas(const Shape& s, int64_t rows) {
     return ctas < fit ? ctas : fit;
 }
 inline int64_t part_rows(int64_t rows, int64_t cols) {
-    int64_t most = 1;
-    for (int vec = 0; vec < 2; ++vec) {
-        const Shape s = shape_of(cols, vec != 0, 8);
-        const int64_t n = bwd_ctas(s, rows) * s.rows_per_cta;
-        most = n > most ? n : most;
-    }
-    return most;
+    // the cut goes by the columns alone, not by the access
+    const Shape s = shape_of(cols, 1, 8);
+    return bwd_ctas(s, rows) * s.rows_per_cta > 0 ? bwd_ctas(s, rows) * s.rows_per_cta : 1;
 }
 
 template <auto Kernel>
@@ -340,7 +344,10 @@ template <bool POST>
 struct Bwd {
     template <typename RT, typename YT>
     struct Go {
-        static int go(BwdArgs& a, const Shape& s, int64_t ctas, cudaStream_t st) {
+        static int go(BwdArgs& a, bool vec, cudaStream_t st) {
+            constexpr int W = wide_vec<RT, YT>();
+            const Shape s = shape_of(a.cols, vec ? W : 1, 8);
+            const int64_t ctas = bwd_ctas(s, a.rows);
             const int rb = stage_bytes(a.cols, sizeof(RT)), yb = stage_bytes(a.cols, sizeof(YT));
             int at = 0;
             auto place = [&](Source& src, int bytes) {
@@ -353,13 +360,13 @@ struct Bwd {
             place(a.y, yb);
             place(a.full_gate, yb);
             constexpr int sums = POST ? 3 : 1;
-            if (s.vec == 8) {
-                if (s.nv == 1) return start<norm_bwd_kernel<RT, YT, 1, 8, POST>>(s, a, sums, at, ctas, st);
-                if (s.nv == 2) return start<norm_bwd_kernel<RT, YT, 2, 8, POST>>(s, a, sums, at, ctas, st);
-                return start<norm_bwd_kernel<RT, YT, 4, 8, POST>>(s, a, sums, at, ctas, st);
+            if (vec) {
+                if (s.values() == 8) return start<norm_bwd_kernel<RT, YT, 8 / W, W, POST>>(s, a, sums, at, ctas, st);
+                if (s.values() == 16) return start<norm_bwd_kernel<RT, YT, 16 / W, W, POST>>(s, a, sums, at, ctas, st);
+                return start<norm_bwd_kernel<RT, YT, 32 / W, W, POST>>(s, a, sums, at, ctas, st);
             }
-            if (s.nv == 8) return start<norm_bwd_kernel<RT, YT, 8, 1, POST>>(s, a, sums, at, ctas, st);
-            if (s.nv == 16) return start<norm_bwd_kernel<RT, YT, 16, 1, POST>>(s, a, sums, at, ctas, st);
+            if (s.values() == 8) return start<norm_bwd_kernel<RT, YT, 8, 1, POST>>(s, a, sums, at, ctas, st);
+            if (s.values() == 16) return start<norm_bwd_kernel<RT, YT, 16, 1, POST>>(s, a, sums, at, ctas, st);
             return start<norm_bwd_kernel<RT, YT, 32, 1, POST>>(s, a, sums, at, ctas, st);
         }
     };
@@ -371,10 +378,10 @@ template <template <typename, typename> class F>
 inline int run(BwdArgs& a, int rt, int yt, bool vec, float* const (&out)[3], void* ws, cudaStream_t st) {
     a.part = static_cast<float*>(ws);
     a.part_rows = part_rows(a.rows, a.cols);
-    const Shape s = shape_of(a.cols, vec, 8);
+    const Shape s = shape_of(a.cols, 1, 8);
     const int64_t ctas = bwd_ctas(s, a.rows);
     if (ctas > 0) {
-        const int rc = by_types<F>(rt, yt, a, s, ctas, st);
+        const int rc = by_types<F>(rt, yt, a, vec, st);
         if (rc != QMOE_OK) return rc;
     }
     if (!out[0] && !out[1] && !out[2]) return QMOE_OK;

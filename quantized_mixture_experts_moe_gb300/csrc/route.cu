@@ -9,13 +9,16 @@
 //
 // A warp takes a token at a time, its logits spread over the lanes' registers
 // (by 16-byte loads where rows allow it), so a row is read once for the
-// softmax, the selection and the statistics.  Selection is k rounds of a
-// warp-wide maximum over order-preserving integer keys, the lowest expert first
-// among equal keys; a 16-bit logit's key leaves room for the expert's number,
-// so one redux gives both.  These rounds, not the 2 E bytes of a row, are the
-// bound: instruction issue and the latency of redux.  Probabilities are summed
-// per lane over a warp's tokens, then over a CTA's warps, then over CTAs, in a
-// fixed order.
+// softmax, the selection and the statistics.  Selection goes by
+// order-preserving integer keys from the largest down: the next key is the
+// largest below the last one, a warp-wide maximum of key - last, which wraps
+// so that what has been taken falls to the bottom (one fused add-and-maximum
+// for each register, nothing to clear).  A 16-bit logit's key leaves room for
+// the expert's number, so one redux gives both and equal logits come lowest
+// expert first; 32-bit scores are looked up by value, and all experts of one
+// value leave in ascending order.  Instruction issue, not the 2 E bytes of a
+// row, is the bound.  Probabilities are summed per lane over a warp's tokens,
+// then over a CTA's warps, then over CTAs, in a fixed order.
 #include "row_ops.cuh"
 
 namespace qmoe {
@@ -50,44 +53,35 @@ struct Args {
 
 // NaN counts as -inf (an invalid logit selects nothing), +inf as the largest
 // finite value.
-__device__ __forceinline__ float clean(float v) { return v > -INFINITY ? fminf(v, 3.402823466e38f) : -INFINITY; }
+constexpr float LARGEST = 3.402823466e38f;
+__device__ __forceinline__ float clean(float v) { return v > -INFINITY ? fminf(v, LARGEST) : -INFINITY; }
 
-// Larger floats have larger keys; -0 and +0 have the same.  16-bit types: the
-// bits' order alone, in the upper half.
+// Larger floats have larger keys; -0 and +0 have the same.  Keys below
+// AVAILABLE are -inf's.
+constexpr uint32_t AVAILABLE = 0x00800000u;
 __device__ __forceinline__ uint32_t key_of(float v) {
-    const uint32_t u = __float_as_uint(v == 0.f ? 0.f : v);
-    return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
+    const uint32_t u = __float_as_uint(v + 0.f);
+    return u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u);
 }
 __device__ __forceinline__ float value_of(uint32_t key) {
     return __uint_as_float((key & 0x80000000u) ? (key & 0x7FFFFFFFu) : ~key);
 }
-template <typename T> __device__ __forceinline__ uint32_t bits16(float v);
-template <> __device__ __forceinline__ uint32_t bits16<__nv_bfloat16>(float v) {
-    return __bfloat16_as_ushort(__float2bfloat16_rn(v));
-}
-template <> __device__ __forceinline__ uint32_t bits16<__half>(float v) { return __half_as_ushort(__float2half_rn(v)); }
-template <typename T> __device__ __forceinline__ float from16(uint32_t u);
-template <> __device__ __forceinline__ float from16<__nv_bfloat16>(uint32_t u) { return __uint_as_float(u << 16); }
-template <> __device__ __forceinline__ float from16<__half>(uint32_t u) {
-    return __half2float(__ushort_as_half((unsigned short)u));
-}
-
-// The keys of a lane's experts and the k rounds.  PACK: 16-bit logits without
-// a bias, key = order of the 16 bits << 16 | (0xFFFF - expert), 0 for a gone or
-// unavailable expert; else key = 32-bit order of the score, where -inf has
-// 0x007FFFFF.
-
-template <typename T>
+// A bf16 or fp16 value is told by the upper 19 bits of its fp32 form (8 of
+// exponent, at most 10 of mantissa): below them goes the expert, reversed.
+constexpr uint32_t VALUE_BITS = 0xFFFFE000u;
 __device__ __forceinline__ uint32_t packed_key(float v, int e) {
-    if (!(v > -INFINITY)) return 0u;
-    uint32_t u = bits16<T>(v == 0.f ? 0.f : v);
-    u = (u & 0x8000u) ? (u ^ 0xFFFFu) : (u | 0x8000u);
-    return (u << 16) | (0xFFFFu - (uint32_t)e);
+    return (key_of(v) & VALUE_BITS) | (0x1FFFu - (uint32_t)e);
 }
-template <typename T>
+__device__ __forceinline__ int packed_expert(uint32_t key) { return (int)(0x1FFFu - (key & 0x1FFFu)); }
 __device__ __forceinline__ float packed_value(uint32_t key) {
-    const uint32_t u = key >> 16;
-    return from16<T>((u & 0x8000u) ? (u & 0x7FFFu) : (u ^ 0xFFFFu));
+    return __uint_as_float(((key & 0x80000000u) ? (key & 0x7FFFFFFFu) : ~key) & VALUE_BITS);
+}
+
+using row::warp_sum;
+__device__ __forceinline__ float warp_max(float v) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, o));
+    return v;
 }
 
 // Which experts a lane holds: value i is expert (i / V) 32 V + lane V + i % V.
@@ -99,28 +93,28 @@ __device__ __forceinline__ int expert_of(int i, int lane) {
 // A row's logits, cleaned; -inf past the last expert.
 template <typename T, int NE, int V>
 __device__ __forceinline__ void load_logits(const T* row, int E, int lane, float (&v)[NE]) {
+    bool fine = true;
 #pragma unroll
     for (int i = 0; i < NE; i += V) {
         const int e = expert_of<V>(i, lane);
         if (V == 1) {
-            v[i] = e < E ? clean(row::to_f32(row[e])) : -INFINITY;
+            v[i] = e < E ? row::to_f32(row[e]) : -INFINITY;
         } else if (e < E) {
             struct alignas(sizeof(T) * V) Pack { T x[V]; };
             const Pack p = *reinterpret_cast<const Pack*>(row + e);
 #pragma unroll
-            for (int j = 0; j < V; ++j) v[i + j] = clean(row::to_f32(p.x[j]));
+            for (int j = 0; j < V; ++j) v[i + j] = row::to_f32(p.x[j]);
         } else {
 #pragma unroll
             for (int j = 0; j < V; ++j) v[i + j] = -INFINITY;
         }
     }
-}
-
-using row::warp_sum;
-__device__ __forceinline__ float warp_max(float v) {
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, o));
-    return v;
+    for (int i = 0; i < NE; ++i) fine = fine && v[i] <= LARGEST;
+    if (!fine) {
+#pragma unroll
+        for (int i = 0; i < NE; ++i) v[i] = clean(v[i]);
+    }
 }
 
 template <typename T, int NE, int V, bool PACK>
@@ -159,7 +153,7 @@ route_kernel(const Args a) {
 #pragma unroll
         for (int i = 0; i < NE; ++i) {
             const int e = expert_of<V>(i, lane);
-            if constexpr (PACK) key[i] = packed_key<T>(v[i], e);
+            if constexpr (PACK) key[i] = packed_key(v[i], e);
             else key[i] = e < E ? key_of(a.bias ? clean(v[i] + a.bias[e]) : v[i]) : 0u;
         }
         float sum = 0.f;
@@ -174,39 +168,44 @@ route_kernel(const Args a) {
 #pragma unroll
             for (int i = 0; i < NE; ++i) psum[i] = fmaf(v[i], inv, psum[i]);
         }
-        int mine = -1;  // lane j: the expert of rank j, and its key
-        uint32_t my_key = 0;
-        for (int j = 0; j < a.k; ++j) {
-            uint32_t best = key[0];
+        // lane j: the expert of rank j and its key
+        int mine = -1;
+        uint32_t my_key = 0, last = 0;  // key - 0: at first all keys are below
+        for (int j = 0; j < a.k;) {
+            uint32_t best = 0;
 #pragma unroll
-            for (int i = 1; i < NE; ++i) best = max(best, key[i]);
-            const uint32_t top = __reduce_max_sync(0xFFFFFFFFu, best);
-            int win;
+            for (int i = 0; i < NE; ++i) best = __viaddmax_u32(key[i], 0u - last, best);
+            const uint32_t top = __reduce_max_sync(0xFFFFFFFFu, best) + last;
+            if (top < AVAILABLE || (last != 0 && top >= last)) break;  // nothing left
+            last = top;
             if constexpr (PACK) {
-                if (top == 0u) break;
-                win = 0xFFFF - (int)(top & 0xFFFFu);
+                if (lane == j) {
+                    mine = packed_expert(top);
+                    my_key = top;
+                }
+                ++j;
             } else {
-                if (top <= 0x007FFFFFu) break;
-                unsigned at = 0x7FFFFFFFu;
+                uint32_t here = 0;  // which of this lane's experts have this score
 #pragma unroll
-                for (int i = NE - 1; i >= 0; --i)
-                    if (key[i] == top) at = expert_of<V>(i, lane);
-                win = (int)__reduce_min_sync(0xFFFFFFFFu, at);
+                for (int i = 0; i < NE; ++i) here |= key[i] == top ? 1u << i : 0u;
+                while (j < a.k) {
+                    const int i = __ffs(here) - 1;
+                    const unsigned e = here ? (unsigned)expert_of<V>(i, lane) : 0x7FFFFFFFu;
+                    const unsigned win = __reduce_min_sync(0xFFFFFFFFu, e);
+                    if (win == 0x7FFFFFFFu) break;
+                    if (e == win) here &= here - 1;
+                    if (lane == j) {
+                        mine = (int)win;
+                        my_key = top;
+                    }
+                    ++j;
+                }
             }
-            if (lane == j) {
-                mine = win;
-                my_key = top;
-            }
-            // the winner leaves: its register is the same in every lane, its lane is not
-            const int reg = (win / (32 * V)) * V + win % V;
-            const bool owner = (win / V) % 32 == lane;
-#pragma unroll
-            for (int i = 0; i < NE; ++i)
-                if (i == reg && owner) key[i] = 0u;
         }
         float l = -INFINITY;
         if (mine >= 0) {
-            if constexpr (PACK) l = clean(packed_value<T>(my_key));
+            // beside a bias the key is not the logit's: read that again (it is in L1)
+            if constexpr (PACK) l = packed_value(my_key);
             else l = a.bias ? clean(row::to_f32(row[mine])) : value_of(my_key);
         }
         float w;

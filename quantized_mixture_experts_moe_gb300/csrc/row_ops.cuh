@@ -57,16 +57,20 @@ __device__ __forceinline__ uint32_t pack2(float a, float b, __half) {
 }
 
 // VEC consecutive values as they lie in memory: loaded early, widened when
-// they are used.  VEC = 8 needs a 16-byte aligned address.
+// they are used.  VEC = 4 and 8 need an address aligned to their bytes, up to 16.
 template <typename T, int VEC> struct Raw { T v; };
 template <typename T> struct Raw<T, 8> { uint4 v; };
+template <typename T> struct Raw<T, 4> { uint2 v; };
 template <> struct Raw<float, 8> { float4 a, b; };
+template <> struct Raw<float, 4> { float4 a; };
 
 template <int VEC>
 __device__ __forceinline__ void load_raw(Raw<float, VEC>& r, const float* p) {
     if constexpr (VEC == 8) {
         r.a = reinterpret_cast<const float4*>(p)[0];
         r.b = reinterpret_cast<const float4*>(p)[1];
+    } else if constexpr (VEC == 4) {
+        r.a = reinterpret_cast<const float4*>(p)[0];
     } else {
         r.v = p[0];
     }
@@ -74,6 +78,7 @@ __device__ __forceinline__ void load_raw(Raw<float, VEC>& r, const float* p) {
 template <int VEC, typename T>
 __device__ __forceinline__ void load_raw(Raw<T, VEC>& r, const T* p) {
     if constexpr (VEC == 8) r.v = *reinterpret_cast<const uint4*>(p);
+    else if constexpr (VEC == 4) r.v = *reinterpret_cast<const uint2*>(p);
     else r.v = p[0];
 }
 template <int VEC>
@@ -81,6 +86,8 @@ __device__ __forceinline__ void widen(const Raw<float, VEC>& r, float* v) {
     if constexpr (VEC == 8) {
         v[0] = r.a.x; v[1] = r.a.y; v[2] = r.a.z; v[3] = r.a.w;
         v[4] = r.b.x; v[5] = r.b.y; v[6] = r.b.z; v[7] = r.b.w;
+    } else if constexpr (VEC == 4) {
+        v[0] = r.a.x; v[1] = r.a.y; v[2] = r.a.z; v[3] = r.a.w;
     } else {
         v[0] = r.v;
     }
@@ -95,6 +102,9 @@ __device__ __forceinline__ void widen(const Raw<T, VEC>& r, float* v) {
             v[2 * i] = f.x;
             v[2 * i + 1] = f.y;
         }
+    } else if constexpr (VEC == 4) {
+        const float2 f = unpack2(r.v.x, T{}), g = unpack2(r.v.y, T{});
+        v[0] = f.x; v[1] = f.y; v[2] = g.x; v[3] = g.y;
     } else {
         v[0] = to_f32(r.v);
     }
@@ -110,6 +120,8 @@ __device__ __forceinline__ void store(float* p, const float* v) {
     if constexpr (VEC == 8) {
         reinterpret_cast<float4*>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
         reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
+    } else if constexpr (VEC == 4) {
+        reinterpret_cast<float4*>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
     } else {
         p[0] = v[0];
     }
@@ -119,6 +131,8 @@ __device__ __forceinline__ void store(T* p, const float* v) {
     if constexpr (VEC == 8) {
         *reinterpret_cast<uint4*>(p) = make_uint4(pack2(v[0], v[1], T{}), pack2(v[2], v[3], T{}),
                                                   pack2(v[4], v[5], T{}), pack2(v[6], v[7], T{}));
+    } else if constexpr (VEC == 4) {
+        *reinterpret_cast<uint2*>(p) = make_uint2(pack2(v[0], v[1], T{}), pack2(v[2], v[3], T{}));
     } else {
         p[0] = from_f32<T>(v[0]);
     }
