@@ -35,7 +35,7 @@ __global__ void __launch_bounds__(512, 1)
 norm_fwd_kernel(const FwdArgs a) {
     constexpr int E = NV * VEC;
     constexpr bool KEEP = E <= 16;  // the weights stay in registers from row to row
-    __shared__ __align__(16) float sums[2][16];
+    __shared__ __align__(16) float sums[2][2][16];
     __shared__ uint64_t full[MAX_ROWS][MAX_STAGES];
     extern __shared__ __align__(128) uint8_t dynamic[];
     const int tx = threadIdx.x, cols = a.cols;
@@ -43,19 +43,18 @@ norm_fwd_kernel(const FwdArgs a) {
     const float inv_cols = 1.f / (float)cols;
     int flip = 0;
 
-    auto ring = make_ring(full[threadIdx.y], dynamic + (int64_t)threadIdx.y * a.stages * a.stage_bytes, a.stages,
-                          a.stage_bytes, a.rows, stride, tx == 0, [&](int64_t row, uint8_t* to, uint64_t* bar) {
-                              uint32_t n = send_row<VEC, RT>(a.r, to, row, a.rows, cols, bar);
-                              if (POST) n += send_row<VEC, YT>(a.y, to, row, a.rows, cols, bar);
-                              if (POST) n += send_row<VEC, YT>(a.full_gate, to, row, a.rows, cols, bar);
-                              return n;
-                          });
+    int64_t row = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
+    Ring<VEC> ring = {full[threadIdx.y], dynamic + (int64_t)threadIdx.y * a.stages * a.stage_bytes, a.stages,
+                      a.stage_bytes, a.rows, stride};
+    int matrices = 0;
+    ring.feed.take(a.r, sizeof(RT), matrices, tx, row, stride, cols);
+    if (POST) ring.feed.take(a.y, sizeof(YT), matrices, tx, row, stride, cols);
+    if (POST) ring.feed.take(a.full_gate, sizeof(YT), matrices, tx, row, stride, cols);
     if (tx == 0)
-        for (int i = 0; i < MAX_STAGES; ++i) tc::mbar_init(&full[threadIdx.y][i], 1);
-    if (tx < 32) sums[tx >> 4][tx & 15] = 0.f;
+        for (int i = 0; i < MAX_STAGES; ++i) tc::mbar_init(&full[threadIdx.y][i], matrices);
+    for (int i = tx; i < 64; i += blockDim.x) (&sums[0][0][0])[i] = 0.f;
     tc::fence_barrier_init();
     __syncthreads();
-    int64_t row = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
     pdl_sync();
     ring.begin(row);
     // what a column of y and of out is multiplied by: w and a column gate in one

@@ -71,31 +71,48 @@ inline int stages_of(int64_t bytes_per_stage, int64_t other_bytes, int ctas_per_
     return n > MAX_STAGES ? MAX_STAGES : n > 0 ? (int)n : 0;
 }
 
-// Sends for one row of a matrix; returns the bytes that the barrier will count.
-template <int VEC, typename T>
-__device__ __forceinline__ uint32_t send_row(const Source& s, uint8_t* stage, int64_t row, int64_t rows, int cols,
-                                             uint64_t* bar) {
-    if (!s.p) return 0;
-    const T* src = static_cast<const T*>(s.p) + row * s.ld;
-    uint8_t* dst = stage + s.off;
-    if constexpr (VEC > 1) {
-        tc::bulk_load(dst, src, cols * sizeof(T), bar);
-        return cols * sizeof(T);
-    } else {
-        const uintptr_t g0 = reinterpret_cast<uintptr_t>(src), g1 = g0 + (uintptr_t)cols * sizeof(T);
-        const uintptr_t base = g0 & ~uintptr_t(15);
-        uintptr_t a0 = base, a1 = (g1 + 15) & ~uintptr_t(15);
-        if (row == 0 && a0 < g0) a0 += 16;
-        if (row == rows - 1 && a1 > g1) a1 -= 16;
-        if (a1 < a0) a1 = a0;  // a row within one granule
-        for (uintptr_t b = g0; b < a0 && b < g1; b += sizeof(T))
-            *reinterpret_cast<T*>(dst + (b - base)) = *reinterpret_cast<const T*>(b);
-        for (uintptr_t b = a1 > g0 ? a1 : g0; b < g1; b += sizeof(T))
-            *reinterpret_cast<T*>(dst + (b - base)) = *reinterpret_cast<const T*>(b);
-        if (a1 > a0) tc::bulk_load(dst + (a0 - base), reinterpret_cast<const void*>(a0), (uint32_t)(a1 - a0), bar);
-        return (uint32_t)(a1 - a0);
+// One thread's part in filling the ring: the rows of one matrix.
+struct Feed {
+    const uint8_t* p = nullptr;  // the next row to send for (null: this thread has no matrix)
+    int64_t step = 0;            // bytes from one row of this ring to the next
+    int off = 0, bytes = 0;      // its place in a stage; the bytes of a row
+
+    __device__ __forceinline__ void take(const Source& s, int size, int& turn, int id, int64_t row, int64_t stride,
+                                         int cols) {
+        if (!s.p) return;
+        if (turn++ == id) {
+            p = static_cast<const uint8_t*>(s.p) + row * s.ld * size;
+            step = stride * s.ld * size;
+            off = s.off;
+            bytes = cols * size;
+        }
     }
-}
+    // Sends for row `row` of `rows` and tells the barrier.
+    template <int VEC>
+    __device__ __forceinline__ void send(uint8_t* stage, int64_t row, int64_t rows, uint64_t* bar) {
+        uint8_t* dst = stage + off;
+        if constexpr (VEC > 1) {
+            tc::mbar_arrive_expect_tx(bar, bytes);
+            tc::bulk_load(dst, p, bytes, bar);
+        } else {
+            const uintptr_t g0 = reinterpret_cast<uintptr_t>(p), g1 = g0 + (uintptr_t)bytes;
+            const uintptr_t base = g0 & ~uintptr_t(15);
+            uintptr_t a0 = base, a1 = (g1 + 15) & ~uintptr_t(15);
+            if (row == 0 && a0 < g0) a0 += 16;
+            if (row == rows - 1 && a1 > g1) a1 -= 16;
+            if (a1 < a0) a1 = a0;  // a row within one granule
+            auto one_by_one = [&](uintptr_t b, uintptr_t e) {
+                for (; b < e; b += 2)  // values are 2 or 4 bytes, aligned
+                    *reinterpret_cast<uint16_t*>(dst + (b - base)) = *reinterpret_cast<const uint16_t*>(b);
+            };
+            if (a0 > g0) one_by_one(g0, a0 < g1 ? a0 : g1);
+            if (a1 < g1) one_by_one(a1 > g0 ? a1 : g0, g1);
+            tc::mbar_arrive_expect_tx(bar, (uint32_t)(a1 - a0));
+            if (a1 > a0) tc::bulk_load(dst + (a0 - base), reinterpret_cast<const void*>(a0), (uint32_t)(a1 - a0), bar);
+        }
+        p += step;
+    }
+};
 
 // This thread's values of a row, widened; zeros past the row's end.  RING: from
 // a stage; else straight from the matrix.
@@ -115,30 +132,34 @@ __device__ __forceinline__ void read_row(const Source& s, const uint8_t* stage, 
     }
 }
 
-// The ring of one row's threads.  send(row, stage, barrier) issues a row's
-// copies and returns their bytes; one thread calls it.  A stage is refilled
-// when its row's threads have met once more after reading it (refill).
-template <typename Send>
+// The ring of one row's threads.  Its first threads send, each for the rows of
+// one matrix (one thread that sent for all of them took 1,100 cycles a row, and
+// the others waited for it at the row's next barrier).  A stage is refilled
+// when its row's threads have met once more after reading it.
+template <int VEC>
 struct Ring {
     uint64_t* full;
     uint8_t* base;
     int stages, bytes;
     int64_t rows, stride;
-    bool lead;
-    Send send;
+    Feed feed;
     int stage = 0;
     uint32_t phase = 0;
     bool lost = false;  // a copy did not arrive in time: what follows is NaN
 
     __device__ __forceinline__ void post(int64_t row, int at) {
-        if (lead && row < rows) tc::mbar_arrive_expect_tx(&full[at], send(row, base + at * bytes, &full[at]));
+        if (feed.p && row < rows) feed.template send<VEC>(base + at * bytes, row, rows, &full[at]);
     }
     __device__ __forceinline__ void begin(int64_t row) {
         for (int i = 0; i + 1 < stages || i == 0; ++i) post(row + i * stride, i);
     }
-    // The stage of the present row.
+    // The stage of the present row.  One lane of a warp waits (32 lanes that ask the same barrier are served one by
+    // one); __syncwarp passes on to the others what it guards.
     __device__ __forceinline__ const uint8_t* wait() {
-        if (!lost && !tc::mbar_wait(&full[stage], phase)) lost = true;
+        int late = 0;
+        if ((threadIdx.x & 31) == 0 && !lost) late = !tc::mbar_wait(&full[stage], phase);
+        lost = lost || __shfl_sync(0xFFFFFFFFu, late, 0);
+        __syncwarp();
         return base + stage * bytes;
     }
     // The row's threads have met since `row` was waited for: the stage read before it is free.
@@ -152,11 +173,6 @@ struct Ring {
         }
     }
 };
-template <typename Send>
-__device__ __forceinline__ Ring<Send> make_ring(uint64_t* full, uint8_t* base, int stages, int bytes, int64_t rows,
-                                                int64_t stride, bool lead, Send send) {
-    return Ring<Send>{full, base, stages, bytes, rows, stride, lead, send};
-}
 
 // The threads of a row meet.
 __device__ __forceinline__ void row_barrier() {

@@ -76,7 +76,7 @@ __global__ void __launch_bounds__(512, 1)
 norm_bwd_kernel(const BwdArgs a) {
     constexpr int E = NV * VEC;
     constexpr bool SMEM = E > 16, RING = !SMEM, KEEP = E <= 8, W_SMEM = E == 16;
-    __shared__ __align__(16) float sums[2][16];
+    __shared__ __align__(16) float sums[2][2][16];
     __shared__ uint64_t full[MAX_ROWS][MAX_STAGES];
     extern __shared__ __align__(128) uint8_t dynamic[];  // the ring; column sums or weights [w_next, w]
     const int tx = threadIdx.x, cols = a.cols;
@@ -92,21 +92,20 @@ norm_bwd_kernel(const BwdArgs a) {
         sum_w.init(cols_smem + E * blockDim.x);
         sum_g.init(cols_smem + 2 * E * blockDim.x);
     }
-    auto ring = make_ring(full[threadIdx.y], dynamic + (int64_t)threadIdx.y * a.stages * a.stage_bytes, a.stages,
-                          a.stage_bytes, a.rows, stride, tx == 0, [&](int64_t row, uint8_t* to, uint64_t* bar) {
-                              uint32_t n = send_row<VEC, RT>(a.dout, to, row, a.rows, cols, bar);
-                              n += send_row<VEC, YT>(a.dn, to, row, a.rows, cols, bar);
-                              n += send_row<VEC, RT>(a.out, to, row, a.rows, cols, bar);
-                              if (POST) n += send_row<VEC, YT>(a.y, to, row, a.rows, cols, bar);
-                              if (POST) n += send_row<VEC, YT>(a.full_gate, to, row, a.rows, cols, bar);
-                              return n;
-                          });
+    int64_t row = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
+    Ring<VEC> ring = {full[threadIdx.y], dynamic + (int64_t)threadIdx.y * a.stages * a.stage_bytes, a.stages,
+                      a.stage_bytes, a.rows, stride};
+    int matrices = 0;
+    ring.feed.take(a.dout, sizeof(RT), matrices, tx, row, stride, cols);
+    ring.feed.take(a.dn, sizeof(YT), matrices, tx, row, stride, cols);
+    ring.feed.take(a.out, sizeof(RT), matrices, tx, row, stride, cols);
+    if (POST) ring.feed.take(a.y, sizeof(YT), matrices, tx, row, stride, cols);
+    if (POST) ring.feed.take(a.full_gate, sizeof(YT), matrices, tx, row, stride, cols);
     if (RING && tx == 0)
-        for (int i = 0; i < MAX_STAGES; ++i) tc::mbar_init(&full[threadIdx.y][i], 1);
-    if (tx < 32) sums[tx >> 4][tx & 15] = 0.f;
+        for (int i = 0; i < MAX_STAGES; ++i) tc::mbar_init(&full[threadIdx.y][i], matrices);
+    for (int i = tx; i < 64; i += blockDim.x) (&sums[0][0][0])[i] = 0.f;
     tc::fence_barrier_init();
     __syncthreads();
-    int64_t row = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
     pdl_sync();
     if (RING) ring.begin(row);
     float w[KEEP ? E : VEC], wn[KEEP ? E : VEC], gc[KEEP ? E : VEC];
@@ -234,16 +233,19 @@ norm_bwd_kernel(const BwdArgs a) {
                 if (a.gate_mode == QMOE_GATE_FULL)
                     row::store<VEC>(static_cast<YT*>(a.dgate) + row * a.lddg + c, dg);
             }
-            if (a.gate_mode == QMOE_GATE_ROW) {
-                s_gate = row::row_sum(s_gate, sums[flip]);
+            if (a.w || a.gate_mode == QMOE_GATE_ROW) {
+                if (a.gate_mode == QMOE_GATE_ROW) {
+                    const float2 both = row::row_sums<true>(s, s_gate, sums[flip]);
+                    s = both.x;
+                    if (tx == 0) static_cast<float*>(a.dgate)[row] = both.y;
+                } else {
+                    s = row::row_sum(s, sums[flip]);
+                }
                 flip ^= 1;
                 meet();
-                if (tx == 0) static_cast<float*>(a.dgate)[row] = s_gate;
+                s *= inv_cols;
             }
             if (a.w) {
-                s = row::row_sum(s, sums[flip]) * inv_cols;
-                flip ^= 1;
-                meet();
 #pragma unroll
                 for (int e = 0; e < E; ++e) d[e] = rstd * (d[e] - t[e] * s);
             }

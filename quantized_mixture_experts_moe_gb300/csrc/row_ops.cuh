@@ -143,25 +143,35 @@ __device__ __forceinline__ float warp_sum(float v) {
     for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
     return v;
 }
-// Sum of v over the threads of a row: the lanes of a warp where the row has 32
-// threads, else the whole CTA (blockDim.x <= 512 threads).  `buf` is one of the
-// two halves of a 2 x 16 float array, zeroed before the first sum and
-// alternated by the caller, so that one barrier per sum is enough.  The order
-// is fixed.
-__device__ __forceinline__ float row_sum(float v, float (&buf)[16]) {
-    v = warp_sum(v);
-    if (blockDim.x == 32) return v;
-    if ((threadIdx.x & 31) == 0) buf[threadIdx.x >> 5] = v;
-    __syncthreads();
-    const float4* part = reinterpret_cast<const float4*>(buf);
-    const float4 p = part[0], q = part[1];
-    v = ((p.x + p.y) + (p.z + p.w)) + ((q.x + q.y) + (q.z + q.w));
-    if (blockDim.x > 256) {
-        const float4 r = part[2], s = part[3];
-        v += ((r.x + r.y) + (r.z + r.w)) + ((s.x + s.y) + (s.z + s.w));
+// Sums of a (and of b where TWO) over the threads of a row: the lanes of a warp
+// where the row has 32 threads, else the whole CTA (blockDim.x <= 512 threads).
+// `buf` is one of the two halves of a 2 x 2 x 16 float array, zeroed before the
+// first sum and alternated by the caller, so that one barrier is enough.  The
+// order is fixed.
+template <bool TWO>
+__device__ __forceinline__ float2 row_sums(float a, float b, float (&buf)[2][16]) {
+    a = warp_sum(a);
+    if (TWO) b = warp_sum(b);
+    if (blockDim.x == 32) return make_float2(a, b);
+    if ((threadIdx.x & 31) == 0) {
+        buf[0][threadIdx.x >> 5] = a;
+        if (TWO) buf[1][threadIdx.x >> 5] = b;
     }
-    return v;
+    __syncthreads();
+    float sum[2] = {0.f, 0.f};
+#pragma unroll
+    for (int i = 0; i < (TWO ? 2 : 1); ++i) {
+        const float4* part = reinterpret_cast<const float4*>(buf[i]);
+        const float4 p = part[0], q = part[1];
+        sum[i] = ((p.x + p.y) + (p.z + p.w)) + ((q.x + q.y) + (q.z + q.w));
+        if (blockDim.x > 256) {
+            const float4 r = part[2], s = part[3];
+            sum[i] += ((r.x + r.y) + (r.z + r.w)) + ((s.x + s.y) + (s.z + s.w));
+        }
+    }
+    return make_float2(sum[0], sum[1]);
 }
+__device__ __forceinline__ float row_sum(float a, float (&buf)[2][16]) { return row_sums<false>(a, 0.f, buf).x; }
 
 }  // namespace row
 }  // namespace qmoe
