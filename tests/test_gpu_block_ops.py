@@ -661,3 +661,47 @@ def test_refusals_of_tensors():
         qb.fp8_matmul(torch.zeros(4, 80, dtype=torch.uint8).cuda()[:, 1:65], s, q, s)
     with pytest.raises(qb.QmoeError, match="-1"):
         qb.fp8_matmul(torch.zeros(4, 72, dtype=torch.uint8).cuda()[:, :64], s, q, s)
+
+
+# ------------------------------------------------------------------ together
+
+def test_block_example_gradients():
+    """examples/moe_block.py: the operators together.  A small step along the gradients changes the loss as they say; the
+    routed experts' output and the codes' rounding stay as they are along it, so the step goes through the norms, the gate
+    and the balance loss, whose gradients do not pass through them."""
+    import importlib.util
+    import os
+
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "moe_block.py")
+    spec = importlib.util.spec_from_file_location("moe_block", path)
+    m = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(m)
+    block = m.MoeBlock(H=256, I=128, E=8, k=2, seed=3)
+    g = gen(91)
+    r = randn(g, 40, 256, dtype=BF16).cuda()
+    mask = (torch.rand(40, generator=g) < 0.8).cuda()
+    dout, dn = randn(g, 40, 256, dtype=BF16, scale=0.1).cuda(), randn(g, 40, 256, dtype=BF16, scale=0.1).cuda()
+    out, n_next, s = block.forward(r, mask=mask, coef=0.5)
+    dx, grads, route = block.train_step(r, dout, dn, coef=0.5, mask=mask)
+    assert dx.shape == r.shape and all(torch.isfinite(t).all() for t in grads.values())
+    assert int(route.counts[-1]) == int(mask.sum()) and torch.equal(route.counts, s["route"].counts)
+    # the norms and the gate against the 64-bit block end on the same y
+    y = f64(s["y"].cpu()).requires_grad_()
+    leaves = [f64(t.cpu()).requires_grad_() for t in (block.w_out, block.gate, block.w_next)]
+    o, n = ref.post(f64(r.cpu()), y, leaves[0], leaves[1], block.alpha, leaves[2], m.EPS)
+    c = (256 / 128 + 56) * U
+    ref.close(out, o.detach(), c * (f64(r.cpu()).abs() + (o.detach() - f64(r.cpu())).abs()), "out")
+    want = torch.autograd.grad((o * f64(dout.cpu())).sum() + (n * f64(dn.cpu())).sum(), leaves)
+    for name, got, w in zip(("w_out", "gate", "w_next"), (grads["w_out"], grads["gate"], grads["w_next"]), want):
+        # out is rounded to bf16 before the gradient reads it: 2^-8 of each of the 40 terms, of random signs
+        assert float((got.cpu().double() - w).norm() / w.norm()) < 2.0 ** -7, name
+    # one token is served as it is in the batch (quantised row by row)
+    one = block.forward(r[:1], mask=mask[:1])[0]
+    assert torch.allclose(one.float(), out[:1].float(), rtol=2.0 ** -6, atol=2.0 ** -6)
+    # the shared expert's second product, whose gradient is the formula on what the codes stand for
+    dy = qb.norm_post_backward(dout, s["y"], w=block.w_out, rstd=s["rstd"], gate=block.gate, alpha=block.alpha, dn=dn, out=out,
+                               w_next=block.w_next, rstd_next=s["rstd_next"])[1].cpu()
+    a = s["a"].cpu()
+    want, slack = ref.product(ref.dequant(*ref.quant(dy.t().contiguous(), 1)), ref.dequant(*ref.quant(a.t().contiguous(), 1)))
+    ref.close(grads["w2"], want, slack, "w2")
+    assert int(qb.status_word("cuda")) == 0
