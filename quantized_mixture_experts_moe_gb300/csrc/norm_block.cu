@@ -16,6 +16,8 @@ namespace norm {
 struct FwdArgs {
     int64_t rows;
     int cols, stages, stage_bytes;
+    int lie_base, lie_step;  // Lie
+    bool fp32;               // Columns
     Source r, y, full_gate;  // r: the stream (norm_pre: x)
     const float* w;
     int gate_mode;
@@ -30,11 +32,11 @@ struct FwdArgs {
 };
 
 // POST: y, its norm and gate; without it the kernel is norm_pre (out = r, not written).
-template <typename RT, typename YT, int NV, int VEC, bool POST>
+template <typename RT, typename YT, int NV, int VEC, bool SHIFT, bool POST>
 __global__ void __launch_bounds__(512, 1)
 norm_fwd_kernel(const FwdArgs a) {
     constexpr int E = NV * VEC;
-    constexpr bool KEEP = E <= 16;  // the weights stay in registers from row to row
+    constexpr bool KEEP = E <= 16;  // the weights stay in registers from row to row, y from sum to sum
     __shared__ __align__(16) float sums[2][2][16];
     __shared__ uint64_t full[MAX_ROWS][MAX_STAGES];
     extern __shared__ __align__(128) uint8_t dynamic[];
@@ -44,8 +46,10 @@ norm_fwd_kernel(const FwdArgs a) {
     int flip = 0;
 
     int64_t row = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
-    Ring<VEC> ring = {full[threadIdx.y], dynamic + (int64_t)threadIdx.y * a.stages * a.stage_bytes, a.stages,
-                      a.stage_bytes, a.rows, stride};
+    const int shift = SHIFT ? (int)((a.lie_base + row * a.lie_step) % VEC) : 0;
+    const Columns<VEC, SHIFT> k = {cols, shift, a.fp32 && shift == 0};
+    Ring<VEC != 1 && !SHIFT> ring = {full[threadIdx.y], dynamic + (int64_t)threadIdx.y * a.stages * a.stage_bytes, a.stages,
+                                     a.stage_bytes, a.rows, stride};
     int matrices = 0;
     ring.feed.take(a.r, sizeof(RT), matrices, tx, row, stride, cols);
     if (POST) ring.feed.take(a.y, sizeof(YT), matrices, tx, row, stride, cols);
@@ -58,33 +62,27 @@ norm_fwd_kernel(const FwdArgs a) {
     pdl_sync();
     ring.begin(row);
     // what a column of y and of out is multiplied by: w and a column gate in one
-    float wg[E], wn[E];
-    auto col_factors = [&] {
+    constexpr int HELD = KEEP ? E : VEC;
+    float wg[HELD], wn[HELD], y[HELD];
+    auto col_factors = [&](int c, float* to) {
 #pragma unroll
-        for (int v = 0; v < NV; ++v) {
-            const int c = (v * blockDim.x + tx) * VEC;
-            if (c >= cols) continue;
+        for (int i = 0; i < VEC; ++i) to[i] = 1.f;
+        if (a.w) load_columns(k, a.w, c, to);
+        if (a.gate_mode == QMOE_GATE_COL) {
+            float g[VEC];
+            load_columns(k, a.gate, c, g);
 #pragma unroll
-            for (int i = 0; i < VEC; ++i) wg[v * VEC + i] = 1.f;
-            if (a.w) row::load<VEC>(a.w + c, &wg[v * VEC]);
-            if (a.gate_mode == QMOE_GATE_COL) {
-                float g[VEC];
-                row::load<VEC>(a.gate + c, g);
-#pragma unroll
-                for (int i = 0; i < VEC; ++i) wg[v * VEC + i] *= g[i];
-            }
-        }
-    };
-    auto next_weights = [&] {
-#pragma unroll
-        for (int v = 0; v < NV; ++v) {
-            const int c = (v * blockDim.x + tx) * VEC;
-            if (c < cols && a.w_next) row::load<VEC>(a.w_next + c, &wn[v * VEC]);
+            for (int i = 0; i < VEC; ++i) to[i] *= g[i];
         }
     };
     if (KEEP) {
-        if (POST) col_factors();
-        next_weights();
+#pragma unroll
+        for (int v = 0; v < NV; ++v) {
+            const int c = k.at(v);
+            if (!k.live(c)) continue;
+            if (POST) col_factors(c, &wg[v * VEC]);
+            if (a.w_next) load_columns(k, a.w_next, c, &wn[v * VEC]);
+        }
     }
     // a row's own scalars are asked for one row early
     const bool row_gate = POST && a.gate_mode == QMOE_GATE_ROW;
@@ -95,17 +93,26 @@ norm_fwd_kernel(const FwdArgs a) {
         const uint8_t* const from = ring.wait();
         bool met = false;
         float o[E];
-        read_row<VEC, NV, true, RT>(a.r, from, row, cols, o);
+        read_row<NV, true, RT>(a.r, from, row, k, o);
         if (ring.lost) o[0] = NAN;
         if (POST) {
-            float y[E];
-            read_row<VEC, NV, true, YT>(a.y, from, row, cols, y);
-            if (!KEEP) col_factors();
+            if (KEEP) read_row<NV, true, YT>(a.y, from, row, k, y);
+            // the v-th access of y; wide rows read it once more from the stage
+            auto y_of = [&](int v) -> float* {
+                if (KEEP) return &y[v * VEC];
+                read_columns<true>(k, row_at<true, YT>(k, a.y, from, row), k.at(v), y);
+                return y;
+            };
             float scale = a.alpha * g_row;
             if (a.w) {
                 float s = 0.f;
 #pragma unroll
-                for (int i = 0; i < E; ++i) s = fmaf(y[i], y[i], s);
+                for (int v = 0; v < NV; ++v) {
+                    if (!k.live(k.at(v))) continue;
+                    const float* const yv = y_of(v);
+#pragma unroll
+                    for (int i = 0; i < VEC; ++i) s = fmaf(yv[i], yv[i], s);
+                }
                 const float rstd = rsqrtf(row::row_sum(s, sums[flip]) * inv_cols + a.eps);
                 flip ^= 1;
                 met = true;
@@ -113,26 +120,28 @@ norm_fwd_kernel(const FwdArgs a) {
                 if (tx == 0 && a.rstd) a.rstd[row] = rstd;
                 scale *= rstd;
             }
-            if (a.gate_mode == QMOE_GATE_FULL) {
-                float g[E];
-                read_row<VEC, NV, true, YT>(a.full_gate, from, row, cols, g);
-#pragma unroll
-                for (int i = 0; i < E; ++i) y[i] *= g[i];
-            }
 #pragma unroll
             for (int v = 0; v < NV; ++v) {
-                const int c = (v * blockDim.x + tx) * VEC;
-                if (c >= cols) continue;
+                const int c = k.at(v);
+                if (!k.live(c)) continue;
+                float* const yv = y_of(v);
+                if (a.gate_mode == QMOE_GATE_FULL) {
+                    float g[VEC];
+                    read_columns<true>(k, row_at<true, YT>(k, a.full_gate, from, row), c, g);
+#pragma unroll
+                    for (int i = 0; i < VEC; ++i) yv[i] *= g[i];
+                }
+                if (!KEEP) col_factors(c, wg);
 #pragma unroll
                 for (int i = 0; i < VEC; ++i) {
                     const int e = v * VEC + i;
-                    o[e] = fmaf(y[e] * scale, wg[e], o[e]);
+                    o[e] = fmaf(yv[i] * scale, wg[KEEP ? e : i], o[e]);
                 }
-                row::store<VEC>(static_cast<RT*>(a.out) + row * a.ldo + c, &o[v * VEC]);
+                clear_outside(k, c, &o[v * VEC]);  // 0 times a scale that is not finite
+                store_columns(k, static_cast<RT*>(a.out) + row * a.ldo, c, &o[v * VEC]);
             }
         }
         if (a.w_next) {
-            if (!KEEP) next_weights();
             float s = 0.f;
 #pragma unroll
             for (int i = 0; i < E; ++i) s = fmaf(o[i], o[i], s);
@@ -143,12 +152,13 @@ norm_fwd_kernel(const FwdArgs a) {
             if (tx == 0 && a.rstd_next) a.rstd_next[row] = rstd;
 #pragma unroll
             for (int v = 0; v < NV; ++v) {
-                const int c = (v * blockDim.x + tx) * VEC;
-                if (c >= cols) continue;
+                const int c = k.at(v);
+                if (!k.live(c)) continue;
                 float n[VEC];
+                if (!KEEP) load_columns(k, a.w_next, c, wn);
 #pragma unroll
-                for (int i = 0; i < VEC; ++i) n[i] = o[v * VEC + i] * rstd * wn[v * VEC + i];
-                row::store<VEC>(static_cast<YT*>(a.n) + row * a.ldn + c, n);
+                for (int i = 0; i < VEC; ++i) n[i] = o[v * VEC + i] * rstd * wn[KEEP ? v * VEC + i : i];
+                store_columns(k, static_cast<YT*>(a.n) + row * a.ldn, c, n);
             }
         }
         if (!met || blockDim.x == 32) {
@@ -186,19 +196,34 @@ template <bool POST>
 struct Fwd {
     template <typename RT, typename YT>
     struct Go {
-        static int go(FwdArgs& a, bool vec, cudaStream_t st) {
+        static int go(FwdArgs& a, cudaStream_t st) {
             constexpr int W = wide_vec<RT, YT>();
-            const Shape s = shape_of(a.cols, vec ? W : 1, 16);
+            Lie lie = {W, a.cols};
+            lie.add(a.r.p, a.r.ld, sizeof(RT));
+            if (POST) lie.add(a.y.p, a.y.ld, sizeof(YT));
+            if (a.full_gate.p) lie.add(a.full_gate.p, a.full_gate.ld, sizeof(YT));
+            if (POST) lie.add(a.out, a.ldo, sizeof(RT));
+            if (a.w_next) lie.add(a.n, a.ldn, sizeof(YT));
+            a.lie_base = lie.base;
+            a.lie_step = lie.step;
+            a.fp32 = aligned16(a.w) && aligned16(a.w_next) && aligned16(a.gate_mode == QMOE_GATE_COL ? a.gate : nullptr);
+            const bool at_zero = lie.at_zero() && a.fp32;
+            Shape s = shape_of(a.cols, W, 16);
+            const bool shifted = !at_zero && fits(s, lie);
+            if (!at_zero && !shifted) s = shape_of(a.cols, 1, 16);
             const int rb = stage_bytes(a.cols, sizeof(RT)), yb = stage_bytes(a.cols, sizeof(YT));
             a.y.off = rb;
             a.full_gate.off = rb + yb;
             const int bytes = rb + (POST ? yb : 0) + (a.full_gate.p ? yb : 0);
-            if (vec) {
-                if (s.values() == 16) return start<norm_fwd_kernel<RT, YT, 16 / W, W, POST>>(s, a, bytes, st);
-                return start<norm_fwd_kernel<RT, YT, 32 / W, W, POST>>(s, a, bytes, st);
-            }
-            if (s.values() == 16) return start<norm_fwd_kernel<RT, YT, 16, 1, POST>>(s, a, bytes, st);
-            return start<norm_fwd_kernel<RT, YT, 32, 1, POST>>(s, a, bytes, st);
+            const bool few = s.values() == 16;
+            if (at_zero)
+                return few ? start<norm_fwd_kernel<RT, YT, 16 / W, W, false, POST>>(s, a, bytes, st)
+                           : start<norm_fwd_kernel<RT, YT, 32 / W, W, false, POST>>(s, a, bytes, st);
+            if (shifted)
+                return few ? start<norm_fwd_kernel<RT, YT, 16 / W, W, true, POST>>(s, a, bytes, st)
+                           : start<norm_fwd_kernel<RT, YT, 32 / W, W, true, POST>>(s, a, bytes, st);
+            return few ? start<norm_fwd_kernel<RT, YT, 16, 1, false, POST>>(s, a, bytes, st)
+                       : start<norm_fwd_kernel<RT, YT, 32, 1, false, POST>>(s, a, bytes, st);
         }
     };
 };
@@ -229,8 +254,7 @@ extern "C" int qmoe_norm_pre(int64_t rows, int64_t cols, int stream_dtype, int b
     a.n = n;
     a.ldn = ldn;
     a.rstd_next = rstd;
-    const bool vec = cols % 8 == 0 && norm::row_aligned(x, ldx, rs) && norm::row_aligned(n, ldn, bs) && aligned16(w);
-    return norm::by_types<norm::PreGo>(stream_dtype, block_dtype, a, vec, (cudaStream_t)stream);
+    return norm::by_types<norm::PreGo>(stream_dtype, block_dtype, a, (cudaStream_t)stream);
 }
 
 extern "C" int qmoe_norm_post(int64_t rows, int64_t cols, int stream_dtype, int block_dtype, const void* r,
@@ -270,10 +294,5 @@ extern "C" int qmoe_norm_post(int64_t rows, int64_t cols, int stream_dtype, int 
     a.ldn = ldn;
     a.rstd = w ? rstd : nullptr;
     a.rstd_next = rstd_next;
-    bool vec = cols % 8 == 0 && norm::row_aligned(r, ldr, rs) && norm::row_aligned(y, ldy, bs) &&
-               norm::row_aligned(out, ldo, rs) && aligned16(w) && aligned16(w_next);
-    if (w_next) vec = vec && norm::row_aligned(n, ldn, bs);
-    if (gate_mode == QMOE_GATE_FULL) vec = vec && norm::row_aligned(gate, ldg, bs);
-    if (gate_mode == QMOE_GATE_COL) vec = vec && aligned16(gate);
-    return norm::by_types<norm::PostGo>(stream_dtype, block_dtype, a, vec, (cudaStream_t)stream);
+    return norm::by_types<norm::PostGo>(stream_dtype, block_dtype, a, (cudaStream_t)stream);
 }

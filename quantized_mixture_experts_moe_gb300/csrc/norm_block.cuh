@@ -12,8 +12,34 @@ constexpr int64_t MAX_COLS = 16384;
 
 inline bool gate_mode_ok(int m) { return m >= QMOE_GATE_NONE && m <= QMOE_GATE_FULL; }
 
-// Rows of 16-byte accesses: an aligned base and row stride.
-inline bool row_aligned(const void* p, int64_t ld, int size) { return aligned16(p) && (ld * size) % 16 == 0; }
+// How the rows of all matrices of a call lie against accesses of `vec` values.
+// A row's first value is (base + row * step) % vec values past a boundary; where
+// base and step are the same for all matrices, accesses that start that much
+// before the row are aligned in each of them, and since a CTA's rows lie a
+// multiple of 8 apart, the shift is one for all rows of a CTA.  Odd widths of
+// contiguous tensors are of this kind; others go value by value (T=4096, H=4097,
+// 16-bit: forward 52 us against 82 value by value, gradient 120 against 332).
+struct Lie {
+    int vec;
+    int64_t cols;
+    bool first = true, same = true, whole = cols % 8 == 0;
+    int base = 0, step = 0;
+
+    int most() const { return step ? vec - 1 : base; }  // the largest shift of a row
+    bool at_zero() const { return whole; }              // all rows begin and end on 16-byte boundaries
+
+    void add(const void* p, int64_t ld, int size) {
+        const uintptr_t at = reinterpret_cast<uintptr_t>(p);
+        const int b = (int)(at / size % vec), s = (int)(ld % vec);
+        if (first) {
+            base = b;
+            step = s;
+            first = false;
+        }
+        same = same && base == b && step == s;
+        whole = whole && aligned16(p) && ld * size % 16 == 0;
+    }
+};
 
 // How a row is cut: nv vectors of vec columns in each of `threads` threads, at
 // least `values` each, then 16 and 32 where that takes more than 512 threads;
@@ -32,14 +58,22 @@ constexpr int wide_vec() { return sizeof(RT) == 4 || sizeof(YT) == 4 ? 4 : 8; }
 inline Shape shape_of(int64_t cols, int vec, int values) {
     Shape s;
     s.vec = vec;
+    // Widths off the vector leave room for a shift, except where that takes more
+    // threads than a CTA has (the last columns below the widest row).
+    constexpr int MOST = 512 * 32;
+    const int64_t room = cols % vec != 0 && cols + vec - 1 <= MOST ? vec - 1 : 0;
     for (;; values *= 2) {
         s.nv = values / s.vec;
-        const int64_t per = (cols + values - 1) / values;
+        const int64_t per = (cols + room + values - 1) / values;
         s.threads = (int)((per + 31) / 32 * 32);
         if (s.threads <= 512 || values == 32) break;
     }
     s.rows_per_cta = s.threads == 32 ? 4 : 1;
     return s;
+}
+// Whether rows of any shift of `lie` end within the threads' columns.
+inline bool fits(const Shape& s, const Lie& lie) {
+    return lie.same && lie.cols + lie.most() <= (int64_t)s.values() * s.threads;
 }
 
 // ------------------------------------------------------------------ rows on their way
@@ -87,11 +121,11 @@ struct Feed {
             bytes = cols * size;
         }
     }
-    // Sends for row `row` of `rows` and tells the barrier.
-    template <int VEC>
+    // Sends for row `row` of `rows` and tells the barrier.  WHOLE: rows on 16-byte boundaries.
+    template <bool WHOLE>
     __device__ __forceinline__ void send(uint8_t* stage, int64_t row, int64_t rows, uint64_t* bar) {
         uint8_t* dst = stage + off;
-        if constexpr (VEC > 1) {
+        if constexpr (WHOLE) {
             tc::mbar_arrive_expect_tx(bar, bytes);
             tc::bulk_load(dst, p, bytes, bar);
         } else {
@@ -114,17 +148,86 @@ struct Feed {
     }
 };
 
-// This thread's values of a row, widened; zeros past the row's end.  RING: from
-// a stage; else straight from the matrix.
-template <int VEC, int NV, bool RING, typename T>
-__device__ __forceinline__ void read_row(const Source& s, const uint8_t* stage, int64_t row, int cols, float* v) {
+// How a kernel reads a row: by accesses of VEC columns.  AT_ZERO: all rows begin
+// and end on an access's boundaries; SHIFTED: rows begin `shift` columns past
+// one, so that a row's first and last access reach past it.  (A kernel that
+// keeps both cases open spends 5 to 20% more on the first: H=4096 forward 28 us
+// for 26, gradient 70 for 59.)
+// A thread's columns.
+template <int VEC, bool SHIFT>
+struct Columns {
+    int cols, shift;
+    bool fp32;  // fp32 values for each column may be read VEC at a time (16-byte boundaries, no shift)
+
+    // first column of the thread's v-th access
+    __device__ __forceinline__ int at(int v) const {
+        return (int)(v * blockDim.x + threadIdx.x) * VEC - (SHIFT ? shift : 0);
+    }
+    __device__ __forceinline__ bool live(int c) const { return c < cols && (!SHIFT || c > -VEC); }
+    __device__ __forceinline__ bool whole(int c) const { return !SHIFT || (c >= 0 && c + VEC <= cols); }
+    __device__ __forceinline__ bool in(int c) const { return !SHIFT || (c >= 0 && c < cols); }
+};
+
+// Zeros for an access's columns outside the row.
+template <int VEC, bool SHIFT>
+__device__ __forceinline__ void clear_outside(const Columns<VEC, SHIFT>& k, int c, float* v) {
+    if constexpr (SHIFT) {
+        if (k.whole(c)) return;
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) v[i] = k.in(c + i) ? v[i] : 0.f;
+    }
+}
+// fp32 values of the columns of an access (weights), 0 outside the row.
+template <int VEC, bool SHIFT>
+__device__ __forceinline__ void load_columns(const Columns<VEC, SHIFT>& k, const float* w, int c, float* v) {
+    if (!SHIFT || (k.fp32 && k.whole(c))) {
+        row::load<VEC>(w + c, v);
+    } else {
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) v[i] = k.in(c + i) ? w[c + i] : 0.f;
+    }
+}
+// VEC values of a row of a matrix.
+template <int VEC, bool SHIFT, typename T>
+__device__ __forceinline__ void store_columns(const Columns<VEC, SHIFT>& k, T* dst, int c, const float* v) {
+    if (k.whole(c)) {
+        row::store<VEC>(dst + c, v);
+    } else {
+#pragma unroll
+        for (int i = 0; i < VEC; ++i)
+            if (k.in(c + i)) dst[c + i] = row::from_f32<T>(v[i]);
+    }
+}
+
+// One access of a row, widened; zeros outside it.  RING: the row lies in a
+// stage, whose granules reach past it; else straight from the matrix.
+template <bool RING, int VEC, bool SHIFT, typename T>
+__device__ __forceinline__ void read_columns(const Columns<VEC, SHIFT>& k, const T* src, int c, float* v) {
+    if (RING || k.whole(c)) {
+        row::load<VEC>(src + c, v);
+        clear_outside(k, c, v);
+    } else {
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) v[i] = k.in(c + i) ? row::to_f32(src[c + i]) : 0.f;
+    }
+}
+template <bool RING, typename T, int VEC, bool SHIFT>
+__device__ __forceinline__ const T* row_at(const Columns<VEC, SHIFT>&, const Source& s, const uint8_t* stage,
+                                           int64_t row) {
+    if (RING && VEC > 1 && !SHIFT) return reinterpret_cast<const T*>(stage + s.off);
     const T* src = static_cast<const T*>(s.p) + row * s.ld;
-    if (RING) src = reinterpret_cast<const T*>(stage + s.off + (VEC == 1 ? reinterpret_cast<uintptr_t>(src) & 15 : 0));
+    return RING ? reinterpret_cast<const T*>(stage + s.off + (reinterpret_cast<uintptr_t>(src) & 15)) : src;
+}
+// This thread's values of a row.
+template <int NV, bool RING, typename T, int VEC, bool SHIFT>
+__device__ __forceinline__ void read_row(const Source& s, const uint8_t* stage, int64_t row,
+                                         const Columns<VEC, SHIFT>& k, float* v) {
+    const T* src = row_at<RING, T>(k, s, stage, row);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-        const int c = (i * blockDim.x + threadIdx.x) * VEC;
-        if (c < cols) {
-            row::load<VEC>(src + c, &v[i * VEC]);
+        const int c = k.at(i);
+        if (k.live(c)) {
+            read_columns<RING>(k, src, c, &v[i * VEC]);
         } else {
 #pragma unroll
             for (int j = 0; j < VEC; ++j) v[i * VEC + j] = 0.f;
@@ -136,7 +239,7 @@ __device__ __forceinline__ void read_row(const Source& s, const uint8_t* stage, 
 // one matrix (one thread that sent for all of them took 1,100 cycles a row, and
 // the others waited for it at the row's next barrier).  A stage is refilled
 // when its row's threads have met once more after reading it.
-template <int VEC>
+template <bool WHOLE>
 struct Ring {
     uint64_t* full;
     uint8_t* base;
@@ -148,7 +251,7 @@ struct Ring {
     bool lost = false;  // a copy did not arrive in time: what follows is NaN
 
     __device__ __forceinline__ void post(int64_t row, int at) {
-        if (feed.p && row < rows) feed.template send<VEC>(base + at * bytes, row, rows, &full[at]);
+        if (feed.p && row < rows) feed.template send<WHOLE>(base + at * bytes, row, rows, &full[at]);
     }
     __device__ __forceinline__ void begin(int64_t row) {
         for (int i = 0; i + 1 < stages || i == 0; ++i) post(row + i * stride, i);

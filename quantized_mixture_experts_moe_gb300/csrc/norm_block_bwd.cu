@@ -20,6 +20,8 @@ namespace norm {
 struct BwdArgs {
     int64_t rows;
     int cols, stages, stage_bytes;
+    int lie_base, lie_step;  // Lie
+    bool fp32;               // Columns
     // dout (norm_pre: dres) and out (what the next norm read; norm_pre: x) have the stream's type, dn, y and a full
     // gate the block's; dn null: no next norm
     Source dout, dn, out, y, full_gate;
@@ -71,7 +73,7 @@ struct ColSums {
 // registers; 16: the weights in shared memory; 32: the sums there, and then no
 // room for a ring, so rows and weights come straight from global memory.
 // POST: the whole sandwich; without it the kernel is norm_pre's gradient.
-template <typename RT, typename YT, int NV, int VEC, bool POST>
+template <typename RT, typename YT, int NV, int VEC, bool SHIFT, bool POST>
 __global__ void __launch_bounds__(512, 1)
 norm_bwd_kernel(const BwdArgs a) {
     constexpr int E = NV * VEC;
@@ -93,8 +95,10 @@ norm_bwd_kernel(const BwdArgs a) {
         sum_g.init(cols_smem + 2 * E * blockDim.x);
     }
     int64_t row = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
-    Ring<VEC> ring = {full[threadIdx.y], dynamic + (int64_t)threadIdx.y * a.stages * a.stage_bytes, a.stages,
-                      a.stage_bytes, a.rows, stride};
+    const int shift = SHIFT ? (int)((a.lie_base + row * a.lie_step) % VEC) : 0;
+    const Columns<VEC, SHIFT> k = {cols, shift, a.fp32 && shift == 0};
+    Ring<VEC != 1 && !SHIFT> ring = {full[threadIdx.y], dynamic + (int64_t)threadIdx.y * a.stages * a.stage_bytes, a.stages,
+                                     a.stage_bytes, a.rows, stride};
     int matrices = 0;
     ring.feed.take(a.dout, sizeof(RT), matrices, tx, row, stride, cols);
     ring.feed.take(a.dn, sizeof(YT), matrices, tx, row, stride, cols);
@@ -109,33 +113,34 @@ norm_bwd_kernel(const BwdArgs a) {
     pdl_sync();
     if (RING) ring.begin(row);
     float w[KEEP ? E : VEC], wn[KEEP ? E : VEC], gc[KEEP ? E : VEC];
-    auto column = [&](int v) { return (int)(v * blockDim.x + tx) * VEC; };
+    auto column = [&](int v) { return k.at(v); };
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
         const int c = column(v);
-        if (c >= cols) continue;
+        if (!k.live(c)) continue;
         if (KEEP) {
 #pragma unroll
             for (int i = 0; i < VEC; ++i) w[v * VEC + i] = gc[v * VEC + i] = 1.f;
-            if (POST && a.w) row::load<VEC>(a.w + c, &w[v * VEC]);
-            if (next) row::load<VEC>(a.w_next + c, &wn[v * VEC]);
-            if (POST && a.gate_mode == QMOE_GATE_COL) row::load<VEC>(a.gate + c, &gc[v * VEC]);
+            if (POST && a.w) load_columns(k, a.w, c, &w[v * VEC]);
+            if (next) load_columns(k, a.w_next, c, &wn[v * VEC]);
+            if (POST && a.gate_mode == QMOE_GATE_COL) load_columns(k, a.gate, c, &gc[v * VEC]);
         } else if (W_SMEM) {  // a thread reads back what it wrote itself
             float t[VEC];
             if (next) {
-                row::load<VEC>(a.w_next + c, t);
-                row::store<VEC>(cols_smem + c, t);
+                load_columns(k, a.w_next, c, t);
+                row::store<VEC>(cols_smem + c + k.shift, t);
             }
             if (POST && a.w) {
-                row::load<VEC>(a.w + c, t);
-                row::store<VEC>(cols_smem + (cols + 7) / 8 * 8 + c, t);
+                load_columns(k, a.w, c, t);
+                row::store<VEC>(cols_smem + E * blockDim.x + c + k.shift, t);
             }
         }
     }
     // a vector's weights, where they are not in registers from row to row
     auto weights_next = [&](int c, int v) -> const float* {
         if (KEEP) return &wn[v * VEC];
-        row::load<VEC>(W_SMEM ? cols_smem + c : a.w_next + c, wn);
+        if (W_SMEM) row::load<VEC>(cols_smem + c + k.shift, wn);
+        else load_columns(k, a.w_next, c, wn);
         return wn;
     };
     // a row's own scalars are asked for one row early
@@ -158,7 +163,7 @@ norm_bwd_kernel(const BwdArgs a) {
         };
         float d[E];
         if (a.dout.p) {
-            read_row<VEC, NV, RING, RT>(a.dout, from, row, cols, d);
+            read_row<NV, RING, RT>(a.dout, from, row, k, d);
         } else {
 #pragma unroll
             for (int e = 0; e < E; ++e) d[e] = 0.f;
@@ -166,11 +171,11 @@ norm_bwd_kernel(const BwdArgs a) {
         if (RING && ring.lost) d[0] = NAN;
         if (next) {
             float x[E], dn[E], s = 0.f;
-            read_row<VEC, NV, RING, YT>(a.dn, from, row, cols, dn);
-            read_row<VEC, NV, RING, RT>(a.out, from, row, cols, x);
+            read_row<NV, RING, YT>(a.dn, from, row, k, dn);
+            read_row<NV, RING, RT>(a.out, from, row, k, x);
 #pragma unroll
             for (int v = 0; v < NV; ++v) {
-                if (column(v) >= cols) continue;
+                if (!k.live(column(v))) continue;
                 const float* const wv = weights_next(column(v), v);
 #pragma unroll
                 for (int i = 0; i < VEC; ++i) {
@@ -186,18 +191,21 @@ norm_bwd_kernel(const BwdArgs a) {
             meet();
 #pragma unroll
             for (int e = 0; e < E; ++e) d[e] = fmaf(rstd_n, dn[e] - x[e] * mean, d[e]);
+#pragma unroll
+            for (int v = 0; v < NV; ++v) clear_outside(k, column(v), &d[v * VEC]);  // 0 times a mean that is not finite
         }
 #pragma unroll
         for (int v = 0; v < NV; ++v)
-            if (column(v) < cols) row::store<VEC>(static_cast<RT*>(a.dr) + row * a.lddr + column(v), &d[v * VEC]);
+            if (k.live(column(v)))
+                store_columns(k, static_cast<RT*>(a.dr) + row * a.lddr, column(v), &d[v * VEC]);
         if (POST) {
             float t[E], s = 0.f, s_gate = 0.f;
-            read_row<VEC, NV, RING, YT>(a.y, from, row, cols, t);
+            read_row<NV, RING, YT>(a.y, from, row, k, t);
             // t = y rstd; d becomes dz w
 #pragma unroll
             for (int v = 0; v < NV; ++v) {
                 const int c = column(v);
-                if (c >= cols) continue;
+                if (!k.live(c)) continue;
                 float wt[VEC], g[VEC], dg[VEC];
 #pragma unroll
                 for (int i = 0; i < VEC; ++i) {
@@ -205,15 +213,12 @@ norm_bwd_kernel(const BwdArgs a) {
                     g[i] = g_row;
                     if (KEEP) g[i] *= gc[v * VEC + i];
                 }
-                if (!KEEP && a.w) row::load<VEC>(W_SMEM ? cols_smem + (cols + 7) / 8 * 8 + c : a.w + c, wt);
-                if (!KEEP && a.gate_mode == QMOE_GATE_COL) row::load<VEC>(a.gate + c, g);
-                if (a.gate_mode == QMOE_GATE_FULL) {
-                    const YT* at = static_cast<const YT*>(a.full_gate.p) + row * a.full_gate.ld;
-                    if (RING)
-                        at = reinterpret_cast<const YT*>(
-                            from + a.full_gate.off + (VEC == 1 ? reinterpret_cast<uintptr_t>(at) & 15 : 0));
-                    row::load<VEC>(at + c, g);
-                }
+                if (W_SMEM && a.w) row::load<VEC>(cols_smem + E * blockDim.x + c + k.shift, wt);
+                if (!W_SMEM && !KEEP && a.w) load_columns(k, a.w, c, wt);
+                if (!KEEP && a.gate_mode == QMOE_GATE_COL) load_columns(k, a.gate, c, g);
+                if (a.gate_mode == QMOE_GATE_FULL)
+                    read_columns<RING>(k, row_at<RING, YT>(k, a.full_gate, from, row), c, g);
+                clear_outside(k, c, g);
 #pragma unroll
                 for (int i = 0; i < VEC; ++i) {
                     const int e = v * VEC + i;
@@ -231,7 +236,7 @@ norm_bwd_kernel(const BwdArgs a) {
                     for (int i = 0; i < VEC; ++i) sum_g.add(v * VEC + i, dg[i]);
                 }
                 if (a.gate_mode == QMOE_GATE_FULL)
-                    row::store<VEC>(static_cast<YT*>(a.dgate) + row * a.lddg + c, dg);
+                    store_columns(k, static_cast<YT*>(a.dgate) + row * a.lddg, c, dg);
             }
             if (a.w || a.gate_mode == QMOE_GATE_ROW) {
                 if (a.gate_mode == QMOE_GATE_ROW) {
@@ -251,7 +256,8 @@ norm_bwd_kernel(const BwdArgs a) {
             }
 #pragma unroll
             for (int v = 0; v < NV; ++v)
-                if (column(v) < cols) row::store<VEC>(static_cast<YT*>(a.dy) + row * a.lddy + column(v), &d[v * VEC]);
+                if (k.live(column(v)))
+                    store_columns(k, static_cast<YT*>(a.dy) + row * a.lddy, column(v), &d[v * VEC]);
         }
         if (RING) {
             if (!met || blockDim.x == 32) {
@@ -269,14 +275,15 @@ norm_bwd_kernel(const BwdArgs a) {
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
         const int c = column(v);
-        if (c >= cols) continue;
+        if (!k.live(c)) continue;
         float t[VEC];
         auto put = [&](ColSums<E, SMEM>& s, int which) {
 #pragma unroll
             for (int i = 0; i < VEC; ++i) t[i] = s.get(v * VEC + i);
             float* to = a.part + (which * a.part_rows + part) * cols + c;
 #pragma unroll
-            for (int i = 0; i < VEC; ++i) to[i] = t[i];
+            for (int i = 0; i < VEC; ++i)
+                if (k.in(c + i)) to[i] = t[i];
         };
         if (next) put(sum_wn, 0);
         if (POST && a.w) put(sum_w, 1);
@@ -312,6 +319,8 @@ __global__ void __launch_bounds__(1024) norm_sum_kernel(const SumArgs a) {
     if (threadIdx.x == 0 && oc < a.cols) out[oc] = s;
 }
 
+// The threads of a row go by the columns alone, not by the access.
+inline Shape cut_of(int64_t cols) { return shape_of(cols, 8, 8); }
 // CTAs of a launch: one wave of 512 threads an SM.
 inline int per_sm_of(const Shape& s) { return 512 / (s.threads * s.rows_per_cta); }
 inline int64_t bwd_ctas(const Shape& s, int64_t rows) {
@@ -320,16 +329,14 @@ inline int64_t bwd_ctas(const Shape& s, int64_t rows) {
     return ctas < fit ? ctas : fit;
 }
 inline int64_t part_rows(int64_t rows, int64_t cols) {
-    // the cut goes by the columns alone, not by the access
-    const Shape s = shape_of(cols, 1, 8);
+    const Shape s = cut_of(cols);
     return bwd_ctas(s, rows) * s.rows_per_cta > 0 ? bwd_ctas(s, rows) * s.rows_per_cta : 1;
 }
 
 template <auto Kernel>
 inline int start(const Shape& s, BwdArgs& a, int sums, int row_bytes, int64_t ctas, cudaStream_t st) {
-    const int64_t padded = (a.cols + 7) / 8 * 8;
     const int64_t besides = s.values() == 32   ? (int64_t)sums * 32 * s.threads * 4
-                            : s.values() == 16 ? (sums == 3 ? 2 : 1) * padded * 4
+                            : s.values() == 16 ? (int64_t)(sums == 3 ? 2 : 1) * 16 * s.threads * 4
                                                : 0;
     a.stage_bytes = row_bytes;
     a.stages = s.values() == 32 ? 0 : stages_of((int64_t)row_bytes * s.rows_per_cta, besides, per_sm_of(s));
@@ -346,11 +353,43 @@ template <bool POST>
 struct Bwd {
     template <typename RT, typename YT>
     struct Go {
-        static int go(BwdArgs& a, bool vec, cudaStream_t st) {
+        // WIDE, FEW: columns of an access for rows of 16 values a thread and more, and of 8
+        template <int WIDE, int FEW, bool SHIFT>
+        static int by_values(const Shape& s, BwdArgs& a, int bytes, int64_t ctas, cudaStream_t st) {
+            constexpr int sums = POST ? 3 : 1;
+            if (s.values() == 8)
+                return start<norm_bwd_kernel<RT, YT, 8 / FEW, FEW, SHIFT, POST>>(s, a, sums, bytes, ctas, st);
+            if (s.values() == 16)
+                return start<norm_bwd_kernel<RT, YT, 16 / WIDE, WIDE, SHIFT, POST>>(s, a, sums, bytes, ctas, st);
+            return start<norm_bwd_kernel<RT, YT, 32 / WIDE, WIDE, SHIFT, POST>>(s, a, sums, bytes, ctas, st);
+        }
+        static int go(BwdArgs& a, cudaStream_t st) {
+            Shape s = cut_of(a.cols);
             // rows of 8 values a thread: in two accesses of 4 columns (T=4096, H=4096, 16-bit 59 us against 61 in one of 8,
             // H=1024 21 against 24); wider rows by 8 where the types allow it (H=8192: 117 us against 131)
-            constexpr int W = wide_vec<RT, YT>();
-            const Shape s = shape_of(a.cols, vec ? (shape_of(a.cols, 1, 8).values() == 8 ? 4 : W) : 1, 8);
+            constexpr int WIDE = wide_vec<RT, YT>();
+            const int W = s.values() == 8 ? 4 : WIDE;
+            Lie lie = {W, a.cols};
+            auto lies = [&](const Source& m, int size) {
+                if (m.p) lie.add(m.p, m.ld, size);
+            };
+            lies(a.dout, sizeof(RT));
+            lies(a.dn, sizeof(YT));
+            lies(a.out, sizeof(RT));
+            lie.add(a.dr, a.lddr, sizeof(RT));
+            if (POST) {
+                lies(a.y, sizeof(YT));
+                lies(a.full_gate, sizeof(YT));
+                lie.add(a.dy, a.lddy, sizeof(YT));
+                if (a.full_gate.p) lie.add(a.dgate, a.lddg, sizeof(YT));
+            }
+            a.lie_base = lie.base;
+            a.lie_step = lie.step;
+            a.fp32 = aligned16(a.w) && aligned16(a.w_next) && aligned16(a.gate_mode == QMOE_GATE_COL ? a.gate : nullptr);
+            const bool at_zero = lie.at_zero() && a.fp32, shifted = !at_zero && fits(s, lie);
+            const int vec = at_zero || shifted ? W : 1;
+            s.nv = s.values() / vec;
+            s.vec = vec;
             const int64_t ctas = bwd_ctas(s, a.rows);
             const int rb = stage_bytes(a.cols, sizeof(RT)), yb = stage_bytes(a.cols, sizeof(YT));
             int at = 0;
@@ -363,15 +402,9 @@ struct Bwd {
             place(a.out, rb);
             place(a.y, yb);
             place(a.full_gate, yb);
-            constexpr int sums = POST ? 3 : 1;
-            if (vec) {
-                if (s.values() == 8) return start<norm_bwd_kernel<RT, YT, 2, 4, POST>>(s, a, sums, at, ctas, st);
-                if (s.values() == 16) return start<norm_bwd_kernel<RT, YT, 16 / W, W, POST>>(s, a, sums, at, ctas, st);
-                return start<norm_bwd_kernel<RT, YT, 32 / W, W, POST>>(s, a, sums, at, ctas, st);
-            }
-            if (s.values() == 8) return start<norm_bwd_kernel<RT, YT, 8, 1, POST>>(s, a, sums, at, ctas, st);
-            if (s.values() == 16) return start<norm_bwd_kernel<RT, YT, 16, 1, POST>>(s, a, sums, at, ctas, st);
-            return start<norm_bwd_kernel<RT, YT, 32, 1, POST>>(s, a, sums, at, ctas, st);
+            if (at_zero) return by_values<WIDE, 4, false>(s, a, at, ctas, st);
+            if (shifted) return by_values<WIDE, 4, true>(s, a, at, ctas, st);
+            return by_values<1, 1, false>(s, a, at, ctas, st);
         }
     };
 };
@@ -379,13 +412,13 @@ template <typename RT, typename YT> using PreGo = Bwd<false>::Go<RT, YT>;
 template <typename RT, typename YT> using PostGo = Bwd<true>::Go<RT, YT>;
 
 template <template <typename, typename> class F>
-inline int run(BwdArgs& a, int rt, int yt, bool vec, float* const (&out)[3], void* ws, cudaStream_t st) {
+inline int run(BwdArgs& a, int rt, int yt, float* const (&out)[3], void* ws, cudaStream_t st) {
     a.part = static_cast<float*>(ws);
     a.part_rows = part_rows(a.rows, a.cols);
-    const Shape s = shape_of(a.cols, 1, 8);
+    const Shape s = cut_of(a.cols);
     const int64_t ctas = bwd_ctas(s, a.rows);
     if (ctas > 0) {
-        const int rc = by_types<F>(rt, yt, a, vec, st);
+        const int rc = by_types<F>(rt, yt, a, st);
         if (rc != QMOE_OK) return rc;
     }
     if (!out[0] && !out[1] && !out[2]) return QMOE_OK;
@@ -433,10 +466,7 @@ extern "C" int qmoe_norm_pre_backward(int64_t rows, int64_t cols, int stream_dty
     a.rstd_next = rstd;
     a.dr = dx;
     a.lddr = lddx;
-    bool vec = cols % 8 == 0 && norm::row_aligned(dn, lddn, bs) && norm::row_aligned(x, ldx, rs) &&
-               norm::row_aligned(dx, lddx, rs) && aligned16(w);
-    if (dres) vec = vec && norm::row_aligned(dres, lddres, rs);
-    return norm::run<norm::PreGo>(a, stream_dtype, block_dtype, vec, {dw, nullptr, nullptr}, ws, (cudaStream_t)stream);
+    return norm::run<norm::PreGo>(a, stream_dtype, block_dtype, {dw, nullptr, nullptr}, ws, (cudaStream_t)stream);
 }
 
 extern "C" int qmoe_norm_post_backward(int64_t rows, int64_t cols, int stream_dtype, int block_dtype, const void* dout,
@@ -487,19 +517,13 @@ extern "C" int qmoe_norm_post_backward(int64_t rows, int64_t cols, int stream_dt
     a.lddy = lddy;
     a.dgate = dgate;
     a.lddg = lddg;
-    bool vec = cols % 8 == 0 && norm::row_aligned(y, ldy, bs) && norm::row_aligned(dr, lddr, rs) &&
-               norm::row_aligned(dy, lddy, bs) && aligned16(w);
-    if (dout) vec = vec && norm::row_aligned(dout, lddout, rs);
-    if (full) vec = vec && norm::row_aligned(gate, ldg, bs) && norm::row_aligned(dgate, lddg, bs);
-    if (gate_mode == QMOE_GATE_COL) vec = vec && aligned16(gate);
     if (dn) {
         a.dn = {dn, lddn, 0};
         a.out = {out, ldo, 0};
         a.w_next = w_next;
         a.rstd_next = rstd_next;
-        vec = vec && norm::row_aligned(dn, lddn, bs) && norm::row_aligned(out, ldo, rs) && aligned16(w_next);
     }
     float* const col_gate = gate_mode == QMOE_GATE_COL ? static_cast<float*>(dgate) : nullptr;
-    return norm::run<norm::PostGo>(a, stream_dtype, block_dtype, vec,
+    return norm::run<norm::PostGo>(a, stream_dtype, block_dtype,
                                    {dn ? dw_next : nullptr, w ? dw : nullptr, col_gate}, ws, (cudaStream_t)stream);
 }

@@ -237,6 +237,55 @@ def test_norm_gradients_against_differences():
     assert abs(a - b) <= 256 * U * size + 1e-6
 
 
+# rows that begin at every place of a 16-byte access, several for each CTA; weights off the boundaries
+@pytest.mark.parametrize("i,size", list(enumerate([(1300, 6), (700, 1021), (400, 4095), (340, 4099), (320, 6001), (170, 8195)])))
+def test_norm_odd_rows(i, size):
+    T, H = size
+    for j in range(2):
+        st, bt = TYPES[(2 * i + j) % 5]
+        g = gen(700 + i)
+        r, y, w, w_next = randn(g, T, H, dtype=st), randn(g, T, H, dtype=bt, scale=0.3), randn(g, H + 1)[1:], randn(g, H + 1)[1:]
+        gate, dout, dn = torch.rand(T, H, generator=g).to(bt), randn(g, T, H, dtype=st), randn(g, T, H, dtype=bt)
+        c = (H / 128 + 56) * U
+        on = [dev(torch.cat([torch.zeros(1), v]))[1:] for v in (w, w_next)]
+        out, n, rstd, rstd_next = qb.norm_post(dev(r), dev(y), w=on[0], gate=dev(gate), w_next=on[1], eps=EPS)
+        ro, rn = ref.post(f64(r), f64(y), f64(w), f64(gate), 1.0, f64(w_next), EPS)
+        size_out, rr = f64(r).abs() + (ro - f64(r)).abs(), ref.norm(ro, 1.0, EPS)[1]
+        ref.close(out, ro, c * size_out, "out")
+        ref.close(n, rn, c * (rn.abs() + size_out * rr[:, None] * f64(w_next).abs()), "n")
+        rstd = ref.norm(f64(y), 1.0, EPS)[1].float()
+        o = ro.to(st)
+        rstd_next = ref.norm(f64(o), 1.0, EPS)[1].float()
+        dr, dy, dw, dgate, dw_next = qb.norm_post_backward(dev(dout), dev(y), w=on[0], rstd=dev(rstd), gate=dev(gate), dn=dev(dn),
+                                                           out=dev(o), w_next=on[1], rstd_next=dev(rstd_next))
+        lo, lw = f64(o).requires_grad_(), f64(w_next).requires_grad_()
+        through, rw = torch.autograd.grad(ref.norm(lo, lw, EPS)[0], (lo, lw), f64(dn))
+        d = f64(dout) + through
+        d_slack = _norm_bwd_slack(f64(o), f64(w_next), f64(dn), rstd_next.double(), H) + 2 * U * d.abs()
+        ref.close(dr, d, d_slack, "dr")
+        ref.close(dw_next, rw, (T + 48) * U * (f64(dn) * f64(o) * rstd_next.double()[:, None]).abs().sum(0), "dw_next")
+        leaves = [v.requires_grad_() for v in (f64(y), f64(w), f64(gate))]
+        ry, rw, rg = torch.autograd.grad(ref.post(torch.zeros(T, H).double(), *leaves, 1.0, None, EPS)[0], leaves, d)
+        rs, ga, ww = rstd.double()[:, None], f64(gate), f64(w)
+        xhat, dz = (f64(y) * rs).abs(), ga * (d_slack + 4 * U * d.abs())
+        lost = rs * (dz * ww.abs() + xhat * (dz * ww.abs() * xhat).mean(-1, keepdim=True))
+        ref.close(dy, ry, _norm_bwd_slack(f64(y), ww, ga * d, rs[:, 0], H) + lost, "dy")
+        ref.close(dw, rw, (dz * xhat).sum(0) + (T + 48) * U * ((ga * d).abs() * xhat).sum(0), "dw")
+        ref.close(dgate, rg, (d_slack + 8 * U * d.abs()) * xhat * ww.abs(), "dgate")
+
+
+def test_norm_odd_rows_beside_an_infinite_gate():
+    # a row gate that is infinite makes its own row infinite (1 / rms = 0), whatever lies past the ends of the row
+    g = gen(91)
+    T, H = 9, 1021
+    r, y, gate, w = randn(g, T, H), randn(g, T, H).abs() + 0.1, torch.rand(T, 1, generator=g), torch.ones(H)
+    gate[4] = math.inf
+    out, n, _, rstd_next = qb.norm_post(dev(r), dev(y), w=dev(w), gate=dev(gate), w_next=dev(w), eps=EPS)
+    assert torch.isinf(out[4]).all() and float(rstd_next[4].cpu()) == 0
+    others = [i for i in range(T) if i != 4]
+    assert torch.isfinite(out[others]).all() and torch.isfinite(n[others]).all() and (rstd_next[others] > 0).all()
+
+
 def test_norm_strides_and_alignment():
     # rows with a stride, a base off the 16-byte boundary, and outputs whose padding stays as it was
     T, H = 5, 96
