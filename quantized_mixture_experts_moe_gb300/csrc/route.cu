@@ -15,8 +15,10 @@
 // so that what has been taken falls to the bottom (one fused add-and-maximum
 // for each register, nothing to clear).  A 16-bit logit's key leaves room for
 // the expert's number, so one redux gives both and equal logits come lowest
-// expert first; 32-bit scores are looked up by value, and all experts of one
-// value leave in ascending order.  Instruction issue, not the 2 E bytes of a
+// expert first.  32-bit scores (fp32 logits, a bias) give their lowest bits, up
+// to 10, to the number; where the k + 1 largest differ above them, that order is the
+// scores' own, and the rare token where two do not is selected anew by whole
+// scores.  Instruction issue, not the 2 E bytes of a
 // row, is the bound.  Probabilities are summed per lane over a warp's tokens,
 // then over a CTA's warps, then over CTAs, in a fixed order.
 #include "row_ops.cuh"
@@ -63,9 +65,6 @@ __device__ __forceinline__ uint32_t key_of(float v) {
     const uint32_t u = __float_as_uint(v + 0.f);
     return u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u);
 }
-__device__ __forceinline__ float value_of(uint32_t key) {
-    return __uint_as_float((key & 0x80000000u) ? (key & 0x7FFFFFFFu) : ~key);
-}
 // A bf16 or fp16 value is told by the upper 19 bits of its fp32 form (8 of
 // exponent, at most 10 of mantissa): below them goes the expert, reversed.
 constexpr uint32_t VALUE_BITS = 0xFFFFE000u;
@@ -75,6 +74,18 @@ __device__ __forceinline__ uint32_t packed_key(float v, int e) {
 __device__ __forceinline__ int packed_expert(uint32_t key) { return (int)(0x1FFFu - (key & 0x1FFFu)); }
 __device__ __forceinline__ float packed_value(uint32_t key) {
     return __uint_as_float(((key & 0x80000000u) ? (key & 0x7FFFFFFFu) : ~key) & VALUE_BITS);
+}
+
+// A 32-bit score's key with the expert, reversed, in the bits that number the NE * 32 experts.
+template <int NE>
+constexpr uint32_t NUMBER_BITS = NE * 32 - 1;
+template <int NE>
+__device__ __forceinline__ uint32_t rough_key(float v, int e) {
+    return (key_of(v) & ~NUMBER_BITS<NE>) | (NUMBER_BITS<NE> - (uint32_t)e);
+}
+template <int NE>
+__device__ __forceinline__ int rough_expert(uint32_t key) {
+    return (int)(NUMBER_BITS<NE> - (key & NUMBER_BITS<NE>));
 }
 
 using row::warp_sum;
@@ -117,6 +128,73 @@ __device__ __forceinline__ void load_logits(const T* row, int E, int lane, float
     }
 }
 
+// Keys of a lane's scores; past the last expert, where a logit is -inf, not
+// available.  The bias comes 16 bytes at a time where logits do.
+template <int NE, int V>
+__device__ __forceinline__ void rough_keys(const float* bias, int E, int lane, const float (&v)[NE], uint32_t (&key)[NE]) {
+    constexpr int W = V < 4 ? V : 4;
+    struct alignas(4 * W) Pack { float x[W]; };
+#pragma unroll
+    for (int i = 0; i < NE; i += W) {
+        const int e = expert_of<V>(i, lane);
+        Pack p = {};
+        if (bias && e < E) p = *reinterpret_cast<const Pack*>(bias + e);
+        bool fine = true;
+#pragma unroll
+        for (int j = 0; j < W; ++j) {
+            p.x[j] += v[i + j];
+            fine = fine && p.x[j] <= LARGEST;
+        }
+        if (!fine) {
+#pragma unroll
+            for (int j = 0; j < W; ++j) p.x[j] = clean(p.x[j]);
+        }
+#pragma unroll
+        for (int j = 0; j < W; ++j) key[i + j] = rough_key<NE>(p.x[j], e + j);
+    }
+}
+
+// The largest key below `last` of all lanes' (last = 0: of all); false: there is none that is available.
+template <int NE>
+__device__ __forceinline__ bool next_key(const uint32_t (&key)[NE], uint32_t& last) {
+    uint32_t best = 0;
+#pragma unroll
+    for (int i = 0; i < NE; ++i) best = __viaddmax_u32(key[i], 0u - last, best);
+    const uint32_t top = __reduce_max_sync(0xFFFFFFFFu, best) + last;
+    if (top < AVAILABLE || (last != 0 && top >= last)) return false;
+    last = top;
+    return true;
+}
+
+// Selection by whole 32-bit scores: all experts of one score leave in ascending order.  Lane j gets the j-th.
+template <typename T, int NE, int V>
+__device__ __noinline__ int select_by_score(const T* row, const float* bias, int E, int k, int lane) {
+    float v[NE];
+    uint32_t key[NE], last = 0;
+    load_logits<T, NE, V>(row, E, lane, v);
+#pragma unroll
+    for (int i = 0; i < NE; ++i) {
+        const int e = expert_of<V>(i, lane);
+        key[i] = e < E ? key_of(bias ? clean(v[i] + bias[e]) : v[i]) : 0u;
+    }
+    int mine = -1;
+    for (int j = 0; j < k && next_key(key, last);) {
+        uint32_t here = 0;  // which of this lane's experts have this score
+#pragma unroll
+        for (int i = 0; i < NE; ++i) here |= key[i] == last ? 1u << i : 0u;
+        while (j < k) {
+            const int i = __ffs(here) - 1;
+            const unsigned e = here ? (unsigned)expert_of<V>(i, lane) : 0x7FFFFFFFu;
+            const unsigned win = __reduce_min_sync(0xFFFFFFFFu, e);
+            if (win == 0x7FFFFFFFu) break;
+            if (e == win) here &= here - 1;
+            if (lane == j) mine = (int)win;
+            ++j;
+        }
+    }
+    return mine;
+}
+
 template <typename T, int NE, int V, bool PACK>
 __global__ void __launch_bounds__(WARPS * 32, NE > 16 ? 1 : 2)
 route_kernel(const Args a) {
@@ -150,11 +228,11 @@ route_kernel(const Args a) {
             continue;
         }
         uint32_t key[NE];
+        if constexpr (PACK) {
 #pragma unroll
-        for (int i = 0; i < NE; ++i) {
-            const int e = expert_of<V>(i, lane);
-            if constexpr (PACK) key[i] = packed_key(v[i], e);
-            else key[i] = e < E ? key_of(a.bias ? clean(v[i] + a.bias[e]) : v[i]) : 0u;
+            for (int i = 0; i < NE; ++i) key[i] = packed_key(v[i], expert_of<V>(i, lane));
+        } else {
+            rough_keys<NE, V>(a.bias, E, lane, v, key);
         }
         float sum = 0.f;
 #pragma unroll
@@ -168,45 +246,27 @@ route_kernel(const Args a) {
 #pragma unroll
             for (int i = 0; i < NE; ++i) psum[i] = fmaf(v[i], inv, psum[i]);
         }
-        // lane j: the expert of rank j and its key
+        // lane j: the expert of rank j and its logit
         int mine = -1;
-        uint32_t my_key = 0, last = 0;  // key - 0: at first all keys are below
-        for (int j = 0; j < a.k;) {
-            uint32_t best = 0;
-#pragma unroll
-            for (int i = 0; i < NE; ++i) best = __viaddmax_u32(key[i], 0u - last, best);
-            const uint32_t top = __reduce_max_sync(0xFFFFFFFFu, best) + last;
-            if (top < AVAILABLE || (last != 0 && top >= last)) break;  // nothing left
-            last = top;
-            if constexpr (PACK) {
-                if (lane == j) {
-                    mine = packed_expert(top);
-                    my_key = top;
-                }
-                ++j;
-            } else {
-                uint32_t here = 0;  // which of this lane's experts have this score
-#pragma unroll
-                for (int i = 0; i < NE; ++i) here |= key[i] == top ? 1u << i : 0u;
-                while (j < a.k) {
-                    const int i = __ffs(here) - 1;
-                    const unsigned e = here ? (unsigned)expert_of<V>(i, lane) : 0x7FFFFFFFu;
-                    const unsigned win = __reduce_min_sync(0xFFFFFFFFu, e);
-                    if (win == 0x7FFFFFFFu) break;
-                    if (e == win) here &= here - 1;
-                    if (lane == j) {
-                        mine = (int)win;
-                        my_key = top;
-                    }
-                    ++j;
-                }
-            }
-        }
         float l = -INFINITY;
-        if (mine >= 0) {
-            // beside a bias the key is not the logit's: read that again (it is in L1)
-            if constexpr (PACK) l = packed_value(my_key);
-            else l = a.bias ? clean(row::to_f32(row[mine])) : value_of(my_key);
+        uint32_t last = 0;  // key - 0: at first all keys are below
+        if constexpr (PACK) {
+            for (int j = 0; j < a.k && next_key(key, last); ++j)
+                if (lane == j) {
+                    mine = packed_expert(last);
+                    l = packed_value(last);
+                }
+        } else {
+            bool sure = true;
+            for (int j = 0; j <= a.k; ++j) {
+                const uint32_t before = last;
+                if (!next_key(key, last)) break;
+                sure = j == 0 || (before ^ last) > NUMBER_BITS<NE>;
+                if (!sure) break;
+                if (lane == j && j < a.k) mine = rough_expert<NE>(last);
+            }
+            if (!sure) mine = select_by_score<T, NE, V>(row, a.bias, E, a.k, lane);
+            if (mine >= 0) l = clean(row::to_f32(row[mine]));
         }
         float w;
         if (a.renorm) {
@@ -414,6 +474,7 @@ inline int by_rows(const Args& a, cudaStream_t st) {
     constexpr int most = 16 / sizeof(T), V = NE < most ? NE : most;
     const uintptr_t bytes = V * sizeof(T);
     const bool fits = a.E % V == 0 && reinterpret_cast<uintptr_t>(a.logits) % bytes == 0 && a.ld % V == 0 &&
+                      (BWD || !a.bias || reinterpret_cast<uintptr_t>(a.bias) % (V < 4 ? V * 4 : 16) == 0) &&
                       (!BWD || (reinterpret_cast<uintptr_t>(a.dlogits) % bytes == 0 && a.ldd % V == 0));
     return fits ? start<BWD, T, NE, V>(a, st) : start<BWD, T, NE, 1>(a, st);
 }

@@ -435,6 +435,43 @@ def test_route_gradient_against_differences():
         assert abs(a - b) <= 256 * U * float((got.cpu().double() * ds[0]).abs().sum() + f64(dw).abs().sum()) + 1e-7
 
 
+@pytest.mark.parametrize("E", [5, 64, 300, 512, 1024])
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_route_scores_that_differ_in_their_last_bits(E, dtype):
+    # the choice goes by whole 32-bit scores, ties by the lower expert, among neighbouring floats too
+    g = gen(60 + E)
+    T, k = 40, min(E, 7)
+    step = torch.randint(0, 3 * E, (T, E), generator=g).float()
+    if dtype == F32:
+        lg, bias = 1.0 + step * 2.0 ** -23, None
+        lg[::4] = -lg[::4]
+        lg[1::4, E // 2:] += 3.0
+    else:
+        lg, bias = (1.0 + step / 128).to(BF16), torch.randint(0, 4, (E,), generator=g).float() * 2.0 ** -20
+    score = lg.float() if bias is None else lg.float() + bias
+    got = qb.route_topk(dev(lg), k, bias=dev(bias))
+    want = torch.sort(score, dim=1, descending=True, stable=True).indices[:, :k]
+    assert torch.equal(got.ids.cpu().long(), want)
+    p = torch.softmax(f64(lg), 1).gather(1, want)
+    w = p / p.sum(1, keepdim=True)
+    ref.close(got.w, w, _route_slack(got, f64(lg), E) * w, "w")
+
+
+@pytest.mark.parametrize("E", [6, 64, 512, 1000])
+def test_route_bias_off_its_boundaries_and_not_finite(E):
+    # -inf and NaN in the bias take an expert out, +inf puts it first; weights are of the logits alone
+    g = gen(80 + E)
+    T, k = 33, 3
+    lg, whole = randn(g, T, E, dtype=BF16), randn(g, E + 1)
+    whole[[1, 4]], whole[2], whole[5] = -math.inf, math.nan, math.inf
+    got = qb.route_topk(dev(lg), k, bias=dev(whole)[1:])
+    score = lg.float() + whole[1:].nan_to_num(nan=-math.inf, posinf=1e30)
+    want = torch.sort(score, dim=1, descending=True, stable=True).indices[:, :k]
+    assert torch.equal(got.ids.cpu().long(), want) and (want[:, 0] == 4).all()
+    w = torch.softmax(f64(lg).gather(1, want), 1)
+    ref.close(got.w, w, _route_slack(got, f64(lg), E) * w, "w")
+
+
 def test_route_values_that_are_not_numbers():
     lg = torch.zeros(4, 8)
     lg[0] = torch.arange(8.0)
