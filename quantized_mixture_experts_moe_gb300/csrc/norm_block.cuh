@@ -55,21 +55,25 @@ struct Shape {
 template <typename RT, typename YT>
 constexpr int wide_vec() { return sizeof(RT) == 4 || sizeof(YT) == 4 ? 4 : 8; }
 
-inline Shape shape_of(int64_t cols, int vec, int values) {
+inline Shape shape_for(int64_t cols, int vec, int values) {
     Shape s;
     s.vec = vec;
-    // Widths off the vector leave room for a shift, except where that takes more
-    // threads than a CTA has (the last columns below the widest row).
-    constexpr int MOST = 512 * 32;
-    const int64_t room = cols % vec != 0 && cols + vec - 1 <= MOST ? vec - 1 : 0;
     for (;; values *= 2) {
         s.nv = values / s.vec;
-        const int64_t per = (cols + room + values - 1) / values;
+        const int64_t per = (cols + values - 1) / values;
         s.threads = (int)((per + 31) / 32 * 32);
         if (s.threads <= 512 || values == 32) break;
     }
     s.rows_per_cta = s.threads == 32 ? 4 : 1;
     return s;
+}
+// With room for a shift where the width is off the access, as long as that takes
+// no more values a thread, nor (`exact`) more threads.
+inline Shape shape_of(int64_t cols, int vec, int values, bool exact) {
+    const Shape s = shape_for(cols, vec, values);
+    if (cols % vec == 0) return s;
+    const Shape r = shape_for(cols + vec - 1, vec, values);
+    return r.threads <= 512 && r.nv == s.nv && (!exact || r.threads == s.threads) ? r : s;
 }
 // Whether rows of any shift of `lie` end within the threads' columns.
 inline bool fits(const Shape& s, const Lie& lie) {
