@@ -24,7 +24,7 @@ constexpr int EPI_REGS = 200, OTHER_REGS = 56;
 struct Side {
     const float* s;
     int64_t s_row, s_blk;
-    int rows, shift;  // shift: log2 of the rows that share a scale (0 or 7)
+    int shift;  // log2 of the rows that share a scale (0 or 7)
 };
 
 struct GemmArgs {
@@ -34,7 +34,7 @@ struct GemmArgs {
     int64_t ldc;
     int ctype;
     int32_t* status;
-    int weights_early;  // b does not depend on the kernel before this one
+    int weights_early;  // b does not depend on the kernel before this one (narrow kernel)
 };
 
 __device__ __forceinline__ void mma_f8(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,

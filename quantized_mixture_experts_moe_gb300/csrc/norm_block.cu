@@ -7,7 +7,10 @@
 // and y are read once and out and n written once (8 bytes a column in 16-bit
 // types), and the second sum runs on values already at hand.  The bound is
 // HBM; what there is besides are the two sums of a row, each a latency of two
-// shuffles' trees and a barrier, which the rows on their way hide.
+// shuffles' trees and a barrier, which the rows on their way hide in part.
+// T=4096, H=4096 with the next norm: 16-bit 27 us, 5.0 TB/s (0.75 of a copy's
+// rate); fp32 stream 34 us, 6.0 TB/s; H=8192, 16-bit 49 us, 5.5 TB/s.  One row
+// of T: 4 us, launch and two sums.
 #include "norm_block.cuh"
 
 namespace qmoe {

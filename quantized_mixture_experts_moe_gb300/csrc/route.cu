@@ -18,9 +18,14 @@
 // expert first.  32-bit scores (fp32 logits, a bias) give their lowest bits, up
 // to 10, to the number; where the k + 1 largest differ above them, that order is the
 // scores' own, and the rare token where two do not is selected anew by whole
-// scores.  Instruction issue, not the 2 E bytes of a
-// row, is the bound.  Probabilities are summed per lane over a warp's tokens,
-// then over a CTA's warps, then over CTAs, in a fixed order.
+// scores.  Instruction issue, not the 2 E bytes of a row, is the bound.
+// Probabilities are summed per lane over a warp's tokens, then over a CTA's
+// warps, then over CTAs, in a fixed order, so the loss has the same bits every
+// time.
+//
+// T=8192, E=512, k=8, bf16: 9.7 us without statistics (0.9 TB/s), 17.5 with
+// them, which takes a second launch; with a bias 16 and 23 us, fp32 logits 14.5
+// and 22; the gradient 8.8 us.
 #include "row_ops.cuh"
 
 namespace qmoe {
