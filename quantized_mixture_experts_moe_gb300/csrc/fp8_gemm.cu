@@ -20,7 +20,7 @@
 // memory in rank order: the same bits every time, one launch, no workspace.
 //
 // What bounds it: few tokens, the weight's bytes behind the start of the pipeline
-// (1 x 2048 x 4096 5.7 us, 256 x 2816 x 4096 12.3 us); many, the sum in fp32
+// (1 x 2048 x 4096 5.6 us, 256 x 2816 x 4096 10.8 us); many, the sum in fp32
 // registers, 64 paired fused multiply-adds a thread and block beside the reads
 // of TMEM.  Operands that both have a scale for each row (a weight's gradient,
 // 2048 x 4096 x 4096) run here at any size: 68 us, 1.0 PFLOP/s, bound by a read
@@ -318,11 +318,30 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant
         const float* sums = reinterpret_cast<const float*>(smem);
         const int p0 = (first % p_tiles) * 128, q0 = (first / p_tiles) * NT;
         const int cols = min(NT, g.M - q0);
-        for (int i = part * THREADS + threadIdx.x; i < cols * 128; i += parts * THREADS) {
-            float v = 0.f;
-            for (int r = 0; r < parts; ++r) v += peer_load(sums + i, r);
-            const int n = p0 + (i & 127), m = q0 + (i >> 7);
-            if (n < g.N) put(g.c, g.ctype, (int64_t)m * g.ldc + n, v);
+        // four rows of b at a time, the loads of up to four CTAs on their way at once (one value after the other cost
+        // 2.5 us more at 128 columns); added in rank order
+        for (int i = part * THREADS + threadIdx.x; i < cols * 32; i += parts * THREADS) {
+            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int r0 = 0; r0 < parts; r0 += 4) {
+                float4 x[4];
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+                    if (r0 + r < parts) x[r] = peer_load(sums + i * 4, r0 + r);
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+                    if (r0 + r < parts) {
+                        v.x += x[r].x;
+                        v.y += x[r].y;
+                        v.z += x[r].z;
+                        v.w += x[r].w;
+                    }
+            }
+            const int n = p0 + (i & 31) * 4, m = q0 + (i >> 5);
+            const int64_t at = (int64_t)m * g.ldc + n;
+            const float e[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (n + j < g.N) put(g.c, g.ctype, at + j, e[j]);
         }
         cluster_sync();
     }
@@ -356,12 +375,13 @@ struct Plan {
 // Tile and split by a model of the time in us, fitted to sweeps of both on
 // GB300 (K 64 to 8192, M 1 to 2048, N 1024 to 4096; within 15% of every
 // measured time):
-//   start + rounds * blocks * per_block + (split: 1.3 + nt / 30)
+//   start + rounds * blocks * per_block + (split: 1.5 + nt / 80)
 // rounds: tiles an SM takes in turn; blocks: of 128 along the reduction, in one
 // part.  A split gives every cluster one tile; clusters of 8 fill no more than
 // some 96 SMs, smaller ones 132.  A block costs a narrow tile little more than
 // its handshakes (0.24 us at 16 columns, 0.29 at 64), so few tokens take the
-// narrowest tile and split far: 5.7 us at M 1, N 2048, K 4096, 10.8 unsplit.
+// narrowest tile and split far: 5.6 us at M 1, N 2048, K 4096, 10.8 unsplit; at
+// M 256, N 2816 three parts of 128 columns take 10.8, 64 columns unsplit 12.0.
 // The wide kernel does twice the columns of nt = 128 in 0.55 us against 0.43,
 // and only where a row block of b shares its scales: with column scales it took
 // 0.92.
@@ -383,7 +403,7 @@ inline Plan plan_of(int M, int N, int K, bool uniform) {
             if (parts > 1 && (parts > blocks || tiles * parts > (parts == 8 ? 96 : 132))) continue;
             const int64_t rounds = parts > 1 ? 1 : (tiles + row::kSMs - 1) / row::kSMs;
             const float us = c.start + (float)rounds * (float)((blocks + parts - 1) / parts) * c.per_block +
-                             (parts > 1 ? 1.3f + (float)c.nt / 30.f : 0.f);
+                             (parts > 1 ? 1.5f + (float)c.nt / 80.f : 0.f);
             if (us < least) {
                 least = us;
                 best = {c.nt, parts};
