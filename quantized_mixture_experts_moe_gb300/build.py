@@ -92,7 +92,7 @@ def build(force: bool = False, verbose: bool = False) -> str:
     os.replace(tmp, LIB)
     tmp = BIND + f".tmp{os.getpid()}"
     torch_lib = os.path.join(_torch_dir(), "lib")
-    cmd = ["g++", "-shared", "-o", tmp, bind_obj, LIB, "-L", torch_lib, "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda",
+    cmd = ["g++", "-shared", "-o", tmp, bind_obj, LIB, "-L", torch_lib, "-ltorch_python", "-ltorch_cpu", "-ltorch_cuda", "-lc10", "-lc10_cuda",
            "-Wl,-rpath,$ORIGIN", f"-Wl,-rpath,{torch_lib}"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
