@@ -24,8 +24,9 @@
 // time.
 //
 // T=8192, E=512, k=8, bf16: 9.7 us without statistics (0.9 TB/s), 17.5 with
-// them, which takes a second launch; with a bias 16 and 23 us, fp32 logits 14.5
-// and 22; the gradient 8.8 us.
+// them, which takes a second launch (up to 16 tokens one CTA does both: T=1
+// 4.6 us, 8.2 with two launches); with a bias 16 and 23 us, fp32 logits 14.5 and
+// 22; the gradient 8.8 us.
 #include "row_ops.cuh"
 
 namespace qmoe {
@@ -49,9 +50,12 @@ struct Args {
     float* part_p;
     int32_t* part_c;
     int32_t* arrived;
+    float coef;
+    // where one CTA has all tokens, what route_stats_kernel writes otherwise
+    int32_t* counts_out;
+    float *probs, *loss;
     // gradient
     const float* dw;
-    float coef;
     const int32_t* counts;
     const float* dloss;
     void* dlogits;
@@ -298,6 +302,30 @@ route_kernel(const Args a) {
         if (e < E) smem[warp * E + e] = psum[i];
     }
     __syncthreads();
+    if (gridDim.x == 1) {  // a launch less: T=16, E=512, k=8 5.4 us against 9.0
+        const int n = count[E];
+        const float total = (float)max(n, 1);
+        float part = 0.f;
+        for (int e = threadIdx.x; e < E; e += blockDim.x) {
+            float p = 0.f;
+#pragma unroll
+            for (int i = 0; i < WARPS; ++i) p += smem[i * E + e];
+            p /= total;
+            a.counts_out[e] = count[e];
+            a.probs[e] = p;
+            part = fmaf((float)count[e] / (total * (float)a.k), p, part);
+        }
+        if (threadIdx.x == 0) a.counts_out[E] = n;
+        part = warp_sum(part);
+        __syncthreads();
+        if (lane == 0) smem[warp] = part;
+        __syncthreads();
+        if (warp == 0) {
+            part = warp_sum(lane < WARPS ? smem[lane] : 0.f);
+            if (lane == 0) a.loss[0] = a.coef * (float)E * part;
+        }
+        return;
+    }
     for (int e = threadIdx.x; e <= E; e += blockDim.x) {
         a.part_c[(int64_t)blockIdx.x * (E + 1) + e] = count[e];
         if (e == E) break;
@@ -554,6 +582,10 @@ extern "C" int qmoe_route_topk(int64_t T, int E, int k, int dtype, const void* l
         a.part_c = reinterpret_cast<int32_t*>(a.part_p + (size_t)parts * E);
         float* const part_loss = reinterpret_cast<float*>(a.part_c + (size_t)parts * (E + 1));
         a.arrived = reinterpret_cast<int32_t*>(part_loss + 32);
+        a.coef = coef;
+        a.counts_out = counts;
+        a.probs = probs;
+        a.loss = loss;
         s = {parts, E, k, a.part_p, a.part_c, part_loss, a.arrived, coef, counts, probs, loss};
         if (T == 0 && cudaMemsetAsync(a.arrived, 0, 4, (cudaStream_t)stream) != cudaSuccess) return QMOE_ERR_CUDA;
     }
@@ -561,7 +593,7 @@ extern "C" int qmoe_route_topk(int64_t T, int E, int k, int dtype, const void* l
         const int started = route::run<false>(dtype, a, (cudaStream_t)stream);
         if (started != QMOE_OK) return started;
     }
-    if (!stats) return QMOE_OK;
+    if (!stats || parts == 1) return QMOE_OK;
     return launch_pdl(route::route_stats_kernel, ceil_div(E, 32), 1024, 0, (cudaStream_t)stream, s);
 }
 
