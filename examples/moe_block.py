@@ -103,7 +103,8 @@ def main():
           f"pairs per expert {s['route'].counts[:-1].tolist()}")
     out1, n1, _ = block.forward(r[:1])
     print(f"decode of one token: {'the same row' if torch.allclose(out1.float(), out[:1].float(), rtol=2e-2, atol=2e-2) else 'ANOTHER row'}")
-    dx, grads, _ = block.train_step(r, torch.randn_like(r) * 0.1, torch.randn_like(r) * 0.1)
+    dout, dn_next = ((0.1 * torch.randn(r.shape, generator=g, device="cuda")).bfloat16() for _ in range(2))
+    dx, grads, _ = block.train_step(r, dout, dn_next)
     print("gradients: dx %.4f, " % dx.float().norm().item() + ", ".join(f"{n} {t.float().norm().item():.4f}" for n, t in grads.items()))
     assert int(qb.status_word("cuda").item()) == 0
 

@@ -12,6 +12,7 @@
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <array>
 #include <sstream>
 #include <string>
 
@@ -160,6 +161,36 @@ at::Tensor make(at::IntArrayRef size, at::ScalarType type, const at::Tensor& lik
     // past the dispatcher: half the host time of an output
     return at::Tensor(at::detail::empty_cuda(size, type, like.device(), std::nullopt));
 }
+// Small outputs of one call, in one allocation: each on a 256-byte boundary.
+struct Pieces {
+    struct Piece {
+        std::array<int64_t, 2> size;
+        int dims;
+        at::ScalarType type;
+        int64_t at;
+    };
+    std::array<Piece, 6> piece;
+    int n = 0;
+    int64_t bytes = 0;
+
+    int add(int64_t a, int64_t b, int dims, at::ScalarType type) {
+        piece[n] = {{a, b}, dims, type, bytes};
+        bytes += (a * b * 4 + 255) / 256 * 256;  // 32-bit types
+        return n++;
+    }
+    std::array<at::Tensor, 6> allocate(const at::Tensor& like) const {
+        const at::Tensor block = make({bytes / 4}, at::kFloat, like);
+        std::array<at::Tensor, 6> out;
+        for (int i = 0; i < n; ++i) {
+            out[i] = at::detail::make_tensor<c10::TensorImpl>(c10::Storage(block.storage()), block.key_set(),
+                                                              at::scalarTypeToTypeMeta(piece[i].type));
+            c10::TensorImpl* const t = out[i].unsafeGetTensorImpl();
+            t->set_storage_offset(piece[i].at / 4);
+            t->set_sizes_contiguous(at::IntArrayRef(piece[i].size.data(), piece[i].dims));
+        }
+        return out;
+    }
+};
 qmoe_stream_t stream_of(const at::Tensor& t) {
     return reinterpret_cast<qmoe_stream_t>(c10::cuda::getCurrentCUDAStream(t.get_device()).stream());
 }
@@ -298,17 +329,23 @@ PyObject* route_topk(const Args& a) {  // logits, k, bias, mask, renorm, scale, 
     const uint8_t* mp = nullptr;
     if (mask)
         mp = mask->scalar_type() == at::kBool ? vec_of<uint8_t>(mask, T, at::kBool) : vec_of<uint8_t>(mask, T, at::kByte);
-    const at::Tensor ids = make({T, k}, at::kInt, lg), w = make({T, k}, at::kFloat, lg), lse = make({T}, at::kFloat, lg);
-    at::Tensor counts, probs, loss;
-    if (a.none(6)) {
+    const bool stats = !a.none(6);
+    Pieces pieces;
+    pieces.add(T, k, 2, at::kInt);
+    pieces.add(T, k, 2, at::kFloat);
+    pieces.add(T, 1, 1, at::kFloat);
+    if (stats) {
+        pieces.add(E + 1, 1, 1, at::kInt);
+        pieces.add(E, 1, 1, at::kFloat);
+        pieces.add(1, 1, 1, at::kFloat);
+    }
+    const auto [ids, w, lse, counts, probs, loss] = pieces.allocate(lg);
+    if (!stats) {
         check(qmoe_route_topk(T, (int)E, (int)k, code, r.p, r.ld, bias, mp, a.truth(4), (float)a.number(5),
                               static_cast<int32_t*>(ids.data_ptr()), f32_of(w), f32_of(lse), 0.f, nullptr, nullptr,
                               nullptr, nullptr, 0, stream_of(lg)),
               "qmoe_route_topk");
     } else {
-        counts = make({E + 1}, at::kInt, lg);
-        probs = make({E}, at::kFloat, lg);
-        loss = make({1}, at::kFloat, lg);
         const Workspace ws(qmoe_route_workspace_bytes(T, (int)E), a.maybe(7), lg);
         check(qmoe_route_topk(T, (int)E, (int)k, code, r.p, r.ld, bias, mp, a.truth(4), (float)a.number(5),
                               static_cast<int32_t*>(ids.data_ptr()), f32_of(w), f32_of(lse), (float)a.number(6),
