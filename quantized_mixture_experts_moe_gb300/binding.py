@@ -629,15 +629,4 @@ def fp8_linear_backward(dy, x, wt_q, w_s, dev_status=None, stream=None):
     if stream is not None:
         with torch.cuda.stream(stream):
             return fp8_linear_backward(dy, x, wt_q, w_s, dev_status)
-    T, N = dy.shape
-    K = x.shape[1]
-    if x.shape[0] != T or wt_q.shape != (K, N):
-        raise ValueError("dy [T, N], x [T, K] and wt_q [K, N] do not go together")
-    if T == 0:
-        return (torch.empty((0, K), dtype=dy.dtype, device=dy.device),
-                torch.zeros((N, K), dtype=torch.float32, device=dy.device))
-    dyt_q, dyt_s, dy_q, dy_s = fp8_quant_cols(dy, True)
-    xt_q, xt_s = fp8_quant_cols(x)
-    dx = fp8_matmul(dy_q, dy_s, wt_q, w_s.t(), dy.dtype, dev_status)
-    dw = fp8_matmul(dyt_q, dyt_s, xt_q, xt_s, torch.float32, dev_status)
-    return dx, dw
+    return (_bind or _load_bind()).fp8_linear_backward(dy, x, wt_q, w_s, _status(dy) if dev_status is None else dev_status)

@@ -7,6 +7,7 @@
 
 #include <ATen/core/Tensor.h>
 #include <ATen/cuda/EmptyTensor.h>
+#include <ATen/ops/zeros.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Dtype.h>
 #include <torch/csrc/Exceptions.h>
@@ -495,6 +496,50 @@ PyObject* fp8_linear(const Args& a) {  // x, w_q, w_s, out_dtype, dev_status, ws
     return wrap(y);
 }
 
+PyObject* fp8_linear_backward(const Args& a) {  // dy, x, wt_q, w_s, dev_status
+    const at::Tensor &dy = a.tensor(0), &x = a.tensor(1), &wt = a.tensor(2);
+    matrix(dy, "fp8_linear_backward");
+    matrix(x, "fp8_linear_backward");
+    matrix(wt, "fp8_linear_backward");
+    const int64_t T = dy.size(0), N = dy.size(1), K = x.size(1);
+    if (x.size(0) != T || wt.size(0) != K || wt.size(1) != N)
+        bad("dy [T, N], x [T, K] and wt_q [K, N] do not go together: " + shape_str(dy) + ", " + shape_str(x) + " and " +
+            shape_str(wt));
+    on_device(dy);
+    const at::Tensor dx = make({T, K}, dy.scalar_type(), dy);
+    if (T == 0) return tuple_of({dx, at::zeros({N, K}, at::TensorOptions().dtype(at::kFloat).device(dy.device()))});
+    const qmoe_fp8_mat w = mat_of(wt, a.tensor(3).t());
+    const Rows yr = rows_of(dy, T, N), xr = rows_of(x, T, K);
+    const int yc = code_of(dy.scalar_type()), xc = code_of(x.scalar_type());
+    int32_t* const status = status_of(a.tensor(4));
+    const qmoe_stream_t st = stream_of(dy);
+    const at::Tensor dw = make({N, K}, at::kFloat, dy);
+    // codes and scales of dy^T, dy and x^T, in one allocation
+    const int64_t rows[3] = {N, T, K}, cols[3] = {T, N, T};
+    int64_t at[6], bytes = 0;
+    for (int i = 0; i < 3; ++i) {
+        at[2 * i] = bytes;
+        bytes += (rows[i] * up16(cols[i]) + 255) / 256 * 256;
+        at[2 * i + 1] = bytes;
+        bytes += (rows[i] * blocks_of(cols[i]) * 4 + 255) / 256 * 256;
+    }
+    const at::Tensor held = make({bytes}, at::kByte, dy);
+    uint8_t* const base = static_cast<uint8_t*>(held.data_ptr());
+    qmoe_fp8_mat m[3];
+    float* s[3];
+    for (int i = 0; i < 3; ++i) {
+        s[i] = reinterpret_cast<float*>(base + at[2 * i + 1]);
+        m[i] = {base + at[2 * i], up16(cols[i]), s[i], 1, rows[i], 1, 0};
+    }
+    check(qmoe_fp8_quant_cols(T, N, yc, yr.p, yr.ld, base + at[0], m[0].ld, s[0], base + at[2], m[1].ld, s[1], st),
+          "qmoe_fp8_quant_cols");
+    check(qmoe_fp8_quant_cols(T, K, xc, xr.p, xr.ld, base + at[4], m[2].ld, s[2], nullptr, 0, nullptr, st),
+          "qmoe_fp8_quant_cols");
+    check(qmoe_fp8_matmul(T, K, N, &m[1], &w, dx.data_ptr(), yc, K, status, st), "qmoe_fp8_matmul");
+    check(qmoe_fp8_matmul(N, K, T, &m[0], &m[2], dw.data_ptr(), QMOE_F32, K, status, st), "qmoe_fp8_matmul");
+    return tuple_of({dx, dw});
+}
+
 // ------------------------------------------------------------------ module
 
 template <PyObject* (*F)(const Args&), int N>
@@ -529,6 +574,7 @@ PyMethodDef methods[] = {
     ENTRY(fp8_quant_blocks, 2),
     ENTRY(fp8_matmul, 6),
     ENTRY(fp8_linear, 6),
+    ENTRY(fp8_linear_backward, 5),
     {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_bind", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};

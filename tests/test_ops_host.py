@@ -143,3 +143,15 @@ def test_reference_notices_a_planted_mistake():
     one = ref.route(lg, 2, None, None, True, 1.0, 1.0)
     other = ref.route(lg, 2, None, torch.tensor([1, 1, 1, 1, 1, 0]).bool(), True, 1.0, 1.0)
     assert not torch.equal(one["counts"], other["counts"]) and abs(float((one["loss"] - other["loss"]).detach())) > 1e-4
+
+
+def test_linear_backward_refuses_shapes_that_do_not_go_together():
+    status = torch.zeros(1, dtype=torch.int32)
+    dy, x, wt, s = torch.zeros(3, 8), torch.zeros(3, 16), torch.zeros(16, 8, dtype=torch.uint8), torch.ones(1, 1)
+    for bad in [(dy[:2], x, wt, s), (dy, x[:, :8], wt, s), (dy, x, wt.t(), s), (dy[0], x, wt, s), (dy, x, wt[0], s)]:
+        with pytest.raises(ValueError):
+            qb.fp8_linear_backward(*bad, dev_status=status)
+    with pytest.raises(qb.QmoeError, match="device"):
+        qb.fp8_linear_backward(dy, x, wt, s, dev_status=status)
+    with pytest.raises(qb.QmoeError, match="device"):
+        qb.fp8_linear_backward(dy, x, wt, s)
