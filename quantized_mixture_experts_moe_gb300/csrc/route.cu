@@ -76,13 +76,16 @@ __device__ __forceinline__ uint32_t key_of(float v) {
 }
 // A bf16 or fp16 value is told by the upper 19 bits of its fp32 form (8 of
 // exponent, at most 10 of mantissa): below them goes the expert, reversed.
+// Only what +inf became has bits below them; it is above every 16-bit value.
 constexpr uint32_t VALUE_BITS = 0xFFFFE000u;
+constexpr float LARGEST_16 = 3.38953139e38f;  // bf16's
 __device__ __forceinline__ uint32_t packed_key(float v, int e) {
     return (key_of(v) & VALUE_BITS) | (0x1FFFu - (uint32_t)e);
 }
 __device__ __forceinline__ int packed_expert(uint32_t key) { return (int)(0x1FFFu - (key & 0x1FFFu)); }
 __device__ __forceinline__ float packed_value(uint32_t key) {
-    return __uint_as_float(((key & 0x80000000u) ? (key & 0x7FFFFFFFu) : ~key) & VALUE_BITS);
+    const float v = __uint_as_float(((key & 0x80000000u) ? (key & 0x7FFFFFFFu) : ~key) & VALUE_BITS);
+    return v > LARGEST_16 ? LARGEST : v;
 }
 
 // A 32-bit score's key with the expert, reversed, in the bits that number the NE * 32 experts.

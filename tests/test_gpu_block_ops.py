@@ -487,6 +487,51 @@ def test_route_values_that_are_not_numbers():
     assert int(r.counts[-1]) == 3 and bool(torch.isfinite(r.loss).all())
 
 
+def _infinite_rows(E, dtype):
+    """Rows with one, two and four logits of +inf, beside the type's largest finite value, NaN and -inf; the experts with
+    +inf by row."""
+    top = torch.finfo(dtype).max
+    lg = torch.linspace(-2.0, 2.0, E).repeat(4, 1)
+    lg[0, 5] = math.inf
+    lg[1, [1, E - 1]] = math.inf
+    lg[2, [0, 2, 3, 6]] = math.inf
+    lg[3, 4], lg[3, 0], lg[3, 1], lg[3, 2] = math.inf, top, math.nan, -math.inf
+    return lg.to(dtype), [[5], [1, E - 1], [0, 2, 3, 6], [0, 4] if dtype == F32 else [4]]
+
+
+@pytest.mark.parametrize("renorm", [False, True])
+@pytest.mark.parametrize("dtype", [F32, BF16, F16])
+@pytest.mark.parametrize("E", [8, 65, 512, 1024])
+def test_route_infinite_logits_take_all_the_weight(E, dtype, renorm):
+    # +inf counts as the largest finite value: equal shares for the experts that have it, and exactly 0 for all others
+    lg, there = _infinite_rows(E, dtype)
+    k, scale = 6, 2.0
+    dw = torch.full((4, k), 3.0)
+    dw[:, 0], dw[:, 1] = 0.25, -0.5
+    for wide in (False, True):  # contiguous rows, and rows off the 16-byte boundaries
+        on = torch.zeros(4, E + 3, dtype=dtype).cuda()[:, 1:E + 1] if wide else torch.zeros(4, E, dtype=dtype).cuda()
+        on.copy_(lg)
+        r = qb.route_topk(on, k, renorm=renorm, scale=scale, coef=1.0)
+        bare = qb.route_topk(on, k, renorm=renorm, scale=scale)
+        dl = qb.route_topk_backward(on, r, dw=dw.cuda()).cpu().float()
+        ids, w = r.ids.cpu(), r.w.cpu()
+        assert torch.equal(bare.ids, r.ids) and torch.equal(bare.w, r.w)
+        probs = torch.zeros(E)
+        for t, at in enumerate(there):
+            n = len(at)
+            assert ids[t, :n].tolist() == at
+            assert w[t].tolist() == [scale / n] * n + [0.0] * (k - n)
+            probs[at] += 1.0 / n / 4
+            # w_j (dw_j - sum_i w_i dw_i / scale), exact in every type; 0 for the experts without weight
+            mean = sum(dw[t, :n].tolist()) / n
+            want = torch.zeros(E)
+            want[at] = scale / n * (dw[t, :n] - mean)
+            assert torch.equal(dl[t], want), (t, dl[t][at], want[at])
+        assert torch.equal(r.probs.cpu(), probs) and int(r.counts[-1]) == 4
+        largest = torch.finfo(F32).max
+        assert (r.lse.cpu() == largest).all()
+
+
 def test_route_feeds_the_routing_sort():
     # ids of -1 (masked tokens) take no slot
     g = gen(31)
