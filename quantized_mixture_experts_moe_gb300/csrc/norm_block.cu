@@ -176,6 +176,8 @@ norm_fwd_kernel(const FwdArgs a) {
     }
 }
 
+static_assert(3 * (int64_t)stage_bytes(MAX_COLS, 4) <= room_of(0, 1), "a stage of the widest rows: r, y and a full gate");
+
 template <auto Kernel>
 inline int start(const Shape& s, FwdArgs& a, int row_bytes, cudaStream_t st) {
     const int threads = s.threads * s.rows_per_cta;

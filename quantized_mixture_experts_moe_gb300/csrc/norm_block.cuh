@@ -101,11 +101,13 @@ struct Source {
 
 constexpr int MAX_STAGES = 6, MAX_ROWS = 4;  // stages of a ring, rings of a CTA
 
-inline int stage_bytes(int64_t cols, int size) { return (int)((cols * size + 15) / 16 * 16 + 16); }
+constexpr int stage_bytes(int64_t cols, int size) { return (int)((cols * size + 15) / 16 * 16 + 16); }
 
-// Stages that fit in a CTA's share of an SM's shared memory.
+// Stages that fit in a CTA's share of an SM's shared memory, of which the system
+// keeps 1 KB a CTA and the kernels' own arrays take less than half of one.
+constexpr int64_t room_of(int64_t other_bytes, int ctas_per_sm) { return 226 * 1024 / ctas_per_sm - 1536 - other_bytes; }
 inline int stages_of(int64_t bytes_per_stage, int64_t other_bytes, int ctas_per_sm) {
-    const int64_t n = (226 * 1024 / ctas_per_sm - 2048 - other_bytes) / bytes_per_stage;
+    const int64_t n = room_of(other_bytes, ctas_per_sm) / bytes_per_stage;
     return n > MAX_STAGES ? MAX_STAGES : n > 0 ? (int)n : 0;
 }
 

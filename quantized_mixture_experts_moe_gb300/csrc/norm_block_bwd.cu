@@ -338,11 +338,25 @@ inline int64_t part_rows(int64_t rows, int64_t cols) {
     return bwd_ctas(s, rows) * s.rows_per_cta > 0 ? bwd_ctas(s, rows) * s.rows_per_cta : 1;
 }
 
+// Bytes beside the ring: sums (32 values a thread) or weights (16).
+constexpr int64_t besides_of(int values, int threads, int sums) {
+    return values == 32 ? (int64_t)sums * 32 * threads * 4 : values == 16 ? (int64_t)(sums == 3 ? 2 : 1) * 16 * threads * 4 : 0;
+}
+// Every width that goes through the ring has room for a stage of five fp32
+// matrices (a full gate, dout and dn): at 8192 columns 432 bytes remain.
+constexpr bool all_fit() {
+    for (int threads = 32; threads <= 512; threads += 32) {
+        const int rows = threads == 32 ? 4 : 1;
+        if (5 * (int64_t)stage_bytes(8 * threads, 4) * rows > room_of(0, 512 / (threads * rows))) return false;
+        if (threads > 256 && 5 * (int64_t)stage_bytes(16 * threads, 4) > room_of(besides_of(16, threads, 3), 1)) return false;
+    }
+    return true;
+}
+static_assert(all_fit(), "a stage of the widest rows");
+
 template <auto Kernel>
 inline int start(const Shape& s, BwdArgs& a, int sums, int row_bytes, int64_t ctas, cudaStream_t st) {
-    const int64_t besides = s.values() == 32   ? (int64_t)sums * 32 * s.threads * 4
-                            : s.values() == 16 ? (int64_t)(sums == 3 ? 2 : 1) * 16 * s.threads * 4
-                                               : 0;
+    const int64_t besides = besides_of(s.values(), s.threads, sums);
     a.stage_bytes = row_bytes;
     a.stages = s.values() == 32 ? 0 : stages_of((int64_t)row_bytes * s.rows_per_cta, besides, per_sm_of(s));
     if (s.values() < 32 && !a.stages) return QMOE_ERR_UNSUPPORTED;

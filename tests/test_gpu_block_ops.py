@@ -274,6 +274,31 @@ def test_norm_odd_rows(i, size):
         ref.close(dgate, rg, (d_slack + 8 * U * d.abs()) * xhat * ww.abs(), "dgate")
 
 
+# the widest rows that go through the ring, five fp32 matrices: a stage, and with it the whole ring, of 164 KB
+@pytest.mark.parametrize("T,H", [(3, 8188), (3, 8189), (310, 8191), (310, 8192)])
+def test_norm_gradient_of_five_matrices_of_the_widest_rows(T, H):
+    g = gen(760)
+    y, out, dout, dn = randn(g, T, H, scale=0.5), randn(g, T, H), randn(g, T, H), randn(g, T, H)
+    gate, w, w_next = torch.rand(T, H, generator=g), 1 + randn(g, H, scale=0.2), 1 + randn(g, H, scale=0.2)
+    rstd, rstd_next = ref.norm(f64(y), 1.0, EPS)[1].float(), ref.norm(f64(out), 1.0, EPS)[1].float()
+    dr, dy, dw, dgate, dw_next = qb.norm_post_backward(dev(dout), dev(y), w=dev(w), rstd=dev(rstd), gate=dev(gate), alpha=0.8, dn=dev(dn),
+                                                       out=dev(out), w_next=dev(w_next), rstd_next=dev(rstd_next))
+    lo, lw = f64(out).requires_grad_(), f64(w_next).requires_grad_()
+    through, rw = torch.autograd.grad(ref.norm(lo, lw, EPS)[0], (lo, lw), f64(dn))
+    d = f64(dout) + through
+    d_slack = _norm_bwd_slack(f64(out), f64(w_next), f64(dn), rstd_next.double(), H) + 2 * U * d.abs()
+    ref.close(dr, d, d_slack, "dr")
+    ref.close(dw_next, rw, (T + 48) * U * (f64(dn) * f64(out) * rstd_next.double()[:, None]).abs().sum(0), "dw_next")
+    leaves = [v.requires_grad_() for v in (f64(y), f64(w), f64(gate))]
+    ry, rw, rg = torch.autograd.grad(ref.post(torch.zeros(T, H).double(), *leaves, 0.8, None, EPS)[0], leaves, d)
+    rs, ga, ww = rstd.double()[:, None], 0.8 * f64(gate), f64(w)
+    xhat, dz = (f64(y) * rs).abs(), ga * (d_slack + 4 * U * d.abs())
+    lost = rs * (dz * ww.abs() + xhat * (dz * ww.abs() * xhat).mean(-1, keepdim=True))
+    ref.close(dy, ry, _norm_bwd_slack(f64(y), ww, ga * d, rs[:, 0], H) + lost, "dy")
+    ref.close(dw, rw, (dz * xhat).sum(0) + (T + 48) * U * ((ga * d).abs() * xhat).sum(0), "dw")
+    ref.close(dgate, rg, 0.8 * (d_slack + 8 * U * d.abs()) * xhat * ww.abs(), "dgate")
+
+
 def test_norm_odd_rows_beside_an_infinite_gate():
     # a row gate that is infinite makes its own row infinite (1 / rms = 0), whatever lies past the ends of the row
     g = gen(91)
