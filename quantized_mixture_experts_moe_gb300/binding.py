@@ -590,10 +590,14 @@ _status_words = {}
 
 def status_word(device):
     """The int32 device word where the FP8 products report a wait that ran out (QMOE_DEV_WAIT_TIMEOUT) unless a call is
-    given its own: one for each device, zero until then."""
+    given its own: one for each device, zero until then.  It is made by the first call that wants it, which may not be within
+    a graph capture (QmoeError): call this before one."""
     device = torch.device(device)
     index = torch.cuda.current_device() if device.index is None else device.index
     if index not in _status_words:
+        # made within a capture it would lie in the graph's memory, and no stream could be waited for
+        if torch.cuda.is_current_stream_capturing():
+            raise QmoeError(f"the first FP8 product of a process cannot be captured without a dev_status: call status_word('cuda:{index}') before the capture")
         _status_words[index] = torch.zeros(1, dtype=torch.int32, device=f"cuda:{index}")
         torch.cuda.synchronize(index)  # seen by every stream
     return _status_words[index]

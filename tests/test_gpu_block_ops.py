@@ -781,6 +781,40 @@ def test_graph_capture():
     assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
 
 
+def test_first_fp8_call_in_a_graph_capture_is_refused(monkeypatch):
+    # the word where a product reports is made by the first call outside a capture, or by status_word; a capture goes on
+    # after the refusal
+    g = gen(73)
+    x, w = randn(g, 16, 256).cuda(), torch.ones(256).cuda()
+    w_q, w_s = qb.fp8_quant_blocks(randn(g, 128, 256).cuda())
+    x_q, x_s = qb.fp8_quant_rows(x)
+    want, n_want = qb.fp8_linear(x, w_q, w_s), qb.norm_pre(x, w)[0]
+    own = torch.zeros(1, dtype=torch.int32, device="cuda")
+    torch.cuda.synchronize()
+    with monkeypatch.context() as m:
+        m.setattr(qb, "_status_words", {})
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            n, _ = qb.norm_pre(x, w)
+            with pytest.raises(qb.QmoeError, match="status_word"):
+                qb.fp8_linear(x, w_q, w_s)
+            with pytest.raises(qb.QmoeError, match="status_word"):
+                qb.fp8_matmul(x_q, x_s, w_q, w_s)
+            with pytest.raises(qb.QmoeError, match="status_word"):
+                qb.status_word("cuda")
+            y = qb.fp8_linear(x, w_q, w_s, dev_status=own)  # with a word of its own a call is captured
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(n, n_want) and torch.equal(y, want) and int(own) == 0
+        qb.status_word("cuda")
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            y = qb.fp8_linear(x, w_q, w_s)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(y, want)
+
+
 def test_refusals_of_tensors():
     x, w = torch.zeros(4, 64).cuda(), torch.ones(64).cuda()
     with pytest.raises(ValueError):
