@@ -8,12 +8,14 @@
 #include <ATen/core/Tensor.h>
 #include <ATen/cuda/EmptyTensor.h>
 #include <ATen/ops/zeros.h>
+#include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Dtype.h>
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <array>
+#include <optional>
 #include <sstream>
 #include <string>
 
@@ -55,6 +57,23 @@ struct Args {
         if (n != want) refuse(PyExc_TypeError, std::string(name) + ": wrong number of arguments");
     }
     bool none(int i) const { return v[i] == Py_None; }
+    // The device of the arguments that lie on one: launches go to it.
+    std::optional<at::Device> device() const {
+        std::optional<at::Device> one;
+        for (Py_ssize_t i = 0; i < n; ++i) {
+            // what is told by its type alone first: the tensors' check is a slow one for all else (0.3 us a call)
+            if (v[i] == Py_None || PyFloat_CheckExact(v[i]) || PyLong_Check(v[i]) || !THPVariable_Check(v[i])) continue;
+            const at::Device d = THPVariable_Unpack(v[i]).device();
+            if (!d.is_cuda()) continue;
+            if (one && *one != d) {
+                std::ostringstream s;
+                s << "qmoe kernels take tensors of one device, got " << *one << " and " << d;
+                refuse(qmoe_error, s.str());
+            }
+            one = d;
+        }
+        return one;
+    }
     const at::Tensor& tensor(int i) const {
         if (!THPVariable_Check(v[i])) refuse(PyExc_TypeError, std::string(name) + ": expected a torch.Tensor");
         return THPVariable_Unpack(v[i]);
@@ -546,7 +565,11 @@ template <PyObject* (*F)(const Args&), int N>
 PyObject* entry(PyObject* self, PyObject* const* v, Py_ssize_t n) {
     HANDLE_TH_ERRORS
     try {
-        return F(Args(v, n, N, PyModule_GetName(self)));
+        const Args a(v, n, N, PyModule_GetName(self));
+        const std::optional<at::Device> device = a.device();
+        c10::cuda::OptionalCUDAGuard guard;
+        if (device && device->index() != c10::cuda::current_device()) guard.set_device(*device);
+        return F(a);
     } catch (const PythonError&) {
         return nullptr;
     }

@@ -155,3 +155,27 @@ def test_linear_backward_refuses_shapes_that_do_not_go_together():
         qb.fp8_linear_backward(dy, x, wt, s, dev_status=status)
     with pytest.raises(qb.QmoeError, match="device"):
         qb.fp8_linear_backward(dy, x, wt, s)
+
+
+def test_tensors_of_two_devices_are_refused(lib):
+    # tensors that say where they lie and have no memory: a call ends before it asks for their pointers
+    from torch._subclasses.fake_tensor import FakeTensorMode
+
+    with FakeTensorMode():
+        a, b = ([torch.empty(s, device=f"cuda:{i}") for s in ((4, 64), (64,), (4,))] for i in range(2))
+        codes = [torch.empty(4, 64, dtype=torch.uint8, device=f"cuda:{i}") for i in range(2)]
+        scales = [torch.empty(4, 1, device=f"cuda:{i}") for i in range(2)]
+        word = [torch.empty(1, dtype=torch.int32, device=f"cuda:{i}") for i in range(2)]
+    r = qb.Routing()
+    r.ids, r.w, r.lse, r.counts, r.renorm, r.scale, r.coef = word[0], a[1], a[2], word[0], True, 1.0, 1.0
+    for call in (lambda: qb.norm_pre(a[0], b[1]),
+                 lambda: qb.norm_pre_backward(a[0], a[0], a[2], a[1], dres=b[0]),
+                 lambda: qb.norm_post(a[0], b[0]),
+                 lambda: qb.norm_post_backward(a[0], a[0], gate=b[1]),
+                 lambda: qb.route_topk(a[0], 2, bias=b[1]),
+                 lambda: qb.route_topk_backward(a[0], r, dloss=b[2]),
+                 lambda: qb.fp8_matmul(codes[0], scales[0], codes[1], scales[1], dev_status=word[0]),
+                 lambda: qb.fp8_linear(a[0], codes[0], scales[0], dev_status=word[1]),
+                 lambda: qb.fp8_linear_backward(a[0], a[0], codes[0], scales[1], dev_status=word[0])):
+        with pytest.raises(qb.QmoeError, match="one device"):
+            call()
