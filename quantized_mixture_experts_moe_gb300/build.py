@@ -2,8 +2,9 @@
 (the compiled argument marshalling of the calls around the experts) with g++.
 
 Each .cu file is compiled separately and in parallel, then linked into one
-shared library next to this file; _bind.so links against it.  Rebuilds only
-when a source is newer than the libraries."""
+shared library next to this file; _bind.so finds it by its name in its own
+folder, so the package can be moved.  Rebuilds only when a source is newer than
+the libraries, or _bind.so was built for another Python or torch."""
 
 from __future__ import annotations
 
@@ -12,6 +13,7 @@ import glob
 import importlib.util
 import os
 import subprocess
+import sys
 import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -21,6 +23,7 @@ LIB = os.path.join(PKG, "libqmoe.so")
 BIND_SRC = os.path.join(CSRC, "bind.cpp")
 BIND = os.path.join(PKG, "_bind.so")
 BUILD_DIR = os.path.join(PKG, "_build")
+STAMP = os.path.join(BUILD_DIR, "bind.txt")  # what _bind.so was built for
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-I", INCLUDE, *ARCH]
 
@@ -38,8 +41,22 @@ def _deps():
     return sources() + [BIND_SRC] + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(INCLUDE, "*.h"))
 
 
+def bind_target() -> str:
+    """The interpreter and the torch whose interfaces _bind.so is compiled against."""
+    with open(os.path.join(_torch_dir(), "version.py")) as f:
+        return f"python {sys.version}\ntorch in {_torch_dir()}\n{f.read()}"
+
+
+def _stamped() -> bool:
+    try:
+        with open(STAMP) as f:
+            return f.read() == bind_target()
+    except OSError:
+        return False
+
+
 def up_to_date() -> bool:
-    if not os.path.exists(LIB) or not os.path.exists(BIND):
+    if not os.path.exists(LIB) or not os.path.exists(BIND) or not _stamped():
         return False
     t = min(os.path.getmtime(LIB), os.path.getmtime(BIND))
     return all(os.path.getmtime(p) <= t for p in _deps())
@@ -85,7 +102,7 @@ def build(force: bool = False, verbose: bool = False) -> str:
         objs = sorted(ex.map(compile_one, order))
         bind_obj = bind.result()
     tmp = LIB + f".tmp{os.getpid()}"
-    cmd = [nvcc, *ARCH, "-shared", "-o", tmp, *objs, "-lcudart"]
+    cmd = [nvcc, *ARCH, "-shared", "-Xlinker", "-soname=" + os.path.basename(LIB), "-o", tmp, *objs, "-lcudart"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
@@ -98,6 +115,8 @@ def build(force: bool = False, verbose: bool = False) -> str:
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, BIND)
+    with open(STAMP, "w") as f:
+        f.write(bind_target())
     return LIB
 
 

@@ -179,3 +179,23 @@ def test_tensors_of_two_devices_are_refused(lib):
                  lambda: qb.fp8_linear_backward(a[0], a[0], codes[0], scales[1], dev_status=word[0])):
         with pytest.raises(qb.QmoeError, match="one device"):
             call()
+
+
+def test_a_moved_package_loads_its_own_library(lib, tmp_path):
+    import shutil
+    import subprocess
+    import sys
+
+    shutil.copytree(qbuild.PKG, tmp_path / "quantized_mixture_experts_moe_gb300", ignore=shutil.ignore_patterns("_build", "__pycache__"))
+    code = ("from quantized_mixture_experts_moe_gb300 import binding as qb\n"
+            "assert qb._load_bind().__file__.startswith({0!r})\n"
+            "maps = {{line.split()[-1] for line in open('/proc/self/maps') if 'libqmoe.so' in line}}\n"
+            "assert len(maps) == 1 and maps.pop().startswith({0!r}), maps\n").format(str(tmp_path))
+    r = subprocess.run([sys.executable, "-c", code], cwd=tmp_path, capture_output=True, text=True)
+    assert r.returncode == 0, r.stderr
+
+
+def test_a_module_for_another_torch_is_built_again(lib, monkeypatch):
+    assert qbuild.up_to_date()
+    monkeypatch.setattr(qbuild, "bind_target", lambda: "python 3.0\ntorch 1.0\n")
+    assert not qbuild.up_to_date()
