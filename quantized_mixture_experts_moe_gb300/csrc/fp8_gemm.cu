@@ -345,6 +345,9 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant
         }
         cluster_sync();
     }
+    // a kernel is let go only after the wait: a CTA counts as having done so by its first warp, and the warps without
+    // work have not waited for weights_early's predecessor
+    if (g.weights_early) pdl_wait();
     pdl_trigger();
     tc::tc_fence_before();
     __syncthreads();

@@ -731,6 +731,27 @@ def test_fp8_linear_and_backward(size, dtype):
     ref.close(dw, *ref.product(ref.dequant(*ref.quant(dy.t().contiguous(), 1)), ref.dequant(*ref.quant(x.t().contiguous(), 1))), "dw")
 
 
+@pytest.mark.parametrize("T,N,K", [(1, 2048, 4096), (1, 128, 256), (40, 1500, 512), (300, 640, 1024)])
+def test_fp8_linear_with_weights_written_by_the_calls_around_it(T, N, K):
+    # products read weight tiles before the kernel ahead of them has ended: codes and scales that are written anew between
+    # two products on one stream are those of the call's own turn
+    g = gen(74)
+    x, ws = randn(g, T, K, dtype=BF16).cuda(), [randn(g, N, K, dtype=BF16).cuda() for _ in range(6)]
+    want = []
+    for w in ws:
+        want.append(qb.fp8_linear(x, *qb.fp8_quant_blocks(w), out_dtype=F32))
+        torch.cuda.synchronize()
+    q, s = qb.fp8_quant_blocks(ws[0])
+    for _ in range(10):
+        got = []
+        for w in ws:
+            assert qb.lib().qmoe_fp8_quant_blocks(N, K, 1, w.data_ptr(), K, q.data_ptr(), K, None, 0, s.data_ptr(),
+                                                  torch.cuda.current_stream().cuda_stream) == 0
+            got.append(qb.fp8_linear(x, q, s, out_dtype=F32))
+        for a, b in zip(got, want):
+            assert torch.equal(a, b)
+
+
 def test_fp8_linear_gradient_against_differences():
     # the product of what the codes stand for, along a direction of it: quantisation itself has no gradient
     g = gen(62)
