@@ -254,7 +254,9 @@ struct Ring {
     Feed feed;
     int stage = 0;
     uint32_t phase = 0;
-    bool lost = false;  // a copy did not arrive in time: what follows is NaN
+    // a copy did not arrive in time: what follows is NaN, and no more is sent for (what had been, before that wait, has
+    // had the wait's 2 s to land)
+    bool lost = false;
 
     __device__ __forceinline__ void post(int64_t row, int at) {
         if (feed.p && row < rows) feed.template send<WHOLE>(base + at * bytes, row, rows, &full[at]);
@@ -274,6 +276,10 @@ struct Ring {
     // The row's threads have met since `row` was waited for: the stage read before it is free.
     __device__ __forceinline__ void refill(int64_t row) {
         if (stages > 1 && !lost) post(row + (stages - 1) * stride, stage == 0 ? stages - 1 : stage - 1);
+    }
+    // A ring of one stage: the row's threads have met after their last read of it.
+    __device__ __forceinline__ void reuse(int64_t row) {
+        if (!lost) post(row + stride, 0);
     }
     __device__ __forceinline__ void next() {
         if (++stage == stages) {

@@ -269,7 +269,7 @@ norm_bwd_kernel(const BwdArgs a) {
             }
             if (a.stages == 1) {
                 row_barrier();
-                ring.post(row + stride, 0);
+                ring.reuse(row);
             }
             ring.next();
         }
