@@ -557,6 +557,24 @@ def test_route_infinite_logits_take_all_the_weight(E, dtype, renorm):
         assert (r.lse.cpu() == largest).all()
 
 
+@pytest.mark.parametrize("renorm", [False, True])
+@pytest.mark.parametrize("biased", [False, True])
+@pytest.mark.parametrize("dtype", [F32, BF16, F16])
+@pytest.mark.parametrize("i,size", list(enumerate([(3, 8, 3), (40, 60, 7), (700, 128, 8), (33, 512, 10), (20, 1000, 32)])))
+def test_route_weights_by_type_bias_and_renorm(i, size, dtype, biased, renorm):
+    T, E, k = size
+    g = gen(900 + i)
+    lg = _logits(g, T, E, dtype, "holes" if i % 2 else "plain")
+    bias, mask = randn(g, E, scale=0.3) if biased else None, torch.rand(T, generator=g) < 0.8
+    got = qb.route_topk(dev(lg), k, bias=dev(bias), mask=dev(mask), renorm=renorm, scale=1.5, coef=0.1)
+    want = ref.route(f64(lg), k, bias, mask, renorm, 1.5, 0.1)
+    assert torch.equal(got.ids.cpu(), want["ids"]) and torch.equal(got.counts.cpu(), want["counts"])
+    c = _route_slack(want, f64(lg), E)
+    ref.close(got.w, want["w"], c * want["w"], "w")
+    ref.close(got.probs, want["probs"], (c + (T + 48) * U) * want["probs"], "probs")
+    ref.close(got.loss, want["loss"][None], (c + (T + E + 64) * U) * want["loss"].abs(), "loss")
+
+
 def test_route_feeds_the_routing_sort():
     # ids of -1 (masked tokens) take no slot
     g = gen(31)
