@@ -84,8 +84,7 @@ __device__ __forceinline__ uint32_t packed_key(float v, int e) {
 }
 __device__ __forceinline__ int packed_expert(uint32_t key) { return (int)(0x1FFFu - (key & 0x1FFFu)); }
 __device__ __forceinline__ float packed_value(uint32_t key) {
-    const float v = __uint_as_float(((key & 0x80000000u) ? (key & 0x7FFFFFFFu) : ~key) & VALUE_BITS);
-    return v > LARGEST_16 ? LARGEST : v;
+    return __uint_as_float(((key & 0x80000000u) ? (key & 0x7FFFFFFFu) : ~key) & VALUE_BITS);
 }
 
 // A 32-bit score's key with the expert, reversed, in the bits that number the NE * 32 experts.
@@ -268,6 +267,7 @@ route_kernel(const Args a) {
                     mine = packed_expert(last);
                     l = packed_value(last);
                 }
+            if (l > LARGEST_16) l = LARGEST;  // +inf's key without its low bits
         } else {
             bool sure = true;
             for (int j = 0; j <= a.k; ++j) {
