@@ -170,7 +170,7 @@ norm_fwd_kernel(const FwdArgs a) {
         }
         if (a.stages == 1) {
             row_barrier();
-            ring.reuse(row);
+            ring.post(row + stride, 0);
         }
         ring.next();
     }

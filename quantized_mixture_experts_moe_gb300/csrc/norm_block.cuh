@@ -269,17 +269,16 @@ struct Ring {
     __device__ __forceinline__ const uint8_t* wait() {
         int late = 0;
         if ((threadIdx.x & 31) == 0 && !lost) late = !tc::mbar_wait(&full[stage], phase);
-        lost = lost || __shfl_sync(0xFFFFFFFFu, late, 0);
+        if (__shfl_sync(0xFFFFFFFFu, late, 0)) {
+            lost = true;
+            feed.p = nullptr;
+        }
         __syncwarp();
         return base + stage * bytes;
     }
     // The row's threads have met since `row` was waited for: the stage read before it is free.
     __device__ __forceinline__ void refill(int64_t row) {
-        if (stages > 1 && !lost) post(row + (stages - 1) * stride, stage == 0 ? stages - 1 : stage - 1);
-    }
-    // A ring of one stage: the row's threads have met after their last read of it.
-    __device__ __forceinline__ void reuse(int64_t row) {
-        if (!lost) post(row + stride, 0);
+        if (stages > 1) post(row + (stages - 1) * stride, stage == 0 ? stages - 1 : stage - 1);
     }
     __device__ __forceinline__ void next() {
         if (++stage == stages) {

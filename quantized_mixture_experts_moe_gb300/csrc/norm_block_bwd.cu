@@ -269,7 +269,7 @@ norm_bwd_kernel(const BwdArgs a) {
             }
             if (a.stages == 1) {
                 row_barrier();
-                ring.reuse(row);
+                ring.post(row + stride, 0);
             }
             ring.next();
         }
