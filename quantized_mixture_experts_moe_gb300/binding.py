@@ -471,9 +471,6 @@ def moe_forward(scheme, x, topk_ids, topk_w, w1, w1_s, w2, w2_s, H=None, I=None,
 # shapes or types do not go together.  The marshalling itself is compiled
 # (csrc/bind.cpp): for a single token a kernel takes a few microseconds.
 
-GATE_NONE, GATE_ROW, GATE_COL, GATE_FULL = 0, 1, 2, 3
-FP8_BLOCK = 128
-
 _bind = None
 
 
