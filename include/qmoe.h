@@ -510,7 +510,8 @@ int qmoe_moe_forward(int scheme, const qmoe_dims* d, const uint16_t* x_bf16, con
  * code, mode or stride outside these rules returns QMOE_ERR_ARG, a shape
  * beyond a stated limit QMOE_ERR_UNSUPPORTED.  An output may not overlap an
  * input unless the call says so.  Zero rows are valid and write what sums over
- * no rows give. */
+ * no rows give.  The norms' waits for their own copies give up after some 2 s,
+ * as only a fault of the machine makes them; the row then has NaN values. */
 enum { QMOE_F32 = 0, QMOE_BF16 = 1, QMOE_F16 = 2 };
 
 /* What a block's gate is one value for: nothing (no gate), a row (fp32 [rows]),
@@ -575,12 +576,16 @@ int qmoe_norm_post_backward(int64_t rows, int64_t cols, int stream_dtype, int bl
  *   (bias NULL: 0; an fp32 sum), largest first, the lower id first where equal;
  *   w[t][j] = scale * p[t][ids[t][j]], or with renorm scale * softmax over the
  *   k chosen logits.
+ * The bias is added to the logit.  (Routers that balance their experts by a bias
+ * on the score, the sigmoid or the softmax of the logit, choose otherwise: their
+ * biases are not meant here, and there is no sigmoid score.)
  * A logit of -inf is an expert that is not available: it has p = 0 and is never
- * chosen; NaN counts as -inf, +inf as the largest finite value.  Places that no
- * available expert fills hold id -1 and weight 0.  A token whose mask byte is 0
- * (mask NULL: none) or whose logits are all -inf is routed nowhere: ids -1,
- * weights 0, lse -inf, no part in the statistics.  (An id of -1 in topk_ids
- * contributes nothing to qmoe_moe_forward and raises QMOE_DEV_BAD_EXPERT_ID.)
+ * chosen; NaN counts as -inf, +inf as the largest finite fp32 value, whatever
+ * the logits' type.  Places that no available expert fills hold id -1 and weight
+ * 0.  A token whose mask byte is 0 (mask NULL: none) or whose logits are all -inf
+ * is routed nowhere: ids -1, weights 0, lse -inf, no part in the statistics.  (An
+ * id of -1 in topk_ids contributes nothing to qmoe_moe_forward and raises
+ * QMOE_DEV_BAD_EXPERT_ID.)
  * Statistics (counts, probs, loss: all three or none), over the n routed tokens:
  *   counts[e] = pairs of expert e, counts[E] = n;  probs[e] = mean_t p[t][e];
  *   loss = coef * E * sum_e counts[e] / (k n) * probs[e]  (0 for n = 0).

@@ -468,8 +468,11 @@ def moe_forward(scheme, x, topk_ids, topk_w, w1, w1_s, w2, w2_s, H=None, I=None,
 # They allocate their outputs, run on the current stream (or on the one that
 # the keyword `stream` names, on which their outputs then belong) and raise
 # QmoeError for what the library refuses and ValueError for tensors whose
-# shapes or types do not go together.  The marshalling itself is compiled
-# (csrc/bind.cpp): for a single token a kernel takes a few microseconds.
+# shapes or types do not go together.  All tensors of a call lie on one device.
+# Autograd does not see these calls: what they return has no history, also for
+# inputs that require gradients; the gradients are the ..._backward calls.  The
+# marshalling itself is compiled (csrc/bind.cpp): for a single token a kernel
+# takes a few microseconds.
 
 _bind = None
 
@@ -531,13 +534,15 @@ def norm_post_backward(dout, y, w=None, rstd=None, gate=None, alpha=1.0, dn=None
 class Routing:
     """What route_topk returns, and what its gradient takes: ids int32 [T, k], w fp32 [T, k], lse fp32 [T]; with coef also
     counts int32 [E + 1] (the last is the number of routed tokens), probs fp32 [E], loss fp32 [1] (else None); and the
-    call's renorm, scale and coef."""
+    call's renorm, scale and coef.  The tensors share one allocation: keeping or saving one of them keeps or saves them all,
+    so clone what outlives the step (a loss that is logged)."""
     __slots__ = ("ids", "w", "lse", "counts", "probs", "loss", "renorm", "scale", "coef")
 
 
 def route_topk(logits, k, bias=None, mask=None, renorm=True, scale=1.0, coef=None, ws=None, stream=None) -> Routing:
     """The k experts of largest logit + bias of each row of logits [T, E] and their weights; with coef also the balance
-    loss and the per-expert counts.  mask (bool or uint8 [T]): rows where it is 0 are routed nowhere (ids -1)."""
+    loss and the per-expert counts.  mask (bool or uint8 [T]): rows where it is 0 are routed nowhere (ids -1).  bias is
+    added to the logit, not to a sigmoid or softmax of it."""
     if stream is not None:
         with torch.cuda.stream(stream):
             return route_topk(logits, k, bias, mask, renorm, scale, coef, ws)

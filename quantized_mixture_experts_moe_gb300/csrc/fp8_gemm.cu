@@ -12,8 +12,8 @@
 // columns rows m of a (tokens): few tokens then make narrow tiles, whose loads
 // are almost all weight; and a store of one token's 128 outputs is contiguous
 // across lanes.  Warps: 8 scale and sum (two for each quadrant of lanes, half
-// the columns each), one loads tiles by TMA, one issues the products, one
-// brings the scales with cp.async.
+// the columns each); two load tiles by TMA, two issue the products and two
+// bring the scales by plain loads, each pair taking the blocks in turn.
 //
 // Where the tiles are fewer than the SMs, the reduction axis is cut in S parts
 // for a cluster of S CTAs, which add their parts through distributed shared
@@ -23,9 +23,13 @@
 // (1 x 2048 x 4096 5.6 us, 256 x 2816 x 4096 10.8 us); many, the sum in fp32
 // registers, 64 paired fused multiply-adds a thread and block beside the reads
 // of TMEM.  Operands that both have a scale for each row (a weight's gradient,
-// 2048 x 4096 x 4096) run here at any size: 68 us, 1.0 PFLOP/s, bound by a read
-// of the column's scale from shared memory for every pair that is added.  Many
-// rows of a and a b scaled by 128 rows go to the wide kernel.
+// 2048 x 4096 x 4096) run here at any size: 68 us, 1.0 PFLOP/s; every pair that
+// is added needs its columns' scales read from shared memory and multiplied
+// first.  A tile of two rows a thread, which read them half as often, was no
+// faster (70 us): it issued 202 instructions a warp and block for the 128
+// needed, with the FMA pipe 35% busy, so latency has a part in it that is not
+// traced further.  Many rows of a and a b scaled by 128 rows go to the wide
+// kernel.
 #include "fp8_gemm.cuh"
 
 namespace qmoe {

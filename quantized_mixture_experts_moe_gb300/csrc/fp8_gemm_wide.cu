@@ -8,7 +8,8 @@
 // two accumulators take the blocks in turn, and their halves are handed over
 // separately: a block's products are 512 cycles, but issuing four of them and
 // the way to the epilogue and back cost as much again, which the halves hide
-// in part.  8192 x 2816 x 4096: 93 us, 2.02 PFLOP/s.
+// in part.  8192 x 2816 x 4096: 93 us, 2.02 PFLOP/s, with the tensor pipe 43% and
+// the issue slots 42% busy: neither is the bound, the handing over is.
 //
 // Two-CTA products (256 x 256 a pair, half the rows of b loaded by each) were
 // slower, 189 us at that size against 135 of the narrow kernel: loads that

@@ -8,11 +8,13 @@
 //
 // Both divisions and the product are correctly rounded fp32 operations, so a
 // code does not depend on which of the kernels made it.  Each value is read
-// once; HBM is the bound (2 bytes in and 1 out for each code of a 16-bit
-// input).
+// once; HBM is the bound of the row form (2 bytes in and 1 out for each code of
+// a 16-bit input).  The tile forms reach 0.57 of a copy's rate: a CTA has one
+// tile, so its loads, sums and stores follow one another, and 512 or 1024 CTAs
+// on 304 places end unevenly.
 //
 // 16-bit input: rows of 8192 x 4096 19.3 us, 5.2 TB/s (0.78 of a copy's rate);
-// columns of 4096 x 4096 13.4 us, rows and columns from one read 17.7; 128 x 128
+// columns of 4096 x 4096 13.2 us, rows and columns from one read 17.7; 128 x 128
 // blocks of 2048 x 4096 with both orders of the codes 8.8 us.  Rows off the
 // 16-byte boundaries are read value by value: 8192 x 4095 31 us.
 #include "row_ops.cuh"

@@ -8,9 +8,9 @@
 // types), and the second sum runs on values already at hand.  The bound is
 // HBM; what there is besides are the two sums of a row, each a latency of two
 // shuffles' trees and a barrier, which the rows on their way hide in part.
-// T=4096, H=4096 with the next norm: 16-bit 27 us, 5.0 TB/s (0.75 of a copy's
-// rate); fp32 stream 34 us, 6.0 TB/s; H=8192, 16-bit 49 us, 5.5 TB/s.  One row
-// of T: 4 us, launch and two sums.
+// T=4096, H=4096 with the next norm: 16-bit 26.5 us, 5.1 TB/s (0.76 of a copy's
+// rate); fp32 stream 35 us, 5.7 TB/s; H=8192, 16-bit 49 us, 5.5 TB/s.  One row
+// of T: 4 us, launch and two sums (2.7 us in a graph).
 #include "norm_block.cuh"
 
 namespace qmoe {
@@ -213,8 +213,8 @@ struct Fwd {
             a.lie_step = lie.step;
             a.fp32 = aligned16(a.w) && aligned16(a.w_next) && aligned16(a.gate_mode == QMOE_GATE_COL ? a.gate : nullptr);
             const bool at_zero = lie.at_zero() && a.fp32;
-            // a warp more for the shift is worth it (T=4096, 16-bit: H=2047 21.5 us against 30 value by value, H=4095 51.5
-            // against 56), twice the values a thread are not (H=8191 145 us against 106)
+            // a warp more for the shift is worth it (T=4096, 16-bit: H=2047 21 us against 30 value by value, H=4095 50.5
+            // against 56), twice the values a thread are not (H=8191 145 us against 105)
             Shape s = shape_of(a.cols, W, 16, false);
             const bool shifted = !at_zero && fits(s, lie);
             if (!at_zero && !shifted) s = shape_for(a.cols, 1, 16);

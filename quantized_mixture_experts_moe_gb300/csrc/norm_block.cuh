@@ -18,7 +18,7 @@ inline bool gate_mode_ok(int m) { return m >= QMOE_GATE_NONE && m <= QMOE_GATE_F
 // before the row are aligned in each of them, and since a CTA's rows lie a
 // multiple of 8 apart, the shift is one for all rows of a CTA.  Odd widths of
 // contiguous tensors are of this kind; others go value by value (T=4096, H=4097,
-// 16-bit: forward 52 us against 82 value by value, gradient 120 against 332).
+// 16-bit: forward 51 us against 82 value by value, gradient 106 against 332).
 struct Lie {
     int vec;
     int64_t cols;
@@ -88,9 +88,10 @@ inline bool fits(const Shape& s, const Lie& lie) {
 // their work, and one thread's bulk copies cost the others no instructions
 // (with a cp.async by each thread for its own values the kernels were bound by
 // instruction issue).  Rows that do not start on 16-byte boundaries are copied
-// by the 16-byte granules that they lie in; a granule reaches past its row but
-// never past the first and the last value of the matrix, where the values are
-// copied one by one.
+// by the 16-byte granules that they lie in.  A granule reaches past its row;
+// before the first row and after the last one values are copied one by one
+// instead.  (Rows narrower than a granule may still share one with what lies
+// before or after the matrix: it is read, in the same 16 bytes, and not used.)
 
 // One matrix that a kernel reads: rows of `cols` values, at `off` in a stage.
 struct Source {
@@ -154,8 +155,8 @@ struct Feed {
     }
 };
 
-// How a kernel reads a row: by accesses of VEC columns.  AT_ZERO: all rows begin
-// and end on an access's boundaries; SHIFTED: rows begin `shift` columns past
+// How a kernel reads a row: by accesses of VEC columns.  Without SHIFT all rows
+// begin and end on an access's boundaries; with it they begin `shift` columns past
 // one, so that a row's first and last access reach past it.  (A kernel that
 // keeps both cases open spends 5 to 20% more on the first: H=4096 forward 28 us
 // for 26, gradient 70 for 59.)

@@ -6,15 +6,19 @@
 //   dw_n = sum_t dn x,  dw = sum_t dz t,  dg = alpha z D  (z = t w)
 //
 // norm_pre's gradient is the first line alone.  As in the forward, a row lives
-// in registers and is read and written once; HBM is the bound (6 values a
-// column for the whole sandwich).  The sums over rows stay in registers (rows
-// of up to 16 values a thread) or in shared memory words that one thread owns,
-// over all the rows of a CTA; each CTA then writes one partial row, and a
-// second launch adds the partial rows in a fixed order, so no atomic decides
-// an order.  T=8192, H=4096, fp32 stream and 16-bit block, the whole sandwich:
-// 108 us, 5.6 TB/s (0.84 of a copy's rate); T=4096, 16-bit 59 us, H=8192 121 us.
-// Rows past 8192 columns (32 values a thread, spilled in part, no ring) run at
-// 1.6 TB/s: T=4096, H=12288, 16-bit 380 us.
+// in registers and is read and written once (6 values a column for the whole
+// sandwich).  The sums over rows stay in registers (rows of up to 16 values a
+// thread) or in shared memory words that one thread owns, over all the rows of
+// a CTA; each CTA then writes one partial row, and a second launch adds the
+// partial rows in a fixed order, so no atomic decides an order.
+//
+// HBM is the bound beside an fp32 stream: T=8192, H=4096, the whole sandwich
+// 106 us, 5.7 TB/s (0.85 of a copy's rate).  With a 16-bit one it is not: an SM
+// has one row of 4096 columns at a time, whose wait, two sums and barriers take
+// as long for two thirds of the bytes: T=4096 58 us, 3.5 TB/s (0.52), H=8192
+// 106 us (128 with a gate for each column); norm_pre's, one sum, 32 us (0.63)
+// and 52.  Rows past 8192 columns (32 values a thread, spilled in part, no ring)
+// run at 1.6 TB/s: T=4096, H=12288, 16-bit 374 us.
 #include "norm_block.cuh"
 
 namespace qmoe {
@@ -324,7 +328,7 @@ __global__ void __launch_bounds__(1024) norm_sum_kernel(const SumArgs a) {
 
 // The threads of a row go by the columns alone, not by the access.  No warp more
 // for a shift: that would leave an SM fewer rows, and value by value is faster
-// then (T=4096, 16-bit: H=2047 51 us against 67, H=4095 94 against 120).
+// then (T=4096, 16-bit: H=2047 50 us against 67, H=4095 93 against 120).
 inline Shape cut_of(int64_t cols) { return shape_of(cols, 8, 8, true); }
 // CTAs of a launch: one wave of 512 threads an SM.
 inline int per_sm_of(const Shape& s) { return 512 / (s.threads * s.rows_per_cta); }
@@ -385,8 +389,8 @@ struct Bwd {
         static int go(BwdArgs& a, cudaStream_t st) {
             Shape s = cut_of(a.cols);
             // rows of 8 values a thread: in two accesses of 4 columns (T=4096, H=4096, 16-bit 59 us against 61 in one of 8,
-            // H=1024 21 against 24); wider rows by 8 where the types allow it
-            // (H=8192: 117 us against 131 when it was chosen)
+            // H=1024 21 against 24); wider rows by 8 where the types allow it (H=8192: 117 us against 131; all when it was
+            // chosen)
             constexpr int WIDE = wide_vec<RT, YT>();
             const int W = s.values() == 8 ? 4 : WIDE;
             Lie lie = {W, a.cols};

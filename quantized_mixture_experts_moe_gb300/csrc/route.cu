@@ -21,7 +21,8 @@
 // scores.  Instruction issue, not the 2 E bytes of a row, is the bound.
 // Probabilities are summed per lane over a warp's tokens, then over a CTA's
 // warps, then over CTAs, in a fixed order, so the loss has the same bits every
-// time.
+// time.  Exponentials are __expf's: a relative error of about |logit - maximum|
+// roundings, which is most for the experts of least weight.
 //
 // T=8192, E=512, k=8, bf16: 9.7 us without statistics (0.9 TB/s), 17.5 with
 // them, which takes a second launch (up to 16 tokens one CTA does both: T=1
