@@ -159,13 +159,17 @@ def test_linear_backward_refuses_shapes_that_do_not_go_together():
 
 def test_tensors_of_two_devices_are_refused(lib):
     # tensors that say where they lie and have no memory: a call ends before it asks for their pointers
-    from torch._subclasses.fake_tensor import FakeTensorMode
+    class Placed(torch.Tensor):
+        @classmethod
+        def __torch_dispatch__(cls, func, types, args=(), kwargs=None):
+            raise NotImplementedError(func)
 
-    with FakeTensorMode():
-        a, b = ([torch.empty(s, device=f"cuda:{i}") for s in ((4, 64), (64,), (4,))] for i in range(2))
-        codes = [torch.empty(4, 64, dtype=torch.uint8, device=f"cuda:{i}") for i in range(2)]
-        scales = [torch.empty(4, 1, device=f"cuda:{i}") for i in range(2)]
-        word = [torch.empty(1, dtype=torch.int32, device=f"cuda:{i}") for i in range(2)]
+    def at(i, *shape, dtype=torch.float32):
+        return torch.Tensor._make_wrapper_subclass(Placed, shape, dtype=dtype, device=torch.device("cuda", i))
+
+    a, b = ([at(i, 4, 64), at(i, 64), at(i, 4)] for i in range(2))
+    codes, scales = [at(i, 4, 64, dtype=torch.uint8) for i in range(2)], [at(i, 4, 1) for i in range(2)]
+    word = [at(i, 1, dtype=torch.int32) for i in range(2)]
     r = qb.Routing()
     r.ids, r.w, r.lse, r.counts, r.renorm, r.scale, r.coef = word[0], a[1], a[2], word[0], True, 1.0, 1.0
     for call in (lambda: qb.norm_pre(a[0], b[1]),
