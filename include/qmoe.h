@@ -76,7 +76,7 @@ typedef enum {
 } qmoe_status;
 
 /* Bits of the device status word. */
-enum { QMOE_DEV_BAD_EXPERT_ID = 1, QMOE_DEV_WAIT_TIMEOUT = 2 };
+enum { QMOE_DEV_BAD_EXPERT_ID = 1, QMOE_DEV_WAIT_TIMEOUT = 2, QMOE_DEV_BAD_OFFSETS = 4 };
 
 typedef struct {
     int32_t T, k, H, I, E;
@@ -663,6 +663,99 @@ size_t qmoe_fp8_linear_workspace_bytes(int64_t M, int64_t K);
 int qmoe_fp8_linear(int64_t M, int64_t N, int64_t K, int x_dtype, const void* x, int64_t ldx, const qmoe_fp8_mat* w,
                     void* y, int y_dtype, int64_t ldy, int32_t* dev_status, void* ws, size_t ws_bytes,
                     qmoe_stream_t stream);
+
+/* ---------------------------------------------------------------- training the experts: grouped products
+ *
+ * Rows in expert order (slots): expert e has the rows offsets[e] <= s <
+ * offsets[e + 1] of P, as qmoe_align_sort gives them; rows from offsets[E] on
+ * have no expert.  Weights [E, N, K], 16 bits (dtype QMOE_BF16 or QMOE_F16, of all
+ * matrices of a call), row stride ldw, w_expert elements from expert to expert.
+ *
+ * qmoe_expert_linear -- y[s][n] = sum_k w[e][n][k] x[s][k].
+ * qmoe_expert_linear_dx -- dx[s][k] = sum_n w[e][n][k] dy[s][n].
+ * qmoe_expert_linear_dw -- dw[e][n][k] = sum_s dy[s][n] x[s][k], contiguous [E, N, K];
+ *   zeros for an expert without rows.
+ * Sums are fp32 and rounded once, to dtype or, where y_dtype, dx_dtype or dw_dtype
+ * is QMOE_F32, not at all.  Rows of y and dx without an expert are zeros.  The same
+ * inputs give the same bits.
+ * pairs (may be NULL) int32 [P]: x has x_rows rows and the row of slot s is
+ *   x[pairs[s] / k], as for sorted_pair_ids of qmoe_align_sort and x token by
+ *   token; an entry below 0 or past x counts as a row of zeros.  Without pairs x
+ *   has P rows, and k and x_rows are ignored.
+ * offsets int32 [E + 1] from 0 to at most P, none below the one before it; else bit
+ *   QMOE_DEV_BAD_OFFSETS of *dev_status is set, and which rows belong to which
+ *   expert is undefined.  QMOE_DEV_WAIT_TIMEOUT as for qmoe_fp8_matmul.
+ * An x, dy or w whose base or strides are no multiples of 16 bytes is first copied
+ * into the workspace (256-byte aligned), which then needs the sum of
+ * qmoe_expert_copy_bytes(rows, columns) of each such operand (for w E * N rows);
+ * without such an operand ws may be NULL.  E <= 1024, other sizes <= 2^30. */
+size_t qmoe_expert_copy_bytes(int64_t rows, int64_t cols);
+int qmoe_expert_linear(int64_t P, int E, int64_t N, int64_t K, int dtype, const void* x, int64_t ldx, int64_t x_rows,
+                       const int32_t* pairs, int k, const void* w, int64_t ldw, int64_t w_expert,
+                       const int32_t* offsets, void* y, int y_dtype, int64_t ldy, int32_t* dev_status, void* ws,
+                       size_t ws_bytes, qmoe_stream_t stream);
+int qmoe_expert_linear_dx(int64_t P, int E, int64_t N, int64_t K, int dtype, const void* dy, int64_t lddy,
+                          const void* w, int64_t ldw, int64_t w_expert, const int32_t* offsets, void* dx, int dx_dtype,
+                          int64_t lddx, int32_t* dev_status, void* ws, size_t ws_bytes, qmoe_stream_t stream);
+int qmoe_expert_linear_dw(int64_t P, int E, int64_t N, int64_t K, int dtype, const void* dy, int64_t lddy,
+                          const void* x, int64_t ldx, int64_t x_rows, const int32_t* pairs, int k,
+                          const int32_t* offsets, void* dw, int dw_dtype, int32_t* dev_status, void* ws,
+                          size_t ws_bytes, qmoe_stream_t stream);
+
+/* ---------------------------------------------------------------- training the experts: SwiGLU, weighted sum
+ *
+ * qmoe_swiglu -- h = silu(g) u for rows gu = [g, u] [rows, 2 I], silu(v) = v s(v),
+ *   s(v) = 1 / (1 + exp(-v)).  gu, h of type dtype.
+ * qmoe_swiglu_backward -- dg = dh u s (1 + g (1 - s)), du = dh g s, dgu = [dg, du];
+ *   h (NULL: not made) as qmoe_swiglu gives it.  dgu may be gu. */
+int qmoe_swiglu(int64_t rows, int64_t I, int dtype, const void* gu, int64_t ldgu, void* h, int64_t ldh,
+                qmoe_stream_t stream);
+int qmoe_swiglu_backward(int64_t rows, int64_t I, int dtype, const void* dh, int64_t lddh, const void* gu, int64_t ldgu,
+                         void* dgu, int64_t lddgu, void* h, int64_t ldh, qmoe_stream_t stream);
+
+/* qmoe_weighted_sum -- qmoe_combine for any type, width and stride:
+ *   out[t] = sum_j w[t][j] y[pair_slot[t][j]]  (w NULL: 1, the gradient of a gather),
+ *   summed in fp32 with j ascending.  y [P, H], out [T, H] of type dtype; a slot
+ *   outside [0, P) contributes nothing.
+ * qmoe_weighted_sum_backward -- dy[pair_slot[t][j]] = w[t][j] dout[t], zeros in the
+ *   rows of dy from *routed on (offsets + E of qmoe_align_sort); dw[t][j] =
+ *   <y[pair_slot[t][j]], dout[t]>, 0 for a pair without a slot.  y and dw both or
+ *   neither (NULL).  No slot may be there twice.  H <= 2^30, T * k < 2^31, P < 2^31. */
+int qmoe_weighted_sum(int64_t T, int k, int64_t P, int64_t H, int dtype, const void* y, int64_t ldy, const float* w,
+                      const int32_t* pair_slot, void* out, int64_t ldo, qmoe_stream_t stream);
+int qmoe_weighted_sum_backward(int64_t T, int k, int64_t P, int64_t H, int dtype, const void* dout, int64_t lddout,
+                               const void* y, int64_t ldy, const float* w, const int32_t* pair_slot,
+                               const int32_t* routed, void* dy, int64_t lddy, float* dw, qmoe_stream_t stream);
+
+/* ---------------------------------------------------------------- 4-bit products of few tokens
+ *
+ * Weights as the checkpoint holds them, not prepacked: codes uint8 [N, K / 2]
+ * (16-byte aligned, rows and experts one behind the other; element 2i in the low
+ * nibble of byte i) and a scale for each `group` values of a row.
+ *   QMOE_W4_INT4  value (n - 8) s, s fp16 [N, K / group], group 32, 64 or 128;
+ *   QMOE_W4_E2M1  E2M1 elements, s E8M0 bytes [N, K / 32], group 32.
+ * K is a multiple of group.
+ *
+ * qmoe_w4_linear -- y[t] = W x[t], or with ids int32 [T, k] of E matrices the
+ *   products of each token with its experts, y [T * k, N]:
+ *   y[t k + j] = W[ids[t][j]] x[t]; a row whose id is outside [0, E) is zeros.
+ *   (ids NULL: one matrix, E = k = 1.)  x [T, K] and y of type dtype (QMOE_BF16 or
+ *   QMOE_F16; y_dtype may be QMOE_F32).  Codes are multiplied exactly, sums and
+ *   scales are fp32, up to QMOE_W4_FEW tokens (and always with ids); above it W is
+ *   widened into the workspace, rounded to dtype, for the grouped product.
+ * qmoe_w4_linear_dx -- dx = dy W for one matrix, W widened as above.
+ * ws of qmoe_w4_workspace_bytes(T, N, K, dx) bytes (dx 0 for the product, 1 for the
+ * gradient; 0 bytes: NULL), 256-byte aligned, and dev_status as for
+ * qmoe_expert_linear. */
+enum { QMOE_W4_INT4 = 0, QMOE_W4_E2M1 = 1 };
+#define QMOE_W4_FEW 32
+size_t qmoe_w4_workspace_bytes(int64_t T, int64_t N, int64_t K, int dx);
+int qmoe_w4_linear(int64_t T, int k, int E, int64_t N, int64_t K, int format, int group, int dtype, const void* x,
+                   int64_t ldx, const uint8_t* w, const void* s, const int32_t* ids, void* y, int y_dtype, int64_t ldy,
+                   int32_t* dev_status, void* ws, size_t ws_bytes, qmoe_stream_t stream);
+int qmoe_w4_linear_dx(int64_t T, int64_t N, int64_t K, int format, int group, int dtype, const void* dy, int64_t lddy,
+                      const uint8_t* w, const void* s, void* dx, int dx_dtype, int64_t lddx, int32_t* dev_status,
+                      void* ws, size_t ws_bytes, qmoe_stream_t stream);
 
 #ifdef __cplusplus
 }

@@ -20,6 +20,7 @@ LIB_PATH = os.path.join(_PKG, "libqmoe.so")
 SCHEME_ID = {"w4a16": 0, "mxfp4": 1, "w8a8": 2, "w4a8": 3}
 DEV_BAD_EXPERT_ID = 1
 DEV_WAIT_TIMEOUT = 2
+DEV_BAD_OFFSETS = 4
 
 
 class QmoeError(RuntimeError):
@@ -109,6 +110,22 @@ SIGNATURES = {
     "qmoe_fp8_matmul": ([_i64, _i64, _i64, _MP, _MP, _vp, _i32, _i64, _vp, _vp], _i32),
     "qmoe_fp8_linear_workspace_bytes": ([_i64, _i64], _sz),
     "qmoe_fp8_linear": ([_i64, _i64, _i64, _i32, _vp, _i64, _MP, _vp, _i32, _i64, _vp, _vp, _sz, _vp], _i32),
+    "qmoe_expert_copy_bytes": ([_i64, _i64], _sz),
+    "qmoe_expert_linear": ([_i64, _i32, _i64, _i64, _i32, _vp, _i64, _i64, _vp, _i32, _vp, _i64, _i64, _vp, _vp, _i32, _i64, _vp,
+                            _vp, _sz, _vp], _i32),
+    "qmoe_expert_linear_dx": ([_i64, _i32, _i64, _i64, _i32, _vp, _i64, _vp, _i64, _i64, _vp, _vp, _i32, _i64, _vp, _vp, _sz,
+                               _vp], _i32),
+    "qmoe_expert_linear_dw": ([_i64, _i32, _i64, _i64, _i32, _vp, _i64, _vp, _i64, _i64, _vp, _i32, _vp, _vp, _i32, _vp, _vp,
+                               _sz, _vp], _i32),
+    "qmoe_swiglu": ([_i64, _i64, _i32, _vp, _i64, _vp, _i64, _vp], _i32),
+    "qmoe_swiglu_backward": ([_i64, _i64, _i32, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _i64, _vp], _i32),
+    "qmoe_weighted_sum": ([_i64, _i32, _i64, _i64, _i32, _vp, _i64, _vp, _vp, _vp, _i64, _vp], _i32),
+    "qmoe_weighted_sum_backward": ([_i64, _i32, _i64, _i64, _i32, _vp, _i64, _vp, _i64, _vp, _vp, _vp, _vp, _i64, _vp, _vp],
+                                   _i32),
+    "qmoe_w4_workspace_bytes": ([_i64, _i64, _i64, _i32], _sz),
+    "qmoe_w4_linear": ([_i64, _i32, _i32, _i64, _i64, _i32, _i32, _i32, _vp, _i64, _vp, _vp, _vp, _vp, _i32, _i64, _vp, _vp,
+                        _sz, _vp], _i32),
+    "qmoe_w4_linear_dx": ([_i64, _i64, _i64, _i32, _i32, _i32, _vp, _i64, _vp, _vp, _vp, _i32, _i64, _vp, _vp, _sz, _vp], _i32),
     "qmoe_moe_forward": ([_i32, _DP, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp], _i32),
 }
 
@@ -636,3 +653,103 @@ def fp8_linear_backward(dy, x, wt_q, w_s, dev_status=None, stream=None):
         with torch.cuda.stream(stream):
             return fp8_linear_backward(dy, x, wt_q, w_s, dev_status)
     return (_bind or _load_bind()).fp8_linear_backward(dy, x, wt_q, w_s, _status(dy) if dev_status is None else dev_status)
+
+
+# ------------------------------------------------------------------ the experts in training, and 4-bit products of few tokens
+#
+# As the calls above in every rule.  The rows of the experts lie in expert
+# order, offsets int32 [E + 1] as qmoe_align_sort gives them; rows from
+# offsets[E] on have no expert and get zeros.
+
+
+def align_sort(topk_ids, E, dev_status=None, ws=None, stream=None):
+    """The routed pairs of topk_ids int32 [T, k] in expert order: (offsets int32 [E + 1], pairs int32 [T * k], the pair t * k + j
+    of each slot, pair_slot int32 [T, k], the slot of each pair), -1 where there is none: ids outside [0, E) are routed
+    nowhere (and set DEV_BAD_EXPERT_ID in dev_status).  What expert_linear, combine and their gradients take."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return align_sort(topk_ids, E, dev_status, ws)
+    if topk_ids.dim() != 2 or topk_ids.dtype != torch.int32:
+        raise ValueError(f"expected int32 ids of shape [tokens, k], got {tuple(topk_ids.shape)} of {topk_ids.dtype}")
+    T, k = topk_ids.shape
+    d = dims(T, k, 32, 32, E)  # the hidden sizes have no part in the sort
+    with torch.cuda.device(topk_ids.device):
+        new = functools.partial(torch.empty, dtype=torch.int32, device=topk_ids.device)
+        counts, offsets, pairs, pair_slot = new(E), new(E + 1), new(T * k), new((T, k))
+        if dev_status is None:
+            dev_status = torch.zeros(1, dtype=torch.int32, device=topk_ids.device)
+        if ws is None:
+            ws = alloc_workspace(workspace_bytes(d), topk_ids.device)
+        qmoe_align_sort(d, topk_ids, counts, offsets, pairs, pair_slot, dev_status, ws)
+    return offsets, pairs, pair_slot
+
+
+def expert_linear(x, w, offsets, pairs=None, k=1, out_dtype=None, dev_status=None, ws=None, stream=None):
+    """y[s] = w[e] x[s] for the rows s of each expert e: x [P, K], w [E, N, K] of one 16-bit type, y [P, N] of that type or
+    out_dtype float32.  With pairs int32 [P] x is [T, K], token by token, and the row of slot s is x[pairs[s] // k]."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return expert_linear(x, w, offsets, pairs, k, out_dtype, dev_status, ws)
+    return (_bind or _load_bind()).expert_linear(x, w, offsets, pairs, k, out_dtype, _status(x) if dev_status is None else dev_status, ws)
+
+
+def expert_linear_backward(dy, x, w, offsets, pairs=None, k=1, dw_dtype=None, need_dx=True, need_dw=True, dev_status=None, ws=None,
+                           stream=None):
+    """Gradients of expert_linear: (dx [P, K] in x's type, dw [E, N, K] in fp32, or the weights' type by dw_dtype), None for one
+    that is not needed.  dx is one row for each slot; with pairs the gradient of x is combine(dx, None, pair_slot)."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return expert_linear_backward(dy, x, w, offsets, pairs, k, dw_dtype, need_dx, need_dw, dev_status, ws)
+    return (_bind or _load_bind()).expert_linear_backward(dy, x, w, offsets, pairs, k, dw_dtype, need_dx, need_dw,
+                                                          _status(dy) if dev_status is None else dev_status, ws)
+
+
+def swiglu(gu, stream=None):
+    """h = silu(g) * u for rows gu = [g, u] [P, 2 I]."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return swiglu(gu)
+    return (_bind or _load_bind()).swiglu(gu)
+
+
+def swiglu_backward(dh, gu, h_too=False, stream=None):
+    """Gradient of swiglu: (dgu [P, 2 I], h again where h_too, for the next product's gradient, else None)."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return swiglu_backward(dh, gu, h_too)
+    return (_bind or _load_bind()).swiglu_backward(dh, gu, h_too)
+
+
+def combine(y, w, pair_slot, stream=None):
+    """out[t] = sum over j of w[t, j] * y[pair_slot[t, j]], j ascending, in y's type: y [P, H], w fp32 [T, k] (None: 1, the
+    gradient of a gather).  Slots outside [0, P) contribute nothing."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return combine(y, w, pair_slot)
+    return (_bind or _load_bind()).combine(y, w, pair_slot)
+
+
+def combine_backward(dout, y, w, pair_slot, offsets, stream=None):
+    """Gradients of combine: (dy [P, H], dw fp32 [T, k], None where w is).  The rows of dy from offsets[E] on are zeros."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return combine_backward(dout, y, w, pair_slot, offsets)
+    return (_bind or _load_bind()).combine_backward(dout, y, w, pair_slot, offsets)
+
+
+def w4_linear(x, w_q, w_s, ids=None, out_dtype=None, dev_status=None, ws=None, stream=None):
+    """y = x w^T with 4-bit weights as a checkpoint holds them: codes uint8 [N, K / 2] and scales [N, K / group], float16
+    beside int4 codes (group 32, 64 or 128), uint8 (E8M0) beside E2M1 codes (group 32).  With ids int32 [T, k] the codes and
+    scales are [E, N, ...] and y [T * k, N] holds the products of each token with its experts, for a few tokens."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return w4_linear(x, w_q, w_s, ids, out_dtype, dev_status, ws)
+    return (_bind or _load_bind()).w4_linear(x, w_q, w_s, ids, out_dtype, _status(x) if dev_status is None else dev_status, ws)
+
+
+def w4_linear_backward(dy, w_q, w_s, dev_status=None, ws=None, stream=None):
+    """Gradient of w4_linear's x: dx = dy w in dy's type (the weights are held fixed)."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return w4_linear_backward(dy, w_q, w_s, dev_status, ws)
+    return (_bind or _load_bind()).w4_linear_backward(dy, w_q, w_s, _status(dy) if dev_status is None else dev_status, ws)

@@ -1,5 +1,5 @@
 // Argument marshalling of the calls around the experts (norms, routing, FP8
-// products) between torch tensors and the C ABI: checks, output allocation and
+// products, the experts' products for training, 4-bit products) between torch tensors and the C ABI: checks, output allocation and
 // one call each, no arithmetic.  The kernels take a few microseconds for a
 // single token; marshalled from Python through ctypes a call took 13 to 19 us
 // of host time.  binding.py wraps these functions and documents them.
@@ -14,6 +14,7 @@
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <algorithm>
 #include <array>
 #include <optional>
 #include <sstream>
@@ -559,6 +560,267 @@ PyObject* fp8_linear_backward(const Args& a) {  // dy, x, wt_q, w_s, dev_status
     return tuple_of({dx, dw});
 }
 
+// ------------------------------------------------------------------ the experts' products
+
+// Weights [E, N, K] (or [N, K], one expert) of contiguous columns.
+struct Experts {
+    void* p = nullptr;
+    int64_t E = 1, N = 0, K = 0, ld = 0, stride = 0;
+};
+Experts experts_of(const at::Tensor& w, const char* what) {
+    if (w.dim() != 3) bad(std::string(what) + ": expected weights of shape [experts, outputs, inputs], got " + shape_str(w));
+    on_device(w);
+    Experts m = {w.data_ptr(), w.size(0), w.size(1), w.size(2), w.stride(1), w.stride(0)};
+    if (m.E > 1 << 20) check(QMOE_ERR_UNSUPPORTED, what);
+    if (w.stride(2) != 1 && m.K > 1) refuse(qmoe_error, "qmoe kernels take rows of contiguous columns");
+    if (m.ld < m.K) {
+        if (m.N > 1) refuse(qmoe_error, "qmoe kernels take rows that do not overlap");
+        m.ld = m.K;
+    }
+    if (m.stride < m.ld * (m.N - 1) + m.K) {
+        if (m.E > 1) refuse(qmoe_error, "qmoe kernels take rows that do not overlap");
+        m.stride = m.ld * m.N;
+    }
+    return m;
+}
+bool in_pieces(const void* p, int64_t rows, int64_t ld) {
+    return (reinterpret_cast<uintptr_t>(p) & 15) == 0 && (rows == 1 || ld % 8 == 0);
+}
+size_t copy_of(const Rows& r, int64_t rows, int64_t cols) {
+    return in_pieces(r.p, rows, r.ld) ? 0 : qmoe_expert_copy_bytes(rows, cols);
+}
+size_t copy_of(const Experts& m) {
+    return in_pieces(m.p, m.N, m.ld) && (m.E == 1 || m.stride % 8 == 0) ? 0 : qmoe_expert_copy_bytes(m.E * m.N, m.K);
+}
+// What a call needs of the workspace is mostly nothing: then none is made.
+struct MaybeWorkspace {
+    std::optional<Workspace> held;
+    void* p = nullptr;
+    size_t n = 0;
+    MaybeWorkspace(size_t need, const at::Tensor* given, const at::Tensor& like) {
+        if (!given && !need) return;
+        held.emplace(need, given, like);
+        p = held->p;
+        n = held->n;
+    }
+};
+int same_type(const at::Tensor& a, const at::Tensor& b, const char* what) {
+    if (a.scalar_type() != b.scalar_type()) bad(std::string(what) + " have one type, got " + shape_str(a) + " and " + shape_str(b));
+    const int code = code_of(a.scalar_type());
+    if (code == QMOE_F32) bad(std::string(what) + " are of bfloat16 or float16");
+    return code;
+}
+// The rows in expert order and where they lie in x.
+struct Gathered {
+    int64_t P, rows;
+    Rows x;
+    const int32_t* pairs = nullptr;
+    int k = 1;
+};
+Gathered gathered(const at::Tensor& x, const at::Tensor* pairs, int64_t k, const char* what) {
+    matrix(x, what);
+    Gathered g;
+    g.rows = x.size(0);
+    g.x = rows_of(x, g.rows, x.size(1));
+    g.P = pairs ? pairs->numel() : g.rows;
+    if (pairs) {
+        if (k <= 0 || k > 1 << 20) bad(std::string(what) + ": k is the number of experts of a token");
+        g.pairs = vec_of<int32_t>(pairs, g.P, at::kInt);
+        g.k = (int)k;
+    }
+    return g;
+}
+
+PyObject* expert_linear(const Args& a) {  // x, w, offsets, pairs, k, out_dtype, dev_status, ws
+    const at::Tensor &x = a.tensor(0), &w = a.tensor(1);
+    const Experts m = experts_of(w, "expert_linear");
+    const Gathered g = gathered(x, a.maybe(3), a.whole(4), "expert_linear");
+    if (x.size(1) != m.K) bad("the reduction lengths differ: " + shape_str(x) + " and " + shape_str(w));
+    const int code = same_type(x, w, "x and w");
+    const auto yt = a.dtype(5, x.scalar_type());
+    const at::Tensor y = make({g.P, m.N}, yt, x);
+    const int yc = code_of(yt);
+    const int32_t* offsets = vec_of<int32_t>(&a.tensor(2), m.E + 1, at::kInt);
+    const MaybeWorkspace ws(copy_of(g.x, g.rows, m.K) + copy_of(m), a.maybe(7), x);
+    check(qmoe_expert_linear(g.P, (int)m.E, m.N, m.K, code, g.x.p, g.x.ld, g.rows, g.pairs, g.k, m.p, m.ld, m.stride,
+                             offsets, y.data_ptr(), yc, m.N, status_of(a.tensor(6)), ws.p, ws.n, stream_of(x)),
+          "qmoe_expert_linear");
+    return wrap(y);
+}
+
+PyObject* expert_linear_backward(const Args& a) {  // dy, x, w, offsets, pairs, k, dw_dtype, need_dx, need_dw, dev_status, ws
+    const at::Tensor &dy = a.tensor(0), &x = a.tensor(1), &w = a.tensor(2);
+    const Experts m = experts_of(w, "expert_linear_backward");
+    const Gathered g = gathered(x, a.maybe(4), a.whole(5), "expert_linear_backward");
+    if (x.size(1) != m.K) bad("the reduction lengths differ: " + shape_str(x) + " and " + shape_str(w));
+    const Rows d = rows_of(dy, g.P, m.N);
+    const int code = same_type(x, w, "x and w");
+    same_type(dy, w, "dy and w");
+    const auto wt = a.dtype(6, at::kFloat);
+    const int32_t* offsets = vec_of<int32_t>(&a.tensor(3), m.E + 1, at::kInt);
+    int32_t* const status = status_of(a.tensor(9));
+    const qmoe_stream_t st = stream_of(dy);
+    const size_t cd = copy_of(d, g.P, m.N), cx = copy_of(g.x, g.rows, m.K), cw = copy_of(m);
+    const bool to_x = a.truth(7), to_w = a.truth(8);
+    const size_t need = std::max(to_x ? cd + cw : 0, to_w ? cd + cx : 0);
+    const MaybeWorkspace ws(need, a.maybe(10), dy);
+    at::Tensor dx, dw;
+    if (to_x) {
+        dx = make({g.P, m.K}, x.scalar_type(), x);
+        check(qmoe_expert_linear_dx(g.P, (int)m.E, m.N, m.K, code, d.p, d.ld, m.p, m.ld, m.stride, offsets, dx.data_ptr(),
+                                    code, m.K, status, ws.p, ws.n, st),
+              "qmoe_expert_linear_dx");
+    }
+    if (to_w) {
+        dw = make({m.E, m.N, m.K}, wt, w);
+        check(qmoe_expert_linear_dw(g.P, (int)m.E, m.N, m.K, code, d.p, d.ld, g.x.p, g.x.ld, g.rows, g.pairs, g.k, offsets,
+                                    dw.data_ptr(), code_of(wt), status, ws.p, ws.n, st),
+              "qmoe_expert_linear_dw");
+    }
+    return tuple_of({dx, dw});
+}
+
+PyObject* swiglu(const Args& a) {  // gu
+    const at::Tensor& gu = a.tensor(0);
+    matrix(gu, "swiglu");
+    const int64_t P = gu.size(0), I = gu.size(1) / 2;
+    if (gu.size(1) != 2 * I) bad("swiglu takes gate and up columns, [rows, 2 I]; got " + shape_str(gu));
+    const Rows r = rows_of(gu, P, 2 * I);
+    const int code = code_of(gu.scalar_type());
+    const at::Tensor h = make({P, I}, gu.scalar_type(), gu);
+    check(qmoe_swiglu(P, I, code, r.p, r.ld, h.data_ptr(), I, stream_of(gu)), "qmoe_swiglu");
+    return wrap(h);
+}
+
+PyObject* swiglu_backward(const Args& a) {  // dh, gu, h_too
+    const at::Tensor &dh = a.tensor(0), &gu = a.tensor(1);
+    matrix(dh, "swiglu_backward");
+    const int64_t P = dh.size(0), I = dh.size(1);
+    const Rows d = rows_of(dh, P, I), r = rows_of(gu, P, 2 * I);
+    const int code = code_of(gu.scalar_type());
+    if (dh.scalar_type() != gu.scalar_type()) bad("dh has gu's type");
+    const at::Tensor dgu = make({P, 2 * I}, gu.scalar_type(), gu);
+    at::Tensor h;
+    if (a.truth(2)) h = make({P, I}, gu.scalar_type(), gu);
+    check(qmoe_swiglu_backward(P, I, code, d.p, d.ld, r.p, r.ld, dgu.data_ptr(), 2 * I, at_of(h), I, stream_of(gu)),
+          "qmoe_swiglu_backward");
+    return tuple_of({dgu, h});
+}
+
+struct Slots {
+    int64_t T, k;
+    const int32_t* p;
+};
+Slots slots_of(const at::Tensor& t, const char* what) {
+    if (t.dim() != 2) bad(std::string(what) + ": expected pair_slot of shape [tokens, k], got " + shape_str(t));
+    if (t.size(1) > 1 << 20) check(QMOE_ERR_UNSUPPORTED, what);
+    return {t.size(0), t.size(1), vec_of<int32_t>(&t, t.numel(), at::kInt)};
+}
+
+PyObject* combine(const Args& a) {  // y, w, pair_slot
+    const at::Tensor& y = a.tensor(0);
+    matrix(y, "combine");
+    const Slots s = slots_of(a.tensor(2), "combine");
+    const int64_t P = y.size(0), H = y.size(1);
+    const Rows r = rows_of(y, P, H);
+    const int code = code_of(y.scalar_type());
+    const float* w = floats(a.maybe(1), s.T * s.k);
+    const at::Tensor out = make({s.T, H}, y.scalar_type(), y);
+    check(qmoe_weighted_sum(s.T, (int)s.k, P, H, code, r.p, r.ld, w, s.p, out.data_ptr(), H, stream_of(y)), "qmoe_weighted_sum");
+    return wrap(out);
+}
+
+PyObject* combine_backward(const Args& a) {  // dout, y, w, pair_slot, offsets
+    const at::Tensor &dout = a.tensor(0), &y = a.tensor(1), *w = a.maybe(2), &offsets = a.tensor(4);
+    matrix(y, "combine_backward");
+    const Slots s = slots_of(a.tensor(3), "combine_backward");
+    const int64_t P = y.size(0), H = y.size(1), E = offsets.numel() - 1;
+    const Rows d = rows_of(dout, s.T, H), r = rows_of(y, P, H);
+    const int code = code_of(y.scalar_type());
+    if (dout.scalar_type() != y.scalar_type()) bad("dout has y's type");
+    if (E < 0) bad("combine_backward: expected offsets of shape [experts + 1], got " + shape_str(offsets));
+    const int32_t* routed = vec_of<int32_t>(&offsets, E + 1, at::kInt) + E;
+    const float* wp = floats(w, s.T * s.k);
+    at::Tensor dy = make({P, H}, y.scalar_type(), y), dw;
+    if (w) dw = make({s.T, s.k}, at::kFloat, y);
+    if (P == 0 && w) dw.zero_();
+    else
+        check(qmoe_weighted_sum_backward(s.T, (int)s.k, P, H, code, d.p, d.ld, w ? r.p : nullptr, r.ld, wp, s.p, routed,
+                                         dy.data_ptr(), H, f32_of(dw), stream_of(y)),
+              "qmoe_weighted_sum_backward");
+    return tuple_of({dy, dw});
+}
+
+// ------------------------------------------------------------------ 4-bit products
+
+struct Codes4 {
+    int64_t E = 1, N, K;
+    int format, group;
+    const uint8_t* w;
+    const void* s;
+};
+Codes4 codes4_of(const at::Tensor& q, const at::Tensor& s, bool experts, const char* what) {
+    const int64_t d = experts ? 3 : 2;
+    if (q.dim() != d || s.dim() != d || q.scalar_type() != at::kByte)
+        bad(std::string(what) + ": expected uint8 codes and scales of " + (experts ? "[experts, outputs, ...]" : "[outputs, ...]") +
+            ", got " + shape_str(q) + " and " + shape_str(s));
+    Codes4 c;
+    c.E = experts ? q.size(0) : 1;
+    c.N = q.size(d - 2);
+    c.K = q.size(d - 1) * 2;
+    const int64_t groups = s.size(d - 1);
+    if ((experts && s.size(0) != c.E) || s.size(d - 2) != c.N || groups <= 0 || c.K % groups || c.K / groups > 1 << 20)
+        bad(std::string(what) + ": codes and scales do not go together: " + shape_str(q) + " and " + shape_str(s));
+    c.group = (int)(c.K / groups);
+    if (s.scalar_type() == at::kHalf) c.format = QMOE_W4_INT4;
+    else if (s.scalar_type() == at::kByte) c.format = QMOE_W4_E2M1;
+    else bad(std::string(what) + ": scales are float16 (int4 codes) or uint8 (E2M1 codes), got " + shape_str(s));
+    if (c.E > 1 << 20) check(QMOE_ERR_UNSUPPORTED, what);
+    on_device(q);
+    on_device(s);
+    if (!q.is_contiguous() || !s.is_contiguous()) refuse(qmoe_error, "qmoe kernels take contiguous tensors");
+    c.w = static_cast<const uint8_t*>(q.data_ptr());
+    c.s = s.data_ptr();
+    return c;
+}
+
+PyObject* w4_linear(const Args& a) {  // x, w_q, w_s, ids, out_dtype, dev_status, ws
+    const at::Tensor &x = a.tensor(0), *ids = a.maybe(3);
+    matrix(x, "w4_linear");
+    const Codes4 c = codes4_of(a.tensor(1), a.tensor(2), ids != nullptr, "w4_linear");
+    const int64_t T = x.size(0), k = ids ? (ids->dim() == 2 ? ids->size(1) : -1) : 1;
+    if (ids && (k <= 0 || k > 65535 || ids->size(0) != T)) bad("w4_linear: expected ids of shape [tokens, k], got " + shape_str(*ids));
+    if (x.size(1) != c.K) bad("the reduction lengths differ: " + shape_str(x) + " and " + shape_str(a.tensor(1)));
+    const Rows r = rows_of(x, T, c.K);
+    const int code = code_of(x.scalar_type());
+    if (code == QMOE_F32) bad("w4_linear: x is of bfloat16 or float16");
+    const auto yt = a.dtype(4, x.scalar_type());
+    const int yc = code_of(yt);
+    const at::Tensor y = make({T * k, c.N}, yt, x);
+    const MaybeWorkspace ws(ids ? 0 : qmoe_w4_workspace_bytes(T, c.N, c.K, 0), a.maybe(6), x);
+    check(qmoe_w4_linear(T, (int)k, (int)c.E, c.N, c.K, c.format, c.group, code, r.p, r.ld, c.w, c.s,
+                         vec_of<int32_t>(ids, T * k, at::kInt), y.data_ptr(), yc, c.N, status_of(a.tensor(5)), ws.p, ws.n,
+                         stream_of(x)),
+          "qmoe_w4_linear");
+    return wrap(y);
+}
+
+PyObject* w4_linear_backward(const Args& a) {  // dy, w_q, w_s, dev_status, ws
+    const at::Tensor& dy = a.tensor(0);
+    matrix(dy, "w4_linear_backward");
+    const Codes4 c = codes4_of(a.tensor(1), a.tensor(2), false, "w4_linear_backward");
+    const int64_t T = dy.size(0);
+    const Rows r = rows_of(dy, T, c.N);
+    const int code = code_of(dy.scalar_type());
+    if (code == QMOE_F32) bad("w4_linear_backward: dy is of bfloat16 or float16");
+    const at::Tensor dx = make({T, c.K}, dy.scalar_type(), dy);
+    const MaybeWorkspace ws(qmoe_w4_workspace_bytes(T, c.N, c.K, 1), a.maybe(4), dy);
+    check(qmoe_w4_linear_dx(T, c.N, c.K, c.format, c.group, code, r.p, r.ld, c.w, c.s, dx.data_ptr(), code, c.K,
+                            status_of(a.tensor(3)), ws.p, ws.n, stream_of(dy)),
+          "qmoe_w4_linear_dx");
+    return wrap(dx);
+}
+
 // ------------------------------------------------------------------ module
 
 template <PyObject* (*F)(const Args&), int N>
@@ -598,6 +860,14 @@ PyMethodDef methods[] = {
     ENTRY(fp8_matmul, 6),
     ENTRY(fp8_linear, 6),
     ENTRY(fp8_linear_backward, 5),
+    ENTRY(expert_linear, 8),
+    ENTRY(expert_linear_backward, 11),
+    ENTRY(swiglu, 1),
+    ENTRY(swiglu_backward, 3),
+    ENTRY(combine, 3),
+    ENTRY(combine_backward, 5),
+    ENTRY(w4_linear, 7),
+    ENTRY(w4_linear_backward, 5),
     {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_bind", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
