@@ -1,0 +1,318 @@
+// Pieces shared by the kernels of the experts' products (expert_gemm.cu,
+// expert_gemm_pair.cu): arguments, the walk over tiles, stores of sums.
+#pragma once
+
+#include "row_ops.cuh"
+#include "tc_ptx.cuh"
+#include "tma_host.cuh"
+
+namespace qmoe {
+namespace eg {
+
+enum { FWD = 0, DX = 1, DW = 2 };
+
+constexpr int EPI_WARPS = 8;     // read sums and store them: two for each quadrant of lanes
+constexpr int STEP = 64;         // reduction values of a stage: 128 bytes
+constexpr int MAX_E = 1024;
+constexpr int STAGE_OUT = 2048;  // bytes of a warp's output stage: 32 rows of 64
+constexpr int Q_BOX = 32;        // rows of a box of the column side (y, dx)
+
+struct Args {
+    int P, E;
+    int lanes, cols, red;  // lanes of all tiles; columns (dw), reduction length (y, dx)
+    const int32_t* offsets;
+    const int32_t* pairs;  // NULL: the row of a slot is the slot
+    const void* x;         // and its row stride, where pairs are given
+    int64_t ldx;
+    int k, x_rows;
+    void* out;
+    int64_t ld, out_e;     // row stride, expert stride (dw)
+    int ctype;
+    int wide;              // rows of out start on 16-byte boundaries
+    uint32_t idesc;        // without M and N
+    int32_t* status;
+};
+
+// Operand whose reduction axis is not the contiguous one: blocks of 64 lanes (or
+// columns), 8192 bytes apart; in each, reduction rows of 128 bytes, swizzled in
+// groups of 8 rows.
+__device__ __forceinline__ uint64_t sdesc_across(uint32_t saddr) { return tc::smem_desc(saddr, 8192, 1024, 2); }
+
+// Rows of x that are gathered come by cp.async, 16 bytes a lane, into the place
+// and swizzle in which TMA would leave them (TMA's own gather of four rows takes
+// some 70 cycles each: 2.4 us for the 256 rows of a step that takes 0.3).  Eight
+// lanes take a row's 128 bytes; GATHER_WARPS warps a stage.
+constexpr int GATHER_WARPS = 4;
+
+// 16 bytes, of which the first `real` come from `src` and the rest are zeros.
+__device__ __forceinline__ void cp_async_16_part(uint32_t dst, const void* src, int real) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(real) : "memory");
+}
+
+// The row of x of a slot, NULL for a row of zeros.
+__device__ __forceinline__ const uint16_t* row_of(const Args& g, int pair) {
+    const int r = pair >= 0 ? pair / g.k : g.x_rows;
+    return r < g.x_rows ? static_cast<const uint16_t*>(g.x) + r * g.ldx : nullptr;
+}
+
+// This lane's part of a gather warp's rows for y: rows lane / 8 + 4 (warp + i WARPS)
+// of a tile, 16-byte piece lane % 8 of each step.
+template <int NI>
+struct GatherRows {
+    const uint16_t* at[NI];
+    // rows q0 .. q0 + n - 1
+    __device__ __forceinline__ void set(const Args& g, int q0, int n, int gw, int lane) {
+#pragma unroll
+        for (int i = 0; i < NI; ++i) {
+            const int r = (gw + i * GATHER_WARPS) * 4 + (lane >> 3);
+            at[i] = r < n ? row_of(g, g.pairs[q0 + r]) : nullptr;
+        }
+    }
+    __device__ __forceinline__ void load(const Args& g, uint8_t* sq, int n, int k0, int gw, int lane) const {
+        const int k = k0 + (lane & 7) * 8;
+        const int bytes = max(0, min(16, (g.red - k) * 2));
+        const uint32_t to = tc::smem_u32(sq);
+#pragma unroll
+        for (int i = 0; i < NI; ++i) {
+            const int r = (gw + i * GATHER_WARPS) * 4 + (lane >> 3);
+            const bool real = at[i] != nullptr && bytes > 0;
+            if (r < n) cp_async_16_part(to + tc::sw128_offset(r, lane & 7), real ? at[i] + k : static_cast<const uint16_t*>(g.x), real ? bytes : 0);
+        }
+    }
+};
+
+// One lane waits (a wait by all 32 takes four times as long even where the phase is
+// over); __syncwarp passes on to the others what the barrier guards.
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag, int32_t* status) {
+    int ok = 1;
+    if ((threadIdx.x & 31) == 0 && !tc::mbar_wait(bar, parity)) {
+        *abort_flag = 1;
+        atomicOr(status, QMOE_DEV_WAIT_TIMEOUT);
+        ok = 0;
+    }
+    ok = __shfl_sync(0xFFFFFFFFu, ok, 0);
+    __syncwarp();
+    return ok != 0;
+}
+
+// 32 columns of this warp's 32 lanes.
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,"
+        "%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+          "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+          "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(taddr));
+}
+
+// A tile: its expert, first lane, first column (a row s, or a column of dw), the
+// columns it has and its reduction steps.
+struct Unit {
+    int e, l0, q0, n, steps, row0;
+};
+
+// The units, in order.  For y and dx an expert has ceil(lanes / LT) tiles for
+// each of its ceil(count / NT) parts of about the same number of rows (a multiple
+// of ROUND); after the experts come the rows of none, whose outputs are zeros.
+template <int MODE, int LT, int NT, int ROUND>
+struct Walk {
+    const Args& g;
+    const int* off;   // [E + 1], clamped to [0, P]
+    const int* base;  // [E + 2]: units before expert e (y, dx)
+    int e = 0;
+    __device__ Walk(const Args& g_, const int* off_, const int* base_) : g(g_), off(off_), base(base_) {}
+    __device__ int total() const {
+        if (MODE == DW) return g.E * ((g.lanes + LT - 1) / LT) * ((g.cols + NT - 1) / NT);
+        return base[g.E + 1];
+    }
+    __device__ Unit at(int u) {
+        const int lt = (g.lanes + LT - 1) / LT;
+        Unit t;
+        if (MODE == DW) {
+            const int qt = (g.cols + NT - 1) / NT;
+            t.e = u / (lt * qt);
+            const int i = u - t.e * lt * qt;
+            t.l0 = (i % lt) * LT;
+            t.q0 = (i / lt) * NT;
+            t.n = min(NT, g.cols - t.q0);
+            t.row0 = off[t.e];
+            t.steps = (off[t.e + 1] - t.row0 + STEP - 1) / STEP;
+        } else {
+            while (u >= base[e + 1]) ++e;
+            t.e = e;
+            const int i = u - base[e], q = i / lt;
+            const int r0 = off[e], count = (e < g.E ? off[e + 1] : g.P) - r0;
+            const int qt = (count + NT - 1) / NT, per = ((count + qt - 1) / qt + ROUND - 1) & ~(ROUND - 1);
+            t.l0 = (i - q * lt) * LT;
+            t.q0 = r0 + q * per;
+            t.n = min(per, r0 + count - t.q0);
+            t.row0 = 0;
+            t.steps = e < g.E ? (g.red + STEP - 1) / STEP : 0;
+        }
+        return t;
+    }
+};
+
+template <typename T> struct Bits;
+template <> struct Bits<__nv_bfloat16> {
+    static __device__ __forceinline__ uint16_t of(float v) { return __bfloat16_as_ushort(__float2bfloat16_rn(v)); }
+};
+template <> struct Bits<__half> {
+    static __device__ __forceinline__ uint16_t of(float v) { return __half_as_ushort(__float2half_rn(v)); }
+};
+
+// 32 columns of y or dx: lane l holds output l0 + l of rows q0 .. q0 + n - 1.
+template <typename T>
+__device__ __forceinline__ void put_rows(const Args& g, uint8_t* stage, int l0, int q0, int n, int lane,
+                                         const uint32_t (&r)[32]) {
+    T* const out = static_cast<T*>(g.out);
+    if constexpr (sizeof(T) == 2) {
+        if (g.wide) {
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+                *reinterpret_cast<uint16_t*>(stage + j * 64 + lane * 2) = Bits<T>::of(__uint_as_float(r[j]));
+            __syncwarp();
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int row = i * 8 + (lane >> 2), l = l0 + (lane & 3) * 8;
+                const uint4 v = *reinterpret_cast<const uint4*>(stage + row * 64 + (lane & 3) * 16);
+                if (row < n && l < g.lanes) {
+                    T* const to = out + (int64_t)(q0 + row) * g.ld + l;
+                    if (l + 8 <= g.lanes) {
+                        *reinterpret_cast<uint4*>(to) = v;
+                    } else {
+                        for (int j = 0; j < 8 && l + j < g.lanes; ++j) to[j] = reinterpret_cast<const T*>(&v)[j];
+                    }
+                }
+            }
+            __syncwarp();
+            return;
+        }
+    }
+    if (l0 + lane < g.lanes) {
+        T* to = out + (int64_t)q0 * g.ld + l0 + lane;
+#pragma unroll
+        for (int j = 0; j < 32; ++j) {
+            if (j < n) *to = row::from_f32<T>(__uint_as_float(r[j]));
+            to += g.ld;
+        }
+    }
+}
+
+// 32 columns of dw: lane l holds columns q0 .. q0 + n - 1 of row l0 + l.
+template <typename T>
+__device__ __forceinline__ void put_dw(const Args& g, uint8_t* stage, int e, int l0, int q0, int n, int lane,
+                                       const uint32_t (&r)[32]) {
+    constexpr int PER = 16 / sizeof(T), COLS = 64 / sizeof(T);
+    T* const out = static_cast<T*>(g.out) + (int64_t)e * g.out_e;
+#pragma unroll
+    for (int h = 0; h < 32 / COLS; ++h) {
+#pragma unroll
+        for (int p = 0; p < 4; ++p) {
+            uint4 v;
+            uint32_t* w = &v.x;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                if constexpr (sizeof(T) == 2)
+                    w[i] = row::pack2(__uint_as_float(r[p * 8 + 2 * i]), __uint_as_float(r[p * 8 + 2 * i + 1]), T{});
+                else
+                    w[i] = r[h * 16 + p * 4 + i];
+            }
+            *reinterpret_cast<uint4*>(stage + lane * 64 + ((p ^ (lane >> 1 & 3)) * 16)) = v;
+        }
+        __syncwarp();
+        if (g.wide) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int row = i * 8 + (lane >> 2), p = lane & 3, c = h * COLS + p * PER;
+                const uint4 v = *reinterpret_cast<const uint4*>(stage + row * 64 + ((p ^ (row >> 1 & 3)) * 16));
+                if (l0 + row < g.lanes && c < n) {
+                    T* const to = out + (int64_t)(l0 + row) * g.ld + q0 + c;
+                    if (c + PER <= n) {
+                        *reinterpret_cast<uint4*>(to) = v;
+                    } else {
+                        for (int j = 0; j < PER && c + j < n; ++j) to[j] = reinterpret_cast<const T*>(&v)[j];
+                    }
+                }
+            }
+        } else {
+            const int col = lane % COLS, c = h * COLS + col;
+#pragma unroll 4
+            for (int row = lane / COLS; row < 32; row += 32 / COLS) {
+                const T v = reinterpret_cast<const T*>(stage + row * 64 + (((col / PER) ^ (row >> 1 & 3)) * 16))[col % PER];
+                if (l0 + row < g.lanes && c < n) out[(int64_t)(l0 + row) * g.ld + q0 + c] = v;
+            }
+        }
+        __syncwarp();
+    }
+}
+
+template <int MODE>
+__device__ __forceinline__ void put(const Args& g, uint8_t* stage, int e, int l0, int q0, int n, int lane,
+                                    const uint32_t (&r)[32]) {
+    if constexpr (MODE == DW) {
+        if (g.ctype == QMOE_F32) put_dw<float>(g, stage, e, l0, q0, n, lane, r);
+        else if (g.ctype == QMOE_BF16) put_dw<__nv_bfloat16>(g, stage, e, l0, q0, n, lane, r);
+        else put_dw<__half>(g, stage, e, l0, q0, n, lane, r);
+    } else {
+        if (g.ctype == QMOE_F32) put_rows<float>(g, stage, l0, q0, n, lane, r);
+        else if (g.ctype == QMOE_BF16) put_rows<__nv_bfloat16>(g, stage, l0, q0, n, lane, r);
+        else put_rows<__half>(g, stage, l0, q0, n, lane, r);
+    }
+}
+
+// The offsets, clamped to [0, P] and raised to the largest before them (no row
+// has two experts, whatever they say), and the units before each expert, by all
+// threads of the CTA; the caller's barrier makes them seen.
+template <int MODE, int LT, int NT>
+__device__ __forceinline__ void read_offsets(const Args& g, int* off, int* base) {
+    bool bad = false;
+    for (int i = threadIdx.x; i <= g.E; i += blockDim.x) {
+        const int o = g.offsets[i], next = i < g.E ? g.offsets[i + 1] : o;
+        bad |= o < 0 || o > g.P || next < o || (i == 0 && o != 0);
+        off[i] = min(max(o, 0), g.P);
+    }
+    if (bad) atomicOr(g.status, QMOE_DEV_BAD_OFFSETS);
+    __syncthreads();
+    if (threadIdx.x >= 32) return;
+    const int lane = threadIdx.x, lt = (g.lanes + LT - 1) / LT;
+    int most = 0;
+    for (int i0 = 0; i0 <= g.E; i0 += 32) {
+        const int i = i0 + lane;
+        int v = max(i <= g.E ? off[i] : 0, most);
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int w = __shfl_up_sync(0xFFFFFFFFu, v, o);
+            if (lane >= o) v = max(v, w);
+        }
+        if (i <= g.E) off[i] = v;
+        most = __shfl_sync(0xFFFFFFFFu, v, 31);
+    }
+    __syncwarp();
+    if (MODE == DW) return;
+    int sum = 0;
+    for (int i0 = 0; i0 <= g.E; i0 += 32) {
+        const int i = i0 + lane;
+        const int count = i < g.E ? off[i + 1] - off[i] : i == g.E ? g.P - off[i] : 0;
+        int v = (count + NT - 1) / NT * lt;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int w = __shfl_up_sync(0xFFFFFFFFu, v, o);
+            if (lane >= o) v += w;
+        }
+        if (i <= g.E) base[i + 1] = sum + v;
+        sum += __shfl_sync(0xFFFFFFFFu, v, 31);
+    }
+    if (lane == 0) base[0] = 0;
+}
+
+// What the kernels take: map_p of the lane side, map_q of the column side.
+//
+// Pairs of CTAs, 256 x 256 tiles: for many rows an expert, and for dw.
+template <int MODE, bool GATHER>
+int launch_pair(const CUtensorMap& mp, const CUtensorMap& mq, const Args& g, int64_t most, cudaStream_t st);
+
+}  // namespace eg
+}  // namespace qmoe

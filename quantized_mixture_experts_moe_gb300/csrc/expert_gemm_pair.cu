@@ -1,0 +1,367 @@
+// The experts' products in 256 x 256 tiles of two CTAs (see expert_gemm.cu for the
+// three forms): each CTA has 128 of the lanes and loads its own part of them and
+// half of the columns, so that a value of the column side comes to shared memory
+// once for 256 lanes; one of the two issues the products of both.
+//
+// Both CTAs' loads report to the first one's barrier.  Where a thread has to touch
+// a stage before its products (rows that threads gather; zeros in place of another
+// expert's rows in the last step of dw), the second CTA's loads report to its own
+// barrier, its product warp, which has no products to issue, waits for them, and
+// arrives at a barrier of the first.  That arrival is of the CTA's scope, as the
+// tile was written by the async proxy or is ordered by its fence: one that
+// releases at the cluster's scope took 1100 cycles, twice what a step's products
+// take.
+#include "expert_gemm.cuh"
+
+namespace qmoe {
+namespace eg {
+
+// Warps: the epilogue's, two that load tiles, step by step in turn (a load takes a
+// thread some 100 cycles to issue), one that issues products, then those that gather.
+constexpr int PAIR_TMA = 8, TURNS = 2, PAIR_MMA = PAIR_TMA + TURNS;
+constexpr int pair_threads(bool gather) { return (PAIR_MMA + 1 + (gather ? GATHER_WARPS : 0)) * 32; }
+
+template <int MODE>
+struct PairCfg {
+    static constexpr int P_BYTES = 128 * STEP * 2, STAGE = 2 * P_BYTES;
+    static constexpr int LIST = (MODE == DW ? MAX_E + 1 : 2 * (MAX_E + 2)) * 4;
+    static constexpr int STAGES = 6;
+    static constexpr int OUT_OFF = STAGES * STAGE;
+    static constexpr int LIST_OFF = OUT_OFF + EPI_WARPS * STAGE_OUT;
+    static constexpr int BAR_OFF = LIST_OFF + (LIST + 15) / 16 * 16;
+    static constexpr int MISC_OFF = BAR_OFF + (3 * STAGES + 4) * 8;
+    static constexpr int SMEM = MISC_OFF + 64 + 1024;
+    static_assert(SMEM <= 232448, "shared memory per CTA");
+};
+
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+// The address of this barrier in a CTA of the pair.
+__device__ __forceinline__ uint32_t bar_in(uint64_t* bar, uint32_t rank) {
+    uint32_t at;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(tc::smem_u32(bar)), "r"(rank));
+    return at;
+}
+__device__ __forceinline__ void arrive_first(uint64_t* bar) {
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar_in(bar, 0)) : "memory");
+}
+// Tiles into this CTA's shared memory that report to a barrier of either.
+__device__ __forceinline__ void pair_load_2d(void* dst, const CUtensorMap* map, uint32_t bar, int x, int y) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], "
+        "[%2];" ::"r"(tc::smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y)
+        : "memory");
+}
+__device__ __forceinline__ void pair_load_3d(void* dst, const CUtensorMap* map, uint32_t bar, int x, int y, int z) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, "
+        "%5}], [%2];" ::"r"(tc::smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "r"(z)
+        : "memory");
+}
+// A bounded wait of one lane; false, and the flag set, where it ran out.
+__device__ __forceinline__ bool lane_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag, int32_t* status) {
+    if (tc::mbar_wait(bar, parity)) return true;
+    *abort_flag = 1;
+    atomicOr(status, QMOE_DEV_WAIT_TIMEOUT);
+    return false;
+}
+__device__ __forceinline__ void mma_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+// Arrives at this barrier of both CTAs once the products issued so far are done.
+__device__ __forceinline__ void commit_pair(uint64_t* bar) {
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+            tc::smem_u32(bar)),
+        "h"((uint16_t)3)
+        : "memory");
+}
+
+template <int MODE, bool GATHER>
+__global__ void __launch_bounds__(pair_threads(GATHER), 1)
+expert_pair_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_constant__ CUtensorMap map_q, const Args g) {
+    using C = PairCfg<MODE>;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    int* off = reinterpret_cast<int*>(smem + C::LIST_OFF);
+    int* base = off + MAX_E + 1;
+    uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::BAR_OFF);
+    uint64_t* empty = full + C::STAGES;
+    uint64_t* other = empty + C::STAGES;  // of the first CTA: the second one's stage is full
+    uint64_t* acc_full = other + C::STAGES;
+    uint64_t* acc_empty = acc_full + 2;  // of the first CTA: both have read the sums
+    uint32_t* tmem_at = reinterpret_cast<uint32_t*>(smem + C::MISC_OFF);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::MISC_OFF + 8);
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int rank = (int)cluster_rank();
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < C::STAGES; ++i) {
+            tc::mbar_init(&full[i], GATHER ? 1 + GATHER_WARPS * 32 : 1);
+            tc::mbar_init(&empty[i], 1);
+            tc::mbar_init(&other[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            tc::mbar_init(&acc_full[i], 1);
+            tc::mbar_init(&acc_empty[i], 2 * EPI_WARPS);
+        }
+        *abort_flag = 0;
+        tc::fence_barrier_init();
+    }
+    if (warp == PAIR_MMA) {
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(tc::smem_u32(tmem_at)), "r"(512)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    }
+    pdl_wait();
+    read_offsets<MODE, 256, 256>(g, off, base);
+    tc::tc_fence_before();
+    __syncthreads();
+    cluster_sync();
+    tc::tc_fence_after();
+    const uint32_t tm = *tmem_at;
+    Walk<MODE, 256, 256, 32> walk(g, off, base);
+    const int total = walk.total(), first = blockIdx.x >> 1, stride = gridDim.x >> 1;
+
+    if (warp >= PAIR_TMA && warp < PAIR_MMA) {
+        if (lane == 0) {
+            const int turn = warp - PAIR_TMA;
+            int it = 0;
+            for (int u = first; u < total && !*abort_flag; u += stride) {
+                const Unit t = walk.at(u);
+                const int half = ((t.n + 31) & ~31) / 2, l0 = t.l0 + rank * 128, q0 = t.q0 + rank * half;
+                const int boxes = GATHER ? 0 : MODE == DW ? (half + 63) / 64 : 1;
+                const uint32_t bytes = C::P_BYTES + boxes * (MODE == DW ? 8192 : 128 * 128);
+                const int end = MODE == DW ? off[t.e + 1] : 0;
+                for (int s = 0; s < t.steps; ++s, ++it) {
+                    if (it % TURNS != turn) continue;
+                    const int slot = it % C::STAGES;
+                    if (!lane_wait(&empty[slot], (it / C::STAGES & 1) ^ 1, abort_flag, g.status)) break;
+                    uint8_t* st = smem + slot * C::STAGE;
+                    uint8_t* sq = st + C::P_BYTES;
+                    const int k0 = s * STEP, row = t.row0 + k0;
+                    const bool relay = GATHER || (MODE == DW && end - row < STEP);
+                    const uint32_t bar = bar_in(&full[slot], relay ? rank : 0);
+                    if (relay) tc::mbar_arrive_expect_tx(&full[slot], bytes);
+                    else if (rank == 0) tc::mbar_arrive_expect_tx(&full[slot], 2 * bytes);
+                    if constexpr (MODE == FWD) {
+                        pair_load_3d(st, &map_p, bar, k0, l0, t.e);
+                    } else if constexpr (MODE == DX) {
+                        pair_load_3d(st, &map_p, bar, l0, k0, t.e);
+                        pair_load_3d(st + 8192, &map_p, bar, l0 + 64, k0, t.e);
+                    } else {
+                        pair_load_2d(st, &map_p, bar, l0, row);
+                        pair_load_2d(st + 8192, &map_p, bar, l0 + 64, row);
+                    }
+                    if constexpr (!GATHER && MODE != DW) pair_load_2d(sq, &map_q, bar, k0, q0);
+                    if constexpr (!GATHER && MODE == DW)
+                        for (int b = 0; b < boxes; ++b) pair_load_2d(sq + b * 8192, &map_q, bar, q0 + b * 64, row);
+                }
+            }
+        }
+        __syncwarp();
+    } else if (warp == PAIR_MMA) {
+        // lane 0 waits and issues; the others join it where rows have to be zeroed
+        int it = 0, buf = 0;
+        uint32_t acc_phase = 0, relayed = 0, here = 0;  // of each stage: the phases of other, and of full in the second CTA
+        bool ok = true;
+        for (int u = first; u < total; u += stride) {
+            const Unit t = walk.at(u);
+            if (t.steps == 0) continue;  // zeros: no sums to wait for
+            const uint32_t n32 = (uint32_t)(t.n + 31) & ~31u;
+            const uint32_t idesc = g.idesc | (n32 >> 3) << 17 | (256u >> 4) << 24;
+            if (rank == 0 && lane == 0) ok = ok && lane_wait(&acc_empty[buf], acc_phase ^ 1, abort_flag, g.status);
+            for (int s = 0; s < t.steps; ++s, ++it) {
+                const int slot = it % C::STAGES;
+                const uint32_t bit = 1u << slot;
+                uint8_t* st = smem + slot * C::STAGE;
+                const int left = MODE == DW ? off[t.e + 1] - t.row0 - s * STEP : STEP;
+                const bool tail = MODE == DW && left < STEP, relay = GATHER || tail;
+                const int k16 = tail ? (left + 15) / 16 : STEP / 16;
+                if (lane == 0) {
+                    if (rank == 0) ok = ok && lane_wait(&full[slot], it / C::STAGES & 1, abort_flag, g.status);
+                    else if (relay) ok = ok && lane_wait(&full[slot], here >> slot & 1, abort_flag, g.status);
+                }
+                if (relay && rank != 0) here ^= bit;
+                if (tail) {
+                    // rows behind the expert's last, up to the 16 of a product, are another's: zeros in their place
+                    __syncwarp();
+                    const int zero = k16 * 16 - left;
+                    for (int i = lane; i < 4 * zero * 8; i += 32) {
+                        const int b = i / (zero * 8), c = i - b * zero * 8;
+                        *reinterpret_cast<uint4*>(st + b * 8192 + left * 128 + c * 16) = make_uint4(0, 0, 0, 0);
+                    }
+                    tc::fence_proxy_async_smem();
+                    __syncwarp();
+                }
+                if (lane != 0) continue;
+                // gathered rows were written by threads: order them before the tensor core's reads
+                if constexpr (GATHER) tc::fence_proxy_async_smem();
+                if (rank != 0) {
+                    if (relay && ok) arrive_first(&other[slot]);
+                    continue;
+                }
+                if (relay) {
+                    ok = ok && lane_wait(&other[slot], relayed >> slot & 1, abort_flag, g.status);
+                    relayed ^= bit;
+                }
+                if (!ok) continue;
+                tc::tc_fence_after();
+                const uint32_t sa = tc::smem_u32(st), sb = sa + C::P_BYTES;
+                const uint64_t da = MODE == FWD ? tc::sdesc_kmajor_sw128(sa) : sdesc_across(sa);
+                const uint64_t db = MODE == DW ? sdesc_across(sb) : tc::sdesc_kmajor_sw128(sb);
+                constexpr int SA = MODE == FWD ? 2 : 128, SB = MODE == DW ? 128 : 2;  // of 16 values, in 16 bytes
+                if (MODE != DW || k16 == 4) {
+#pragma unroll
+                    for (int k = 0; k < STEP / 16; ++k)
+                        mma_pair(tm + buf * 256, da + SA * k, db + SB * k, idesc, s > 0 || k > 0);
+                } else {
+                    for (int k = 0; k < k16; ++k) mma_pair(tm + buf * 256, da + SA * k, db + SB * k, idesc, s > 0 || k > 0);
+                }
+                commit_pair(&empty[slot]);
+            }
+            if (rank == 0 && lane == 0 && ok) commit_pair(&acc_full[buf]);
+            if (++buf == 2) { buf = 0; acc_phase ^= 1; }
+        }
+        __syncwarp();
+    } else if (warp > PAIR_MMA) {
+        const int gw = warp - PAIR_MMA - 1;
+        int slot = 0;
+        uint32_t phase = 0;
+        for (int u = first; u < total && !*abort_flag; u += stride) {
+            const Unit t = walk.at(u);
+            const int half = ((t.n + 31) & ~31) / 2, q0 = t.q0 + rank * half;
+            if constexpr (MODE == FWD) {
+                const int n = max(0, min(half, t.n - rank * half));
+                GatherRows<8> rows;
+                if (t.steps > 0) rows.set(g, q0, n, gw, lane);
+                for (int s = 0; s < t.steps; ++s) {
+                    if (!warp_wait(&empty[slot], phase ^ 1, abort_flag, g.status)) break;
+                    rows.load(g, smem + slot * C::STAGE + C::P_BYTES, n, s * STEP, gw, lane);
+                    tc::cp_async_mbar_arrive_noinc(&full[slot]);
+                    if (++slot == C::STAGES) { slot = 0; phase ^= 1; }
+                }
+            } else {
+                // rows lane / 8 + 4 (warp + 4 i) of a step, i < 4, columns of two blocks of 64
+                const int end = off[t.e + 1], piece = lane & 7, r0 = gw * 4 + (lane >> 3);
+                int next[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int r = t.row0 + r0 + 16 * i;
+                    next[i] = t.steps > 0 && r < end ? g.pairs[r] : -1;
+                }
+                for (int s = 0; s < t.steps; ++s) {
+                    const uint16_t* at[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        at[i] = row_of(g, next[i]);
+                        const int r = t.row0 + (s + 1) * STEP + r0 + 16 * i;
+                        next[i] = s + 1 < t.steps && r < end ? g.pairs[r] : -1;
+                    }
+                    if (!warp_wait(&empty[slot], phase ^ 1, abort_flag, g.status)) break;
+                    const uint32_t sq = tc::smem_u32(smem + slot * C::STAGE + C::P_BYTES);
+#pragma unroll
+                    for (int b = 0; b < 2; ++b) {
+                        const int c = q0 + b * 64 + piece * 8;
+                        const int bytes = max(0, min(16, (g.cols - c) * 2));
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const bool real = at[i] != nullptr && bytes > 0;
+                            if (b * 64 < half)
+                                cp_async_16_part(sq + b * 8192 + tc::sw128_offset(r0 + 16 * i, piece),
+                                                 real ? at[i] + c : static_cast<const uint16_t*>(g.x), real ? bytes : 0);
+                        }
+                    }
+                    tc::cp_async_mbar_arrive_noinc(&full[slot]);
+                    if (++slot == C::STAGES) { slot = 0; phase ^= 1; }
+                }
+            }
+        }
+        tc::cp_async_wait<0>();
+    } else {
+        const int quad = warp & 3, half = warp >> 2;
+        uint8_t* const stage = smem + C::OUT_OFF + warp * STAGE_OUT;
+        int buf = 0;
+        uint32_t acc_phase = 0;
+        for (int u = first; u < total && !*abort_flag; u += stride) {
+            const Unit t = walk.at(u);
+            const int l0 = t.l0 + rank * 128 + quad * 32;
+            if (t.steps > 0) {
+                if (!warp_wait(&acc_full[buf], acc_phase, abort_flag, g.status)) break;
+                tc::tc_fence_after();
+            }
+            for (int c = half * 32; c < t.n; c += 64) {
+                uint32_t r[32];
+                if (t.steps > 0) {
+                    tmem_ld32(tm + ((uint32_t)(quad * 32) << 16) + buf * 256 + c, r);
+                    tc::tmem_ld_wait();
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) r[j] = 0;
+                }
+                put<MODE>(g, stage, t.e, l0, t.q0 + c, t.n - c, lane, r);
+            }
+            if (t.steps > 0) {
+                tc::tc_fence_before();
+                __syncwarp();
+                if (lane == 0) arrive_first(&acc_empty[buf]);
+                if (++buf == 2) { buf = 0; acc_phase ^= 1; }
+            }
+        }
+    }
+    __syncwarp();
+    pdl_trigger();
+    tc::tc_fence_before();
+    __syncthreads();
+    // after a wait that ran out: time for the loads and products in flight to end (they take microseconds)
+    if (*abort_flag)
+        for (const long long t0 = clock64(); clock64() - t0 < 4000000ll;) __nanosleep(1000);
+    cluster_sync();  // neither CTA leaves while the other's products read its tiles or arrive at its barriers
+    tc::tc_fence_after();
+    if (warp == PAIR_MMA)
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tm), "r"(512) : "memory");
+}
+
+template <int MODE, bool GATHER>
+int launch_pair(const CUtensorMap& mp, const CUtensorMap& mq, const Args& g, int64_t most, cudaStream_t st) {
+    using C = PairCfg<MODE>;
+    const int rc = row::allow_smem<expert_pair_kernel<MODE, GATHER>>(C::SMEM);
+    if (rc != QMOE_OK) return rc;
+    const int64_t pairs = most < row::kSMs / 2 ? most : row::kSMs / 2;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = 2;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(2 * pairs));
+    cfg.blockDim = dim3(pair_threads(GATHER));
+    cfg.dynamicSmemBytes = C::SMEM;
+    cfg.stream = st;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, expert_pair_kernel<MODE, GATHER>, mp, mq, g) == cudaSuccess ? QMOE_OK : QMOE_ERR_LAUNCH;
+}
+
+template int launch_pair<FWD, false>(const CUtensorMap&, const CUtensorMap&, const Args&, int64_t, cudaStream_t);
+template int launch_pair<FWD, true>(const CUtensorMap&, const CUtensorMap&, const Args&, int64_t, cudaStream_t);
+template int launch_pair<DX, false>(const CUtensorMap&, const CUtensorMap&, const Args&, int64_t, cudaStream_t);
+template int launch_pair<DW, false>(const CUtensorMap&, const CUtensorMap&, const Args&, int64_t, cudaStream_t);
+template int launch_pair<DW, true>(const CUtensorMap&, const CUtensorMap&, const Args&, int64_t, cudaStream_t);
+
+}  // namespace eg
+}  // namespace qmoe
