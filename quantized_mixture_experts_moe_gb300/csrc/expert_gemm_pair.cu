@@ -73,20 +73,34 @@ __device__ __forceinline__ bool lane_wait(uint64_t* bar, uint32_t parity, volati
     atomicOr(status, QMOE_DEV_WAIT_TIMEOUT);
     return false;
 }
+// All lanes of the warp call these with the same operands (which then stay in
+// uniform registers) and one issues.
 __device__ __forceinline__ void mma_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "{\n\t.reg .pred p, e;\n\telect.sync _|e, 0xffffffff;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "@e tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
         "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
         : "memory");
 }
 // Arrives at this barrier of both CTAs once the products issued so far are done.
 __device__ __forceinline__ void commit_pair(uint64_t* bar) {
     asm volatile(
-        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+        "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
+        "@e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;\n\t}" ::"r"(
             tc::smem_u32(bar)),
         "h"((uint16_t)3)
         : "memory");
+}
+// The products of K16 times 16 values of a stage.
+template <int MODE>
+__device__ __forceinline__ void mma_stage(uint32_t d, uint32_t stage, uint32_t idesc, bool first, int k16 = STEP / 16) {
+    const uint32_t sb = stage + 128 * STEP * 2;
+    const uint64_t da = MODE == FWD ? tc::sdesc_kmajor_sw128(stage) : sdesc_across(stage);
+    const uint64_t db = MODE == DW ? sdesc_across(sb) : tc::sdesc_kmajor_sw128(sb);
+    constexpr int SA = MODE == FWD ? 2 : 128, SB = MODE == DW ? 128 : 2;  // of 16 values, in 16 bytes
+#pragma unroll
+    for (int k = 0; k < STEP / 16; ++k)
+        if (k < k16) mma_pair(d, da + SA * k, db + SB * k, idesc, !first || k > 0);
 }
 
 template <int MODE, bool GATHER>
@@ -173,66 +187,66 @@ expert_pair_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_const
         }
         __syncwarp();
     } else if (warp == PAIR_MMA) {
-        // lane 0 waits and issues; the others join it where rows have to be zeroed
-        int it = 0, buf = 0;
-        uint32_t acc_phase = 0, relayed = 0, here = 0;  // of each stage: the phases of other, and of full in the second CTA
-        bool ok = true;
+        int slot = 0, buf = 0;
+        uint32_t phase = 0, acc_phase = 0, relayed = 0, here = 0;  // of each stage: the phases of other, and of full in the second CTA
+        bool ok = true;  // lane 0's; after a wait that ran out nothing is waited for any more
         for (int u = first; u < total; u += stride) {
             const Unit t = walk.at(u);
             if (t.steps == 0) continue;  // zeros: no sums to wait for
             const uint32_t n32 = (uint32_t)(t.n + 31) & ~31u;
             const uint32_t idesc = g.idesc | (n32 >> 3) << 17 | (256u >> 4) << 24;
+            const uint32_t d = tm + buf * 256;
+            const int left = MODE == DW ? (off[t.e + 1] - t.row0) % STEP : 0, whole = t.steps - (left > 0);
             if (rank == 0 && lane == 0) ok = ok && lane_wait(&acc_empty[buf], acc_phase ^ 1, abort_flag, g.status);
-            for (int s = 0; s < t.steps; ++s, ++it) {
-                const int slot = it % C::STAGES;
-                const uint32_t bit = 1u << slot;
-                uint8_t* st = smem + slot * C::STAGE;
-                const int left = MODE == DW ? off[t.e + 1] - t.row0 - s * STEP : STEP;
-                const bool tail = MODE == DW && left < STEP, relay = GATHER || tail;
-                const int k16 = tail ? (left + 15) / 16 : STEP / 16;
-                if (lane == 0) {
-                    if (rank == 0) ok = ok && lane_wait(&full[slot], it / C::STAGES & 1, abort_flag, g.status);
-                    else if (relay) ok = ok && lane_wait(&full[slot], here >> slot & 1, abort_flag, g.status);
+            __syncwarp();
+            if (!GATHER && rank == 0) {
+#pragma unroll 1
+                for (int s = 0; s < whole; ++s) {
+                    if (lane == 0) ok = ok && lane_wait(&full[slot], phase, abort_flag, g.status);
+                    __syncwarp();
+                    tc::tc_fence_after();
+                    mma_stage<MODE>(d, tc::smem_u32(smem) + slot * C::STAGE, idesc, s == 0);
+                    commit_pair(&empty[slot]);
+                    if (++slot == C::STAGES) { slot = 0; phase ^= 1; }
                 }
-                if (relay && rank != 0) here ^= bit;
+            } else if (!GATHER) {
+                slot += whole;  // the first CTA's affair
+                phase ^= slot / C::STAGES & 1;
+                slot %= C::STAGES;
+            }
+            // what this warp of the second CTA passes on
+            for (int s = GATHER ? 0 : whole; s < t.steps; ++s) {
+                const bool tail = MODE == DW && s == whole;
+                const int k16 = tail ? (left + 15) / 16 : STEP / 16;
+                uint8_t* st = smem + slot * C::STAGE;
+                if (lane == 0) ok = ok && lane_wait(&full[slot], rank == 0 ? phase : here >> slot & 1, abort_flag, g.status);
+                here ^= 1u << slot;
+                __syncwarp();
                 if (tail) {
                     // rows behind the expert's last, up to the 16 of a product, are another's: zeros in their place
-                    __syncwarp();
                     const int zero = k16 * 16 - left;
                     for (int i = lane; i < 4 * zero * 8; i += 32) {
                         const int b = i / (zero * 8), c = i - b * zero * 8;
                         *reinterpret_cast<uint4*>(st + b * 8192 + left * 128 + c * 16) = make_uint4(0, 0, 0, 0);
                     }
-                    tc::fence_proxy_async_smem();
+                }
+                // what threads wrote (gathered rows, zeros), before the tensor core's reads
+                tc::fence_proxy_async_smem();
+                __syncwarp();
+                if (rank == 0) {
+                    if (lane == 0) ok = ok && lane_wait(&other[slot], relayed >> slot & 1, abort_flag, g.status);
+                    relayed ^= 1u << slot;
                     __syncwarp();
+                    tc::tc_fence_after();
+                    mma_stage<MODE>(d, tc::smem_u32(st), idesc, s == 0, k16);
+                    commit_pair(&empty[slot]);
+                } else if (lane == 0) {
+                    arrive_first(&other[slot]);
                 }
-                if (lane != 0) continue;
-                // gathered rows were written by threads: order them before the tensor core's reads
-                if constexpr (GATHER) tc::fence_proxy_async_smem();
-                if (rank != 0) {
-                    if (relay && ok) arrive_first(&other[slot]);
-                    continue;
-                }
-                if (relay) {
-                    ok = ok && lane_wait(&other[slot], relayed >> slot & 1, abort_flag, g.status);
-                    relayed ^= bit;
-                }
-                if (!ok) continue;
-                tc::tc_fence_after();
-                const uint32_t sa = tc::smem_u32(st), sb = sa + C::P_BYTES;
-                const uint64_t da = MODE == FWD ? tc::sdesc_kmajor_sw128(sa) : sdesc_across(sa);
-                const uint64_t db = MODE == DW ? sdesc_across(sb) : tc::sdesc_kmajor_sw128(sb);
-                constexpr int SA = MODE == FWD ? 2 : 128, SB = MODE == DW ? 128 : 2;  // of 16 values, in 16 bytes
-                if (MODE != DW || k16 == 4) {
-#pragma unroll
-                    for (int k = 0; k < STEP / 16; ++k)
-                        mma_pair(tm + buf * 256, da + SA * k, db + SB * k, idesc, s > 0 || k > 0);
-                } else {
-                    for (int k = 0; k < k16; ++k) mma_pair(tm + buf * 256, da + SA * k, db + SB * k, idesc, s > 0 || k > 0);
-                }
-                commit_pair(&empty[slot]);
+                __syncwarp();
+                if (++slot == C::STAGES) { slot = 0; phase ^= 1; }
             }
-            if (rank == 0 && lane == 0 && ok) commit_pair(&acc_full[buf]);
+            if (rank == 0) commit_pair(&acc_full[buf]);
             if (++buf == 2) { buf = 0; acc_phase ^= 1; }
         }
         __syncwarp();
