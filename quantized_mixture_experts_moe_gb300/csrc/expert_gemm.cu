@@ -55,7 +55,7 @@ expert_gemm_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_const
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
         for (int i = 0; i < C::STAGES; ++i) {
-            tc::mbar_init(&full[i], GATHER ? 1 + GATHER_WARPS * 32 : 1);
+            tc::mbar_init(&full[i], 1);
             tc::mbar_init(&empty[i], 1);
         }
         for (int i = 0; i < 2; ++i) {
@@ -89,7 +89,7 @@ expert_gemm_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_const
                 uint8_t* st = smem + slot * C::STAGE;
                 const int k0 = s * STEP;
                 if (lane == 0) {
-                    tc::mbar_arrive_expect_tx(&full[slot], C::P_BYTES + boxes * Q_BOX * 128);
+                    tc::mbar_arrive_expect_tx(&full[slot], C::P_BYTES + (GATHER ? (t.n + 3) / 4 * 512 : boxes * Q_BOX * 128));
                     if constexpr (MODE == FWD) {
                         tc::tma_load_3d(st, &map_p, &full[slot], k0, t.l0, t.e);
                     } else {
@@ -127,8 +127,6 @@ expert_gemm_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_const
                 ok = warp_wait(&full[slot], phase, abort_flag, g.status);
                 if (!ok) break;
                 if (lane == 0) {
-                    // gathered rows were written by threads: order them before the tensor core's reads
-                    if constexpr (GATHER) tc::fence_proxy_async_smem();
                     tc::tc_fence_after();
                     const uint32_t sa = tc::smem_u32(smem + slot * C::STAGE), sb = sa + C::P_BYTES;
                     const uint64_t da = MODE == FWD ? tc::sdesc_kmajor_sw128(sa) : sdesc_across(sa);
@@ -153,21 +151,27 @@ expert_gemm_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_const
             tc::mbar_wait(&empty[last], last_phase);
         __syncwarp();
     } else if (warp > WARP_MMA) {
-        const int gw = warp - WARP_MMA - 1;
-        int slot = 0;
-        uint32_t phase = 0;
+        const int gw = warp - WARP_MMA - 1, turn = gw / GATHER_SHARE, share = gw % GATHER_SHARE;
+        int it = 0;
         for (int u = blockIdx.x; u < total && !*abort_flag; u += gridDim.x) {
             const Unit t = walk.at(u);
-            GatherRows<(NT + 15) / 16> rows;
-            if (t.steps > 0) rows.set(g, t.q0, t.n, gw, lane);
-            for (int s = 0; s < t.steps; ++s) {
-                if (!warp_wait(&empty[slot], phase ^ 1, abort_flag, g.status)) break;
-                rows.load(g, smem + slot * C::STAGE + C::P_BYTES, t.n, s * STEP, gw, lane);
-                tc::cp_async_mbar_arrive_noinc(&full[slot]);
-                if (++slot == C::STAGES) { slot = 0; phase ^= 1; }
+            // lane j has the group share + 4 j of the tile
+            const int group = share + GATHER_SHARE * lane;
+            const bool mine = lane < NT / (4 * GATHER_SHARE) && group * 4 < t.n;
+            GatherRows rows;
+            if (t.steps > 0 && mine) {
+                rows.read(g, t.q0, t.n, group);
+                rows.to_rows(g);
+            }
+            for (int s = 0; s < t.steps; ++s, ++it) {
+                if (it % GATHER_TURNS != turn) continue;
+                const int slot = it % C::STAGES;
+                if (!warp_wait(&empty[slot], (it / C::STAGES & 1) ^ 1, abort_flag, g.status)) break;
+                if (mine)
+                    tma_gather4(smem + slot * C::STAGE + C::P_BYTES + group * 512, &map_q, tc::smem_u32(&full[slot]), s * STEP, rows);
+                __syncwarp();
             }
         }
-        tc::cp_async_wait<0>();
     } else {
         const int quad = warp & 3, half = warp >> 2;
         uint8_t* const stage = smem + C::OUT_OFF + warp * STAGE_OUT;
@@ -287,7 +291,7 @@ static int run_rows(Mat w, Mat q, Args& g, int dtype, cudaStream_t st) {
     CUtensorMap mp, mq;
     int rc = MODE == FWD ? map_of(&mp, w, dtype, STEP, 128, true) : map_of(&mp, w, dtype, 64, STEP, true);
     if (rc != QMOE_OK) return rc;
-    rc = map_of(&mq, q, dtype, STEP, nt == 256 ? 128 : Q_BOX, false);
+    rc = map_of(&mq, q, dtype, STEP, GATHER ? 1 : nt == 256 ? 128 : Q_BOX, false);
     if (rc != QMOE_OK) return rc;
     // no more units than this, whatever the offsets
     const int64_t parts = (g.P < g.E ? g.P : g.E) + 1 + g.P / nt, most = parts * ((g.lanes + lt - 1) / lt);
@@ -350,7 +354,7 @@ extern "C" int qmoe_expert_linear(int64_t P, int E, int64_t N, int64_t K, int dt
     size_t left = ws && !(reinterpret_cast<uintptr_t>(ws) & 255u) ? ws_bytes : 0;
     if ((rc = eg::as_tma(mw, at, left, st)) != QMOE_OK || (rc = eg::as_tma(mx, at, left, st)) != QMOE_OK) return rc;
     const int size = row::dtype_size(y_dtype);
-    eg::Args g = {(int)P, E, (int)N, 0, (int)K, offsets, pairs, mx.p, mx.ld, k, (int)mx.rows, y, ldy, 0, y_dtype,
+    eg::Args g = {(int)P, E, (int)N, 0, (int)K, offsets, pairs, k, (int)mx.rows, y, ldy, 0, y_dtype,
                   aligned16(y) && ldy * size % 16 == 0,
                   dtype == QMOE_BF16 ? tc::idesc_bf16_f32(0, 0) : tc::idesc_f16_f32(0, 0), dev_status};
     return pairs ? eg::run_rows<eg::FWD, true>(mw, mx, g, dtype, st) : eg::run_rows<eg::FWD, false>(mw, mx, g, dtype, st);
@@ -374,7 +378,7 @@ extern "C" int qmoe_expert_linear_dx(int64_t P, int E, int64_t N, int64_t K, int
     size_t left = ws && !(reinterpret_cast<uintptr_t>(ws) & 255u) ? ws_bytes : 0;
     if ((rc = eg::as_tma(mw, at, left, st)) != QMOE_OK || (rc = eg::as_tma(my, at, left, st)) != QMOE_OK) return rc;
     const int size = row::dtype_size(dx_dtype);
-    eg::Args g = {(int)P, E, (int)K, 0, (int)N, offsets, nullptr, nullptr, 0, 0, (int)P, dx, lddx, 0, dx_dtype,
+    eg::Args g = {(int)P, E, (int)K, 0, (int)N, offsets, nullptr, 0, (int)P, dx, lddx, 0, dx_dtype,
                   aligned16(dx) && lddx * size % 16 == 0,
                   (dtype == QMOE_BF16 ? tc::idesc_bf16_f32(0, 0) : tc::idesc_f16_f32(0, 0)) | 1u << 15, dev_status};
     return eg::run_rows<eg::DX, false>(mw, my, g, dtype, st);
@@ -402,13 +406,13 @@ extern "C" int qmoe_expert_linear_dw(int64_t P, int E, int64_t N, int64_t K, int
     uint8_t* at = static_cast<uint8_t*>(ws);
     size_t left = ws && !(reinterpret_cast<uintptr_t>(ws) & 255u) ? ws_bytes : 0;
     if ((rc = eg::as_tma(my, at, left, st)) != QMOE_OK || (rc = eg::as_tma(mx, at, left, st)) != QMOE_OK) return rc;
-    eg::Args g = {(int)P, E, (int)N, (int)K, 0, offsets, pairs, mx.p, mx.ld, k, (int)mx.rows, dw, K, N * K, dw_dtype,
+    eg::Args g = {(int)P, E, (int)N, (int)K, 0, offsets, pairs, k, (int)mx.rows, dw, K, N * K, dw_dtype,
                   aligned16(dw) && K * size % 16 == 0,
                   (dtype == QMOE_BF16 ? tc::idesc_bf16_f32(0, 0) : tc::idesc_f16_f32(0, 0)) | 3u << 15, dev_status};
     CUtensorMap mp, mq;
     rc = eg::map_of(&mp, my, dtype, 64, eg::STEP, false);
     if (rc != QMOE_OK) return rc;
-    rc = eg::map_of(&mq, mx, dtype, 64, eg::STEP, false);
+    rc = eg::map_of(&mq, mx, dtype, 64, pairs ? 1 : eg::STEP, false);
     if (rc != QMOE_OK) return rc;
     return pairs ? eg::launch_pair<eg::DW, true>(mp, mq, g, units, st) : eg::launch_pair<eg::DW, false>(mp, mq, g, units, st);
 }

@@ -22,8 +22,6 @@ struct Args {
     int lanes, cols, red;  // lanes of all tiles; columns (dw), reduction length (y, dx)
     const int32_t* offsets;
     const int32_t* pairs;  // NULL: the row of a slot is the slot
-    const void* x;         // and its row stride, where pairs are given
-    int64_t ldx;
     int k, x_rows;
     void* out;
     int64_t ld, out_e;     // row stride, expert stride (dw)
@@ -38,48 +36,43 @@ struct Args {
 // groups of 8 rows.
 __device__ __forceinline__ uint64_t sdesc_across(uint32_t saddr) { return tc::smem_desc(saddr, 8192, 1024, 2); }
 
-// Rows of x that are gathered come by cp.async, 16 bytes a lane, into the place
-// and swizzle in which TMA would leave them (TMA's own gather of four rows takes
-// some 70 cycles each: 2.4 us for the 256 rows of a step that takes 0.3).  Eight
-// lanes take a row's 128 bytes; GATHER_WARPS warps a stage.
-constexpr int GATHER_WARPS = 4;
+// Rows of x that are gathered come four at a time (TMA's gather; its map has boxes
+// of one row).  A warp takes some 100 cycles to issue one, so four warps share a
+// step's, and two sets of four take the steps in turn: 64 gathers by one warp took
+// 2.4 us.
+constexpr int GATHER_WARPS = 8, GATHER_SHARE = 4, GATHER_TURNS = GATHER_WARPS / GATHER_SHARE;
 
-// 16 bytes, of which the first `real` come from `src` and the rest are zeros.
-__device__ __forceinline__ void cp_async_16_part(uint32_t dst, const void* src, int real) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(real) : "memory");
-}
+// The row of x of a slot; past its end, which reads as zeros, for none.
+__device__ __forceinline__ int row_of(const Args& g, int pair) { return pair >= 0 ? min(pair / g.k, g.x_rows) : g.x_rows; }
 
-// The row of x of a slot, NULL for a row of zeros.
-__device__ __forceinline__ const uint16_t* row_of(const Args& g, int pair) {
-    const int r = pair >= 0 ? pair / g.k : g.x_rows;
-    return r < g.x_rows ? static_cast<const uint16_t*>(g.x) + r * g.ldx : nullptr;
-}
-
-// This lane's part of a gather warp's rows for y: rows lane / 8 + 4 (warp + i WARPS)
-// of a tile, 16-byte piece lane % 8 of each step.
-template <int NI>
+// Four rows: of a tile's rows q0 .. q0 + n - 1 those of a group.
 struct GatherRows {
-    const uint16_t* at[NI];
-    // rows q0 .. q0 + n - 1
-    __device__ __forceinline__ void set(const Args& g, int q0, int n, int gw, int lane) {
+    int at[4];
+    __device__ __forceinline__ void read(const Args& g, int q0, int n, int group) {
 #pragma unroll
-        for (int i = 0; i < NI; ++i) {
-            const int r = (gw + i * GATHER_WARPS) * 4 + (lane >> 3);
-            at[i] = r < n ? row_of(g, g.pairs[q0 + r]) : nullptr;
-        }
+        for (int i = 0; i < 4; ++i) at[i] = group * 4 + i < n ? g.pairs[q0 + group * 4 + i] : -1;
     }
-    __device__ __forceinline__ void load(const Args& g, uint8_t* sq, int n, int k0, int gw, int lane) const {
-        const int k = k0 + (lane & 7) * 8;
-        const int bytes = max(0, min(16, (g.red - k) * 2));
-        const uint32_t to = tc::smem_u32(sq);
+    __device__ __forceinline__ void to_rows(const Args& g) {
 #pragma unroll
-        for (int i = 0; i < NI; ++i) {
-            const int r = (gw + i * GATHER_WARPS) * 4 + (lane >> 3);
-            const bool real = at[i] != nullptr && bytes > 0;
-            if (r < n) cp_async_16_part(to + tc::sw128_offset(r, lane & 7), real ? at[i] + k : static_cast<const uint16_t*>(g.x), real ? bytes : 0);
-        }
+        for (int i = 0; i < 4; ++i) at[i] = row_of(g, at[i]);
     }
 };
+
+template <bool PAIR = false>
+__device__ __forceinline__ void tma_gather4(void* dst, const CUtensorMap* map, uint32_t bar, int x, const GatherRows& r) {
+    if constexpr (PAIR)
+        asm volatile(
+            "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes.cta_group::2 [%0], "
+            "[%1, {%3, %4, %5, %6, %7}], [%2];" ::"r"(tc::smem_u32(dst)),
+            "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(r.at[0]), "r"(r.at[1]), "r"(r.at[2]), "r"(r.at[3])
+            : "memory");
+    else
+        asm volatile(
+            "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, "
+            "%5, %6, %7}], [%2];" ::"r"(tc::smem_u32(dst)),
+            "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(r.at[0]), "r"(r.at[1]), "r"(r.at[2]), "r"(r.at[3])
+            : "memory");
+}
 
 // One lane waits (a wait by all 32 takes four times as long even where the phase is
 // over); __syncwarp passes on to the others what the barrier guards.

@@ -4,10 +4,10 @@
 // once for 256 lanes; one of the two issues the products of both.
 //
 // Both CTAs' loads report to the first one's barrier.  Where a thread has to touch
-// a stage before its products (rows that threads gather; zeros in place of another
-// expert's rows in the last step of dw), the second CTA's loads report to its own
-// barrier, its product warp, which has no products to issue, waits for them, and
-// arrives at a barrier of the first.  That arrival is of the CTA's scope, as the
+// a stage before its products (zeros in place of another expert's rows in the last
+// step of dw), the second CTA's loads report to its own barrier, its product warp,
+// which has no products to issue, waits for them, and arrives at a barrier of the
+// first.  That arrival is of the CTA's scope, as the
 // tile was written by the async proxy or is ordered by its fence: one that
 // releases at the cluster's scope took 1100 cycles, twice what a step's products
 // take.
@@ -123,7 +123,7 @@ expert_pair_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_const
     const int rank = (int)cluster_rank();
     if (threadIdx.x == 0) {
         for (int i = 0; i < C::STAGES; ++i) {
-            tc::mbar_init(&full[i], GATHER ? 1 + GATHER_WARPS * 32 : 1);
+            tc::mbar_init(&full[i], 1);
             tc::mbar_init(&empty[i], 1);
             tc::mbar_init(&other[i], 1);
         }
@@ -157,7 +157,13 @@ expert_pair_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_const
                 const Unit t = walk.at(u);
                 const int half = ((t.n + 31) & ~31) / 2, l0 = t.l0 + rank * 128, q0 = t.q0 + rank * half;
                 const int boxes = GATHER ? 0 : MODE == DW ? (half + 63) / 64 : 1;
-                const uint32_t bytes = C::P_BYTES + boxes * (MODE == DW ? 8192 : 128 * 128);
+                // bytes of this CTA's stage, and of both
+                auto loaded = [&](int r) {
+                    if (!GATHER) return C::P_BYTES + boxes * (MODE == DW ? 8192 : 128 * 128);
+                    if (MODE == DW) return C::P_BYTES + (half + 63) / 64 * 8192;
+                    return C::P_BYTES + (max(0, min(half, t.n - r * half)) + 3) / 4 * 512;
+                };
+                const uint32_t bytes = loaded(rank), both = loaded(0) + loaded(1);
                 const int end = MODE == DW ? off[t.e + 1] : 0;
                 for (int s = 0; s < t.steps; ++s, ++it) {
                     if (it % TURNS != turn) continue;
@@ -166,10 +172,10 @@ expert_pair_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_const
                     uint8_t* st = smem + slot * C::STAGE;
                     uint8_t* sq = st + C::P_BYTES;
                     const int k0 = s * STEP, row = t.row0 + k0;
-                    const bool relay = GATHER || (MODE == DW && end - row < STEP);
+                    const bool relay = MODE == DW && end - row < STEP;
                     const uint32_t bar = bar_in(&full[slot], relay ? rank : 0);
                     if (relay) tc::mbar_arrive_expect_tx(&full[slot], bytes);
-                    else if (rank == 0) tc::mbar_arrive_expect_tx(&full[slot], 2 * bytes);
+                    else if (rank == 0) tc::mbar_arrive_expect_tx(&full[slot], both);
                     if constexpr (MODE == FWD) {
                         pair_load_3d(st, &map_p, bar, k0, l0, t.e);
                     } else if constexpr (MODE == DX) {
@@ -199,7 +205,7 @@ expert_pair_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_const
             const int left = MODE == DW ? (off[t.e + 1] - t.row0) % STEP : 0, whole = t.steps - (left > 0);
             if (rank == 0 && lane == 0) ok = ok && lane_wait(&acc_empty[buf], acc_phase ^ 1, abort_flag, g.status);
             __syncwarp();
-            if (!GATHER && rank == 0) {
+            if (rank == 0) {
 #pragma unroll 1
                 for (int s = 0; s < whole; ++s) {
                     if (lane == 0) ok = ok && lane_wait(&full[slot], phase, abort_flag, g.status);
@@ -209,101 +215,92 @@ expert_pair_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_const
                     commit_pair(&empty[slot]);
                     if (++slot == C::STAGES) { slot = 0; phase ^= 1; }
                 }
-            } else if (!GATHER) {
+            } else {
                 slot += whole;  // the first CTA's affair
                 phase ^= slot / C::STAGES & 1;
                 slot %= C::STAGES;
             }
-            // what this warp of the second CTA passes on
-            for (int s = GATHER ? 0 : whole; s < t.steps; ++s) {
-                const bool tail = MODE == DW && s == whole;
-                const int k16 = tail ? (left + 15) / 16 : STEP / 16;
-                uint8_t* st = smem + slot * C::STAGE;
-                if (lane == 0) ok = ok && lane_wait(&full[slot], rank == 0 ? phase : here >> slot & 1, abort_flag, g.status);
-                here ^= 1u << slot;
-                __syncwarp();
-                if (tail) {
+            if constexpr (MODE == DW) {
+                if (left > 0) {
+                    const int k16 = (left + 15) / 16;
+                    uint8_t* st = smem + slot * C::STAGE;
+                    if (lane == 0) ok = ok && lane_wait(&full[slot], rank == 0 ? phase : here >> slot & 1, abort_flag, g.status);
+                    here ^= 1u << slot;
+                    __syncwarp();
                     // rows behind the expert's last, up to the 16 of a product, are another's: zeros in their place
                     const int zero = k16 * 16 - left;
                     for (int i = lane; i < 4 * zero * 8; i += 32) {
                         const int b = i / (zero * 8), c = i - b * zero * 8;
                         *reinterpret_cast<uint4*>(st + b * 8192 + left * 128 + c * 16) = make_uint4(0, 0, 0, 0);
                     }
-                }
-                // what threads wrote (gathered rows, zeros), before the tensor core's reads
-                tc::fence_proxy_async_smem();
-                __syncwarp();
-                if (rank == 0) {
-                    if (lane == 0) ok = ok && lane_wait(&other[slot], relayed >> slot & 1, abort_flag, g.status);
-                    relayed ^= 1u << slot;
+                    tc::fence_proxy_async_smem();
                     __syncwarp();
-                    tc::tc_fence_after();
-                    mma_stage<MODE>(d, tc::smem_u32(st), idesc, s == 0, k16);
-                    commit_pair(&empty[slot]);
-                } else if (lane == 0) {
-                    arrive_first(&other[slot]);
+                    if (rank == 0) {
+                        if (lane == 0) ok = ok && lane_wait(&other[slot], relayed >> slot & 1, abort_flag, g.status);
+                        relayed ^= 1u << slot;
+                        __syncwarp();
+                        tc::tc_fence_after();
+                        mma_stage<MODE>(d, tc::smem_u32(st), idesc, whole == 0, k16);
+                        commit_pair(&empty[slot]);
+                    } else if (lane == 0) {
+                        arrive_first(&other[slot]);
+                    }
+                    __syncwarp();
+                    if (++slot == C::STAGES) { slot = 0; phase ^= 1; }
                 }
-                __syncwarp();
-                if (++slot == C::STAGES) { slot = 0; phase ^= 1; }
             }
             if (rank == 0) commit_pair(&acc_full[buf]);
             if (++buf == 2) { buf = 0; acc_phase ^= 1; }
         }
         __syncwarp();
     } else if (warp > PAIR_MMA) {
-        const int gw = warp - PAIR_MMA - 1;
-        int slot = 0;
-        uint32_t phase = 0;
+        const int gw = warp - PAIR_MMA - 1, turn = gw / GATHER_SHARE, share = gw % GATHER_SHARE;
+        int it = 0;
         for (int u = first; u < total && !*abort_flag; u += stride) {
             const Unit t = walk.at(u);
             const int half = ((t.n + 31) & ~31) / 2, q0 = t.q0 + rank * half;
             if constexpr (MODE == FWD) {
-                const int n = max(0, min(half, t.n - rank * half));
-                GatherRows<8> rows;
-                if (t.steps > 0) rows.set(g, q0, n, gw, lane);
-                for (int s = 0; s < t.steps; ++s) {
-                    if (!warp_wait(&empty[slot], phase ^ 1, abort_flag, g.status)) break;
-                    rows.load(g, smem + slot * C::STAGE + C::P_BYTES, n, s * STEP, gw, lane);
-                    tc::cp_async_mbar_arrive_noinc(&full[slot]);
-                    if (++slot == C::STAGES) { slot = 0; phase ^= 1; }
+                // lane j has the group share + 4 j of this CTA's rows
+                const int n = min(half, t.n - rank * half), group = share + GATHER_SHARE * lane;
+                const bool mine = lane < 32 / GATHER_SHARE && group * 4 < n;
+                GatherRows rows;
+                if (t.steps > 0 && mine) {
+                    rows.read(g, q0, n, group);
+                    rows.to_rows(g);
+                }
+                for (int s = 0; s < t.steps; ++s, ++it) {
+                    if (it % GATHER_TURNS != turn) continue;
+                    const int slot = it % C::STAGES;
+                    if (!warp_wait(&empty[slot], (it / C::STAGES & 1) ^ 1, abort_flag, g.status)) break;
+                    if (mine)
+                        tma_gather4<true>(smem + slot * C::STAGE + C::P_BYTES + group * 512, &map_q, bar_in(&full[slot], 0),
+                                          s * STEP, rows);
+                    __syncwarp();
                 }
             } else {
-                // rows lane / 8 + 4 (warp + 4 i) of a step, i < 4, columns of two blocks of 64
-                const int end = off[t.e + 1], piece = lane & 7, r0 = gw * 4 + (lane >> 3);
-                int next[4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int r = t.row0 + r0 + 16 * i;
-                    next[i] = t.steps > 0 && r < end ? g.pairs[r] : -1;
+                // lane j has the group (share + 4 j) % 16 of a step's rows, in the block of 64 columns (share + 4 j) / 16
+                const int end = off[t.e + 1], job = share + GATHER_SHARE * lane, group = job & 15, block = job >> 4;
+                const bool mine = lane < 32 / GATHER_SHARE && block * 64 < half;
+                GatherRows next;
+                int s = (turn - it % GATHER_TURNS + GATHER_TURNS) % GATHER_TURNS;
+                it += s;
+                if (mine) next.read(g, t.row0 + s * STEP, s < t.steps ? end - t.row0 - s * STEP : 0, group);
+                for (; s < t.steps; s += GATHER_TURNS, it += GATHER_TURNS) {
+                    const int row = t.row0 + s * STEP, slot = it % C::STAGES;
+                    GatherRows rows = next;
+                    // the next step's entries are read while this one's place is waited for
+                    const int later = row + GATHER_TURNS * STEP;
+                    if (mine) next.read(g, later, s + GATHER_TURNS < t.steps ? end - later : 0, group);
+                    rows.to_rows(g);
+                    if (!warp_wait(&empty[slot], (it / C::STAGES & 1) ^ 1, abort_flag, g.status)) break;
+                    if (mine)
+                        tma_gather4<true>(smem + slot * C::STAGE + C::P_BYTES + block * 8192 + group * 512, &map_q,
+                                          bar_in(&full[slot], end - row < STEP ? rank : 0), q0 + block * 64, rows);
+                    __syncwarp();
                 }
-                for (int s = 0; s < t.steps; ++s) {
-                    const uint16_t* at[4];
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        at[i] = row_of(g, next[i]);
-                        const int r = t.row0 + (s + 1) * STEP + r0 + 16 * i;
-                        next[i] = s + 1 < t.steps && r < end ? g.pairs[r] : -1;
-                    }
-                    if (!warp_wait(&empty[slot], phase ^ 1, abort_flag, g.status)) break;
-                    const uint32_t sq = tc::smem_u32(smem + slot * C::STAGE + C::P_BYTES);
-#pragma unroll
-                    for (int b = 0; b < 2; ++b) {
-                        const int c = q0 + b * 64 + piece * 8;
-                        const int bytes = max(0, min(16, (g.cols - c) * 2));
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const bool real = at[i] != nullptr && bytes > 0;
-                            if (b * 64 < half)
-                                cp_async_16_part(sq + b * 8192 + tc::sw128_offset(r0 + 16 * i, piece),
-                                                 real ? at[i] + c : static_cast<const uint16_t*>(g.x), real ? bytes : 0);
-                        }
-                    }
-                    tc::cp_async_mbar_arrive_noinc(&full[slot]);
-                    if (++slot == C::STAGES) { slot = 0; phase ^= 1; }
-                }
+                it += t.steps - s;
             }
         }
-        tc::cp_async_wait<0>();
     } else {
         const int quad = warp & 3, half = warp >> 2;
         uint8_t* const stage = smem + C::OUT_OFF + warp * STAGE_OUT;
