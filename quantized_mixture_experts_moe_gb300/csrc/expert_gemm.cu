@@ -168,7 +168,7 @@ expert_gemm_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_const
                 const int slot = it % C::STAGES;
                 if (!warp_wait(&empty[slot], (it / C::STAGES & 1) ^ 1, abort_flag, g.status)) break;
                 if (mine)
-                    tma_gather4(smem + slot * C::STAGE + C::P_BYTES + group * 512, &map_q, tc::smem_u32(&full[slot]), s * STEP, rows);
+                    tma_gather4(smem + slot * C::STAGE + C::P_BYTES + group * 512, &map_q, &full[slot], s * STEP, rows);
                 __syncwarp();
             }
         }
@@ -211,14 +211,76 @@ expert_gemm_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_const
     if (warp == WARP_MMA) tc::tmem_dealloc(tm, C::TMEM_COLS);
 }
 
-// Rows whose start TMA cannot address, copied to rows of whole 16-byte pieces.
-__global__ void __launch_bounds__(256) pad_rows_kernel(const uint16_t* x, int64_t rows_inner, int64_t ld, int64_t outer,
-                                                       int64_t cols, uint16_t* to, int64_t ldt, int64_t rows) {
+// Rows of 16-bit values laid out for TMA: rows that start off the 16-byte
+// boundaries, and rows of x in expert order.  A warp takes a row; a lane loads
+// aligned pieces of 16 bytes, only such as hold values of the row, and takes what
+// lies in the next piece from its neighbour.
+struct RowCopy {
+    const uint16_t* x;
+    int64_t rows, inner, ld, outer;  // row r: (r / inner) * outer + (r % inner) * ld
+    const int32_t* pairs;            // or the row of x of a slot
+    int k, x_rows;
+    int cols;
+    uint16_t* to;
+    int64_t ldt;
+};
+__device__ __forceinline__ uint4 shifted(uint4 v, uint4 w, int words, bool half) {
+    uint32_t a, b, c, d, e;
+    switch (words) {
+        case 0: a = v.x; b = v.y; c = v.z; d = v.w; e = w.x; break;
+        case 1: a = v.y; b = v.z; c = v.w; d = w.x; e = w.y; break;
+        case 2: a = v.z; b = v.w; c = w.x; d = w.y; e = w.z; break;
+        default: a = v.w; b = w.x; c = w.y; d = w.z; e = w.w; break;
+    }
+    if (!half) return make_uint4(a, b, c, d);
+    return make_uint4(__byte_perm(a, b, 0x5432), __byte_perm(b, c, 0x5432), __byte_perm(c, d, 0x5432), __byte_perm(d, e, 0x5432));
+}
+__global__ void __launch_bounds__(256) copy_rows_kernel(const RowCopy c) {
     pdl_wait();
     pdl_trigger();
-    for (int64_t r = blockIdx.x; r < rows; r += gridDim.x) {
-        const uint16_t* from = x + (r / rows_inner) * outer + (r % rows_inner) * ld;
-        for (int64_t c = threadIdx.x; c < cols; c += 256) to[r * ldt + c] = from[c];
+    const int lane = threadIdx.x & 31;
+    constexpr int U = 4;  // pieces of a lane on their way
+    for (int64_t r = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5); r < c.rows; r += (int64_t)gridDim.x * 8) {
+        const uint16_t* from;
+        if (c.pairs) {
+            const int p = c.pairs[r], t = p >= 0 ? p / c.k : c.x_rows;
+            from = t < c.x_rows ? c.x + t * c.ld : nullptr;
+        } else {
+            from = c.x + r / c.inner * c.outer + r % c.inner * c.ld;
+        }
+        uint16_t* const to = c.to + r * c.ldt;
+        const int pieces = (c.cols + 7) / 8;
+        if (!from) {
+            for (int i = lane; i < pieces; i += 32) *reinterpret_cast<uint4*>(to + i * 8) = make_uint4(0, 0, 0, 0);
+            continue;
+        }
+        const int shift = (int)(reinterpret_cast<uintptr_t>(from) & 15);  // bytes
+        const uint4* const base = reinterpret_cast<const uint4*>(reinterpret_cast<uintptr_t>(from) - shift);
+        const int there = (shift + c.cols * 2 + 15) / 16;  // pieces that hold values of the row
+        for (int i0 = lane; i0 - lane < pieces; i0 += 32 * U) {
+            uint4 v[U + 1];
+#pragma unroll
+            for (int j = 0; j < U; ++j) v[j] = i0 + j * 32 < there ? base[i0 + j * 32] : make_uint4(0, 0, 0, 0);
+            if (shift) {
+                // lane 31's neighbour is lane 0's next piece
+                v[U] = lane == 0 && i0 + U * 32 < there ? base[i0 + U * 32] : make_uint4(0, 0, 0, 0);
+#pragma unroll
+                for (int j = 0; j < U; ++j) {
+                    const uint4 mine = lane == 0 ? v[j + 1] : v[j];  // what the lane below wants
+                    uint4 w;
+                    w.x = __shfl_sync(0xFFFFFFFFu, mine.x, (lane + 1) & 31);
+                    w.y = __shfl_sync(0xFFFFFFFFu, mine.y, (lane + 1) & 31);
+                    w.z = __shfl_sync(0xFFFFFFFFu, mine.z, (lane + 1) & 31);
+                    w.w = __shfl_sync(0xFFFFFFFFu, mine.w, (lane + 1) & 31);
+                    if (i0 + j * 32 < pieces)
+                        *reinterpret_cast<uint4*>(to + (i0 + j * 32) * 8) = shifted(v[j], w, shift >> 2, shift & 2);
+                }
+            } else {
+#pragma unroll
+                for (int j = 0; j < U; ++j)
+                    if (i0 + j * 32 < pieces) *reinterpret_cast<uint4*>(to + (i0 + j * 32) * 8) = v[j];
+            }
+        }
     }
 }
 
@@ -235,23 +297,27 @@ inline bool fits(const Mat& m) {
     return aligned16(m.p) && (m.rows == 1 || m.ld % 8 == 0) && (m.experts == 1 || m.stride % 8 == 0);
 }
 
-static int as_tma(Mat& m, uint8_t*& ws, size_t& left, cudaStream_t st) {
-    if (fits(m)) {
-        if (m.ld % 8) m.ld = (m.cols + 7) / 8 * 8;  // a single row: the stride is not used
-        return QMOE_OK;
-    }
-    const int64_t rows = m.rows * m.experts, ld = (m.cols + 7) / 8 * 8;
+// Copies m (or its rows in the order of pairs) into the workspace.
+static int copy_rows(Mat& m, const int32_t* pairs, int64_t P, int k, uint8_t*& ws, size_t& left, cudaStream_t st) {
+    const int64_t rows = pairs ? P : m.rows * m.experts, ld = (m.cols + 7) / 8 * 8;
     const size_t need = padded(rows, m.cols);
     if (need > left) return QMOE_ERR_ARG;
-    const int64_t grid = rows < 8 * row::kSMs ? rows : 8 * row::kSMs;
-    const int rc = launch_pdl(pad_rows_kernel, dim3((unsigned)grid), dim3(256), 0, st, static_cast<const uint16_t*>(m.p),
-                              m.rows, m.ld, m.stride, m.cols, reinterpret_cast<uint16_t*>(ws), ld, rows);
+    const RowCopy c = {static_cast<const uint16_t*>(m.p), rows, m.rows, m.ld, m.stride, pairs, k, (int)(pairs ? m.rows : 0),
+                       (int)m.cols, reinterpret_cast<uint16_t*>(ws), ld};
+    const int64_t grid = (rows + 7) / 8, most = 32 * row::kSMs;
+    const int rc = launch_pdl(copy_rows_kernel, dim3((unsigned)(grid < most ? grid : most)), dim3(256), 0, st, c);
     m.p = ws;
     m.ld = ld;
     m.stride = ld * m.rows;
+    if (pairs) m.rows = P;
     ws += need;
     left -= need;
     return rc;
+}
+static int as_tma(Mat& m, uint8_t*& ws, size_t& left, cudaStream_t st) {
+    if (!fits(m)) return copy_rows(m, nullptr, 0, 0, ws, left, st);
+    if (m.ld % 8) m.ld = (m.cols + 7) / 8 * 8;  // a single row: the stride is not used
+    return QMOE_OK;
 }
 
 static int map_of(CUtensorMap* map, const Mat& m, int dtype, int box_cols, int box_rows, bool three) {
@@ -280,6 +346,10 @@ static int launch(const CUtensorMap& mp, const CUtensorMap& mq, const Args& g, i
 }
 
 // Few rows for each expert: narrow tiles, whose stages are almost all weight, so that more of them are in flight.
+// Gathered rows of x are read as they lie for few rows an expert; for many they are
+// laid out in expert order first: a tile's rows are read again for every 256
+// outputs, and TMA's gather of four rows takes as long as a box of 128 (8192 x 8
+// rows of 4096, 2816 outputs: 1136 us gathered in the product, 960 laid out).
 inline int tile_of(int64_t P, int E) {
     const int64_t touched = P < E ? P : E;
     return P <= 16 * touched ? 32 : P <= 96 * touched ? 128 : 256;
@@ -299,7 +369,7 @@ static int run_rows(Mat w, Mat q, Args& g, int dtype, cudaStream_t st) {
     switch (nt) {
         case 32: return launch<MODE, 32, GATHER>(mp, mq, g, most, st);
         case 128: return launch<MODE, 128, GATHER>(mp, mq, g, most, st);
-        default: return launch_pair<MODE, GATHER>(mp, mq, g, most, st);
+        default: return GATHER ? QMOE_ERR_UNSUPPORTED : launch_pair<MODE>(mp, mq, g, most, st);
     }
 }
 
@@ -335,6 +405,11 @@ extern "C" size_t qmoe_expert_copy_bytes(int64_t rows, int64_t cols) {
     return eg::padded(rows, cols);
 }
 
+extern "C" size_t qmoe_expert_gather_bytes(int64_t P, int E, int64_t K, int dw) {
+    if (P <= 0 || E <= 0 || K <= 0 || (!dw && eg::tile_of(P, E) < 256)) return 0;
+    return eg::padded(P, K);
+}
+
 extern "C" int qmoe_expert_linear(int64_t P, int E, int64_t N, int64_t K, int dtype, const void* x, int64_t ldx,
                                   int64_t x_rows, const int32_t* pairs, int k, const void* w, int64_t ldw, int64_t w_expert,
                                   const int32_t* offsets, void* y, int y_dtype, int64_t ldy, int32_t* dev_status, void* ws,
@@ -352,7 +427,11 @@ extern "C" int qmoe_expert_linear(int64_t P, int E, int64_t N, int64_t K, int dt
     cudaStream_t st = (cudaStream_t)stream;
     uint8_t* at = static_cast<uint8_t*>(ws);
     size_t left = ws && !(reinterpret_cast<uintptr_t>(ws) & 255u) ? ws_bytes : 0;
-    if ((rc = eg::as_tma(mw, at, left, st)) != QMOE_OK || (rc = eg::as_tma(mx, at, left, st)) != QMOE_OK) return rc;
+    if ((rc = eg::as_tma(mw, at, left, st)) != QMOE_OK) return rc;
+    const bool lay_out = pairs && qmoe_expert_gather_bytes(P, E, K, 0);
+    rc = lay_out ? eg::copy_rows(mx, pairs, P, k, at, left, st) : eg::as_tma(mx, at, left, st);
+    if (rc != QMOE_OK) return rc;
+    if (lay_out) pairs = nullptr;
     const int size = row::dtype_size(y_dtype);
     eg::Args g = {(int)P, E, (int)N, 0, (int)K, offsets, pairs, k, (int)mx.rows, y, ldy, 0, y_dtype,
                   aligned16(y) && ldy * size % 16 == 0,
@@ -405,14 +484,16 @@ extern "C" int qmoe_expert_linear_dw(int64_t P, int E, int64_t N, int64_t K, int
     if (!eg::mat_ok(my, 2) || !eg::mat_ok(mx, 2)) return QMOE_ERR_ARG;
     uint8_t* at = static_cast<uint8_t*>(ws);
     size_t left = ws && !(reinterpret_cast<uintptr_t>(ws) & 255u) ? ws_bytes : 0;
-    if ((rc = eg::as_tma(my, at, left, st)) != QMOE_OK || (rc = eg::as_tma(mx, at, left, st)) != QMOE_OK) return rc;
-    eg::Args g = {(int)P, E, (int)N, (int)K, 0, offsets, pairs, k, (int)mx.rows, dw, K, N * K, dw_dtype,
+    if ((rc = eg::as_tma(my, at, left, st)) != QMOE_OK) return rc;
+    rc = pairs ? eg::copy_rows(mx, pairs, P, k, at, left, st) : eg::as_tma(mx, at, left, st);
+    if (rc != QMOE_OK) return rc;
+    eg::Args g = {(int)P, E, (int)N, (int)K, 0, offsets, nullptr, 0, (int)mx.rows, dw, K, N * K, dw_dtype,
                   aligned16(dw) && K * size % 16 == 0,
                   (dtype == QMOE_BF16 ? tc::idesc_bf16_f32(0, 0) : tc::idesc_f16_f32(0, 0)) | 3u << 15, dev_status};
     CUtensorMap mp, mq;
     rc = eg::map_of(&mp, my, dtype, 64, eg::STEP, false);
     if (rc != QMOE_OK) return rc;
-    rc = eg::map_of(&mq, mx, dtype, 64, pairs ? 1 : eg::STEP, false);
+    rc = eg::map_of(&mq, mx, dtype, 64, eg::STEP, false);
     if (rc != QMOE_OK) return rc;
-    return pairs ? eg::launch_pair<eg::DW, true>(mp, mq, g, units, st) : eg::launch_pair<eg::DW, false>(mp, mq, g, units, st);
+    return eg::launch_pair<eg::DW>(mp, mq, g, units, st);
 }

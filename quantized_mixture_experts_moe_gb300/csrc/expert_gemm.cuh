@@ -58,20 +58,12 @@ struct GatherRows {
     }
 };
 
-template <bool PAIR = false>
-__device__ __forceinline__ void tma_gather4(void* dst, const CUtensorMap* map, uint32_t bar, int x, const GatherRows& r) {
-    if constexpr (PAIR)
-        asm volatile(
-            "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes.cta_group::2 [%0], "
-            "[%1, {%3, %4, %5, %6, %7}], [%2];" ::"r"(tc::smem_u32(dst)),
-            "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(r.at[0]), "r"(r.at[1]), "r"(r.at[2]), "r"(r.at[3])
-            : "memory");
-    else
-        asm volatile(
-            "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, "
-            "%5, %6, %7}], [%2];" ::"r"(tc::smem_u32(dst)),
-            "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(r.at[0]), "r"(r.at[1]), "r"(r.at[2]), "r"(r.at[3])
-            : "memory");
+__device__ __forceinline__ void tma_gather4(void* dst, const CUtensorMap* map, uint64_t* bar, int x, const GatherRows& r) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, "
+        "%5, %6, %7}], [%2];" ::"r"(tc::smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(tc::smem_u32(bar)), "r"(x), "r"(r.at[0]), "r"(r.at[1]), "r"(r.at[2]), "r"(r.at[3])
+        : "memory");
 }
 
 // One lane waits (a wait by all 32 takes four times as long even where the phase is
@@ -304,7 +296,7 @@ __device__ __forceinline__ void read_offsets(const Args& g, int* off, int* base)
 // What the kernels take: map_p of the lane side, map_q of the column side.
 //
 // Pairs of CTAs, 256 x 256 tiles: for many rows an expert, and for dw.
-template <int MODE, bool GATHER>
+template <int MODE>
 int launch_pair(const CUtensorMap& mp, const CUtensorMap& mq, const Args& g, int64_t most, cudaStream_t st);
 
 }  // namespace eg

@@ -17,9 +17,9 @@ namespace qmoe {
 namespace eg {
 
 // Warps: the epilogue's, two that load tiles, step by step in turn (a load takes a
-// thread some 100 cycles to issue), one that issues products, then those that gather.
+// thread some 100 cycles to issue), one that issues products.
 constexpr int PAIR_TMA = 8, TURNS = 2, PAIR_MMA = PAIR_TMA + TURNS;
-constexpr int pair_threads(bool gather) { return (PAIR_MMA + 1 + (gather ? GATHER_WARPS : 0)) * 32; }
+constexpr int PAIR_THREADS = (PAIR_MMA + 1) * 32;
 
 template <int MODE>
 struct PairCfg {
@@ -103,8 +103,8 @@ __device__ __forceinline__ void mma_stage(uint32_t d, uint32_t stage, uint32_t i
         if (k < k16) mma_pair(d, da + SA * k, db + SB * k, idesc, !first || k > 0);
 }
 
-template <int MODE, bool GATHER>
-__global__ void __launch_bounds__(pair_threads(GATHER), 1)
+template <int MODE>
+__global__ void __launch_bounds__(PAIR_THREADS, 1)
 expert_pair_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_constant__ CUtensorMap map_q, const Args g) {
     using C = PairCfg<MODE>;
     extern __shared__ uint8_t smem_raw[];
@@ -156,14 +156,8 @@ expert_pair_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_const
             for (int u = first; u < total && !*abort_flag; u += stride) {
                 const Unit t = walk.at(u);
                 const int half = ((t.n + 31) & ~31) / 2, l0 = t.l0 + rank * 128, q0 = t.q0 + rank * half;
-                const int boxes = GATHER ? 0 : MODE == DW ? (half + 63) / 64 : 1;
-                // bytes of this CTA's stage, and of both
-                auto loaded = [&](int r) {
-                    if (!GATHER) return C::P_BYTES + boxes * (MODE == DW ? 8192 : 128 * 128);
-                    if (MODE == DW) return C::P_BYTES + (half + 63) / 64 * 8192;
-                    return C::P_BYTES + (max(0, min(half, t.n - r * half)) + 3) / 4 * 512;
-                };
-                const uint32_t bytes = loaded(rank), both = loaded(0) + loaded(1);
+                const int boxes = MODE == DW ? (half + 63) / 64 : 1;
+                const uint32_t bytes = C::P_BYTES + boxes * (MODE == DW ? 8192 : 128 * 128);
                 const int end = MODE == DW ? off[t.e + 1] : 0;
                 for (int s = 0; s < t.steps; ++s, ++it) {
                     if (it % TURNS != turn) continue;
@@ -175,7 +169,7 @@ expert_pair_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_const
                     const bool relay = MODE == DW && end - row < STEP;
                     const uint32_t bar = bar_in(&full[slot], relay ? rank : 0);
                     if (relay) tc::mbar_arrive_expect_tx(&full[slot], bytes);
-                    else if (rank == 0) tc::mbar_arrive_expect_tx(&full[slot], both);
+                    else if (rank == 0) tc::mbar_arrive_expect_tx(&full[slot], 2 * bytes);
                     if constexpr (MODE == FWD) {
                         pair_load_3d(st, &map_p, bar, k0, l0, t.e);
                     } else if constexpr (MODE == DX) {
@@ -185,9 +179,10 @@ expert_pair_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_const
                         pair_load_2d(st, &map_p, bar, l0, row);
                         pair_load_2d(st + 8192, &map_p, bar, l0 + 64, row);
                     }
-                    if constexpr (!GATHER && MODE != DW) pair_load_2d(sq, &map_q, bar, k0, q0);
-                    if constexpr (!GATHER && MODE == DW)
-                        for (int b = 0; b < boxes; ++b) pair_load_2d(sq + b * 8192, &map_q, bar, q0 + b * 64, row);
+                    for (int b = 0; b < boxes; ++b) {
+                        if constexpr (MODE == DW) pair_load_2d(sq + b * 8192, &map_q, bar, q0 + b * 64, row);
+                        else pair_load_2d(sq, &map_q, bar, k0, q0);
+                    }
                 }
             }
         }
@@ -253,54 +248,6 @@ expert_pair_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_const
             if (++buf == 2) { buf = 0; acc_phase ^= 1; }
         }
         __syncwarp();
-    } else if (warp > PAIR_MMA) {
-        const int gw = warp - PAIR_MMA - 1, turn = gw / GATHER_SHARE, share = gw % GATHER_SHARE;
-        int it = 0;
-        for (int u = first; u < total && !*abort_flag; u += stride) {
-            const Unit t = walk.at(u);
-            const int half = ((t.n + 31) & ~31) / 2, q0 = t.q0 + rank * half;
-            if constexpr (MODE == FWD) {
-                // lane j has the group share + 4 j of this CTA's rows
-                const int n = min(half, t.n - rank * half), group = share + GATHER_SHARE * lane;
-                const bool mine = lane < 32 / GATHER_SHARE && group * 4 < n;
-                GatherRows rows;
-                if (t.steps > 0 && mine) {
-                    rows.read(g, q0, n, group);
-                    rows.to_rows(g);
-                }
-                for (int s = 0; s < t.steps; ++s, ++it) {
-                    if (it % GATHER_TURNS != turn) continue;
-                    const int slot = it % C::STAGES;
-                    if (!warp_wait(&empty[slot], (it / C::STAGES & 1) ^ 1, abort_flag, g.status)) break;
-                    if (mine)
-                        tma_gather4<true>(smem + slot * C::STAGE + C::P_BYTES + group * 512, &map_q, bar_in(&full[slot], 0),
-                                          s * STEP, rows);
-                    __syncwarp();
-                }
-            } else {
-                // lane j has the group (share + 4 j) % 16 of a step's rows, in the block of 64 columns (share + 4 j) / 16
-                const int end = off[t.e + 1], job = share + GATHER_SHARE * lane, group = job & 15, block = job >> 4;
-                const bool mine = lane < 32 / GATHER_SHARE && block * 64 < half;
-                GatherRows next;
-                int s = (turn - it % GATHER_TURNS + GATHER_TURNS) % GATHER_TURNS;
-                it += s;
-                if (mine) next.read(g, t.row0 + s * STEP, s < t.steps ? end - t.row0 - s * STEP : 0, group);
-                for (; s < t.steps; s += GATHER_TURNS, it += GATHER_TURNS) {
-                    const int row = t.row0 + s * STEP, slot = it % C::STAGES;
-                    GatherRows rows = next;
-                    // the next step's entries are read while this one's place is waited for
-                    const int later = row + GATHER_TURNS * STEP;
-                    if (mine) next.read(g, later, s + GATHER_TURNS < t.steps ? end - later : 0, group);
-                    rows.to_rows(g);
-                    if (!warp_wait(&empty[slot], (it / C::STAGES & 1) ^ 1, abort_flag, g.status)) break;
-                    if (mine)
-                        tma_gather4<true>(smem + slot * C::STAGE + C::P_BYTES + block * 8192 + group * 512, &map_q,
-                                          bar_in(&full[slot], end - row < STEP ? rank : 0), q0 + block * 64, rows);
-                    __syncwarp();
-                }
-                it += t.steps - s;
-            }
-        }
     } else {
         const int quad = warp & 3, half = warp >> 2;
         uint8_t* const stage = smem + C::OUT_OFF + warp * STAGE_OUT;
@@ -345,10 +292,10 @@ expert_pair_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_const
         asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tm), "r"(512) : "memory");
 }
 
-template <int MODE, bool GATHER>
+template <int MODE>
 int launch_pair(const CUtensorMap& mp, const CUtensorMap& mq, const Args& g, int64_t most, cudaStream_t st) {
     using C = PairCfg<MODE>;
-    const int rc = row::allow_smem<expert_pair_kernel<MODE, GATHER>>(C::SMEM);
+    const int rc = row::allow_smem<expert_pair_kernel<MODE>>(C::SMEM);
     if (rc != QMOE_OK) return rc;
     const int64_t pairs = most < row::kSMs / 2 ? most : row::kSMs / 2;
     cudaLaunchAttribute attr[2];
@@ -360,19 +307,17 @@ int launch_pair(const CUtensorMap& mp, const CUtensorMap& mq, const Args& g, int
     attr[1].val.clusterDim.z = 1;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(2 * pairs));
-    cfg.blockDim = dim3(pair_threads(GATHER));
+    cfg.blockDim = dim3(PAIR_THREADS);
     cfg.dynamicSmemBytes = C::SMEM;
     cfg.stream = st;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, expert_pair_kernel<MODE, GATHER>, mp, mq, g) == cudaSuccess ? QMOE_OK : QMOE_ERR_LAUNCH;
+    return cudaLaunchKernelEx(&cfg, expert_pair_kernel<MODE>, mp, mq, g) == cudaSuccess ? QMOE_OK : QMOE_ERR_LAUNCH;
 }
 
-template int launch_pair<FWD, false>(const CUtensorMap&, const CUtensorMap&, const Args&, int64_t, cudaStream_t);
-template int launch_pair<FWD, true>(const CUtensorMap&, const CUtensorMap&, const Args&, int64_t, cudaStream_t);
-template int launch_pair<DX, false>(const CUtensorMap&, const CUtensorMap&, const Args&, int64_t, cudaStream_t);
-template int launch_pair<DW, false>(const CUtensorMap&, const CUtensorMap&, const Args&, int64_t, cudaStream_t);
-template int launch_pair<DW, true>(const CUtensorMap&, const CUtensorMap&, const Args&, int64_t, cudaStream_t);
+template int launch_pair<FWD>(const CUtensorMap&, const CUtensorMap&, const Args&, int64_t, cudaStream_t);
+template int launch_pair<DX>(const CUtensorMap&, const CUtensorMap&, const Args&, int64_t, cudaStream_t);
+template int launch_pair<DW>(const CUtensorMap&, const CUtensorMap&, const Args&, int64_t, cudaStream_t);
 
 }  // namespace eg
 }  // namespace qmoe
