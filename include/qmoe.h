@@ -685,15 +685,14 @@ int qmoe_fp8_linear(int64_t M, int64_t N, int64_t K, int x_dtype, const void* x,
  * offsets int32 [E + 1] from 0 to at most P, none below the one before it; else bit
  *   QMOE_DEV_BAD_OFFSETS of *dev_status is set, and which rows belong to which
  *   expert is undefined.  QMOE_DEV_WAIT_TIMEOUT as for qmoe_fp8_matmul.
- * An x, dy or w whose base or strides are no multiples of 16 bytes is first copied
- * into the workspace (256-byte aligned), which then needs the sum of
- * qmoe_expert_copy_bytes(rows, columns) of each such operand (for w E * N rows).
- * Where pairs are given and qmoe_expert_gather_bytes(P, E, K, dw) (dw 0 for
- * qmoe_expert_linear, 1 for qmoe_expert_linear_dw) is not 0, x is laid out in
- * expert order first, and the workspace needs that in place of x's copy.  A call
- * that needs nothing of it takes ws NULL.  E <= 1024, other sizes <= 2^30. */
+ * ws (256-byte aligned; NULL where nothing is needed): qmoe_expert_workspace_bytes
+ *   (op 0 for qmoe_expert_linear, 1 for ..._dx, 2 for ..._dw; pairs: whether they are
+ *   given), and for each x, dy or w whose base or strides are no multiples of 16
+ *   bytes, which is copied first, qmoe_expert_copy_bytes(rows, columns) (for w E * N
+ *   rows; x with pairs as it lies).
+ * E <= 1024, other sizes <= 2^30. */
 size_t qmoe_expert_copy_bytes(int64_t rows, int64_t cols);
-size_t qmoe_expert_gather_bytes(int64_t P, int E, int64_t K, int dw);
+size_t qmoe_expert_workspace_bytes(int64_t P, int E, int64_t N, int64_t K, int op, int pairs);
 int qmoe_expert_linear(int64_t P, int E, int64_t N, int64_t K, int dtype, const void* x, int64_t ldx, int64_t x_rows,
                        const int32_t* pairs, int k, const void* w, int64_t ldw, int64_t w_expert,
                        const int32_t* offsets, void* y, int y_dtype, int64_t ldy, int32_t* dev_status, void* ws,

@@ -631,10 +631,8 @@ Gathered gathered(const at::Tensor& x, const at::Tensor* pairs, int64_t k, const
     return g;
 }
 
-// What x needs of the workspace.
-size_t x_bytes(const Gathered& g, const Experts& m, bool dw) {
-    const size_t n = g.pairs ? qmoe_expert_gather_bytes(g.P, (int)m.E, m.K, dw) : 0;
-    return n ? n : copy_of(g.x, g.rows, m.K);
+size_t product_bytes(const Gathered& g, const Experts& m, int op) {
+    return qmoe_expert_workspace_bytes(g.P, (int)m.E, m.N, m.K, op, g.pairs != nullptr);
 }
 
 PyObject* expert_linear(const Args& a) {  // x, w, offsets, pairs, k, out_dtype, dev_status, ws
@@ -647,7 +645,7 @@ PyObject* expert_linear(const Args& a) {  // x, w, offsets, pairs, k, out_dtype,
     const at::Tensor y = make({g.P, m.N}, yt, x);
     const int yc = code_of(yt);
     const int32_t* offsets = vec_of<int32_t>(&a.tensor(2), m.E + 1, at::kInt);
-    const MaybeWorkspace ws(x_bytes(g, m, false) + copy_of(m), a.maybe(7), x);
+    const MaybeWorkspace ws(product_bytes(g, m, 0) + copy_of(g.x, g.rows, m.K) + copy_of(m), a.maybe(7), x);
     check(qmoe_expert_linear(g.P, (int)m.E, m.N, m.K, code, g.x.p, g.x.ld, g.rows, g.pairs, g.k, m.p, m.ld, m.stride,
                              offsets, y.data_ptr(), yc, m.N, status_of(a.tensor(6)), ws.p, ws.n, stream_of(x)),
           "qmoe_expert_linear");
@@ -666,9 +664,9 @@ PyObject* expert_linear_backward(const Args& a) {  // dy, x, w, offsets, pairs, 
     const int32_t* offsets = vec_of<int32_t>(&a.tensor(3), m.E + 1, at::kInt);
     int32_t* const status = status_of(a.tensor(9));
     const qmoe_stream_t st = stream_of(dy);
-    const size_t cd = copy_of(d, g.P, m.N), cx = x_bytes(g, m, true), cw = copy_of(m);
+    const size_t cd = copy_of(d, g.P, m.N), cx = copy_of(g.x, g.rows, m.K), cw = copy_of(m);
     const bool to_x = a.truth(7), to_w = a.truth(8);
-    const size_t need = std::max(to_x ? cd + cw : 0, to_w ? cd + cx : 0);
+    const size_t need = std::max(to_x ? product_bytes(g, m, 1) + cd + cw : 0, to_w ? product_bytes(g, m, 2) + cd + cx : 0);
     const MaybeWorkspace ws(need, a.maybe(10), dy);
     at::Tensor dx, dw;
     if (to_x) {

@@ -18,6 +18,9 @@ namespace eg {
 
 // Warps: the epilogue's, one that loads tiles, one that issues products, then
 // those that gather.
+#ifndef FEW_MOST
+#define FEW_MOST 0
+#endif
 constexpr int WARP_TMA = 8, WARP_MMA = 9;
 constexpr int threads_of(bool gather) { return (10 + (gather ? GATHER_WARPS : 0)) * 32; }
 
@@ -37,7 +40,63 @@ struct Cfg {
     static_assert(SMEM <= 232448 && STAGES >= 4, "shared memory per CTA");
 };
 
-template <int MODE, int NT, bool GATHER>
+// What a CTA works on: whole tiles in turn; or, SPLIT, its even share of the steps
+// of all tiles in one piece, so that few tiles keep all SMs busy.  The sums of a
+// tile that starts or ends within the share go to the workspace, in fp32, and
+// join_kernel adds the parts of a tile in the CTAs' order.
+struct Segment {
+    Unit t;
+    int s0, s1;  // steps
+    int part;    // -1: the whole tile; 0: it starts before the share, 1: it ends behind it
+};
+template <int MODE, int NT, bool SPLIT>
+struct Segments {
+    Walk<MODE, 128, NT, 16> walk;
+    int64_t at, end;  // steps (SPLIT)
+    int64_t each;     // of a share; the first `more` shares have one step more
+    int more;
+    int u, total, per;
+    __device__ Segments(const Args& g, const int* off, const int* base) : walk(g, off, base) {
+        total = base[g.E + 1];
+        per = (g.red + STEP - 1) / STEP;
+        u = (SPLIT ? base[g.E] : 0) + blockIdx.x;
+        if (SPLIT) {
+            const int64_t steps = (int64_t)base[g.E] * per;
+            each = steps < (1ll << 32) ? (uint32_t)steps / gridDim.x : steps / gridDim.x;
+            more = (int)(steps - each * gridDim.x);
+            at = share(blockIdx.x);
+            end = share(blockIdx.x + 1);
+        }
+    }
+    __device__ __forceinline__ int64_t share(int i) const { return i * each + min(i, more); }
+    __device__ __forceinline__ bool next(Segment& s) {
+        if (SPLIT && at < end) {
+            const int unit = (int)(at < (1ll << 32) ? (uint32_t)at / (uint32_t)per : at / per);
+            s.t = walk.at(unit);
+            s.s0 = (int)(at - (int64_t)unit * per);
+            s.s1 = (int)min((int64_t)per, s.s0 + (end - at));
+            s.part = s.s0 > 0 ? 0 : s.s1 < per ? 1 : -1;
+            at += s.s1 - s.s0;
+            return true;
+        }
+        if (u >= total) return false;
+        s.t = walk.at(u);
+        s.s0 = 0;
+        s.s1 = s.t.steps;
+        s.part = -1;
+        u += gridDim.x;
+        return true;
+    }
+    // CTAs after this one that have a part of the tile that it leaves unfinished
+    __device__ __forceinline__ int others(const Segment& s) const {
+        const int64_t last = end + per - s.s1;
+        int n = 1;
+        while ((int)blockIdx.x + n + 1 < (int)gridDim.x && share(blockIdx.x + n + 1) < last) ++n;
+        return n;
+    }
+};
+
+template <int MODE, int NT, bool GATHER, bool SPLIT>
 __global__ void __launch_bounds__(threads_of(GATHER), 1)
 expert_gemm_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_constant__ CUtensorMap map_q, const Args g) {
     using C = Cfg<MODE, NT>;
@@ -70,21 +129,24 @@ expert_gemm_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_const
         tc::tmem_relinquish();
     }
     pdl_wait();
+    __shared__ int slot_rows[GATHER ? FEW_SLOTS : 1];
+    if (GATHER && g.P <= FEW_SLOTS && threadIdx.x < g.P) slot_rows[threadIdx.x] = row_of(g, g.pairs[threadIdx.x]);
     read_offsets<MODE, 128, NT>(g, off, base);
     tc::tc_fence_before();
     __syncthreads();
     tc::tc_fence_after();
     const uint32_t tm = *tmem_at;
-    Walk<MODE, 128, NT, 16> walk(g, off, base);
-    const int total = walk.total();
+    Segments<MODE, NT, SPLIT> segments(g, off, base);
+    Segment seg;
+    const Unit& t = seg.t;
+    if (SPLIT) pdl_trigger();  // join_kernel needs little, and waits
 
     if (warp == WARP_TMA) {
-        int slot = 0, in_flight = 0;
+        int slot = 0;
         uint32_t phase = 0;
-        for (int u = blockIdx.x; u < total && !*abort_flag; u += gridDim.x) {
-            const Unit t = walk.at(u);
+        while (!*abort_flag && segments.next(seg)) {
             const int boxes = GATHER ? 0 : (t.n + Q_BOX - 1) / Q_BOX;
-            for (int s = 0; s < t.steps; ++s) {
+            for (int s = seg.s0; s < seg.s1; ++s) {
                 if (!warp_wait(&empty[slot], phase ^ 1, abort_flag, g.status)) break;
                 uint8_t* st = smem + slot * C::STAGE;
                 const int k0 = s * STEP;
@@ -101,69 +163,55 @@ expert_gemm_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_const
                 if (lane < boxes)
                     tc::tma_load_2d(st + C::P_BYTES + lane * Q_BOX * 128, &map_q, &full[slot], k0, t.q0 + lane * Q_BOX);
                 __syncwarp();
-                if (in_flight < C::STAGES) ++in_flight;
                 if (++slot == C::STAGES) { slot = 0; phase ^= 1; }
             }
         }
-        if (*abort_flag && lane == 0)  // nobody may have waited for these: no load outlives the CTA
-            for (; in_flight > 0; --in_flight) {
-                if (slot == 0) { slot = C::STAGES; phase ^= 1; }
-                --slot;
-                tc::mbar_wait(&full[slot], phase);
-            }
         __syncwarp();
     } else if (warp == WARP_MMA) {
         int slot = 0, buf = 0;
         uint32_t phase = 0, acc_phase = 0;
-        int last = -1;
-        uint32_t last_phase = 0;
-        for (int u = blockIdx.x; u < total && !*abort_flag; u += gridDim.x) {
-            const Unit t = walk.at(u);
-            if (t.steps == 0) continue;  // zeros: no sums to wait for
+        bool ok = true;  // lane 0's; after a wait that ran out nothing is waited for any more
+        while (segments.next(seg)) {
+            if (seg.s1 == 0) continue;  // zeros: no sums to wait for
             const uint32_t n16 = (uint32_t)(t.n + 15) & ~15u;
-            const uint32_t idesc = g.idesc | (n16 >> 3) << 17 | (128u >> 4) << 24;
-            bool ok = warp_wait(&acc_empty[buf], acc_phase ^ 1, abort_flag, g.status);
-            for (int s = 0; s < t.steps && ok; ++s) {
-                ok = warp_wait(&full[slot], phase, abort_flag, g.status);
-                if (!ok) break;
-                if (lane == 0) {
-                    tc::tc_fence_after();
-                    const uint32_t sa = tc::smem_u32(smem + slot * C::STAGE), sb = sa + C::P_BYTES;
-                    const uint64_t da = MODE == FWD ? tc::sdesc_kmajor_sw128(sa) : sdesc_across(sa);
-                    const uint64_t db = tc::sdesc_kmajor_sw128(sb);
-                    constexpr int SA = MODE == FWD ? 2 : 128, SB = 2;  // of 16 values, in 16 bytes
-#pragma unroll
-                    for (int k = 0; k < STEP / 16; ++k)
-                        tc::mma_f16(tm + buf * NT, da + SA * k, db + SB * k, idesc, s > 0 || k > 0);
-                    tc::mma_commit(&empty[slot]);
-                }
+            const uint32_t idesc = g.idesc | (n16 >> 3) << 17 | (128u >> 4) << 24, d = tm + buf * NT;
+            if (lane == 0) ok = ok && lane_wait(&acc_empty[buf], acc_phase ^ 1, abort_flag, g.status);
+#pragma unroll 1
+            for (int s = seg.s0; s < seg.s1; ++s) {
+                if (lane == 0) ok = ok && lane_wait(&full[slot], phase, abort_flag, g.status);
                 __syncwarp();
-                last = slot;
-                last_phase = phase;
+                tc::tc_fence_after();
+                const uint32_t sa = tc::smem_u32(smem) + slot * C::STAGE, sb = sa + C::P_BYTES;
+                const uint64_t da = MODE == FWD ? tc::sdesc_kmajor_sw128(sa) : sdesc_across(sa);
+                const uint64_t db = tc::sdesc_kmajor_sw128(sb);
+                constexpr int SA = MODE == FWD ? 2 : 128, SB = 2;  // of 16 values, in 16 bytes
+#pragma unroll
+                for (int k = 0; k < STEP / 16; ++k)
+                    tc::mma_f16_elect(d, da + SA * k, db + SB * k, idesc, s > seg.s0 || k > 0);
+                tc::mma_commit_elect(&empty[slot]);
                 if (++slot == C::STAGES) { slot = 0; phase ^= 1; }
             }
-            if (!ok) break;
-            if (lane == 0) tc::mma_commit(&acc_full[buf]);
-            __syncwarp();
+            tc::mma_commit_elect(&acc_full[buf]);
             if (++buf == 2) { buf = 0; acc_phase ^= 1; }
         }
-        if (*abort_flag && last >= 0 && lane == 0)  // no product outlives the accumulators
-            tc::mbar_wait(&empty[last], last_phase);
         __syncwarp();
     } else if (warp > WARP_MMA) {
         const int gw = warp - WARP_MMA - 1, turn = gw / GATHER_SHARE, share = gw % GATHER_SHARE;
         int it = 0;
-        for (int u = blockIdx.x; u < total && !*abort_flag; u += gridDim.x) {
-            const Unit t = walk.at(u);
+        while (!*abort_flag && segments.next(seg)) {
             // lane j has the group share + 4 j of the tile
             const int group = share + GATHER_SHARE * lane;
             const bool mine = lane < NT / (4 * GATHER_SHARE) && group * 4 < t.n;
             GatherRows rows;
-            if (t.steps > 0 && mine) {
-                rows.read(g, t.q0, t.n, group);
-                rows.to_rows(g);
+            if (seg.s1 > 0 && mine) {
+                if (g.P <= FEW_SLOTS) {
+                    rows.take(g, slot_rows, t.q0, t.n, group);
+                } else {
+                    rows.read(g, t.q0, t.n, group);
+                    rows.to_rows(g);
+                }
             }
-            for (int s = 0; s < t.steps; ++s, ++it) {
+            for (int s = seg.s0; s < seg.s1; ++s, ++it) {
                 if (it % GATHER_TURNS != turn) continue;
                 const int slot = it % C::STAGES;
                 if (!warp_wait(&empty[slot], (it / C::STAGES & 1) ^ 1, abort_flag, g.status)) break;
@@ -174,41 +222,77 @@ expert_gemm_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_const
         }
     } else {
         const int quad = warp & 3, half = warp >> 2;
+        int4 join = make_int4(0, 0, 0, 0);
         uint8_t* const stage = smem + C::OUT_OFF + warp * STAGE_OUT;
         int buf = 0;
         uint32_t acc_phase = 0;
-        for (int u = blockIdx.x; u < total && !*abort_flag; u += gridDim.x) {
-            const Unit t = walk.at(u);
+        while (!*abort_flag && segments.next(seg)) {
             const int l0 = t.l0 + quad * 32;
-            if (t.steps > 0) {
+            if (SPLIT && seg.part == 1) join = make_int4(t.l0, t.q0, t.n, segments.others(seg));
+            if (seg.s1 > 0) {
                 if (!warp_wait(&acc_full[buf], acc_phase, abort_flag, g.status)) break;
                 tc::tc_fence_after();
             }
             for (int c = half * 32; c < t.n; c += 64) {
                 uint32_t r[32];
-                if (t.steps > 0) {
+                if (seg.s1 > 0) {
                     tmem_ld32(tm + ((uint32_t)(quad * 32) << 16) + buf * NT + c, r);
                     tc::tmem_ld_wait();
                 } else {
 #pragma unroll
                     for (int j = 0; j < 32; ++j) r[j] = 0;
                 }
-                put<MODE>(g, stage, t.e, l0, t.q0 + c, t.n - c, lane, r);
+                if (SPLIT && seg.part >= 0) {
+                    float* to = g.parts + (((int64_t)blockIdx.x * 2 + seg.part) * NT + c) * 128 + quad * 32 + lane;
+#pragma unroll
+                    for (int j = 0; j < 32; ++j)
+                        if (c + j < t.n) to[j * 128] = __uint_as_float(r[j]);
+                } else {
+                    put<MODE>(g, stage, t.e, l0, t.q0 + c, t.n - c, lane, r);
+                }
             }
-            if (t.steps > 0) {
+            if (seg.s1 > 0) {
                 tc::tc_fence_before();
                 __syncwarp();
                 if (lane == 0) tc::mbar_arrive(&acc_empty[buf]);
                 if (++buf == 2) { buf = 0; acc_phase ^= 1; }
             }
         }
+        if (SPLIT && threadIdx.x == 0) g.joins[blockIdx.x] = join;
     }
     __syncwarp();
-    pdl_trigger();
+    if (!SPLIT) pdl_trigger();
     tc::tc_fence_before();
     __syncthreads();
+    wind_down(abort_flag);
     tc::tc_fence_after();
     if (warp == WARP_MMA) tc::tmem_dealloc(tm, C::TMEM_COLS);
+}
+
+// The tiles that Segments left in parts: block j has the one that starts within
+// the share of CTA j and ends behind it.
+template <int NT>
+__global__ void __launch_bounds__(512) join_kernel(const Args g) {
+    pdl_wait();
+    pdl_trigger();
+    const int4 t = g.joins[blockIdx.x];  // first lane, first row, rows, CTAs that go on
+    const int l = threadIdx.x & 127;
+    constexpr int U = 4;
+    for (int c0 = (threadIdx.x >> 7) * U; c0 < t.z; c0 += 4 * U) {
+        float sum[U];
+#pragma unroll
+        for (int j = 0; j < U; ++j) sum[j] = 0.f;
+#pragma unroll 4
+        for (int q = 0; q <= t.w; ++q) {
+            const float* from = g.parts + (((int64_t)(blockIdx.x + q) * 2 + (q == 0)) * NT + c0) * 128 + l;
+#pragma unroll
+            for (int j = 0; j < U; ++j)
+                if (c0 + j < t.z) sum[j] += from[j * 128];
+        }
+#pragma unroll
+        for (int j = 0; j < U; ++j)
+            if (c0 + j < t.z && t.x + l < g.lanes) put_value(g.out, g.ctype, (int64_t)(t.y + c0 + j) * g.ld + t.x + l, sum[j]);
+    }
 }
 
 // Rows of 16-bit values laid out for TMA: rows that start off the 16-byte
@@ -286,17 +370,7 @@ __global__ void __launch_bounds__(256) copy_rows_kernel(const RowCopy c) {
 
 // ------------------------------------------------------------------ host side
 
-// A matrix of 16-bit values, or one for each expert.
-struct Mat {
-    const void* p;
-    int64_t rows, cols, ld, experts, stride;
-};
-
 inline size_t padded(int64_t rows, int64_t cols) { return ((size_t)rows * (size_t)((cols + 7) / 8 * 8) * 2 + 255) / 256 * 256; }
-inline bool fits(const Mat& m) {
-    return aligned16(m.p) && (m.rows == 1 || m.ld % 8 == 0) && (m.experts == 1 || m.stride % 8 == 0);
-}
-
 // Copies m (or its rows in the order of pairs) into the workspace.
 static int copy_rows(Mat& m, const int32_t* pairs, int64_t P, int k, uint8_t*& ws, size_t& left, cudaStream_t st) {
     const int64_t rows = pairs ? P : m.rows * m.experts, ld = (m.cols + 7) / 8 * 8;
@@ -335,14 +409,16 @@ static int map_of(CUtensorMap* map, const Mat& m, int dtype, int box_cols, int b
                : QMOE_ERR_UNSUPPORTED;
 }
 
-template <int MODE, int NT, bool GATHER>
-static int launch(const CUtensorMap& mp, const CUtensorMap& mq, const Args& g, int64_t most, cudaStream_t st) {
+template <int MODE, int NT, bool GATHER, bool SPLIT>
+static int launch_as(const CUtensorMap& mp, const CUtensorMap& mq, const Args& g, int64_t most, cudaStream_t st) {
     using C = Cfg<MODE, NT>;
-    const int rc = row::allow_smem<expert_gemm_kernel<MODE, NT, GATHER>>(C::SMEM);
+    const auto kernel = expert_gemm_kernel<MODE, NT, GATHER, SPLIT>;
+    int rc = row::allow_smem<expert_gemm_kernel<MODE, NT, GATHER, SPLIT>>(C::SMEM);
     if (rc != QMOE_OK) return rc;
-    const int64_t grid = most < row::kSMs ? most : row::kSMs;
-    return launch_pdl(expert_gemm_kernel<MODE, NT, GATHER>, dim3((unsigned)grid), dim3(threads_of(GATHER)), (size_t)C::SMEM, st, mp, mq,
-                      g);
+    const int64_t grid = SPLIT || most > row::kSMs ? row::kSMs : most;
+    rc = launch_pdl(kernel, dim3((unsigned)grid), dim3(threads_of(GATHER)), (size_t)C::SMEM, st, mp, mq, g);
+    if (rc != QMOE_OK || !SPLIT) return rc;
+    return launch_pdl(join_kernel<NT>, dim3((unsigned)grid), dim3(512), 0, st, g);
 }
 
 // Few rows for each expert: narrow tiles, whose stages are almost all weight, so that more of them are in flight.
@@ -355,20 +431,50 @@ inline int tile_of(int64_t P, int E) {
     return P <= 16 * touched ? 32 : P <= 96 * touched ? 128 : 256;
 }
 
+// No more tiles than this, whatever the offsets.
+inline int64_t most_tiles(int64_t P, int E, int64_t lanes, int nt) {
+    const int lt = nt == 256 ? 256 : 128;
+    return ((P < E ? P : E) + 1 + P / nt) * ((lanes + lt - 1) / lt);
+}
+// Whether the SMs share the steps of all tiles evenly, and a second kernel joins the
+// parts, by a model of the time in us fitted to GB300: a step of 64 x 128 weights
+// takes 0.39 where all SMs load (HBM), 0.25 where few do; the join 2.5.  T=1 of 10
+// experts 4096 -> 2048 (160 tiles of 64 steps): 62 us in whole tiles, 51 shared;
+// 8 experts 2048 -> 1536 (96 of 32): 14.5 against 16.8.
+inline bool split(int64_t P, int E, int64_t lanes, int64_t red, int nt) {
+    if (nt == 256) return false;
+    const int64_t tiles = ((P < E ? P : E) + P / nt) * ((lanes + 127) / 128), per = (red + STEP - 1) / STEP;
+    if (tiles > 16 * row::kSMs) return false;
+    const float busy = tiles < row::kSMs ? (float)tiles / row::kSMs : 1.f;
+    const float whole = (float)((tiles + row::kSMs - 1) / row::kSMs) * per * (0.39f * busy > 0.25f ? 0.39f * busy : 0.25f);
+    return (float)tiles * per / row::kSMs * 0.39f + 2.5f < whole;
+}
+inline size_t part_bytes(int nt) { return (size_t)row::kSMs * 2 * nt * 128 * 4 + (row::kSMs * 16 + 255) / 256 * 256; }
+
+// So few rows that the weights pass through once or twice.
+inline bool few(int64_t P, int E, bool fit) { return P <= (fit ? FEW_MOST : 4) * (int64_t)E && P <= 65535; }
+
 template <int MODE, bool GATHER>
-static int run_rows(Mat w, Mat q, Args& g, int dtype, cudaStream_t st) {
-    const int nt = tile_of(g.P, g.E), lt = nt == 256 ? 256 : 128;
+static int run_rows(Mat w, Mat q, Args& g, int dtype, uint8_t* ws, size_t left, cudaStream_t st) {
+    const int nt = tile_of(g.P, g.E);
     CUtensorMap mp, mq;
     int rc = MODE == FWD ? map_of(&mp, w, dtype, STEP, 128, true) : map_of(&mp, w, dtype, 64, STEP, true);
     if (rc != QMOE_OK) return rc;
     rc = map_of(&mq, q, dtype, STEP, GATHER ? 1 : nt == 256 ? 128 : Q_BOX, false);
     if (rc != QMOE_OK) return rc;
-    // no more units than this, whatever the offsets
-    const int64_t parts = (g.P < g.E ? g.P : g.E) + 1 + g.P / nt, most = parts * ((g.lanes + lt - 1) / lt);
+    const int64_t most = most_tiles(g.P, g.E, g.lanes, nt);
     if (most >= (1ll << 31)) return QMOE_ERR_UNSUPPORTED;
+    const bool shares = split(g.P, g.E, g.lanes, g.red, nt);
+    if (shares) {
+        if (left < part_bytes(nt)) return QMOE_ERR_ARG;
+        g.parts = reinterpret_cast<float*>(ws);
+        g.joins = reinterpret_cast<int4*>(ws + (size_t)row::kSMs * 2 * nt * 128 * 4);
+    }
     switch (nt) {
-        case 32: return launch<MODE, 32, GATHER>(mp, mq, g, most, st);
-        case 128: return launch<MODE, 128, GATHER>(mp, mq, g, most, st);
+        case 32:
+            return shares ? launch_as<MODE, 32, GATHER, true>(mp, mq, g, most, st) : launch_as<MODE, 32, GATHER, false>(mp, mq, g, most, st);
+        case 128:
+            return shares ? launch_as<MODE, 128, GATHER, true>(mp, mq, g, most, st) : launch_as<MODE, 128, GATHER, false>(mp, mq, g, most, st);
         default: return GATHER ? QMOE_ERR_UNSUPPORTED : launch_pair<MODE>(mp, mq, g, most, st);
     }
 }
@@ -405,9 +511,12 @@ extern "C" size_t qmoe_expert_copy_bytes(int64_t rows, int64_t cols) {
     return eg::padded(rows, cols);
 }
 
-extern "C" size_t qmoe_expert_gather_bytes(int64_t P, int E, int64_t K, int dw) {
-    if (P <= 0 || E <= 0 || K <= 0 || (!dw && eg::tile_of(P, E) < 256)) return 0;
-    return eg::padded(P, K);
+extern "C" size_t qmoe_expert_workspace_bytes(int64_t P, int E, int64_t N, int64_t K, int op, int pairs) {
+    if (P <= 0 || E <= 0 || N <= 0 || K <= 0 || op < 0 || op > 2 || P > eg::kMost || N > eg::kMost || K > eg::kMost) return 0;
+    if (op == eg::DW) return pairs ? eg::padded(P, K) : 0;
+    const int nt = eg::tile_of(P, E);
+    if (nt == 256) return pairs && op == eg::FWD ? eg::padded(P, K) : 0;
+    return eg::split(P, E, op == eg::FWD ? N : K, op == eg::FWD ? K : N, nt) ? eg::part_bytes(nt) : 0;
 }
 
 extern "C" int qmoe_expert_linear(int64_t P, int E, int64_t N, int64_t K, int dtype, const void* x, int64_t ldx,
@@ -427,16 +536,18 @@ extern "C" int qmoe_expert_linear(int64_t P, int E, int64_t N, int64_t K, int dt
     cudaStream_t st = (cudaStream_t)stream;
     uint8_t* at = static_cast<uint8_t*>(ws);
     size_t left = ws && !(reinterpret_cast<uintptr_t>(ws) & 255u) ? ws_bytes : 0;
-    if ((rc = eg::as_tma(mw, at, left, st)) != QMOE_OK) return rc;
-    const bool lay_out = pairs && qmoe_expert_gather_bytes(P, E, K, 0);
-    rc = lay_out ? eg::copy_rows(mx, pairs, P, k, at, left, st) : eg::as_tma(mx, at, left, st);
-    if (rc != QMOE_OK) return rc;
-    if (lay_out) pairs = nullptr;
     const int size = row::dtype_size(y_dtype);
     eg::Args g = {(int)P, E, (int)N, 0, (int)K, offsets, pairs, k, (int)mx.rows, y, ldy, 0, y_dtype,
                   aligned16(y) && ldy * size % 16 == 0,
-                  dtype == QMOE_BF16 ? tc::idesc_bf16_f32(0, 0) : tc::idesc_f16_f32(0, 0), dev_status};
-    return pairs ? eg::run_rows<eg::FWD, true>(mw, mx, g, dtype, st) : eg::run_rows<eg::FWD, false>(mw, mx, g, dtype, st);
+                  dtype == QMOE_BF16 ? tc::idesc_bf16_f32(0, 0) : tc::idesc_f16_f32(0, 0), dev_status, nullptr, nullptr};
+    if (eg::few(P, E, eg::fits(mw))) return eg::launch_few(mw, mx, g, dtype, st);
+    if ((rc = eg::as_tma(mw, at, left, st)) != QMOE_OK) return rc;
+    const bool lay_out = pairs && eg::tile_of(P, E) == 256;
+    rc = lay_out ? eg::copy_rows(mx, pairs, P, k, at, left, st) : eg::as_tma(mx, at, left, st);
+    if (rc != QMOE_OK) return rc;
+    if (lay_out) g.pairs = nullptr;
+    return g.pairs ? eg::run_rows<eg::FWD, true>(mw, mx, g, dtype, at, left, st)
+                   : eg::run_rows<eg::FWD, false>(mw, mx, g, dtype, at, left, st);
 }
 
 extern "C" int qmoe_expert_linear_dx(int64_t P, int E, int64_t N, int64_t K, int dtype, const void* dy, int64_t lddy,
@@ -459,8 +570,8 @@ extern "C" int qmoe_expert_linear_dx(int64_t P, int E, int64_t N, int64_t K, int
     const int size = row::dtype_size(dx_dtype);
     eg::Args g = {(int)P, E, (int)K, 0, (int)N, offsets, nullptr, 0, (int)P, dx, lddx, 0, dx_dtype,
                   aligned16(dx) && lddx * size % 16 == 0,
-                  (dtype == QMOE_BF16 ? tc::idesc_bf16_f32(0, 0) : tc::idesc_f16_f32(0, 0)) | 1u << 15, dev_status};
-    return eg::run_rows<eg::DX, false>(mw, my, g, dtype, st);
+                  (dtype == QMOE_BF16 ? tc::idesc_bf16_f32(0, 0) : tc::idesc_f16_f32(0, 0)) | 1u << 15, dev_status, nullptr, nullptr};
+    return eg::run_rows<eg::DX, false>(mw, my, g, dtype, at, left, st);
 }
 
 extern "C" int qmoe_expert_linear_dw(int64_t P, int E, int64_t N, int64_t K, int dtype, const void* dy, int64_t lddy,
@@ -489,7 +600,7 @@ extern "C" int qmoe_expert_linear_dw(int64_t P, int E, int64_t N, int64_t K, int
     if (rc != QMOE_OK) return rc;
     eg::Args g = {(int)P, E, (int)N, (int)K, 0, offsets, nullptr, 0, (int)mx.rows, dw, K, N * K, dw_dtype,
                   aligned16(dw) && K * size % 16 == 0,
-                  (dtype == QMOE_BF16 ? tc::idesc_bf16_f32(0, 0) : tc::idesc_f16_f32(0, 0)) | 3u << 15, dev_status};
+                  (dtype == QMOE_BF16 ? tc::idesc_bf16_f32(0, 0) : tc::idesc_f16_f32(0, 0)) | 3u << 15, dev_status, nullptr, nullptr};
     CUtensorMap mp, mq;
     rc = eg::map_of(&mp, my, dtype, 64, eg::STEP, false);
     if (rc != QMOE_OK) return rc;

@@ -2,6 +2,8 @@
 // expert_gemm_pair.cu): arguments, the walk over tiles, stores of sums.
 #pragma once
 
+#include <type_traits>
+
 #include "row_ops.cuh"
 #include "tc_ptx.cuh"
 #include "tma_host.cuh"
@@ -29,6 +31,8 @@ struct Args {
     int wide;              // rows of out start on 16-byte boundaries
     uint32_t idesc;        // without M and N
     int32_t* status;
+    float* parts;          // sums of tiles in parts (few tiles), and where they belong
+    int4* joins;
 };
 
 // Operand whose reduction axis is not the contiguous one: blocks of 64 lanes (or
@@ -56,7 +60,15 @@ struct GatherRows {
 #pragma unroll
         for (int i = 0; i < 4; ++i) at[i] = row_of(g, at[i]);
     }
+    // from the rows of x of all slots
+    __device__ __forceinline__ void take(const Args& g, const int* rows, int q0, int n, int group) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) at[i] = group * 4 + i < n ? rows[q0 + group * 4 + i] : g.x_rows;
+    }
 };
+// So few slots that a CTA reads where all their rows lie while it waits for the
+// offsets, and the first gather waits for no load of its own.
+constexpr int FEW_SLOTS = 128;
 
 __device__ __forceinline__ void tma_gather4(void* dst, const CUtensorMap* map, uint64_t* bar, int x, const GatherRows& r) {
     asm volatile(
@@ -78,6 +90,20 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volati
     ok = __shfl_sync(0xFFFFFFFFu, ok, 0);
     __syncwarp();
     return ok != 0;
+}
+
+// A bounded wait of one lane; false, and the flag set, where it ran out.
+__device__ __forceinline__ bool lane_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag, int32_t* status) {
+    if (tc::mbar_wait(bar, parity)) return true;
+    *abort_flag = 1;
+    atomicOr(status, QMOE_DEV_WAIT_TIMEOUT);
+    return false;
+}
+// After a wait that ran out: time for the loads and products in flight to end (they
+// take microseconds), so that none outlives the CTA.
+__device__ __forceinline__ void wind_down(volatile int* abort_flag) {
+    if (*abort_flag)
+        for (const long long t0 = clock64(); clock64() - t0 < 4000000ll;) __nanosleep(1000);
 }
 
 // 32 columns of this warp's 32 lanes.
@@ -125,7 +151,15 @@ struct Walk {
             t.row0 = off[t.e];
             t.steps = (off[t.e + 1] - t.row0 + STEP - 1) / STEP;
         } else {
-            while (u >= base[e + 1]) ++e;
+            if (u >= base[e + 1]) {  // the last expert that starts at u or before (empty ones start where the next does)
+                int hi = g.E;
+                ++e;
+                while (e < hi) {
+                    const int mid = (e + hi + 1) >> 1;
+                    if (base[mid] <= u) e = mid;
+                    else hi = mid - 1;
+                }
+            }
             t.e = e;
             const int i = u - base[e], q = i / lt;
             const int r0 = off[e], count = (e < g.E ? off[e + 1] : g.P) - r0;
@@ -250,36 +284,31 @@ __device__ __forceinline__ void put(const Args& g, uint8_t* stage, int e, int l0
 
 // The offsets, clamped to [0, P] and raised to the largest before them (no row
 // has two experts, whatever they say), and the units before each expert, by all
-// threads of the CTA; the caller's barrier makes them seen.
+// threads of the CTA; the caller's barrier makes them seen.  Chunks of 32 experts
+// are scanned by a warp each, all at once (one warp after the other took 2 us of
+// the 10 of a decoded token).
 template <int MODE, int LT, int NT>
 __device__ __forceinline__ void read_offsets(const Args& g, int* off, int* base) {
+    constexpr int CHUNKS = (MAX_E + 32) / 32;
+    __shared__ int sums[CHUNKS];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
     bool bad = false;
     for (int i = threadIdx.x; i <= g.E; i += blockDim.x) {
         const int o = g.offsets[i], next = i < g.E ? g.offsets[i + 1] : o;
         bad |= o < 0 || o > g.P || next < o || (i == 0 && o != 0);
         off[i] = min(max(o, 0), g.P);
     }
-    if (bad) atomicOr(g.status, QMOE_DEV_BAD_OFFSETS);
-    __syncthreads();
-    if (threadIdx.x >= 32) return;
-    const int lane = threadIdx.x, lt = (g.lanes + LT - 1) / LT;
-    int most = 0;
-    for (int i0 = 0; i0 <= g.E; i0 += 32) {
-        const int i = i0 + lane;
-        int v = max(i <= g.E ? off[i] : 0, most);
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int w = __shfl_up_sync(0xFFFFFFFFu, v, o);
-            if (lane >= o) v = max(v, w);
+    if (__syncthreads_or(bad)) {
+        if (threadIdx.x == 0) {
+            atomicOr(g.status, QMOE_DEV_BAD_OFFSETS);
+            for (int i = 1; i <= g.E; ++i) off[i] = max(off[i], off[i - 1]);
         }
-        if (i <= g.E) off[i] = v;
-        most = __shfl_sync(0xFFFFFFFFu, v, 31);
+        __syncthreads();
     }
-    __syncwarp();
     if (MODE == DW) return;
-    int sum = 0;
-    for (int i0 = 0; i0 <= g.E; i0 += 32) {
-        const int i = i0 + lane;
+    const int lt = (g.lanes + LT - 1) / LT;
+    for (int c = warp; c * 32 <= g.E; c += warps) {
+        const int i = c * 32 + lane;
         const int count = i < g.E ? off[i + 1] - off[i] : i == g.E ? g.P - off[i] : 0;
         int v = (count + NT - 1) / NT * lt;
 #pragma unroll
@@ -287,11 +316,40 @@ __device__ __forceinline__ void read_offsets(const Args& g, int* off, int* base)
             const int w = __shfl_up_sync(0xFFFFFFFFu, v, o);
             if (lane >= o) v += w;
         }
-        if (i <= g.E) base[i + 1] = sum + v;
-        sum += __shfl_sync(0xFFFFFFFFu, v, 31);
+        if (i <= g.E) base[i + 1] = v;
+        if (lane == 31) sums[c] = v;
     }
-    if (lane == 0) base[0] = 0;
+    if (threadIdx.x == 0) base[0] = 0;
+    if (g.E < 32) return;
+    __syncthreads();
+    for (int c = warp; c * 32 <= g.E; c += warps) {
+        int before = 0;
+        for (int j = lane; j < c; j += 32) before += sums[j];
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) before += __shfl_xor_sync(0xFFFFFFFFu, before, o);
+        const int i = c * 32 + lane;
+        if (i <= g.E) base[i + 1] += before;
+    }
 }
+
+__device__ __forceinline__ void put_value(void* y, int type, int64_t at, float v) {
+    if (type == QMOE_F32) static_cast<float*>(y)[at] = v;
+    else if (type == QMOE_BF16) static_cast<__nv_bfloat16*>(y)[at] = __float2bfloat16_rn(v);
+    else static_cast<__half*>(y)[at] = __float2half_rn(v);
+}
+
+// A matrix of 16-bit values, or one for each expert.
+struct Mat {
+    const void* p;
+    int64_t rows, cols, ld, experts, stride;
+};
+// Whether all its rows start on 16-byte boundaries.
+inline bool fits(const Mat& m) {
+    return aligned16(m.p) && (m.rows == 1 || m.ld % 8 == 0) && (m.experts == 1 || m.stride % 8 == 0);
+}
+
+// y for few rows an expert, of any alignment.
+int launch_few(const Mat& w, const Mat& x, const Args& g, int dtype, cudaStream_t st);
 
 // What the kernels take: map_p of the lane side, map_q of the column side.
 //

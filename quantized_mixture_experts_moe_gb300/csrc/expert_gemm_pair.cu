@@ -66,13 +66,6 @@ __device__ __forceinline__ void pair_load_3d(void* dst, const CUtensorMap* map, 
         "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "r"(z)
         : "memory");
 }
-// A bounded wait of one lane; false, and the flag set, where it ran out.
-__device__ __forceinline__ bool lane_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag, int32_t* status) {
-    if (tc::mbar_wait(bar, parity)) return true;
-    *abort_flag = 1;
-    atomicOr(status, QMOE_DEV_WAIT_TIMEOUT);
-    return false;
-}
 // All lanes of the warp call these with the same operands (which then stay in
 // uniform registers) and one issues.
 __device__ __forceinline__ void mma_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
@@ -283,9 +276,7 @@ expert_pair_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_const
     pdl_trigger();
     tc::tc_fence_before();
     __syncthreads();
-    // after a wait that ran out: time for the loads and products in flight to end (they take microseconds)
-    if (*abort_flag)
-        for (const long long t0 = clock64(); clock64() - t0 < 4000000ll;) __nanosleep(1000);
+    wind_down(abort_flag);
     cluster_sync();  // neither CTA leaves while the other's products read its tiles or arrive at its barriers
     tc::tc_fence_after();
     if (warp == PAIR_MMA)

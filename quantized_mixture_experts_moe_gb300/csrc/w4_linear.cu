@@ -360,7 +360,8 @@ using namespace qmoe;
 
 extern "C" size_t qmoe_w4_workspace_bytes(int64_t T, int64_t N, int64_t K, int dx) {
     if (T <= 0 || N <= 0 || K <= 0 || (!dx && T <= QMOE_W4_FEW)) return 0;
-    return w4::up256((size_t)N * K * 2) + 256 + qmoe_expert_copy_bytes(T, dx ? N : K);
+    return w4::up256((size_t)N * K * 2) + 256 + qmoe_expert_copy_bytes(T, dx ? N : K) +
+           qmoe_expert_workspace_bytes(T, 1, N, K, dx ? 1 : 0, 0);
 }
 
 extern "C" int qmoe_w4_linear(int64_t T, int k, int E, int64_t N, int64_t K, int format, int group, int dtype, const void* x,
