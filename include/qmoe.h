@@ -751,7 +751,7 @@ int qmoe_weighted_sum_backward(int64_t T, int k, int64_t P, int64_t H, int dtype
  * gradient; 0 bytes: NULL), 256-byte aligned, and dev_status as for
  * qmoe_expert_linear. */
 enum { QMOE_W4_INT4 = 0, QMOE_W4_E2M1 = 1 };
-#define QMOE_W4_FEW 32
+#define QMOE_W4_FEW 16
 size_t qmoe_w4_workspace_bytes(int64_t T, int64_t N, int64_t K, int dx);
 int qmoe_w4_linear(int64_t T, int k, int E, int64_t N, int64_t K, int format, int group, int dtype, const void* x,
                    int64_t ldx, const uint8_t* w, const void* s, const int32_t* ids, void* y, int y_dtype, int64_t ldy,

@@ -3,17 +3,30 @@
 //
 //   y[t][n] = sum over groups G of s[n][G] sum_{k in G} v(code[n][k]) x[t][k]
 //
-// Few tokens: the codes' bytes are what the product cannot do without, so they go
-// straight from HBM to the tensor core's registers.  mma.sync m16n8k16 with 16
-// rows of W and 8 tokens: a code becomes the 16-bit float 16 + n by two bit
-// operations for two codes (n in the top mantissa bits of a float between 16 and
-// 32), exactly, and the sum of a group starts from -24 sum x, so that it ends as
-// the sum of (n - 8) x; E2M1 codes are shifted to a float's sign, exponent and top
-// mantissa bit and multiplied by the power of two that is missing.  A group's sum
-// is then scaled in fp32: nothing is rounded before the output but fp32 sums.
-// The order of the reduction inside a group is free, so the codes of a 32-bit
-// word are taken as they come (0 4 1 5 2 6 3 7), and x lies in shared memory in
-// that order.
+// Few tokens: the codes' bytes are what the product cannot do without, and turning
+// them into numbers is what it spends its instructions on.  mma.sync m16n8k16 with
+// 16 rows of W and 8 tokens.  An int4 code becomes the 16-bit float 16 + n by two
+// bit operations for two codes (n in the top mantissa bits of a float between 16
+// and 32), exactly, and the sum of 32 values starts from -24 sum x, so that it ends
+// as the sum of (n - 8) x.  The order of the reduction inside such a sum is free, so
+// the codes of a word are taken as they come (0 4 1 5 2 6 3 7), and x lies in shared
+// memory in that order.  E2M1 codes are converted to fp16, two by an instruction; x
+// is then taken to fp16 too, each 32 values of a token by the power of two that
+// moves the largest into [2^14, 2^15) (exact for values above 2^-28 of it).  Sums of
+// 32 values are scaled in fp32.
+//
+// Up to 4 tokens leave columns of the tensor core's 8 unused.  These then keep GC
+// groups of 32 values apart: a lane takes 32 GC / 4 contiguous codes of its row, all of
+// one group, and column (token, group) has x where the lane's group is its own, and
+// zeros elsewhere.  A scale is then applied once for GC groups, by the lane that has
+// both, and codes come 16 bytes (GC = 4) or 8 at a time.
+//
+// Persistent CTAs, up to three an SM as x leaves room: each takes a run of (expert,
+// rows) tiles and its warps keep their next three blocks of 16 rows x 256 codes on
+// the way, over the ends of tiles too.  One CTA a tile spent 9 us on each, waiting
+// for ids, codes, x and scales in turn.
+#include <type_traits>
+
 #include "row_ops.cuh"
 #include "tc_ptx.cuh"
 #include "tma_host.cuh"
@@ -21,10 +34,11 @@
 namespace qmoe {
 namespace w4 {
 
-constexpr int WARPS = 8, THREADS = WARPS * 32;
-constexpr int ROWS = 16;          // of W, of a CTA
+constexpr int WARPS = 8, THREADS = (WARPS + 1) * 32;  // of products, and one that sends for codes
+constexpr int ROWS = 16;          // of W, of a warp
 constexpr int BLOCK = 256;        // values of a row in a stage (128 bytes)
 constexpr int STAGE = ROWS * 128, DEPTH = 4;
+constexpr int MOST_PAIRS = 256;   // of a CTA's run
 
 struct Args {
     int T, k, E, N, K;
@@ -37,7 +51,11 @@ struct Args {
     void* y;
     int64_t ldy;
     int ytype;
-    int chunk;  // values of x in shared memory at once, a multiple of WARPS * BLOCK or all
+    int chunk;   // values of x in shared memory at once, a multiple of WARPS * BLOCK or all
+    int tiles;   // of a matrix, of ROWS * WARPS / kw rows
+    int units;   // tiles of all pairs
+    int kw_log;  // warps that share a reduction
+    int pairs;   // scales of two neighbouring groups can be read at once
     int32_t* status;
 };
 
@@ -45,54 +63,50 @@ template <typename T> struct Num;
 template <> struct Num<__half> {
     static constexpr uint32_t BASE = 0x4C004C00u;  // 16
     static constexpr int UP = 6;                   // from bit 0 to the top four mantissa bits
-    static constexpr int E2M1 = 9;                 // from bits 0..2 to two exponent bits and a mantissa bit
-    static __device__ __forceinline__ uint32_t rescale(uint32_t v) {  // by 2^14
-        const __half2 r = __hmul2(*reinterpret_cast<const __half2*>(&v), __half2{__ushort_as_half(0x7400), __ushort_as_half(0x7400)});
-        return *reinterpret_cast<const uint32_t*>(&r);
-    }
-    static __device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-        asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-            : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-    }
 };
 template <> struct Num<__nv_bfloat16> {
     static constexpr uint32_t BASE = 0x41804180u;  // 16
     static constexpr int UP = 3;
-    static constexpr int E2M1 = 6;
-    static __device__ __forceinline__ uint32_t rescale(uint32_t v) {  // by 2^126
-        const __nv_bfloat162 r = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&v),
-                                         __nv_bfloat162{__ushort_as_bfloat16(0x7E80), __ushort_as_bfloat16(0x7E80)});
-        return *reinterpret_cast<const uint32_t*>(&r);
-    }
-    static __device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+};
+template <bool BF16>
+__device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    if constexpr (BF16)
         asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
             : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
             : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-    }
-};
+    else
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+            : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
 
-// Codes j and j + 4 of a word, as the two halves of a register: 16 + n, or E2M1
-// values.
+// Codes of a word as numbers in the halves of a register.  int4: codes j and j + 4,
+// as 16 + n.  E2M1: codes 2 j and 2 j + 1.
 template <typename T, int FORMAT, int J>
 __device__ __forceinline__ uint32_t pair_of(uint32_t word) {
-    using M = Num<T>;
     if constexpr (FORMAT == QMOE_W4_INT4) {
+        using M = Num<T>;
         constexpr int by = M::UP - 4 * J;
         const uint32_t v = by >= 0 ? word << (by >= 0 ? by : 0) : word >> (by < 0 ? -by : 0);
         return (v & (0x000F000Fu << M::UP)) | M::BASE;
     } else {
-        constexpr int by = M::E2M1 - 4 * J, sign = 12 - 4 * J;
-        const uint32_t m = by >= 0 ? word << (by >= 0 ? by : 0) : word >> (by < 0 ? -by : 0);
-        const uint32_t s = word << sign;
-        return M::rescale((m & (0x00070007u << M::E2M1)) | (s & 0x80008000u));
+        uint32_t v;
+        asm("{\n\t.reg .b8 b<4>;\n\tmov.b32 {b0, b1, b2, b3}, %1;\n\tcvt.rn.f16x2.e2m1x2 %0, b%2;\n\t}" : "=r"(v) : "r"(word), "n"(J));
+        return v;
     }
 }
 
+// A scale as it lies in memory, and what it stands for.
+template <int FORMAT> struct Scale { typedef uint8_t Raw; };
+template <> struct Scale<QMOE_W4_INT4> { typedef uint16_t Raw; };
+template <int FORMAT>
+__device__ __forceinline__ float scale_of(uint32_t raw) {
+    if constexpr (FORMAT == QMOE_W4_INT4) return __half2float(__ushort_as_half((unsigned short)raw));
+    else return e8m0_to_float((uint8_t)raw);
+}
 template <int FORMAT>
 __device__ __forceinline__ float scale_at(const void* s, int64_t i) {
-    if constexpr (FORMAT == QMOE_W4_INT4) return __half2float(static_cast<const __half*>(s)[i]);
-    else return e8m0_to_float(static_cast<const uint8_t*>(s)[i]);
+    return scale_of<FORMAT>(static_cast<const typename Scale<FORMAT>::Raw*>(s)[i]);
 }
 
 __device__ __forceinline__ void put(void* y, int type, int64_t at, float v) {
@@ -104,167 +118,380 @@ __device__ __forceinline__ void put(void* y, int type, int64_t at, float v) {
 // Bytes of a token's x in shared memory: rows of two neighbouring tokens fall into
 // different halves of the banks.
 __host__ __device__ constexpr int pitch_of(int chunk) { return chunk * 2 + 64; }
+// Shared memory: rings, then x, a number for each 32 values of a token, the sums
+// of the warps (two tiles' for up to 8 tokens), and the experts of the run.
+constexpr int RING = WARPS * DEPTH * STAGE;
+__host__ __device__ constexpr int bufs_of(int nt) { return nt == 1 ? 2 : 1; }
+inline int smem_of(int tokens, int chunk, int nt) {
+    return 1024 + RING + tokens * pitch_of(chunk) + chunk / 32 * 8 * nt * 4 + bufs_of(nt) * WARPS * nt * 8 * ROWS * 4 +
+           MOST_PAIRS * 4;
+}
 
-template <typename T, int FORMAT, int NT>  // NT: tiles of 8 tokens
-__global__ void __launch_bounds__(THREADS) w4_few_kernel(const __grid_constant__ CUtensorMap map, const Args g) {
+// Whether a phase is over, without waiting for it.
+__device__ __forceinline__ bool is_over(uint64_t* bar, uint32_t parity) {
+    uint32_t over;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(over)
+        : "r"(tc::smem_u32(bar)), "r"(parity)
+        : "memory");
+    return over != 0;
+}
+// A barrier of the warps of products.
+__device__ __forceinline__ void products_sync() { asm volatile("bar.sync 1, %0;" ::"n"(WARPS * 32) : "memory"); }
+
+// x of tokens t0 .. in [c0, c0 + len), zeros up to whole blocks; and for each 32
+// values of a token -24 times their sum (int4), or the power of two that they were
+// divided by (E2M1).
+template <typename T, int FORMAT, int NT, int GC>
+__device__ __forceinline__ void stage_x(const Args& g, uint8_t* xs, float* sums, int pitch, int64_t t0, int tokens, int c0, int len) {
+    for (int i = threadIdx.x; i < tokens * (len / 8); i += WARPS * 32) {
+        const int t = i / (len / 8), k = (i - t * (len / 8)) * 8;
+        uint4 v = make_uint4(0, 0, 0, 0);
+        if (c0 + k < g.K) {
+            const T* from = static_cast<const T*>(g.x) + (t0 + t) * g.ldx + c0 + k;
+            if (g.x_wide) {
+                v = *reinterpret_cast<const uint4*>(from);
+            } else {
+                uint32_t u[8];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) u[j] = reinterpret_cast<const uint16_t*>(from)[j];
+                v = make_uint4(u[0] | u[1] << 16, u[2] | u[3] << 16, u[4] | u[5] << 16, u[6] | u[7] << 16);
+            }
+        }
+        const float2 a = row::unpack2(v.x, T{}), b = row::unpack2(v.y, T{}), c = row::unpack2(v.z, T{}), d = row::unpack2(v.w, T{});
+        // len / 8 is a multiple of 32: the lanes of a warp hold one token's neighbouring values
+        float of;
+        if constexpr (FORMAT == QMOE_W4_INT4) {
+            of = ((a.x + a.y) + (b.x + b.y)) + ((c.x + c.y) + (d.x + d.y));
+            of += __shfl_xor_sync(0xFFFFFFFFu, of, 1);
+            of += __shfl_xor_sync(0xFFFFFFFFu, of, 2);
+            of *= -24.f;
+        } else {
+            float m = fmaxf(fmaxf(fmaxf(fabsf(a.x), fabsf(a.y)), fmaxf(fabsf(b.x), fabsf(b.y))),
+                            fmaxf(fmaxf(fabsf(c.x), fabsf(c.y)), fmaxf(fabsf(d.x), fabsf(d.y))));
+            m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
+            m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
+            const int e = f16_row_exponent(m);
+            const float by = exp2i(-e);
+            v = make_uint4(row::pack2(a.x * by, a.y * by, __half{}), row::pack2(b.x * by, b.y * by, __half{}),
+                           row::pack2(c.x * by, c.y * by, __half{}), row::pack2(d.x * by, d.y * by, __half{}));
+            of = exp2i(e);
+        }
+        if ((i & 3) == 0) sums[GC ? t * (g.chunk / 32) + k / 32 : (k / 32) * (8 * NT) + t] = of;
+        if constexpr (FORMAT == QMOE_W4_INT4)  // in the order of the codes
+            v = make_uint4(__byte_perm(v.x, v.z, 0x5410), __byte_perm(v.x, v.z, 0x7632), __byte_perm(v.y, v.w, 0x5410),
+                           __byte_perm(v.y, v.w, 0x7632));
+        *reinterpret_cast<uint4*>(xs + t * pitch + k * 2) = v;
+    }
+    if (GC && threadIdx.x < 4) *reinterpret_cast<uint4*>(xs + g.chunk * 2 + threadIdx.x * 16) = make_uint4(0, 0, 0, 0);
+}
+
+template <typename T, int FORMAT, int NT, int GC>  // NT: tiles of 8 tokens; GC 0: columns are tokens
+__global__ void __launch_bounds__(THREADS, NT == 1 ? 2 : 1) w4_few_kernel(const __grid_constant__ CUtensorMap map, const Args g) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    __shared__ uint64_t bars[WARPS * DEPTH];
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, row = lane >> 2, quad = lane & 3;
-    const int n0 = blockIdx.x * ROWS;
-    uint8_t* const ring = smem + warp * DEPTH * STAGE;
-    uint64_t* const bar = bars + warp * DEPTH;
-    uint8_t* const xs = smem + WARPS * DEPTH * STAGE;
+    __shared__ uint64_t bars[2 * WARPS * DEPTH];  // full and empty stages of each warp's ring
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, quad = lane & 3, col = lane >> 2;
+    // the row of W of a lane: with GC the lanes that read shared memory together have rows 4 apart, whose swizzles differ
+    const int row = GC ? (col >> 1) | (col & 1) << 2 : col;
+    const int kw = 1 << g.kw_log, part = warp & (kw - 1), rows = ROWS * (WARPS >> g.kw_log);
+    const int first_row = (warp >> g.kw_log) * ROWS;  // of this warp in a tile
+    uint8_t* const xs = smem + RING;
     const int tokens = g.ids ? 1 : g.T, pitch = pitch_of(g.chunk);
-    float* const sums = reinterpret_cast<float*>(xs + tokens * pitch);  // [groups of 32 in a chunk][8 NT]
+    float* const sums = reinterpret_cast<float*>(xs + tokens * pitch);  // [groups of 32 in a chunk][8 NT], with GC [token][groups]
+    float* const parts = sums + g.chunk / 32 * 8 * NT;                  // [bufs][WARPS][8 NT][ROWS]
+    int* const experts = reinterpret_cast<int*>(parts + bufs_of(NT) * WARPS * NT * 8 * ROWS);
+    // this CTA's run
+    const int u0 = (int)((int64_t)g.units * blockIdx.x / gridDim.x), u1 = (int)((int64_t)g.units * (blockIdx.x + 1) / gridDim.x);
+    const int p0 = u0 / g.tiles;
+    const int blocks = (g.K + BLOCK - 1) / BLOCK, mine = (blocks - part + kw - 1) >> g.kw_log;  // of a tile, of this warp
 
     pdl_wait();
-    int e = 0;
-    const int64_t t0 = g.ids ? blockIdx.y / g.k : 0;
-    if (g.ids) {
-        e = g.ids[blockIdx.y];
-        if (e < 0 || e >= g.E) {
-            pdl_trigger();
-            if (threadIdx.x < ROWS && n0 + threadIdx.x < g.N) put(g.y, g.ytype, blockIdx.y * g.ldy + n0 + threadIdx.x, 0.f);
-            return;
-        }
-    }
-    const int blocks = (g.K + BLOCK - 1) / BLOCK;
-    if (lane == 0) {
-        for (int i = 0; i < DEPTH; ++i) tc::mbar_init(&bar[i], 1);
+    if (threadIdx.x < 2 * WARPS * DEPTH) {
+        tc::mbar_init(&bars[threadIdx.x], 1);
         tc::fence_barrier_init();
-        for (int i = 0; i < DEPTH; ++i) {
-            const int b = warp + i * WARPS;
-            if (b < blocks) {
-                tc::mbar_arrive_expect_tx(&bar[i], STAGE);
-                tc::tma_load_3d(ring + i * STAGE, &map, &bar[i], b * (BLOCK / 2), n0, e);
-            }
+    }
+    if (g.ids) {
+        const int n = (u1 - 1) / g.tiles - p0 + 1;
+        for (int i = threadIdx.x; i < n; i += THREADS) {
+            const int e = g.ids[p0 + i];
+            experts[i] = e >= 0 && e < g.E ? e : -1;
         }
     }
+    __syncthreads();
     pdl_trigger();
-    const int per_row = g.K >> g.shift;
-    const int64_t s_row = ((int64_t)e * g.N + n0 + row) * per_row;
-    const bool there[2] = {n0 + row < g.N, n0 + row + 8 < g.N};
-    // scales of groups 2 quad and 2 quad + 1 of a block, rows row and row + 8
-    float sc[2][2];
-    auto scales = [&](int b, float (&to)[2][2]) {
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const int k = b * BLOCK + (2 * quad + i) * 32;
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-                to[h][i] = k < g.K && there[h] ? scale_at<FORMAT>(g.s, s_row + (int64_t)h * 8 * per_row + (k >> g.shift)) : 0.f;
+    // a place in the run: unit, pair, tile and the pair's expert (-1: none)
+    struct Place {
+        int u, pair, tile, e;
+    };
+    auto look = [&](Place& p) { p.e = p.u < u1 ? (g.ids ? experts[p.pair - p0] : 0) : -1; };
+    auto step = [&](Place& p) {
+        ++p.u;
+        if (++p.tile == g.tiles) {
+            p.tile = 0;
+            ++p.pair;
+            look(p);
+        } else if (p.u >= u1) {
+            p.e = -1;
         }
     };
-    if (warp < blocks) scales(warp, sc);
+    auto settle = [&](Place& p) {  // at p or the next unit of an expert
+        while (p.e < 0 && p.u < u1) step(p);
+    };
+    Place start = {u0, p0, u0 - p0 * g.tiles, 0};
+    look(start);
+    if (warp == WARPS) {
+        // lane i sends for warp i: block j of its part of unit `at`
+        const int of = lane & (kw - 1), first = (lane >> g.kw_log) * ROWS, n = (blocks - of + kw - 1) >> g.kw_log;
+        Place at = start;
+        settle(at);
+        int j = 0, slot = 0;
+        uint32_t phase = 1;
+        bool more = lane < WARPS && at.e >= 0;
+        long long since = clock64();
+        while (__any_sync(0xFFFFFFFFu, more)) {
+            uint64_t* const full = &bars[(lane * DEPTH + slot) & (WARPS * DEPTH - 1)];
+            const bool free = more && is_over(full + WARPS * DEPTH, phase);
+            if (free) {
+                tc::mbar_arrive_expect_tx(full, STAGE);
+                tc::tma_load_3d(smem + (lane * DEPTH + slot) * STAGE, &map, full, (of + j * kw) * (BLOCK / 2), at.tile * rows + first, at.e);
+                if (++slot == DEPTH) { slot = 0; phase ^= 1; }
+                if (++j == n) {
+                    j = 0;
+                    step(at);
+                    settle(at);
+                    more = at.e >= 0;
+                }
+            }
+            if (__any_sync(0xFFFFFFFFu, free)) {
+                since = clock64();
+                continue;
+            }
+            __nanosleep(64);  // a stage lasts a warp some 1500
+            if (clock64() - since > 4000000000ll) {
+                if (lane == 0) atomicOr(g.status, QMOE_DEV_WAIT_TIMEOUT);
+                break;
+            }
+        }
+        return;
+    }
 
-    float acc[NT][4];
+    // Scales, a block ahead: rows row and row + 8; with GC the groups of this lane's columns 2 quad and 2 quad + 1 in each
+    // span of GC groups, else groups 2 quad and 2 quad + 1 of the block, which the lanes of a quad share.  Behind the
+    // last row and the last group the last ones are read: those rows are not stored, and x is zero there.
+    typedef typename Scale<FORMAT>::Raw Raw;
+    typedef typename std::conditional<sizeof(Raw) == 2, uint32_t, uint16_t>::type Two;
+    constexpr int SPANS = GC ? 8 / GC : 1, RAW_BITS = 8 * sizeof(Raw);
+    const int per_row = g.K >> g.shift, g0 = GC == 4 ? 2 * (quad & 1) : GC == 2 ? 0 : 2 * quad;
+    Place later = start;
+    settle(later);
+    const Raw* at_row[2] = {};
+    int later_j = 0;
+    uint32_t raw[SPANS][2];
+    auto find_rows = [&]() {
+        const int n = later.tile * rows + first_row + row;
+        const Raw* const of = static_cast<const Raw*>(g.s) + (int64_t)later.e * g.N * per_row;
+        at_row[0] = of + (int64_t)min(n, g.N - 1) * per_row;
+        at_row[1] = of + (int64_t)min(n + 8, g.N - 1) * per_row;
+    };
+    auto fetch = [&]() {
+        if (later.e < 0) return;
+        const int b = part + later_j * kw;
+        if (g.pairs && (b + 1) * BLOCK <= g.K) {  // both in one word
 #pragma unroll
-    for (int i = 0; i < NT; ++i)
+            for (int h = 0; h < 2; ++h) {
+                const Two* const from = reinterpret_cast<const Two*>(at_row[h] + b * 8 + g0);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) acc[i][j] = 0.f;
+                for (int s = 0; s < SPANS; ++s) raw[s][h] = from[s * GC / 2];
+            }
+        } else {
+#pragma unroll
+            for (int s = 0; s < SPANS; ++s) {
+                const int k0 = b * BLOCK + (s * GC + g0) * 32;
+                const int i0 = min(k0, g.K - 32) >> g.shift, i1 = min(k0 + 32, g.K - 32) >> g.shift;
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const uint32_t one = at_row[h][i0];
+                    raw[s][h] = one | (i1 == i0 ? one : (uint32_t)at_row[h][i1]) << RAW_BITS;
+                }
+            }
+        }
+        if (++later_j == mine) {
+            later_j = 0;
+            step(later);
+            settle(later);
+            if (later.e >= 0) find_rows();
+        }
+    };
+    if (later.e >= 0) find_rows();
+    fetch();
+
     bool ok = true;
-    int it = 0;
-    for (int c0 = 0; c0 < g.K; c0 += g.chunk) {
-        // x of this chunk, zeros up to whole blocks, and the sum of each 32 values
-        const int len = min(g.chunk, (g.K - c0 + BLOCK - 1) / BLOCK * BLOCK);
-        if (c0) __syncthreads();
-        for (int i = threadIdx.x; i < tokens * (len / 8); i += THREADS) {
-            const int t = i / (len / 8), k = (i - t * (len / 8)) * 8;
-            uint4 v = make_uint4(0, 0, 0, 0);
-            if (c0 + k < g.K) {
-                const T* from = static_cast<const T*>(g.x) + (t0 + t) * g.ldx + c0 + k;
-                if (g.x_wide) {
-                    v = *reinterpret_cast<const uint4*>(from);
-                } else {
-                    uint32_t u[8];
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) u[j] = reinterpret_cast<const uint16_t*>(from)[j];
-                    v = make_uint4(u[0] | u[1] << 16, u[2] | u[3] << 16, u[4] | u[5] << 16, u[6] | u[7] << 16);
-                }
-            }
-            const float2 a = row::unpack2(v.x, T{}), b = row::unpack2(v.y, T{}), c = row::unpack2(v.z, T{}), d = row::unpack2(v.w, T{});
-            float sum = ((a.x + a.y) + (b.x + b.y)) + ((c.x + c.y) + (d.x + d.y));
-            // len / 8 is a multiple of 32: the lanes of a warp hold one token's neighbouring values
-            sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 1);
-            sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 2);
-            if (FORMAT == QMOE_W4_INT4 && (i & 3) == 0) sums[(k / 32) * (8 * NT) + t] = -24.f * sum;
-            *reinterpret_cast<uint4*>(xs + t * pitch + k * 2) =
-                make_uint4(__byte_perm(v.x, v.z, 0x5410), __byte_perm(v.x, v.z, 0x7632), __byte_perm(v.y, v.w, 0x5410),
-                           __byte_perm(v.y, v.w, 0x7632));
+    int slot = 0, buf = 0, staged_c = -1;
+    uint32_t phase = 0;
+    int64_t staged_t = -1;
+    for (Place at = start; at.u < u1; step(at)) {
+        const int pair = at.pair, n0 = at.tile * rows;
+        if (at.e < 0) {
+            for (int i = threadIdx.x; i < rows; i += WARPS * 32)
+                if (n0 + i < g.N) put(g.y, g.ytype, pair * g.ldy + n0 + i, 0.f);
+            continue;
         }
-        __syncthreads();
-        for (int b = c0 / BLOCK + warp; b < (c0 + len) / BLOCK && ok; b += WARPS, ++it) {
-            const int slot = it % DEPTH;
-            float next[2][2] = {};
-            if (b + WARPS < blocks) scales(b + WARPS, next);
-            ok = __all_sync(0xFFFFFFFFu, tc::mbar_wait(&bar[slot], it / DEPTH & 1));
-            const uint8_t* st = ring + slot * STAGE + row * 128 + quad * 4;
-            const uint8_t* xb = xs + (b * BLOCK - c0) * 2 + quad * 16;
+        const int64_t t0 = g.ids ? pair / g.k : 0;
+        float acc[NT][4];
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const uint32_t at = (j ^ (row & 7)) * 16;
-                const uint32_t lo = *reinterpret_cast<const uint32_t*>(st + at);
-                const uint32_t hi = *reinterpret_cast<const uint32_t*>(st + 1024 + at);
-                const uint32_t a0[4] = {pair_of<T, FORMAT, 0>(lo), pair_of<T, FORMAT, 0>(hi), pair_of<T, FORMAT, 1>(lo),
-                                        pair_of<T, FORMAT, 1>(hi)};
-                const uint32_t a1[4] = {pair_of<T, FORMAT, 2>(lo), pair_of<T, FORMAT, 2>(hi), pair_of<T, FORMAT, 3>(lo),
-                                        pair_of<T, FORMAT, 3>(hi)};
-                const float f0 = __shfl_sync(0xFFFFFFFFu, sc[0][j & 1], (lane & 28) | (j >> 1));
-                const float f1 = __shfl_sync(0xFFFFFFFFu, sc[1][j & 1], (lane & 28) | (j >> 1));
+        for (int i = 0; i < NT; ++i)
 #pragma unroll
-                for (int i = 0; i < NT; ++i) {
-                    const int t = min(i * 8 + row, tokens - 1);
-                    const uint4 v = *reinterpret_cast<const uint4*>(xb + t * pitch + j * 64);
-                    float d[4] = {0.f, 0.f, 0.f, 0.f};
-                    if constexpr (FORMAT == QMOE_W4_INT4) {
-                        const float2 z = *reinterpret_cast<const float2*>(sums + ((b * BLOCK - c0) / 32 + j) * (8 * NT) + i * 8 + quad * 2);
-                        d[0] = d[2] = z.x;
-                        d[1] = d[3] = z.y;
+            for (int j = 0; j < 4; ++j) acc[i][j] = 0.f;
+        int j0 = 0;
+        for (int c0 = 0; c0 < g.K; c0 += g.chunk) {
+            const int len = min(g.chunk, (g.K - c0 + BLOCK - 1) / BLOCK * BLOCK);
+            if (staged_c != c0 || staged_t != t0) {
+                if (staged_c >= 0) products_sync();
+                stage_x<T, FORMAT, NT, GC>(g, xs, sums, pitch, t0, tokens, c0, len);
+                staged_c = c0;
+                staged_t = t0;
+                products_sync();
+            }
+            for (; j0 < mine && (part + j0 * kw) * BLOCK < c0 + len; ++j0) {
+                const int b = part + j0 * kw;
+                float sc[SPANS][2][2];
+#pragma unroll
+                for (int s = 0; s < SPANS; ++s)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h)
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) sc[s][h][i] = scale_of<FORMAT>(raw[s][h] >> i * RAW_BITS & (Raw)~Raw(0));
+                fetch();
+                if (ok) ok = __all_sync(0xFFFFFFFFu, tc::mbar_wait(&bars[warp * DEPTH + slot], phase));
+                constexpr bool INT4 = FORMAT == QMOE_W4_INT4, BF16 = INT4 && std::is_same<T, __nv_bfloat16>::value;
+                if constexpr (GC > 0) {
+                    const uint8_t* st = smem + (warp * DEPTH + slot) * STAGE + row * 128;
+                    // this lane's column's x, or zeros; its columns' numbers
+                    const bool own_x = col % GC == quad * GC / 4 && col / GC < tokens;
+                    const uint8_t* xp = own_x ? xs + col / GC * pitch + (b * BLOCK - c0) * 2 + quad * GC * 16 : xs + g.chunk * 2;
+                    const int x_step = own_x ? GC * 64 : 0;
+                    const int t = min(GC == 4 ? quad >> 1 : quad, tokens - 1);
+                    const float* zp = sums + t * (g.chunk / 32) + (b * BLOCK - c0) / 32 + g0;
+#pragma unroll
+                    for (int s = 0; s < SPANS; ++s) {
+                        uint32_t lo[GC], hi[GC];
+                        if constexpr (GC == 4) {
+                            const uint32_t at = ((s * 4 + quad) ^ (row & 7)) * 16;
+                            *reinterpret_cast<uint4*>(lo) = *reinterpret_cast<const uint4*>(st + at);
+                            *reinterpret_cast<uint4*>(hi) = *reinterpret_cast<const uint4*>(st + 1024 + at);
+                        } else {
+                            const uint32_t at = ((s * 2 + (quad >> 1)) ^ (row & 7)) * 16 + (quad & 1) * 8;
+                            *reinterpret_cast<uint2*>(lo) = *reinterpret_cast<const uint2*>(st + at);
+                            *reinterpret_cast<uint2*>(hi) = *reinterpret_cast<const uint2*>(st + 1024 + at);
+                        }
+                        const float2 z = *reinterpret_cast<const float2*>(zp + s * GC);
+                        float d[4] = {INT4 ? z.x : 0.f, INT4 ? z.y : 0.f, INT4 ? z.x : 0.f, INT4 ? z.y : 0.f};
+#pragma unroll
+                        for (int i = 0; i < GC; ++i) {
+                            const uint4 v = *reinterpret_cast<const uint4*>(xp + i * 16);
+                            const uint32_t a0[4] = {pair_of<T, FORMAT, 0>(lo[i]), pair_of<T, FORMAT, 0>(hi[i]),
+                                                    pair_of<T, FORMAT, 1>(lo[i]), pair_of<T, FORMAT, 1>(hi[i])};
+                            const uint32_t a1[4] = {pair_of<T, FORMAT, 2>(lo[i]), pair_of<T, FORMAT, 2>(hi[i]),
+                                                    pair_of<T, FORMAT, 3>(lo[i]), pair_of<T, FORMAT, 3>(hi[i])};
+                            mma<BF16>(d, a0, v.x, v.y);
+                            mma<BF16>(d, a1, v.z, v.w);
+                        }
+                        xp += x_step;
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            acc[0][2 * h] = fmaf(sc[s][h][0], INT4 ? d[2 * h] : d[2 * h] * z.x, acc[0][2 * h]);
+                            acc[0][2 * h + 1] = fmaf(sc[s][h][1], INT4 ? d[2 * h + 1] : d[2 * h + 1] * z.y, acc[0][2 * h + 1]);
+                        }
                     }
-                    Num<T>::mma(d, a0, v.x, v.y);
-                    Num<T>::mma(d, a1, v.z, v.w);
-                    acc[i][0] = fmaf(f0, d[0], acc[i][0]);
-                    acc[i][1] = fmaf(f0, d[1], acc[i][1]);
-                    acc[i][2] = fmaf(f1, d[2], acc[i][2]);
-                    acc[i][3] = fmaf(f1, d[3], acc[i][3]);
+                } else {
+                    const uint8_t* st = smem + (warp * DEPTH + slot) * STAGE + row * 128 + quad * 4;
+                    const uint8_t* xb = xs + (b * BLOCK - c0) * 2 + quad * 16;
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        const uint32_t at = (j ^ (row & 7)) * 16;
+                        const uint32_t lo = *reinterpret_cast<const uint32_t*>(st + at);
+                        const uint32_t hi = *reinterpret_cast<const uint32_t*>(st + 1024 + at);
+                        const uint32_t a0[4] = {pair_of<T, FORMAT, 0>(lo), pair_of<T, FORMAT, 0>(hi), pair_of<T, FORMAT, 1>(lo),
+                                                pair_of<T, FORMAT, 1>(hi)};
+                        const uint32_t a1[4] = {pair_of<T, FORMAT, 2>(lo), pair_of<T, FORMAT, 2>(hi), pair_of<T, FORMAT, 3>(lo),
+                                                pair_of<T, FORMAT, 3>(hi)};
+                        const float f0 = __shfl_sync(0xFFFFFFFFu, sc[0][0][j & 1], (lane & 28) | (j >> 1));
+                        const float f1 = __shfl_sync(0xFFFFFFFFu, sc[0][1][j & 1], (lane & 28) | (j >> 1));
+#pragma unroll
+                        for (int i = 0; i < NT; ++i) {
+                            const int t = min(i * 8 + col, tokens - 1);
+                            const uint4 v = *reinterpret_cast<const uint4*>(xb + t * pitch + j * 64);
+                            const float2 z = *reinterpret_cast<const float2*>(sums + ((b * BLOCK - c0) / 32 + j) * (8 * NT) + i * 8 + quad * 2);
+                            float d[4] = {INT4 ? z.x : 0.f, INT4 ? z.y : 0.f, INT4 ? z.x : 0.f, INT4 ? z.y : 0.f};
+                            mma<BF16>(d, a0, v.x, v.y);
+                            mma<BF16>(d, a1, v.z, v.w);
+                            if constexpr (!INT4) {
+                                d[0] *= z.x;
+                                d[1] *= z.y;
+                                d[2] *= z.x;
+                                d[3] *= z.y;
+                            }
+                            acc[i][0] = fmaf(f0, d[0], acc[i][0]);
+                            acc[i][1] = fmaf(f0, d[1], acc[i][1]);
+                            acc[i][2] = fmaf(f1, d[2], acc[i][2]);
+                            acc[i][3] = fmaf(f1, d[3], acc[i][3]);
+                        }
+                    }
                 }
-            }
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-#pragma unroll
-                for (int i = 0; i < 2; ++i) sc[h][i] = next[h][i];
-            __syncwarp();
-            if (lane == 0 && b + DEPTH * WARPS < blocks) {
-                tc::mbar_arrive_expect_tx(&bar[slot], STAGE);
-                tc::tma_load_3d(ring + slot * STAGE, &map, &bar[slot], (b + DEPTH * WARPS) * (BLOCK / 2), n0, e);
+                __syncwarp();
+                if (lane == 0) tc::mbar_arrive(&bars[WARPS * DEPTH + warp * DEPTH + slot]);
+                if (++slot == DEPTH) { slot = 0; phase ^= 1; }
             }
         }
+        if constexpr (GC > 0) {  // a token's groups, into acc[0][0] and acc[0][2]
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                float v = acc[0][2 * h] + acc[0][2 * h + 1];
+                if (GC == 4) v += __shfl_xor_sync(0xFFFFFFFFu, v, 1);
+                acc[0][2 * h] = v;
+            }
+        }
+        // this lane's sums: token, row of the warp, value
+        auto each = [&](auto f) {
+            if constexpr (GC > 0) {
+                if (GC == 2 || (quad & 1) == 0) {
+                    f(GC == 4 ? quad >> 1 : quad, row, acc[0][0]);
+                    f(GC == 4 ? quad >> 1 : quad, row + 8, acc[0][2]);
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < NT; ++i)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) f(i * 8 + quad * 2 + (j & 1), row + (j >> 1) * 8, acc[i][j]);
+            }
+        };
+        if (kw == 1) {  // all of them
+            each([&](int t, int r, float v) {
+                const int n = n0 + first_row + r;
+                if (t < tokens && n < g.N) put(g.y, g.ytype, (g.ids ? (int64_t)pair : t) * g.ldy + n, v);
+            });
+            continue;
+        }
+        // the warps' sums, added in order
+        float* const to = parts + (buf * WARPS + warp) * NT * 8 * ROWS;
+        each([&](int t, int r, float v) { to[t * ROWS + r] = v; });
+        products_sync();
+        for (int i = threadIdx.x; i < tokens * rows; i += WARPS * 32) {
+            const int row_log = 7 - g.kw_log, t = i >> row_log, n = i & (rows - 1);
+            const float* from = parts + (buf * WARPS + (n / ROWS) * kw) * NT * 8 * ROWS + t * ROWS + n % ROWS;
+            float v = 0.f;
+            for (int w = 0; w < kw; ++w) v += from[w * NT * 8 * ROWS];
+            if (n0 + n < g.N) put(g.y, g.ytype, (g.ids ? (int64_t)pair : t) * g.ldy + n0 + n, v);
+        }
+        if (bufs_of(NT) == 2) buf ^= 1;
+        else products_sync();
     }
     if (!ok && lane == 0) {
         atomicOr(g.status, QMOE_DEV_WAIT_TIMEOUT);
-        // the blocks asked for and not waited for: no load outlives the CTA
-        for (int i = it - 1; i < it - 1 + DEPTH; ++i)
-            if (warp + i * WARPS < blocks) tc::mbar_wait(&bar[i % DEPTH], i / DEPTH & 1);
-    }
-    // the warps' sums, added in order
-    __syncthreads();
-    float* const part = reinterpret_cast<float*>(xs);
-#pragma unroll
-    for (int i = 0; i < NT; ++i) {
-        float* to = part + ((warp * NT + i) * 8 + quad * 2) * ROWS + row;
-        to[0] = acc[i][0];
-        to[ROWS] = acc[i][1];
-        to[8] = acc[i][2];
-        to[ROWS + 8] = acc[i][3];
-    }
-    __syncthreads();
-    for (int i = threadIdx.x; i < tokens * ROWS; i += THREADS) {
-        float v = 0.f;
-#pragma unroll
-        for (int w = 0; w < WARPS; ++w) v += part[w * NT * 8 * ROWS + i];
-        const int t = i / ROWS, n = n0 + i % ROWS;
-        if (n < g.N) put(g.y, g.ytype, (g.ids ? (int64_t)blockIdx.y : t) * g.ldy + n, v);
+        // time for the loads in flight to end (they take microseconds): none outlives the CTA
+        for (const long long c = clock64(); clock64() - c < 4000000ll;) __nanosleep(1000);
     }
 }
 
@@ -294,25 +521,43 @@ __global__ void __launch_bounds__(256) w4_widen_kernel(int64_t words, int per_ro
 
 // ------------------------------------------------------------------ host side
 
-template <typename T, int FORMAT, int NT>
+constexpr int kMostSmem = 220 * 1024;
+
+template <typename T, int FORMAT, int NT, int GC>
 static int few(const CUtensorMap& map, Args& g, int64_t pairs, cudaStream_t st) {
-    const int tokens = g.ids ? 1 : g.T, all = (g.K + BLOCK - 1) / BLOCK * BLOCK;
-    const int most = NT == 1 ? 4096 : 2048;
-    g.chunk = all < most ? all : most;
-    const int x = tokens * pitch_of(g.chunk) + g.chunk / 32 * 8 * NT * 4, part = WARPS * NT * 8 * ROWS * 4;
-    const int smem = 1024 + WARPS * DEPTH * STAGE + (x > part ? x : part);
-    constexpr int kMostSmem = 220 * 1024;
-    const int rc = row::allow_smem<w4_few_kernel<T, FORMAT, NT>>(kMostSmem);
+    const int tokens = g.ids ? 1 : g.T, blocks = (g.K + BLOCK - 1) / BLOCK;
+    g.chunk = blocks * BLOCK;
+    constexpr int LEAST = WARPS * BLOCK;
+    static_assert(1024 + RING + 8 * NT * pitch_of(LEAST) + LEAST / 32 * 8 * NT * 4 + bufs_of(NT) * WARPS * NT * 8 * ROWS * 4 +
+                          MOST_PAIRS * 4 <= kMostSmem, "the least chunk fits");
+    while (smem_of(tokens, g.chunk, NT) > kMostSmem) g.chunk = (g.chunk / 2 + LEAST - 1) / LEAST * LEAST;
+    const int smem = smem_of(tokens, g.chunk, NT);
+    const int fit = 227 * 1024 / (smem + 1024);  // 1 KB a CTA is the system's
+    const int64_t most = (fit > 2 ? 2 : fit) * row::kSMs;
+    // As few warps share a reduction as keep the CTAs evenly busy: a tile's end costs a warp as much as a block.
+    const int most_log = blocks >= 8 ? 3 : blocks >= 4 ? 2 : blocks >= 2 ? 1 : 0;
+    int64_t units = 0;
+    for (g.kw_log = 0;; ++g.kw_log) {
+        const int rows = ROWS * (WARPS >> g.kw_log);
+        g.tiles = (g.N + rows - 1) / rows;
+        units = g.tiles * pairs;
+        const int64_t rounds = (units + most - 1) / most;
+        if (g.kw_log == most_log || units * 8 >= rounds * most * 7) break;
+    }
+    if (units >= (1ll << 31)) return QMOE_ERR_UNSUPPORTED;
+    g.units = (int)units;
+    const int rc = row::allow_smem<w4_few_kernel<T, FORMAT, NT, GC>>(kMostSmem);
     if (rc != QMOE_OK) return rc;
-    return launch_pdl(w4_few_kernel<T, FORMAT, NT>, dim3((unsigned)((g.N + ROWS - 1) / ROWS), (unsigned)pairs), dim3(THREADS),
-                      (size_t)smem, st, map, g);
+    return launch_pdl(w4_few_kernel<T, FORMAT, NT, GC>, dim3((unsigned)(units < most ? units : most)), dim3(THREADS), (size_t)smem, st,
+                      map, g);
 }
 template <typename T, int FORMAT>
 static int few_tokens(const CUtensorMap& map, Args& g, int64_t pairs, cudaStream_t st) {
     const int tokens = g.ids ? 1 : g.T;
-    if (tokens <= 8) return few<T, FORMAT, 1>(map, g, pairs, st);
-    if (tokens <= 16) return few<T, FORMAT, 2>(map, g, pairs, st);
-    return few<T, FORMAT, 4>(map, g, pairs, st);
+    if (tokens <= 2) return few<T, FORMAT, 1, 4>(map, g, pairs, st);
+    if (tokens <= 4) return few<T, FORMAT, 1, 2>(map, g, pairs, st);
+    if (tokens <= 8) return few<T, FORMAT, 1, 0>(map, g, pairs, st);
+    return few<T, FORMAT, 2, 0>(map, g, pairs, st);
 }
 
 inline bool format_ok(int format, int group) {
@@ -395,7 +640,8 @@ extern "C" int qmoe_w4_linear(int64_t T, int k, int E, int64_t N, int64_t K, int
             CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
         return QMOE_ERR_UNSUPPORTED;
     w4::Args g = {(int)T, k, E, (int)N, (int)K, w4::log2_of(group), x, ldx, aligned16(x) && (ldx % 8 == 0 || T == 1), s, ids, y, ldy,
-                  y_dtype, 0, dev_status};
+                  y_dtype, 0, 0, 0, 0,
+                  group == 32 && K % 64 == 0 && row::type_aligned(s, format == QMOE_W4_INT4 ? 4 : 2), dev_status};
     const int64_t pairs = ids ? T * k : 1;
     if (dtype == QMOE_BF16)
         return format == QMOE_W4_INT4 ? w4::few_tokens<__nv_bfloat16, QMOE_W4_INT4>(map, g, pairs, st)
