@@ -51,12 +51,12 @@ struct Segment {
 };
 template <int MODE, int NT, bool SPLIT>
 struct Segments {
-    Walk<MODE, 128, NT, 16> walk;
+    Walk<128, 16> walk;
     int64_t at, end;  // steps (SPLIT)
     int64_t each;     // of a share; the first `more` shares have one step more
     int more;
     int u, total, per;
-    __device__ Segments(const Args& g, const int* off, const int* base) : walk(g, off, base) {
+    __device__ Segments(const Args& g, const int* off, const int* base) : walk(g, off, base, NT) {
         total = base[g.E + 1];
         per = (g.red + STEP - 1) / STEP;
         u = (SPLIT ? base[g.E] : 0) + blockIdx.x;
@@ -131,7 +131,7 @@ expert_gemm_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_const
     pdl_wait();
     __shared__ int slot_rows[GATHER ? FEW_SLOTS : 1];
     if (GATHER && g.P <= FEW_SLOTS && threadIdx.x < g.P) slot_rows[threadIdx.x] = row_of(g, g.pairs[threadIdx.x]);
-    read_offsets<MODE, 128, NT>(g, off, base);
+    read_offsets<128, NT, false>(g, off, base);
     tc::tc_fence_before();
     __syncthreads();
     tc::tc_fence_after();
@@ -444,7 +444,7 @@ inline int64_t most_tiles(int64_t P, int E, int64_t lanes, int nt) {
 inline bool split(int64_t P, int E, int64_t lanes, int64_t red, int nt) {
     if (nt == 256) return false;
     const int64_t tiles = ((P < E ? P : E) + P / nt) * ((lanes + 127) / 128), per = (red + STEP - 1) / STEP;
-    if (tiles > 16 * row::kSMs) return false;
+    if (tiles > 2 * row::kSMs) return false;  // measured no faster, up to a fifth slower, with more
     const float busy = tiles < row::kSMs ? (float)tiles / row::kSMs : 1.f;
     const float whole = (float)((tiles + row::kSMs - 1) / row::kSMs) * per * (0.39f * busy > 0.25f ? 0.39f * busy : 0.25f);
     return (float)tiles * per / row::kSMs * 0.39f + 2.5f < whole;

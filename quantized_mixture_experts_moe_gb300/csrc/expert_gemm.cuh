@@ -16,7 +16,7 @@ enum { FWD = 0, DX = 1, DW = 2 };
 constexpr int EPI_WARPS = 8;     // read sums and store them: two for each quadrant of lanes
 constexpr int STEP = 64;         // reduction values of a stage: 128 bytes
 constexpr int MAX_E = 1024;
-constexpr int STAGE_OUT = 2048;  // bytes of a warp's output stage: 32 rows of 64
+constexpr int STAGE_OUT = 2048, STAGE_DW = 4096;  // bytes of a warp's output stage: 32 rows of 64, or 128
 constexpr int Q_BOX = 32;        // rows of a box of the column side (y, dx)
 
 struct Args {
@@ -121,58 +121,96 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
 // A tile: its expert, first lane, first column (a row s, or a column of dw), the
 // columns it has and its reduction steps.
 struct Unit {
-    int e, l0, q0, n, steps, row0;
+    int e, l0, q0, n, steps;
+    int row0, end;  // dw: the expert's rows
 };
 
 // The units, in order.  For y and dx an expert has ceil(lanes / LT) tiles for
-// each of its ceil(count / NT) parts of about the same number of rows (a multiple
+// each of its ceil(count / cap) parts of about the same number of rows (a multiple
 // of ROUND); after the experts come the rows of none, whose outputs are zeros.
-template <int MODE, int LT, int NT, int ROUND>
+template <int LT, int ROUND>
 struct Walk {
     const Args& g;
     const int* off;   // [E + 1], clamped to [0, P]
-    const int* base;  // [E + 2]: units before expert e (y, dx)
+    const int* base;  // [E + 2]: units before expert e
+    int cap;          // most columns of a tile
     int e = 0;
-    __device__ Walk(const Args& g_, const int* off_, const int* base_) : g(g_), off(off_), base(base_) {}
-    __device__ int total() const {
-        if (MODE == DW) return g.E * ((g.lanes + LT - 1) / LT) * ((g.cols + NT - 1) / NT);
-        return base[g.E + 1];
-    }
+    __device__ Walk(const Args& g_, const int* off_, const int* base_, int cap_) : g(g_), off(off_), base(base_), cap(cap_) {}
+    __device__ int total() const { return base[g.E + 1]; }
     __device__ Unit at(int u) {
         const int lt = (g.lanes + LT - 1) / LT;
         Unit t;
-        if (MODE == DW) {
-            const int qt = (g.cols + NT - 1) / NT;
-            t.e = u / (lt * qt);
-            const int i = u - t.e * lt * qt;
-            t.l0 = (i % lt) * LT;
-            t.q0 = (i / lt) * NT;
-            t.n = min(NT, g.cols - t.q0);
-            t.row0 = off[t.e];
-            t.steps = (off[t.e + 1] - t.row0 + STEP - 1) / STEP;
-        } else {
-            if (u >= base[e + 1]) {  // the last expert that starts at u or before (empty ones start where the next does)
-                int hi = g.E;
-                ++e;
-                while (e < hi) {
-                    const int mid = (e + hi + 1) >> 1;
-                    if (base[mid] <= u) e = mid;
-                    else hi = mid - 1;
-                }
+        if (u >= base[e + 1]) {  // the last expert that starts at u or before (empty ones start where the next does)
+            int hi = g.E;
+            ++e;
+            while (e < hi) {
+                const int mid = (e + hi + 1) >> 1;
+                if (base[mid] <= u) e = mid;
+                else hi = mid - 1;
             }
-            t.e = e;
-            const int i = u - base[e], q = i / lt;
-            const int r0 = off[e], count = (e < g.E ? off[e + 1] : g.P) - r0;
-            const int qt = (count + NT - 1) / NT, per = ((count + qt - 1) / qt + ROUND - 1) & ~(ROUND - 1);
-            t.l0 = (i - q * lt) * LT;
-            t.q0 = r0 + q * per;
-            t.n = min(per, r0 + count - t.q0);
-            t.row0 = 0;
-            t.steps = e < g.E ? (g.red + STEP - 1) / STEP : 0;
+        }
+        t.e = e;
+        const int i = u - base[e], q = i / lt;
+        const int r0 = off[e], count = (e < g.E ? off[e + 1] : g.P) - r0;
+        const int qt = (count + cap - 1) / cap, per = ((count + qt - 1) / qt + ROUND - 1) & ~(ROUND - 1);
+        t.l0 = (i - q * lt) * LT;
+        t.q0 = r0 + q * per;
+        t.n = min(per, r0 + count - t.q0);
+        t.row0 = t.end = 0;
+        t.steps = e < g.E ? (g.red + STEP - 1) / STEP : 0;
+        return t;
+    }
+};
+
+// The units of dw: the tiles of an expert, then the next one's.  The offsets are
+// read where they are used, a unit ahead (shared memory has no room for them).
+template <int LT, int NT>
+struct WalkDw {
+    const Args& g;
+    int stride, lt, per;  // tiles of lanes, of an expert
+    int e, i, a, b;       // the next unit's expert, place among its tiles, and offsets
+    __device__ WalkDw(const Args& g_, int first, int stride_) : g(g_), stride(stride_) {
+        lt = (g.lanes + LT - 1) / LT;
+        per = lt * ((g.cols + NT - 1) / NT);
+        e = first / per;
+        i = first - e * per;
+        read();
+    }
+    __device__ int total() const { return g.E * per; }
+    __device__ void read() {
+        const int32_t* from = g.offsets + min(e, g.E - 1);
+        a = from[0];
+        b = from[1];
+    }
+    __device__ Unit at(int) {
+        Unit t;
+        const int q = i / lt;
+        t.e = e;
+        t.l0 = (i - q * lt) * LT;
+        t.q0 = q * NT;
+        t.n = min(NT, g.cols - t.q0);
+        t.row0 = min(max(a, 0), g.P);
+        t.end = min(max(b, t.row0), g.P);
+        t.steps = (t.end - t.row0 + STEP - 1) / STEP;
+        i += stride;
+        if (i >= per) {
+            const int more = i / per;
+            e += more;
+            i -= more * per;
+            read();
         }
         return t;
     }
 };
+// Offsets that fall, or lie outside [0, P].
+__device__ __forceinline__ void check_offsets(const Args& g) {
+    bool bad = false;
+    for (int i = threadIdx.x; i <= g.E; i += blockDim.x) {
+        const int o = g.offsets[i], next = i < g.E ? g.offsets[i + 1] : o;
+        bad |= o < 0 || o > g.P || next < o || (i == 0 && o != 0);
+    }
+    if (bad) atomicOr(g.status, QMOE_DEV_BAD_OFFSETS);
+}
 
 template <typename T> struct Bits;
 template <> struct Bits<__nv_bfloat16> {
@@ -220,52 +258,56 @@ __device__ __forceinline__ void put_rows(const Args& g, uint8_t* stage, int l0, 
     }
 }
 
-// 32 columns of dw: lane l holds columns q0 .. q0 + n - 1 of row l0 + l.
+// 32 columns of dw: lane l holds columns q0 .. q0 + n - 1 of row l0 + l.  Through
+// shared memory, so that a store instruction writes whole rows of 128 bytes (64 in
+// 16 bits).  (512 experts of 8 rows, 1024 x 2048: 818 us with rows of 64 bytes, 698
+// with 128.)
 template <typename T>
 __device__ __forceinline__ void put_dw(const Args& g, uint8_t* stage, int e, int l0, int q0, int n, int lane,
                                        const uint32_t (&r)[32]) {
-    constexpr int PER = 16 / sizeof(T), COLS = 64 / sizeof(T);
+    constexpr int PER = 16 / sizeof(T), PIECES = 32 / PER, ROW = 32 * sizeof(T);  // of 16 bytes
+    constexpr int ROWS = 32;
+    static_assert(ROWS * ROW <= STAGE_DW, "");
     T* const out = static_cast<T*>(g.out) + (int64_t)e * g.out_e;
+    // where a row's piece lies: rows that are read or written together fall on all banks
+    auto place = [](int row, int p) { return row * ROW + ((p ^ (sizeof(T) == 4 ? row & 7 : row >> 1 & 3)) * 16); };
 #pragma unroll
-    for (int h = 0; h < 32 / COLS; ++h) {
+    for (int p = 0; p < PIECES; ++p) {
+        uint4 v;
+        uint32_t* w = &v.x;
 #pragma unroll
-        for (int p = 0; p < 4; ++p) {
-            uint4 v;
-            uint32_t* w = &v.x;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                if constexpr (sizeof(T) == 2)
-                    w[i] = row::pack2(__uint_as_float(r[p * 8 + 2 * i]), __uint_as_float(r[p * 8 + 2 * i + 1]), T{});
-                else
-                    w[i] = r[h * 16 + p * 4 + i];
-            }
-            *reinterpret_cast<uint4*>(stage + lane * 64 + ((p ^ (lane >> 1 & 3)) * 16)) = v;
+        for (int i = 0; i < 4; ++i) {
+            if constexpr (sizeof(T) == 2)
+                w[i] = row::pack2(__uint_as_float(r[p * 8 + 2 * i]), __uint_as_float(r[p * 8 + 2 * i + 1]), T{});
+            else
+                w[i] = r[p * 4 + i];
         }
-        __syncwarp();
-        if (g.wide) {
+        *reinterpret_cast<uint4*>(stage + place(lane, p)) = v;
+    }
+    __syncwarp();
+    if (g.wide) {
+        constexpr int EACH = 32 / PIECES;  // rows of an instruction
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int row = i * 8 + (lane >> 2), p = lane & 3, c = h * COLS + p * PER;
-                const uint4 v = *reinterpret_cast<const uint4*>(stage + row * 64 + ((p ^ (row >> 1 & 3)) * 16));
-                if (l0 + row < g.lanes && c < n) {
-                    T* const to = out + (int64_t)(l0 + row) * g.ld + q0 + c;
-                    if (c + PER <= n) {
-                        *reinterpret_cast<uint4*>(to) = v;
-                    } else {
-                        for (int j = 0; j < PER && c + j < n; ++j) to[j] = reinterpret_cast<const T*>(&v)[j];
-                    }
+        for (int i = 0; i < ROWS / EACH; ++i) {
+            const int row = i * EACH + lane / PIECES, p = lane % PIECES, c = p * PER;
+            const uint4 v = *reinterpret_cast<const uint4*>(stage + place(row, p));
+            if (l0 + row < g.lanes && c < n) {
+                T* const to = out + (int64_t)(l0 + row) * g.ld + q0 + c;
+                if (c + PER <= n) {
+                    *reinterpret_cast<uint4*>(to) = v;
+                } else {
+                    for (int j = 0; j < PER && c + j < n; ++j) to[j] = reinterpret_cast<const T*>(&v)[j];
                 }
             }
-        } else {
-            const int col = lane % COLS, c = h * COLS + col;
-#pragma unroll 4
-            for (int row = lane / COLS; row < 32; row += 32 / COLS) {
-                const T v = reinterpret_cast<const T*>(stage + row * 64 + (((col / PER) ^ (row >> 1 & 3)) * 16))[col % PER];
-                if (l0 + row < g.lanes && c < n) out[(int64_t)(l0 + row) * g.ld + q0 + c] = v;
-            }
         }
-        __syncwarp();
+    } else {
+#pragma unroll 8
+        for (int row = 0; row < ROWS; ++row) {
+            const T v = reinterpret_cast<const T*>(stage + place(row, lane / PER))[lane % PER];
+            if (l0 + row < g.lanes && lane < n) out[(int64_t)(l0 + row) * g.ld + q0 + lane] = v;
+        }
     }
+    __syncwarp();
 }
 
 template <int MODE>
@@ -287,11 +329,17 @@ __device__ __forceinline__ void put(const Args& g, uint8_t* stage, int e, int l0
 // threads of the CTA; the caller's barrier makes them seen.  Chunks of 32 experts
 // are scanned by a warp each, all at once (one warp after the other took 2 us of
 // the 10 of a decoded token).
-template <int MODE, int LT, int NT>
-__device__ __forceinline__ void read_offsets(const Args& g, int* off, int* base) {
+//
+// Returns the most columns of a tile: CAP, or where `workers` then take their last
+// tiles in a round of few, 7/8 or 6/8 of it if that makes for a shorter sum of rounds
+// (2048 rows, 2816 outputs: 88 tiles of 256 are two rounds of 76, and so are 121 of
+// 192).  Fewer columns do not make a step of the reduction shorter.
+template <int LT, int CAP, bool CHOOSE>
+__device__ __forceinline__ int read_offsets(const Args& g, int* off, int* base, int workers = 0) {
     constexpr int CHUNKS = (MAX_E + 32) / 32;
-    __shared__ int sums[CHUNKS];
+    __shared__ int sums[CHUNKS], parts[2];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+    if (CHOOSE && threadIdx.x < 2) parts[threadIdx.x] = 0;
     bool bad = false;
     for (int i = threadIdx.x; i <= g.E; i += blockDim.x) {
         const int o = g.offsets[i], next = i < g.E ? g.offsets[i + 1] : o;
@@ -305,23 +353,54 @@ __device__ __forceinline__ void read_offsets(const Args& g, int* off, int* base)
         }
         __syncthreads();
     }
-    if (MODE == DW) return;
     const int lt = (g.lanes + LT - 1) / LT;
-    for (int c = warp; c * 32 <= g.E; c += warps) {
-        const int i = c * 32 + lane;
+    // parts of expert i for tiles of cap columns
+    auto parts_of = [&](int i, int cap) {
         const int count = i < g.E ? off[i + 1] - off[i] : i == g.E ? g.P - off[i] : 0;
-        int v = (count + NT - 1) / NT * lt;
+        return (count + cap - 1) / cap;
+    };
+    auto scan = [&](int cap) {
+        for (int c = warp; c * 32 <= g.E; c += warps) {
+            const int i = c * 32 + lane;
+            int v = parts_of(i, cap) * lt;
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int w = __shfl_up_sync(0xFFFFFFFFu, v, o);
-            if (lane >= o) v += w;
+            for (int o = 1; o < 32; o <<= 1) {
+                const int w = __shfl_up_sync(0xFFFFFFFFu, v, o);
+                if (lane >= o) v += w;
+            }
+            if (i <= g.E) base[i + 1] = v;
+            if (lane == 31) sums[c] = v;
         }
-        if (i <= g.E) base[i + 1] = v;
-        if (lane == 31) sums[c] = v;
+    };
+    int cap = CAP;
+    if (CHOOSE) {
+        int a = 0, b = 0;
+        for (int i = threadIdx.x; i < g.E; i += blockDim.x) {
+            a += parts_of(i, CAP * 7 / 8);
+            b += parts_of(i, CAP * 6 / 8);
+        }
+        if (a) atomicAdd(&parts[0], a);
+        if (b) atomicAdd(&parts[1], b);
     }
+    scan(cap);
     if (threadIdx.x == 0) base[0] = 0;
-    if (g.E < 32) return;
+    if (!CHOOSE && g.E < 32) return cap;
     __syncthreads();
+    if (CHOOSE) {
+        int units = 0;
+        for (int c = 0; c * 32 <= g.E; ++c) units += sums[c];
+        if (units < 8 * workers) {
+            auto cost = [&](int n, int columns) { return (n + workers - 1) / workers * columns; };
+            const int whole = cost(units, 8), a = cost(parts[0] * lt, 7), b = cost(parts[1] * lt, 6);
+            if (a < whole || b < whole) cap = a <= b ? CAP * 7 / 8 : CAP * 6 / 8;
+        }
+        if (cap != CAP) {
+            __syncthreads();
+            scan(cap);
+            __syncthreads();
+        }
+    }
+    if (g.E < 32) return cap;
     for (int c = warp; c * 32 <= g.E; c += warps) {
         int before = 0;
         for (int j = lane; j < c; j += 32) before += sums[j];
@@ -330,6 +409,7 @@ __device__ __forceinline__ void read_offsets(const Args& g, int* off, int* base)
         const int i = c * 32 + lane;
         if (i <= g.E) base[i + 1] += before;
     }
+    return cap;
 }
 
 __device__ __forceinline__ void put_value(void* y, int type, int64_t at, float v) {

@@ -21,13 +21,19 @@ namespace eg {
 constexpr int PAIR_TMA = 8, TURNS = 2, PAIR_MMA = PAIR_TMA + TURNS;
 constexpr int PAIR_THREADS = (PAIR_MMA + 1) * 32;
 
+// Steps from which a sum of dw is made in two halves, added in the epilogue: the
+// tensor core cuts its sums off where fp32 would round them, which adds up (8192
+// rows: 9.1e-6 of the result).
+constexpr int LONG = 32;
+
 template <int MODE>
 struct PairCfg {
     static constexpr int P_BYTES = 128 * STEP * 2, STAGE = 2 * P_BYTES;
-    static constexpr int LIST = (MODE == DW ? MAX_E + 1 : 2 * (MAX_E + 2)) * 4;
+    static constexpr int LIST = MODE == DW ? 0 : 2 * (MAX_E + 2) * 4;
+    static constexpr int OUT = MODE == DW ? STAGE_DW : STAGE_OUT;
     static constexpr int STAGES = 6;
     static constexpr int OUT_OFF = STAGES * STAGE;
-    static constexpr int LIST_OFF = OUT_OFF + EPI_WARPS * STAGE_OUT;
+    static constexpr int LIST_OFF = OUT_OFF + EPI_WARPS * OUT;
     static constexpr int BAR_OFF = LIST_OFF + (LIST + 15) / 16 * 16;
     static constexpr int MISC_OFF = BAR_OFF + (3 * STAGES + 4) * 8;
     static constexpr int SMEM = MISC_OFF + 64 + 1024;
@@ -133,14 +139,23 @@ expert_pair_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_const
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
     }
     pdl_wait();
-    read_offsets<MODE, 256, 256>(g, off, base);
+    int cap = 256;
+    if constexpr (MODE == DW) {
+        if (blockIdx.x == 0) check_offsets(g);
+    } else {
+        cap = read_offsets<256, 256, true>(g, off, base, gridDim.x >> 1);
+    }
     tc::tc_fence_before();
     __syncthreads();
     cluster_sync();
     tc::tc_fence_after();
     const uint32_t tm = *tmem_at;
-    Walk<MODE, 256, 256, 32> walk(g, off, base);
-    const int total = walk.total(), first = blockIdx.x >> 1, stride = gridDim.x >> 1;
+    const int first = blockIdx.x >> 1, stride = gridDim.x >> 1;
+    auto walk = [&] {
+        if constexpr (MODE == DW) return WalkDw<256, 256>(g, first, stride);
+        else return Walk<256, 32>(g, off, base, cap);
+    }();
+    const int total = walk.total();
 
     if (warp >= PAIR_TMA && warp < PAIR_MMA) {
         if (lane == 0) {
@@ -151,7 +166,6 @@ expert_pair_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_const
                 const int half = ((t.n + 31) & ~31) / 2, l0 = t.l0 + rank * 128, q0 = t.q0 + rank * half;
                 const int boxes = MODE == DW ? (half + 63) / 64 : 1;
                 const uint32_t bytes = C::P_BYTES + boxes * (MODE == DW ? 8192 : 128 * 128);
-                const int end = MODE == DW ? off[t.e + 1] : 0;
                 for (int s = 0; s < t.steps; ++s, ++it) {
                     if (it % TURNS != turn) continue;
                     const int slot = it % C::STAGES;
@@ -159,7 +173,7 @@ expert_pair_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_const
                     uint8_t* st = smem + slot * C::STAGE;
                     uint8_t* sq = st + C::P_BYTES;
                     const int k0 = s * STEP, row = t.row0 + k0;
-                    const bool relay = MODE == DW && end - row < STEP;
+                    const bool relay = MODE == DW && t.end - row < STEP;
                     const uint32_t bar = bar_in(&full[slot], relay ? rank : 0);
                     if (relay) tc::mbar_arrive_expect_tx(&full[slot], bytes);
                     else if (rank == 0) tc::mbar_arrive_expect_tx(&full[slot], 2 * bytes);
@@ -189,17 +203,32 @@ expert_pair_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_const
             if (t.steps == 0) continue;  // zeros: no sums to wait for
             const uint32_t n32 = (uint32_t)(t.n + 31) & ~31u;
             const uint32_t idesc = g.idesc | (n32 >> 3) << 17 | (256u >> 4) << 24;
-            const uint32_t d = tm + buf * 256;
-            const int left = MODE == DW ? (off[t.e + 1] - t.row0) % STEP : 0, whole = t.steps - (left > 0);
-            if (rank == 0 && lane == 0) ok = ok && lane_wait(&acc_empty[buf], acc_phase ^ 1, abort_flag, g.status);
-            __syncwarp();
+            uint32_t d = tm + buf * 256;
+            const int left = MODE == DW ? (t.end - t.row0) % STEP : 0, whole = t.steps - (left > 0);
+            auto take = [&]() {  // an accumulator
+                if (rank == 0 && lane == 0) ok = ok && lane_wait(&acc_empty[buf], acc_phase ^ 1, abort_flag, g.status);
+                __syncwarp();
+                d = tm + buf * 256;
+            };
+            auto give = [&]() {
+                if (rank == 0) commit_pair(&acc_full[buf]);
+                if (++buf == 2) { buf = 0; acc_phase ^= 1; }
+            };
+            take();
+            const int turn = MODE == DW && t.steps > LONG ? t.steps / 2 : 0;  // a long sum's second half has its own accumulator
+            int from = 0;
             if (rank == 0) {
 #pragma unroll 1
                 for (int s = 0; s < whole; ++s) {
+                    if (MODE == DW && turn && s == turn) {
+                        give();
+                        take();
+                        from = s;
+                    }
                     if (lane == 0) ok = ok && lane_wait(&full[slot], phase, abort_flag, g.status);
                     __syncwarp();
                     tc::tc_fence_after();
-                    mma_stage<MODE>(d, tc::smem_u32(smem) + slot * C::STAGE, idesc, s == 0);
+                    mma_stage<MODE>(d, tc::smem_u32(smem) + slot * C::STAGE, idesc, s == from);
                     commit_pair(&empty[slot]);
                     if (++slot == C::STAGES) { slot = 0; phase ^= 1; }
                 }
@@ -228,7 +257,7 @@ expert_pair_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_const
                         relayed ^= 1u << slot;
                         __syncwarp();
                         tc::tc_fence_after();
-                        mma_stage<MODE>(d, tc::smem_u32(st), idesc, whole == 0, k16);
+                        mma_stage<MODE>(d, tc::smem_u32(st), idesc, whole == from, k16);
                         commit_pair(&empty[slot]);
                     } else if (lane == 0) {
                         arrive_first(&other[slot]);
@@ -237,39 +266,72 @@ expert_pair_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_const
                     if (++slot == C::STAGES) { slot = 0; phase ^= 1; }
                 }
             }
-            if (rank == 0) commit_pair(&acc_full[buf]);
-            if (++buf == 2) { buf = 0; acc_phase ^= 1; }
+            give();
         }
         __syncwarp();
     } else {
         const int quad = warp & 3, half = warp >> 2;
-        uint8_t* const stage = smem + C::OUT_OFF + warp * STAGE_OUT;
+        uint8_t* const stage = smem + C::OUT_OFF + warp * C::OUT;
         int buf = 0;
         uint32_t acc_phase = 0;
         for (int u = first; u < total && !*abort_flag; u += stride) {
             const Unit t = walk.at(u);
             const int l0 = t.l0 + rank * 128 + quad * 32;
-            if (t.steps > 0) {
-                if (!warp_wait(&acc_full[buf], acc_phase, abort_flag, g.status)) break;
-                tc::tc_fence_after();
-            }
-            for (int c = half * 32; c < t.n; c += 64) {
+            if (t.steps == 0) {
                 uint32_t r[32];
-                if (t.steps > 0) {
-                    tmem_ld32(tm + ((uint32_t)(quad * 32) << 16) + buf * 256 + c, r);
-                    tc::tmem_ld_wait();
-                } else {
 #pragma unroll
-                    for (int j = 0; j < 32; ++j) r[j] = 0;
-                }
-                put<MODE>(g, stage, t.e, l0, t.q0 + c, t.n - c, lane, r);
+                for (int j = 0; j < 32; ++j) r[j] = 0;
+                for (int c = half * 32; c < t.n; c += 64) put<MODE>(g, stage, t.e, l0, t.q0 + c, t.n - c, lane, r);
+                continue;
             }
-            if (t.steps > 0) {
+            if (!warp_wait(&acc_full[buf], acc_phase, abort_flag, g.status)) break;
+            tc::tc_fence_after();
+            const uint32_t from = tm + ((uint32_t)(quad * 32) << 16) + buf * 256;
+            if (MODE == DW && t.steps > LONG) {
+                // both halves of the sum
+                const int other = buf ^ 1;
+                if (!warp_wait(&acc_full[other], acc_phase ^ (other == 0), abort_flag, g.status)) break;
+                tc::tc_fence_after();
+                for (int c = half * 32; c < t.n; c += 64) {
+                    uint32_t x[32], y[32];
+                    tmem_ld32(from + c, x);
+                    tmem_ld32(tm + ((uint32_t)(quad * 32) << 16) + other * 256 + c, y);
+                    tc::tmem_ld_wait();
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) x[j] = __float_as_uint(__uint_as_float(x[j]) + __uint_as_float(y[j]));
+                    put<MODE>(g, stage, t.e, l0, t.q0 + c, t.n - c, lane, x);
+                }
                 tc::tc_fence_before();
                 __syncwarp();
-                if (lane == 0) arrive_first(&acc_empty[buf]);
-                if (++buf == 2) { buf = 0; acc_phase ^= 1; }
+                if (lane == 0) {
+                    arrive_first(&acc_empty[0]);
+                    arrive_first(&acc_empty[1]);
+                }
+                acc_phase ^= 1;  // two accumulators on
+                continue;
             }
+            // the next 32 columns are on their way while these are stored; the sums are let go when the last have come
+            uint32_t r[2][32];
+            int at = half * 32;
+            if (at < t.n) tmem_ld32(from + at, r[0]);
+            auto turn = [&](uint32_t (&now)[32], uint32_t (&next)[32]) {
+                tc::tmem_ld_wait();
+                if (at + 64 < t.n) {
+                    tmem_ld32(from + at + 64, next);
+                } else {
+                    tc::tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) arrive_first(&acc_empty[buf]);
+                }
+                put<MODE>(g, stage, t.e, l0, t.q0 + at, t.n - at, lane, now);
+                at += 64;
+            };
+            if (at >= t.n && lane == 0) arrive_first(&acc_empty[buf]);  // no columns for this warp
+            while (at < t.n) {
+                turn(r[0], r[1]);
+                if (at < t.n) turn(r[1], r[0]);
+            }
+            if (++buf == 2) { buf = 0; acc_phase ^= 1; }
         }
     }
     __syncwarp();

@@ -495,6 +495,9 @@ __global__ void __launch_bounds__(THREADS, NT == 1 ? 2 : 1) w4_few_kernel(const 
     }
 }
 
+// Two E2M1 codes as fp16.
+__device__ __forceinline__ uint32_t e2m1_pair(uint32_t byte) { return pair_of<__half, QMOE_W4_E2M1, 0>(byte); }
+
 // W in 16 bits, [N, K], and {0, T} for the grouped product with one expert.
 template <typename T, int FORMAT>
 __global__ void __launch_bounds__(256) w4_widen_kernel(int64_t words, int per_row, int shift, const uint32_t* w, const void* s,
@@ -512,9 +515,12 @@ __global__ void __launch_bounds__(256) w4_widen_kernel(int64_t words, int per_ro
     const uint32_t v = w[i];
     float d[8];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        const uint32_t c = v >> 4 * j & 15;
-        d[j] = f * (FORMAT == QMOE_W4_INT4 ? (float)((int)c - 8) : e2m1_to_float(c));
+    for (int j = 0; j < 4; ++j) {
+        float2 c;
+        if constexpr (FORMAT == QMOE_W4_INT4) c = make_float2((int)(v >> 8 * j & 15) - 8, (int)(v >> (8 * j + 4) & 15) - 8);
+        else c = row::unpack2(e2m1_pair(v >> 8 * j & 255), __half{});
+        d[2 * j] = f * c.x;
+        d[2 * j + 1] = f * c.y;
     }
     row::store<8>(reinterpret_cast<T*>(to + i), d);
 }
