@@ -10,6 +10,13 @@
 `forward` serves (any number of tokens, one for a decode step); `train_step` adds the gradients of what such a block
 trains beside frozen routed experts: its norms, its gate, the shared expert and, through the balance loss, the router.
 
+`TrainedExperts` are routed experts in 16 bits with their gradients, and the router's through the routing weights:
+
+    offsets, pairs, slot = align_sort(ids)
+    gu  = expert_linear(n, w1, offsets, pairs)                     gate and up projections, rows in expert order
+    y   = expert_linear(swiglu(gu), w2, offsets)                   down projection
+    out = combine(y, w, slot)                                      weighted sum over a token's experts
+
     python examples/moe_block.py [--tokens 64] [--hidden 512] [--experts 16] [--top-k 4] [--inter 256]
 """
 
@@ -87,6 +94,34 @@ class MoeBlock:
         return dx, dict(w_in=dw_in, w_out=dw_out, w_next=dw_next, gate=dgate, router=dlogits.t() @ s["n"].float(), w1=dw1, w2=dw2), s["route"]
 
 
+class TrainedExperts:
+    """Routed experts in bf16 that are trained: forward, and every gradient."""
+
+    def __init__(self, H=512, I=256, E=16, seed=0, device="cuda"):
+        g = torch.Generator(device=device).manual_seed(seed)
+        self.w1 = (torch.randn(E, 2 * I, H, generator=g, device=device) * H ** -0.5).bfloat16()
+        self.w2 = (torch.randn(E, H, I, generator=g, device=device) * I ** -0.5).bfloat16()
+
+    def forward(self, n, ids, w):
+        """n [T, H] bf16, ids int32 and w fp32 [T, k] (ids of -1: not routed).  Returns (out, what backward needs)."""
+        offsets, pairs, slot = qb.align_sort(ids, self.w1.shape[0])
+        gu = qb.expert_linear(n, self.w1, offsets, pairs=pairs, k=ids.shape[1])
+        h = qb.swiglu(gu)
+        y = qb.expert_linear(h, self.w2, offsets)
+        return qb.combine(y, w, slot), dict(n=n, w=w, offsets=offsets, pairs=pairs, slot=slot, gu=gu, y=y)
+
+    def backward(self, dout, s):
+        """Gradients of n, of the routing weights and of both projections; h is made again on the way."""
+        k = s["w"].shape[1]
+        dy, dw = qb.combine_backward(dout, s["y"], s["w"], s["slot"], s["offsets"])
+        # dh needs no h, and dw2 does: the product's two gradients are asked for one by one
+        dh, _ = qb.expert_linear_backward(dy, dy.new_empty(dy.shape[0], self.w2.shape[2]), self.w2, s["offsets"], need_dw=False)
+        dgu, h = qb.swiglu_backward(dh, s["gu"], h_too=True)
+        _, dw2 = qb.expert_linear_backward(dy, h, self.w2, s["offsets"], need_dx=False)
+        dn, dw1 = qb.expert_linear_backward(dgu, s["n"], self.w1, s["offsets"], pairs=s["pairs"], k=k)
+        return qb.combine(dn, None, s["slot"]), dw, dw1, dw2
+
+
 def main():
     ap = argparse.ArgumentParser(description=__doc__.splitlines()[0])
     ap.add_argument("--tokens", type=int, default=64)
@@ -106,6 +141,14 @@ def main():
     dout, dn_next = ((0.1 * torch.randn(r.shape, generator=g, device="cuda")).bfloat16() for _ in range(2))
     dx, grads, _ = block.train_step(r, dout, dn_next)
     print("gradients: dx %.4f, " % dx.float().norm().item() + ", ".join(f"{n} {t.float().norm().item():.4f}" for n, t in grads.items()))
+    experts = TrainedExperts(a.hidden, a.inter, a.experts)
+    n, _ = qb.norm_pre(r, block.w_in, eps=EPS)
+    route = qb.route_topk(n.float() @ block.router.t(), a.top_k)
+    y, kept = experts.forward(n, route.ids, route.w)
+    dn, dw, dw1, dw2 = experts.backward(dout, kept)
+    dlogits = qb.route_topk_backward(n.float() @ block.router.t(), route, dw=dw)
+    print("trained experts: |y| %.4f, gradients: n %.4f, router %.4f, w1 %.4f, w2 %.4f"
+          % tuple(t.float().norm().item() for t in (y, dn, dlogits.t() @ n.float(), dw1, dw2)))
     assert int(qb.status_word("cuda").item()) == 0
 
 

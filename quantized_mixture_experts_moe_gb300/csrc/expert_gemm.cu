@@ -388,6 +388,7 @@ static int copy_rows(Mat& m, const int32_t* pairs, int64_t P, int k, uint8_t*& w
     left -= need;
     return rc;
 }
+inline size_t copy_need(const Mat& m) { return fits(m) ? 0 : padded(m.rows * m.experts, m.cols); }
 static int as_tma(Mat& m, uint8_t*& ws, size_t& left, cudaStream_t st) {
     if (!fits(m)) return copy_rows(m, nullptr, 0, 0, ws, left, st);
     if (m.ld % 8) m.ld = (m.cols + 7) / 8 * 8;  // a single row: the stride is not used
@@ -466,7 +467,7 @@ static int run_rows(Mat w, Mat q, Args& g, int dtype, uint8_t* ws, size_t left, 
     if (most >= (1ll << 31)) return QMOE_ERR_UNSUPPORTED;
     const bool shares = split(g.P, g.E, g.lanes, g.red, nt);
     if (shares) {
-        if (left < part_bytes(nt)) return QMOE_ERR_ARG;
+        if (left < part_bytes(nt)) return QMOE_ERR_ARG;  // asked for above
         g.parts = reinterpret_cast<float*>(ws);
         g.joins = reinterpret_cast<int4*>(ws + (size_t)row::kSMs * 2 * nt * 128 * 4);
     }
@@ -541,8 +542,10 @@ extern "C" int qmoe_expert_linear(int64_t P, int E, int64_t N, int64_t K, int dt
                   aligned16(y) && ldy * size % 16 == 0,
                   dtype == QMOE_BF16 ? tc::idesc_bf16_f32(0, 0) : tc::idesc_f16_f32(0, 0), dev_status, nullptr, nullptr};
     if (eg::few(P, E, eg::fits(mw))) return eg::launch_few(mw, mx, g, dtype, st);
-    if ((rc = eg::as_tma(mw, at, left, st)) != QMOE_OK) return rc;
     const bool lay_out = pairs && eg::tile_of(P, E) == 256;
+    const size_t need = qmoe_expert_workspace_bytes(P, E, N, K, eg::FWD, pairs != nullptr);
+    if (left < need + eg::copy_need(mw) + (lay_out ? 0 : eg::copy_need(mx))) return QMOE_ERR_ARG;
+    if ((rc = eg::as_tma(mw, at, left, st)) != QMOE_OK) return rc;
     rc = lay_out ? eg::copy_rows(mx, pairs, P, k, at, left, st) : eg::as_tma(mx, at, left, st);
     if (rc != QMOE_OK) return rc;
     if (lay_out) g.pairs = nullptr;
@@ -566,6 +569,7 @@ extern "C" int qmoe_expert_linear_dx(int64_t P, int E, int64_t N, int64_t K, int
     cudaStream_t st = (cudaStream_t)stream;
     uint8_t* at = static_cast<uint8_t*>(ws);
     size_t left = ws && !(reinterpret_cast<uintptr_t>(ws) & 255u) ? ws_bytes : 0;
+    if (left < qmoe_expert_workspace_bytes(P, E, N, K, eg::DX, 0) + eg::copy_need(mw) + eg::copy_need(my)) return QMOE_ERR_ARG;
     if ((rc = eg::as_tma(mw, at, left, st)) != QMOE_OK || (rc = eg::as_tma(my, at, left, st)) != QMOE_OK) return rc;
     const int size = row::dtype_size(dx_dtype);
     eg::Args g = {(int)P, E, (int)K, 0, (int)N, offsets, nullptr, 0, (int)P, dx, lddx, 0, dx_dtype,
@@ -595,6 +599,7 @@ extern "C" int qmoe_expert_linear_dw(int64_t P, int E, int64_t N, int64_t K, int
     if (!eg::mat_ok(my, 2) || !eg::mat_ok(mx, 2)) return QMOE_ERR_ARG;
     uint8_t* at = static_cast<uint8_t*>(ws);
     size_t left = ws && !(reinterpret_cast<uintptr_t>(ws) & 255u) ? ws_bytes : 0;
+    if (left < (pairs ? eg::padded(P, K) : eg::copy_need(mx)) + eg::copy_need(my)) return QMOE_ERR_ARG;
     if ((rc = eg::as_tma(my, at, left, st)) != QMOE_OK) return rc;
     rc = pairs ? eg::copy_rows(mx, pairs, P, k, at, left, st) : eg::as_tma(mx, at, left, st);
     if (rc != QMOE_OK) return rc;

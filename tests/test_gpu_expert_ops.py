@@ -535,3 +535,65 @@ def test_first_call_in_a_capture_is_refused_without_a_status():
         assert (y == 64).all()
     finally:
         qb._status_words.update(held)
+
+
+def test_trained_experts_example():
+    """examples/moe_block.py's trained experts: gradients against the 64-bit step, with tokens that are not routed."""
+    import importlib.util
+    import os
+
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "moe_block.py")
+    spec = importlib.util.spec_from_file_location("moe_block", path)
+    m = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(m)
+    x, ids, wr, _, _, dout = layer(21, T=30, k=3, E=5, H=128, I=64)
+    experts = m.TrainedExperts(H=128, I=64, E=5, seed=2)
+    out, kept = experts.forward(dev(x), dev(ids), dev(wr))
+    got = (out,) + experts.backward(dev(dout), kept)
+    want = plain_step(x, ids, wr, experts.w1.cpu(), experts.w2.cpu(), dout)
+    for name, a, b in zip(("out", "dn", "dw", "dw1", "dw2"), got, want):
+        rel = float((a.cpu().double() - b).norm() / b.norm())
+        assert rel < 9 * 2.0 ** -8, (name, rel)  # as in test_training_step
+    assert status() == 0
+
+
+# ------------------------------------------------------------------ what the binding refuses
+
+def test_binding_refuses():
+    z = lambda *s, dtype=BF16: torch.zeros(*s, dtype=dtype, device="cuda")
+    off = torch.tensor([0, 4, 8], dtype=torch.int32, device="cuda")
+    x, w = z(8, 64), z(2, 32, 64)
+    for f in (lambda: qb.expert_linear(x, z(2, 32, 63), off), lambda: qb.expert_linear(x, w, off[:2]), lambda: qb.expert_linear(x, w.half(), off),
+              lambda: qb.expert_linear(x.float(), w.float(), off), lambda: qb.expert_linear(x, w, off.long()), lambda: qb.expert_linear(x, w[0], off),
+              lambda: qb.expert_linear(x[0], w, off), lambda: qb.expert_linear(x, w, off, pairs=off.float()), lambda: qb.expert_linear(x, w, off, pairs=off, k=0),
+              lambda: qb.expert_linear(x, w, off, out_dtype=torch.int64), lambda: qb.expert_linear_backward(z(7, 32), x, w, off),
+              lambda: qb.expert_linear_backward(z(8, 33), x, w, off), lambda: qb.expert_linear_backward(z(8, 32).half(), x, w, off),
+              lambda: qb.swiglu(z(4, 7)), lambda: qb.swiglu_backward(z(4, 8), z(4, 15)), lambda: qb.swiglu_backward(z(4, 8), z(4, 16).half()),
+              lambda: qb.combine(x, z(4, 2), off.view(1, 3)), lambda: qb.combine(x, None, off), lambda: qb.combine_backward(z(4, 64), x, None, off.view(1, 3), off),
+              lambda: qb.combine_backward(z(1, 64).half(), x, None, off.view(1, 3), off),
+              lambda: qb.w4_linear(x, z(16, 32, dtype=torch.uint8), z(16, 3, dtype=F16)), lambda: qb.w4_linear(x, z(16, 32, dtype=torch.uint8), z(16, 2, dtype=F32)),
+              lambda: qb.w4_linear(x, z(16, 31, dtype=torch.uint8), z(16, 2, dtype=F16)), lambda: qb.w4_linear(x, z(16, 32, dtype=torch.int8), z(16, 2, dtype=F16)),
+              lambda: qb.w4_linear(x.float(), z(16, 32, dtype=torch.uint8), z(16, 2, dtype=F16)),
+              lambda: qb.w4_linear(x, z(2, 16, 32, dtype=torch.uint8), z(2, 16, 2, dtype=F16), ids=off), lambda: qb.align_sort(off, 4)):
+        with pytest.raises(ValueError):
+            f()
+    for f in (lambda: qb.expert_linear(x.t(), z(2, 32, 8), off), lambda: qb.expert_linear(x, w.transpose(1, 2).contiguous().transpose(1, 2), off),
+              lambda: qb.expert_linear(x.cpu(), w, off), lambda: qb.expert_linear(x, w, off, out_dtype=F16), lambda: qb.expert_linear(z(1, 64).expand(8, 64), w, off),
+              lambda: qb.w4_linear(z(4, 64), z(16, 32, dtype=torch.uint8), z(16, 4, dtype=F16)),
+              lambda: qb.w4_linear(z(4, 64), z(32, 16, dtype=torch.uint8).t(), z(16, 2, dtype=F16)),
+              lambda: qb.expert_linear(x, w, off, ws=torch.empty(1, dtype=torch.uint8).cuda()) if qb.lib().qmoe_expert_workspace_bytes(8, 2, 32, 64, 0, 0)
+              else (_ for _ in ()).throw(qb.QmoeError()),
+              lambda: qb.w4_linear(z(20, 64), z(16, 32, dtype=torch.uint8), z(16, 2, dtype=F16), ws=torch.empty(256, dtype=torch.uint8).cuda())):
+        with pytest.raises(qb.QmoeError):
+            f()
+    assert status() == 0
+
+
+def test_align_sort():
+    ids = torch.tensor([[2, 0], [1, 2], [-1, 5], [2, 1]], dtype=torch.int32, device="cuda")
+    word = torch.zeros(1, dtype=torch.int32, device="cuda")
+    offsets, pairs, slot = qb.align_sort(ids, 3, dev_status=word)
+    assert offsets.tolist() == [0, 1, 3, 6] and pairs.tolist() == [1, 2, 7, 0, 3, 6, -1, -1]
+    assert slot.tolist() == [[3, 0], [1, 4], [-1, -1], [5, 2]] and int(word) == qb.DEV_BAD_EXPERT_ID
+    offsets, pairs, slot = qb.align_sort(ids[:0], 3)
+    assert offsets.tolist() == [0, 0, 0, 0] and pairs.numel() == 0 == slot.numel()
