@@ -16,18 +16,21 @@
 namespace qmoe {
 namespace eg {
 
-// Warps: the epilogue's, one that loads tiles, one that issues products, then
-// those that gather.
+// Warps: the epilogue's, two that load tiles and two that issue products, each pair
+// taking the steps in turn (each of the two that issue has a sum of its own), then
+// those that gather.  With one warp of each: 16 tokens x 2 of 8 experts 4096 -> 2816
+// 40.5 us for 38.4, one row 4096 -> 4096 14.9 for 14.0, but one token x 8 of 128
+// experts 14.5 for 15.0.
 #ifndef FEW_MOST
 #define FEW_MOST 0
 #endif
-constexpr int WARP_TMA = 8, WARP_MMA = 9;
-constexpr int threads_of(bool gather) { return (10 + (gather ? GATHER_WARPS : 0)) * 32; }
+constexpr int TURNS = 2, WARP_TMA = 8, WARP_MMA = WARP_TMA + TURNS, WARP_GATHER = WARP_MMA + TURNS;
+constexpr int threads_of(bool gather) { return (WARP_GATHER + (gather ? GATHER_WARPS : 0)) * 32; }
 
 template <int MODE, int NT>
 struct Cfg {
     static constexpr int P_BYTES = 128 * STEP * 2, Q_BYTES = NT * STEP * 2, STAGE = P_BYTES + Q_BYTES;
-    static constexpr int TMEM_COLS = 2 * NT < 32 ? 32 : 2 * NT;
+    static constexpr int TMEM_COLS = 2 * TURNS * NT;  // two tiles' sums of each warp that issues
     static constexpr int LIST = 2 * (MAX_E + 2) * 4;
     static constexpr int FIXED = EPI_WARPS * STAGE_OUT + (LIST + 15) / 16 * 16 + 512 + 1024;
     static constexpr int FIT = (232448 - FIXED) / STAGE;
@@ -112,13 +115,17 @@ expert_gemm_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_const
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::MISC_OFF + 8);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (threadIdx.x == 32) {
+        tc::prefetch_tensormap(&map_p);
+        tc::prefetch_tensormap(&map_q);
+    }
     if (threadIdx.x == 0) {
         for (int i = 0; i < C::STAGES; ++i) {
             tc::mbar_init(&full[i], 1);
             tc::mbar_init(&empty[i], 1);
         }
         for (int i = 0; i < 2; ++i) {
-            tc::mbar_init(&acc_full[i], 1);
+            tc::mbar_init(&acc_full[i], TURNS);
             tc::mbar_init(&acc_empty[i], EPI_WARPS);
         }
         *abort_flag = 0;
@@ -141,13 +148,14 @@ expert_gemm_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_const
     const Unit& t = seg.t;
     if (SPLIT) pdl_trigger();  // join_kernel needs little, and waits
 
-    if (warp == WARP_TMA) {
-        int slot = 0;
-        uint32_t phase = 0;
+    if (warp >= WARP_TMA && warp < WARP_MMA) {
+        int it = 0;
         while (!*abort_flag && segments.next(seg)) {
             const int boxes = GATHER ? 0 : (t.n + Q_BOX - 1) / Q_BOX;
-            for (int s = seg.s0; s < seg.s1; ++s) {
-                if (!warp_wait(&empty[slot], phase ^ 1, abort_flag, g.status)) break;
+            for (int s = seg.s0; s < seg.s1; ++s, ++it) {
+                if (it % TURNS != warp - WARP_TMA) continue;
+                const int slot = it % C::STAGES;
+                if (!warp_wait(&empty[slot], (it / C::STAGES & 1) ^ 1, abort_flag, g.status)) break;
                 uint8_t* st = smem + slot * C::STAGE;
                 const int k0 = s * STEP;
                 if (lane == 0) {
@@ -163,22 +171,26 @@ expert_gemm_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_const
                 if (lane < boxes)
                     tc::tma_load_2d(st + C::P_BYTES + lane * Q_BOX * 128, &map_q, &full[slot], k0, t.q0 + lane * Q_BOX);
                 __syncwarp();
-                if (++slot == C::STAGES) { slot = 0; phase ^= 1; }
             }
         }
         __syncwarp();
-    } else if (warp == WARP_MMA) {
-        int slot = 0, buf = 0;
-        uint32_t phase = 0, acc_phase = 0;
+    } else if (warp >= WARP_MMA && warp < WARP_GATHER) {
+        const int turn = warp - WARP_MMA;
+        int it = 0, buf = 0;
+        uint32_t acc_phase = 0;
         bool ok = true;  // lane 0's; after a wait that ran out nothing is waited for any more
         while (segments.next(seg)) {
             if (seg.s1 == 0) continue;  // zeros: no sums to wait for
             const uint32_t n16 = (uint32_t)(t.n + 15) & ~15u;
-            const uint32_t idesc = g.idesc | (n16 >> 3) << 17 | (128u >> 4) << 24, d = tm + buf * NT;
+            const uint32_t idesc = g.idesc | (n16 >> 3) << 17 | (128u >> 4) << 24, d = tm + (buf * TURNS + turn) * NT;
             if (lane == 0) ok = ok && lane_wait(&acc_empty[buf], acc_phase ^ 1, abort_flag, g.status);
+            // the tile's steps s0 + turn, s0 + turn + 2, ..: a sum of its own
+            const int last = it + seg.s1 - seg.s0;
+            uint32_t more = 0;
 #pragma unroll 1
-            for (int s = seg.s0; s < seg.s1; ++s) {
-                if (lane == 0) ok = ok && lane_wait(&full[slot], phase, abort_flag, g.status);
+            for (int i = it + turn; i < last; i += TURNS) {
+                const int slot = i % C::STAGES;
+                if (lane == 0) ok = ok && lane_wait(&full[slot], i / C::STAGES & 1, abort_flag, g.status);
                 __syncwarp();
                 tc::tc_fence_after();
                 const uint32_t sa = tc::smem_u32(smem) + slot * C::STAGE, sb = sa + C::P_BYTES;
@@ -186,17 +198,17 @@ expert_gemm_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_const
                 const uint64_t db = tc::sdesc_kmajor_sw128(sb);
                 constexpr int SA = MODE == FWD ? 2 : 128, SB = 2;  // of 16 values, in 16 bytes
 #pragma unroll
-                for (int k = 0; k < STEP / 16; ++k)
-                    tc::mma_f16_elect(d, da + SA * k, db + SB * k, idesc, s > seg.s0 || k > 0);
+                for (int k = 0; k < STEP / 16; ++k) tc::mma_f16_elect(d, da + SA * k, db + SB * k, idesc, k > 0 ? 1 : more);
                 tc::mma_commit_elect(&empty[slot]);
-                if (++slot == C::STAGES) { slot = 0; phase ^= 1; }
+                more = 1;
             }
+            it = last;
             tc::mma_commit_elect(&acc_full[buf]);
             if (++buf == 2) { buf = 0; acc_phase ^= 1; }
         }
         __syncwarp();
-    } else if (warp > WARP_MMA) {
-        const int gw = warp - WARP_MMA - 1, turn = gw / GATHER_SHARE, share = gw % GATHER_SHARE;
+    } else if (warp >= WARP_GATHER) {
+        const int gw = warp - WARP_GATHER, turn = gw / GATHER_SHARE, share = gw % GATHER_SHARE;
         int it = 0;
         while (!*abort_flag && segments.next(seg)) {
             // lane j has the group share + 4 j of the tile
@@ -236,8 +248,20 @@ expert_gemm_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_const
             for (int c = half * 32; c < t.n; c += 64) {
                 uint32_t r[32];
                 if (seg.s1 > 0) {
-                    tmem_ld32(tm + ((uint32_t)(quad * 32) << 16) + buf * NT + c, r);
+                    const uint32_t from = tm + ((uint32_t)(quad * 32) << 16) + buf * TURNS * NT + c;
+                    tmem_ld32(from, r);
                     tc::tmem_ld_wait();
+                    if (seg.s1 - seg.s0 > 1) {
+#pragma unroll
+                        for (int h = 0; h < 32; h += 16) {
+                            uint32_t y[16];
+                            tc::tmem_ld_32x32b_x16(from + NT + h, y);
+                            tc::tmem_ld_wait();
+#pragma unroll
+                            for (int j = 0; j < 16; ++j)
+                                r[h + j] = __float_as_uint(__uint_as_float(r[h + j]) + __uint_as_float(y[j]));
+                        }
+                    }
                 } else {
 #pragma unroll
                     for (int j = 0; j < 32; ++j) r[j] = 0;

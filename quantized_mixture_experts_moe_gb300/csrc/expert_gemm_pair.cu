@@ -120,6 +120,10 @@ expert_pair_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_const
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int rank = (int)cluster_rank();
+    if (threadIdx.x == 32) {
+        tc::prefetch_tensormap(&map_p);
+        tc::prefetch_tensormap(&map_q);
+    }
     if (threadIdx.x == 0) {
         for (int i = 0; i < C::STAGES; ++i) {
             tc::mbar_init(&full[i], 1);

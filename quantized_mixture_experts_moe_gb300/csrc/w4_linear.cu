@@ -207,6 +207,7 @@ __global__ void __launch_bounds__(THREADS, NT == 1 ? 2 : 1) w4_few_kernel(const 
     const int p0 = u0 / g.tiles;
     const int blocks = (g.K + BLOCK - 1) / BLOCK, mine = (blocks - part + kw - 1) >> g.kw_log;  // of a tile, of this warp
 
+    if (threadIdx.x == 0) tc::prefetch_tensormap(&map);
     pdl_wait();
     if (threadIdx.x < 2 * WARPS * DEPTH) {
         tc::mbar_init(&bars[threadIdx.x], 1);
