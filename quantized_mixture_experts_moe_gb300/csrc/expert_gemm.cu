@@ -21,9 +21,6 @@ namespace eg {
 // those that gather.  With one warp of each: 16 tokens x 2 of 8 experts 4096 -> 2816
 // 40.5 us for 38.4, one row 4096 -> 4096 14.9 for 14.0, but one token x 8 of 128
 // experts 14.5 for 15.0.
-#ifndef FEW_MOST
-#define FEW_MOST 0
-#endif
 constexpr int TURNS = 2, WARP_TMA = 8, WARP_MMA = WARP_TMA + TURNS, WARP_GATHER = WARP_MMA + TURNS;
 constexpr int threads_of(bool gather) { return (WARP_GATHER + (gather ? GATHER_WARPS : 0)) * 32; }
 
@@ -56,8 +53,11 @@ template <int MODE, int NT, bool SPLIT>
 struct Segments {
     Walk<128, 16> walk;
     int64_t at, end;  // steps (SPLIT)
-    int64_t each;     // of a share; the first `more` shares have one step more
-    int more;
+    // Of at least LEAST steps: a tile in many short parts takes longer to join than the steps do.  `each` is a share's
+    // length, the first `more` have one step more.
+    static constexpr int LEAST = 6;
+    int64_t each;
+    int more, ctas;
     int u, total, per;
     __device__ Segments(const Args& g, const int* off, const int* base) : walk(g, off, base, NT) {
         total = base[g.E + 1];
@@ -65,10 +65,11 @@ struct Segments {
         u = (SPLIT ? base[g.E] : 0) + blockIdx.x;
         if (SPLIT) {
             const int64_t steps = (int64_t)base[g.E] * per;
-            each = steps < (1ll << 32) ? (uint32_t)steps / gridDim.x : steps / gridDim.x;
-            more = (int)(steps - each * gridDim.x);
-            at = share(blockIdx.x);
-            end = share(blockIdx.x + 1);
+            ctas = (int)max((int64_t)1, min((int64_t)gridDim.x, steps / LEAST));
+            each = steps < (1ll << 32) ? (uint32_t)steps / ctas : steps / ctas;
+            more = (int)(steps - each * ctas);
+            at = share(min((int)blockIdx.x, ctas));
+            end = share(min((int)blockIdx.x + 1, ctas));
         }
     }
     __device__ __forceinline__ int64_t share(int i) const { return i * each + min(i, more); }
@@ -94,7 +95,7 @@ struct Segments {
     __device__ __forceinline__ int others(const Segment& s) const {
         const int64_t last = end + per - s.s1;
         int n = 1;
-        while ((int)blockIdx.x + n + 1 < (int)gridDim.x && share(blockIdx.x + n + 1) < last) ++n;
+        while ((int)blockIdx.x + n + 1 < ctas && share(blockIdx.x + n + 1) < last) ++n;
         return n;
     }
 };
@@ -301,22 +302,22 @@ __global__ void __launch_bounds__(512) join_kernel(const Args g) {
     pdl_trigger();
     const int4 t = g.joins[blockIdx.x];  // first lane, first row, rows, CTAs that go on
     const int l = threadIdx.x & 127;
-    constexpr int U = 4;
-    for (int c0 = (threadIdx.x >> 7) * U; c0 < t.z; c0 += 4 * U) {
-        float sum[U];
+    constexpr int U = 4;  // columns of a thread; the grid's y has 16 of a tile each
+    const int c0 = blockIdx.y * 4 * U + (threadIdx.x >> 7) * U;
+    if (c0 >= t.z) return;
+    float sum[U];
 #pragma unroll
-        for (int j = 0; j < U; ++j) sum[j] = 0.f;
+    for (int j = 0; j < U; ++j) sum[j] = 0.f;
 #pragma unroll 4
-        for (int q = 0; q <= t.w; ++q) {
-            const float* from = g.parts + (((int64_t)(blockIdx.x + q) * 2 + (q == 0)) * NT + c0) * 128 + l;
-#pragma unroll
-            for (int j = 0; j < U; ++j)
-                if (c0 + j < t.z) sum[j] += from[j * 128];
-        }
+    for (int q = 0; q <= t.w; ++q) {
+        const float* from = g.parts + (((int64_t)(blockIdx.x + q) * 2 + (q == 0)) * NT + c0) * 128 + l;
 #pragma unroll
         for (int j = 0; j < U; ++j)
-            if (c0 + j < t.z && t.x + l < g.lanes) put_value(g.out, g.ctype, (int64_t)(t.y + c0 + j) * g.ld + t.x + l, sum[j]);
+            if (c0 + j < t.z) sum[j] += from[j * 128];
     }
+#pragma unroll
+    for (int j = 0; j < U; ++j)
+        if (c0 + j < t.z && t.x + l < g.lanes) put_value(g.out, g.ctype, (int64_t)(t.y + c0 + j) * g.ld + t.x + l, sum[j]);
 }
 
 // Rows of 16-bit values laid out for TMA: rows that start off the 16-byte
@@ -331,6 +332,7 @@ struct RowCopy {
     int cols;
     uint16_t* to;
     int64_t ldt;
+    const int32_t* offsets;          // of the experts whose rows (inner of each) these are: those without rows are left out
 };
 __device__ __forceinline__ uint4 shifted(uint4 v, uint4 w, int words, bool half) {
     uint32_t a, b, c, d, e;
@@ -354,7 +356,9 @@ __global__ void __launch_bounds__(256) copy_rows_kernel(const RowCopy c) {
             const int p = c.pairs[r], t = p >= 0 ? p / c.k : c.x_rows;
             from = t < c.x_rows ? c.x + t * c.ld : nullptr;
         } else {
-            from = c.x + r / c.inner * c.outer + r % c.inner * c.ld;
+            const int64_t e = r / c.inner;
+            if (c.offsets && c.offsets[e + 1] <= c.offsets[e]) continue;
+            from = c.x + e * c.outer + (r - e * c.inner) * c.ld;
         }
         uint16_t* const to = c.to + r * c.ldt;
         const int pieces = (c.cols + 7) / 8;
@@ -396,12 +400,13 @@ __global__ void __launch_bounds__(256) copy_rows_kernel(const RowCopy c) {
 
 inline size_t padded(int64_t rows, int64_t cols) { return ((size_t)rows * (size_t)((cols + 7) / 8 * 8) * 2 + 255) / 256 * 256; }
 // Copies m (or its rows in the order of pairs) into the workspace.
-static int copy_rows(Mat& m, const int32_t* pairs, int64_t P, int k, uint8_t*& ws, size_t& left, cudaStream_t st) {
+static int copy_rows(Mat& m, const int32_t* pairs, int64_t P, int k, const int32_t* offsets, uint8_t*& ws, size_t& left,
+                     cudaStream_t st) {
     const int64_t rows = pairs ? P : m.rows * m.experts, ld = (m.cols + 7) / 8 * 8;
     const size_t need = padded(rows, m.cols);
     if (need > left) return QMOE_ERR_ARG;
     const RowCopy c = {static_cast<const uint16_t*>(m.p), rows, m.rows, m.ld, m.stride, pairs, k, (int)(pairs ? m.rows : 0),
-                       (int)m.cols, reinterpret_cast<uint16_t*>(ws), ld};
+                       (int)m.cols, reinterpret_cast<uint16_t*>(ws), ld, offsets};
     const int64_t grid = (rows + 7) / 8, most = 32 * row::kSMs;
     const int rc = launch_pdl(copy_rows_kernel, dim3((unsigned)(grid < most ? grid : most)), dim3(256), 0, st, c);
     m.p = ws;
@@ -413,8 +418,8 @@ static int copy_rows(Mat& m, const int32_t* pairs, int64_t P, int k, uint8_t*& w
     return rc;
 }
 inline size_t copy_need(const Mat& m) { return fits(m) ? 0 : padded(m.rows * m.experts, m.cols); }
-static int as_tma(Mat& m, uint8_t*& ws, size_t& left, cudaStream_t st) {
-    if (!fits(m)) return copy_rows(m, nullptr, 0, 0, ws, left, st);
+static int as_tma(Mat& m, const int32_t* offsets, uint8_t*& ws, size_t& left, cudaStream_t st) {
+    if (!fits(m)) return copy_rows(m, nullptr, 0, 0, offsets, ws, left, st);
     if (m.ld % 8) m.ld = (m.cols + 7) / 8 * 8;  // a single row: the stride is not used
     return QMOE_OK;
 }
@@ -443,7 +448,7 @@ static int launch_as(const CUtensorMap& mp, const CUtensorMap& mq, const Args& g
     const int64_t grid = SPLIT || most > row::kSMs ? row::kSMs : most;
     rc = launch_pdl(kernel, dim3((unsigned)grid), dim3(threads_of(GATHER)), (size_t)C::SMEM, st, mp, mq, g);
     if (rc != QMOE_OK || !SPLIT) return rc;
-    return launch_pdl(join_kernel<NT>, dim3((unsigned)grid), dim3(512), 0, st, g);
+    return launch_pdl(join_kernel<NT>, dim3((unsigned)grid, NT / 16), dim3(512), 0, st, g);
 }
 
 // Few rows for each expert: narrow tiles, whose stages are almost all weight, so that more of them are in flight.
@@ -472,12 +477,22 @@ inline bool split(int64_t P, int E, int64_t lanes, int64_t red, int nt) {
     if (tiles > 2 * row::kSMs) return false;  // measured no faster, up to a fifth slower, with more
     const float busy = tiles < row::kSMs ? (float)tiles / row::kSMs : 1.f;
     const float whole = (float)((tiles + row::kSMs - 1) / row::kSMs) * per * (0.39f * busy > 0.25f ? 0.39f * busy : 0.25f);
-    return (float)tiles * per / row::kSMs * 0.39f + 2.5f < whole;
+    const float ctas = (float)(tiles * per / 6 < row::kSMs ? tiles * per / 6 + 1 : row::kSMs);
+    const float share = (float)tiles * per / ctas;
+    return share * (0.39f * ctas / row::kSMs > 0.25f ? 0.39f * ctas / row::kSMs : 0.25f) + 2.5f < whole;
 }
 inline size_t part_bytes(int nt) { return (size_t)row::kSMs * 2 * nt * 128 * 4 + (row::kSMs * 16 + 255) / 256 * 256; }
 
-// So few rows that the weights pass through once or twice.
-inline bool few(int64_t P, int E, bool fit) { return P <= (fit ? FEW_MOST : 4) * (int64_t)E && P <= 65535; }
+// Whether y is better made by expert_few_kernel: for weights off the 16-byte
+// boundaries, where its CTAs (8.5 ns each, or the time of their 16 rows of w at 2.3
+// TB/s) take less than a copy of the weights.  One token x 8 of 128 experts, 2047 ->
+// 1536: 22 us against 255; 141 x 7 of 256, 1095 -> 1408: 905 against 400.
+inline bool few(int64_t P, int E, int64_t N, int64_t K, bool fit) {
+    if (fit || P > 65535) return false;
+    const double cta = K * 32 / 2.3e6 > 0.0085 ? K * 32 / 2.3e6 : 0.0085;
+    const double copied = (double)(P < E ? P : E) * N * K * 4 / 6e6;
+    return (double)P * ((N + 15) / 16) * cta < copied + 4;
+}
 
 template <int MODE, bool GATHER>
 static int run_rows(Mat w, Mat q, Args& g, int dtype, uint8_t* ws, size_t left, cudaStream_t st) {
@@ -565,12 +580,12 @@ extern "C" int qmoe_expert_linear(int64_t P, int E, int64_t N, int64_t K, int dt
     eg::Args g = {(int)P, E, (int)N, 0, (int)K, offsets, pairs, k, (int)mx.rows, y, ldy, 0, y_dtype,
                   aligned16(y) && ldy * size % 16 == 0,
                   dtype == QMOE_BF16 ? tc::idesc_bf16_f32(0, 0) : tc::idesc_f16_f32(0, 0), dev_status, nullptr, nullptr};
-    if (eg::few(P, E, eg::fits(mw))) return eg::launch_few(mw, mx, g, dtype, st);
+    if (eg::few(P, E, N, K, eg::fits(mw))) return eg::launch_few(mw, mx, g, dtype, st);
     const bool lay_out = pairs && eg::tile_of(P, E) == 256;
     const size_t need = qmoe_expert_workspace_bytes(P, E, N, K, eg::FWD, pairs != nullptr);
     if (left < need + eg::copy_need(mw) + (lay_out ? 0 : eg::copy_need(mx))) return QMOE_ERR_ARG;
-    if ((rc = eg::as_tma(mw, at, left, st)) != QMOE_OK) return rc;
-    rc = lay_out ? eg::copy_rows(mx, pairs, P, k, at, left, st) : eg::as_tma(mx, at, left, st);
+    if ((rc = eg::as_tma(mw, offsets, at, left, st)) != QMOE_OK) return rc;
+    rc = lay_out ? eg::copy_rows(mx, pairs, P, k, nullptr, at, left, st) : eg::as_tma(mx, nullptr, at, left, st);
     if (rc != QMOE_OK) return rc;
     if (lay_out) g.pairs = nullptr;
     return g.pairs ? eg::run_rows<eg::FWD, true>(mw, mx, g, dtype, at, left, st)
@@ -594,7 +609,7 @@ extern "C" int qmoe_expert_linear_dx(int64_t P, int E, int64_t N, int64_t K, int
     uint8_t* at = static_cast<uint8_t*>(ws);
     size_t left = ws && !(reinterpret_cast<uintptr_t>(ws) & 255u) ? ws_bytes : 0;
     if (left < qmoe_expert_workspace_bytes(P, E, N, K, eg::DX, 0) + eg::copy_need(mw) + eg::copy_need(my)) return QMOE_ERR_ARG;
-    if ((rc = eg::as_tma(mw, at, left, st)) != QMOE_OK || (rc = eg::as_tma(my, at, left, st)) != QMOE_OK) return rc;
+    if ((rc = eg::as_tma(mw, offsets, at, left, st)) != QMOE_OK || (rc = eg::as_tma(my, nullptr, at, left, st)) != QMOE_OK) return rc;
     const int size = row::dtype_size(dx_dtype);
     eg::Args g = {(int)P, E, (int)K, 0, (int)N, offsets, nullptr, 0, (int)P, dx, lddx, 0, dx_dtype,
                   aligned16(dx) && lddx * size % 16 == 0,
@@ -624,8 +639,8 @@ extern "C" int qmoe_expert_linear_dw(int64_t P, int E, int64_t N, int64_t K, int
     uint8_t* at = static_cast<uint8_t*>(ws);
     size_t left = ws && !(reinterpret_cast<uintptr_t>(ws) & 255u) ? ws_bytes : 0;
     if (left < (pairs ? eg::padded(P, K) : eg::copy_need(mx)) + eg::copy_need(my)) return QMOE_ERR_ARG;
-    if ((rc = eg::as_tma(my, at, left, st)) != QMOE_OK) return rc;
-    rc = pairs ? eg::copy_rows(mx, pairs, P, k, at, left, st) : eg::as_tma(mx, at, left, st);
+    if ((rc = eg::as_tma(my, nullptr, at, left, st)) != QMOE_OK) return rc;
+    rc = pairs ? eg::copy_rows(mx, pairs, P, k, nullptr, at, left, st) : eg::as_tma(mx, nullptr, at, left, st);
     if (rc != QMOE_OK) return rc;
     eg::Args g = {(int)P, E, (int)N, (int)K, 0, offsets, nullptr, 0, (int)mx.rows, dw, K, N * K, dw_dtype,
                   aligned16(dw) && K * size % 16 == 0,
