@@ -236,6 +236,7 @@ expert_gemm_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_const
     } else {
         const int quad = warp & 3, half = warp >> 2;
         int4 join = make_int4(0, 0, 0, 0);
+        const bool matrices = by_matrices<MODE>(g);
         uint8_t* const stage = smem + C::OUT_OFF + warp * STAGE_OUT;
         int buf = 0;
         uint32_t acc_phase = 0;
@@ -248,32 +249,29 @@ expert_gemm_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_const
             }
             for (int c = half * 32; c < t.n; c += 64) {
                 uint32_t r[32];
+                const bool part = SPLIT && seg.part >= 0;
                 if (seg.s1 > 0) {
                     const uint32_t from = tm + ((uint32_t)(quad * 32) << 16) + buf * TURNS * NT + c;
-                    tmem_ld32(from, r);
+                    take<MODE>(matrices && !part, from, r);
                     tc::tmem_ld_wait();
                     if (seg.s1 - seg.s0 > 1) {
+                        uint32_t y[32];
+                        take<MODE>(matrices && !part, from + NT, y);
+                        tc::tmem_ld_wait();
 #pragma unroll
-                        for (int h = 0; h < 32; h += 16) {
-                            uint32_t y[16];
-                            tc::tmem_ld_32x32b_x16(from + NT + h, y);
-                            tc::tmem_ld_wait();
-#pragma unroll
-                            for (int j = 0; j < 16; ++j)
-                                r[h + j] = __float_as_uint(__uint_as_float(r[h + j]) + __uint_as_float(y[j]));
-                        }
+                        for (int j = 0; j < 32; ++j) r[j] = __float_as_uint(__uint_as_float(r[j]) + __uint_as_float(y[j]));
                     }
                 } else {
 #pragma unroll
                     for (int j = 0; j < 32; ++j) r[j] = 0;
                 }
-                if (SPLIT && seg.part >= 0) {
+                if (part) {
                     float* to = g.parts + (((int64_t)blockIdx.x * 2 + seg.part) * NT + c) * 128 + quad * 32 + lane;
 #pragma unroll
                     for (int j = 0; j < 32; ++j)
                         if (c + j < t.n) to[j * 128] = __uint_as_float(r[j]);
                 } else {
-                    put<MODE>(g, stage, t.e, l0, t.q0 + c, t.n - c, lane, r);
+                    put<MODE>(g, matrices, stage, t.e, l0, t.q0 + c, t.n - c, lane, r);
                 }
             }
             if (seg.s1 > 0) {
@@ -321,7 +319,7 @@ __global__ void __launch_bounds__(512) join_kernel(const Args g) {
 }
 
 // Rows of 16-bit values laid out for TMA: rows that start off the 16-byte
-// boundaries, and rows of x in expert order.  A warp takes a row; a lane loads
+// boundaries, and rows of x in expert order.  Up to a warp takes a row; a lane loads
 // aligned pieces of 16 bytes, only such as hold values of the row, and takes what
 // lies in the next piece from its neighbour.
 struct RowCopy {
@@ -345,52 +343,55 @@ __device__ __forceinline__ uint4 shifted(uint4 v, uint4 w, int words, bool half)
     if (!half) return make_uint4(a, b, c, d);
     return make_uint4(__byte_perm(a, b, 0x5432), __byte_perm(b, c, 0x5432), __byte_perm(c, d, 0x5432), __byte_perm(d, e, 0x5432));
 }
+template <int LANES>  // that take a row
 __global__ void __launch_bounds__(256) copy_rows_kernel(const RowCopy c) {
     pdl_wait();
     pdl_trigger();
-    const int lane = threadIdx.x & 31;
-    constexpr int U = 4;  // pieces of a lane on their way
-    for (int64_t r = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5); r < c.rows; r += (int64_t)gridDim.x * 8) {
+    const int lane = threadIdx.x & (LANES - 1), first = (threadIdx.x & 31) & ~(LANES - 1);
+    const uint32_t mask = LANES == 32 ? 0xFFFFFFFFu : ((1u << LANES) - 1) << first;
+    constexpr int U = 4, ROWS = 256 / LANES;  // pieces of a lane on their way; rows of a CTA
+    for (int64_t r = (int64_t)blockIdx.x * ROWS + threadIdx.x / LANES; r < c.rows; r += (int64_t)gridDim.x * ROWS) {
         const uint16_t* from;
         if (c.pairs) {
             const int p = c.pairs[r], t = p >= 0 ? p / c.k : c.x_rows;
             from = t < c.x_rows ? c.x + t * c.ld : nullptr;
         } else {
-            const int64_t e = r / c.inner;
+            const int64_t e = c.rows < (1ll << 31) ? (uint32_t)r / (uint32_t)c.inner : r / c.inner;
             if (c.offsets && c.offsets[e + 1] <= c.offsets[e]) continue;
             from = c.x + e * c.outer + (r - e * c.inner) * c.ld;
         }
         uint16_t* const to = c.to + r * c.ldt;
         const int pieces = (c.cols + 7) / 8;
         if (!from) {
-            for (int i = lane; i < pieces; i += 32) *reinterpret_cast<uint4*>(to + i * 8) = make_uint4(0, 0, 0, 0);
+            for (int i = lane; i < pieces; i += LANES) *reinterpret_cast<uint4*>(to + i * 8) = make_uint4(0, 0, 0, 0);
             continue;
         }
         const int shift = (int)(reinterpret_cast<uintptr_t>(from) & 15);  // bytes
         const uint4* const base = reinterpret_cast<const uint4*>(reinterpret_cast<uintptr_t>(from) - shift);
         const int there = (shift + c.cols * 2 + 15) / 16;  // pieces that hold values of the row
-        for (int i0 = lane; i0 - lane < pieces; i0 += 32 * U) {
+        for (int i0 = lane; i0 - lane < pieces; i0 += LANES * U) {
             uint4 v[U + 1];
 #pragma unroll
-            for (int j = 0; j < U; ++j) v[j] = i0 + j * 32 < there ? base[i0 + j * 32] : make_uint4(0, 0, 0, 0);
+            for (int j = 0; j < U; ++j) v[j] = i0 + j * LANES < there ? base[i0 + j * LANES] : make_uint4(0, 0, 0, 0);
             if (shift) {
-                // lane 31's neighbour is lane 0's next piece
-                v[U] = lane == 0 && i0 + U * 32 < there ? base[i0 + U * 32] : make_uint4(0, 0, 0, 0);
+                // the last lane's neighbour is the first one's next piece
+                v[U] = lane == 0 && i0 + U * LANES < there ? base[i0 + U * LANES] : make_uint4(0, 0, 0, 0);
 #pragma unroll
                 for (int j = 0; j < U; ++j) {
                     const uint4 mine = lane == 0 ? v[j + 1] : v[j];  // what the lane below wants
+                    const int above = first + ((lane + 1) & (LANES - 1));
                     uint4 w;
-                    w.x = __shfl_sync(0xFFFFFFFFu, mine.x, (lane + 1) & 31);
-                    w.y = __shfl_sync(0xFFFFFFFFu, mine.y, (lane + 1) & 31);
-                    w.z = __shfl_sync(0xFFFFFFFFu, mine.z, (lane + 1) & 31);
-                    w.w = __shfl_sync(0xFFFFFFFFu, mine.w, (lane + 1) & 31);
-                    if (i0 + j * 32 < pieces)
-                        *reinterpret_cast<uint4*>(to + (i0 + j * 32) * 8) = shifted(v[j], w, shift >> 2, shift & 2);
+                    w.x = __shfl_sync(mask, mine.x, above);
+                    w.y = __shfl_sync(mask, mine.y, above);
+                    w.z = __shfl_sync(mask, mine.z, above);
+                    w.w = __shfl_sync(mask, mine.w, above);
+                    if (i0 + j * LANES < pieces)
+                        *reinterpret_cast<uint4*>(to + (i0 + j * LANES) * 8) = shifted(v[j], w, shift >> 2, shift & 2);
                 }
             } else {
 #pragma unroll
                 for (int j = 0; j < U; ++j)
-                    if (i0 + j * 32 < pieces) *reinterpret_cast<uint4*>(to + (i0 + j * 32) * 8) = v[j];
+                    if (i0 + j * LANES < pieces) *reinterpret_cast<uint4*>(to + (i0 + j * LANES) * 8) = v[j];
             }
         }
     }
@@ -407,8 +408,11 @@ static int copy_rows(Mat& m, const int32_t* pairs, int64_t P, int k, const int32
     if (need > left) return QMOE_ERR_ARG;
     const RowCopy c = {static_cast<const uint16_t*>(m.p), rows, m.rows, m.ld, m.stride, pairs, k, (int)(pairs ? m.rows : 0),
                        (int)m.cols, reinterpret_cast<uint16_t*>(ws), ld, offsets};
-    const int64_t grid = (rows + 7) / 8, most = 32 * row::kSMs;
-    const int rc = launch_pdl(copy_rows_kernel, dim3((unsigned)(grid < most ? grid : most)), dim3(256), 0, st, c);
+    // a lane for each piece of a narrow row
+    const int lanes = m.cols <= 64 ? 8 : m.cols <= 128 ? 16 : 32;
+    const int64_t grid = (rows * lanes + 255) / 256, most = 32 * row::kSMs;
+    const int rc = launch_pdl(lanes == 8 ? copy_rows_kernel<8> : lanes == 16 ? copy_rows_kernel<16> : copy_rows_kernel<32>,
+                              dim3((unsigned)(grid < most ? grid : most)), dim3(256), 0, st, c);
     m.p = ws;
     m.ld = ld;
     m.stride = ld * m.rows;

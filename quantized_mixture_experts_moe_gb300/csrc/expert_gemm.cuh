@@ -212,42 +212,60 @@ __device__ __forceinline__ void check_offsets(const Args& g) {
     if (bad) atomicOr(g.status, QMOE_DEV_BAD_OFFSETS);
 }
 
-template <typename T> struct Bits;
-template <> struct Bits<__nv_bfloat16> {
-    static __device__ __forceinline__ uint16_t of(float v) { return __bfloat16_as_ushort(__float2bfloat16_rn(v)); }
-};
-template <> struct Bits<__half> {
-    static __device__ __forceinline__ uint16_t of(float v) { return __half_as_ushort(__float2half_rn(v)); }
-};
+// 32 columns of this warp's 32 lanes as 8 x 8 matrices: lane t holds of lanes
+// 8 m + t / 4 the columns 8 i + 2 (t % 4) and the next, for m = 0, 1 in r[4 i ..],
+// for m = 2, 3 in r[16 + 4 i ..].
+__device__ __forceinline__ void tmem_ld_matrices(uint32_t taddr, uint32_t (&r)[32]) {
+#pragma unroll
+    for (int h = 0; h < 32; h += 16)
+        asm volatile(
+            "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+            : "=r"(r[h]), "=r"(r[h + 1]), "=r"(r[h + 2]), "=r"(r[h + 3]), "=r"(r[h + 4]), "=r"(r[h + 5]), "=r"(r[h + 6]),
+              "=r"(r[h + 7]), "=r"(r[h + 8]), "=r"(r[h + 9]), "=r"(r[h + 10]), "=r"(r[h + 11]), "=r"(r[h + 12]), "=r"(r[h + 13]),
+              "=r"(r[h + 14]), "=r"(r[h + 15])
+            : "r"(taddr + ((uint32_t)h << 16)));
+}
+// 32 columns of y or dx in 16 bits, from matrices: transposed on their way to shared
+// memory, so that a column (a row of y) lies there as it is stored.
+template <typename T>
+__device__ __forceinline__ void put_matrices(const Args& g, uint8_t* stage, int l0, int q0, int n, int lane, const uint32_t (&r)[32]) {
+    T* const out = static_cast<T*>(g.out);
+    // 16-byte pieces of 64-byte rows, changed about so that 8 rows fall on all banks
+    auto place = [](int row, int p) { return row * 64 + ((p ^ (row >> 1 & 3)) * 16); };
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        uint32_t w[4];
+#pragma unroll
+        for (int m = 0; m < 4; ++m)
+            w[m] = row::pack2(__uint_as_float(r[(m >> 1) * 16 + 4 * i + (m & 1) * 2]),
+                              __uint_as_float(r[(m >> 1) * 16 + 4 * i + (m & 1) * 2 + 1]), T{});
+        asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(
+                         tc::smem_u32(stage + place(8 * i + (lane & 7), lane >> 3))),
+                     "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3])
+                     : "memory");
+    }
+    __syncwarp();
+    const int l = l0 + (lane & 3) * 8;
+    uint4 v[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = *reinterpret_cast<const uint4*>(stage + place(i * 8 + (lane >> 2), lane & 3));
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int row = i * 8 + (lane >> 2);
+        T* const to = out + (int64_t)(q0 + row) * g.ld + l;
+        if (row < n && l + 8 <= g.lanes) {
+            *reinterpret_cast<uint4*>(to) = v[i];
+        } else if (row < n) {
+            for (int j = 0; j < 8 && l + j < g.lanes; ++j) to[j] = reinterpret_cast<const T*>(&v[i])[j];
+        }
+    }
+    __syncwarp();
+}
 
 // 32 columns of y or dx: lane l holds output l0 + l of rows q0 .. q0 + n - 1.
 template <typename T>
-__device__ __forceinline__ void put_rows(const Args& g, uint8_t* stage, int l0, int q0, int n, int lane,
-                                         const uint32_t (&r)[32]) {
+__device__ __forceinline__ void put_rows(const Args& g, int l0, int q0, int n, int lane, const uint32_t (&r)[32]) {
     T* const out = static_cast<T*>(g.out);
-    if constexpr (sizeof(T) == 2) {
-        if (g.wide) {
-#pragma unroll
-            for (int j = 0; j < 32; ++j)
-                *reinterpret_cast<uint16_t*>(stage + j * 64 + lane * 2) = Bits<T>::of(__uint_as_float(r[j]));
-            __syncwarp();
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int row = i * 8 + (lane >> 2), l = l0 + (lane & 3) * 8;
-                const uint4 v = *reinterpret_cast<const uint4*>(stage + row * 64 + (lane & 3) * 16);
-                if (row < n && l < g.lanes) {
-                    T* const to = out + (int64_t)(q0 + row) * g.ld + l;
-                    if (l + 8 <= g.lanes) {
-                        *reinterpret_cast<uint4*>(to) = v;
-                    } else {
-                        for (int j = 0; j < 8 && l + j < g.lanes; ++j) to[j] = reinterpret_cast<const T*>(&v)[j];
-                    }
-                }
-            }
-            __syncwarp();
-            return;
-        }
-    }
     if (l0 + lane < g.lanes) {
         T* to = out + (int64_t)q0 * g.ld + l0 + lane;
 #pragma unroll
@@ -301,26 +319,46 @@ __device__ __forceinline__ void put_dw(const Args& g, uint8_t* stage, int e, int
             }
         }
     } else {
-#pragma unroll 8
-        for (int row = 0; row < ROWS; ++row) {
-            const T v = reinterpret_cast<const T*>(stage + place(row, lane / PER))[lane % PER];
-            if (l0 + row < g.lanes && lane < n) out[(int64_t)(l0 + row) * g.ld + q0 + lane] = v;
+        T* to = out + (int64_t)l0 * g.ld + q0 + lane;
+        const int rows = lane < n ? min(ROWS, g.lanes - l0) : 0;
+#pragma unroll
+        for (int r0 = 0; r0 < ROWS; r0 += 16) {  // all reads of shared memory, then all stores
+            T v[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) v[i] = reinterpret_cast<const T*>(stage + place(r0 + i, lane / PER))[lane % PER];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                if (r0 + i < rows) *to = v[i];
+                to += g.ld;
+            }
         }
     }
     __syncwarp();
 }
 
+// Whether a warp takes its sums from TMEM as matrices.
 template <int MODE>
-__device__ __forceinline__ void put(const Args& g, uint8_t* stage, int e, int l0, int q0, int n, int lane,
+__device__ __forceinline__ bool by_matrices(const Args& g) { return MODE != DW && g.wide && g.ctype != QMOE_F32; }
+
+template <int MODE>
+__device__ __forceinline__ void take(bool matrices, uint32_t taddr, uint32_t (&r)[32]) {
+    if (MODE != DW && matrices) tmem_ld_matrices(taddr, r);
+    else tmem_ld32(taddr, r);
+}
+template <int MODE>
+__device__ __forceinline__ void put(const Args& g, bool matrices, uint8_t* stage, int e, int l0, int q0, int n, int lane,
                                     const uint32_t (&r)[32]) {
     if constexpr (MODE == DW) {
         if (g.ctype == QMOE_F32) put_dw<float>(g, stage, e, l0, q0, n, lane, r);
         else if (g.ctype == QMOE_BF16) put_dw<__nv_bfloat16>(g, stage, e, l0, q0, n, lane, r);
         else put_dw<__half>(g, stage, e, l0, q0, n, lane, r);
+    } else if (matrices) {
+        if (g.ctype == QMOE_BF16) put_matrices<__nv_bfloat16>(g, stage, l0, q0, n, lane, r);
+        else put_matrices<__half>(g, stage, l0, q0, n, lane, r);
     } else {
-        if (g.ctype == QMOE_F32) put_rows<float>(g, stage, l0, q0, n, lane, r);
-        else if (g.ctype == QMOE_BF16) put_rows<__nv_bfloat16>(g, stage, l0, q0, n, lane, r);
-        else put_rows<__half>(g, stage, l0, q0, n, lane, r);
+        if (g.ctype == QMOE_F32) put_rows<float>(g, l0, q0, n, lane, r);
+        else if (g.ctype == QMOE_BF16) put_rows<__nv_bfloat16>(g, l0, q0, n, lane, r);
+        else put_rows<__half>(g, l0, q0, n, lane, r);
     }
 }
 

@@ -276,6 +276,7 @@ expert_pair_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_const
     } else {
         const int quad = warp & 3, half = warp >> 2;
         uint8_t* const stage = smem + C::OUT_OFF + warp * C::OUT;
+        const bool matrices = by_matrices<MODE>(g);
         int buf = 0;
         uint32_t acc_phase = 0;
         for (int u = first; u < total && !*abort_flag; u += stride) {
@@ -285,7 +286,7 @@ expert_pair_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_const
                 uint32_t r[32];
 #pragma unroll
                 for (int j = 0; j < 32; ++j) r[j] = 0;
-                for (int c = half * 32; c < t.n; c += 64) put<MODE>(g, stage, t.e, l0, t.q0 + c, t.n - c, lane, r);
+                for (int c = half * 32; c < t.n; c += 64) put<MODE>(g, matrices, stage, t.e, l0, t.q0 + c, t.n - c, lane, r);
                 continue;
             }
             if (!warp_wait(&acc_full[buf], acc_phase, abort_flag, g.status)) break;
@@ -303,7 +304,7 @@ expert_pair_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_const
                     tc::tmem_ld_wait();
 #pragma unroll
                     for (int j = 0; j < 32; ++j) x[j] = __float_as_uint(__uint_as_float(x[j]) + __uint_as_float(y[j]));
-                    put<MODE>(g, stage, t.e, l0, t.q0 + c, t.n - c, lane, x);
+                    put<MODE>(g, matrices, stage, t.e, l0, t.q0 + c, t.n - c, lane, x);
                 }
                 tc::tc_fence_before();
                 __syncwarp();
@@ -317,17 +318,17 @@ expert_pair_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_const
             // the next 32 columns are on their way while these are stored; the sums are let go when the last have come
             uint32_t r[2][32];
             int at = half * 32;
-            if (at < t.n) tmem_ld32(from + at, r[0]);
+            if (at < t.n) take<MODE>(matrices, from + at, r[0]);
             auto turn = [&](uint32_t (&now)[32], uint32_t (&next)[32]) {
                 tc::tmem_ld_wait();
                 if (at + 64 < t.n) {
-                    tmem_ld32(from + at + 64, next);
+                    take<MODE>(matrices, from + at + 64, next);
                 } else {
                     tc::tc_fence_before();
                     __syncwarp();
                     if (lane == 0) arrive_first(&acc_empty[buf]);
                 }
-                put<MODE>(g, stage, t.e, l0, t.q0 + at, t.n - at, lane, now);
+                put<MODE>(g, matrices, stage, t.e, l0, t.q0 + at, t.n - at, lane, now);
                 at += 64;
             };
             if (at >= t.n && lane == 0) arrive_first(&acc_empty[buf]);  // no columns for this warp
