@@ -38,7 +38,7 @@ constexpr int WARPS = 8, THREADS = (WARPS + 1) * 32;  // of products, and one th
 constexpr int ROWS = 16;          // of W, of a warp
 constexpr int BLOCK = 256;        // values of a row in a stage (128 bytes)
 constexpr int STAGE = ROWS * 128, DEPTH = 4;
-constexpr int MOST_PAIRS = 256;   // of a CTA's run
+constexpr int MOST_PAIRS = 256;   // that are put in expert order, or of a CTA's run
 
 struct Args {
     int T, k, E, N, K;
@@ -55,7 +55,9 @@ struct Args {
     int tiles;   // of a matrix, of ROWS * WARPS / kw rows
     int units;   // tiles of all pairs
     int kw_log;  // warps that share a reduction
-    int pairs;   // scales of two neighbouring groups can be read at once
+    int two;     // scales of two neighbouring groups can be read at once
+    int pairs;   // rows of y with ids, 0: without
+    int share;   // most tokens that share a tile: pairs of one expert (1: each by itself)
     int32_t* status;
 };
 
@@ -119,12 +121,12 @@ __device__ __forceinline__ void put(void* y, int type, int64_t at, float v) {
 // different halves of the banks.
 __host__ __device__ constexpr int pitch_of(int chunk) { return chunk * 2 + 64; }
 // Shared memory: rings, then x, a number for each 32 values of a token, the sums
-// of the warps (two tiles' for up to 8 tokens), and the experts of the run.
+// of the warps (two tiles' for up to 8 tokens), and the sets of pairs.
 constexpr int RING = WARPS * DEPTH * STAGE;
+constexpr int LISTS = (3 * MOST_PAIRS + 16) * 4;  // sets of pairs, and their pairs
 __host__ __device__ constexpr int bufs_of(int nt) { return nt == 1 ? 2 : 1; }
 inline int smem_of(int tokens, int chunk, int nt) {
-    return 1024 + RING + tokens * pitch_of(chunk) + chunk / 32 * 8 * nt * 4 + bufs_of(nt) * WARPS * nt * 8 * ROWS * 4 +
-           MOST_PAIRS * 4;
+    return 1024 + RING + tokens * pitch_of(chunk) + chunk / 32 * 8 * nt * 4 + bufs_of(nt) * WARPS * nt * 8 * ROWS * 4 + LISTS;
 }
 
 // Whether a phase is over, without waiting for it.
@@ -140,16 +142,16 @@ __device__ __forceinline__ bool is_over(uint64_t* bar, uint32_t parity) {
 // A barrier of the warps of products.
 __device__ __forceinline__ void products_sync() { asm volatile("bar.sync 1, %0;" ::"n"(WARPS * 32) : "memory"); }
 
-// x of tokens t0 .. in [c0, c0 + len), zeros up to whole blocks; and for each 32
+// x of a set's tokens (without ids of all) in [c0, c0 + len), zeros up to whole blocks; and for each 32
 // values of a token -24 times their sum (int4), or the power of two that they were
 // divided by (E2M1).
 template <typename T, int FORMAT, int NT, int GC>
-__device__ __forceinline__ void stage_x(const Args& g, uint8_t* xs, float* sums, int pitch, int64_t t0, int tokens, int c0, int len) {
+__device__ __forceinline__ void stage_x(const Args& g, uint8_t* xs, float* sums, int pitch, const int* pairs, int tokens, int c0, int len) {
     for (int i = threadIdx.x; i < tokens * (len / 8); i += WARPS * 32) {
         const int t = i / (len / 8), k = (i - t * (len / 8)) * 8;
         uint4 v = make_uint4(0, 0, 0, 0);
         if (c0 + k < g.K) {
-            const T* from = static_cast<const T*>(g.x) + (t0 + t) * g.ldx + c0 + k;
+            const T* from = static_cast<const T*>(g.x) + (int64_t)(pairs ? pairs[t] / g.k : t) * g.ldx + c0 + k;
             if (g.x_wide) {
                 v = *reinterpret_cast<const uint4*>(from);
             } else {
@@ -198,13 +200,12 @@ __global__ void __launch_bounds__(THREADS, NT == 1 ? 2 : 1) w4_few_kernel(const 
     const int kw = 1 << g.kw_log, part = warp & (kw - 1), rows = ROWS * (WARPS >> g.kw_log);
     const int first_row = (warp >> g.kw_log) * ROWS;  // of this warp in a tile
     uint8_t* const xs = smem + RING;
-    const int tokens = g.ids ? 1 : g.T, pitch = pitch_of(g.chunk);
-    float* const sums = reinterpret_cast<float*>(xs + tokens * pitch);  // [groups of 32 in a chunk][8 NT], with GC [token][groups]
-    float* const parts = sums + g.chunk / 32 * 8 * NT;                  // [bufs][WARPS][8 NT][ROWS]
+    const int most = g.pairs ? g.share : g.T, pitch = pitch_of(g.chunk);  // tokens of a tile
+    float* const sums = reinterpret_cast<float*>(xs + most * pitch);  // [groups of 32 in a chunk][8 NT], with GC [token][groups]
+    float* const parts = sums + g.chunk / 32 * 8 * NT;                // [bufs][WARPS][8 NT][ROWS]
+    // sets of pairs of one expert: the expert (-1: none), the first of its pairs in `order`; order: the pairs
     int* const experts = reinterpret_cast<int*>(parts + bufs_of(NT) * WARPS * NT * 8 * ROWS);
-    // this CTA's run
-    const int u0 = (int)((int64_t)g.units * blockIdx.x / gridDim.x), u1 = (int)((int64_t)g.units * (blockIdx.x + 1) / gridDim.x);
-    const int p0 = u0 / g.tiles;
+    int *const starts = experts + MOST_PAIRS, *const order = starts + MOST_PAIRS + 1, *const marks = order + MOST_PAIRS;
     const int blocks = (g.K + BLOCK - 1) / BLOCK, mine = (blocks - part + kw - 1) >> g.kw_log;  // of a tile, of this warp
 
     if (threadIdx.x == 0) tc::prefetch_tensormap(&map);
@@ -213,20 +214,70 @@ __global__ void __launch_bounds__(THREADS, NT == 1 ? 2 : 1) w4_few_kernel(const 
         tc::mbar_init(&bars[threadIdx.x], 1);
         tc::fence_barrier_init();
     }
-    if (g.ids) {
+    int units = g.tiles, p0 = 0;  // of all sets; the first set that is listed
+    if (g.pairs && g.share > 1) {
+        // The pairs in expert order, those of no expert last, cut into sets of `share`: by every CTA for itself.
+        const int p = threadIdx.x;
+        auto key = [&](int e) { return e >= 0 && e < g.E ? e : g.E; };
+        int e = g.E;
+        if (p < g.pairs) experts[p] = e = key(g.ids[p]);
+        __syncthreads();
+        int rank = 0, less = 0;  // pairs before this one, pairs of experts before its
+        if (p < g.pairs)
+            for (int q = 0; q < g.pairs; ++q) {
+                const int f = experts[q];
+                less += f < e;
+                rank += f < e || (f == e && q < p);
+            }
+        __syncthreads();
+        if (p < g.pairs) {
+            order[rank] = p;
+            experts[rank] = e;
+        }
+        if (p < 9) marks[p] = 0;
+        // where a set starts, by its place in the order: bits of words of 32
+        __syncthreads();
+        if (p < g.pairs && (rank - less) % g.share == 0) atomicOr(&marks[rank >> 5], 1 << (rank & 31));
+        __syncthreads();
+        int sets = 0, before = 0, sorted = g.E;
+        const bool first_of = p < g.pairs && (marks[p >> 5] >> (p & 31) & 1);
+        if (p < g.pairs) sorted = experts[p];
+        for (int w = 0; w * 32 < g.pairs; ++w) {
+            const int n = __popc(marks[w]);
+            if (w < (p >> 5)) before += n;
+            sets += n;
+        }
+        if (p < g.pairs) before += __popc(marks[p >> 5] & ((1 << (p & 31)) - 1));
+        __syncthreads();
+        if (first_of) {
+            starts[before] = p;
+            experts[before] = sorted < g.E ? sorted : -1;
+        }
+        if (p == 0) starts[sets] = g.pairs;
+        units = sets * g.tiles;
+    } else if (g.pairs) {
+        units = g.units;
+    }
+    // this CTA's run
+    const int u0 = (int)((int64_t)units * blockIdx.x / gridDim.x), u1 = (int)((int64_t)units * (blockIdx.x + 1) / gridDim.x);
+    if (g.pairs && g.share == 1 && u0 < u1) {
+        p0 = u0 / g.tiles;
         const int n = (u1 - 1) / g.tiles - p0 + 1;
         for (int i = threadIdx.x; i < n; i += THREADS) {
             const int e = g.ids[p0 + i];
             experts[i] = e >= 0 && e < g.E ? e : -1;
+            starts[i] = i;
+            order[i] = p0 + i;
+            if (i == n - 1) starts[n] = n;
         }
     }
     __syncthreads();
     pdl_trigger();
-    // a place in the run: unit, pair, tile and the pair's expert (-1: none)
+    // a place in the run: unit, set, tile and the set's expert (-1: none)
     struct Place {
         int u, pair, tile, e;
     };
-    auto look = [&](Place& p) { p.e = p.u < u1 ? (g.ids ? experts[p.pair - p0] : 0) : -1; };
+    auto look = [&](Place& p) { p.e = p.u < u1 ? (g.pairs ? experts[p.pair - p0] : 0) : -1; };
     auto step = [&](Place& p) {
         ++p.u;
         if (++p.tile == g.tiles) {
@@ -240,7 +291,7 @@ __global__ void __launch_bounds__(THREADS, NT == 1 ? 2 : 1) w4_few_kernel(const 
     auto settle = [&](Place& p) {  // at p or the next unit of an expert
         while (p.e < 0 && p.u < u1) step(p);
     };
-    Place start = {u0, p0, u0 - p0 * g.tiles, 0};
+    Place start = {u0, u0 / g.tiles, u0 % g.tiles, 0};
     look(start);
     if (warp == WARPS) {
         // lane i sends for warp i: block j of its part of unit `at`
@@ -299,7 +350,7 @@ __global__ void __launch_bounds__(THREADS, NT == 1 ? 2 : 1) w4_few_kernel(const 
     auto fetch = [&]() {
         if (later.e < 0) return;
         const int b = part + later_j * kw;
-        if (g.pairs && (b + 1) * BLOCK <= g.K) {  // both in one word
+        if (g.two && (b + 1) * BLOCK <= g.K) {  // both in one word
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 const Two* const from = reinterpret_cast<const Two*>(at_row[h] + b * 8 + g0);
@@ -331,15 +382,18 @@ __global__ void __launch_bounds__(THREADS, NT == 1 ? 2 : 1) w4_few_kernel(const 
     bool ok = true;
     int slot = 0, buf = 0, staged_c = -1;
     uint32_t phase = 0;
-    int64_t staged_t = -1;
+    int staged_set = -1;
     for (Place at = start; at.u < u1; step(at)) {
-        const int pair = at.pair, n0 = at.tile * rows;
+        const int n0 = at.tile * rows;
+        const int* const set = g.pairs ? order + starts[at.pair - p0] : nullptr;
+        const int tokens = g.pairs ? starts[at.pair - p0 + 1] - starts[at.pair - p0] : g.T;
+        auto row_of = [&](int t) { return (int64_t)(set ? set[t] : t) * g.ldy; };  // of y
         if (at.e < 0) {
-            for (int i = threadIdx.x; i < rows; i += WARPS * 32)
-                if (n0 + i < g.N) put(g.y, g.ytype, pair * g.ldy + n0 + i, 0.f);
+            for (int t = 0; t < tokens; ++t)
+                for (int i = threadIdx.x; i < rows; i += WARPS * 32)
+                    if (n0 + i < g.N) put(g.y, g.ytype, row_of(t) + n0 + i, 0.f);
             continue;
         }
-        const int64_t t0 = g.ids ? pair / g.k : 0;
         float acc[NT][4];
 #pragma unroll
         for (int i = 0; i < NT; ++i)
@@ -348,11 +402,11 @@ __global__ void __launch_bounds__(THREADS, NT == 1 ? 2 : 1) w4_few_kernel(const 
         int j0 = 0;
         for (int c0 = 0; c0 < g.K; c0 += g.chunk) {
             const int len = min(g.chunk, (g.K - c0 + BLOCK - 1) / BLOCK * BLOCK);
-            if (staged_c != c0 || staged_t != t0) {
+            if (staged_c != c0 || staged_set != at.pair) {
                 if (staged_c >= 0) products_sync();
-                stage_x<T, FORMAT, NT, GC>(g, xs, sums, pitch, t0, tokens, c0, len);
+                stage_x<T, FORMAT, NT, GC>(g, xs, sums, pitch, set, tokens, c0, len);
                 staged_c = c0;
-                staged_t = t0;
+                staged_set = at.pair;
                 products_sync();
             }
             for (; j0 < mine && (part + j0 * kw) * BLOCK < c0 + len; ++j0) {
@@ -471,7 +525,7 @@ __global__ void __launch_bounds__(THREADS, NT == 1 ? 2 : 1) w4_few_kernel(const 
         if (kw == 1) {  // all of them
             each([&](int t, int r, float v) {
                 const int n = n0 + first_row + r;
-                if (t < tokens && n < g.N) put(g.y, g.ytype, (g.ids ? (int64_t)pair : t) * g.ldy + n, v);
+                if (t < tokens && n < g.N) put(g.y, g.ytype, row_of(t) + n, v);
             });
             continue;
         }
@@ -484,7 +538,7 @@ __global__ void __launch_bounds__(THREADS, NT == 1 ? 2 : 1) w4_few_kernel(const 
             const float* from = parts + (buf * WARPS + (n / ROWS) * kw) * NT * 8 * ROWS + t * ROWS + n % ROWS;
             float v = 0.f;
             for (int w = 0; w < kw; ++w) v += from[w * NT * 8 * ROWS];
-            if (n0 + n < g.N) put(g.y, g.ytype, (g.ids ? (int64_t)pair : t) * g.ldy + n0 + n, v);
+            if (n0 + n < g.N) put(g.y, g.ytype, row_of(t) + n0 + n, v);
         }
         if (bufs_of(NT) == 2) buf ^= 1;
         else products_sync();
@@ -531,12 +585,12 @@ __global__ void __launch_bounds__(256) w4_widen_kernel(int64_t words, int per_ro
 constexpr int kMostSmem = 220 * 1024;
 
 template <typename T, int FORMAT, int NT, int GC>
-static int few(const CUtensorMap& map, Args& g, int64_t pairs, cudaStream_t st) {
-    const int tokens = g.ids ? 1 : g.T, blocks = (g.K + BLOCK - 1) / BLOCK;
+static int few(const CUtensorMap& map, Args& g, int64_t sets, cudaStream_t st) {
+    const int tokens = g.pairs ? g.share : g.T, blocks = (g.K + BLOCK - 1) / BLOCK;
     g.chunk = blocks * BLOCK;
     constexpr int LEAST = WARPS * BLOCK;
     static_assert(1024 + RING + 8 * NT * pitch_of(LEAST) + LEAST / 32 * 8 * NT * 4 + bufs_of(NT) * WARPS * NT * 8 * ROWS * 4 +
-                          MOST_PAIRS * 4 <= kMostSmem, "the least chunk fits");
+                          LISTS <= kMostSmem, "the least chunk fits");
     while (smem_of(tokens, g.chunk, NT) > kMostSmem) g.chunk = (g.chunk / 2 + LEAST - 1) / LEAST * LEAST;
     const int smem = smem_of(tokens, g.chunk, NT);
     const int fit = 227 * 1024 / (smem + 1024);  // 1 KB a CTA is the system's
@@ -547,7 +601,7 @@ static int few(const CUtensorMap& map, Args& g, int64_t pairs, cudaStream_t st) 
     for (g.kw_log = 0;; ++g.kw_log) {
         const int rows = ROWS * (WARPS >> g.kw_log);
         g.tiles = (g.N + rows - 1) / rows;
-        units = g.tiles * pairs;
+        units = g.tiles * sets;
         const int64_t rounds = (units + most - 1) / most;
         if (g.kw_log == most_log || units * 8 >= rounds * most * 7) break;
     }
@@ -559,12 +613,21 @@ static int few(const CUtensorMap& map, Args& g, int64_t pairs, cudaStream_t st) 
                       map, g);
 }
 template <typename T, int FORMAT>
-static int few_tokens(const CUtensorMap& map, Args& g, int64_t pairs, cudaStream_t st) {
-    const int tokens = g.ids ? 1 : g.T;
-    if (tokens <= 2) return few<T, FORMAT, 1, 4>(map, g, pairs, st);
-    if (tokens <= 4) return few<T, FORMAT, 1, 2>(map, g, pairs, st);
-    if (tokens <= 8) return few<T, FORMAT, 1, 0>(map, g, pairs, st);
-    return few<T, FORMAT, 2, 0>(map, g, pairs, st);
+static int few_tokens(const CUtensorMap& map, Args& g, cudaStream_t st) {
+    if (g.pairs > MOST_PAIRS) {
+        g.share = 1;
+        return few<T, FORMAT, 1, 4>(map, g, g.pairs, st);
+    }
+    // with ids as many tokens as the pairs of an expert are likely to be (84 pairs of 8 experts, 2816 -> 2048 int4: 90 us
+    // pair by pair)
+    const int each = g.pairs ? (g.pairs + g.E - 1) / g.E : g.T;
+    g.share = each <= 1 ? 2 : each <= 2 ? 4 : each <= 6 ? 8 : 16;
+    const int64_t sets = g.pairs ? (g.pairs < g.E ? g.pairs : g.E) : 1;  // about
+    const int tokens = g.pairs ? g.share : g.T;
+    if (tokens <= 2) return few<T, FORMAT, 1, 4>(map, g, sets, st);
+    if (tokens <= 4) return few<T, FORMAT, 1, 2>(map, g, sets, st);
+    if (tokens <= 8) return few<T, FORMAT, 1, 0>(map, g, sets, st);
+    return few<T, FORMAT, 2, 0>(map, g, sets, st);
 }
 
 inline bool format_ok(int format, int group) {
@@ -624,7 +687,7 @@ extern "C" int qmoe_w4_linear(int64_t T, int k, int E, int64_t N, int64_t K, int
     if (k <= 0 || E <= 0 || (!ids && (k != 1 || E != 1))) return QMOE_ERR_ARG;
     if (T == 0) return QMOE_OK;
     if (!w4::arrays_ok(x, ldx, K, w, s, format, y, y_dtype, dev_status) || (ids && !row::type_aligned(ids, 4))) return QMOE_ERR_ARG;
-    if (ids && (T * k > 65535 || (int64_t)E * N > w4::kMost)) return QMOE_ERR_UNSUPPORTED;
+    if (ids && (T * k > 32768 || (int64_t)E * N > w4::kMost)) return QMOE_ERR_UNSUPPORTED;
     cudaStream_t st = (cudaStream_t)stream;
     if (!ids && T > QMOE_W4_FEW) {
         if (!ws || (reinterpret_cast<uintptr_t>(ws) & 255u) || ws_bytes < qmoe_w4_workspace_bytes(T, N, K, 0)) return QMOE_ERR_ARG;
@@ -648,13 +711,13 @@ extern "C" int qmoe_w4_linear(int64_t T, int k, int E, int64_t N, int64_t K, int
         return QMOE_ERR_UNSUPPORTED;
     w4::Args g = {(int)T, k, E, (int)N, (int)K, w4::log2_of(group), x, ldx, aligned16(x) && (ldx % 8 == 0 || T == 1), s, ids, y, ldy,
                   y_dtype, 0, 0, 0, 0,
-                  group == 32 && K % 64 == 0 && row::type_aligned(s, format == QMOE_W4_INT4 ? 4 : 2), dev_status};
-    const int64_t pairs = ids ? T * k : 1;
+                  group == 32 && K % 64 == 0 && row::type_aligned(s, format == QMOE_W4_INT4 ? 4 : 2), (int)(ids ? T * k : 0), 1,
+                  dev_status};
     if (dtype == QMOE_BF16)
-        return format == QMOE_W4_INT4 ? w4::few_tokens<__nv_bfloat16, QMOE_W4_INT4>(map, g, pairs, st)
-                                      : w4::few_tokens<__nv_bfloat16, QMOE_W4_E2M1>(map, g, pairs, st);
-    return format == QMOE_W4_INT4 ? w4::few_tokens<__half, QMOE_W4_INT4>(map, g, pairs, st)
-                                  : w4::few_tokens<__half, QMOE_W4_E2M1>(map, g, pairs, st);
+        return format == QMOE_W4_INT4 ? w4::few_tokens<__nv_bfloat16, QMOE_W4_INT4>(map, g, st)
+                                      : w4::few_tokens<__nv_bfloat16, QMOE_W4_E2M1>(map, g, st);
+    return format == QMOE_W4_INT4 ? w4::few_tokens<__half, QMOE_W4_INT4>(map, g, st)
+                                  : w4::few_tokens<__half, QMOE_W4_E2M1>(map, g, st);
 }
 
 extern "C" int qmoe_w4_linear_dx(int64_t T, int64_t N, int64_t K, int format, int group, int dtype, const void* dy, int64_t lddy,

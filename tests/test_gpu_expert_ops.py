@@ -361,7 +361,8 @@ def test_w4_linear_backward_few(T, N, K):
 
 
 @pytest.mark.parametrize("format,group", FORMATS)
-@pytest.mark.parametrize("T,k,E,N,K", [(1, 8, 128, 64, 256), (4, 10, 16, 33, 640), (3, 1, 5, 16, 4352), (40, 2, 4, 20, 128)])
+@pytest.mark.parametrize("T,k,E,N,K", [(1, 8, 128, 64, 256), (4, 10, 16, 33, 640), (3, 1, 5, 16, 4352), (40, 2, 4, 20, 128), (150, 2, 3, 20, 128), (64, 4, 30, 17, 256),
+                                       (16, 8, 8, 40, 512), (33, 1, 1, 130, 1152), (5, 3, 9, 300, 384), (7, 6, 14, 24, 2304)])
 def test_w4_experts(T, k, E, N, K, format, group):
     g = gen(T + k + E + group)
     dtype = (BF16, F16)[T % 2]
