@@ -189,7 +189,7 @@ __device__ __forceinline__ void stage_x(const Args& g, uint8_t* xs, float* sums,
     if (GC && threadIdx.x < 4) *reinterpret_cast<uint4*>(xs + g.chunk * 2 + threadIdx.x * 16) = make_uint4(0, 0, 0, 0);
 }
 
-template <typename T, int FORMAT, int NT, int GC>  // NT: tiles of 8 tokens; GC 0: columns are tokens
+template <typename T, int FORMAT, int NT, int GC, bool IDS>  // NT: tiles of 8 tokens; GC 0: columns are tokens
 __global__ void __launch_bounds__(THREADS, NT == 1 ? 2 : 1) w4_few_kernel(const __grid_constant__ CUtensorMap map, const Args g) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -200,7 +200,7 @@ __global__ void __launch_bounds__(THREADS, NT == 1 ? 2 : 1) w4_few_kernel(const 
     const int kw = 1 << g.kw_log, part = warp & (kw - 1), rows = ROWS * (WARPS >> g.kw_log);
     const int first_row = (warp >> g.kw_log) * ROWS;  // of this warp in a tile
     uint8_t* const xs = smem + RING;
-    const int most = g.pairs ? g.share : g.T, pitch = pitch_of(g.chunk);  // tokens of a tile
+    const int most = IDS ? g.share : g.T, pitch = pitch_of(g.chunk);  // tokens of a tile
     float* const sums = reinterpret_cast<float*>(xs + most * pitch);  // [groups of 32 in a chunk][8 NT], with GC [token][groups]
     float* const parts = sums + g.chunk / 32 * 8 * NT;                // [bufs][WARPS][8 NT][ROWS]
     // sets of pairs of one expert: the expert (-1: none), the first of its pairs in `order`; order: the pairs
@@ -215,7 +215,7 @@ __global__ void __launch_bounds__(THREADS, NT == 1 ? 2 : 1) w4_few_kernel(const 
         tc::fence_barrier_init();
     }
     int units = g.tiles, p0 = 0;  // of all sets; the first set that is listed
-    if (g.pairs && g.share > 1) {
+    if (IDS && g.share > 1) {
         // The pairs in expert order, those of no expert last, cut into sets of `share`: by every CTA for itself.
         const int p = threadIdx.x;
         auto key = [&](int e) { return e >= 0 && e < g.E ? e : g.E; };
@@ -255,12 +255,12 @@ __global__ void __launch_bounds__(THREADS, NT == 1 ? 2 : 1) w4_few_kernel(const 
         }
         if (p == 0) starts[sets] = g.pairs;
         units = sets * g.tiles;
-    } else if (g.pairs) {
+    } else if (IDS) {
         units = g.units;
     }
     // this CTA's run
     const int u0 = (int)((int64_t)units * blockIdx.x / gridDim.x), u1 = (int)((int64_t)units * (blockIdx.x + 1) / gridDim.x);
-    if (g.pairs && g.share == 1 && u0 < u1) {
+    if (IDS && g.share == 1 && u0 < u1) {
         p0 = u0 / g.tiles;
         const int n = (u1 - 1) / g.tiles - p0 + 1;
         for (int i = threadIdx.x; i < n; i += THREADS) {
@@ -277,7 +277,7 @@ __global__ void __launch_bounds__(THREADS, NT == 1 ? 2 : 1) w4_few_kernel(const 
     struct Place {
         int u, pair, tile, e;
     };
-    auto look = [&](Place& p) { p.e = p.u < u1 ? (g.pairs ? experts[p.pair - p0] : 0) : -1; };
+    auto look = [&](Place& p) { p.e = p.u < u1 ? (IDS ? experts[p.pair - p0] : 0) : -1; };
     auto step = [&](Place& p) {
         ++p.u;
         if (++p.tile == g.tiles) {
@@ -385,8 +385,8 @@ __global__ void __launch_bounds__(THREADS, NT == 1 ? 2 : 1) w4_few_kernel(const 
     int staged_set = -1;
     for (Place at = start; at.u < u1; step(at)) {
         const int n0 = at.tile * rows;
-        const int* const set = g.pairs ? order + starts[at.pair - p0] : nullptr;
-        const int tokens = g.pairs ? starts[at.pair - p0 + 1] - starts[at.pair - p0] : g.T;
+        const int* const set = IDS ? order + starts[at.pair - p0] : nullptr;
+        const int tokens = IDS ? starts[at.pair - p0 + 1] - starts[at.pair - p0] : g.T;
         auto row_of = [&](int t) { return (int64_t)(set ? set[t] : t) * g.ldy; };  // of y
         if (at.e < 0) {
             for (int t = 0; t < tokens; ++t)
@@ -584,8 +584,8 @@ __global__ void __launch_bounds__(256) w4_widen_kernel(int64_t words, int per_ro
 
 constexpr int kMostSmem = 220 * 1024;
 
-template <typename T, int FORMAT, int NT, int GC>
-static int few(const CUtensorMap& map, Args& g, int64_t sets, cudaStream_t st) {
+template <typename T, int FORMAT, int NT, int GC, bool IDS>
+static int few_as(const CUtensorMap& map, Args& g, int64_t sets, cudaStream_t st) {
     const int tokens = g.pairs ? g.share : g.T, blocks = (g.K + BLOCK - 1) / BLOCK;
     g.chunk = blocks * BLOCK;
     constexpr int LEAST = WARPS * BLOCK;
@@ -607,11 +607,16 @@ static int few(const CUtensorMap& map, Args& g, int64_t sets, cudaStream_t st) {
     }
     if (units >= (1ll << 31)) return QMOE_ERR_UNSUPPORTED;
     g.units = (int)units;
-    const int rc = row::allow_smem<w4_few_kernel<T, FORMAT, NT, GC>>(kMostSmem);
+    const int rc = row::allow_smem<w4_few_kernel<T, FORMAT, NT, GC, IDS>>(kMostSmem);
     if (rc != QMOE_OK) return rc;
-    return launch_pdl(w4_few_kernel<T, FORMAT, NT, GC>, dim3((unsigned)(units < most ? units : most)), dim3(THREADS), (size_t)smem, st,
+    return launch_pdl(w4_few_kernel<T, FORMAT, NT, GC, IDS>, dim3((unsigned)(units < most ? units : most)), dim3(THREADS), (size_t)smem, st,
                       map, g);
 }
+template <typename T, int FORMAT, int NT, int GC>
+static int few(const CUtensorMap& map, Args& g, int64_t sets, cudaStream_t st) {
+    return g.pairs ? few_as<T, FORMAT, NT, GC, true>(map, g, sets, st) : few_as<T, FORMAT, NT, GC, false>(map, g, sets, st);
+}
+
 template <typename T, int FORMAT>
 static int few_tokens(const CUtensorMap& map, Args& g, cudaStream_t st) {
     if (g.pairs > MOST_PAIRS) {
