@@ -742,7 +742,8 @@ int qmoe_weighted_sum_backward(int64_t T, int k, int64_t P, int64_t H, int dtype
  * qmoe_w4_linear -- y[t] = W x[t], or with ids int32 [T, k] of E matrices the
  *   products of each token with its experts, y [T * k, N]:
  *   y[t k + j] = W[ids[t][j]] x[t]; a row whose id is outside [0, E) is zeros.
- *   (ids NULL: one matrix, E = k = 1.)  x [T, K] and y of type dtype (QMOE_BF16 or
+ *   (ids NULL: one matrix, E = k = 1; T * k <= 32768 with ids.)  A row of x with an
+ *   infinity or NaN gives NaN.  x [T, K] and y of type dtype (QMOE_BF16 or
  *   QMOE_F16; y_dtype may be QMOE_F32).  Codes are multiplied exactly, sums and
  *   scales are fp32, up to QMOE_W4_FEW tokens (and always with ids); above it W is
  *   widened into the workspace, rounded to dtype, for the grouped product.

@@ -11,6 +11,12 @@
 // tile was written by the async proxy or is ordered by its fence: one that
 // releases at the cluster's scope took 1100 cycles, twice what a step's products
 // take.
+//
+// What bounds it: the tensor core under the power limit (64 x 1024 rows 4096 -> 2816:
+// y 853 us, 1.77 PFLOP/s, dx 813, 1.86, against 1.97 of a library's product of one
+// matrix); for dw's 32-bit sums the stores too (64 x 512 rows, 2816 x 2048: 347 us,
+// 1.09 PFLOP/s and 5.2 TB/s).  A lone CTA with 128 x 256 tiles reached 1.36 PFLOP/s:
+// its loads, half as much again.
 #include "expert_gemm.cuh"
 
 namespace qmoe {

@@ -382,6 +382,34 @@ def test_w4_experts(T, k, E, N, K, format, group):
             close(y[p:p + 1], row @ w[e].t(), ref.w4_slack(row, w[e], s[e], K), f"pair {p}")
 
 
+@pytest.mark.parametrize("format", ["int4", "mxfp4"])
+@pytest.mark.parametrize("T,N,K", [(1, 40, 96), (4, 24, 160), (7, 33, 32), (16, 17, 288), (20, 16, 96)])
+def test_w4_linear_odd_groups(T, N, K, format):
+    """Reductions of an odd number of groups: no two scales in one word, a last block that is short."""
+    g = gen(T + K)
+    x = randn(g, T, K, dtype=BF16)
+    q, s = weights4(g, (), N, K, format, 32)
+    w = ref.codes4(q, s)
+    slack = ref.w4_slack(x.double(), w, s, K) if T <= 16 else (x.double().abs() @ w.abs().t()) * (ref.sums(K) + ROUND[BF16] * 1.01)
+    close(qb.w4_linear(dev(x), dev(q), dev(s)), x.double() @ w.t(), slack, "y")
+
+
+def test_w4_linear_special_values():
+    """Extreme scales, and NaN and infinities that stay in their token."""
+    g = gen(40)
+    x = randn(g, 3, 128, dtype=F16)
+    q, s = weights4(g, (), 20, 128, "mxfp4", 32)
+    s[0, 0], s[1, 1], s[2, :] = 0, 30, 140
+    w = ref.codes4(q, s)
+    close(qb.w4_linear(dev(x), dev(q), dev(s), out_dtype=F32), x.double() @ w.t(), ref.w4_slack(x.double(), w, s, 128), "y")
+    s[5, 2] = 255
+    x[1, 7], x[2, 100] = float("inf"), float("nan")
+    for scales in (s, (s.float() * 0 + 0.01).half()):
+        y = qb.w4_linear(dev(x), dev(q), dev(scales), out_dtype=F32).cpu()
+        assert not y[1:].isfinite().any() or scales.dtype == torch.uint8
+        assert y[2].isnan().all() and y[0].isfinite().sum() >= 19
+
+
 def test_w4_linear_strides():
     g = gen(4)
     q, s = weights4(g, (), 40, 256, "int4", 32)
