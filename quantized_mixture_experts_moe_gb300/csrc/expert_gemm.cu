@@ -45,6 +45,7 @@ struct Cfg {
     static constexpr int MISC_OFF = BAR_OFF + (2 * STAGES + 4) * 8;
     static constexpr int SMEM = MISC_OFF + 64 + 1024;
     static_assert(SMEM <= 232448 && STAGES >= 4, "shared memory per CTA");
+    static_assert(TURNS == 2 && STAGES % TURNS == 0, "a stage has one warp that loads it and one that issues its products");
 };
 
 // What a CTA works on: whole tiles in turn; or, SPLIT, its even share of the steps
@@ -192,11 +193,13 @@ expert_gemm_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_const
             const uint32_t n16 = (uint32_t)(t.n + 15) & ~15u;
             const uint32_t idesc = g.idesc | (n16 >> 3) << 17 | (128u >> 4) << 24, d = tm + (buf * TURNS + turn) * NT;
             if (lane == 0) ok = ok && lane_wait(&acc_empty[buf], acc_phase ^ 1, abort_flag, g.status);
-            // the tile's steps s0 + turn, s0 + turn + 2, ..: a sum of its own
+            // every second step, a sum of its own: by the steps' count from the first tile's on, so that a stage is always one
+            // warp's.  By turns within a tile, odd ones gave a stage to the other warp, which took a load that was two rounds
+            // behind for one that had come: the parity of a barrier does not tell them apart.
             const int last = it + seg.s1 - seg.s0;
             uint32_t more = 0;
 #pragma unroll 1
-            for (int i = it + turn; i < last; i += TURNS) {
+            for (int i = it + ((it ^ turn) & 1); i < last; i += TURNS) {
                 const int slot = i % C::STAGES;
                 if (lane == 0) ok = ok && lane_wait(&full[slot], i / C::STAGES & 1, abort_flag, g.status);
                 __syncwarp();
@@ -245,7 +248,7 @@ expert_gemm_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_const
         int4 join = make_int4(0, 0, 0, 0);
         const bool matrices = by_matrices<MODE>(g);
         uint8_t* const stage = smem + C::OUT_OFF + warp * STAGE_OUT;
-        int buf = 0;
+        int buf = 0, it = 0;
         uint32_t acc_phase = 0;
         while (!*abort_flag && segments.next(seg)) {
             const int l0 = t.l0 + quad * 32;
@@ -259,11 +262,12 @@ expert_gemm_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_const
                 const bool part = SPLIT && seg.part >= 0;
                 if (seg.s1 > 0) {
                     const uint32_t from = tm + ((uint32_t)(quad * 32) << 16) + buf * TURNS * NT + c;
-                    take<MODE>(matrices && !part, from, r);
+                    const uint32_t one = from + (it & 1) * NT;  // of the warp that has the first step
+                    take<MODE>(matrices && !part, one, r);
                     tc::tmem_ld_wait();
                     if (seg.s1 - seg.s0 > 1) {
                         uint32_t y[32];
-                        take<MODE>(matrices && !part, from + NT, y);
+                        take<MODE>(matrices && !part, from + (~it & 1) * NT, y);
                         tc::tmem_ld_wait();
 #pragma unroll
                         for (int j = 0; j < 32; ++j) r[j] = __float_as_uint(__uint_as_float(r[j]) + __uint_as_float(y[j]));
@@ -281,6 +285,7 @@ expert_gemm_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_const
                     put<MODE>(g, matrices, stage, t.e, l0, t.q0 + c, t.n - c, lane, r);
                 }
             }
+            it += seg.s1 - seg.s0;
             if (seg.s1 > 0) {
                 tc::tc_fence_before();
                 __syncwarp();

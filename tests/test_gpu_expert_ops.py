@@ -111,6 +111,28 @@ def test_expert_linear_backward(i, shape, gather):
     assert status() == 0
 
 
+@pytest.mark.parametrize("E,most,steps", [(400, 92, 13), (700, 9, 5), (700, 9, 1), (310, 40, 3), (40, 3, 7)])
+def test_expert_linear_many_odd(E, most, steps):
+    """Several tiles a CTA, each of an odd number of steps of 64: no step may be taken for the one two rounds before it."""
+    g = gen(50 + E + steps)
+    counts = torch.randint(1, most + 1, (E,), generator=g).tolist()
+    P, K, N, offsets = sum(counts), 64 * steps - 43, 64, offsets_of(counts)
+    x, dx_of = randn(g, P, K, dtype=BF16), randn(g, P, K, dtype=BF16)
+    w, wt = randn(g, E, N, K, dtype=BF16, scale=K ** -0.5), randn(g, E, K, N, dtype=BF16, scale=K ** -0.5)
+    want, back = ref.linear(x.double(), w.double(), offsets), ref.linear_dx(dx_of.double(), wt.double(), offsets)
+    args = [dev(t) for t in (x, w, dx_of, wt, offsets)]
+    held = randn(g, P, N, dtype=BF16).cuda()
+    for i in range(12):
+        y = qb.expert_linear(args[0], args[1], args[4])
+        dx, _ = qb.expert_linear_backward(args[2], held, args[3], args[4], need_dw=False)
+        if i == 0:
+            first = (y, dx)
+        assert torch.equal(y, first[0]) and torch.equal(dx, first[1])
+    close(first[0], *want, "y")
+    close(first[1], *back, "dx")
+    assert status() == 0
+
+
 @pytest.mark.parametrize("shift,pad", [(0, 8), (1, 0), (3, 5), (8, 24), (0, 1)])
 def test_expert_linear_strides(shift, pad):
     """Views: rows that start off the 16-byte boundaries, and rows with a stride."""
