@@ -282,7 +282,7 @@ expert_gemm_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_const
                     for (int j = 0; j < 32; ++j)
                         if (c + j < t.n) to[j * 128] = __uint_as_float(r[j]);
                 } else {
-                    put<MODE>(g, matrices, stage, t.e, l0, t.q0 + c, t.n - c, lane, r);
+                    put<MODE, false>(g, nullptr, matrices, stage, t.e, l0, t.q0 + c, t.n - c, lane, r);
                 }
             }
             it += seg.s1 - seg.s0;
@@ -440,16 +440,20 @@ static int as_tma(Mat& m, const int32_t* offsets, uint8_t*& ws, size_t& left, cu
     return QMOE_OK;
 }
 
-static int map_of(CUtensorMap* map, const Mat& m, int dtype, int box_cols, int box_rows, bool three) {
+// store: a box's rows have 32 values, elsewhere 128 bytes.
+static int map_of(CUtensorMap* map, const Mat& m, int dtype, int box_cols, int box_rows, bool three, bool store = false) {
     EncodeTiledFn enc = encode_tiled_fn();
     if (!enc) return QMOE_ERR_CUDA;
+    const cuuint64_t size = (cuuint64_t)row::dtype_size(dtype);
     const cuuint64_t dim[3] = {(cuuint64_t)m.cols, (cuuint64_t)m.rows, (cuuint64_t)m.experts};
-    const cuuint64_t stride[2] = {(cuuint64_t)m.ld * 2, (cuuint64_t)(m.experts > 1 ? m.stride : m.ld * m.rows) * 2};
+    const cuuint64_t stride[2] = {(cuuint64_t)m.ld * size, (cuuint64_t)(m.experts > 1 ? m.stride : m.ld * m.rows) * size};
     const cuuint32_t box[3] = {(cuuint32_t)box_cols, (cuuint32_t)box_rows, 1};
     const cuuint32_t one[3] = {1, 1, 1};
-    return enc(map, dtype == QMOE_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
-               three ? 3 : 2, const_cast<void*>(m.p), dim, stride, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
-               CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+    const CUtensorMapDataType type = dtype == QMOE_F32    ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
+                                     : dtype == QMOE_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                                          : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+    return enc(map, type, three ? 3 : 2, const_cast<void*>(m.p), dim, stride, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+               store && size == 2 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
                ? QMOE_OK
                : QMOE_ERR_UNSUPPORTED;
@@ -531,7 +535,7 @@ static int run_rows(Mat w, Mat q, Args& g, int dtype, uint8_t* ws, size_t left, 
             return shares ? launch_as<MODE, 32, GATHER, true>(mp, mq, g, most, st) : launch_as<MODE, 32, GATHER, false>(mp, mq, g, most, st);
         case 128:
             return shares ? launch_as<MODE, 128, GATHER, true>(mp, mq, g, most, st) : launch_as<MODE, 128, GATHER, false>(mp, mq, g, most, st);
-        default: return GATHER ? QMOE_ERR_UNSUPPORTED : launch_pair<MODE>(mp, mq, g, most, st);
+        default: return GATHER ? QMOE_ERR_UNSUPPORTED : launch_pair<MODE>(mp, mq, mq, g, most, st);
     }
 }
 
@@ -666,5 +670,11 @@ extern "C" int qmoe_expert_linear_dw(int64_t P, int E, int64_t N, int64_t K, int
     if (rc != QMOE_OK) return rc;
     rc = eg::map_of(&mq, mx, dtype, 64, eg::STEP, false);
     if (rc != QMOE_OK) return rc;
-    return eg::launch_pair<eg::DW>(mp, mq, g, units, st);
+    if (!g.wide || (int64_t)size * P > 512ll * E) return eg::launch_pair<eg::DW>(mp, mq, mq, g, units, st);
+    // few rows an expert: put_dw has both sides
+    CUtensorMap mo;
+    const eg::Mat out = {dw, N, K, K, E, N * K};
+    rc = eg::map_of(&mo, out, dw_dtype, 32, 32, true, true);
+    if (rc != QMOE_OK) return rc;
+    return eg::launch_pair<eg::DW, true>(mp, mq, mo, g, units, st);
 }

@@ -277,18 +277,26 @@ __device__ __forceinline__ void put_rows(const Args& g, int l0, int q0, int n, i
 }
 
 // 32 columns of dw: lane l holds columns q0 .. q0 + n - 1 of row l0 + l.  Through
-// shared memory, so that a store instruction writes whole rows of 128 bytes (64 in
-// 16 bits).  (512 experts of 8 rows, 1024 x 2048: 818 us with rows of 64 bytes, 698
-// with 128.)
-template <typename T>
-__device__ __forceinline__ void put_dw(const Args& g, uint8_t* stage, int e, int l0, int q0, int n, int lane,
+// shared memory, so that rows of 128 bytes (64 in 16 bits) are written whole: by a TMA
+// store (BULK), which runs while the warp goes on and leaves out what lies outside the
+// expert's matrix, or by the warp's own stores, where TMA is to feed long sums at the
+// same time.  us with the warp's stores and with TMA's, in fp32 and in bf16, rows an
+// expert: 512 x 8 (1024 x 2048) 847 and 729, 571 and 465; 64 x 80 (2816 x 4096) 590
+// and 564, 401 and 284; 128 x 256 (2048 x 768) 172 and 185, 133 and 107; 64 x 512
+// (2816 x 2048) 342 and 354, 267 and 272.
+template <bool BULK, typename T>
+__device__ __forceinline__ void put_dw(const Args& g, const CUtensorMap* map, uint8_t* stage, int e, int l0, int q0, int n, int lane,
                                        const uint32_t (&r)[32]) {
     constexpr int PER = 16 / sizeof(T), PIECES = 32 / PER, ROW = 32 * sizeof(T);  // of 16 bytes
     constexpr int ROWS = 32;
     static_assert(ROWS * ROW <= STAGE_DW, "");
     T* const out = static_cast<T*>(g.out) + (int64_t)e * g.out_e;
-    // where a row's piece lies: rows that are read or written together fall on all banks
+    // where a row's piece lies: rows that are read or written together fall on all banks, and the store's swizzle has it so
     auto place = [](int row, int p) { return row * ROW + ((p ^ (sizeof(T) == 4 ? row & 7 : row >> 1 & 3)) * 16); };
+    if constexpr (BULK) {
+        if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+        __syncwarp();
+    }
 #pragma unroll
     for (int p = 0; p < PIECES; ++p) {
         uint4 v;
@@ -301,6 +309,18 @@ __device__ __forceinline__ void put_dw(const Args& g, uint8_t* stage, int e, int
                 w[i] = r[p * 4 + i];
         }
         *reinterpret_cast<uint4*>(stage + place(lane, p)) = v;
+    }
+    if constexpr (BULK) {
+        tc::fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0 && l0 < g.lanes && n > 0) {
+            asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(
+                             reinterpret_cast<uint64_t>(map)),
+                         "r"(tc::smem_u32(stage)), "r"(q0), "r"(l0), "r"(e)
+                         : "memory");
+            asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+        }
+        return;
     }
     __syncwarp();
     if (g.wide) {
@@ -345,13 +365,13 @@ __device__ __forceinline__ void take(bool matrices, uint32_t taddr, uint32_t (&r
     if (MODE != DW && matrices) tmem_ld_matrices(taddr, r);
     else tmem_ld32(taddr, r);
 }
-template <int MODE>
-__device__ __forceinline__ void put(const Args& g, bool matrices, uint8_t* stage, int e, int l0, int q0, int n, int lane,
-                                    const uint32_t (&r)[32]) {
+template <int MODE, bool BULK>
+__device__ __forceinline__ void put(const Args& g, const CUtensorMap* map, bool matrices, uint8_t* stage, int e, int l0, int q0, int n,
+                                    int lane, const uint32_t (&r)[32]) {
     if constexpr (MODE == DW) {
-        if (g.ctype == QMOE_F32) put_dw<float>(g, stage, e, l0, q0, n, lane, r);
-        else if (g.ctype == QMOE_BF16) put_dw<__nv_bfloat16>(g, stage, e, l0, q0, n, lane, r);
-        else put_dw<__half>(g, stage, e, l0, q0, n, lane, r);
+        if (g.ctype == QMOE_F32) put_dw<BULK, float>(g, map, stage, e, l0, q0, n, lane, r);
+        else if (g.ctype == QMOE_BF16) put_dw<BULK, __nv_bfloat16>(g, map, stage, e, l0, q0, n, lane, r);
+        else put_dw<BULK, __half>(g, map, stage, e, l0, q0, n, lane, r);
     } else if (matrices) {
         if (g.ctype == QMOE_BF16) put_matrices<__nv_bfloat16>(g, stage, l0, q0, n, lane, r);
         else put_matrices<__half>(g, stage, l0, q0, n, lane, r);
@@ -472,8 +492,9 @@ int launch_few(const Mat& w, const Mat& x, const Args& g, int dtype, cudaStream_
 // What the kernels take: map_p of the lane side, map_q of the column side.
 //
 // Pairs of CTAs, 256 x 256 tiles: for many rows an expert, and for dw.
-template <int MODE>
-int launch_pair(const CUtensorMap& mp, const CUtensorMap& mq, const Args& g, int64_t most, cudaStream_t st);
+// BULK: dw goes out by TMA stores of 32 x 32 values, by way of mo.
+template <int MODE, bool BULK = false>
+int launch_pair(const CUtensorMap& mp, const CUtensorMap& mq, const CUtensorMap& mo, const Args& g, int64_t most, cudaStream_t st);
 
 }  // namespace eg
 }  // namespace qmoe

@@ -108,9 +108,10 @@ __device__ __forceinline__ void mma_stage(uint32_t d, uint32_t stage, uint32_t i
         if (k < k16) mma_pair(d, da + SA * k, db + SB * k, idesc, !first || k > 0);
 }
 
-template <int MODE>
+template <int MODE, bool BULK>
 __global__ void __launch_bounds__(PAIR_THREADS, 1)
-expert_pair_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_constant__ CUtensorMap map_q, const Args g) {
+expert_pair_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_constant__ CUtensorMap map_q,
+                   const __grid_constant__ CUtensorMap map_o, const Args g) {
     using C = PairCfg<MODE>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -292,7 +293,7 @@ expert_pair_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_const
                 uint32_t r[32];
 #pragma unroll
                 for (int j = 0; j < 32; ++j) r[j] = 0;
-                for (int c = half * 32; c < t.n; c += 64) put<MODE>(g, matrices, stage, t.e, l0, t.q0 + c, t.n - c, lane, r);
+                for (int c = half * 32; c < t.n; c += 64) put<MODE, BULK>(g, &map_o, matrices, stage, t.e, l0, t.q0 + c, t.n - c, lane, r);
                 continue;
             }
             if (!warp_wait(&acc_full[buf], acc_phase, abort_flag, g.status)) break;
@@ -310,7 +311,7 @@ expert_pair_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_const
                     tc::tmem_ld_wait();
 #pragma unroll
                     for (int j = 0; j < 32; ++j) x[j] = __float_as_uint(__uint_as_float(x[j]) + __uint_as_float(y[j]));
-                    put<MODE>(g, matrices, stage, t.e, l0, t.q0 + c, t.n - c, lane, x);
+                    put<MODE, BULK>(g, &map_o, matrices, stage, t.e, l0, t.q0 + c, t.n - c, lane, x);
                 }
                 tc::tc_fence_before();
                 __syncwarp();
@@ -334,7 +335,7 @@ expert_pair_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_const
                     __syncwarp();
                     if (lane == 0) arrive_first(&acc_empty[buf]);
                 }
-                put<MODE>(g, matrices, stage, t.e, l0, t.q0 + at, t.n - at, lane, now);
+                put<MODE, BULK>(g, &map_o, matrices, stage, t.e, l0, t.q0 + at, t.n - at, lane, now);
                 at += 64;
             };
             if (at >= t.n && lane == 0) arrive_first(&acc_empty[buf]);  // no columns for this warp
@@ -345,6 +346,7 @@ expert_pair_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_const
             if (++buf == 2) { buf = 0; acc_phase ^= 1; }
         }
     }
+    if (BULK && warp < EPI_WARPS && lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
     __syncwarp();
     pdl_trigger();
     tc::tc_fence_before();
@@ -356,10 +358,10 @@ expert_pair_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_const
         asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tm), "r"(512) : "memory");
 }
 
-template <int MODE>
-int launch_pair(const CUtensorMap& mp, const CUtensorMap& mq, const Args& g, int64_t most, cudaStream_t st) {
+template <int MODE, bool BULK>
+int launch_pair(const CUtensorMap& mp, const CUtensorMap& mq, const CUtensorMap& mo, const Args& g, int64_t most, cudaStream_t st) {
     using C = PairCfg<MODE>;
-    const int rc = row::allow_smem<expert_pair_kernel<MODE>>(C::SMEM);
+    const int rc = row::allow_smem<expert_pair_kernel<MODE, BULK>>(C::SMEM);
     if (rc != QMOE_OK) return rc;
     const int64_t pairs = most < row::kSMs / 2 ? most : row::kSMs / 2;
     cudaLaunchAttribute attr[2];
@@ -376,12 +378,13 @@ int launch_pair(const CUtensorMap& mp, const CUtensorMap& mq, const Args& g, int
     cfg.stream = st;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, expert_pair_kernel<MODE>, mp, mq, g) == cudaSuccess ? QMOE_OK : QMOE_ERR_LAUNCH;
+    return cudaLaunchKernelEx(&cfg, expert_pair_kernel<MODE, BULK>, mp, mq, mo, g) == cudaSuccess ? QMOE_OK : QMOE_ERR_LAUNCH;
 }
 
-template int launch_pair<FWD>(const CUtensorMap&, const CUtensorMap&, const Args&, int64_t, cudaStream_t);
-template int launch_pair<DX>(const CUtensorMap&, const CUtensorMap&, const Args&, int64_t, cudaStream_t);
-template int launch_pair<DW>(const CUtensorMap&, const CUtensorMap&, const Args&, int64_t, cudaStream_t);
+template int launch_pair<FWD, false>(const CUtensorMap&, const CUtensorMap&, const CUtensorMap&, const Args&, int64_t, cudaStream_t);
+template int launch_pair<DX, false>(const CUtensorMap&, const CUtensorMap&, const CUtensorMap&, const Args&, int64_t, cudaStream_t);
+template int launch_pair<DW, true>(const CUtensorMap&, const CUtensorMap&, const CUtensorMap&, const Args&, int64_t, cudaStream_t);
+template int launch_pair<DW, false>(const CUtensorMap&, const CUtensorMap&, const CUtensorMap&, const Args&, int64_t, cudaStream_t);
 
 }  // namespace eg
 }  // namespace qmoe
