@@ -320,6 +320,7 @@ __device__ __forceinline__ void put_dw(const Args& g, const CUtensorMap* map, ui
                          : "memory");
             asm volatile("cp.async.bulk.commit_group;" ::: "memory");
         }
+        __syncwarp();  // what follows reads TMEM, which all lanes do together
         return;
     }
     __syncwarp();
