@@ -573,7 +573,11 @@ __global__ void __launch_bounds__(THREADS, NT == 1 ? 2 : 1) w4_few_kernel(const 
 // Two E2M1 codes as fp16.
 __device__ __forceinline__ uint32_t e2m1_pair(uint32_t byte) { return pair_of<__half, QMOE_W4_E2M1, 0>(byte); }
 
-// W in 16 bits, [N, K], and {0, T} for the grouped product with one expert.
+// W in 16 bits, [N, K], and {0, T} for the grouped product with one expert.  The
+// tensor core takes no scale for each group of int4 values beside 16-bit x, so a
+// weight is rounded to x's type, by half a step at most (bf16: 0.0024 of the result's
+// norm off, of which 0.0017 is the output's own rounding; E2M1 values with their power
+// of two are exact).  2816 x 4096: 8.5 us.
 template <typename T, int FORMAT>
 __global__ void __launch_bounds__(256) w4_widen_kernel(int64_t words, int per_row, int shift, const uint32_t* w, const void* s,
                                                        uint4* to, int32_t* offsets, int tokens) {
