@@ -187,12 +187,12 @@ expert_gemm_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_const
         const int turn = warp - WARP_MMA;
         int it = 0, buf = 0;
         uint32_t acc_phase = 0;
-        bool ok = true;  // lane 0's; after a wait that ran out nothing is waited for any more
-        while (segments.next(seg)) {
+        bool ok = true;  // after a wait that ran out no more products are issued and no more stages let go
+        while (ok && segments.next(seg)) {
             if (seg.s1 == 0) continue;  // zeros: no sums to wait for
             const uint32_t n16 = (uint32_t)(t.n + 15) & ~15u;
             const uint32_t idesc = g.idesc | (n16 >> 3) << 17 | (128u >> 4) << 24, d = tm + (buf * TURNS + turn) * NT;
-            if (lane == 0) ok = ok && lane_wait(&acc_empty[buf], acc_phase ^ 1, abort_flag, g.status);
+            if (!(ok = warp_wait(&acc_empty[buf], acc_phase ^ 1, abort_flag, g.status))) break;
             // every second step, a sum of its own: by the steps' count from the first tile's on, so that a stage is always one
             // warp's.  By turns within a tile, odd ones gave a stage to the other warp, which took a load that was two rounds
             // behind for one that had come: the parity of a barrier does not tell them apart.
@@ -201,8 +201,7 @@ expert_gemm_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_const
 #pragma unroll 1
             for (int i = it + ((it ^ turn) & 1); i < last; i += TURNS) {
                 const int slot = i % C::STAGES;
-                if (lane == 0) ok = ok && lane_wait(&full[slot], i / C::STAGES & 1, abort_flag, g.status);
-                __syncwarp();
+                if (!(ok = warp_wait(&full[slot], i / C::STAGES & 1, abort_flag, g.status))) break;
                 tc::tc_fence_after();
                 const uint32_t sa = tc::smem_u32(smem) + slot * C::STAGE, sb = sa + C::P_BYTES;
                 const uint64_t da = MODE == FWD ? tc::sdesc_kmajor_sw128(sa) : sdesc_across(sa);
@@ -213,6 +212,7 @@ expert_gemm_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_const
                 tc::mma_commit_elect(&empty[slot]);
                 more = 1;
             }
+            if (!ok) break;
             it = last;
             tc::mma_commit_elect(&acc_full[buf]);
             if (++buf == 2) { buf = 0; acc_phase ^= 1; }

@@ -208,8 +208,8 @@ expert_pair_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_const
     } else if (warp == PAIR_MMA) {
         int slot = 0, buf = 0;
         uint32_t phase = 0, acc_phase = 0, relayed = 0, here = 0;  // of each stage: the phases of other, and of full in the second CTA
-        bool ok = true;  // lane 0's; after a wait that ran out nothing is waited for any more
-        for (int u = first; u < total; u += stride) {
+        bool ok = true;  // after a wait that ran out no more products are issued and no more stages let go
+        for (int u = first; u < total && ok; u += stride) {
             const Unit t = walk.at(u);
             if (t.steps == 0) continue;  // zeros: no sums to wait for
             const uint32_t n32 = (uint32_t)(t.n + 31) & ~31u;
@@ -217,8 +217,7 @@ expert_pair_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_const
             uint32_t d = tm + buf * 256;
             const int left = MODE == DW ? (t.end - t.row0) % STEP : 0, whole = t.steps - (left > 0);
             auto take = [&]() {  // an accumulator
-                if (rank == 0 && lane == 0) ok = ok && lane_wait(&acc_empty[buf], acc_phase ^ 1, abort_flag, g.status);
-                __syncwarp();
+                if (rank == 0) ok = ok && warp_wait(&acc_empty[buf], acc_phase ^ 1, abort_flag, g.status);
                 d = tm + buf * 256;
             };
             auto give = [&]() {
@@ -226,6 +225,7 @@ expert_pair_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_const
                 if (++buf == 2) { buf = 0; acc_phase ^= 1; }
             };
             take();
+            if (!ok) break;
             const int turn = MODE == DW && t.steps > LONG ? t.steps / 2 : 0;  // a long sum's second half has its own accumulator
             int from = 0;
             if (rank == 0) {
@@ -236,8 +236,8 @@ expert_pair_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_const
                         take();
                         from = s;
                     }
-                    if (lane == 0) ok = ok && lane_wait(&full[slot], phase, abort_flag, g.status);
-                    __syncwarp();
+                    ok = ok && warp_wait(&full[slot], phase, abort_flag, g.status);
+                    if (!ok) break;
                     tc::tc_fence_after();
                     mma_stage<MODE>(d, tc::smem_u32(smem) + slot * C::STAGE, idesc, s == from);
                     commit_pair(&empty[slot]);
@@ -248,13 +248,13 @@ expert_pair_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_const
                 phase ^= slot / C::STAGES & 1;
                 slot %= C::STAGES;
             }
+            if (!ok) break;
             if constexpr (MODE == DW) {
                 if (left > 0) {
                     const int k16 = (left + 15) / 16;
                     uint8_t* st = smem + slot * C::STAGE;
-                    if (lane == 0) ok = ok && lane_wait(&full[slot], rank == 0 ? phase : here >> slot & 1, abort_flag, g.status);
+                    if (!(ok = warp_wait(&full[slot], rank == 0 ? phase : here >> slot & 1, abort_flag, g.status))) break;
                     here ^= 1u << slot;
-                    __syncwarp();
                     // rows behind the expert's last, up to the 16 of a product, are another's: zeros in their place
                     const int zero = k16 * 16 - left;
                     for (int i = lane; i < 4 * zero * 8; i += 32) {
@@ -264,9 +264,8 @@ expert_pair_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_const
                     tc::fence_proxy_async_smem();
                     __syncwarp();
                     if (rank == 0) {
-                        if (lane == 0) ok = ok && lane_wait(&other[slot], relayed >> slot & 1, abort_flag, g.status);
+                        if (!(ok = warp_wait(&other[slot], relayed >> slot & 1, abort_flag, g.status))) break;
                         relayed ^= 1u << slot;
-                        __syncwarp();
                         tc::tc_fence_after();
                         mma_stage<MODE>(d, tc::smem_u32(st), idesc, whole == from, k16);
                         commit_pair(&empty[slot]);

@@ -399,6 +399,8 @@ __global__ void __launch_bounds__(THREADS, NT == 1 ? 2 : 1) w4_few_kernel(const 
     if (later.e >= 0) find_rows();
     fetch();
 
+    // after a wait that ran out a warp frees no more stages (the one that sends gives up by itself) and only keeps the others'
+    // barriers company
     bool ok = true;
     int slot = 0, buf = 0, staged_c = -1;
     uint32_t phase = 0;
@@ -516,7 +518,7 @@ __global__ void __launch_bounds__(THREADS, NT == 1 ? 2 : 1) w4_few_kernel(const 
                     }
                 }
                 __syncwarp();
-                if (lane == 0) tc::mbar_arrive(&bars[WARPS * DEPTH + warp * DEPTH + slot]);
+                if (ok && lane == 0) tc::mbar_arrive(&bars[WARPS * DEPTH + warp * DEPTH + slot]);
                 if (++slot == DEPTH) { slot = 0; phase ^= 1; }
             }
         }
