@@ -131,10 +131,11 @@ __global__ void __launch_bounds__(FEW_THREADS) expert_few_kernel(const FewArgs g
             }
             if (r < g.x_rows) x = g.x + r * g.ldx;
         }
-        float acc[4] = {0.f, 0.f, 0.f, 0.f};
+        float acc[4] = {0.f, 0.f, 0.f, 0.f};  // sums of a round's products, which the tensor core cuts off, added by fp32's rounding
         for (int i0 = warp; i0 < pieces; i0 += FEW_WARPS * FEW_DEPTH) {
             Piece<false> a[FEW_DEPTH], b[FEW_DEPTH];
             Piece<WIDE_X> v[FEW_DEPTH];
+            float d[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
             for (int j = 0; j < FEW_DEPTH; ++j) {
                 const int k = (i0 + j * FEW_WARPS) * 32 + quad * 8;
@@ -146,9 +147,11 @@ __global__ void __launch_bounds__(FEW_THREADS) expert_few_kernel(const FewArgs g
             for (int j = 0; j < FEW_DEPTH; ++j) {
                 const int k = (i0 + j * FEW_WARPS) * 32 + quad * 8;
                 const uint4 p = a[j].get(w0, k, g.K), q = b[j].get(w1, k, g.K), r = v[j].get(x, k, g.K);
-                mma_few<T>(acc, p.x, q.x, p.y, q.y, r.x, r.y);
-                mma_few<T>(acc, p.z, q.z, p.w, q.w, r.z, r.w);
+                mma_few<T>(d, p.x, q.x, p.y, q.y, r.x, r.y);
+                mma_few<T>(d, p.z, q.z, p.w, q.w, r.z, r.w);
             }
+#pragma unroll
+            for (int j = 0; j < 4; ++j) acc[j] += d[j];
         }
         if (s > s0) __syncthreads();
         part[warp][quad * 2][row] = acc[0];

@@ -29,6 +29,7 @@ namespace eg {
 // 40.5 us for 38.4, one row 4096 -> 4096 14.9 for 14.0, but one token x 8 of 128
 // experts 14.5 for 15.0.
 constexpr int TURNS = 2, WARP_TMA = 8, WARP_MMA = WARP_TMA + TURNS, WARP_GATHER = WARP_MMA + TURNS;
+constexpr int PIECE = TURNS * LONG;  // steps of a piece of a long sum
 constexpr int threads_of(bool gather) { return (WARP_GATHER + (gather ? GATHER_WARPS : 0)) * 32; }
 
 template <int MODE, int NT>
@@ -191,31 +192,35 @@ expert_gemm_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_const
         while (ok && segments.next(seg)) {
             if (seg.s1 == 0) continue;  // zeros: no sums to wait for
             const uint32_t n16 = (uint32_t)(t.n + 15) & ~15u;
-            const uint32_t idesc = g.idesc | (n16 >> 3) << 17 | (128u >> 4) << 24, d = tm + (buf * TURNS + turn) * NT;
-            if (!(ok = warp_wait(&acc_empty[buf], acc_phase ^ 1, abort_flag, g.status))) break;
-            // every second step, a sum of its own: by the steps' count from the first tile's on, so that a stage is always one
-            // warp's.  By turns within a tile, odd ones gave a stage to the other warp, which took a load that was two rounds
-            // behind for one that had come: the parity of a barrier does not tell them apart.
-            const int last = it + seg.s1 - seg.s0;
-            uint32_t more = 0;
+            const uint32_t idesc = g.idesc | (n16 >> 3) << 17 | (128u >> 4) << 24;
+            const int end = it + seg.s1 - seg.s0;
+            while (it < end) {  // pieces of the sum, each in an accumulator of its own
+                const uint32_t d = tm + (buf * TURNS + turn) * NT;
+                if (!(ok = warp_wait(&acc_empty[buf], acc_phase ^ 1, abort_flag, g.status))) break;
+                // every second step, a sum of its own: by the steps' count from the first tile's on, so that a stage is always one
+                // warp's.  By turns within a tile, odd ones gave a stage to the other warp, which took a load that was two rounds
+                // behind for one that had come: the parity of a barrier does not tell them apart.
+                const int last = min(it + PIECE, end);
+                uint32_t more = 0;
 #pragma unroll 1
-            for (int i = it + ((it ^ turn) & 1); i < last; i += TURNS) {
-                const int slot = i % C::STAGES;
-                if (!(ok = warp_wait(&full[slot], i / C::STAGES & 1, abort_flag, g.status))) break;
-                tc::tc_fence_after();
-                const uint32_t sa = tc::smem_u32(smem) + slot * C::STAGE, sb = sa + C::P_BYTES;
-                const uint64_t da = MODE == FWD ? tc::sdesc_kmajor_sw128(sa) : sdesc_across(sa);
-                const uint64_t db = tc::sdesc_kmajor_sw128(sb);
-                constexpr int SA = MODE == FWD ? 2 : 128, SB = 2;  // of 16 values, in 16 bytes
+                for (int i = it + ((it ^ turn) & 1); i < last; i += TURNS) {
+                    const int slot = i % C::STAGES;
+                    if (!(ok = warp_wait(&full[slot], i / C::STAGES & 1, abort_flag, g.status))) break;
+                    tc::tc_fence_after();
+                    const uint32_t sa = tc::smem_u32(smem) + slot * C::STAGE, sb = sa + C::P_BYTES;
+                    const uint64_t da = MODE == FWD ? tc::sdesc_kmajor_sw128(sa) : sdesc_across(sa);
+                    const uint64_t db = tc::sdesc_kmajor_sw128(sb);
+                    constexpr int SA = MODE == FWD ? 2 : 128, SB = 2;  // of 16 values, in 16 bytes
 #pragma unroll
-                for (int k = 0; k < STEP / 16; ++k) tc::mma_f16_elect(d, da + SA * k, db + SB * k, idesc, k > 0 ? 1 : more);
-                tc::mma_commit_elect(&empty[slot]);
-                more = 1;
+                    for (int k = 0; k < STEP / 16; ++k) tc::mma_f16_elect(d, da + SA * k, db + SB * k, idesc, k > 0 ? 1 : more);
+                    tc::mma_commit_elect(&empty[slot]);
+                    more = 1;
+                }
+                if (!ok) break;
+                it = last;
+                tc::mma_commit_elect(&acc_full[buf]);
+                if (++buf == 2) { buf = 0; acc_phase ^= 1; }
             }
-            if (!ok) break;
-            it = last;
-            tc::mma_commit_elect(&acc_full[buf]);
-            if (++buf == 2) { buf = 0; acc_phase ^= 1; }
         }
         __syncwarp();
     } else if (warp >= WARP_GATHER) {
@@ -244,6 +249,7 @@ expert_gemm_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_const
             }
         }
     } else {
+        constexpr int CHUNKS = (NT + 63) / 64;  // of 32 columns, every second one this warp's
         const int quad = warp & 3, half = warp >> 2;
         int4 join = make_int4(0, 0, 0, 0);
         const bool matrices = by_matrices<MODE>(g);
@@ -253,44 +259,53 @@ expert_gemm_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_const
         while (!*abort_flag && segments.next(seg)) {
             const int l0 = t.l0 + quad * 32;
             if (SPLIT && seg.part == 1) join = make_int4(t.l0, t.q0, t.n, segments.others(seg));
-            if (seg.s1 > 0) {
-                if (!warp_wait(&acc_full[buf], acc_phase, abort_flag, g.status)) break;
+            // all of this warp's columns: of each piece what both warps have summed up, then of all pieces
+            const bool part = SPLIT && seg.part >= 0, by_8 = matrices && !part;
+            uint32_t r[CHUNKS][32];
+            if (seg.s1 == 0) {
+#pragma unroll
+                for (int i = 0; i < CHUNKS; ++i)
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) r[i][j] = 0;
+            }
+            bool ok = true;
+            const int end = it + seg.s1 - seg.s0, begin = it;
+#pragma unroll 1
+            for (; it < end; it = min(it + PIECE, end)) {
+                ok = warp_wait(&acc_full[buf], acc_phase, abort_flag, g.status);
+                if (!ok) break;
                 tc::tc_fence_after();
-            }
-            for (int c = half * 32; c < t.n; c += 64) {
-                uint32_t r[32];
-                const bool part = SPLIT && seg.part >= 0;
-                if (seg.s1 > 0) {
-                    const uint32_t from = tm + ((uint32_t)(quad * 32) << 16) + buf * TURNS * NT + c;
-                    const uint32_t one = from + (it & 1) * NT;  // of the warp that has the first step
-                    take<MODE>(matrices && !part, one, r);
-                    tc::tmem_ld_wait();
-                    if (seg.s1 - seg.s0 > 1) {
-                        uint32_t y[32];
-                        take<MODE>(matrices && !part, from + (~it & 1) * NT, y);
-                        tc::tmem_ld_wait();
+                const uint32_t from = tm + ((uint32_t)(quad * 32) << 16) + buf * TURNS * NT + half * 32;
+                const uint32_t one = from + (it & 1) * NT, other = from + (~it & 1) * NT;  // one: of the warp that has the first step
 #pragma unroll
-                        for (int j = 0; j < 32; ++j) r[j] = __float_as_uint(__uint_as_float(r[j]) + __uint_as_float(y[j]));
+                for (int i = 0; i < CHUNKS; ++i)
+                    if (half * 32 + i * 64 < t.n) {
+                        if (it == begin) {
+                            take<MODE>(by_8, one + i * 64, r[i]);
+                            tc::tmem_ld_wait();
+                        } else {
+                            add<MODE>(by_8, one + i * 64, r[i]);
+                        }
+                        if (end - it > 1) add<MODE>(by_8, other + i * 64, r[i]);
                     }
-                } else {
-#pragma unroll
-                    for (int j = 0; j < 32; ++j) r[j] = 0;
-                }
-                if (part) {
-                    float* to = g.parts + (((int64_t)blockIdx.x * 2 + seg.part) * NT + c) * 128 + quad * 32 + lane;
-#pragma unroll
-                    for (int j = 0; j < 32; ++j)
-                        if (c + j < t.n) to[j * 128] = __uint_as_float(r[j]);
-                } else {
-                    put<MODE, false>(g, nullptr, matrices, stage, t.e, l0, t.q0 + c, t.n - c, lane, r);
-                }
-            }
-            it += seg.s1 - seg.s0;
-            if (seg.s1 > 0) {
                 tc::tc_fence_before();
                 __syncwarp();
                 if (lane == 0) tc::mbar_arrive(&acc_empty[buf]);
                 if (++buf == 2) { buf = 0; acc_phase ^= 1; }
+            }
+            if (!ok) break;
+#pragma unroll
+            for (int i = 0; i < CHUNKS; ++i) {
+                const int c = half * 32 + i * 64;
+                if (c >= t.n) break;
+                if (part) {
+                    float* to = g.parts + (((int64_t)blockIdx.x * 2 + seg.part) * NT + c) * 128 + quad * 32 + lane;
+#pragma unroll
+                    for (int j = 0; j < 32; ++j)
+                        if (c + j < t.n) to[j * 128] = __uint_as_float(r[i][j]);
+                } else {
+                    put<MODE, false>(g, nullptr, matrices, stage, t.e, l0, t.q0 + c, t.n - c, lane, r[i]);
+                }
             }
         }
         if (SPLIT && threadIdx.x == 0) g.joins[blockIdx.x] = join;

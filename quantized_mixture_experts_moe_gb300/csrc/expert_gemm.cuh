@@ -18,6 +18,12 @@ constexpr int STEP = 64;         // reduction values of a stage: 128 bytes
 constexpr int MAX_E = 1024;
 constexpr int STAGE_OUT = 2048, STAGE_DW = 4096;  // bytes of a warp's output stage: 32 rows of 64, or 128
 constexpr int Q_BOX = 32;        // rows of a box of the column side (y, dx)
+// Most steps that the tensor core sums up by itself.  It cuts a sum off where fp32
+// would round it, by up to 2^-23 for each 16 values and always towards zero: 8192
+// values were 9.1e-6 of the result off, 65536 in two halves 3.8e-5.  Longer sums are
+// made in pieces, each in an accumulator of its own, that are added with fp32's
+// rounding: 2.1e-6 at any length.
+constexpr int LONG = 32;
 
 struct Args {
     int P, E;
@@ -118,6 +124,16 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
         : "r"(taddr));
 }
 
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,"
+        "%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31};" ::"r"(r[0]),
+        "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]),
+        "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]),
+        "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31]), "r"(taddr)
+        : "memory");
+}
+
 // A tile: its expert, first lane, first column (a row s, or a column of dw), the
 // columns it has and its reduction steps.
 struct Unit {
@@ -215,23 +231,27 @@ __device__ __forceinline__ void check_offsets(const Args& g) {
 // 32 columns of this warp's 32 lanes as 8 x 8 matrices: lane t holds of lanes
 // 8 m + t / 4 the columns 8 i + 2 (t % 4) and the next, for m = 0, 1 in r[4 i ..],
 // for m = 2, 3 in r[16 + 4 i ..].
+__device__ __forceinline__ void tmem_ld_half_matrices(uint32_t taddr, uint32_t* r) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]),
+          "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr));
+}
 __device__ __forceinline__ void tmem_ld_matrices(uint32_t taddr, uint32_t (&r)[32]) {
 #pragma unroll
-    for (int h = 0; h < 32; h += 16)
-        asm volatile(
-            "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
-            : "=r"(r[h]), "=r"(r[h + 1]), "=r"(r[h + 2]), "=r"(r[h + 3]), "=r"(r[h + 4]), "=r"(r[h + 5]), "=r"(r[h + 6]),
-              "=r"(r[h + 7]), "=r"(r[h + 8]), "=r"(r[h + 9]), "=r"(r[h + 10]), "=r"(r[h + 11]), "=r"(r[h + 12]), "=r"(r[h + 13]),
-              "=r"(r[h + 14]), "=r"(r[h + 15])
-            : "r"(taddr + ((uint32_t)h << 16)));
+    for (int h = 0; h < 32; h += 16) tmem_ld_half_matrices(taddr + ((uint32_t)h << 16), r + h);
 }
-// 32 columns of y or dx in 16 bits, from matrices: transposed on their way to shared
-// memory, so that a column (a row of y) lies there as it is stored.
+// A warp stores 32 columns of its 32 lanes in two steps: from registers to shared
+// memory (stage_*), and on to HBM (send_*), so that a loop over columns, which lie in
+// other registers each time, has the second one's code once.
+
+// y or dx in 16 bits, from matrices: transposed on their way to shared memory, so that
+// a column (a row of y) lies there as it is stored.  16-byte pieces of 64-byte rows,
+// changed about so that 8 rows fall on all banks.
+__device__ __forceinline__ int place_matrices(int row, int p) { return row * 64 + ((p ^ (row >> 1 & 3)) * 16); }
 template <typename T>
-__device__ __forceinline__ void put_matrices(const Args& g, uint8_t* stage, int l0, int q0, int n, int lane, const uint32_t (&r)[32]) {
-    T* const out = static_cast<T*>(g.out);
-    // 16-byte pieces of 64-byte rows, changed about so that 8 rows fall on all banks
-    auto place = [](int row, int p) { return row * 64 + ((p ^ (row >> 1 & 3)) * 16); };
+__device__ __forceinline__ void stage_matrices(uint8_t* stage, int lane, const uint32_t (&r)[32]) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         uint32_t w[4];
@@ -240,24 +260,27 @@ __device__ __forceinline__ void put_matrices(const Args& g, uint8_t* stage, int 
             w[m] = row::pack2(__uint_as_float(r[(m >> 1) * 16 + 4 * i + (m & 1) * 2]),
                               __uint_as_float(r[(m >> 1) * 16 + 4 * i + (m & 1) * 2 + 1]), T{});
         asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(
-                         tc::smem_u32(stage + place(8 * i + (lane & 7), lane >> 3))),
+                         tc::smem_u32(stage + place_matrices(8 * i + (lane & 7), lane >> 3))),
                      "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3])
                      : "memory");
     }
+}
+__device__ __forceinline__ void send_matrices(const Args& g, uint8_t* stage, int l0, int q0, int n, int lane) {
     __syncwarp();
-    const int l = l0 + (lane & 3) * 8;
+    const int l = l0 + (lane & 3) * 8, row = lane >> 2;
+    const uint8_t* const from = stage + place_matrices(row, lane & 3);  // and every 8th row
+    uint16_t* to = static_cast<uint16_t*>(g.out) + (int64_t)(q0 + row) * g.ld + l;  // two types of two bytes
     uint4 v[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] = *reinterpret_cast<const uint4*>(stage + place(i * 8 + (lane >> 2), lane & 3));
+    for (int i = 0; i < 4; ++i) v[i] = *reinterpret_cast<const uint4*>(from + i * 8 * 64);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const int row = i * 8 + (lane >> 2);
-        T* const to = out + (int64_t)(q0 + row) * g.ld + l;
-        if (row < n && l + 8 <= g.lanes) {
+        if (row + i * 8 < n && l + 8 <= g.lanes) {
             *reinterpret_cast<uint4*>(to) = v[i];
-        } else if (row < n) {
-            for (int j = 0; j < 8 && l + j < g.lanes; ++j) to[j] = reinterpret_cast<const T*>(&v[i])[j];
+        } else if (row + i * 8 < n) {
+            for (int j = 0; j < 8 && l + j < g.lanes; ++j) to[j] = reinterpret_cast<const uint16_t*>(&v[i])[j];
         }
+        to += 8 * g.ld;
     }
     __syncwarp();
 }
@@ -284,19 +307,23 @@ __device__ __forceinline__ void put_rows(const Args& g, int l0, int q0, int n, i
 // expert: 512 x 8 (1024 x 2048) 847 and 729, 571 and 465; 64 x 80 (2816 x 4096) 590
 // and 564, 401 and 284; 128 x 256 (2048 x 768) 172 and 185, 133 and 107; 64 x 512
 // (2816 x 2048) 342 and 354, 267 and 272.
+//
+// Where a row's piece of 16 bytes lies: rows that are read or written together fall on
+// all banks, and the store's swizzle has it so.
+template <typename T>
+__device__ __forceinline__ int place_dw(int row, int p) {
+    return row * 32 * (int)sizeof(T) + ((p ^ (sizeof(T) == 4 ? row & 7 : row >> 1 & 3)) * 16);
+}
 template <bool BULK, typename T>
-__device__ __forceinline__ void put_dw(const Args& g, const CUtensorMap* map, uint8_t* stage, int e, int l0, int q0, int n, int lane,
-                                       const uint32_t (&r)[32]) {
-    constexpr int PER = 16 / sizeof(T), PIECES = 32 / PER, ROW = 32 * sizeof(T);  // of 16 bytes
-    constexpr int ROWS = 32;
-    static_assert(ROWS * ROW <= STAGE_DW, "");
-    T* const out = static_cast<T*>(g.out) + (int64_t)e * g.out_e;
-    // where a row's piece lies: rows that are read or written together fall on all banks, and the store's swizzle has it so
-    auto place = [](int row, int p) { return row * ROW + ((p ^ (sizeof(T) == 4 ? row & 7 : row >> 1 & 3)) * 16); };
+__device__ __forceinline__ void stage_dw(uint8_t* stage, int lane, const uint32_t (&r)[32]) {
+    constexpr int PER = 16 / sizeof(T), PIECES = 32 / PER;  // of 16 bytes
+    static_assert(32 * 32 * sizeof(T) <= STAGE_DW, "");
     if constexpr (BULK) {
         if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
         __syncwarp();
     }
+    int at = place_dw<T>(lane, 0);
+    asm volatile("" : "+r"(at));  // one address, not one for each piece that is kept over all tiles
 #pragma unroll
     for (int p = 0; p < PIECES; ++p) {
         uint4 v;
@@ -308,8 +335,13 @@ __device__ __forceinline__ void put_dw(const Args& g, const CUtensorMap* map, ui
             else
                 w[i] = r[p * 4 + i];
         }
-        *reinterpret_cast<uint4*>(stage + place(lane, p)) = v;
+        *reinterpret_cast<uint4*>(stage + (at ^ p * 16)) = v;
     }
+}
+template <bool BULK, typename T>
+__device__ __forceinline__ void send_dw(const Args& g, const CUtensorMap* map, uint8_t* stage, int e, int l0, int q0, int n, int lane) {
+    constexpr int PER = 16 / sizeof(T), PIECES = 32 / PER, ROWS = 32;
+    T* const out = static_cast<T*>(g.out) + (int64_t)e * g.out_e;
     if constexpr (BULK) {
         tc::fence_proxy_async_smem();
         __syncwarp();
@@ -326,18 +358,22 @@ __device__ __forceinline__ void put_dw(const Args& g, const CUtensorMap* map, ui
     __syncwarp();
     if (g.wide) {
         constexpr int EACH = 32 / PIECES;  // rows of an instruction
+        const int row = lane / PIECES, p = lane % PIECES, c = p * PER;
+        int at = place_dw<T>(row, p);
+        asm volatile("" : "+r"(at));
+        T* to = out + (int64_t)(l0 + row) * g.ld + q0 + c;
 #pragma unroll
         for (int i = 0; i < ROWS / EACH; ++i) {
-            const int row = i * EACH + lane / PIECES, p = lane % PIECES, c = p * PER;
-            const uint4 v = *reinterpret_cast<const uint4*>(stage + place(row, p));
-            if (l0 + row < g.lanes && c < n) {
-                T* const to = out + (int64_t)(l0 + row) * g.ld + q0 + c;
+            // in fp32 rows 4 apart have their pieces 4 apart
+            const uint4 v = *reinterpret_cast<const uint4*>(stage + (sizeof(T) == 4 ? at ^ (i & 1) * 64 : at) + i * EACH * 32 * sizeof(T));
+            if (l0 + row + i * EACH < g.lanes && c < n) {
                 if (c + PER <= n) {
                     *reinterpret_cast<uint4*>(to) = v;
                 } else {
                     for (int j = 0; j < PER && c + j < n; ++j) to[j] = reinterpret_cast<const T*>(&v)[j];
                 }
             }
+            to += EACH * g.ld;
         }
     } else {
         T* to = out + (int64_t)l0 * g.ld + q0 + lane;
@@ -346,7 +382,7 @@ __device__ __forceinline__ void put_dw(const Args& g, const CUtensorMap* map, ui
         for (int r0 = 0; r0 < ROWS; r0 += 16) {  // all reads of shared memory, then all stores
             T v[16];
 #pragma unroll
-            for (int i = 0; i < 16; ++i) v[i] = reinterpret_cast<const T*>(stage + place(r0 + i, lane / PER))[lane % PER];
+            for (int i = 0; i < 16; ++i) v[i] = reinterpret_cast<const T*>(stage + place_dw<T>(r0 + i, lane / PER))[lane % PER];
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
                 if (r0 + i < rows) *to = v[i];
@@ -366,21 +402,50 @@ __device__ __forceinline__ void take(bool matrices, uint32_t taddr, uint32_t (&r
     if (MODE != DW && matrices) tmem_ld_matrices(taddr, r);
     else tmem_ld32(taddr, r);
 }
+// The same columns, added to r; half of them at a time, as r leaves few registers.
+template <int MODE>
+__device__ __forceinline__ void add(bool matrices, uint32_t taddr, uint32_t (&r)[32]) {
+#pragma unroll
+    for (int h = 0; h < 32; h += 16) {
+        uint32_t x[16];
+        if (MODE != DW && matrices) tmem_ld_half_matrices(taddr + ((uint32_t)h << 16), x);
+        else tc::tmem_ld_32x32b_x16(taddr + h, x);
+        tc::tmem_ld_wait();
+#pragma unroll
+        for (int j = 0; j < 16; ++j) r[h + j] = __float_as_uint(__uint_as_float(r[h + j]) + __uint_as_float(x[j]));
+    }
+}
 template <int MODE, bool BULK>
-__device__ __forceinline__ void put(const Args& g, const CUtensorMap* map, bool matrices, uint8_t* stage, int e, int l0, int q0, int n,
-                                    int lane, const uint32_t (&r)[32]) {
+__device__ __forceinline__ void stage_sums(const Args& g, bool matrices, uint8_t* stage, int l0, int q0, int n, int lane,
+                                           const uint32_t (&r)[32]) {
     if constexpr (MODE == DW) {
-        if (g.ctype == QMOE_F32) put_dw<BULK, float>(g, map, stage, e, l0, q0, n, lane, r);
-        else if (g.ctype == QMOE_BF16) put_dw<BULK, __nv_bfloat16>(g, map, stage, e, l0, q0, n, lane, r);
-        else put_dw<BULK, __half>(g, map, stage, e, l0, q0, n, lane, r);
+        if (g.ctype == QMOE_F32) stage_dw<BULK, float>(stage, lane, r);
+        else if (g.ctype == QMOE_BF16) stage_dw<BULK, __nv_bfloat16>(stage, lane, r);
+        else stage_dw<BULK, __half>(stage, lane, r);
     } else if (matrices) {
-        if (g.ctype == QMOE_BF16) put_matrices<__nv_bfloat16>(g, stage, l0, q0, n, lane, r);
-        else put_matrices<__half>(g, stage, l0, q0, n, lane, r);
+        if (g.ctype == QMOE_BF16) stage_matrices<__nv_bfloat16>(stage, lane, r);
+        else stage_matrices<__half>(stage, lane, r);
     } else {
         if (g.ctype == QMOE_F32) put_rows<float>(g, l0, q0, n, lane, r);
         else if (g.ctype == QMOE_BF16) put_rows<__nv_bfloat16>(g, l0, q0, n, lane, r);
         else put_rows<__half>(g, l0, q0, n, lane, r);
     }
+}
+template <int MODE, bool BULK>
+__device__ __forceinline__ void send_sums(const Args& g, const CUtensorMap* map, bool matrices, uint8_t* stage, int e, int l0, int q0,
+                                          int n, int lane) {
+    if constexpr (MODE == DW) {
+        if (g.ctype == QMOE_F32) send_dw<BULK, float>(g, map, stage, e, l0, q0, n, lane);
+        else send_dw<BULK, uint16_t>(g, map, stage, e, l0, q0, n, lane);  // two types of two bytes
+    } else if (matrices) {
+        send_matrices(g, stage, l0, q0, n, lane);
+    }
+}
+template <int MODE, bool BULK>
+__device__ __forceinline__ void put(const Args& g, const CUtensorMap* map, bool matrices, uint8_t* stage, int e, int l0, int q0, int n,
+                                    int lane, const uint32_t (&r)[32]) {
+    stage_sums<MODE, BULK>(g, matrices, stage, l0, q0, n, lane, r);
+    send_sums<MODE, BULK>(g, map, matrices, stage, e, l0, q0, n, lane);
 }
 
 // The offsets, clamped to [0, P] and raised to the largest before them (no row

@@ -27,10 +27,8 @@ namespace eg {
 constexpr int PAIR_TMA = 8, TURNS = 2, PAIR_MMA = PAIR_TMA + TURNS;
 constexpr int PAIR_THREADS = (PAIR_MMA + 1) * 32;
 
-// Steps from which a sum of dw is made in two halves, added in the epilogue: the
-// tensor core cuts its sums off where fp32 would round them, which adds up (8192
-// rows: 9.1e-6 of the result).
-constexpr int LONG = 32;
+// Pieces of a sum: of steps / pieces_of(steps) steps each, rounded up.
+__device__ __forceinline__ int pieces_of(int steps) { return (steps + LONG - 1) / LONG; }
 
 template <int MODE>
 struct PairCfg {
@@ -214,43 +212,28 @@ expert_pair_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_const
             if (t.steps == 0) continue;  // zeros: no sums to wait for
             const uint32_t n32 = (uint32_t)(t.n + 31) & ~31u;
             const uint32_t idesc = g.idesc | (n32 >> 3) << 17 | (256u >> 4) << 24;
-            uint32_t d = tm + buf * 256;
             const int left = MODE == DW ? (t.end - t.row0) % STEP : 0, whole = t.steps - (left > 0);
-            auto take = [&]() {  // an accumulator
-                if (rank == 0) ok = ok && warp_wait(&acc_empty[buf], acc_phase ^ 1, abort_flag, g.status);
-                d = tm + buf * 256;
-            };
-            auto give = [&]() {
-                if (rank == 0) commit_pair(&acc_full[buf]);
-                if (++buf == 2) { buf = 0; acc_phase ^= 1; }
-            };
-            take();
-            if (!ok) break;
-            const int turn = MODE == DW && t.steps > LONG ? t.steps / 2 : 0;  // a long sum's second half has its own accumulator
-            int from = 0;
-            if (rank == 0) {
+            const int pieces = pieces_of(t.steps), per = pieces > 1 ? (t.steps + pieces - 1) / pieces : t.steps;
+            for (int from = 0; from < t.steps; from += per) {  // the sum's pieces, each in an accumulator of its own
+                if (rank == 0 && !(ok = warp_wait(&acc_empty[buf], acc_phase ^ 1, abort_flag, g.status))) break;
+                const uint32_t d = tm + buf * 256;
+                const int to = min(from + per, whole);
+                if (rank == 0) {
 #pragma unroll 1
-                for (int s = 0; s < whole; ++s) {
-                    if (MODE == DW && turn && s == turn) {
-                        give();
-                        take();
-                        from = s;
+                    for (int s = from; s < to; ++s) {
+                        if (!(ok = warp_wait(&full[slot], phase, abort_flag, g.status))) break;
+                        tc::tc_fence_after();
+                        mma_stage<MODE>(d, tc::smem_u32(smem) + slot * C::STAGE, idesc, s == from);
+                        commit_pair(&empty[slot]);
+                        if (++slot == C::STAGES) { slot = 0; phase ^= 1; }
                     }
-                    ok = ok && warp_wait(&full[slot], phase, abort_flag, g.status);
-                    if (!ok) break;
-                    tc::tc_fence_after();
-                    mma_stage<MODE>(d, tc::smem_u32(smem) + slot * C::STAGE, idesc, s == from);
-                    commit_pair(&empty[slot]);
-                    if (++slot == C::STAGES) { slot = 0; phase ^= 1; }
+                } else {
+                    slot += to - from;  // the first CTA's affair
+                    phase ^= slot / C::STAGES & 1;
+                    slot %= C::STAGES;
                 }
-            } else {
-                slot += whole;  // the first CTA's affair
-                phase ^= slot / C::STAGES & 1;
-                slot %= C::STAGES;
-            }
-            if (!ok) break;
-            if constexpr (MODE == DW) {
-                if (left > 0) {
+                if (!ok) break;
+                if (MODE == DW && left > 0 && from + per >= t.steps) {
                     const int k16 = (left + 15) / 16;
                     uint8_t* st = smem + slot * C::STAGE;
                     if (!(ok = warp_wait(&full[slot], rank == 0 ? phase : here >> slot & 1, abort_flag, g.status))) break;
@@ -275,8 +258,9 @@ expert_pair_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_const
                     __syncwarp();
                     if (++slot == C::STAGES) { slot = 0; phase ^= 1; }
                 }
+                if (rank == 0) commit_pair(&acc_full[buf]);
+                if (++buf == 2) { buf = 0; acc_phase ^= 1; }
             }
-            give();
         }
         __syncwarp();
     } else {
@@ -288,56 +272,57 @@ expert_pair_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_const
         for (int u = first; u < total && !*abort_flag; u += stride) {
             const Unit t = walk.at(u);
             const int l0 = t.l0 + rank * 128 + quad * 32;
+            uint32_t r[2][32];
             if (t.steps == 0) {
-                uint32_t r[32];
 #pragma unroll
-                for (int j = 0; j < 32; ++j) r[j] = 0;
-                for (int c = half * 32; c < t.n; c += 64) put<MODE, BULK>(g, &map_o, matrices, stage, t.e, l0, t.q0 + c, t.n - c, lane, r);
+                for (int j = 0; j < 32; ++j) r[0][j] = 0;
+                for (int c = half * 32; c < t.n; c += 64) put<MODE, BULK>(g, &map_o, matrices, stage, t.e, l0, t.q0 + c, t.n - c, lane, r[0]);
                 continue;
             }
-            if (!warp_wait(&acc_full[buf], acc_phase, abort_flag, g.status)) break;
-            tc::tc_fence_after();
-            const uint32_t from = tm + ((uint32_t)(quad * 32) << 16) + buf * 256;
-            if (MODE == DW && t.steps > LONG) {
-                // both halves of the sum
-                const int other = buf ^ 1;
-                if (!warp_wait(&acc_full[other], acc_phase ^ (other == 0), abort_flag, g.status)) break;
-                tc::tc_fence_after();
-                for (int c = half * 32; c < t.n; c += 64) {
-                    uint32_t x[32], y[32];
-                    tmem_ld32(from + c, x);
-                    tmem_ld32(tm + ((uint32_t)(quad * 32) << 16) + other * 256 + c, y);
-                    tc::tmem_ld_wait();
-#pragma unroll
-                    for (int j = 0; j < 32; ++j) x[j] = __float_as_uint(__uint_as_float(x[j]) + __uint_as_float(y[j]));
-                    put<MODE, BULK>(g, &map_o, matrices, stage, t.e, l0, t.q0 + c, t.n - c, lane, x);
-                }
+            const uint32_t all = tm + ((uint32_t)(quad * 32) << 16);
+            auto let_go = [&](int which) {
                 tc::tc_fence_before();
                 __syncwarp();
-                if (lane == 0) {
-                    arrive_first(&acc_empty[0]);
-                    arrive_first(&acc_empty[1]);
+                if (lane == 0) arrive_first(&acc_empty[which]);
+            };
+            if (!warp_wait(&acc_full[buf], acc_phase, abort_flag, g.status)) break;
+            tc::tc_fence_after();
+            bool ok = true;
+#pragma unroll 1
+            for (int p = pieces_of(t.steps); p > 1; --p) {
+                // The sum so far is added to the next piece's, in TMEM, and its accumulator let go: products wait some 0.6 us
+                // for it, as the other accumulator holds the sum (8192 rows 4096 -> 4096: 158 us, 153 in one piece).  128 sums a
+                // thread in registers would leave both accumulators free, but spilled (155 there, but dw of 64 x 512 rows 2816 x
+                // 2048 400 to 600 us for 360).
+                const int before = buf;
+                if (++buf == 2) { buf = 0; acc_phase ^= 1; }
+                ok = warp_wait(&acc_full[buf], acc_phase, abort_flag, g.status);
+                if (!ok) break;
+                tc::tc_fence_after();
+                for (int c = half * 32; c < t.n; c += 64) {
+                    tmem_ld32(all + before * 256 + c, r[0]);
+                    tmem_ld32(all + buf * 256 + c, r[1]);
+                    tc::tmem_ld_wait();
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) r[0][j] = __float_as_uint(__uint_as_float(r[0][j]) + __uint_as_float(r[1][j]));
+                    tmem_st32(all + buf * 256 + c, r[0]);
                 }
-                acc_phase ^= 1;  // two accumulators on
-                continue;
+                tc::tmem_st_wait();
+                let_go(before);
             }
+            if (!ok) break;
             // the next 32 columns are on their way while these are stored; the sums are let go when the last have come
-            uint32_t r[2][32];
+            const uint32_t from = all + buf * 256;
             int at = half * 32;
             if (at < t.n) take<MODE>(matrices, from + at, r[0]);
             auto turn = [&](uint32_t (&now)[32], uint32_t (&next)[32]) {
                 tc::tmem_ld_wait();
-                if (at + 64 < t.n) {
-                    take<MODE>(matrices, from + at + 64, next);
-                } else {
-                    tc::tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) arrive_first(&acc_empty[buf]);
-                }
+                if (at + 64 < t.n) take<MODE>(matrices, from + at + 64, next);
+                else let_go(buf);
                 put<MODE, BULK>(g, &map_o, matrices, stage, t.e, l0, t.q0 + at, t.n - at, lane, now);
                 at += 64;
             };
-            if (at >= t.n && lane == 0) arrive_first(&acc_empty[buf]);  // no columns for this warp
+            if (at >= t.n) let_go(buf);  // no columns for this warp
             while (at < t.n) {
                 turn(r[0], r[1]);
                 if (at < t.n) turn(r[1], r[0]);
