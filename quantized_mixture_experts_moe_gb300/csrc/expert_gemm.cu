@@ -342,7 +342,8 @@ __global__ void __launch_bounds__(512) join_kernel(const Args g) {
     }
 #pragma unroll
     for (int j = 0; j < U; ++j)
-        if (c0 + j < t.z && t.x + l < g.lanes) put_value(g.out, g.ctype, (int64_t)(t.y + c0 + j) * g.ld + t.x + l, sum[j]);
+        if (c0 + j < t.z && t.x + l < g.lanes)
+            put_value(g.out, g.ctype, (int64_t)(t.y + c0 + j) * g.ld + t.x + l, g.by ? sum[j] * g.by[t.x + l] : sum[j]);
 }
 
 // Rows of 16-bit values laid out for TMA: rows that start off the 16-byte
@@ -594,62 +595,88 @@ extern "C" size_t qmoe_expert_workspace_bytes(int64_t P, int E, int64_t N, int64
     return eg::split(P, E, op == eg::FWD ? N : K, op == eg::FWD ? K : N, nt) ? eg::part_bytes(nt) : 0;
 }
 
+namespace qmoe {
+namespace eg {
+
+// by: of each output (y) or input (dx) of the layer, or NULL
+static int linear(const Call& c, const void* x, int64_t ldx, const void* w, int64_t ldw, int64_t w_expert, const float* by, void* y,
+                  int y_dtype, int64_t ldy, void* ws, size_t ws_bytes, cudaStream_t st) {
+    int rc = check(c);
+    if (rc != QMOE_OK) return rc;
+    if ((y_dtype != c.dtype && y_dtype != QMOE_F32) || ldy < c.N) return QMOE_ERR_ARG;
+    if (c.P == 0) return QMOE_OK;
+    if (c.pairs && c.x_rows == 0) return QMOE_ERR_ARG;
+    Mat mw = {w, c.N, c.K, ldw, c.E, w_expert}, mx = {x, c.pairs ? c.x_rows : c.P, c.K, ldx, 1, 0};
+    if (!mat_ok(mw, 2) || !mat_ok(mx, 2) || !word_ok(c.offsets) || !y || !row::type_aligned(y, row::dtype_size(y_dtype)) ||
+        !word_ok(c.status))
+        return QMOE_ERR_ARG;
+    uint8_t* at = static_cast<uint8_t*>(ws);
+    size_t left = ws && !(reinterpret_cast<uintptr_t>(ws) & 255u) ? ws_bytes : 0;
+    const int size = row::dtype_size(y_dtype);
+    Args g = {(int)c.P, c.E, (int)c.N, 0, (int)c.K, c.offsets, c.pairs, c.k, (int)mx.rows, y, ldy, 0, y_dtype,
+              aligned16(y) && ldy * size % 16 == 0, c.dtype == QMOE_BF16 ? tc::idesc_bf16_f32(0, 0) : tc::idesc_f16_f32(0, 0), c.status,
+              nullptr, nullptr, by};
+    if (few(c.P, c.E, c.N, c.K, fits(mw))) return launch_few(mw, mx, g, c.dtype, st);
+    const bool lay_out = c.pairs && tile_of(c.P, c.E) == 256;
+    const size_t need = qmoe_expert_workspace_bytes(c.P, c.E, c.N, c.K, FWD, c.pairs != nullptr);
+    if (left < need + copy_need(mw) + (lay_out ? 0 : copy_need(mx))) return QMOE_ERR_ARG;
+    if ((rc = as_tma(mw, c.offsets, at, left, st)) != QMOE_OK) return rc;
+    rc = lay_out ? copy_rows(mx, c.pairs, c.P, c.k, nullptr, at, left, st) : as_tma(mx, nullptr, at, left, st);
+    if (rc != QMOE_OK) return rc;
+    if (lay_out) g.pairs = nullptr;
+    return g.pairs ? run_rows<FWD, true>(mw, mx, g, c.dtype, at, left, st) : run_rows<FWD, false>(mw, mx, g, c.dtype, at, left, st);
+}
+
+static int linear_dx(const Call& c, const void* dy, int64_t lddy, const void* w, int64_t ldw, int64_t w_expert, const float* by, void* dx,
+                     int dx_dtype, int64_t lddx, void* ws, size_t ws_bytes, cudaStream_t st) {
+    int rc = check(c);
+    if (rc != QMOE_OK) return rc;
+    if ((dx_dtype != c.dtype && dx_dtype != QMOE_F32) || lddx < c.K) return QMOE_ERR_ARG;
+    if (c.P == 0) return QMOE_OK;
+    Mat mw = {w, c.N, c.K, ldw, c.E, w_expert}, my = {dy, c.P, c.N, lddy, 1, 0};
+    if (!mat_ok(mw, 2) || !mat_ok(my, 2) || !word_ok(c.offsets) || !dx || !row::type_aligned(dx, row::dtype_size(dx_dtype)) ||
+        !word_ok(c.status))
+        return QMOE_ERR_ARG;
+    uint8_t* at = static_cast<uint8_t*>(ws);
+    size_t left = ws && !(reinterpret_cast<uintptr_t>(ws) & 255u) ? ws_bytes : 0;
+    if (left < qmoe_expert_workspace_bytes(c.P, c.E, c.N, c.K, DX, 0) + copy_need(mw) + copy_need(my)) return QMOE_ERR_ARG;
+    if ((rc = as_tma(mw, c.offsets, at, left, st)) != QMOE_OK || (rc = as_tma(my, nullptr, at, left, st)) != QMOE_OK) return rc;
+    const int size = row::dtype_size(dx_dtype);
+    Args g = {(int)c.P, c.E, (int)c.K, 0, (int)c.N, c.offsets, nullptr, 0, (int)c.P, dx, lddx, 0, dx_dtype,
+              aligned16(dx) && lddx * size % 16 == 0,
+              (c.dtype == QMOE_BF16 ? tc::idesc_bf16_f32(0, 0) : tc::idesc_f16_f32(0, 0)) | 1u << 15, c.status, nullptr, nullptr, by};
+    return run_rows<DX, false>(mw, my, g, c.dtype, at, left, st);
+}
+
+size_t scaled_bytes(int64_t T, int64_t N, int64_t K, int dx) {
+    return qmoe_expert_copy_bytes(T, dx ? N : K) + qmoe_expert_workspace_bytes(T, 1, N, K, dx ? DX : FWD, 0);
+}
+int scaled_linear(const Scaled& c, const void* x, int64_t ldx, void* y, int y_dtype, int64_t ldy, cudaStream_t st) {
+    const Call call = {c.T, c.N, c.K, 1, c.dtype, c.offsets, nullptr, 0, c.T, c.status};
+    return linear(call, x, ldx, c.w, c.K, c.N * c.K, c.by, y, y_dtype, ldy, c.ws, c.ws_bytes, st);
+}
+int scaled_linear_dx(const Scaled& c, const void* dy, int64_t lddy, void* dx, int dx_dtype, int64_t lddx, cudaStream_t st) {
+    const Call call = {c.T, c.N, c.K, 1, c.dtype, c.offsets, nullptr, 0, c.T, c.status};
+    return linear_dx(call, dy, lddy, c.w, c.K, c.N * c.K, c.by, dx, dx_dtype, lddx, c.ws, c.ws_bytes, st);
+}
+
+}  // namespace eg
+}  // namespace qmoe
+
 extern "C" int qmoe_expert_linear(int64_t P, int E, int64_t N, int64_t K, int dtype, const void* x, int64_t ldx,
                                   int64_t x_rows, const int32_t* pairs, int k, const void* w, int64_t ldw, int64_t w_expert,
                                   const int32_t* offsets, void* y, int y_dtype, int64_t ldy, int32_t* dev_status, void* ws,
                                   size_t ws_bytes, qmoe_stream_t stream) {
-    const eg::Call c = {P, N, K, E, dtype, offsets, pairs, k, x_rows, dev_status};
-    int rc = eg::check(c);
-    if (rc != QMOE_OK) return rc;
-    if ((y_dtype != dtype && y_dtype != QMOE_F32) || ldy < N) return QMOE_ERR_ARG;
-    if (P == 0) return QMOE_OK;
-    if (pairs && x_rows == 0) return QMOE_ERR_ARG;
-    eg::Mat mw = {w, N, K, ldw, E, w_expert}, mx = {x, pairs ? x_rows : P, K, ldx, 1, 0};
-    if (!eg::mat_ok(mw, 2) || !eg::mat_ok(mx, 2) || !eg::word_ok(offsets) || !y ||
-        !row::type_aligned(y, row::dtype_size(y_dtype)) || !eg::word_ok(dev_status))
-        return QMOE_ERR_ARG;
-    cudaStream_t st = (cudaStream_t)stream;
-    uint8_t* at = static_cast<uint8_t*>(ws);
-    size_t left = ws && !(reinterpret_cast<uintptr_t>(ws) & 255u) ? ws_bytes : 0;
-    const int size = row::dtype_size(y_dtype);
-    eg::Args g = {(int)P, E, (int)N, 0, (int)K, offsets, pairs, k, (int)mx.rows, y, ldy, 0, y_dtype,
-                  aligned16(y) && ldy * size % 16 == 0,
-                  dtype == QMOE_BF16 ? tc::idesc_bf16_f32(0, 0) : tc::idesc_f16_f32(0, 0), dev_status, nullptr, nullptr};
-    if (eg::few(P, E, N, K, eg::fits(mw))) return eg::launch_few(mw, mx, g, dtype, st);
-    const bool lay_out = pairs && eg::tile_of(P, E) == 256;
-    const size_t need = qmoe_expert_workspace_bytes(P, E, N, K, eg::FWD, pairs != nullptr);
-    if (left < need + eg::copy_need(mw) + (lay_out ? 0 : eg::copy_need(mx))) return QMOE_ERR_ARG;
-    if ((rc = eg::as_tma(mw, offsets, at, left, st)) != QMOE_OK) return rc;
-    rc = lay_out ? eg::copy_rows(mx, pairs, P, k, nullptr, at, left, st) : eg::as_tma(mx, nullptr, at, left, st);
-    if (rc != QMOE_OK) return rc;
-    if (lay_out) g.pairs = nullptr;
-    return g.pairs ? eg::run_rows<eg::FWD, true>(mw, mx, g, dtype, at, left, st)
-                   : eg::run_rows<eg::FWD, false>(mw, mx, g, dtype, at, left, st);
+    return eg::linear({P, N, K, E, dtype, offsets, pairs, k, x_rows, dev_status}, x, ldx, w, ldw, w_expert, nullptr, y, y_dtype, ldy, ws,
+                      ws_bytes, (cudaStream_t)stream);
 }
 
 extern "C" int qmoe_expert_linear_dx(int64_t P, int E, int64_t N, int64_t K, int dtype, const void* dy, int64_t lddy,
                                      const void* w, int64_t ldw, int64_t w_expert, const int32_t* offsets, void* dx,
                                      int dx_dtype, int64_t lddx, int32_t* dev_status, void* ws, size_t ws_bytes,
                                      qmoe_stream_t stream) {
-    const eg::Call c = {P, N, K, E, dtype, offsets, nullptr, 0, 0, dev_status};
-    int rc = eg::check(c);
-    if (rc != QMOE_OK) return rc;
-    if ((dx_dtype != dtype && dx_dtype != QMOE_F32) || lddx < K) return QMOE_ERR_ARG;
-    if (P == 0) return QMOE_OK;
-    eg::Mat mw = {w, N, K, ldw, E, w_expert}, my = {dy, P, N, lddy, 1, 0};
-    if (!eg::mat_ok(mw, 2) || !eg::mat_ok(my, 2) || !eg::word_ok(offsets) || !dx ||
-        !row::type_aligned(dx, row::dtype_size(dx_dtype)) || !eg::word_ok(dev_status))
-        return QMOE_ERR_ARG;
-    cudaStream_t st = (cudaStream_t)stream;
-    uint8_t* at = static_cast<uint8_t*>(ws);
-    size_t left = ws && !(reinterpret_cast<uintptr_t>(ws) & 255u) ? ws_bytes : 0;
-    if (left < qmoe_expert_workspace_bytes(P, E, N, K, eg::DX, 0) + eg::copy_need(mw) + eg::copy_need(my)) return QMOE_ERR_ARG;
-    if ((rc = eg::as_tma(mw, offsets, at, left, st)) != QMOE_OK || (rc = eg::as_tma(my, nullptr, at, left, st)) != QMOE_OK) return rc;
-    const int size = row::dtype_size(dx_dtype);
-    eg::Args g = {(int)P, E, (int)K, 0, (int)N, offsets, nullptr, 0, (int)P, dx, lddx, 0, dx_dtype,
-                  aligned16(dx) && lddx * size % 16 == 0,
-                  (dtype == QMOE_BF16 ? tc::idesc_bf16_f32(0, 0) : tc::idesc_f16_f32(0, 0)) | 1u << 15, dev_status, nullptr, nullptr};
-    return eg::run_rows<eg::DX, false>(mw, my, g, dtype, at, left, st);
+    return eg::linear_dx({P, N, K, E, dtype, offsets, nullptr, 0, 0, dev_status}, dy, lddy, w, ldw, w_expert, nullptr, dx, dx_dtype, lddx,
+                         ws, ws_bytes, (cudaStream_t)stream);
 }
 
 extern "C" int qmoe_expert_linear_dw(int64_t P, int E, int64_t N, int64_t K, int dtype, const void* dy, int64_t lddy,
@@ -679,7 +706,7 @@ extern "C" int qmoe_expert_linear_dw(int64_t P, int E, int64_t N, int64_t K, int
     if (rc != QMOE_OK) return rc;
     eg::Args g = {(int)P, E, (int)N, (int)K, 0, offsets, nullptr, 0, (int)mx.rows, dw, K, N * K, dw_dtype,
                   aligned16(dw) && K * size % 16 == 0,
-                  (dtype == QMOE_BF16 ? tc::idesc_bf16_f32(0, 0) : tc::idesc_f16_f32(0, 0)) | 3u << 15, dev_status, nullptr, nullptr};
+                  (dtype == QMOE_BF16 ? tc::idesc_bf16_f32(0, 0) : tc::idesc_f16_f32(0, 0)) | 3u << 15, dev_status, nullptr, nullptr, nullptr};
     CUtensorMap mp, mq;
     rc = eg::map_of(&mp, my, dtype, 64, eg::STEP, false);
     if (rc != QMOE_OK) return rc;

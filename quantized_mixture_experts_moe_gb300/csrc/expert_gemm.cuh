@@ -39,6 +39,7 @@ struct Args {
     int32_t* status;
     float* parts;          // sums of tiles in parts (few tiles), and where they belong
     int4* joins;
+    const float* by;       // y, dx: a factor of each lane's sums (NULL: none)
 };
 
 // Operand whose reduction axis is not the contiguous one: blocks of 64 lanes (or
@@ -415,9 +416,29 @@ __device__ __forceinline__ void add(bool matrices, uint32_t taddr, uint32_t (&r)
         for (int j = 0; j < 16; ++j) r[h + j] = __float_as_uint(__uint_as_float(r[h + j]) + __uint_as_float(x[j]));
     }
 }
+// Sums of weights that were divided by a power of two.
+__device__ __forceinline__ void multiply(const Args& g, bool matrices, int l0, int lane, uint32_t (&r)[32]) {
+    auto of = [&](int l) { return l < g.lanes ? g.by[l] : 0.f; };
+    if (matrices) {
+#pragma unroll
+        for (int m = 0; m < 4; ++m) {
+            const float f = of(l0 + 8 * m + (lane >> 2));
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                uint32_t& v = r[(m >> 1) * 16 + (i >> 1) * 4 + (m & 1) * 2 + (i & 1)];
+                v = __float_as_uint(__uint_as_float(v) * f);
+            }
+        }
+    } else {
+        const float f = of(l0 + lane);
+#pragma unroll
+        for (int i = 0; i < 32; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) * f);
+    }
+}
 template <int MODE, bool BULK>
 __device__ __forceinline__ void stage_sums(const Args& g, bool matrices, uint8_t* stage, int l0, int q0, int n, int lane,
-                                           const uint32_t (&r)[32]) {
+                                           uint32_t (&r)[32]) {
+    if (MODE != DW && g.by) multiply(g, matrices, l0, lane, r);
     if constexpr (MODE == DW) {
         if (g.ctype == QMOE_F32) stage_dw<BULK, float>(stage, lane, r);
         else if (g.ctype == QMOE_BF16) stage_dw<BULK, __nv_bfloat16>(stage, lane, r);
@@ -443,7 +464,7 @@ __device__ __forceinline__ void send_sums(const Args& g, const CUtensorMap* map,
 }
 template <int MODE, bool BULK>
 __device__ __forceinline__ void put(const Args& g, const CUtensorMap* map, bool matrices, uint8_t* stage, int e, int l0, int q0, int n,
-                                    int lane, const uint32_t (&r)[32]) {
+                                    int lane, uint32_t (&r)[32]) {
     stage_sums<MODE, BULK>(g, matrices, stage, l0, q0, n, lane, r);
     send_sums<MODE, BULK>(g, map, matrices, stage, e, l0, q0, n, lane);
 }
@@ -551,6 +572,23 @@ struct Mat {
 inline bool fits(const Mat& m) {
     return aligned16(m.p) && (m.rows == 1 || m.ld % 8 == 0) && (m.experts == 1 || m.stride % 8 == 0);
 }
+
+// Products with one matrix w [N, K] of contiguous rows of a multiple of 8 values,
+// each of whose rows (y) or columns (dx) stands for `by` times what it holds.
+// ws: scaled_bytes (dx: 0 or 1).  offsets: {0, T} on the device.
+struct Scaled {
+    const void* w;
+    const float* by;
+    int64_t T, N, K;
+    int dtype;
+    const int32_t* offsets;
+    int32_t* status;
+    void* ws;
+    size_t ws_bytes;
+};
+size_t scaled_bytes(int64_t T, int64_t N, int64_t K, int dx);
+int scaled_linear(const Scaled& c, const void* x, int64_t ldx, void* y, int y_dtype, int64_t ldy, cudaStream_t st);
+int scaled_linear_dx(const Scaled& c, const void* dy, int64_t lddy, void* dx, int dx_dtype, int64_t lddx, cudaStream_t st);
 
 // y for few rows an expert, of any alignment.
 int launch_few(const Mat& w, const Mat& x, const Args& g, int dtype, cudaStream_t st);

@@ -33,9 +33,7 @@
 // operations for two E2M1 codes).  One token 2048 -> 2816, int4: 4.1 us, latency.
 #include <type_traits>
 
-#include "row_ops.cuh"
-#include "tc_ptx.cuh"
-#include "tma_host.cuh"
+#include "expert_gemm.cuh"
 
 namespace qmoe {
 namespace w4 {
@@ -579,31 +577,121 @@ __device__ __forceinline__ uint32_t e2m1_pair(uint32_t byte) { return pair_of<__
 // tensor core takes no scale for each group of int4 values beside 16-bit x, so a
 // weight is rounded to x's type, by half a step at most (bf16: 0.0024 of the result's
 // norm off, of which 0.0017 is the output's own rounding; E2M1 values with their power
-// of two are exact).  2816 x 4096: 8.5 us.
-template <typename T, int FORMAT>
-__global__ void __launch_bounds__(256) w4_widen_kernel(int64_t words, int per_row, int shift, const uint32_t* w, const void* s,
-                                                       uint4* to, int32_t* offsets, int tokens) {
+// of two are exact).
+//
+// Scales may lie anywhere in fp16 (int4) or from 2^-127 to 2^127 (E2M1), weights in
+// fp16 may not.  So each row (the product), or each column (the gradient), is divided
+// by a power of two, `by`, that its sums are multiplied with again.  In fp16 it moves
+// the largest scale's values to at most 2^15: what is 2^-39 of the largest or more
+// keeps its place.  In bf16 E2M1 values are divided by 4 (6 x 2^127 has no place there),
+// which leaves the least of them 2^-130, above bf16's 2^-133.
+struct Widen {
+    int64_t N, K;
+    int shift;
+    const uint32_t* w;
+    const void* s;
+    uint4* to;
+    float* by;
+    int64_t lanes;  // of by
+    int32_t* offsets;
+    int tokens;
+};
+// A scale as a whole number that grows with it; 0 for one that is no finite number.
+template <int FORMAT>
+__device__ __forceinline__ int key_of(const void* s, int64_t i) {
+    const int raw = static_cast<const typename Scale<FORMAT>::Raw*>(s)[i];
+    if constexpr (FORMAT == QMOE_W4_INT4) return (raw & 0x7FFF) < 0x7C00 ? raw & 0x7FFF : 0;
+    else return raw < 255 ? raw : 0;
+}
+// The exponent of `by` in bf16, and in fp16 from the largest key.
+template <int FORMAT> constexpr int BF16_EXPONENT = FORMAT == QMOE_W4_INT4 ? 0 : 2;
+template <int FORMAT>
+__device__ __forceinline__ int exponent_of(int key) {
+    if constexpr (FORMAT == QMOE_W4_INT4) return f16_row_exponent(8.f * __half2float(__ushort_as_half((unsigned short)key)));
+    else return max(key - 127 + 2 - 14, -112);  // 6 x 2^(key - 127) becomes 6 x 2^12 (2^-112 leaves all below their places)
+}
+
+// `by` of each column in fp16.  A CTA takes 2 groups of columns, so that few rows fall to a thread (8 groups: 4096 x 4096 int4
+// in groups of 128 has 4 CTAs, and the gradient of 17 tokens takes 30.5 us for 25.4).
+template <int FORMAT>
+__global__ void __launch_bounds__(1024) w4_columns_kernel(const Widen a) {
+    constexpr int G = 2, EACH = 1024 / G;
+    __shared__ int most[G];
     pdl_wait();
     pdl_trigger();
-    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    if (i == 0) {
-        offsets[0] = 0;
-        offsets[1] = tokens;
+    const int groups = (int)(a.K >> a.shift), mine = threadIdx.x % G, g = blockIdx.x * G + mine;
+    if (threadIdx.x < G) most[threadIdx.x] = 0;
+    __syncthreads();
+    int key = 0;
+    if (g < groups) {
+#pragma unroll 8
+        for (int64_t n = threadIdx.x / G; n < a.N; n += EACH) key = max(key, key_of<FORMAT>(a.s, n * groups + g));
     }
-    if (i >= words) return;
-    const int64_t n = i / per_row, k = (i - n * per_row) * 8;
-    const float f = scale_at<FORMAT>(s, n * ((int64_t)per_row * 8 >> shift) + (k >> shift));
-    const uint32_t v = w[i];
-    float d[8];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        float2 c;
-        if constexpr (FORMAT == QMOE_W4_INT4) c = make_float2((int)(v >> 8 * j & 15) - 8, (int)(v >> (8 * j + 4) & 15) - 8);
-        else c = row::unpack2(e2m1_pair(v >> 8 * j & 255), __half{});
-        d[2 * j] = f * c.x;
-        d[2 * j + 1] = f * c.y;
+    for (int o = 16; o >= G; o >>= 1) key = max(key, __shfl_xor_sync(0xFFFFFFFFu, key, o));
+    if ((threadIdx.x & 31) < G) atomicMax(&most[mine], key);
+    __syncthreads();
+    const float f = exp2i(exponent_of<FORMAT>(most[mine]));
+    for (int k = threadIdx.x / G; g < groups && k < 1 << a.shift; k += EACH) a.by[((int64_t)g << a.shift) + k] = f;
+}
+
+// ROW_WARPS warps take a row (each finds its largest scale for itself).  ROWS_BY: fp16's `by` is made for the row; else it is there,
+// of each column.
+template <typename T, int FORMAT, bool ROWS_BY, int ROW_WARPS>
+__global__ void __launch_bounds__(256) w4_widen_kernel(const Widen a) {
+    constexpr bool HALF = std::is_same<T, __half>::value;
+    pdl_wait();
+    pdl_trigger();
+    const int64_t n = (int64_t)blockIdx.x * (8 / ROW_WARPS) + (threadIdx.x >> 5) / ROW_WARPS;
+    const int lane = threadIdx.x % (32 * ROW_WARPS), words = (int)(a.K / 8), groups = (int)(a.K >> a.shift);
+    if (blockIdx.x == 0 && threadIdx.x == 0) {
+        a.offsets[0] = 0;
+        a.offsets[1] = a.tokens;
     }
-    row::store<8>(reinterpret_cast<T*>(to + i), d);
+    float down = 1.f;  // 1 / by
+    if constexpr (!HALF) {
+        down = exp2i(-BF16_EXPONENT<FORMAT>);
+        for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < a.lanes; i += (int64_t)gridDim.x * 256)
+            a.by[i] = exp2i(BF16_EXPONENT<FORMAT>);
+    }
+    if (n >= a.N) return;
+    if constexpr (HALF && ROWS_BY) {
+        int key = 0;
+        for (int g = threadIdx.x & 31; g < groups; g += 32) key = max(key, key_of<FORMAT>(a.s, n * groups + g));
+        key = __reduce_max_sync(0xFFFFFFFFu, key);
+        const int e = exponent_of<FORMAT>(key);
+        down = exp2i(-e);
+        if (lane == 0) a.by[n] = exp2i(e);
+    }
+    const uint32_t* const from = a.w + n * words;
+    uint4* const to = a.to + n * words;
+    constexpr int U = 4, STEP = 32 * ROW_WARPS;
+    for (int i0 = lane; i0 < words; i0 += STEP * U) {
+        uint32_t v[U];
+        float f[U];
+#pragma unroll
+        for (int j = 0; j < U; ++j)
+            if (i0 + j * STEP < words) {
+                v[j] = from[i0 + j * STEP];
+                const int k = (i0 + j * STEP) * 8;
+                // powers of two first: a scale that fp32 holds times 6 need not be one
+                f[j] = scale_at<FORMAT>(a.s, n * groups + (k >> a.shift)) * (HALF && !ROWS_BY ? 1.f / a.by[k] : down);
+            }
+#pragma unroll
+        for (int j = 0; j < U; ++j)
+            if (i0 + j * STEP < words) {
+                float d[8];
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    float2 c;
+                    if constexpr (FORMAT == QMOE_W4_INT4) c = make_float2((int)(v[j] >> 8 * q & 15) - 8, (int)(v[j] >> (8 * q + 4) & 15) - 8);
+                    else c = row::unpack2(e2m1_pair(v[j] >> 8 * q & 255), __half{});
+                    d[2 * q] = f[j] * c.x;
+                    d[2 * q + 1] = f[j] * c.y;
+                }
+                row::store<8>(reinterpret_cast<T*>(to + i0 + j * STEP), d);
+            }
+    }
 }
 
 // ------------------------------------------------------------------ host side
@@ -667,20 +755,33 @@ inline bool format_ok(int format, int group) {
 inline int log2_of(int group) { return group == 32 ? 5 : group == 64 ? 6 : 7; }
 inline size_t up256(size_t n) { return (n + 255) / 256 * 256; }
 
-template <typename T, int FORMAT>
-static int widen(int64_t N, int64_t K, int group, const uint8_t* w, const void* s, uint8_t* ws, int32_t* offsets, int T_,
-                 cudaStream_t st) {
-    const int64_t words = N * (K / 8);
-    return launch_pdl(w4_widen_kernel<T, FORMAT>, dim3((unsigned)((words + 255) / 256)), dim3(256), 0, st, words, (int)(K / 8),
-                      log2_of(group), reinterpret_cast<const uint32_t*>(w), s, reinterpret_cast<uint4*>(ws), offsets, T_);
+template <typename T, int FORMAT, bool ROWS_BY>
+static int widen_rows(const Widen& a, cudaStream_t st) {
+    if (a.K >= 2048)  // a word at least for each thread of a CTA
+        return launch_pdl(w4_widen_kernel<T, FORMAT, ROWS_BY, 8>, dim3((unsigned)a.N), dim3(256), 0, st, a);
+    return launch_pdl(w4_widen_kernel<T, FORMAT, ROWS_BY, 1>, dim3((unsigned)((a.N + 7) / 8)), dim3(256), 0, st, a);
 }
-static int widen_any(int dtype, int format, int64_t N, int64_t K, int group, const uint8_t* w, const void* s, uint8_t* ws,
-                     int32_t* offsets, int T, cudaStream_t st) {
-    if (dtype == QMOE_BF16)
-        return format == QMOE_W4_INT4 ? widen<__nv_bfloat16, QMOE_W4_INT4>(N, K, group, w, s, ws, offsets, T, st)
-                                      : widen<__nv_bfloat16, QMOE_W4_E2M1>(N, K, group, w, s, ws, offsets, T, st);
-    return format == QMOE_W4_INT4 ? widen<__half, QMOE_W4_INT4>(N, K, group, w, s, ws, offsets, T, st)
-                                  : widen<__half, QMOE_W4_E2M1>(N, K, group, w, s, ws, offsets, T, st);
+template <typename T, int FORMAT>
+static int widen(const Widen& a, int dx, cudaStream_t st) {
+    if (!dx || std::is_same<T, __nv_bfloat16>::value) return widen_rows<T, FORMAT, true>(a, st);
+    const int64_t groups = a.K >> a.shift;
+    const int rc = launch_pdl(w4_columns_kernel<FORMAT>, dim3((unsigned)((groups + 1) / 2)), dim3(1024), 0, st, a);
+    return rc != QMOE_OK ? rc : widen_rows<T, FORMAT, false>(a, st);
+}
+// Widens W into the workspace: {W, by, offsets, what the product needs}.
+static int widen_any(eg::Scaled& c, int format, int group, const uint8_t* w, const void* s, int dx, cudaStream_t st) {
+    uint8_t* at = static_cast<uint8_t*>(c.ws);
+    const size_t wide = up256((size_t)c.N * c.K * 2), lanes = up256((size_t)(dx ? c.K : c.N) * 4), before = wide + lanes + 256;
+    const Widen a = {c.N, c.K, log2_of(group), reinterpret_cast<const uint32_t*>(w), s, reinterpret_cast<uint4*>(at),
+                     reinterpret_cast<float*>(at + wide), dx ? c.K : c.N, reinterpret_cast<int32_t*>(at + wide + lanes), (int)c.T};
+    c.w = at;
+    c.by = a.by;
+    c.offsets = a.offsets;
+    c.ws = at + before;
+    c.ws_bytes -= before;
+    if (c.dtype == QMOE_BF16)
+        return format == QMOE_W4_INT4 ? widen<__nv_bfloat16, QMOE_W4_INT4>(a, dx, st) : widen<__nv_bfloat16, QMOE_W4_E2M1>(a, dx, st);
+    return format == QMOE_W4_INT4 ? widen<__half, QMOE_W4_INT4>(a, dx, st) : widen<__half, QMOE_W4_E2M1>(a, dx, st);
 }
 
 constexpr int64_t kMost = 1ll << 30;
@@ -706,8 +807,7 @@ using namespace qmoe;
 
 extern "C" size_t qmoe_w4_workspace_bytes(int64_t T, int64_t N, int64_t K, int dx) {
     if (T <= 0 || N <= 0 || K <= 0 || (!dx && T <= QMOE_W4_FEW)) return 0;
-    return w4::up256((size_t)N * K * 2) + 256 + qmoe_expert_copy_bytes(T, dx ? N : K) +
-           qmoe_expert_workspace_bytes(T, 1, N, K, dx ? 1 : 0, 0);
+    return w4::up256((size_t)N * K * 2) + w4::up256((size_t)(dx ? K : N) * 4) + 256 + eg::scaled_bytes(T, N, K, dx);
 }
 
 extern "C" int qmoe_w4_linear(int64_t T, int k, int E, int64_t N, int64_t K, int format, int group, int dtype, const void* x,
@@ -722,13 +822,9 @@ extern "C" int qmoe_w4_linear(int64_t T, int k, int E, int64_t N, int64_t K, int
     cudaStream_t st = (cudaStream_t)stream;
     if (!ids && T > QMOE_W4_FEW) {
         if (!ws || (reinterpret_cast<uintptr_t>(ws) & 255u) || ws_bytes < qmoe_w4_workspace_bytes(T, N, K, 0)) return QMOE_ERR_ARG;
-        uint8_t* at = static_cast<uint8_t*>(ws);
-        const size_t wide = w4::up256((size_t)N * K * 2);
-        int32_t* offsets = reinterpret_cast<int32_t*>(at + wide);
-        rc = w4::widen_any(dtype, format, N, K, group, w, s, at, offsets, (int)T, st);
-        if (rc != QMOE_OK) return rc;
-        return qmoe_expert_linear(T, 1, N, K, dtype, x, ldx, T, nullptr, 0, at, K, N * K, offsets, y, y_dtype, ldy, dev_status,
-                                  at + wide + 256, ws_bytes - wide - 256, stream);
+        eg::Scaled c = {nullptr, nullptr, T, N, K, dtype, nullptr, dev_status, ws, ws_bytes};
+        rc = w4::widen_any(c, format, group, w, s, 0, st);
+        return rc != QMOE_OK ? rc : eg::scaled_linear(c, x, ldx, y, y_dtype, ldy, st);
     }
     EncodeTiledFn enc = encode_tiled_fn();
     if (!enc) return QMOE_ERR_CUDA;
@@ -761,11 +857,7 @@ extern "C" int qmoe_w4_linear_dx(int64_t T, int64_t N, int64_t K, int format, in
         ws_bytes < qmoe_w4_workspace_bytes(T, N, K, 1))
         return QMOE_ERR_ARG;
     cudaStream_t st = (cudaStream_t)stream;
-    uint8_t* at = static_cast<uint8_t*>(ws);
-    const size_t wide = w4::up256((size_t)N * K * 2);
-    int32_t* offsets = reinterpret_cast<int32_t*>(at + wide);
-    rc = w4::widen_any(dtype, format, N, K, group, w, s, at, offsets, (int)T, st);
-    if (rc != QMOE_OK) return rc;
-    return qmoe_expert_linear_dx(T, 1, N, K, dtype, dy, lddy, at, K, N * K, offsets, dx, dx_dtype, lddx, dev_status,
-                                 at + wide + 256, ws_bytes - wide - 256, stream);
+    eg::Scaled c = {nullptr, nullptr, T, N, K, dtype, nullptr, dev_status, ws, ws_bytes};
+    rc = w4::widen_any(c, format, group, w, s, 1, st);
+    return rc != QMOE_OK ? rc : eg::scaled_linear_dx(c, dy, lddy, dx, dx_dtype, lddx, st);
 }
