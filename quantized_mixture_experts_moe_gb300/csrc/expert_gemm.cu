@@ -70,7 +70,7 @@ struct Segments {
     int u, total, per;
     __device__ Segments(const Args& g, const int* off, const int* base) : walk(g, off, base, NT) {
         total = base[g.E + 1];
-        per = (g.red + STEP - 1) / STEP;
+        per = g.steps;
         u = (SPLIT ? base[g.E] : 0) + blockIdx.x;
         if (SPLIT) {
             const int64_t steps = (int64_t)base[g.E] * per;
@@ -167,14 +167,14 @@ expert_gemm_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_const
                 const int slot = it % C::STAGES;
                 if (!warp_wait(&empty[slot], (it / C::STAGES & 1) ^ 1, abort_flag, g.status)) break;
                 uint8_t* st = smem + slot * C::STAGE;
-                const int k0 = s * STEP;
+                const int second = s >= g.per, k0 = (s - (second ? g.per : 0)) * STEP, z = t.e + second;
                 if (lane == 0) {
                     tc::mbar_arrive_expect_tx(&full[slot], C::P_BYTES + (GATHER ? (t.n + 3) / 4 * 512 : boxes * Q_BOX * 128));
                     if constexpr (MODE == FWD) {
-                        tc::tma_load_3d(st, &map_p, &full[slot], k0, t.l0, t.e);
+                        tc::tma_load_3d(st, &map_p, &full[slot], k0, t.l0, z);
                     } else {
-                        tc::tma_load_3d(st, &map_p, &full[slot], t.l0, k0, t.e);
-                        tc::tma_load_3d(st + 8192, &map_p, &full[slot], t.l0 + 64, k0, t.e);
+                        tc::tma_load_3d(st, &map_p, &full[slot], t.l0, k0, z);
+                        tc::tma_load_3d(st + 8192, &map_p, &full[slot], t.l0 + 64, k0, z);
                     }
                 }
                 __syncwarp();
@@ -507,9 +507,9 @@ inline int64_t most_tiles(int64_t P, int E, int64_t lanes, int nt) {
 // takes 0.39 where all SMs load (HBM), 0.25 where few do; the join 2.5.  T=1 of 10
 // experts 4096 -> 2048 (160 tiles of 64 steps): 62 us in whole tiles, 51 shared;
 // 8 experts 2048 -> 1536 (96 of 32): 14.5 against 16.8.
-inline bool split(int64_t P, int E, int64_t lanes, int64_t red, int nt) {
+inline bool split(int64_t P, int E, int64_t lanes, int64_t per, int nt) {
     if (nt == 256) return false;
-    const int64_t tiles = ((P < E ? P : E) + P / nt) * ((lanes + 127) / 128), per = (red + STEP - 1) / STEP;
+    const int64_t tiles = ((P < E ? P : E) + P / nt) * ((lanes + 127) / 128);
     if (tiles > 2 * row::kSMs) return false;  // measured no faster, up to a fifth slower, with more
     const float busy = tiles < row::kSMs ? (float)tiles / row::kSMs : 1.f;
     const float whole = (float)((tiles + row::kSMs - 1) / row::kSMs) * per * (0.39f * busy > 0.25f ? 0.39f * busy : 0.25f);
@@ -540,7 +540,7 @@ static int run_rows(Mat w, Mat q, Args& g, int dtype, uint8_t* ws, size_t left, 
     if (rc != QMOE_OK) return rc;
     const int64_t most = most_tiles(g.P, g.E, g.lanes, nt);
     if (most >= (1ll << 31)) return QMOE_ERR_UNSUPPORTED;
-    const bool shares = split(g.P, g.E, g.lanes, g.red, nt);
+    const bool shares = split(g.P, g.E, g.lanes, g.steps, nt);
     if (shares) {
         if (left < part_bytes(nt)) return QMOE_ERR_ARG;  // asked for above
         g.parts = reinterpret_cast<float*>(ws);
@@ -564,6 +564,8 @@ struct Call {
     int k;
     int64_t x_rows;
     int32_t* status;
+    int parts = 1;              // of w, whose products are summed up (E is 1)
+    const float* by = nullptr;  // a factor of each output (y) or input (dx) of the layer
 };
 static int check(const Call& c) {
     if (c.P < 0 || c.E <= 0 || c.N <= 0 || c.K <= 0 || (c.dtype != QMOE_BF16 && c.dtype != QMOE_F16)) return QMOE_ERR_ARG;
@@ -587,26 +589,28 @@ extern "C" size_t qmoe_expert_copy_bytes(int64_t rows, int64_t cols) {
     return eg::padded(rows, cols);
 }
 
-extern "C" size_t qmoe_expert_workspace_bytes(int64_t P, int E, int64_t N, int64_t K, int op, int pairs) {
+static size_t product_bytes(int64_t P, int E, int64_t N, int64_t K, int op, int pairs, int parts) {
     if (P <= 0 || E <= 0 || N <= 0 || K <= 0 || op < 0 || op > 2 || P > eg::kMost || N > eg::kMost || K > eg::kMost) return 0;
     if (op == eg::DW) return pairs ? eg::padded(P, K) : 0;
     const int nt = eg::tile_of(P, E);
     if (nt == 256) return pairs && op == eg::FWD ? eg::padded(P, K) : 0;
-    return eg::split(P, E, op == eg::FWD ? N : K, op == eg::FWD ? K : N, nt) ? eg::part_bytes(nt) : 0;
+    return eg::split(P, E, op == eg::FWD ? N : K, (int64_t)parts * eg::steps_of(op == eg::FWD ? K : N), nt) ? eg::part_bytes(nt) : 0;
+}
+extern "C" size_t qmoe_expert_workspace_bytes(int64_t P, int E, int64_t N, int64_t K, int op, int pairs) {
+    return product_bytes(P, E, N, K, op, pairs, 1);
 }
 
 namespace qmoe {
 namespace eg {
 
-// by: of each output (y) or input (dx) of the layer, or NULL
-static int linear(const Call& c, const void* x, int64_t ldx, const void* w, int64_t ldw, int64_t w_expert, const float* by, void* y,
-                  int y_dtype, int64_t ldy, void* ws, size_t ws_bytes, cudaStream_t st) {
+static int linear(const Call& c, const void* x, int64_t ldx, const void* w, int64_t ldw, int64_t w_expert, void* y, int y_dtype,
+                  int64_t ldy, void* ws, size_t ws_bytes, cudaStream_t st) {
     int rc = check(c);
     if (rc != QMOE_OK) return rc;
     if ((y_dtype != c.dtype && y_dtype != QMOE_F32) || ldy < c.N) return QMOE_ERR_ARG;
     if (c.P == 0) return QMOE_OK;
     if (c.pairs && c.x_rows == 0) return QMOE_ERR_ARG;
-    Mat mw = {w, c.N, c.K, ldw, c.E, w_expert}, mx = {x, c.pairs ? c.x_rows : c.P, c.K, ldx, 1, 0};
+    Mat mw = {w, c.N, c.K, ldw, c.E * c.parts, w_expert}, mx = {x, c.pairs ? c.x_rows : c.P, c.K, ldx, 1, 0};
     if (!mat_ok(mw, 2) || !mat_ok(mx, 2) || !word_ok(c.offsets) || !y || !row::type_aligned(y, row::dtype_size(y_dtype)) ||
         !word_ok(c.status))
         return QMOE_ERR_ARG;
@@ -615,10 +619,10 @@ static int linear(const Call& c, const void* x, int64_t ldx, const void* w, int6
     const int size = row::dtype_size(y_dtype);
     Args g = {(int)c.P, c.E, (int)c.N, 0, (int)c.K, c.offsets, c.pairs, c.k, (int)mx.rows, y, ldy, 0, y_dtype,
               aligned16(y) && ldy * size % 16 == 0, c.dtype == QMOE_BF16 ? tc::idesc_bf16_f32(0, 0) : tc::idesc_f16_f32(0, 0), c.status,
-              nullptr, nullptr, by};
+              nullptr, nullptr, c.by, steps_of(c.K), steps_of(c.K) * c.parts};
     if (few(c.P, c.E, c.N, c.K, fits(mw))) return launch_few(mw, mx, g, c.dtype, st);
     const bool lay_out = c.pairs && tile_of(c.P, c.E) == 256;
-    const size_t need = qmoe_expert_workspace_bytes(c.P, c.E, c.N, c.K, FWD, c.pairs != nullptr);
+    const size_t need = product_bytes(c.P, c.E, c.N, c.K, FWD, c.pairs != nullptr, c.parts);
     if (left < need + copy_need(mw) + (lay_out ? 0 : copy_need(mx))) return QMOE_ERR_ARG;
     if ((rc = as_tma(mw, c.offsets, at, left, st)) != QMOE_OK) return rc;
     rc = lay_out ? copy_rows(mx, c.pairs, c.P, c.k, nullptr, at, left, st) : as_tma(mx, nullptr, at, left, st);
@@ -627,37 +631,37 @@ static int linear(const Call& c, const void* x, int64_t ldx, const void* w, int6
     return g.pairs ? run_rows<FWD, true>(mw, mx, g, c.dtype, at, left, st) : run_rows<FWD, false>(mw, mx, g, c.dtype, at, left, st);
 }
 
-static int linear_dx(const Call& c, const void* dy, int64_t lddy, const void* w, int64_t ldw, int64_t w_expert, const float* by, void* dx,
-                     int dx_dtype, int64_t lddx, void* ws, size_t ws_bytes, cudaStream_t st) {
+static int linear_dx(const Call& c, const void* dy, int64_t lddy, const void* w, int64_t ldw, int64_t w_expert, void* dx, int dx_dtype,
+                     int64_t lddx, void* ws, size_t ws_bytes, cudaStream_t st) {
     int rc = check(c);
     if (rc != QMOE_OK) return rc;
     if ((dx_dtype != c.dtype && dx_dtype != QMOE_F32) || lddx < c.K) return QMOE_ERR_ARG;
     if (c.P == 0) return QMOE_OK;
-    Mat mw = {w, c.N, c.K, ldw, c.E, w_expert}, my = {dy, c.P, c.N, lddy, 1, 0};
+    Mat mw = {w, c.N, c.K, ldw, c.E * c.parts, w_expert}, my = {dy, c.P, c.N, lddy, 1, 0};
     if (!mat_ok(mw, 2) || !mat_ok(my, 2) || !word_ok(c.offsets) || !dx || !row::type_aligned(dx, row::dtype_size(dx_dtype)) ||
         !word_ok(c.status))
         return QMOE_ERR_ARG;
     uint8_t* at = static_cast<uint8_t*>(ws);
     size_t left = ws && !(reinterpret_cast<uintptr_t>(ws) & 255u) ? ws_bytes : 0;
-    if (left < qmoe_expert_workspace_bytes(c.P, c.E, c.N, c.K, DX, 0) + copy_need(mw) + copy_need(my)) return QMOE_ERR_ARG;
+    if (left < product_bytes(c.P, c.E, c.N, c.K, DX, 0, c.parts) + copy_need(mw) + copy_need(my)) return QMOE_ERR_ARG;
     if ((rc = as_tma(mw, c.offsets, at, left, st)) != QMOE_OK || (rc = as_tma(my, nullptr, at, left, st)) != QMOE_OK) return rc;
     const int size = row::dtype_size(dx_dtype);
     Args g = {(int)c.P, c.E, (int)c.K, 0, (int)c.N, c.offsets, nullptr, 0, (int)c.P, dx, lddx, 0, dx_dtype,
               aligned16(dx) && lddx * size % 16 == 0,
-              (c.dtype == QMOE_BF16 ? tc::idesc_bf16_f32(0, 0) : tc::idesc_f16_f32(0, 0)) | 1u << 15, c.status, nullptr, nullptr, by};
+              (c.dtype == QMOE_BF16 ? tc::idesc_bf16_f32(0, 0) : tc::idesc_f16_f32(0, 0)) | 1u << 15, c.status, nullptr, nullptr, c.by,
+              steps_of(c.N), steps_of(c.N) * c.parts};
     return run_rows<DX, false>(mw, my, g, c.dtype, at, left, st);
 }
 
-size_t scaled_bytes(int64_t T, int64_t N, int64_t K, int dx) {
-    return qmoe_expert_copy_bytes(T, dx ? N : K) + qmoe_expert_workspace_bytes(T, 1, N, K, dx ? DX : FWD, 0);
+size_t scaled_bytes(int64_t T, int64_t N, int64_t K, int parts, int dx) {
+    return qmoe_expert_copy_bytes(T, dx ? N : K) + product_bytes(T, 1, N, K, dx ? DX : FWD, 0, parts);
 }
+static Call call_of(const Scaled& c) { return {c.T, c.N, c.K, 1, c.dtype, c.offsets, nullptr, 0, c.T, c.status, c.parts, c.by}; }
 int scaled_linear(const Scaled& c, const void* x, int64_t ldx, void* y, int y_dtype, int64_t ldy, cudaStream_t st) {
-    const Call call = {c.T, c.N, c.K, 1, c.dtype, c.offsets, nullptr, 0, c.T, c.status};
-    return linear(call, x, ldx, c.w, c.K, c.N * c.K, c.by, y, y_dtype, ldy, c.ws, c.ws_bytes, st);
+    return linear(call_of(c), x, ldx, c.w, c.K, c.N * c.K, y, y_dtype, ldy, c.ws, c.ws_bytes, st);
 }
 int scaled_linear_dx(const Scaled& c, const void* dy, int64_t lddy, void* dx, int dx_dtype, int64_t lddx, cudaStream_t st) {
-    const Call call = {c.T, c.N, c.K, 1, c.dtype, c.offsets, nullptr, 0, c.T, c.status};
-    return linear_dx(call, dy, lddy, c.w, c.K, c.N * c.K, c.by, dx, dx_dtype, lddx, c.ws, c.ws_bytes, st);
+    return linear_dx(call_of(c), dy, lddy, c.w, c.K, c.N * c.K, dx, dx_dtype, lddx, c.ws, c.ws_bytes, st);
 }
 
 }  // namespace eg
@@ -667,7 +671,7 @@ extern "C" int qmoe_expert_linear(int64_t P, int E, int64_t N, int64_t K, int dt
                                   int64_t x_rows, const int32_t* pairs, int k, const void* w, int64_t ldw, int64_t w_expert,
                                   const int32_t* offsets, void* y, int y_dtype, int64_t ldy, int32_t* dev_status, void* ws,
                                   size_t ws_bytes, qmoe_stream_t stream) {
-    return eg::linear({P, N, K, E, dtype, offsets, pairs, k, x_rows, dev_status}, x, ldx, w, ldw, w_expert, nullptr, y, y_dtype, ldy, ws,
+    return eg::linear({P, N, K, E, dtype, offsets, pairs, k, x_rows, dev_status}, x, ldx, w, ldw, w_expert, y, y_dtype, ldy, ws,
                       ws_bytes, (cudaStream_t)stream);
 }
 
@@ -675,7 +679,7 @@ extern "C" int qmoe_expert_linear_dx(int64_t P, int E, int64_t N, int64_t K, int
                                      const void* w, int64_t ldw, int64_t w_expert, const int32_t* offsets, void* dx,
                                      int dx_dtype, int64_t lddx, int32_t* dev_status, void* ws, size_t ws_bytes,
                                      qmoe_stream_t stream) {
-    return eg::linear_dx({P, N, K, E, dtype, offsets, nullptr, 0, 0, dev_status}, dy, lddy, w, ldw, w_expert, nullptr, dx, dx_dtype, lddx,
+    return eg::linear_dx({P, N, K, E, dtype, offsets, nullptr, 0, 0, dev_status}, dy, lddy, w, ldw, w_expert, dx, dx_dtype, lddx,
                          ws, ws_bytes, (cudaStream_t)stream);
 }
 
@@ -706,7 +710,7 @@ extern "C" int qmoe_expert_linear_dw(int64_t P, int E, int64_t N, int64_t K, int
     if (rc != QMOE_OK) return rc;
     eg::Args g = {(int)P, E, (int)N, (int)K, 0, offsets, nullptr, 0, (int)mx.rows, dw, K, N * K, dw_dtype,
                   aligned16(dw) && K * size % 16 == 0,
-                  (dtype == QMOE_BF16 ? tc::idesc_bf16_f32(0, 0) : tc::idesc_f16_f32(0, 0)) | 3u << 15, dev_status, nullptr, nullptr, nullptr};
+                  (dtype == QMOE_BF16 ? tc::idesc_bf16_f32(0, 0) : tc::idesc_f16_f32(0, 0)) | 3u << 15, dev_status, nullptr, nullptr, nullptr, 0, 0};
     CUtensorMap mp, mq;
     rc = eg::map_of(&mp, my, dtype, 64, eg::STEP, false);
     if (rc != QMOE_OK) return rc;

@@ -40,7 +40,9 @@ struct Args {
     float* parts;          // sums of tiles in parts (few tiles), and where they belong
     int4* joins;
     const float* by;       // y, dx: a factor of each lane's sums (NULL: none)
+    int per, steps;        // y, dx: steps of a matrix, and of all matrices whose products are summed up (one, or the two parts of w)
 };
+inline int steps_of(int64_t red) { return (int)((red + STEP - 1) / STEP); }
 
 // Operand whose reduction axis is not the contiguous one: blocks of 64 lanes (or
 // columns), 8192 bytes apart; in each, reduction rows of 128 bytes, swizzled in
@@ -174,7 +176,7 @@ struct Walk {
         t.q0 = r0 + q * per;
         t.n = min(per, r0 + count - t.q0);
         t.row0 = t.end = 0;
-        t.steps = e < g.E ? (g.red + STEP - 1) / STEP : 0;
+        t.steps = e < g.E ? g.steps : 0;
         return t;
     }
 };
@@ -573,11 +575,12 @@ inline bool fits(const Mat& m) {
     return aligned16(m.p) && (m.rows == 1 || m.ld % 8 == 0) && (m.experts == 1 || m.stride % 8 == 0);
 }
 
-// Products with one matrix w [N, K] of contiguous rows of a multiple of 8 values,
-// each of whose rows (y) or columns (dx) stands for `by` times what it holds.
-// ws: scaled_bytes (dx: 0 or 1).  offsets: {0, T} on the device.
+// Products with one matrix, the sum of w [parts, N, K] (parts 1 or 2; contiguous rows of
+// a multiple of 8 values), each of whose rows (y) or columns (dx) stands for `by` times
+// what it holds.  ws: scaled_bytes (dx: 0 or 1).  offsets: {0, T} on the device.
 struct Scaled {
     const void* w;
+    int parts;
     const float* by;
     int64_t T, N, K;
     int dtype;
@@ -586,7 +589,7 @@ struct Scaled {
     void* ws;
     size_t ws_bytes;
 };
-size_t scaled_bytes(int64_t T, int64_t N, int64_t K, int dx);
+size_t scaled_bytes(int64_t T, int64_t N, int64_t K, int parts, int dx);
 int scaled_linear(const Scaled& c, const void* x, int64_t ldx, void* y, int y_dtype, int64_t ldy, cudaStream_t st);
 int scaled_linear_dx(const Scaled& c, const void* dy, int64_t lddy, void* dx, int dx_dtype, int64_t lddx, cudaStream_t st);
 

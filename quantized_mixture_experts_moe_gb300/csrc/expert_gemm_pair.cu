@@ -181,16 +181,16 @@ expert_pair_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_const
                     if (!lane_wait(&empty[slot], (it / C::STAGES & 1) ^ 1, abort_flag, g.status)) break;
                     uint8_t* st = smem + slot * C::STAGE;
                     uint8_t* sq = st + C::P_BYTES;
-                    const int k0 = s * STEP, row = t.row0 + k0;
+                    const int second = MODE != DW && s >= g.per, k0 = (s - (second ? g.per : 0)) * STEP, z = t.e + second, row = t.row0 + k0;
                     const bool relay = MODE == DW && t.end - row < STEP;
                     const uint32_t bar = bar_in(&full[slot], relay ? rank : 0);
                     if (relay) tc::mbar_arrive_expect_tx(&full[slot], bytes);
                     else if (rank == 0) tc::mbar_arrive_expect_tx(&full[slot], 2 * bytes);
                     if constexpr (MODE == FWD) {
-                        pair_load_3d(st, &map_p, bar, k0, l0, t.e);
+                        pair_load_3d(st, &map_p, bar, k0, l0, z);
                     } else if constexpr (MODE == DX) {
-                        pair_load_3d(st, &map_p, bar, l0, k0, t.e);
-                        pair_load_3d(st + 8192, &map_p, bar, l0 + 64, k0, t.e);
+                        pair_load_3d(st, &map_p, bar, l0, k0, z);
+                        pair_load_3d(st + 8192, &map_p, bar, l0 + 64, k0, z);
                     } else {
                         pair_load_2d(st, &map_p, bar, l0, row);
                         pair_load_2d(st + 8192, &map_p, bar, l0 + 64, row);

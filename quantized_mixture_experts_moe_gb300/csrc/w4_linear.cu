@@ -31,6 +31,7 @@
 // 178 MB): 56 us, 3.1 TB/s, with 53% of the issue slots busy and the integer pipe,
 // which converts, in the way; int4 64 us (104 at first, a CTA a tile and eight
 // operations for two E2M1 codes).  One token 2048 -> 2816, int4: 4.1 us, latency.
+#include <algorithm>
 #include <type_traits>
 
 #include "expert_gemm.cuh"
@@ -574,10 +575,12 @@ __global__ void __launch_bounds__(THREADS, NT == 1 ? 2 : 1) w4_few_kernel(const 
 __device__ __forceinline__ uint32_t e2m1_pair(uint32_t byte) { return pair_of<__half, QMOE_W4_E2M1, 0>(byte); }
 
 // W in 16 bits, [N, K], and {0, T} for the grouped product with one expert.  The
-// tensor core takes no scale for each group of int4 values beside 16-bit x, so a
-// weight is rounded to x's type, by half a step at most (bf16: 0.0024 of the result's
-// norm off, of which 0.0017 is the output's own rounding; E2M1 values with their power
-// of two are exact).
+// tensor core takes no scale for each group of values beside 16-bit x, so the weights
+// are multiplied with it here.  E2M1 values with their power of two are exact; an int4
+// value has 14 bits with its scale's 11, so that W becomes two matrices whose sum is
+// exact, the values rounded to x's type and what is left of them, and the product
+// takes twice the steps.  (Rounded once: bf16 0.0024 of the result's norm off, of which
+// 0.0017 is the output's own rounding, fp16 2.8e-4 and 2.1e-4.)
 //
 // Scales may lie anywhere in fp16 (int4) or from 2^-127 to 2^127 (E2M1), weights in
 // fp16 may not.  So each row (the product), or each column (the gradient), is divided
@@ -690,6 +693,14 @@ __global__ void __launch_bounds__(256) w4_widen_kernel(const Widen a) {
                     d[2 * q + 1] = f[j] * c.y;
                 }
                 row::store<8>(reinterpret_cast<T*>(to + i0 + j * STEP), d);
+                if constexpr (FORMAT == QMOE_W4_INT4) {
+#pragma unroll
+                    for (int q = 0; q < 8; ++q) {
+                        const float high = row::to_f32(row::from_f32<T>(d[q]));
+                        d[q] = isfinite(high) ? d[q] - high : 0.f;
+                    }
+                    row::store<8>(reinterpret_cast<T*>(to + a.N * words + i0 + j * STEP), d);
+                }
             }
     }
 }
@@ -768,10 +779,22 @@ static int widen(const Widen& a, int dx, cudaStream_t st) {
     const int rc = launch_pdl(w4_columns_kernel<FORMAT>, dim3((unsigned)((groups + 1) / 2)), dim3(1024), 0, st, a);
     return rc != QMOE_OK ? rc : widen_rows<T, FORMAT, false>(a, st);
 }
+// Tokens up to which the codes are multiplied as they are, QMOE_W4_FEW of them by a
+// launch.  us of two launches and widened, int4 bf16 in groups of 128, 17, 24 and 32
+// tokens: 2816 x 2048 13.0 14.6 17.1 and 18.6 18.6 18.8; 2816 x 4096 21.5 25.5 29.5 and
+// 23.7 23.7 23.9; 4096 x 4096 21.8 25.7 29.8 and 30.7 30.8 31.1; 8192 x 8192 99 109 161
+// and 106 106 107.  E2M1, which becomes one matrix, 4096 x 4096: 22.2 from 17 on, one
+// launch of 16 tokens 16.1.
+inline int unwidened(int format) { return format == QMOE_W4_INT4 ? 24 : QMOE_W4_FEW; }
+inline int parts_of(int format) { return format == QMOE_W4_INT4 ? 2 : 1; }
+inline size_t widened_bytes(int64_t T, int64_t N, int64_t K, int parts, int dx) {
+    return up256((size_t)N * K * 2 * parts) + up256((size_t)(dx ? K : N) * 4) + 256 + eg::scaled_bytes(T, N, K, parts, dx);
+}
 // Widens W into the workspace: {W, by, offsets, what the product needs}.
 static int widen_any(eg::Scaled& c, int format, int group, const uint8_t* w, const void* s, int dx, cudaStream_t st) {
     uint8_t* at = static_cast<uint8_t*>(c.ws);
-    const size_t wide = up256((size_t)c.N * c.K * 2), lanes = up256((size_t)(dx ? c.K : c.N) * 4), before = wide + lanes + 256;
+    c.parts = parts_of(format);
+    const size_t wide = up256((size_t)c.N * c.K * 2 * c.parts), lanes = up256((size_t)(dx ? c.K : c.N) * 4), before = wide + lanes + 256;
     const Widen a = {c.N, c.K, log2_of(group), reinterpret_cast<const uint32_t*>(w), s, reinterpret_cast<uint4*>(at),
                      reinterpret_cast<float*>(at + wide), dx ? c.K : c.N, reinterpret_cast<int32_t*>(at + wide + lanes), (int)c.T};
     c.w = at;
@@ -807,7 +830,8 @@ using namespace qmoe;
 
 extern "C" size_t qmoe_w4_workspace_bytes(int64_t T, int64_t N, int64_t K, int dx) {
     if (T <= 0 || N <= 0 || K <= 0 || (!dx && T <= QMOE_W4_FEW)) return 0;
-    return w4::up256((size_t)N * K * 2) + w4::up256((size_t)(dx ? K : N) * 4) + 256 + eg::scaled_bytes(T, N, K, dx);
+    // of either format
+    return std::max(w4::widened_bytes(T, N, K, 1, dx), w4::widened_bytes(T, N, K, 2, dx));
 }
 
 extern "C" int qmoe_w4_linear(int64_t T, int k, int E, int64_t N, int64_t K, int format, int group, int dtype, const void* x,
@@ -820,9 +844,10 @@ extern "C" int qmoe_w4_linear(int64_t T, int k, int E, int64_t N, int64_t K, int
     if (!w4::arrays_ok(x, ldx, K, w, s, format, y, y_dtype, dev_status) || (ids && !row::type_aligned(ids, 4))) return QMOE_ERR_ARG;
     if (ids && (T * k > 32768 || (int64_t)E * N > w4::kMost)) return QMOE_ERR_UNSUPPORTED;
     cudaStream_t st = (cudaStream_t)stream;
-    if (!ids && T > QMOE_W4_FEW) {
-        if (!ws || (reinterpret_cast<uintptr_t>(ws) & 255u) || ws_bytes < qmoe_w4_workspace_bytes(T, N, K, 0)) return QMOE_ERR_ARG;
-        eg::Scaled c = {nullptr, nullptr, T, N, K, dtype, nullptr, dev_status, ws, ws_bytes};
+    if (!ids && T > QMOE_W4_FEW && (!ws || (reinterpret_cast<uintptr_t>(ws) & 255u) || ws_bytes < qmoe_w4_workspace_bytes(T, N, K, 0)))
+        return QMOE_ERR_ARG;
+    if (!ids && T > w4::unwidened(format)) {
+        eg::Scaled c = {nullptr, 1, nullptr, T, N, K, dtype, nullptr, dev_status, ws, ws_bytes};
         rc = w4::widen_any(c, format, group, w, s, 0, st);
         return rc != QMOE_OK ? rc : eg::scaled_linear(c, x, ldx, y, y_dtype, ldy, st);
     }
@@ -840,11 +865,20 @@ extern "C" int qmoe_w4_linear(int64_t T, int k, int E, int64_t N, int64_t K, int
                   y_dtype, 0, 0, 0, 0,
                   group == 32 && K % 64 == 0 && row::type_aligned(s, format == QMOE_W4_INT4 ? 4 : 2), (int)(ids ? T * k : 0), 1,
                   dev_status};
-    if (dtype == QMOE_BF16)
-        return format == QMOE_W4_INT4 ? w4::few_tokens<__nv_bfloat16, QMOE_W4_INT4>(map, g, st)
-                                      : w4::few_tokens<__nv_bfloat16, QMOE_W4_E2M1>(map, g, st);
-    return format == QMOE_W4_INT4 ? w4::few_tokens<__half, QMOE_W4_INT4>(map, g, st)
-                                  : w4::few_tokens<__half, QMOE_W4_E2M1>(map, g, st);
+    const int size = row::dtype_size(y_dtype);
+    for (int64_t left = T; left > 0 && rc == QMOE_OK;) {
+        g.T = ids ? (int)T : (int)(left < QMOE_W4_FEW ? left : QMOE_W4_FEW);
+        if (dtype == QMOE_BF16)
+            rc = format == QMOE_W4_INT4 ? w4::few_tokens<__nv_bfloat16, QMOE_W4_INT4>(map, g, st)
+                                        : w4::few_tokens<__nv_bfloat16, QMOE_W4_E2M1>(map, g, st);
+        else
+            rc = format == QMOE_W4_INT4 ? w4::few_tokens<__half, QMOE_W4_INT4>(map, g, st)
+                                        : w4::few_tokens<__half, QMOE_W4_E2M1>(map, g, st);
+        left -= g.T;
+        g.x = static_cast<const uint8_t*>(g.x) + g.T * ldx * 2;
+        g.y = static_cast<uint8_t*>(g.y) + g.T * ldy * size;
+    }
+    return rc;
 }
 
 extern "C" int qmoe_w4_linear_dx(int64_t T, int64_t N, int64_t K, int format, int group, int dtype, const void* dy, int64_t lddy,
@@ -857,7 +891,7 @@ extern "C" int qmoe_w4_linear_dx(int64_t T, int64_t N, int64_t K, int format, in
         ws_bytes < qmoe_w4_workspace_bytes(T, N, K, 1))
         return QMOE_ERR_ARG;
     cudaStream_t st = (cudaStream_t)stream;
-    eg::Scaled c = {nullptr, nullptr, T, N, K, dtype, nullptr, dev_status, ws, ws_bytes};
+    eg::Scaled c = {nullptr, 1, nullptr, T, N, K, dtype, nullptr, dev_status, ws, ws_bytes};
     rc = w4::widen_any(c, format, group, w, s, 1, st);
     return rc != QMOE_OK ? rc : eg::scaled_linear_dx(c, dy, lddy, dx, dx_dtype, lddx, st);
 }
