@@ -10,14 +10,22 @@
 namespace qmoe {
 namespace er {
 
-// s(v) = 1 / (1 + exp(-v)).  For 16-bit values the fast exponential: its error is
-// some 2^-22 |v| relative, |v| < 2^7 where s is not 0 or 1, against 2^-11 of the
-// rounding that follows.
+// s(v) = 1 / (1 + exp(-v)), as e / (1 + e) with e = exp(v) for v < 0: a divisor is
+// never above 2 (the fast division gives 0 for divisors above 2^126, which is v below
+// -87.3).  For 16-bit values the fast exponential: its error is up to 2 + 1.2 |v| ulp,
+// 2^-16 relative where s is least, against 2^-12 of the rounding that follows.
 template <typename T>
 __device__ __forceinline__ float sigmoid(float v) {
-    if constexpr (sizeof(T) == 4) return 1.0f / (1.0f + expf(-v));
-    else return __fdividef(1.0f, 1.0f + __expf(-v));
+    if constexpr (sizeof(T) == 4) {
+        const float e = expf(-fabsf(v));
+        return (v >= 0.f ? 1.0f : e) / (1.0f + e);
+    } else {
+        const float e = __expf(-fabsf(v));
+        return __fdividef(v >= 0.f ? 1.0f : e, 1.0f + e);
+    }
 }
+template <typename T>
+__device__ __forceinline__ float swiglu_of(float g, float u) { return g * sigmoid<T>(g) * u; }
 
 // One value, or two that lie in one aligned word (16-bit types).
 template <typename T, int VEC> struct Pair {
@@ -53,7 +61,7 @@ swiglu_kernel(int64_t total, uint32_t per_row, int64_t I, const T* gu, int64_t l
         row::widen<VEC>(a, g);
         row::widen<VEC>(b, u);
 #pragma unroll
-        for (int j = 0; j < VEC; ++j) g[j] = g[j] * sigmoid<T>(g[j]) * u[j];
+        for (int j = 0; j < VEC; ++j) g[j] = swiglu_of<T>(g[j], u[j]);
         row::store<VEC>(h + r * ldh + c, g);
     }
 }
@@ -113,7 +121,7 @@ __global__ void __launch_bounds__(256) swiglu_odd_kernel(int64_t rows, int64_t I
                     a[i].widen(g);
                     b[i].widen(u);
 #pragma unroll
-                    for (int j = 0; j < VEC; ++j) g[j] = g[j] * sigmoid<T>(g[j]) * u[j];
+                    for (int j = 0; j < VEC; ++j) g[j] = swiglu_of<T>(g[j], u[j]);
                     Pair<T, VEC>::store(h + r * ldh + c + i * 32 * VEC, g);
                 }
         }
