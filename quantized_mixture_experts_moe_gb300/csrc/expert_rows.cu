@@ -26,6 +26,15 @@ __device__ __forceinline__ float sigmoid(float v) {
 }
 template <typename T>
 __device__ __forceinline__ float swiglu_of(float g, float u) { return g * sigmoid<T>(g) * u; }
+// The gradients in place of g and u, and h.  The factors that are at most 1.1 come
+// before dh: dh u alone may leave fp32 where dg does not.
+template <typename T>
+__device__ __forceinline__ float swiglu_grad(float dh, float& g, float& u) {
+    const float s = sigmoid<T>(g), gs = g * s, h = gs * u, dg = u * (s * (1.0f + g * (1.0f - s))) * dh;
+    u = dh * gs;
+    g = dg;
+    return h;
+}
 
 // One value, or two that lie in one aligned word (16-bit types).
 template <typename T, int VEC> struct Pair {
@@ -85,14 +94,9 @@ swiglu_backward_kernel(int64_t total, uint32_t per_row, int64_t I, const T* dh, 
         row::widen<VEC>(e, d);
         float o[VEC];
 #pragma unroll
-        for (int j = 0; j < VEC; ++j) {
-            const float s = sigmoid<T>(g[j]), gs = g[j] * s;
-            o[j] = gs * u[j];
-            u[j] = d[j] * u[j] * s * (1.0f + g[j] * (1.0f - s));
-            g[j] = d[j] * gs;
-        }
-        row::store<VEC>(dgu + r * lddgu + c, u);
-        row::store<VEC>(dgu + r * lddgu + I + c, g);
+        for (int j = 0; j < VEC; ++j) o[j] = swiglu_grad<T>(d[j], g[j], u[j]);
+        row::store<VEC>(dgu + r * lddgu + c, g);
+        row::store<VEC>(dgu + r * lddgu + I + c, u);
         if (h) row::store<VEC>(h + r * ldh + c, o);
     }
 }
@@ -151,14 +155,9 @@ swiglu_backward_odd_kernel(int64_t rows, int64_t I, const T* dh, int64_t lddh, c
                     b[i].widen(u);
                     e[i].widen(d);
 #pragma unroll
-                    for (int j = 0; j < VEC; ++j) {
-                        const float s = sigmoid<T>(g[j]), gs = g[j] * s;
-                        o[j] = gs * u[j];
-                        u[j] = d[j] * u[j] * s * (1.0f + g[j] * (1.0f - s));
-                        g[j] = d[j] * gs;
-                    }
-                    Pair<T, VEC>::store(dgu + r * lddgu + c + i * 32 * VEC, u);
-                    Pair<T, VEC>::store(dgu + r * lddgu + I + c + i * 32 * VEC, g);
+                    for (int j = 0; j < VEC; ++j) o[j] = swiglu_grad<T>(d[j], g[j], u[j]);
+                    Pair<T, VEC>::store(dgu + r * lddgu + c + i * 32 * VEC, g);
+                    Pair<T, VEC>::store(dgu + r * lddgu + I + c + i * 32 * VEC, u);
                     if (h) Pair<T, VEC>::store(h + r * ldh + c + i * 32 * VEC, o);
                 }
         }

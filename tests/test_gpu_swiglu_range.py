@@ -44,6 +44,20 @@ def test_gates_about_the_least_sigmoid(I, dtype):
     close(dgu, grad, 2 * torch.cat([e, e], 1) * grad.abs() + 2.0 ** -149, "dgu")
 
 
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("I", [64, 65, 66])
+def test_large_gradients_of_closed_gates(I, dtype):
+    """dh u is 10^50, the gate's factor brings it back."""
+    gu = rows([-60.0, -70.0, -80.0, -86.0], 1e25, I, dtype)
+    dh = (torch.ones(3, I) * 1e25).to(dtype)
+    dgu, _ = qb.swiglu_backward(dh.cuda(), gu.cuda())
+    leaf = gu.double().requires_grad_()
+    grad, = torch.autograd.grad(ref.swiglu(leaf), leaf, dh.double())
+    assert grad.abs().max() < 1e38
+    e = err(gu, I, dtype)
+    close(dgu, grad, 2 * torch.cat([e, e], 1) * grad.abs(), "dgu")
+
+
 @pytest.mark.parametrize("dtype", [F32, BF16, F16])
 def test_infinite_gates(dtype):
     """silu(+inf) is +inf; -inf times 0 is NaN, as by the formula; NaN stays NaN."""
