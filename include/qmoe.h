@@ -689,10 +689,13 @@ int qmoe_fp8_linear(int64_t M, int64_t N, int64_t K, int x_dtype, const void* x,
  *   (op 0 for qmoe_expert_linear, 1 for ..._dx, 2 for ..._dw; pairs: whether they are
  *   given), and for each x, dy or w whose base or strides are no multiples of 16
  *   bytes, which is copied first, qmoe_expert_copy_bytes(rows, columns) (for w E * N
- *   rows; x with pairs as it lies).
+ *   rows; x with pairs as it lies).  But qmoe_expert_linear needs none at all where w is
+ *   such and qmoe_expert_linear_in_place is 1: few rows, beside which w is read as it
+ *   lies.
  * E <= 1024, other sizes <= 2^30. */
 size_t qmoe_expert_copy_bytes(int64_t rows, int64_t cols);
 size_t qmoe_expert_workspace_bytes(int64_t P, int E, int64_t N, int64_t K, int op, int pairs);
+int qmoe_expert_linear_in_place(int64_t P, int E, int64_t N, int64_t K);
 int qmoe_expert_linear(int64_t P, int E, int64_t N, int64_t K, int dtype, const void* x, int64_t ldx, int64_t x_rows,
                        const int32_t* pairs, int k, const void* w, int64_t ldw, int64_t w_expert,
                        const int32_t* offsets, void* y, int y_dtype, int64_t ldy, int32_t* dev_status, void* ws,

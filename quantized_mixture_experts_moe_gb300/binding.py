@@ -112,6 +112,7 @@ SIGNATURES = {
     "qmoe_fp8_linear": ([_i64, _i64, _i64, _i32, _vp, _i64, _MP, _vp, _i32, _i64, _vp, _vp, _sz, _vp], _i32),
     "qmoe_expert_copy_bytes": ([_i64, _i64], _sz),
     "qmoe_expert_workspace_bytes": ([_i64, _i32, _i64, _i64, _i32, _i32], _sz),
+    "qmoe_expert_linear_in_place": ([_i64, _i32, _i64, _i64], _i32),
     "qmoe_expert_linear": ([_i64, _i32, _i64, _i64, _i32, _vp, _i64, _i64, _vp, _i32, _vp, _i64, _i64, _vp, _vp, _i32, _i64, _vp,
                             _vp, _sz, _vp], _i32),
     "qmoe_expert_linear_dx": ([_i64, _i32, _i64, _i64, _i32, _vp, _i64, _vp, _i64, _i64, _vp, _vp, _i32, _i64, _vp, _vp, _sz,

@@ -645,7 +645,9 @@ PyObject* expert_linear(const Args& a) {  // x, w, offsets, pairs, k, out_dtype,
     const at::Tensor y = make({g.P, m.N}, yt, x);
     const int yc = code_of(yt);
     const int32_t* offsets = vec_of<int32_t>(&a.tensor(2), m.E + 1, at::kInt);
-    const MaybeWorkspace ws(product_bytes(g, m, 0) + copy_of(g.x, g.rows, m.K) + copy_of(m), a.maybe(7), x);
+    const size_t copied = copy_of(m);
+    const bool in_place = copied && qmoe_expert_linear_in_place(g.P, (int)m.E, m.N, m.K);
+    const MaybeWorkspace ws(in_place ? 0 : product_bytes(g, m, 0) + copy_of(g.x, g.rows, m.K) + copied, a.maybe(7), x);
     check(qmoe_expert_linear(g.P, (int)m.E, m.N, m.K, code, g.x.p, g.x.ld, g.rows, g.pairs, g.k, m.p, m.ld, m.stride,
                              offsets, y.data_ptr(), yc, m.N, status_of(a.tensor(6)), ws.p, ws.n, stream_of(x)),
           "qmoe_expert_linear");

@@ -523,8 +523,8 @@ inline size_t part_bytes(int nt) { return (size_t)row::kSMs * 2 * nt * 128 * 4 +
 // boundaries, where its CTAs (8.5 ns each, or the time of their 16 rows of w at 2.3
 // TB/s) take less than a copy of the weights.  One token x 8 of 128 experts, 2047 ->
 // 1536: 22 us against 255; 141 x 7 of 256, 1095 -> 1408: 905 against 400.
-inline bool few(int64_t P, int E, int64_t N, int64_t K, bool fit) {
-    if (fit || P > 65535) return false;
+inline bool few(int64_t P, int E, int64_t N, int64_t K) {
+    if (P > 65535) return false;
     const double cta = K * 32 / 2.3e6 > 0.0085 ? K * 32 / 2.3e6 : 0.0085;
     const double copied = (double)(P < E ? P : E) * N * K * 4 / 6e6;
     return (double)P * ((N + 15) / 16) * cta < copied + 4;
@@ -599,6 +599,9 @@ static size_t product_bytes(int64_t P, int E, int64_t N, int64_t K, int op, int 
 extern "C" size_t qmoe_expert_workspace_bytes(int64_t P, int E, int64_t N, int64_t K, int op, int pairs) {
     return product_bytes(P, E, N, K, op, pairs, 1);
 }
+extern "C" int qmoe_expert_linear_in_place(int64_t P, int E, int64_t N, int64_t K) {
+    return P >= 0 && E > 0 && N > 0 && K > 0 && eg::few(P, E, N, K);
+}
 
 namespace qmoe {
 namespace eg {
@@ -620,7 +623,7 @@ static int linear(const Call& c, const void* x, int64_t ldx, const void* w, int6
     Args g = {(int)c.P, c.E, (int)c.N, 0, (int)c.K, c.offsets, c.pairs, c.k, (int)mx.rows, y, ldy, 0, y_dtype,
               aligned16(y) && ldy * size % 16 == 0, c.dtype == QMOE_BF16 ? tc::idesc_bf16_f32(0, 0) : tc::idesc_f16_f32(0, 0), c.status,
               nullptr, nullptr, c.by, steps_of(c.K), steps_of(c.K) * c.parts};
-    if (few(c.P, c.E, c.N, c.K, fits(mw))) return launch_few(mw, mx, g, c.dtype, st);
+    if (!fits(mw) && few(c.P, c.E, c.N, c.K)) return launch_few(mw, mx, g, c.dtype, st);
     const bool lay_out = c.pairs && tile_of(c.P, c.E) == 256;
     const size_t need = product_bytes(c.P, c.E, c.N, c.K, FWD, c.pairs != nullptr, c.parts);
     if (left < need + copy_need(mw) + (lay_out ? 0 : copy_need(mx))) return QMOE_ERR_ARG;

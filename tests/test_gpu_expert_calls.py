@@ -1,0 +1,56 @@
+"""GPU tests of what the calls around the experts' products ask for: workspaces, operands that one gradient does not need,
+refusals."""
+
+import pytest
+import torch
+
+from quantized_mixture_experts_moe_gb300 import binding as qb
+from tests import expert_ref as ref
+from tests.block_ref import close
+
+pytestmark = pytest.mark.gpu
+
+F32, BF16, F16 = torch.float32, torch.bfloat16, torch.float16
+
+
+def offsets_of(counts):
+    return torch.tensor([0] + counts, device="cuda").cumsum(0).int()
+
+
+def randn(seed, *shape, dtype=BF16):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    return torch.randn(*shape, generator=g, device="cuda").to(dtype)
+
+
+def test_few_rows_beside_odd_weights_take_no_copy_of_them():
+    """One token on all experts' odd weights, which are read as they lie: 66 MB would be the copy that nobody writes."""
+    E, N, K = 32, 511, 2047
+    w, x = randn(1, E, N, K), randn(2, 2, K)
+    offsets = offsets_of([0] * 7 + [1] + [0] * 20 + [1] + [0] * 3)
+    assert qb.lib().qmoe_expert_linear_in_place(2, E, N, K) == 1
+    qb.expert_linear(x, w, offsets)
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    held = torch.cuda.memory_allocated()
+    torch.cuda.reset_peak_memory_stats()
+    y = qb.expert_linear(x, w, offsets)
+    assert torch.cuda.max_memory_allocated() - held < 1 << 20
+    close(y, *ref.linear(x.cpu().double(), w.cpu().double(), offsets.cpu()), "y")
+
+
+def test_workspaces_that_are_too_small_are_refused():
+    x, w, off = randn(3, 1, 4096), randn(4, 1, 4096, 4096), offsets_of([1])
+    need = qb.lib().qmoe_expert_workspace_bytes(1, 1, 4096, 4096, 0, 0)
+    assert need > 0
+    byte = lambda n: torch.empty(n, dtype=torch.uint8, device="cuda")
+    for n in (1, need - 1):
+        with pytest.raises(qb.QmoeError):
+            qb.expert_linear(x, w, off, ws=byte(n))
+    want = qb.expert_linear(x, w, off)
+    assert torch.equal(qb.expert_linear(x, w, off, ws=byte(need)), want)
+    odd, rows = randn(5, 2, 64, 65), randn(6, 600, 65)
+    offsets, copies = offsets_of([300, 300]), qb.lib().qmoe_expert_copy_bytes(128, 65) + qb.lib().qmoe_expert_copy_bytes(600, 65)
+    assert not qb.lib().qmoe_expert_linear_in_place(600, 2, 64, 65)
+    with pytest.raises(qb.QmoeError):
+        qb.expert_linear(rows, odd, offsets, ws=byte(copies - 256))
+    assert torch.equal(qb.expert_linear(rows, odd, offsets, ws=byte(copies)), qb.expert_linear(rows, odd, offsets))
