@@ -1,6 +1,6 @@
 // y[s] = w[e] x[s] for few rows an expert and weights whose rows lie off the 16-byte
-// boundaries, where TMA cannot read them and a copy would take all experts' bytes
-// twice: they go from HBM into the registers of mma.sync m16n8k16, 16 rows of w and
+// boundaries, where TMA cannot read them and a copy would take the experts' bytes
+// twice more: they go from HBM into the registers of mma.sync m16n8k16, 16 rows of w and
 // 8 rows of x, by aligned loads and shifts.  The order of the
 // reduction is free, so a lane's operand is 16 contiguous bytes of its row of w
 // and of its row of x.  A CTA takes 16 rows of one expert; its 8 warps share the
@@ -9,8 +9,8 @@
 // The CTA of slot s works for the expert whose first row s is, the others of the
 // expert end: no expert without rows costs anything, and every CTA finds its
 // expert in one parallel look at the offsets.  One token x 8 of 128 experts, 2047 ->
-// 1536: 22 us, 2.3 TB/s, bounded by the latency of a CTA's few rounds of loads; 255
-// with a copy of the weights.
+// 1536: 22 us, 2.3 TB/s, bounded by the latency of a CTA's few rounds of loads; 41
+// with a copy of the eight experts' weights.
 #include "expert_gemm.cuh"
 
 namespace qmoe {

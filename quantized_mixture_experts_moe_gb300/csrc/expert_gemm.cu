@@ -519,15 +519,20 @@ inline bool split(int64_t P, int E, int64_t lanes, int64_t per, int nt) {
 }
 inline size_t part_bytes(int nt) { return (size_t)row::kSMs * 2 * nt * 128 * 4 + (row::kSMs * 16 + 255) / 256 * 256; }
 
-// Whether y is better made by expert_few_kernel: for weights off the 16-byte
-// boundaries, where its CTAs (8.5 ns each, or the time of their 16 rows of w at 2.3
-// TB/s) take less than a copy of the weights.  One token x 8 of 128 experts, 2047 ->
-// 1536: 22 us against 255; 141 x 7 of 256, 1095 -> 1408: 905 against 400.
+// Whether y is better made by expert_few_kernel, for weights off the 16-byte
+// boundaries: by a model of the times in us fitted to GB300.  In place: 3 and, shared by
+// all SMs, 16.5 ns for each CTA of 16 rows of an expert's w and 1024 of their values,
+// 5 ns for one whose row is not its expert's first.  Copied: 10, the copy of the
+// experts that have rows (6 TB/s) and the product that reads it (5.3 TB/s).  In place
+// and copied, tokens x experts: 1 x 8 of 128, 2047 -> 1536, 22 and 41; 4 x 8 101 and
+// 104; 1 x 8, 513 -> 767, 7.5 and 18, 4 x 8 29 and 26; 16 x 7 of 256, 1095 -> 1408, 242
+// and 152; 1 x 10 of 512, 4095 -> 2047, 69 and 131; 1, 4 and 16 rows of one matrix, 4095
+// -> 4096, 16 20 41 and 24 29 29.
 inline bool few(int64_t P, int E, int64_t N, int64_t K) {
     if (P > 65535) return false;
-    const double cta = K * 32 / 2.3e6 > 0.0085 ? K * 32 / 2.3e6 : 0.0085;
-    const double copied = (double)(P < E ? P : E) * N * K * 4 / 6e6;
-    return (double)P * ((N + 15) / 16) * cta < copied + 4;
+    const double touched = (double)(P < E ? P : E), tiles = (double)((N + 15) / 16);
+    const double in_place = 3 + touched * tiles * 0.0165 * (double)((K + 1023) / 1024) + (P - touched) * tiles * 0.005;
+    return in_place < 10 + touched * N * K * (4 / 6e6 + 2 / 5.3e6);
 }
 
 template <int MODE, bool GATHER>
