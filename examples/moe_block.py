@@ -115,9 +115,9 @@ class TrainedExperts:
         k = s["w"].shape[1]
         dy, dw = qb.combine_backward(dout, s["y"], s["w"], s["slot"], s["offsets"])
         # dh needs no h, and dw2 does: the product's two gradients are asked for one by one
-        dh, _ = qb.expert_linear_backward(dy, dy.new_empty(dy.shape[0], self.w2.shape[2]), self.w2, s["offsets"], need_dw=False)
+        dh, _ = qb.expert_linear_backward(dy, None, self.w2, s["offsets"], need_dw=False)
         dgu, h = qb.swiglu_backward(dh, s["gu"], h_too=True)
-        _, dw2 = qb.expert_linear_backward(dy, h, self.w2, s["offsets"], need_dx=False)
+        _, dw2 = qb.expert_linear_backward(dy, h, None, s["offsets"], need_dx=False)
         dn, dw1 = qb.expert_linear_backward(dgu, s["n"], self.w1, s["offsets"], pairs=s["pairs"], k=k)
         return qb.combine(dn, None, s["slot"]), dw, dw1, dw2
 

@@ -698,7 +698,8 @@ def expert_linear(x, w, offsets, pairs=None, k=1, out_dtype=None, dev_status=Non
 def expert_linear_backward(dy, x, w, offsets, pairs=None, k=1, dw_dtype=None, need_dx=True, need_dw=True, dev_status=None, ws=None,
                            stream=None):
     """Gradients of expert_linear: (dx [P, K] in x's type, dw [E, N, K] in fp32, or the weights' type by dw_dtype), None for one
-    that is not needed.  dx is one row for each slot; with pairs the gradient of x is combine(dx, None, pair_slot)."""
+    that is not needed.  dx is one row for each slot; with pairs the gradient of x is combine(dx, None, pair_slot).  x may be
+    None where only dx is needed, w where only dw is."""
     if stream is not None:
         with torch.cuda.stream(stream):
             return expert_linear_backward(dy, x, w, offsets, pairs, k, dw_dtype, need_dx, need_dw, dev_status, ws)

@@ -655,30 +655,48 @@ PyObject* expert_linear(const Args& a) {  // x, w, offsets, pairs, k, out_dtype,
 }
 
 PyObject* expert_linear_backward(const Args& a) {  // dy, x, w, offsets, pairs, k, dw_dtype, need_dx, need_dw, dev_status, ws
-    const at::Tensor &dy = a.tensor(0), &x = a.tensor(1), &w = a.tensor(2);
-    const Experts m = experts_of(w, "expert_linear_backward");
-    const Gathered g = gathered(x, a.maybe(4), a.whole(5), "expert_linear_backward");
-    if (x.size(1) != m.K) bad("the reduction lengths differ: " + shape_str(x) + " and " + shape_str(w));
+    const at::Tensor &dy = a.tensor(0), *x = a.maybe(1), *w = a.maybe(2), &off = a.tensor(3);
+    const bool to_x = a.truth(7), to_w = a.truth(8);
+    if (to_x && !w) bad("expert_linear_backward: the gradient of x takes w");
+    if (to_w && !x) bad("expert_linear_backward: the gradient of w takes x");
+    matrix(dy, "expert_linear_backward");
+    // what is not there is of no gradient: its sizes are the others'
+    Experts m;
+    if (w) {
+        m = experts_of(*w, "expert_linear_backward");
+    } else {
+        if (off.numel() < 1) bad("expert_linear_backward: expected offsets of shape [experts + 1], got " + shape_str(off));
+        if (off.numel() > 1 << 20) check(QMOE_ERR_UNSUPPORTED, "expert_linear_backward");
+        m.E = off.numel() - 1;
+        m.N = dy.size(1);
+    }
+    Gathered g;
+    if (x) {
+        g = gathered(*x, a.maybe(4), a.whole(5), "expert_linear_backward");
+        if (!w) m.K = x->size(1);
+        if (x->size(1) != m.K) bad("the reduction lengths differ: " + shape_str(*x) + " and " + shape_str(*w));
+    } else {
+        g.P = g.rows = dy.size(0);
+    }
     const Rows d = rows_of(dy, g.P, m.N);
-    const int code = same_type(x, w, "x and w");
-    same_type(dy, w, "dy and w");
+    if (x && w) same_type(*x, *w, "x and w");
+    const int code = w ? same_type(dy, *w, "dy and w") : x ? same_type(dy, *x, "dy and x") : code_of(dy.scalar_type());
     const auto wt = a.dtype(6, at::kFloat);
-    const int32_t* offsets = vec_of<int32_t>(&a.tensor(3), m.E + 1, at::kInt);
+    const int32_t* offsets = vec_of<int32_t>(&off, m.E + 1, at::kInt);
     int32_t* const status = status_of(a.tensor(9));
     const qmoe_stream_t st = stream_of(dy);
-    const size_t cd = copy_of(d, g.P, m.N), cx = copy_of(g.x, g.rows, m.K), cw = copy_of(m);
-    const bool to_x = a.truth(7), to_w = a.truth(8);
+    const size_t cd = copy_of(d, g.P, m.N), cx = to_w ? copy_of(g.x, g.rows, m.K) : 0, cw = to_x ? copy_of(m) : 0;
     const size_t need = std::max(to_x ? product_bytes(g, m, 1) + cd + cw : 0, to_w ? product_bytes(g, m, 2) + cd + cx : 0);
     const MaybeWorkspace ws(need, a.maybe(10), dy);
     at::Tensor dx, dw;
     if (to_x) {
-        dx = make({g.P, m.K}, x.scalar_type(), x);
+        dx = make({g.P, m.K}, dy.scalar_type(), dy);
         check(qmoe_expert_linear_dx(g.P, (int)m.E, m.N, m.K, code, d.p, d.ld, m.p, m.ld, m.stride, offsets, dx.data_ptr(),
                                     code, m.K, status, ws.p, ws.n, st),
               "qmoe_expert_linear_dx");
     }
     if (to_w) {
-        dw = make({m.E, m.N, m.K}, wt, w);
+        dw = make({m.E, m.N, m.K}, wt, dy);
         check(qmoe_expert_linear_dw(g.P, (int)m.E, m.N, m.K, code, d.p, d.ld, g.x.p, g.x.ld, g.rows, g.pairs, g.k, offsets,
                                     dw.data_ptr(), code_of(wt), status, ws.p, ws.n, st),
               "qmoe_expert_linear_dw");

@@ -54,3 +54,27 @@ def test_workspaces_that_are_too_small_are_refused():
     with pytest.raises(qb.QmoeError):
         qb.expert_linear(rows, odd, offsets, ws=byte(copies - 256))
     assert torch.equal(qb.expert_linear(rows, odd, offsets, ws=byte(copies)), qb.expert_linear(rows, odd, offsets))
+
+
+@pytest.mark.parametrize("odd", [0, 1])
+@pytest.mark.parametrize("gather", [False, True])
+def test_each_gradient_without_what_the_other_takes(gather, odd):
+    counts, N, K, k = [40, 0, 300, 7], 136 - odd, 72 + odd, 2
+    P, offsets = sum(counts) + 3, offsets_of(counts)
+    w, dy = randn(7, 4, N, K), randn(8, P, N)
+    x = randn(9, P // k if gather else P, K)
+    pairs = torch.randperm(P, device="cuda").int() % (P // k * k) if gather else None
+    dx, dw = qb.expert_linear_backward(dy, x, w, offsets, pairs=pairs, k=k)
+    one, none = qb.expert_linear_backward(dy, None, w, offsets, pairs=pairs, k=k, need_dw=False)
+    assert none is None and torch.equal(one, dx)
+    none, one = qb.expert_linear_backward(dy, x, None, offsets, pairs=pairs, k=k, need_dx=False)
+    assert none is None and torch.equal(one, dw)
+    assert qb.expert_linear_backward(dy, None, None, offsets, need_dx=False, need_dw=False) == (None, None)
+    back = lambda *args, **kw: qb.expert_linear_backward(*args, pairs=pairs, k=k, **kw)
+    for f in (lambda: back(dy, None, w, offsets), lambda: back(dy, x, None, offsets), lambda: back(dy, x, None, offsets[:0], need_dx=False),
+              lambda: back(dy, x.half(), None, offsets, need_dx=False), lambda: back(dy[:, :-1], None, w, offsets, need_dw=False),
+              lambda: back(dy.float(), None, w.float(), offsets, need_dw=False), lambda: back(dy, None, w, offsets[1:], need_dw=False)):
+        with pytest.raises(ValueError):
+            f()
+    with pytest.raises(qb.QmoeError):
+        back(dy, x, None, offsets[:1], need_dx=False)  # no experts
