@@ -138,10 +138,15 @@ size_t qmoe_workspace_bytes(const qmoe_dims* d);
  * ws   workspace of qmoe_workspace_bytes(d) bytes, 256-byte aligned; besides
  *      scratch it receives the token-tile schedule and each slot's token-tile
  *      row, which the permute, intermediate and GEMM calls read
- * The result is bit-identical run to run (no atomics decide an order). */
+ * The result is bit-identical run to run (no atomics decide an order).
+ * qmoe_align_sort_routed -- the same, but for an id of -1: a pair that is meant to be
+ *   routed nowhere, which is not reported. */
 int qmoe_align_sort(const qmoe_dims* d, const int32_t* topk_ids, int32_t* counts, int32_t* offsets,
                     int32_t* sorted_pair_ids, int32_t* pair_slot, int32_t* dev_status, void* ws,
                     size_t ws_bytes, qmoe_stream_t stream);
+int qmoe_align_sort_routed(const qmoe_dims* d, const int32_t* topk_ids, int32_t* counts, int32_t* offsets,
+                           int32_t* sorted_pair_ids, int32_t* pair_slot, int32_t* dev_status, void* ws,
+                           size_t ws_bytes, qmoe_stream_t stream);
 
 /* qmoe_align_sort_static_scratch -- the same sort as qmoe_align_sort, for
  * callers that cannot allocate device memory.  The source pages have no

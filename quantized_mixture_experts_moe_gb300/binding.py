@@ -55,6 +55,7 @@ SIGNATURES = {
     "qmoe_version": ([], ctypes.c_char_p),
     "qmoe_workspace_bytes": ([_DP], _sz),
     "qmoe_align_sort": ([_DP, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp], _i32),
+    "qmoe_align_sort_routed": ([_DP, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp], _i32),
     "qmoe_align_sort_static_scratch": ([_DP, _vp, _vp, _vp, _vp, _vp, _vp, _vp], _i32),
     "qmoe_quant_act_mxfp8": ([_i64, _i64, _vp, _vp, _vp, _vp], _i32),
     "qmoe_quant_rows_int8_bf16": ([_i64, _i64, _vp, _vp, _vp, _vp], _i32),
@@ -230,6 +231,14 @@ def qmoe_align_sort(d, topk_ids, counts, offsets, sorted_pair_ids, pair_slot, de
                                _ptr(pair_slot), _ptr(dev_status), _ptr(ws), ws.numel() * ws.element_size(),
                                _stream(stream))
     _check(rc, "qmoe_align_sort")
+
+
+def qmoe_align_sort_routed(d, topk_ids, counts, offsets, sorted_pair_ids, pair_slot, dev_status, ws, stream=None):
+    """qmoe_align_sort, but for ids of -1, which are routed nowhere on purpose and not reported."""
+    rc = lib().qmoe_align_sort_routed(ctypes.byref(d), _ptr(topk_ids), _ptr(counts), _ptr(offsets), _ptr(sorted_pair_ids),
+                                      _ptr(pair_slot), _ptr(dev_status), _ptr(ws), ws.numel() * ws.element_size(),
+                                      _stream(stream))
+    _check(rc, "qmoe_align_sort_routed")
 
 
 STATIC_SCRATCH_BYTES = 1 << 20
@@ -610,8 +619,8 @@ _status_words = {}
 
 
 def status_word(device):
-    """The int32 device word where the FP8 products report a wait that ran out (QMOE_DEV_WAIT_TIMEOUT) unless a call is
-    given its own: one for each device, zero until then.  It is made by the first call that wants it, which may not be within
+    """The int32 device word where the FP8, 4-bit and experts' products and align_sort report (a wait that ran out, bad offsets
+    or ids: DEV_WAIT_TIMEOUT, DEV_BAD_OFFSETS, DEV_BAD_EXPERT_ID) unless a call is given its own: one for each device, zero until then.  It is made by the first call that wants it, which may not be within
     a graph capture (QmoeError): call this before one."""
     device = torch.device(device)
     index = torch.cuda.current_device() if device.index is None else device.index
@@ -667,7 +676,8 @@ def fp8_linear_backward(dy, x, wt_q, w_s, dev_status=None, stream=None):
 def align_sort(topk_ids, E, dev_status=None, ws=None, stream=None):
     """The routed pairs of topk_ids int32 [T, k] in expert order: (offsets int32 [E + 1], pairs int32 [T * k], the pair t * k + j
     of each slot, pair_slot int32 [T, k], the slot of each pair), -1 where there is none: ids outside [0, E) are routed
-    nowhere (and set DEV_BAD_EXPERT_ID in dev_status).  What expert_linear, combine and their gradients take."""
+    nowhere, and others than -1 set DEV_BAD_EXPERT_ID in dev_status (as for the other calls the device's status_word, unless
+    one is given).  What expert_linear, combine and their gradients take."""
     if stream is not None:
         with torch.cuda.stream(stream):
             return align_sort(topk_ids, E, dev_status, ws)
@@ -679,10 +689,10 @@ def align_sort(topk_ids, E, dev_status=None, ws=None, stream=None):
         new = functools.partial(torch.empty, dtype=torch.int32, device=topk_ids.device)
         counts, offsets, pairs, pair_slot = new(E), new(E + 1), new(T * k), new((T, k))
         if dev_status is None:
-            dev_status = torch.zeros(1, dtype=torch.int32, device=topk_ids.device)
+            dev_status = _status(topk_ids)
         if ws is None:
             ws = alloc_workspace(workspace_bytes(d), topk_ids.device)
-        qmoe_align_sort(d, topk_ids, counts, offsets, pairs, pair_slot, dev_status, ws)
+        qmoe_align_sort_routed(d, topk_ids, counts, offsets, pairs, pair_slot, dev_status, ws)
     return offsets, pairs, pair_slot
 
 

@@ -63,10 +63,11 @@ __device__ int block_exclusive_scan(int v, int32_t* ws, int& total) {
 }
 
 // Per-chunk expert histogram: counts do not depend on order, so shared-memory
-// atomics are fine here.
+// atomics are fine here.  none: an id that is of no expert and no error (an id of an
+// expert: there is none such).
 __global__ void __launch_bounds__(kThreads)
 align_hist_kernel(const int32_t* __restrict__ ids, int64_t P, int E, int nchunks, int32_t* __restrict__ hist,
-                  int32_t* __restrict__ dev_status) {
+                  int32_t* __restrict__ dev_status, int none) {
     extern __shared__ int32_t cnt[];
     const int tid = threadIdx.x;
     pdl_sync();
@@ -80,7 +81,7 @@ align_hist_kernel(const int32_t* __restrict__ ids, int64_t P, int E, int nchunks
             const int e = ids[p];
             if (e >= 0 && e < E)
                 atomicAdd(&cnt[e], 1);
-            else
+            else if (e != none)
                 bad = 1;
         }
     }
@@ -247,7 +248,7 @@ __global__ void __launch_bounds__(kThreads)
 align_small_kernel(const int32_t* __restrict__ ids, int64_t P, int E, int nmax, int32_t* __restrict__ counts,
                    int32_t* __restrict__ offsets, int32_t* __restrict__ sorted_pair_ids,
                    int32_t* __restrict__ pair_slot, int32_t* __restrict__ tile_start, int32_t* __restrict__ slot_dest,
-                   int32_t* __restrict__ pair_dest, int32_t* __restrict__ dev_status) {
+                   int32_t* __restrict__ pair_dest, int32_t* __restrict__ dev_status, int none) {
     extern __shared__ int32_t sm[];
     int32_t* cur = sm;  // per-expert counts, then cursors
     int32_t* offs = cur + E;
@@ -263,7 +264,7 @@ align_small_kernel(const int32_t* __restrict__ ids, int64_t P, int E, int nmax, 
         const int e = ids[p];
         if (e >= 0 && e < E)
             atomicAdd(&cur[e], 1);
-        else
+        else if (e != none)
             bad = 1;
     }
     if (__syncthreads_or(bad) && tid == 0) atomicOr(dev_status, QMOE_DEV_BAD_EXPERT_ID);
@@ -316,9 +317,9 @@ size_t align_ws_bytes(int64_t P, int E) {
     return (size_t)((nchunks * E * 4 + 255) / 256 * 256);
 }
 
-int align_sort_launch(int64_t P, int E, const int32_t* ids, int32_t* counts, int32_t* offsets,
-                      int32_t* sorted_pair_ids, int32_t* pair_slot, int32_t* dev_status, int32_t* hist,
-                      int nmax, int32_t* tile_start, cudaStream_t stream) {
+static int launch_sort(int64_t P, int E, const int32_t* ids, int32_t* counts, int32_t* offsets,
+                       int32_t* sorted_pair_ids, int32_t* pair_slot, int32_t* dev_status, int32_t* hist,
+                       int nmax, int32_t* tile_start, cudaStream_t stream, int none) {
     const int nchunks = (int)((P + kChunk - 1) / kChunk);
     const size_t hsmem = (size_t)E * sizeof(int32_t);
     const size_t ssmem = scatter_smem_bytes(E);
@@ -332,12 +333,18 @@ int align_sort_launch(int64_t P, int E, const int32_t* ids, int32_t* counts, int
     }
     if (nchunks <= 1)
         return launch_pdl(align_small_kernel, 1, kThreads, ssmem, stream, ids, P, E, nmax, counts, offsets,
-                          sorted_pair_ids, pair_slot, tile_start, slot_dest, pair_dest, dev_status);
-    int rc = launch_pdl(align_hist_kernel, nchunks, kThreads, hsmem, stream, ids, P, E, nchunks, hist, dev_status);
+                          sorted_pair_ids, pair_slot, tile_start, slot_dest, pair_dest, dev_status, none);
+    int rc = launch_pdl(align_hist_kernel, nchunks, kThreads, hsmem, stream, ids, P, E, nchunks, hist, dev_status, none);
     if (rc == QMOE_OK)
         rc = launch_pdl(align_scan_scatter_kernel, nchunks, kThreads, ssmem, stream, ids, P, E, nchunks, hist, nmax,
                         counts, offsets, sorted_pair_ids, pair_slot, tile_start, slot_dest, pair_dest);
     return rc;
+}
+
+int align_sort_launch(int64_t P, int E, const int32_t* ids, int32_t* counts, int32_t* offsets,
+                      int32_t* sorted_pair_ids, int32_t* pair_slot, int32_t* dev_status, int32_t* hist,
+                      int nmax, int32_t* tile_start, cudaStream_t stream) {
+    return launch_sort(P, E, ids, counts, offsets, sorted_pair_ids, pair_slot, dev_status, hist, nmax, tile_start, stream, 0);
 }
 
 // Kernels align_sort_launch starts for P pairs: one CTA's single launch up to
@@ -358,9 +365,8 @@ extern "C" size_t qmoe_workspace_bytes(const qmoe_dims* d) {
     return qmoe::align_ws_bytes(P, d->E) + (size_t)(qmoe::schedule_ints(d->E) + 2 * qmoe::slot_ints(P)) * 4;
 }
 
-extern "C" int qmoe_align_sort(const qmoe_dims* d, const int32_t* topk_ids, int32_t* counts, int32_t* offsets,
-                               int32_t* sorted_pair_ids, int32_t* pair_slot, int32_t* dev_status, void* ws,
-                               size_t ws_bytes, qmoe_stream_t stream) {
+static int sort_pairs(const qmoe_dims* d, const int32_t* topk_ids, int32_t* counts, int32_t* offsets, int32_t* sorted_pair_ids,
+                      int32_t* pair_slot, int32_t* dev_status, void* ws, size_t ws_bytes, qmoe_stream_t stream, int none) {
     using namespace qmoe;
     if (!dims_ok(d)) return QMOE_ERR_ARG;
     const int64_t P = (int64_t)d->T * d->k;
@@ -370,7 +376,18 @@ extern "C" int qmoe_align_sort(const qmoe_dims* d, const int32_t* topk_ids, int3
     if (d->E > kMaxExperts) return QMOE_ERR_UNSUPPORTED;
     if (ws_bytes < align_ws_bytes(P, d->E)) return QMOE_ERR_ARG;
     if (ws_bytes < qmoe_workspace_bytes(d)) return QMOE_ERR_ARG;
-    return align_sort_launch(P, d->E, topk_ids, counts, offsets, sorted_pair_ids, pair_slot, dev_status,
-                             static_cast<int32_t*>(ws), mxt::nmax_for(d), tile_schedule_in(ws, d),
-                             (cudaStream_t)stream);
+    return launch_sort(P, d->E, topk_ids, counts, offsets, sorted_pair_ids, pair_slot, dev_status,
+                       static_cast<int32_t*>(ws), mxt::nmax_for(d), tile_schedule_in(ws, d), (cudaStream_t)stream, none);
+}
+
+extern "C" int qmoe_align_sort(const qmoe_dims* d, const int32_t* topk_ids, int32_t* counts, int32_t* offsets,
+                               int32_t* sorted_pair_ids, int32_t* pair_slot, int32_t* dev_status, void* ws,
+                               size_t ws_bytes, qmoe_stream_t stream) {
+    return sort_pairs(d, topk_ids, counts, offsets, sorted_pair_ids, pair_slot, dev_status, ws, ws_bytes, stream, 0);
+}
+
+extern "C" int qmoe_align_sort_routed(const qmoe_dims* d, const int32_t* topk_ids, int32_t* counts, int32_t* offsets,
+                                    int32_t* sorted_pair_ids, int32_t* pair_slot, int32_t* dev_status, void* ws,
+                                    size_t ws_bytes, qmoe_stream_t stream) {
+    return sort_pairs(d, topk_ids, counts, offsets, sorted_pair_ids, pair_slot, dev_status, ws, ws_bytes, stream, -1);
 }

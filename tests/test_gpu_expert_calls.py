@@ -78,3 +78,30 @@ def test_each_gradient_without_what_the_other_takes(gather, odd):
             f()
     with pytest.raises(qb.QmoeError):
         back(dy, x, None, offsets[:1], need_dx=False)  # no experts
+
+
+@pytest.mark.parametrize("T", [40, 3000])
+def test_align_sort_reports_bad_ids(T):
+    """To the device's word, as the other calls; an id of -1 is no error, and the sort is the same."""
+    k, E = 2, 7
+    ids = torch.randint(-1, E, (T, k), device="cuda").int()
+    word = qb.status_word("cuda")
+    before = int(word)
+    offsets, pairs, slot = qb.align_sort(ids, E)
+    assert int(word) == before
+    d, new = qb.dims(T, k, 32, 32, E), lambda *s: torch.empty(*s, dtype=torch.int32, device="cuda")
+    own, out = torch.zeros(1, dtype=torch.int32, device="cuda"), (new(E), new(E + 1), new(T * k), new(T, k))
+    qb.qmoe_align_sort(d, ids, *out, own, qb.alloc_workspace(qb.workspace_bytes(d)))
+    assert all(torch.equal(a, b) for a, b in zip(out[1:], (offsets, pairs, slot))) and int(own) == qb.DEV_BAD_EXPERT_ID
+    try:
+        for wrong in (E, -2, 2 ** 31 - 1, -2 ** 31):
+            ids[T // 2, 1] = wrong
+            word.zero_()
+            qb.align_sort(ids, E)
+            assert int(word) == qb.DEV_BAD_EXPERT_ID
+            mine = torch.zeros(1, dtype=torch.int32, device="cuda")
+            word.zero_()
+            qb.align_sort(ids, E, dev_status=mine)
+            assert int(mine) == qb.DEV_BAD_EXPERT_ID and int(word) == 0
+    finally:
+        word.fill_(before)
