@@ -750,14 +750,16 @@ int qmoe_weighted_sum_backward(int64_t T, int k, int64_t P, int64_t H, int dtype
  * qmoe_w4_linear -- y[t] = W x[t], or with ids int32 [T, k] of E matrices the
  *   products of each token with its experts, y [T * k, N]:
  *   y[t k + j] = W[ids[t][j]] x[t]; a row whose id is outside [0, E) is zeros.
- *   (ids NULL: one matrix, E = k = 1; T * k <= 32768 with ids.)  A row of x with an
- *   infinity or NaN gives NaN.  x [T, K] and y of type dtype (QMOE_BF16 or
- *   QMOE_F16; y_dtype may be QMOE_F32).  No weight is rounded, sums are fp32: with ids,
- *   and up to QMOE_W4_FEW or some more tokens, codes are multiplied as they are and
- *   groups' sums by their scales; above it W is widened into the workspace, in dtype
- *   (int4: two matrices whose sum is W), for the grouped product.  Scales may be of any
- *   size their type holds: in fp16 each row of W is widened over a power of two (what is
- *   below 2^-39 of the row's largest is lost).
+ *   (ids NULL: one matrix, E = k = 1; T * k <= 32768 with ids.)  A row of x with a NaN
+ *   gives NaN, one with an infinity no finite value: NaN or an infinity; other rows are
+ *   what they are without it.  Beside int4 codes x is below 2^117.
+ *   x [T, K] and y of type dtype (QMOE_BF16 or QMOE_F16; y_dtype may be QMOE_F32).  No
+ *   weight is rounded, sums are fp32: with ids, and up to QMOE_W4_FEW or some more
+ *   tokens, codes are multiplied as they are and groups' sums by their scales; above it
+ *   W is widened into the workspace, in dtype (int4: two matrices whose sum is W), for
+ *   the grouped product.  Scales may be of any size their type holds: in fp16 each row
+ *   of W is widened over a power of two (what is below 2^-39 of the row's largest is
+ *   lost).
  * qmoe_w4_linear_dx -- dx = dy W for one matrix, W widened as above, in fp16 each
  *   column over a power of two.
  * ws of qmoe_w4_workspace_bytes(T, N, K, dx) bytes (dx 0 for the product, 1 for the
