@@ -31,18 +31,6 @@ struct FewArgs {
     int32_t* status;
 };
 
-template <typename T>
-__device__ __forceinline__ void mma_few(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
-    if constexpr (sizeof(T) == 2 && std::is_same<T, __half>::value)
-        asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-            : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-            : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-    else
-        asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-            : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-            : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-
 // Values k .. k + 7 of a row of n, as they lie in memory: loaded first, put in
 // place when all loads of a round are on their way.  WIDE: rows on 16-byte
 // boundaries; else two aligned pieces, each read only where it holds values of the
@@ -90,6 +78,7 @@ template <typename T, bool WIDE_X>
 __global__ void __launch_bounds__(FEW_THREADS) expert_few_kernel(const FewArgs g) {
     __shared__ float part[FEW_WARPS][FEW_COLS][FEW_ROWS];
     __shared__ int span[2];  // the expert and the end of its rows
+    constexpr bool BF16 = std::is_same<T, __nv_bfloat16>::value;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, row = lane >> 2, quad = lane & 3;
     const int s0 = blockIdx.y, n0 = blockIdx.x * FEW_ROWS;
     if (threadIdx.x == 0) span[0] = -1;
@@ -147,8 +136,8 @@ __global__ void __launch_bounds__(FEW_THREADS) expert_few_kernel(const FewArgs g
             for (int j = 0; j < FEW_DEPTH; ++j) {
                 const int k = (i0 + j * FEW_WARPS) * 32 + quad * 8;
                 const uint4 p = a[j].get(w0, k, g.K), q = b[j].get(w1, k, g.K), r = v[j].get(x, k, g.K);
-                mma_few<T>(d, p.x, q.x, p.y, q.y, r.x, r.y);
-                mma_few<T>(d, p.z, q.z, p.w, q.w, r.z, r.w);
+                tc::mma_sync<BF16>(d, p.x, q.x, p.y, q.y, r.x, r.y);
+                tc::mma_sync<BF16>(d, p.z, q.z, p.w, q.w, r.z, r.w);
             }
 #pragma unroll
             for (int j = 0; j < 4; ++j) acc[j] += d[j];

@@ -75,18 +75,6 @@ template <> struct Num<__nv_bfloat16> {
     static constexpr uint32_t BASE = 0x41804180u;  // 16
     static constexpr int UP = 3;
 };
-template <bool BF16>
-__device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-    if constexpr (BF16)
-        asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-            : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-    else
-        asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-            : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-
 // Codes of a word as numbers in the halves of a register.  int4: codes j and j + 4,
 // as 16 + n.  E2M1: codes 2 j and 2 j + 1.
 template <typename T, int FORMAT, int J>
@@ -114,12 +102,6 @@ __device__ __forceinline__ float scale_of(uint32_t raw) {
 template <int FORMAT>
 __device__ __forceinline__ float scale_at(const void* s, int64_t i) {
     return scale_of<FORMAT>(static_cast<const typename Scale<FORMAT>::Raw*>(s)[i]);
-}
-
-__device__ __forceinline__ void put(void* y, int type, int64_t at, float v) {
-    if (type == QMOE_F32) static_cast<float*>(y)[at] = v;
-    else if (type == QMOE_BF16) static_cast<__nv_bfloat16*>(y)[at] = __float2bfloat16_rn(v);
-    else static_cast<__half*>(y)[at] = __float2half_rn(v);
 }
 
 // Bytes of a token's x in shared memory: rows of two neighbouring tokens fall into
@@ -412,7 +394,7 @@ __global__ void __launch_bounds__(THREADS, NT == 1 ? 2 : 1) w4_few_kernel(const 
         if (at.e < 0) {
             for (int t = 0; t < tokens; ++t)
                 for (int i = threadIdx.x; i < rows; i += WARPS * 32)
-                    if (n0 + i < g.N) put(g.y, g.ytype, row_of(t) + n0 + i, 0.f);
+                    if (n0 + i < g.N) eg::put_value(g.y, g.ytype, row_of(t) + n0 + i, 0.f);
             continue;
         }
         float acc[NT][4];
@@ -471,8 +453,8 @@ __global__ void __launch_bounds__(THREADS, NT == 1 ? 2 : 1) w4_few_kernel(const 
                                                     pair_of<T, FORMAT, 1>(lo[i]), pair_of<T, FORMAT, 1>(hi[i])};
                             const uint32_t a1[4] = {pair_of<T, FORMAT, 2>(lo[i]), pair_of<T, FORMAT, 2>(hi[i]),
                                                     pair_of<T, FORMAT, 3>(lo[i]), pair_of<T, FORMAT, 3>(hi[i])};
-                            mma<BF16>(d, a0, v.x, v.y);
-                            mma<BF16>(d, a1, v.z, v.w);
+                            tc::mma_sync<BF16>(d, a0[0], a0[1], a0[2], a0[3], v.x, v.y);
+                            tc::mma_sync<BF16>(d, a1[0], a1[1], a1[2], a1[3], v.z, v.w);
                         }
                         xp += x_step;
 #pragma unroll
@@ -501,8 +483,8 @@ __global__ void __launch_bounds__(THREADS, NT == 1 ? 2 : 1) w4_few_kernel(const 
                             const uint4 v = *reinterpret_cast<const uint4*>(xb + t * pitch + j * 64);
                             const float2 z = *reinterpret_cast<const float2*>(sums + ((b * BLOCK - c0) / 32 + j) * (8 * NT) + i * 8 + quad * 2);
                             float d[4] = {INT4 ? z.x : 0.f, INT4 ? z.y : 0.f, INT4 ? z.x : 0.f, INT4 ? z.y : 0.f};
-                            mma<BF16>(d, a0, v.x, v.y);
-                            mma<BF16>(d, a1, v.z, v.w);
+                            tc::mma_sync<BF16>(d, a0[0], a0[1], a0[2], a0[3], v.x, v.y);
+                            tc::mma_sync<BF16>(d, a1[0], a1[1], a1[2], a1[3], v.z, v.w);
                             if constexpr (!INT4) {
                                 d[0] *= z.x;
                                 d[1] *= z.y;
@@ -546,7 +528,7 @@ __global__ void __launch_bounds__(THREADS, NT == 1 ? 2 : 1) w4_few_kernel(const 
         if (kw == 1) {  // all of them
             each([&](int t, int r, float v) {
                 const int n = n0 + first_row + r;
-                if (t < tokens && n < g.N) put(g.y, g.ytype, row_of(t) + n, v);
+                if (t < tokens && n < g.N) eg::put_value(g.y, g.ytype, row_of(t) + n, v);
             });
             continue;
         }
@@ -559,7 +541,7 @@ __global__ void __launch_bounds__(THREADS, NT == 1 ? 2 : 1) w4_few_kernel(const 
             const float* from = parts + (buf * WARPS + (n / ROWS) * kw) * NT * 8 * ROWS + t * ROWS + n % ROWS;
             float v = 0.f;
             for (int w = 0; w < kw; ++w) v += from[w * NT * 8 * ROWS];
-            if (n0 + n < g.N) put(g.y, g.ytype, row_of(t) + n0 + n, v);
+            if (n0 + n < g.N) eg::put_value(g.y, g.ytype, row_of(t) + n0 + n, v);
         }
         if (bufs_of(NT) == 2) buf ^= 1;
         else products_sync();
