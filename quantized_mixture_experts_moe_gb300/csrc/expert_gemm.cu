@@ -131,7 +131,7 @@ expert_gemm_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_const
     }
     if (threadIdx.x == 0) {
         for (int i = 0; i < C::STAGES; ++i) {
-            tc::mbar_init(&full[i], 1);
+            tc::mbar_init(&full[i], 1 + (GATHER ? GATHER_SHARE : 0));
             tc::mbar_init(&empty[i], 1);
         }
         for (int i = 0; i < 2; ++i) {
@@ -246,6 +246,10 @@ expert_gemm_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_const
                 if (mine)
                     tma_gather4(smem + slot * C::STAGE + C::P_BYTES + group * 512, &map_q, &full[slot], s * STEP, rows);
                 __syncwarp();
+                // A warp arrives also where none of the tile's rows are its own (12 rows and fewer).  Only with bytes to bring it
+                // would be kept in step by them, and one without, a round behind, took empty's parity for the round it waited for,
+                // and at the end waited for one that did not come.
+                if (lane == 0) tc::mbar_arrive(&full[slot]);
             }
         }
     } else {
