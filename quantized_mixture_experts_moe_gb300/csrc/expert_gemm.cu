@@ -13,8 +13,8 @@
 // values, and the tensor core transposes them as it reads.
 //
 // Many rows an expert, and dw: 256 x 256 tiles of two CTAs (expert_gemm_pair.cu).
-// Here: y and dx for fewer, 128 lanes and up to 32 or 128 columns, so that the ring
-// holds mostly weights, which bound it: 1024 pairs over 128 experts 2048 -> 1536
+// Here: y and dx for fewer, 128 lanes and up to 32 or 128 columns (tile_of), so that the
+// ring holds mostly weights, which bound it: 1024 pairs over 128 experts 2048 -> 1536
 // 132 us, 6.1 TB/s; 64 x 80 rows 4096 -> 2816 285 us, 5.2 TB/s.  One token x 8 of
 // 128 experts (50 MB) 15 us: 2.4 until the first load, 1.5 its latency, 9 the
 // weights at 5.3 TB/s, 1.2 the stores.
@@ -491,14 +491,24 @@ static int launch_as(const CUtensorMap& mp, const CUtensorMap& mq, const Args& g
     return launch_pdl(join_kernel<NT>, dim3((unsigned)grid, NT / 16), dim3(512), 0, st, g);
 }
 
-// Few rows for each expert: narrow tiles, whose stages are almost all weight, so that more of them are in flight.
+// Columns of a tile, by the rows an expert has on average (of up to P experts: the
+// offsets are not known here).  Few: narrow tiles, whose stages are almost all weight, so
+// that more of them are in flight.  Many: tiles of two CTAs.  Tiles of 128 are left for
+// one matrix, whose few tiles the SMs share, which pairs do not.  us of y with tiles of
+// 32, 128 and 256, rows an expert: 64 experts 4096 -> 2816, 16 rows 230 276 261, 32 rows
+// 233 279 262, 48 rows 296 280 264, 96 rows - 287 269; 32 experts 2048 -> 1536, 32 rows
+// 38 47 44, 40 rows 48 48 44; 8 experts 4096 -> 2816, 32 rows 42 44 49, 48 rows 49 44 49
+// (dx 46 43 39), 96 rows 59 58 50; one matrix 4096 -> 4096, 32 rows 14.3 16.0 21.9, 64
+// rows 18.4 16.4 22.2, 192 rows - 21.5 23.6.  Skew, a quarter of all rows one expert's:
+// 8192 rows of 512 experts 2048 -> 1024 354 394 362, 4096 of 64 4096 -> 2816 351 302 266.
+//
 // Gathered rows of x are read as they lie for few rows an expert; for many they are
 // laid out in expert order first: a tile's rows are read again for every 256
 // outputs, and TMA's gather of four rows takes as long as a box of 128 (8192 x 8
 // rows of 4096, 2816 outputs: 1136 us gathered in the product, 960 laid out).
 inline int tile_of(int64_t P, int E) {
     const int64_t touched = P < E ? P : E;
-    return P <= 16 * touched ? 32 : P <= 96 * touched ? 128 : 256;
+    return P <= 32 * touched ? 32 : touched == 1 && P <= 192 ? 128 : 256;
 }
 
 // No more tiles than this, whatever the offsets.
@@ -507,10 +517,13 @@ inline int64_t most_tiles(int64_t P, int E, int64_t lanes, int nt) {
     return ((P < E ? P : E) + 1 + P / nt) * ((lanes + lt - 1) / lt);
 }
 // Whether the SMs share the steps of all tiles evenly, and a second kernel joins the
-// parts, by a model of the time in us fitted to GB300: a step of 64 x 128 weights
-// takes 0.39 where all SMs load (HBM), 0.25 where few do; the join 2.5.  T=1 of 10
-// experts 4096 -> 2048 (160 tiles of 64 steps): 62 us in whole tiles, 51 shared;
-// 8 experts 2048 -> 1536 (96 of 32): 14.5 against 16.8.
+// parts, by a model of the time in us fitted to GB300: beside some 7.5 of either form
+// (offsets, the first loads' latency, the last stores) a step of 64 x 128 weights takes
+// 0.39 where all SMs load (HBM), 0.25 where few do; the join 2.5.  Whole and shared:
+// 10 experts 4096 -> 2048 (160 tiles of 64 steps) 57 and 37 (by the model 57 and 36), 8
+// experts 2048 -> 1536 (96 of 32) 15.3 and 16.3 (15.5 and 17.9), 16 experts (192 of 32)
+// 26.7 and 24.4, one matrix 4096 -> 4096 (32 of 64) 21.2 and 14.7 (23.5 and 15.3), 1408
+// of 2048 by 6 experts (66 of 32) 14.4 and 15.0.
 inline bool split(int64_t P, int E, int64_t lanes, int64_t per, int nt) {
     if (nt == 256) return false;
     const int64_t tiles = ((P < E ? P : E) + P / nt) * ((lanes + 127) / 128);

@@ -109,7 +109,7 @@ def by_expert(f, *tensors, offsets):
 
 
 @pytest.mark.parametrize("steps", [31, 32, 33, 64, 65, 97, 130])
-@pytest.mark.parametrize("E,least,most", [(60, 97, 400), (100, 17, 96), (300, 1, 16)])
+@pytest.mark.parametrize("E,least,most", [(60, 97, 400), (100, 17, 96), (300, 1, 16), (150, 1, 60)])
 def test_pieces_of_many_tiles(E, least, most, steps):
     """Rows of many experts, more tiles than SMs, and sums of one piece, of whole ones, and with a short last one."""
     g = gen(E + steps)
@@ -146,4 +146,21 @@ def test_pieces_of_dw(E, most, dtype):
     wants = by_expert(lambda e, a, b: (a.t() @ b, a.abs().t() @ b.abs()), dy, x, offsets=offsets)
     for e, (want, size) in enumerate(wants):
         assert ((dw[e].double() - want).abs() <= (2.0 ** -24 if dtype == F32 else 2.0 ** -8 * 1.01) * want.abs() + bound(16) * size).all(), e
+    assert status() == 0
+
+
+@pytest.mark.parametrize("P", [32, 33, 64, 65, 100, 128, 129, 192, 193])
+@pytest.mark.parametrize("N,K", [(264, 2120), (20040, 320)])
+def test_one_matrix(P, N, K):
+    """Rows of one matrix about the tiles' widths, its few tiles shared by the SMs or more tiles than SMs."""
+    g = gen(P + N)
+    x, w = (torch.randn(*s, generator=g, device="cuda").to(BF16) for s in ((P, K), (1, N, K)))
+    offsets = offsets_of([P])
+    pairs = torch.randperm(P, generator=g, device="cuda").int()
+    for got, rows in ((qb.expert_linear(x, w, offsets, out_dtype=F32), x), (qb.expert_linear(x, w, offsets, pairs=pairs, k=1, out_dtype=F32), x[pairs.long()])):
+        near(got, rows.double() @ w[0].double().t(), rows.double().abs() @ w[0].double().abs().t(), 16, "y")
+    wt = w.transpose(1, 2).contiguous()
+    dx, _ = qb.expert_linear_backward(x, None, wt, offsets, need_dw=False)
+    want, size = x.double() @ w[0].double().t(), x.double().abs() @ w[0].double().abs().t()
+    assert ((dx.double() - want).abs() <= 2.0 ** -8 * 1.01 * want.abs() + bound(16) * size).all()
     assert status() == 0
