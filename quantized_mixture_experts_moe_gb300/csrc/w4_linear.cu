@@ -763,10 +763,11 @@ static int widen(const Widen& a, int dx, cudaStream_t st) {
 }
 // Tokens up to which the codes are multiplied as they are, QMOE_W4_FEW of them by a
 // launch.  us of two launches and widened, int4 bf16 in groups of 128, 17, 24 and 32
-// tokens: 2816 x 2048 13.0 14.6 17.1 and 18.6 18.6 18.8; 2816 x 4096 21.5 25.5 29.5 and
-// 23.7 23.7 23.9; 4096 x 4096 21.8 25.7 29.8 and 30.7 30.8 31.1; 8192 x 8192 99 109 161
-// and 106 106 107.  E2M1, which becomes one matrix, 4096 x 4096: 22.2 from 17 on, one
-// launch of 16 tokens 16.1.
+// tokens: 1024 x 1024 8.3 8.8 10.2 and 12.0 12.1 12.3; 2816 x 2048 13.1 14.8 17.5 and
+// 17.2 17.2 17.4; 2816 x 4096 21.6 25.6 29.6 and 20.6 20.6 20.9; 4096 x 4096 21.9 25.8
+// 29.8 and 26.9 27.0 27.3; 8192 x 4096 33 39 44 and 51 51 62; 8192 x 8192 99 110 161 and
+// 98 99 117.  E2M1, which becomes one matrix, 4096 x 4096: 19.8 from 17 on, one launch
+// of 16 tokens 16.1.
 inline int unwidened(int format) { return format == QMOE_W4_INT4 ? 24 : QMOE_W4_FEW; }
 inline int parts_of(int format) { return format == QMOE_W4_INT4 ? 2 : 1; }
 inline size_t widened_bytes(int64_t T, int64_t N, int64_t K, int parts, int dx) {
