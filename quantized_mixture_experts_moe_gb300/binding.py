@@ -677,7 +677,7 @@ def align_sort(topk_ids, E, dev_status=None, ws=None, stream=None):
     """The routed pairs of topk_ids int32 [T, k] in expert order: (offsets int32 [E + 1], pairs int32 [T * k], the pair t * k + j
     of each slot, pair_slot int32 [T, k], the slot of each pair), -1 where there is none: ids outside [0, E) are routed
     nowhere, and others than -1 set DEV_BAD_EXPERT_ID in dev_status (as for the other calls the device's status_word, unless
-    one is given).  What expert_linear, combine and their gradients take."""
+    one is given; captured before that was made, the sort reports nowhere).  What expert_linear, combine and their gradients take."""
     if stream is not None:
         with torch.cuda.stream(stream):
             return align_sort(topk_ids, E, dev_status, ws)
@@ -689,7 +689,8 @@ def align_sort(topk_ids, E, dev_status=None, ws=None, stream=None):
         new = functools.partial(torch.empty, dtype=torch.int32, device=topk_ids.device)
         counts, offsets, pairs, pair_slot = new(E), new(E + 1), new(T * k), new((T, k))
         if dev_status is None:
-            dev_status = _status(topk_ids)
+            unmade = topk_ids.get_device() not in _status_words and torch.cuda.is_current_stream_capturing()
+            dev_status = torch.zeros(1, dtype=torch.int32, device=topk_ids.device) if unmade else _status(topk_ids)
         if ws is None:
             ws = alloc_workspace(workspace_bytes(d), topk_ids.device)
         qmoe_align_sort_routed(d, topk_ids, counts, offsets, pairs, pair_slot, dev_status, ws)

@@ -491,16 +491,18 @@ static int launch_as(const CUtensorMap& mp, const CUtensorMap& mq, const Args& g
     return launch_pdl(join_kernel<NT>, dim3((unsigned)grid, NT / 16), dim3(512), 0, st, g);
 }
 
-// Columns of a tile, by the rows an expert has on average (of up to P experts: the
-// offsets are not known here).  Few: narrow tiles, whose stages are almost all weight, so
-// that more of them are in flight.  Many: tiles of two CTAs.  Tiles of 128 are left for
-// one matrix, whose few tiles the SMs share, which pairs do not.  us of y with tiles of
-// 32, 128 and 256, rows an expert: 64 experts 4096 -> 2816, 16 rows 230 276 261, 32 rows
-// 233 279 262, 48 rows 296 280 264, 96 rows - 287 269; 32 experts 2048 -> 1536, 32 rows
-// 38 47 44, 40 rows 48 48 44; 8 experts 4096 -> 2816, 32 rows 42 44 49, 48 rows 49 44 49
-// (dx 46 43 39), 96 rows 59 58 50; one matrix 4096 -> 4096, 32 rows 14.3 16.0 21.9, 64
-// rows 18.4 16.4 22.2, 192 rows - 21.5 23.6.  Skew, a quarter of all rows one expert's:
-// 8192 rows of 512 experts 2048 -> 1024 354 394 362, 4096 of 64 4096 -> 2816 351 302 266.
+// Columns of a tile, by the rows an expert has on average (the offsets are not known
+// here).  Few: narrow tiles, whose stages are almost all weight, so that more of them
+// are in flight.  Many: tiles of two CTAs.  Tiles of 128 are left for one matrix, whose
+// few tiles the SMs share, which pairs do not.  us of y with tiles of 32, 128 and 256,
+// rows an expert: 64 experts 4096 -> 2816, 16 rows 230 276 261, 32 rows 233 279 262, 48
+// rows 296 280 264, 96 rows - 287 269; 32 experts 2048 -> 1536, 32 rows 38 47 44, 40 rows
+// 48 48 44; one matrix 4096 -> 4096, 32 rows 14.3 16.0 21.9, 64 rows 18.4 16.4 22.2, 192
+// rows - 21.5 23.6.  Between 24 and 32 rows uneven loads decide (Zipf's law of the given
+// exponent, largest expert): 64 experts 4096 -> 2816, 25 rows, 0.8, 144 rows 257 278 260,
+// 32 rows, 1.2, 245 rows 281 279 262, all to one expert 123 66 42; 512 experts 2048 ->
+// 1024, 20 rows, 1.2, 964 rows 380 390 349, 16 rows and a quarter of all for one 354 394
+// 362.
 //
 // Gathered rows of x are read as they lie for few rows an expert; for many they are
 // laid out in expert order first: a tile's rows are read again for every 256
@@ -508,7 +510,8 @@ static int launch_as(const CUtensorMap& mp, const CUtensorMap& mq, const Args& g
 // rows of 4096, 2816 outputs: 1136 us gathered in the product, 960 laid out).
 inline int tile_of(int64_t P, int E) {
     const int64_t touched = P < E ? P : E;
-    return P <= 32 * touched ? 32 : touched == 1 && P <= 192 ? 128 : 256;
+    if (touched == 1) return P <= 32 ? 32 : P <= 192 ? 128 : 256;
+    return P <= 24 * touched ? 32 : 256;
 }
 
 // No more tiles than this, whatever the offsets.

@@ -105,3 +105,19 @@ def test_align_sort_reports_bad_ids(T):
             assert int(mine) == qb.DEV_BAD_EXPERT_ID and int(word) == 0
     finally:
         word.fill_(before)
+
+
+def test_align_sort_is_captured_without_a_status_word():
+    ids = torch.tensor([[2, 0], [1, 2], [-1, 7]], dtype=torch.int32, device="cuda")
+    want = qb.align_sort(ids, 3, dev_status=torch.zeros(1, dtype=torch.int32, device="cuda"))
+    held = dict(qb._status_words)
+    qb._status_words.clear()
+    try:
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            got = qb.align_sort(ids, 3)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert not qb._status_words and all(torch.equal(a, b) for a, b in zip(got, want))
+    finally:
+        qb._status_words.update(held)
