@@ -18,6 +18,8 @@
 // 132 us, 6.1 TB/s; 64 x 80 rows 4096 -> 2816 285 us, 5.2 TB/s.  One token x 8 of
 // 128 experts (50 MB) 15 us: 2.4 until the first load, 1.5 its latency, 9 the
 // weights at 5.3 TB/s, 1.2 the stores.
+#include <cmath>
+
 #include "expert_gemm.cuh"
 
 namespace qmoe {
@@ -109,7 +111,7 @@ struct Segments {
     }
 };
 
-template <int MODE, int NT, bool GATHER, bool SPLIT>
+template <int MODE, int NT, bool GATHER, bool SPLIT, bool BY>
 __global__ void __launch_bounds__(threads_of(GATHER), 1)
 expert_gemm_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_constant__ CUtensorMap map_q, const Args g) {
     using C = Cfg<MODE, NT>;
@@ -196,7 +198,7 @@ expert_gemm_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_const
             const int end = it + seg.s1 - seg.s0;
             while (it < end) {  // pieces of the sum, each in an accumulator of its own
                 const uint32_t d = tm + (buf * TURNS + turn) * NT;
-                if (!(ok = warp_wait(&acc_empty[buf], acc_phase ^ 1, abort_flag, g.status))) break;
+                if (!(ok = issue_wait(&acc_empty[buf], acc_phase ^ 1, abort_flag, g.status))) break;
                 // every second step, a sum of its own: by the steps' count from the first tile's on, so that a stage is always one
                 // warp's.  By turns within a tile, odd ones gave a stage to the other warp, which took a load that was two rounds
                 // behind for one that had come: the parity of a barrier does not tell them apart.
@@ -205,7 +207,7 @@ expert_gemm_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_const
 #pragma unroll 1
                 for (int i = it + ((it ^ turn) & 1); i < last; i += TURNS) {
                     const int slot = i % C::STAGES;
-                    if (!(ok = warp_wait(&full[slot], i / C::STAGES & 1, abort_flag, g.status))) break;
+                    if (!(ok = issue_wait(&full[slot], i / C::STAGES & 1, abort_flag, g.status))) break;
                     tc::tc_fence_after();
                     const uint32_t sa = tc::smem_u32(smem) + slot * C::STAGE, sb = sa + C::P_BYTES;
                     const uint64_t da = MODE == FWD ? tc::sdesc_kmajor_sw128(sa) : sdesc_across(sa);
@@ -253,7 +255,6 @@ expert_gemm_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_const
             }
         }
     } else {
-        constexpr int CHUNKS = (NT + 63) / 64;  // of 32 columns, every second one this warp's
         const int quad = warp & 3, half = warp >> 2;
         int4 join = make_int4(0, 0, 0, 0);
         const bool matrices = by_matrices<MODE>(g);
@@ -263,53 +264,77 @@ expert_gemm_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_const
         while (!*abort_flag && segments.next(seg)) {
             const int l0 = t.l0 + quad * 32;
             if (SPLIT && seg.part == 1) join = make_int4(t.l0, t.q0, t.n, segments.others(seg));
-            // all of this warp's columns: of each piece what both warps have summed up, then of all pieces
-            const bool part = SPLIT && seg.part >= 0, by_8 = matrices && !part;
-            uint32_t r[CHUNKS][32];
-            if (seg.s1 == 0) {
-#pragma unroll
-                for (int i = 0; i < CHUNKS; ++i)
-#pragma unroll
-                    for (int j = 0; j < 32; ++j) r[i][j] = 0;
-            }
-            bool ok = true;
-            const int end = it + seg.s1 - seg.s0, begin = it;
-#pragma unroll 1
-            for (; it < end; it = min(it + PIECE, end)) {
-                ok = warp_wait(&acc_full[buf], acc_phase, abort_flag, g.status);
-                if (!ok) break;
+            // where a sum lies in its accumulator: with the warp that has the first step, and (two) the other's
+            const uint32_t all = tm + ((uint32_t)(quad * 32) << 16), one = (it & 1) * NT, other = (~it & 1) * NT;
+            const int steps = seg.s1 - seg.s0;
+            bool two = steps > 1, ok = true;
+            if (seg.s1 > 0) {
+                if (!warp_wait(&acc_full[buf], acc_phase, abort_flag, g.status)) break;
                 tc::tc_fence_after();
-                const uint32_t from = tm + ((uint32_t)(quad * 32) << 16) + buf * TURNS * NT + half * 32;
-                const uint32_t one = from + (it & 1) * NT, other = from + (~it & 1) * NT;  // one: of the warp that has the first step
-#pragma unroll
-                for (int i = 0; i < CHUNKS; ++i)
-                    if (half * 32 + i * 64 < t.n) {
-                        if (it == begin) {
-                            take<MODE>(by_8, one + i * 64, r[i]);
+#pragma unroll 1
+                for (int left = steps - PIECE; left > 0; left -= PIECE) {
+                    // the sum so far is added to the next piece's, in TMEM, and its accumulator let go
+                    const int before = buf;
+                    if (++buf == 2) { buf = 0; acc_phase ^= 1; }
+                    if (!(ok = warp_wait(&acc_full[buf], acc_phase, abort_flag, g.status))) break;
+                    tc::tc_fence_after();
+#pragma unroll 1
+                    for (int h = half * 32; h < t.n; h += h & 16 ? 48 : 16) {  // 16 columns at a time: few registers
+                        const uint32_t from = all + before * TURNS * NT + h, to = all + buf * TURNS * NT + h;
+                        uint32_t r[16], x[16];
+                        auto plus = [&](uint32_t at) {
+                            tc::tmem_ld_32x32b_x16(at, x);
                             tc::tmem_ld_wait();
-                        } else {
-                            add<MODE>(by_8, one + i * 64, r[i]);
-                        }
-                        if (end - it > 1) add<MODE>(by_8, other + i * 64, r[i]);
-                    }
-                tc::tc_fence_before();
-                __syncwarp();
-                if (lane == 0) tc::mbar_arrive(&acc_empty[buf]);
-                if (++buf == 2) { buf = 0; acc_phase ^= 1; }
-            }
-            if (!ok) break;
 #pragma unroll
-            for (int i = 0; i < CHUNKS; ++i) {
-                const int c = half * 32 + i * 64;
-                if (c >= t.n) break;
+                            for (int j = 0; j < 16; ++j) r[j] = __float_as_uint(__uint_as_float(r[j]) + __uint_as_float(x[j]));
+                        };
+                        tc::tmem_ld_32x32b_x16(from + one, r);
+                        if (two) plus(from + other);
+                        plus(to + one);
+                        if (left > 1) plus(to + other);
+                        tc::tmem_st_32x32b_x16(to + one, r);
+                    }
+                    tc::tmem_st_wait();
+                    tc::tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) tc::mbar_arrive(&acc_empty[before]);
+                    two = false;
+                }
+                if (!ok) break;
+            }
+            for (int c = half * 32; c < t.n; c += 64) {
+                uint32_t r[32];
+                const bool part = SPLIT && seg.part >= 0;
+                if (seg.s1 > 0) {
+                    const uint32_t from = all + buf * TURNS * NT + c;
+                    take<MODE>(matrices && !part, from + one, r);
+                    tc::tmem_ld_wait();
+                    if (two) {
+                        uint32_t y[32];
+                        take<MODE>(matrices && !part, from + other, y);
+                        tc::tmem_ld_wait();
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) r[j] = __float_as_uint(__uint_as_float(r[j]) + __uint_as_float(y[j]));
+                    }
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) r[j] = 0;
+                }
                 if (part) {
                     float* to = g.parts + (((int64_t)blockIdx.x * 2 + seg.part) * NT + c) * 128 + quad * 32 + lane;
 #pragma unroll
                     for (int j = 0; j < 32; ++j)
-                        if (c + j < t.n) to[j * 128] = __uint_as_float(r[i][j]);
+                        if (c + j < t.n) to[j * 128] = __uint_as_float(r[j]);
                 } else {
-                    put<MODE, false>(g, nullptr, matrices, stage, t.e, l0, t.q0 + c, t.n - c, lane, r[i]);
+                    put<MODE, false, BY>(g, nullptr, matrices, stage, t.e, l0, t.q0 + c, t.n - c, lane, r);
                 }
+            }
+            it += steps;
+            if (seg.s1 > 0) {
+                tc::tc_fence_before();
+                __syncwarp();
+                if (lane == 0) tc::mbar_arrive(&acc_empty[buf]);
+                if (++buf == 2) { buf = 0; acc_phase ^= 1; }
             }
         }
         if (SPLIT && threadIdx.x == 0) g.joins[blockIdx.x] = join;
@@ -479,11 +504,11 @@ static int map_of(CUtensorMap* map, const Mat& m, int dtype, int box_cols, int b
                : QMOE_ERR_UNSUPPORTED;
 }
 
-template <int MODE, int NT, bool GATHER, bool SPLIT>
+template <int MODE, int NT, bool GATHER, bool BY, bool SPLIT>
 static int launch_as(const CUtensorMap& mp, const CUtensorMap& mq, const Args& g, int64_t most, cudaStream_t st) {
     using C = Cfg<MODE, NT>;
-    const auto kernel = expert_gemm_kernel<MODE, NT, GATHER, SPLIT>;
-    int rc = row::allow_smem<expert_gemm_kernel<MODE, NT, GATHER, SPLIT>>(C::SMEM);
+    const auto kernel = expert_gemm_kernel<MODE, NT, GATHER, SPLIT, BY>;
+    int rc = row::allow_smem<expert_gemm_kernel<MODE, NT, GATHER, SPLIT, BY>>(C::SMEM);
     if (rc != QMOE_OK) return rc;
     const int64_t grid = SPLIT || most > row::kSMs ? row::kSMs : most;
     rc = launch_pdl(kernel, dim3((unsigned)grid), dim3(threads_of(GATHER)), (size_t)C::SMEM, st, mp, mq, g);
@@ -493,25 +518,30 @@ static int launch_as(const CUtensorMap& mp, const CUtensorMap& mq, const Args& g
 
 // Columns of a tile, by the rows an expert has on average (the offsets are not known
 // here).  Few: narrow tiles, whose stages are almost all weight, so that more of them
-// are in flight.  Many: tiles of two CTAs.  Tiles of 128 are left for one matrix, whose
-// few tiles the SMs share, which pairs do not.  us of y with tiles of 32, 128 and 256,
-// rows an expert: 64 experts 4096 -> 2816, 16 rows 230 276 261, 32 rows 233 279 262, 48
-// rows 296 280 264, 96 rows - 287 269; 32 experts 2048 -> 1536, 32 rows 38 47 44, 40 rows
-// 48 48 44; one matrix 4096 -> 4096, 32 rows 14.3 16.0 21.9, 64 rows 18.4 16.4 22.2, 192
-// rows - 21.5 23.6.  Between 24 and 32 rows uneven loads decide (Zipf's law of the given
-// exponent, largest expert): 64 experts 4096 -> 2816, 25 rows, 0.8, 144 rows 257 278 260,
-// 32 rows, 1.2, 245 rows 281 279 262, all to one expert 123 66 42; 512 experts 2048 ->
-// 1024, 20 rows, 1.2, 964 rows 380 390 349, 16 rows and a quarter of all for one 354 394
-// 362.
+// are in flight.  Many: tiles of two CTAs.  Between 24 and 96, these for weights that take
+// some 8 us to read and fill pairs' lanes about as well, in sums of some length, else
+// tiles of 128; also for one matrix, whose few tiles the SMs share, which pairs do not.  us of y with tiles of
+// 32, 128 and 256, rows an expert: 64 experts 4096 -> 2816, 16 rows 230 276 261, 32 rows
+// 233 279 262, 48 rows 296 280 264, 96 rows - 287 269; 32 experts 2048 -> 1536, 32 rows
+// 38 47 44, 40 rows 48 48 44; one matrix 4096 -> 4096, 32 rows 14.3 16.0 21.9, 64 rows
+// 18.4 16.4 22.2, 192 rows - 21.5 23.6; 128 and 256: 16 experts 64 -> 1024, 54 rows 5.5
+// 6.4; 512 experts 256 -> 545 (640 and 768 lanes), 72 rows 42 52; 128 experts 128 -> 1408,
+// 62 rows 20.8 24.2.  Between 24 and 32 rows
+// uneven loads decide (Zipf's law of the given exponent, largest expert): 64 experts 4096
+// -> 2816, 25 rows, 0.8, 144 rows 257 278 260, 32 rows, 1.2, 245 rows 281 279 262, all to
+// one expert 123 66 42; 512 experts 2048 -> 1024, 20 rows, 1.2, 964 rows 380 390 349, 16
+// rows and a quarter of all for one 354 394 362.
 //
 // Gathered rows of x are read as they lie for few rows an expert; for many they are
 // laid out in expert order first: a tile's rows are read again for every 256
 // outputs, and TMA's gather of four rows takes as long as a box of 128 (8192 x 8
 // rows of 4096, 2816 outputs: 1136 us gathered in the product, 960 laid out).
-inline int tile_of(int64_t P, int E) {
+inline int tile_of(int64_t P, int E, int64_t lanes, int64_t red) {
     const int64_t touched = P < E ? P : E;
     if (touched == 1) return P <= 32 ? 32 : P <= 192 ? 128 : 256;
-    return P <= 24 * touched ? 32 : 256;
+    if (P <= 24 * touched) return 32;
+    const bool fills = (lanes + 255) / 256 * 256 * 10 <= (lanes + 127) / 128 * 128 * 11;
+    return P > 96 * touched || (fills && red >= 512 && touched * lanes * red >= 20000000) ? 256 : 128;
 }
 
 // No more tiles than this, whatever the offsets.
@@ -540,24 +570,25 @@ inline bool split(int64_t P, int E, int64_t lanes, int64_t per, int nt) {
 inline size_t part_bytes(int nt) { return (size_t)row::kSMs * 2 * nt * 128 * 4 + (row::kSMs * 16 + 255) / 256 * 256; }
 
 // Whether y is better made by expert_few_kernel, for weights off the 16-byte
-// boundaries: by a model of the times in us fitted to GB300.  In place: 3 and, shared by
-// all SMs, 16.5 ns for each CTA of 16 rows of an expert's w and 1024 of their values,
-// 5 ns for one whose row is not its expert's first.  Copied: 10, the copy of the
-// experts that have rows (6 TB/s) and the product that reads it (5.3 TB/s).  In place
+// boundaries: by a model of the times in us fitted to GB300, for as many experts with
+// rows as P rows spread over E by chance reach.  In place: 3 and, shared by all SMs, 16.5
+// ns for each CTA of 16 rows of an expert's w and 1024 of their values, 5 ns for one
+// whose row is not its expert's first.  Copied: 10, a look at every row of w, the copy of
+// the experts that have rows (6 TB/s) and the product that reads it (5.3 TB/s).  In place
 // and copied, tokens x experts: 1 x 8 of 128, 2047 -> 1536, 22 and 41; 4 x 8 101 and
 // 104; 1 x 8, 513 -> 767, 7.5 and 18, 4 x 8 29 and 26; 16 x 7 of 256, 1095 -> 1408, 242
-// and 152; 1 x 10 of 512, 4095 -> 2047, 69 and 131; 1, 4 and 16 rows of one matrix, 4095
-// -> 4096, 16 20 41 and 24 29 29.
+// and 152; 6 x 9 of 64, 1957 -> 2816, 182 and 162; 1 x 10 of 512, 4095 -> 2047, 69 and
+// 131; 1, 4 and 16 rows of one matrix, 4095 -> 4096, 16 20 41 and 24 29 29.
 inline bool few(int64_t P, int E, int64_t N, int64_t K) {
     if (P > 65535) return false;
-    const double touched = (double)(P < E ? P : E), tiles = (double)((N + 15) / 16);
+    const double touched = E * (1 - std::pow(1 - 1.0 / E, (double)P)), tiles = (double)((N + 15) / 16);
     const double in_place = 3 + touched * tiles * 0.0165 * (double)((K + 1023) / 1024) + (P - touched) * tiles * 0.005;
-    return in_place < 10 + touched * N * K * (4 / 6e6 + 2 / 5.3e6);
+    return in_place < 10 + 3e-5 * E * N + touched * N * K * (4 / 6e6 + 2 / 5.3e6);
 }
 
-template <int MODE, bool GATHER>
+template <int MODE, bool GATHER, bool BY>
 static int run_rows(Mat w, Mat q, Args& g, int dtype, uint8_t* ws, size_t left, cudaStream_t st) {
-    const int nt = tile_of(g.P, g.E);
+    const int nt = tile_of(g.P, g.E, g.lanes, g.red);
     CUtensorMap mp, mq;
     int rc = MODE == FWD ? map_of(&mp, w, dtype, STEP, 128, true) : map_of(&mp, w, dtype, 64, STEP, true);
     if (rc != QMOE_OK) return rc;
@@ -573,10 +604,12 @@ static int run_rows(Mat w, Mat q, Args& g, int dtype, uint8_t* ws, size_t left, 
     }
     switch (nt) {
         case 32:
-            return shares ? launch_as<MODE, 32, GATHER, true>(mp, mq, g, most, st) : launch_as<MODE, 32, GATHER, false>(mp, mq, g, most, st);
+            return shares ? launch_as<MODE, 32, GATHER, BY, true>(mp, mq, g, most, st)
+                          : launch_as<MODE, 32, GATHER, BY, false>(mp, mq, g, most, st);
         case 128:
-            return shares ? launch_as<MODE, 128, GATHER, true>(mp, mq, g, most, st) : launch_as<MODE, 128, GATHER, false>(mp, mq, g, most, st);
-        default: return GATHER ? QMOE_ERR_UNSUPPORTED : launch_pair<MODE>(mp, mq, mq, g, most, st);
+            return shares ? launch_as<MODE, 128, GATHER, BY, true>(mp, mq, g, most, st)
+                          : launch_as<MODE, 128, GATHER, BY, false>(mp, mq, g, most, st);
+        default: return GATHER ? QMOE_ERR_UNSUPPORTED : launch_pair<MODE, false, BY>(mp, mq, mq, g, most, st);
     }
 }
 
@@ -617,9 +650,10 @@ extern "C" size_t qmoe_expert_copy_bytes(int64_t rows, int64_t cols) {
 static size_t product_bytes(int64_t P, int E, int64_t N, int64_t K, int op, int pairs, int parts) {
     if (P <= 0 || E <= 0 || N <= 0 || K <= 0 || op < 0 || op > 2 || P > eg::kMost || N > eg::kMost || K > eg::kMost) return 0;
     if (op == eg::DW) return pairs ? eg::padded(P, K) : 0;
-    const int nt = eg::tile_of(P, E);
+    const int64_t lanes = op == eg::FWD ? N : K, red = op == eg::FWD ? K : N;
+    const int nt = eg::tile_of(P, E, lanes, red);
     if (nt == 256) return pairs && op == eg::FWD ? eg::padded(P, K) : 0;
-    return eg::split(P, E, op == eg::FWD ? N : K, (int64_t)parts * eg::steps_of(op == eg::FWD ? K : N), nt) ? eg::part_bytes(nt) : 0;
+    return eg::split(P, E, lanes, (int64_t)parts * eg::steps_of(red), nt) ? eg::part_bytes(nt) : 0;
 }
 extern "C" size_t qmoe_expert_workspace_bytes(int64_t P, int E, int64_t N, int64_t K, int op, int pairs) {
     return product_bytes(P, E, N, K, op, pairs, 1);
@@ -649,14 +683,15 @@ static int linear(const Call& c, const void* x, int64_t ldx, const void* w, int6
               aligned16(y) && ldy * size % 16 == 0, c.dtype == QMOE_BF16 ? tc::idesc_bf16_f32(0, 0) : tc::idesc_f16_f32(0, 0), c.status,
               nullptr, nullptr, c.by, steps_of(c.K), steps_of(c.K) * c.parts};
     if (!fits(mw) && few(c.P, c.E, c.N, c.K)) return launch_few(mw, mx, g, c.dtype, st);
-    const bool lay_out = c.pairs && tile_of(c.P, c.E) == 256;
+    const bool lay_out = c.pairs && tile_of(c.P, c.E, c.N, c.K) == 256;
     const size_t need = product_bytes(c.P, c.E, c.N, c.K, FWD, c.pairs != nullptr, c.parts);
     if (left < need + copy_need(mw) + (lay_out ? 0 : copy_need(mx))) return QMOE_ERR_ARG;
     if ((rc = as_tma(mw, c.offsets, at, left, st)) != QMOE_OK) return rc;
     rc = lay_out ? copy_rows(mx, c.pairs, c.P, c.k, nullptr, at, left, st) : as_tma(mx, nullptr, at, left, st);
     if (rc != QMOE_OK) return rc;
     if (lay_out) g.pairs = nullptr;
-    return g.pairs ? run_rows<FWD, true>(mw, mx, g, c.dtype, at, left, st) : run_rows<FWD, false>(mw, mx, g, c.dtype, at, left, st);
+    if (g.pairs) return run_rows<FWD, true, false>(mw, mx, g, c.dtype, at, left, st);
+    return c.by ? run_rows<FWD, false, true>(mw, mx, g, c.dtype, at, left, st) : run_rows<FWD, false, false>(mw, mx, g, c.dtype, at, left, st);
 }
 
 static int linear_dx(const Call& c, const void* dy, int64_t lddy, const void* w, int64_t ldw, int64_t w_expert, void* dx, int dx_dtype,
@@ -678,7 +713,7 @@ static int linear_dx(const Call& c, const void* dy, int64_t lddy, const void* w,
               aligned16(dx) && lddx * size % 16 == 0,
               (c.dtype == QMOE_BF16 ? tc::idesc_bf16_f32(0, 0) : tc::idesc_f16_f32(0, 0)) | 1u << 15, c.status, nullptr, nullptr, c.by,
               steps_of(c.N), steps_of(c.N) * c.parts};
-    return run_rows<DX, false>(mw, my, g, c.dtype, at, left, st);
+    return c.by ? run_rows<DX, false, true>(mw, my, g, c.dtype, at, left, st) : run_rows<DX, false, false>(mw, my, g, c.dtype, at, left, st);
 }
 
 size_t scaled_bytes(int64_t T, int64_t N, int64_t K, int parts, int dx) {

@@ -106,7 +106,7 @@ __device__ __forceinline__ void mma_stage(uint32_t d, uint32_t stage, uint32_t i
         if (k < k16) mma_pair(d, da + SA * k, db + SB * k, idesc, !first || k > 0);
 }
 
-template <int MODE, bool BULK>
+template <int MODE, bool BULK, bool BY>
 __global__ void __launch_bounds__(PAIR_THREADS, 1)
 expert_pair_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_constant__ CUtensorMap map_q,
                    const __grid_constant__ CUtensorMap map_o, const Args g) {
@@ -215,13 +215,13 @@ expert_pair_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_const
             const int left = MODE == DW ? (t.end - t.row0) % STEP : 0, whole = t.steps - (left > 0);
             const int pieces = pieces_of(t.steps), per = pieces > 1 ? (t.steps + pieces - 1) / pieces : t.steps;
             for (int from = 0; from < t.steps; from += per) {  // the sum's pieces, each in an accumulator of its own
-                if (rank == 0 && !(ok = warp_wait(&acc_empty[buf], acc_phase ^ 1, abort_flag, g.status))) break;
+                if (rank == 0 && !(ok = issue_wait(&acc_empty[buf], acc_phase ^ 1, abort_flag, g.status))) break;
                 const uint32_t d = tm + buf * 256;
                 const int to = min(from + per, whole);
                 if (rank == 0) {
 #pragma unroll 1
                     for (int s = from; s < to; ++s) {
-                        if (!(ok = warp_wait(&full[slot], phase, abort_flag, g.status))) break;
+                        if (!(ok = issue_wait(&full[slot], phase, abort_flag, g.status))) break;
                         tc::tc_fence_after();
                         mma_stage<MODE>(d, tc::smem_u32(smem) + slot * C::STAGE, idesc, s == from);
                         commit_pair(&empty[slot]);
@@ -236,7 +236,7 @@ expert_pair_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_const
                 if (MODE == DW && left > 0 && from + per >= t.steps) {
                     const int k16 = (left + 15) / 16;
                     uint8_t* st = smem + slot * C::STAGE;
-                    if (!(ok = warp_wait(&full[slot], rank == 0 ? phase : here >> slot & 1, abort_flag, g.status))) break;
+                    if (!(ok = issue_wait(&full[slot], rank == 0 ? phase : here >> slot & 1, abort_flag, g.status))) break;
                     here ^= 1u << slot;
                     // rows behind the expert's last, up to the 16 of a product, are another's: zeros in their place
                     const int zero = k16 * 16 - left;
@@ -247,7 +247,7 @@ expert_pair_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_const
                     tc::fence_proxy_async_smem();
                     __syncwarp();
                     if (rank == 0) {
-                        if (!(ok = warp_wait(&other[slot], relayed >> slot & 1, abort_flag, g.status))) break;
+                        if (!(ok = issue_wait(&other[slot], relayed >> slot & 1, abort_flag, g.status))) break;
                         relayed ^= 1u << slot;
                         tc::tc_fence_after();
                         mma_stage<MODE>(d, tc::smem_u32(st), idesc, whole == from, k16);
@@ -276,7 +276,7 @@ expert_pair_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_const
             if (t.steps == 0) {
 #pragma unroll
                 for (int j = 0; j < 32; ++j) r[0][j] = 0;
-                for (int c = half * 32; c < t.n; c += 64) put<MODE, BULK>(g, &map_o, matrices, stage, t.e, l0, t.q0 + c, t.n - c, lane, r[0]);
+                for (int c = half * 32; c < t.n; c += 64) put<MODE, BULK, BY>(g, &map_o, matrices, stage, t.e, l0, t.q0 + c, t.n - c, lane, r[0]);
                 continue;
             }
             const uint32_t all = tm + ((uint32_t)(quad * 32) << 16);
@@ -291,7 +291,7 @@ expert_pair_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_const
 #pragma unroll 1
             for (int p = pieces_of(t.steps); p > 1; --p) {
                 // The sum so far is added to the next piece's, in TMEM, and its accumulator let go: products wait some 0.6 us
-                // for it, as the other accumulator holds the sum (8192 rows 4096 -> 4096: 158 us, 153 in one piece).  128 sums a
+                // for it, as the other accumulator holds the sum (8192 rows 4096 -> 4096: 154 us, 152 in one piece).  128 sums a
                 // thread in registers would leave both accumulators free, but spilled (155 there, but dw of 64 x 512 rows 2816 x
                 // 2048 400 to 600 us for 360).
                 const int before = buf;
@@ -319,7 +319,7 @@ expert_pair_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_const
                 tc::tmem_ld_wait();
                 if (at + 64 < t.n) take<MODE>(matrices, from + at + 64, next);
                 else let_go(buf);
-                put<MODE, BULK>(g, &map_o, matrices, stage, t.e, l0, t.q0 + at, t.n - at, lane, now);
+                put<MODE, BULK, BY>(g, &map_o, matrices, stage, t.e, l0, t.q0 + at, t.n - at, lane, now);
                 at += 64;
             };
             if (at >= t.n) let_go(buf);  // no columns for this warp
@@ -342,10 +342,10 @@ expert_pair_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_const
         asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tm), "r"(512) : "memory");
 }
 
-template <int MODE, bool BULK>
+template <int MODE, bool BULK, bool BY>
 int launch_pair(const CUtensorMap& mp, const CUtensorMap& mq, const CUtensorMap& mo, const Args& g, int64_t most, cudaStream_t st) {
     using C = PairCfg<MODE>;
-    const int rc = row::allow_smem<expert_pair_kernel<MODE, BULK>>(C::SMEM);
+    const int rc = row::allow_smem<expert_pair_kernel<MODE, BULK, BY>>(C::SMEM);
     if (rc != QMOE_OK) return rc;
     const int64_t pairs = most < row::kSMs / 2 ? most : row::kSMs / 2;
     cudaLaunchAttribute attr[2];
@@ -362,13 +362,15 @@ int launch_pair(const CUtensorMap& mp, const CUtensorMap& mq, const CUtensorMap&
     cfg.stream = st;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, expert_pair_kernel<MODE, BULK>, mp, mq, mo, g) == cudaSuccess ? QMOE_OK : QMOE_ERR_LAUNCH;
+    return cudaLaunchKernelEx(&cfg, expert_pair_kernel<MODE, BULK, BY>, mp, mq, mo, g) == cudaSuccess ? QMOE_OK : QMOE_ERR_LAUNCH;
 }
 
-template int launch_pair<FWD, false>(const CUtensorMap&, const CUtensorMap&, const CUtensorMap&, const Args&, int64_t, cudaStream_t);
-template int launch_pair<DX, false>(const CUtensorMap&, const CUtensorMap&, const CUtensorMap&, const Args&, int64_t, cudaStream_t);
-template int launch_pair<DW, true>(const CUtensorMap&, const CUtensorMap&, const CUtensorMap&, const Args&, int64_t, cudaStream_t);
-template int launch_pair<DW, false>(const CUtensorMap&, const CUtensorMap&, const CUtensorMap&, const Args&, int64_t, cudaStream_t);
+template int launch_pair<FWD, false, false>(const CUtensorMap&, const CUtensorMap&, const CUtensorMap&, const Args&, int64_t, cudaStream_t);
+template int launch_pair<FWD, false, true>(const CUtensorMap&, const CUtensorMap&, const CUtensorMap&, const Args&, int64_t, cudaStream_t);
+template int launch_pair<DX, false, false>(const CUtensorMap&, const CUtensorMap&, const CUtensorMap&, const Args&, int64_t, cudaStream_t);
+template int launch_pair<DX, false, true>(const CUtensorMap&, const CUtensorMap&, const CUtensorMap&, const Args&, int64_t, cudaStream_t);
+template int launch_pair<DW, true, false>(const CUtensorMap&, const CUtensorMap&, const CUtensorMap&, const Args&, int64_t, cudaStream_t);
+template int launch_pair<DW, false, false>(const CUtensorMap&, const CUtensorMap&, const CUtensorMap&, const Args&, int64_t, cudaStream_t);
 
 }  // namespace eg
 }  // namespace qmoe

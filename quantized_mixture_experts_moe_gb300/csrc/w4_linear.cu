@@ -750,7 +750,7 @@ inline size_t up256(size_t n) { return (n + 255) / 256 * 256; }
 
 template <typename T, int FORMAT, bool ROWS_BY>
 static int widen_rows(const Widen& a, cudaStream_t st) {
-    if (a.K >= 2048)  // a word at least for each thread of a CTA
+    if (a.K >= 2048 || a.N < 8 * row::kSMs)  // a word at least for each thread of a CTA, or rows that would leave SMs idle
         return launch_pdl(w4_widen_kernel<T, FORMAT, ROWS_BY, 8>, dim3((unsigned)a.N), dim3(256), 0, st, a);
     return launch_pdl(w4_widen_kernel<T, FORMAT, ROWS_BY, 1>, dim3((unsigned)((a.N + 7) / 8)), dim3(256), 0, st, a);
 }
