@@ -520,17 +520,17 @@ static int launch_as(const CUtensorMap& mp, const CUtensorMap& mq, const Args& g
 // here).  Few: narrow tiles, whose stages are almost all weight, so that more of them
 // are in flight.  Many: tiles of two CTAs.  Between 24 and 96, these for weights that take
 // some 8 us to read and fill pairs' lanes about as well, in sums of some length, else
-// tiles of 128; also for one matrix, whose few tiles the SMs share, which pairs do not.  us of y with tiles of
-// 32, 128 and 256, rows an expert: 64 experts 4096 -> 2816, 16 rows 230 276 261, 32 rows
-// 233 279 262, 48 rows 296 280 264, 96 rows - 287 269; 32 experts 2048 -> 1536, 32 rows
-// 38 47 44, 40 rows 48 48 44; one matrix 4096 -> 4096, 32 rows 14.3 16.0 21.9, 64 rows
-// 18.4 16.4 22.2, 192 rows - 21.5 23.6; 128 and 256: 16 experts 64 -> 1024, 54 rows 5.5
-// 6.4; 512 experts 256 -> 545 (640 and 768 lanes), 72 rows 42 52; 128 experts 128 -> 1408,
-// 62 rows 20.8 24.2.  Between 24 and 32 rows
-// uneven loads decide (Zipf's law of the given exponent, largest expert): 64 experts 4096
-// -> 2816, 25 rows, 0.8, 144 rows 257 278 260, 32 rows, 1.2, 245 rows 281 279 262, all to
-// one expert 123 66 42; 512 experts 2048 -> 1024, 20 rows, 1.2, 964 rows 380 390 349, 16
-// rows and a quarter of all for one 354 394 362.
+// tiles of 128; also for one matrix, whose few tiles the SMs share, which pairs do not.
+// us of y with tiles of 32, 128 and 256, rows an expert: 64 experts 4096 -> 2816, 16 rows
+// 230 276 261, 32 rows 233 279 262, 48 rows 296 280 264, 96 rows - 287 269; 32 experts
+// 2048 -> 1536, 32 rows 38 47 44, 40 rows 48 48 44; one matrix 4096 -> 4096, 32 rows 14.3
+// 16.0 21.9, 64 rows 18.4 16.4 22.2, 192 rows - 21.5 23.6; 128 and 256: 16 experts 64 ->
+// 1024, 54 rows 5.5 6.4; 512 experts 256 -> 545 (640 and 768 lanes), 72 rows 42 52; 128
+// experts 128 -> 1408, 62 rows 20.8 24.2.  Between 24 and 32 rows uneven loads decide
+// (Zipf's law of the given exponent, largest expert): 64 experts 4096 -> 2816, 25 rows,
+// 0.8, 144 rows 257 278 260, 32 rows, 1.2, 245 rows 281 279 262, all to one expert 123 66
+// 42; 512 experts 2048 -> 1024, 20 rows, 1.2, 964 rows 380 390 349, 16 rows and a quarter
+// of all for one 354 394 362.
 //
 // Gathered rows of x are read as they lie for few rows an expert; for many they are
 // laid out in expert order first: a tile's rows are read again for every 256
@@ -779,7 +779,7 @@ extern "C" int qmoe_expert_linear_dw(int64_t P, int E, int64_t N, int64_t K, int
     if (rc != QMOE_OK) return rc;
     rc = eg::map_of(&mq, mx, dtype, 64, eg::STEP, false);
     if (rc != QMOE_OK) return rc;
-    if (!g.wide || (int64_t)size * P > 512ll * E) return eg::launch_pair<eg::DW>(mp, mq, mq, g, units, st);
+    if (!g.wide || P > (size == 4 ? 32ll : 256ll) * E) return eg::launch_pair<eg::DW>(mp, mq, mq, g, units, st);
     // few rows an expert: put_dw has both sides
     CUtensorMap mo;
     const eg::Mat out = {dw, N, K, K, E, N * K};

@@ -316,9 +316,9 @@ __device__ __forceinline__ void put_rows(const Args& g, int l0, int q0, int n, i
 // store (BULK), which runs while the warp goes on and leaves out what lies outside the
 // expert's matrix, or by the warp's own stores, where TMA is to feed long sums at the
 // same time.  us with the warp's stores and with TMA's, in fp32 and in bf16, rows an
-// expert: 512 x 8 (1024 x 2048) 847 and 729, 571 and 465; 64 x 80 (2816 x 4096) 590
-// and 564, 401 and 284; 128 x 256 (2048 x 768) 172 and 185, 133 and 107; 64 x 512
-// (2816 x 2048) 342 and 354, 267 and 272.
+// expert: 512 x 8 (1024 x 2048) 752 and 742, 557 and 464; 64 x 80 (2816 x 4096) 528
+// and 559, 389 and 269; 128 x 256 (2048 x 768) 166 and 185, 119 and 108; 64 x 512
+// (2816 x 2048) 339 and 351, 268 and 268.
 //
 // Where a row's piece of 16 bytes lies: rows that are read or written together fall on
 // all banks, and the store's swizzle has it so.

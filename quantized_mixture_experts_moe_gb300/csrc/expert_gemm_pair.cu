@@ -13,10 +13,10 @@
 // take.
 //
 // What bounds it: the tensor core under the power limit (64 x 1024 rows 4096 -> 2816:
-// y 853 us, 1.77 PFLOP/s, dx 813, 1.86, against 1.97 of a library's product of one
-// matrix); for dw's 32-bit sums the stores too (64 x 512 rows, 2816 x 2048: 347 us,
-// 1.09 PFLOP/s and 5.2 TB/s).  A lone CTA with 128 x 256 tiles reached 1.36 PFLOP/s:
-// its loads, half as much again.
+// y 840 to 890 us by the card's clock, 1.7 to 1.8 PFLOP/s, dx 825 to 865, against 1.97 of
+// a library's product of one matrix); for dw's 32-bit sums the stores too (64 x 512 rows,
+// 2816 x 2048: 339 to 366 us, 1.1 PFLOP/s and 5.2 TB/s).  A lone CTA with 128 x 256 tiles
+// reached 1.36 PFLOP/s: its loads, half as much again.
 #include "expert_gemm.cuh"
 
 namespace qmoe {

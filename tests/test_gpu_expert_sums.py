@@ -84,7 +84,7 @@ def test_long_sums_of_odd_rows(P, N, K):
     near(y, want, want, 160, "y")
 
 
-@pytest.mark.parametrize("counts", [[65536], [3, 70001, 0, 900], [64900] + [1] * 600, [9] * 300 + [65001] + [0] * 400])
+@pytest.mark.parametrize("counts", [[65536], [3, 70001, 0, 900], [30900] + [1] * 1000, [9] * 300 + [22001] + [0] * 600])
 @pytest.mark.parametrize("gather", [False, True])
 def test_long_sums_of_dw(counts, gather):
     """One expert has almost all rows; the last two are stored by TMA, as most experts have few."""
