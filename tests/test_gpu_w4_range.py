@@ -185,3 +185,25 @@ def test_scales_that_are_no_numbers_stay_in_their_row(T):
     assert not y[:, 3].isfinite().any() and y[:, 7].isnan().all()
     keep = [n for n in range(N) if n not in (3, 7)]
     close(y[:, keep], (x.double() @ want.t())[:, keep], slack[:, keep], "y")
+
+
+@pytest.mark.parametrize("format", ["int4", "mxfp4"])
+@pytest.mark.parametrize("T,k,E", [(33, 8, 8), (64, 8, 20), (257, 1, 5), (100, 5, 3), (2, 300, 8), (5, 256, 4), (7, 129, 9)])
+def test_more_pairs_than_a_launch_sorts(T, k, E, format):
+    """Tokens by 256 pairs, and pair by pair where a token has more than that: every pair's row is what its token's call by
+    itself gives, whatever stands beside it."""
+    g = gen(T + k)
+    N, K = 72, 288
+    q = torch.randint(0, 256, (E, N, K // 2), generator=g, dtype=torch.uint8)
+    s = (0.005 + 0.015 * torch.rand(E, N, K // 32, generator=g)).half() if format == "int4" else torch.randint(118, 124, (E, N, K // 32), generator=g, dtype=torch.uint8)
+    x = randn(g, T, K, dtype=BF16)
+    ids = torch.randint(-1, E + 1, (T, k), generator=g).int()
+    y = qb.w4_linear(x.cuda(), q.cuda(), s.cuda(), ids=ids.cuda(), out_dtype=F32).cpu()
+    assert y.shape == (T * k, N)
+    w = ref.codes4(q, s)
+    token = torch.arange(T * k) // k
+    for e in range(E):
+        mine = (ids.view(-1) == e).nonzero().view(-1)
+        rows = x[token[mine]].double()
+        close(y[mine], rows @ w[e].t(), ref.w4_slack(rows, w[e], s[e], K), f"expert {e}")
+    assert (y[(ids.view(-1) < 0) | (ids.view(-1) >= E)] == 0).all()
