@@ -15,7 +15,7 @@
 // Many rows an expert, and dw: 256 x 256 tiles of two CTAs (expert_gemm_pair.cu).
 // Here: y and dx for fewer, 128 lanes and up to 32 or 128 columns (tile_of), so that the
 // ring holds mostly weights, which bound it: 1024 pairs over 128 experts 2048 -> 1536
-// 132 us, 6.1 TB/s; 64 x 80 rows 4096 -> 2816 285 us, 5.2 TB/s.  One token x 8 of
+// 131 us, 6.1 TB/s; 64 x 16 rows 4096 -> 2816 230 us, 6.4 TB/s.  One token x 8 of
 // 128 experts (50 MB) 15 us: 2.4 until the first load, 1.5 its latency, 9 the
 // weights at 5.3 TB/s, 1.2 the stores.
 #include <cmath>
